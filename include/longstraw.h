@@ -21,6 +21,11 @@
  * prompt into context-parallel shards (section 3-2 (2)); a handle may be kept across groups
  * (prefix reuse, section 4-2) with ls_prefix_grad_finalize(..., reset_acc = 1) between them.
  *
+ * Around the replay of a group: ls_policy_loss is the loss of a packed group with per-token
+ * advantages and a reference-policy KL term; ls_rope rotates queries and keys by their
+ * positions (and gradients back); ls_cache_* keep the group's keys and values in pages that
+ * the responses share with their prompt, and attend new tokens over them (rollout, scoring).
+ *
  * Conventions shared by every entry point
  *  - Pointers named "device" must point to device memory of the current CUDA device,
  *    allocated and owned by the caller.  The library allocates no device memory and never
@@ -278,6 +283,255 @@ ls_status ls_grpo_loss_noalloc(int64_t R, int64_t V, int32_t G, const void* logi
 int64_t ls_grpo_loss_noalloc_max_rows(void);
 
 /*
+ * ls_policy_loss -- clipped policy loss with a KL term, forward and backward, over the packed
+ * tokens of any number of responses (review section 1-1: the clipped surrogate of L_policy,
+ * and step 3, the reference policy's log-probabilities).  Per token row t of logits x
+ * [T, V] with sampled id y_t, advantage A_t, weight w_t:
+ *     lse = log sum_v exp(x_v);  logp = x_y - lse;  d = logp - logp_old[t];  rho = exp(d)
+ *     surr = min(rho A_t, clip(rho, 1 - eps_low, 1 + eps_high) A_t)
+ *     clip_mask[t] = 1 iff (A_t > 0 and d > log(1 + eps_high)) or (A_t < 0 and d < log(1 - eps_low))
+ *     r = logp - logp_ref[t];  kl[t] = r (LS_KL_K1), r^2 / 2 (LS_KL_K2) or
+ *                              exp(-r) + r - 1 (LS_KL_K3); 0 with LS_KL_NONE
+ *     *loss = sum_t w_t (beta kl[t] - surr_t)          (written, not accumulated)
+ *     g_t = w_t (beta kl'(r) - [not clipped] A_t rho), kl' = 1, r, 1 - exp(-r)
+ *     dlogits[t,v] = g_t (1[v = y_t] - exp(x_v - lse))
+ * The weights carry the normalisation and the mask: 1/(G R_i) on the tokens of response i
+ * gives the loss of ls_grpo_loss.  A token of weight 0 is left out: its logits, id and
+ * log-probabilities are not looked at (they may be NaN), its outputs are 0.
+ *   logits   device bf16, row t at logits + t logits_stride (elements, >= V)
+ *   ids      device int32 [T] (an id outside [0, V) sets the device status; outputs 0)
+ *   logp_old, advantages, weights  device fp32 [T]; logp_ref device fp32 [T], may be NULL with
+ *            LS_KL_NONE
+ *   loss     device fp32 [1]: the fp64 sum of the tokens' terms in a fixed order, rounded once
+ *   dlogits  device bf16, row t at dlogits + t dlogits_stride; columns past V are left as they
+ *            were.  May be the logits themselves (same pointer and stride): each row is then
+ *            replaced by its gradient.
+ *   clip_mask device uint8 [T]; logp_out, kl_out device fp32 [T], may be NULL
+ *   0 <= eps_low < 1, eps_high >= 0; T >= 1.  workspace device, 16-byte aligned,
+ *   >= ls_policy_loss_workspace_bytes(T) bytes.
+ * Any V, strides and 2-byte alignment of the rows are right; rows that are 16-byte aligned
+ * (a stride that is a multiple of 8) are fast.  Precision as in ls_grpo_loss: compensated fp32
+ * row sums, everything per token in fp64; the clip decision is taken on d in fp64.
+ */
+typedef enum { LS_KL_NONE = 0, LS_KL_K1 = 1, LS_KL_K2 = 2, LS_KL_K3 = 3 } ls_kl_kind;
+typedef struct {
+  int64_t T, V;
+  int64_t logits_stride, dlogits_stride;
+  const void* logits;
+  const int32_t* ids;
+  const float* logp_old;
+  const float* logp_ref;
+  const float* advantages;
+  const float* weights;
+  double eps_low, eps_high, beta;
+  int32_t kl;
+  float* loss;
+  void* dlogits;
+  uint8_t* clip_mask;
+  float* logp_out;
+  float* kl_out;
+} ls_policy_loss_desc;
+size_t ls_policy_loss_workspace_bytes(int64_t T);
+ls_status ls_policy_loss(const ls_policy_loss_desc* d, void* workspace, size_t workspace_bytes,
+                         void* stream);
+
+/*
+ * ls_rope -- rotary positions of queries and keys, and the gradient through them.  With
+ * angle a_i = position_t * inv_freq[i] and factor f = attn_factor, every pair (x, y) of the
+ * first rot_dim values of a head becomes
+ *     (f (x cos a - y sin a), f (y cos a + x sin a));
+ * pair i is (i, i + rot_dim / 2), or (2 i, 2 i + 1) if interleaved.  The other D - rot_dim
+ * values are copied.  inverse = 1 turns by -a with the same f: the gradient of the rotation
+ * (d loss / d input from d loss / d output).
+ *   q, k     device bf16; token t, head h at q + t q_stride + h D (elements), so that rows of
+ *            a fused projection can be given.  Hq = 0 or Hk = 0 leaves that tensor out.
+ *   q_out, k_out  likewise with their own strides; may be the inputs (same pointer and stride).
+ *   positions device int64 [T], or NULL: token t has position pos0 + t.
+ *   inv_freq HOST, rot_dim / 2 doubles, copied during the call.  rot_dim even,
+ *            2 <= rot_dim <= D <= 256; D even; T >= 1.
+ * Angles are reduced exactly: position * (inv_freq / 2 pi mod 1) in 64-bit fixed point, so
+ * far positions (|position| < 2^31) lose nothing; the rotation runs in fp32 and rounds once.
+ * Any 2-byte alignment is right; 16-byte aligned rows with rot_dim a multiple of 16 are fast.
+ *
+ * ls_rope_freqs -- inverse frequencies theta^(-2 i / rot_dim) into inv_freq (host,
+ * rot_dim / 2 doubles), scaled for contexts `factor` times as long as orig_len:
+ * LS_ROPE_LINEAR divides all by factor; LS_ROPE_RAMP keeps those that turn more than
+ * beta_fast times over orig_len, divides those that turn less than beta_slow times, mixes
+ * linearly by the index in between and sets *attn_factor = 0.1 ln(factor) + 1 (1 for the
+ * other two).  theta > 1, factor >= 1, for the ramp orig_len >= 1 and
+ * beta_fast >= beta_slow > 0.
+ */
+typedef enum { LS_ROPE_NONE = 0, LS_ROPE_LINEAR = 1, LS_ROPE_RAMP = 2 } ls_rope_scaling;
+typedef struct {
+  int64_t T;
+  int32_t Hq, Hk, D, rot_dim;
+  int32_t interleaved, inverse;
+  const double* inv_freq;
+  double attn_factor;
+  const int64_t* positions;
+  int64_t pos0;
+  const void* q;
+  int64_t q_stride;
+  void* q_out;
+  int64_t q_out_stride;
+  const void* k;
+  int64_t k_stride;
+  void* k_out;
+  int64_t k_out_stride;
+} ls_rope_desc;
+ls_status ls_rope(const ls_rope_desc* d, void* stream);
+ls_status ls_rope_freqs(int32_t rot_dim, double theta, int32_t scaling, double factor,
+                        int64_t orig_len, double beta_fast, double beta_slow, double* inv_freq,
+                        double* attn_factor);
+
+/*
+ * Paged cache (review section 3-2 (2), physical pages of the prompt's keys and values; the
+ * prompt as state shared by the group, section 2): keys and values of one attention layer in
+ * pages of page_size tokens.  Row r of the page table lists the pages of sequence r, page j
+ * holding its tokens j page_size .. (j + 1) page_size - 1; seq_len[r] is its length; several
+ * rows may list the same page, refcount[p] of them.  A page is free iff its count is 0.
+ * All of it is device memory of the caller, borrowed until ls_cache_destroy:
+ *   k_pages, v_pages  bf16, page p at k_pages + p page_stride (elements, a multiple of 8,
+ *            >= page_size Hkv D), inside a page [page_size, Hkv, D] (LS_CACHE_NHD) or
+ *            [Hkv, page_size, D] (LS_CACHE_HND); 16-byte aligned.  K and V may be
+ *            interleaved in one pool (page_stride = 2 page_size Hkv D).
+ *   page_table int32 [num_rows, table_width]; seq_len int32 [num_rows];
+ *   refcount int32 [num_pages].
+ *   page_size 16, 32, 64, 128 or 256; Hq, Hkv, D, softmax_scale as in ls_prefix_desc.
+ * ls_cache_create only validates and keeps host metadata; ls_cache_reset makes every row
+ * empty and every page free (page_table -1, seq_len 0, refcount 0).  A caller that keeps its
+ * own book may write the arrays itself between calls, in stream order.
+ * Calls on one handle are ordered on one stream, as for a prefix handle.  All lists (rows,
+ * counts, offsets) are device int32 arrays, so calls can be captured into graphs and replayed
+ * with other contents; what the host cannot check is checked on the device: a row outside
+ * [0, num_rows), a length outside [0, table_width page_size] or a listed page outside
+ * [0, num_pages) sets the device status and is left out (nothing is read or written through
+ * it); attention reads keys and values of such a page as zeros.
+ */
+typedef struct ls_cache_s* ls_cache_t;
+typedef enum { LS_CACHE_NHD = 0, LS_CACHE_HND = 1 } ls_cache_layout;
+typedef struct {
+  int64_t num_pages;
+  int32_t page_size, Hq, Hkv, D;
+  int32_t layout;
+  float softmax_scale;
+  int64_t page_stride;
+  void* k_pages;
+  void* v_pages;
+  int32_t num_rows, table_width;
+  int32_t* page_table;
+  int32_t* seq_len;
+  int32_t* refcount;
+} ls_cache_desc;
+ls_status ls_cache_create(const ls_cache_desc* desc, ls_cache_t* out);
+ls_status ls_cache_destroy(ls_cache_t h);
+ls_status ls_cache_reset(ls_cache_t h, void* stream);
+
+/* Bytes of device workspace ls_cache_extend, _fork and _compact (of its source) need. */
+size_t ls_cache_pages_workspace_bytes(ls_cache_t h);
+
+/*
+ * Page management.  n <= 1024 list entries (LS_ERR_UNSUPPORTED above; n = 0 does nothing);
+ * entries take free pages lowest index first, in list order.  A row listed twice counts once:
+ * its later entries set the device status and are left out.
+ *
+ * ls_cache_extend -- seq_len[rows[i]] += add[i], with pages for the new tokens.  An entry that
+ *   does not fit its table row, or that the free pages left do not cover, is left out (its row
+ *   unchanged) and sets the device status (4 in the word for want of pages).
+ * ls_cache_fork -- row children[i] becomes a copy of row parents[i]: whole pages are shared, a
+ *   part-filled last page is copied into a free page of its own (its filled tokens only), so
+ *   both rows can grow.  A child must be empty (length 0) and no parent of this call that
+ *   holds anything; else, or for want of a page, the pair is left out with the status set.
+ * ls_cache_free -- drops the rows' pages (those that no row lists any more become free) and
+ *   empties the rows.
+ * ls_cache_compact -- moves the live pages of src together.  dst a handle over another pool of
+ *   the same page shape, layout and table shape: live pages go to dst pages 0 .. n-1 in
+ *   ascending order, dst's table, lengths and counts are written from src's; src keeps its
+ *   state.  Pages beyond dst's pool set the device status (4 in the word) and are listed as -1.
+ *   dst = src: in place, live pages from n on move into the holes below, in ascending order;
+ *   listed pages are renamed, the pages they left become free.  n_live: device int32 [1], may
+ *   be NULL: the number n of live pages.
+ */
+ls_status ls_cache_extend(ls_cache_t h, int32_t n, const int32_t* rows, const int32_t* add,
+                          void* workspace, size_t workspace_bytes, void* stream);
+ls_status ls_cache_fork(ls_cache_t h, int32_t n, const int32_t* parents, const int32_t* children,
+                        void* workspace, size_t workspace_bytes, void* stream);
+ls_status ls_cache_free(ls_cache_t h, int32_t n, const int32_t* rows, void* stream);
+ls_status ls_cache_compact(ls_cache_t src, ls_cache_t dst, int32_t* n_live, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/*
+ * The new tokens of S sequences, packed: entry b owns packed rows cu_new[b] .. cu_new[b+1]-1
+ * (cu_new device int32 [S + 1], cu_new[0] >= 0, non-decreasing; an entry may have none; packed
+ * rows that no entry owns are left as they were) and is table row rows[b] (rows device int32
+ * [S], or NULL: row b).  seq_len counts the new tokens already (ls_cache_extend comes first):
+ * token i of n new ones of a sequence of length L is at position L - n + i.
+ * 1 <= S <= 2048, T >= 1 packed rows.
+ *
+ * ls_cache_append -- writes the new tokens' keys and values into their pages; with inv_freq
+ *   the keys are rotated on the way as by ls_rope at their positions, and so are the queries
+ *   (q to q_out), in the same pass.  k_new, v_new device bf16, token t, head h at
+ *   k_new + t k_stride + h D; q likewise with Hq heads (NULL: no queries; then q_out is
+ *   ignored), q_out may be q.  inv_freq HOST, rot_dim / 2 doubles, or NULL: no rotation (and q must be
+ *   NULL).  Tokens at a negative position are left out.  Pages of several rows must not be
+ *   appended to (ls_cache_fork copies the page that a row grows into).
+ *
+ * ls_cache_attn -- attention of the new tokens over their sequences' pages, their own keys
+ *   included (append first): token at position p sees keys 0 .. p,
+ *     o[t,h,:] = sum_j softmax_j(s q[t,h,:] . k_j) v_j,  lse[t,h] = log sum_j exp(s q . k_j).
+ *   q device bf16, token t, head h at q + t q_stride + h D, 16-byte aligned, q_stride a multiple
+ *   of 8; o device bf16 THD [T, Hq, D] and lse device fp32 [T, Hq] (written).  A token that
+ *   sees no key (position < 0) gets o = 0, lse = -inf.  What lies in a page behind its
+ *   sequence's length may be anything (NaN as well).  One pass over the keys with the running
+ *   maximum and sum in fp32; long sequences are split over CTAs and joined in a fixed order.
+ *   max_new, max_len: host bounds on the new tokens and the length of any entry; an entry
+ *   above them sets the device status and gets o = 0, lse = -inf.
+ *   group, shared_len: with group > 1 (S a multiple of it) the entries come in groups that
+ *   share their first pages: entries i group .. (i + 1) group - 1 list the same pages for the
+ *   first shared_len[i] tokens (device int32 [S / group]), which are then read once for the
+ *   whole group.  The result is that without it.  group = 1, shared_len = NULL: no sharing.
+ *   workspace device, 16-byte aligned, >= ls_cache_attn_workspace_bytes(h, S, T, max_new,
+ *   max_len) bytes (whatever the group).
+ */
+typedef struct {
+  int32_t S;
+  int64_t T;
+  const int32_t* rows;
+  const int32_t* cu_new;
+  const void* k_new;
+  int64_t k_stride;
+  const void* v_new;
+  int64_t v_stride;
+  const void* q;
+  int64_t q_stride;
+  void* q_out;
+  int64_t q_out_stride;
+  const double* inv_freq;
+  int32_t rot_dim, interleaved;
+  double attn_factor;
+} ls_cache_append_desc;
+ls_status ls_cache_append(ls_cache_t h, const ls_cache_append_desc* d, void* stream);
+
+typedef struct {
+  int32_t S;
+  int64_t T;
+  const int32_t* rows;
+  const int32_t* cu_new;
+  int32_t max_new;
+  int64_t max_len;
+  const void* q;
+  int64_t q_stride;
+  void* o;
+  float* lse;
+  int32_t group;
+  const int32_t* shared_len;
+} ls_cache_attn_desc;
+size_t ls_cache_attn_workspace_bytes(ls_cache_t h, int32_t S, int64_t T, int32_t max_new,
+                                     int64_t max_len);
+ls_status ls_cache_attn(ls_cache_t h, const ls_cache_attn_desc* d, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/*
  * Context-parallel prompt sharding (LongStraw review, section 3-2 (2) "Physical page
  * ownership": each rank owns a slice of the prompt's K/V pages; local attention results are
  * combined by a cross-rank log-sum-exp and output merge).  Every shard is its own handle
@@ -345,7 +599,8 @@ ls_status ls_prefix_grad_finalize_rows(ls_prefix_t h, int64_t row0, int64_t nrow
 /*
  * Read (and clear) the device status word of the current device: synchronises `stream`,
  * returns LS_OK, LS_ERR_TIMEOUT or LS_ERR_DEVICE_STATUS.  *bits (may be NULL) receives
- * the raw word (1 = a bounded wait gave up, 2 = an index was outside its buffer).
+ * the raw word (1 = a bounded wait gave up, 2 = an index was outside its buffer, 4 = no free
+ * page was left).
  */
 ls_status ls_get_device_status(void* stream, uint32_t* bits);
 
@@ -368,7 +623,12 @@ typedef enum {
   LS_KERNEL_MERGE = 8,         /* context-parallel partial-attention merge        */
   LS_KERNEL_SUM = 9,           /* context-parallel dQ part sum                    */
   LS_KERNEL_CAST = 10,         /* context-parallel bf16 <-> fp32 conversions      */
-  LS_KERNEL_COUNT = 11
+  LS_KERNEL_POLICY_LOSS = 11,  /* policy loss with the KL term, row pass and reduction */
+  LS_KERNEL_ROPE = 12,         /* rotary positions                                */
+  LS_KERNEL_CACHE_APPEND = 13, /* new keys and values into pages                  */
+  LS_KERNEL_CACHE_ATTN = 14,   /* attention over pages, and the join of its parts */
+  LS_KERNEL_CACHE_PAGES = 15,  /* extend, fork, free, compact, reset              */
+  LS_KERNEL_COUNT = 16
 } ls_kernel_id;
 
 ls_status ls_timing_enable(int enable);

@@ -40,6 +40,58 @@ class PrefixDesc(ctypes.Structure):
                 ("dk_acc", ctypes.c_void_p), ("dv_acc", ctypes.c_void_p)]
 
 
+class PolicyLossDesc(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("V", ctypes.c_int64), ("logits_stride", ctypes.c_int64),
+                ("dlogits_stride", ctypes.c_int64), ("logits", ctypes.c_void_p),
+                ("ids", ctypes.c_void_p), ("logp_old", ctypes.c_void_p),
+                ("logp_ref", ctypes.c_void_p), ("advantages", ctypes.c_void_p),
+                ("weights", ctypes.c_void_p), ("eps_low", ctypes.c_double),
+                ("eps_high", ctypes.c_double), ("beta", ctypes.c_double), ("kl", ctypes.c_int32),
+                ("loss", ctypes.c_void_p), ("dlogits", ctypes.c_void_p),
+                ("clip_mask", ctypes.c_void_p), ("logp_out", ctypes.c_void_p),
+                ("kl_out", ctypes.c_void_p)]
+
+
+class RopeDesc(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("Hq", ctypes.c_int32), ("Hk", ctypes.c_int32),
+                ("D", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("inverse", ctypes.c_int32),
+                ("inv_freq", ctypes.c_void_p), ("attn_factor", ctypes.c_double),
+                ("positions", ctypes.c_void_p), ("pos0", ctypes.c_int64),
+                ("q", ctypes.c_void_p), ("q_stride", ctypes.c_int64),
+                ("q_out", ctypes.c_void_p), ("q_out_stride", ctypes.c_int64),
+                ("k", ctypes.c_void_p), ("k_stride", ctypes.c_int64),
+                ("k_out", ctypes.c_void_p), ("k_out_stride", ctypes.c_int64)]
+
+
+class CacheDesc(ctypes.Structure):
+    _fields_ = [("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int32),
+                ("Hq", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("D", ctypes.c_int32),
+                ("layout", ctypes.c_int32), ("softmax_scale", ctypes.c_float),
+                ("page_stride", ctypes.c_int64), ("k_pages", ctypes.c_void_p),
+                ("v_pages", ctypes.c_void_p), ("num_rows", ctypes.c_int32),
+                ("table_width", ctypes.c_int32), ("page_table", ctypes.c_void_p),
+                ("seq_len", ctypes.c_void_p), ("refcount", ctypes.c_void_p)]
+
+
+class CacheAppendDesc(ctypes.Structure):
+    _fields_ = [("S", ctypes.c_int32), ("T", ctypes.c_int64), ("rows", ctypes.c_void_p),
+                ("cu_new", ctypes.c_void_p), ("k_new", ctypes.c_void_p),
+                ("k_stride", ctypes.c_int64), ("v_new", ctypes.c_void_p),
+                ("v_stride", ctypes.c_int64), ("q", ctypes.c_void_p), ("q_stride", ctypes.c_int64),
+                ("q_out", ctypes.c_void_p), ("q_out_stride", ctypes.c_int64),
+                ("inv_freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("attn_factor", ctypes.c_double)]
+
+
+class CacheAttnDesc(ctypes.Structure):
+    _fields_ = [("S", ctypes.c_int32), ("T", ctypes.c_int64), ("rows", ctypes.c_void_p),
+                ("cu_new", ctypes.c_void_p), ("max_new", ctypes.c_int32),
+                ("max_len", ctypes.c_int64), ("q", ctypes.c_void_p), ("q_stride", ctypes.c_int64),
+                ("o", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("group", ctypes.c_int32),
+                ("shared_len", ctypes.c_void_p)]
+
+
 def _load():
     if not os.path.exists(library_path):
         raise RuntimeError("liblongstraw.so is not built (run long_context_grpo_gb300/build.py); "
@@ -75,6 +127,22 @@ def _load():
         "ls_replay_bwd_packed": (ctypes.c_int, [vp, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp,
                                                 vp, sz, vp]),
         "ls_block_replay_bwd": (ctypes.c_int, [vp, i64, i64, vp, vp, vp, vp, vp, vp, sz, vp]),
+        "ls_policy_loss_workspace_bytes": (sz, [i64]),
+        "ls_policy_loss": (ctypes.c_int, [ctypes.POINTER(PolicyLossDesc), vp, sz, vp]),
+        "ls_rope": (ctypes.c_int, [ctypes.POINTER(RopeDesc), vp]),
+        "ls_rope_freqs": (ctypes.c_int, [i32, ctypes.c_double, i32, ctypes.c_double, i64,
+                                         ctypes.c_double, ctypes.c_double, vp, vp]),
+        "ls_cache_create": (ctypes.c_int, [ctypes.POINTER(CacheDesc), ctypes.POINTER(vp)]),
+        "ls_cache_destroy": (ctypes.c_int, [vp]),
+        "ls_cache_reset": (ctypes.c_int, [vp, vp]),
+        "ls_cache_pages_workspace_bytes": (sz, [vp]),
+        "ls_cache_extend": (ctypes.c_int, [vp, i32, vp, vp, vp, sz, vp]),
+        "ls_cache_fork": (ctypes.c_int, [vp, i32, vp, vp, vp, sz, vp]),
+        "ls_cache_free": (ctypes.c_int, [vp, i32, vp, vp]),
+        "ls_cache_compact": (ctypes.c_int, [vp, vp, vp, vp, sz, vp]),
+        "ls_cache_append": (ctypes.c_int, [vp, ctypes.POINTER(CacheAppendDesc), vp]),
+        "ls_cache_attn_workspace_bytes": (sz, [vp, i32, i64, i32, i64]),
+        "ls_cache_attn": (ctypes.c_int, [vp, ctypes.POINTER(CacheAttnDesc), vp, sz, vp]),
         "ls_get_device_status": (ctypes.c_int, [vp, ctypes.POINTER(ctypes.c_uint32)]),
         "ls_timing_enable": (ctypes.c_int, [ctypes.c_int]),
         "ls_debug_wait_timeout": (ctypes.c_int, [ctypes.c_uint64, vp]),
@@ -407,7 +475,8 @@ def grpo_loss(logits, ids, logp_old, advantage: float, eps: float, G: int, loss_
 
 
 KERNEL_NAMES = ("zero", "replay_fwd", "bwd_prep", "bwd_dkdv", "bwd_dq", "grpo_loss", "finalize",
-                "token_logp", "merge", "sum", "cast")
+                "token_logp", "merge", "sum", "cast", "policy_loss", "rope", "cache_append",
+                "cache_attn", "cache_pages")
 
 
 def timing_enable(on: bool = True):

@@ -20,8 +20,9 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "liblongstraw.so")
 
 SOURCES = ["ls_api.cu", "k_loss.cu", "k_elementwise.cu", "k_attn_fwd.cu", "k_attn_bwd.cu",
-           "ls_noalloc.cu"]
-HEADERS = ["ls_internal.h", "ptx.cuh"]
+           "ls_noalloc.cu", "ls_ops.cu", "ls_cache.cu", "k_policy.cu", "k_rope.cu", "k_pages.cu",
+           "k_cache_attn.cu"]
+HEADERS = ["ls_internal.h", "ptx.cuh", "ls_host.h", "ls_ops.h", "ls_rope_host.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE]
 

@@ -6,8 +6,6 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
-#include <nvtx3/nvToolsExt.h>
-
 #include <atomic>
 #include <cmath>
 #include <cstdio>
@@ -17,6 +15,7 @@
 #include <vector>
 
 #include "../../include/longstraw.h"
+#include "ls_host.h"
 #include "ls_internal.h"
 #include "ptx.cuh"
 
@@ -66,15 +65,6 @@ ls_status cuda_fail(cudaError_t e, const char* what) {
   return LS_ERR_CUDA;
 }
 
-// One NVTX range per API call (visible to profilers; no-op without one attached).
-struct NvtxRange {
-  explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
-  ~NvtxRange() { nvtxRangePop(); }
-};
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0u; }
-bool aligned_n(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0u; }
-
 ls_status current_device(int* dev) {
   cudaError_t e = cudaGetDevice(dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
@@ -97,8 +87,14 @@ ls_status status_ptr(int dev, uint32_t** out) {
 
 ls_status check_stream(void* stream, int dev) {
   if (stream == nullptr) return LS_OK;
+  // A stream that is being captured may not be asked for its device; a launch into a stream of
+  // another device fails by itself there.
+  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+  cudaError_t e = cudaStreamIsCapturing(static_cast<cudaStream_t>(stream), &cap);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaStreamIsCapturing");
+  if (cap != cudaStreamCaptureStatusNone) return LS_OK;
   int sdev = -1;
-  cudaError_t e = cudaStreamGetDevice(static_cast<cudaStream_t>(stream), &sdev);
+  e = cudaStreamGetDevice(static_cast<cudaStream_t>(stream), &sdev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaStreamGetDevice");
   return sdev == dev ? LS_OK : LS_ERR_WRONG_DEVICE;
 }
@@ -119,19 +115,16 @@ ls_status get_encoder() {
   return LS_OK;
 }
 
-// 3-D bf16 THD tensor [T][H][D] with a {64, hbox, tbox} box and 128-byte swizzle.
-ls_status encode_thd(CUtensorMap* m, const void* base, int64_t T, int H, int D, int hbox,
-                     int tbox) {
+}  // namespace
+
+int encode_bf16_map(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims,
+                    const cuuint64_t* strides, const cuuint32_t* box) {
   ls_status st = get_encoder();
   if (st != LS_OK) return st;
-  cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(H),
-                        static_cast<cuuint64_t>(T)};
-  cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2u,
-                           static_cast<cuuint64_t>(H) * static_cast<cuuint64_t>(D) * 2u};
-  cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(hbox), static_cast<cuuint32_t>(tbox)};
-  cuuint32_t es[3] = {1u, 1u, 1u};
-  CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
-                        strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  cuuint32_t es[5] = {1u, 1u, 1u, 1u, 1u};
+  CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank),
+                        const_cast<void*>(base), dims, strides, box, es,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) {
     snprintf(t_last_error, sizeof(t_last_error), "cuTensorMapEncodeTiled failed (%d)",
@@ -141,7 +134,18 @@ ls_status encode_thd(CUtensorMap* m, const void* base, int64_t T, int H, int D, 
   return LS_OK;
 }
 
-size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+namespace {
+
+// 3-D bf16 THD tensor [T][H][D] with a {64, hbox, tbox} box and 128-byte swizzle.
+ls_status encode_thd(CUtensorMap* m, const void* base, int64_t T, int H, int D, int hbox,
+                     int tbox) {
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(H),
+                        static_cast<cuuint64_t>(T)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2u,
+                           static_cast<cuuint64_t>(H) * static_cast<cuuint64_t>(D) * 2u};
+  cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(hbox), static_cast<cuuint32_t>(tbox)};
+  return static_cast<ls_status>(encode_bf16_map(m, base, 3, dims, strides, box));
+}
 
 // ----- optional per-launch timing (ls_timing_enable / ls_timing_read)
 struct TimedLaunch {
@@ -164,30 +168,21 @@ cudaEvent_t take_event() {
   return e;
 }
 
-// Brackets the launches made during its lifetime when timing is enabled.
-class LaunchTimer {
- public:
-  LaunchTimer(int kernel, cudaStream_t s) : kernel_(kernel), s_(s) {
-    std::lock_guard<std::mutex> lk(g_timing_mu);
-    if (!g_timing) return;
-    start_ = take_event();
-    stop_ = take_event();
-    if (start_ && stop_) cudaEventRecord(start_, s_);
-  }
-  ~LaunchTimer() {
-    if (!start_ || !stop_) return;
-    cudaEventRecord(stop_, s_);
-    std::lock_guard<std::mutex> lk(g_timing_mu);
-    g_timed.push_back({kernel_, start_, stop_});
-  }
-
- private:
-  int kernel_;
-  cudaStream_t s_;
-  cudaEvent_t start_ = nullptr, stop_ = nullptr;
-};
-
 }  // namespace
+
+LaunchTimer::LaunchTimer(int kernel, cudaStream_t s) : kernel_(kernel), s_(s) {
+  std::lock_guard<std::mutex> lk(g_timing_mu);
+  if (!g_timing) return;
+  start_ = take_event();
+  stop_ = take_event();
+  if (start_ && stop_) cudaEventRecord(start_, s_);
+}
+LaunchTimer::~LaunchTimer() {
+  if (!start_ || !stop_) return;
+  cudaEventRecord(stop_, s_);
+  std::lock_guard<std::mutex> lk(g_timing_mu);
+  g_timed.push_back({kernel_, start_, stop_});
+}
 
 int num_sms() {
   int dev = 0;

@@ -17,6 +17,7 @@ enum : uint32_t {
   DEV_OK = 0u,
   DEV_WAIT_TIMEOUT = 1u,       // a bounded mbarrier wait gave up
   DEV_BAD_INDEX = 2u,          // a checked index fell outside its buffer
+  DEV_NO_PAGES = 4u,           // a cache had no free page left for an entry
 };
 
 // A wait that has not completed after this many nanoseconds of %globaltimer gives up.
