@@ -3,8 +3,38 @@
 //   o = softmax(s q K^T) V over the keys 0 .. position of the token's own sequence,
 //   lse = log sum exp(s q k)
 //
-// One warp per (new token, query head): a pass over the keys with the running maximum and sum in
-// fp32, a key's dot product summed over the warp.
+// Three kernels, each started while the one before drains (programmatic launch):
+//
+// cache_plan_kernel (one block).  The lengths live on the device, so the work is cut there.  A
+//   segment is a run of packed tokens and a run of 128-key tiles of one table row: a sequence's
+//   tokens over its keys, or, for a group with shared pages, all the group's tokens over the
+//   shared keys (read once) and each sequence's over the rest.  Key runs are split into
+//   chunks so that the tile counts of all SMs come out even (the chunk length with the least
+//   estimated makespan of 15 candidates); a segment of more than one chunk, or a token in two
+//   segments, leaves partial results.  Output: lists of jobs.
+//
+// cache_attn_kernel<D, wide> (persistent, 384 threads).  Warp 0 feeds Q, K and V by TMA (pages
+//   of 16 .. 256 tokens: a 128-key tile is 128 / page_size boxes), warp 1 issues tcgen05.mma,
+//   warps 4-7 and 8-11 are the softmax of two streams (thread = TMEM lane = (token, head)
+//   row; running maximum and sum in fp32, O rescaled in TMEM only when the maximum grows by
+//   more than 2^8).
+//   wide: segments of more than 64 rows.  The two streams are two 128-row Q tiles that use
+//     the same K and V tiles; bound by the tensor pipe.
+//   narrow: at most 64 rows (a token or a few per sequence).  The two streams are two
+//     independent jobs with K/V tiles of their own, so one's softmax hides the other's loads;
+//     Q takes 16 KB instead of 32, which leaves room for three K and three V tiles in flight
+//     (192 KB an SM).  M = 128 MMAs with most rows idle still take less than half the time that
+//     the tile's 64 KB take from HBM; bound by HBM.
+//
+// cache_join_kernel.  Combines a token's partial results in chunk order (deterministic), and
+//   writes zeros for tokens that see no key.
+//
+// V rows behind a sequence's end are cleared in shared memory before the MMA (0 x NaN); pages
+// outside the pool read as zeros (the TMA's fill).  P is rounded to bf16 for the tensor cores, the
+// sum is taken before that rounding.  Every wait is bounded as in the replay kernels.
+#include <climits>
+#include <utility>
+
 #include "ls_internal.h"
 #include "ls_ops.h"
 #include "ptx.cuh"
@@ -12,87 +42,1084 @@
 namespace ls {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 384;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kRescaleLog2 = 8.0f;
+constexpr int kNarrowRows = 64;
+constexpr int kMaxTiles = 1 << 24;     // 128-key tiles of the longest sequence
 
-template <int D>
-__global__ void __launch_bounds__(kThreads) cache_attn_warp(const __grid_constant__ CacheAttnArgs a) {
-  constexpr int kPer = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int64_t item = blockIdx.x * static_cast<int64_t>(kThreads / 32) + (threadIdx.x >> 5);
-  if (item >= a.T * a.c.Hq) return;
-  const int64_t t = item / a.c.Hq;
-  const int h = static_cast<int>(item - t * a.c.Hq);
-  int b = 0;
-  for (int i = lane; i < a.S; i += 32) b += (a.cu[i + 1] <= t) ? 1 : 0;
+// A run of packed tokens over a run of key tiles of one table row.
+struct Seg {
+  int t0, n_tok;
+  int row;
+  int lim;          // token t sees lim + t keys; INT_MIN: lims[t]
+  int tile0, tiles; // first 128-key tile, tiles in all
+  int key_end;      // keys from here on are not read
+  int chunk, chunks;
+  int part;         // first row of its partial results; -1: written to the output
+  int pad[2];
+};
+// One (key head, chunk) of a segment, for one Q tile (narrow) or two (wide).
+struct Job {
+  int t0, n_tok, row, lim;
+  int tile0, n_tiles, key_end, kv;
+  int part;         // row of its first token's first head among the partial rows; -1: output
+  int pad[3];
+};
+struct Info {
+  int n_jobs[2];    // narrow, wide
+  int grouped;
+};
+
+__device__ __forceinline__ int qt_of(int g, bool wide) { return (wide ? 128 : kNarrowRows) / g; }
+__device__ __forceinline__ bool is_wide(const Seg& s, int g) { return s.n_tok > kNarrowRows / g; }
+
+// Key tiles that tokens t0 .. t0 + n - 1 of a segment need at most.
+__device__ __forceinline__ int tiles_of(const Seg& s, int t_end) {
+  if (s.lim == INT_MIN) return s.tiles;
+  const int keys = s.lim + t_end - 1 - 128 * s.tile0;
+  const int n = keys <= 0 ? 0 : (keys + 127) / 128;
+  return n < s.tiles ? n : s.tiles;
+}
+
+__device__ __forceinline__ int plan_scan(int v, int* sh, int* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int s = v;
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) b += __shfl_xor_sync(0xffffffffu, b, off);
-  if (b >= a.S || t < a.cu[b]) return;
-  const int row = a.rows != nullptr ? a.rows[b] : b;
-  const int n = a.cu[b + 1] - a.cu[b];
-  int64_t len = 0;
-  bool bad = row < 0 || row >= a.c.num_rows || n > a.max_new;
-  if (!bad) {
-    len = a.c.len[row];
-    bad = len < 0 || len > a.max_len || len > (static_cast<int64_t>(a.c.width) << a.c.ps_log2);
+  for (int off = 1; off < 32; off <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, s, off);
+    if (lane >= off) s += u;
   }
-  if (bad && lane == 0) set_device_status(a.status, DEV_BAD_INDEX);
-  const int64_t keys = bad ? 0 : len - (a.cu[b + 1] - t) + 1;
-  const int kv = h / (a.c.Hq / a.c.Hkv);
-  const int ps = 1 << a.c.ps_log2;
-  float q[kPer], acc[kPer];
+  __syncthreads();
+  if (lane == 31) sh[warp] = s;
+  __syncthreads();
+  if (warp == 0) {
+    int w = sh[lane];
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    q[i] = __uint_as_float(static_cast<uint32_t>(a.q[t * a.qs + h * D + lane + 32 * i]) << 16);
-    acc[i] = 0.0f;
+    for (int off = 1; off < 32; off <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, w, off);
+      if (lane >= off) w += u;
+    }
+    sh[lane] = w;
   }
-  float m = -INFINITY, l = 0.0f;
-  for (int64_t k0 = 0; k0 < keys; k0 += ps) {
-    const int page = a.c.table[static_cast<int64_t>(row) * a.c.width + (k0 >> a.c.ps_log2)];
-    const bool in = page >= 0 && page < a.c.num_pages;
-    if (!in && lane == 0) set_device_status(a.status, DEV_BAD_INDEX);
-    const int64_t base = (in ? page : 0) * a.c.page_stride + kv * a.c.head_stride;
-    const int cnt = keys - k0 < ps ? static_cast<int>(keys - k0) : ps;
-    for (int j = 0; j < cnt; ++j) {
-      const int64_t at = base + j * a.c.tok_stride + lane;
-      float d = 0.0f, v[kPer];
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        v[i] = 0.0f;
-        if (in) {
-          d = fmaf(q[i], __uint_as_float(static_cast<uint32_t>(a.c.k[at + 32 * i]) << 16), d);
-          v[i] = __uint_as_float(static_cast<uint32_t>(a.c.v[at + 32 * i]) << 16);
+  __syncthreads();
+  *total = sh[31];
+  return (warp > 0 ? sh[warp - 1] : 0) + s - v;
+}
+
+constexpr int kPlanThreads = 1024;
+constexpr int kMaxSegs = kMaxSeqs + kMaxSeqs / 2;
+
+struct PlanArgs {
+  CacheView c;
+  int S;
+  int64_t T;
+  const int32_t* rows;
+  const int32_t* cu;
+  int max_new;
+  int64_t max_len;
+  int group;
+  const int32_t* shared;
+  uint8_t* ws;
+  CacheAttnLayout l;
+  int sms;
+  uint32_t* status;
+};
+
+__global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const __grid_constant__ PlanArgs a) {
+  extern __shared__ int dyn[];
+  int* first = dyn;                       // jobs of each class before a segment: [2][kMaxSegs + 1]
+  __shared__ int sh[33];
+  __shared__ int sh_max[2], sh_c[2], sh_grouped;
+  __shared__ unsigned long long sh_w[2];
+  __shared__ unsigned long long best[2];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = a.c.Hq / a.c.Hkv;
+  Info* info = reinterpret_cast<Info*>(a.ws + a.l.info);
+  Seg* segs = reinterpret_cast<Seg*>(a.ws + a.l.segs);
+  int* lims = reinterpret_cast<int*>(a.ws + a.l.lims);
+  pdl_launch_dependents();
+
+  if (tid < 2) {
+    sh_max[tid] = 0;
+    sh_w[tid] = 0;
+    best[tid] = ~0ull;
+  }
+  __syncthreads();
+
+  // the entries: tokens, table row, length
+  for (int b = tid; b < a.S; b += kPlanThreads) {
+    Seg s;
+    const int c0 = a.cu[b], c1 = a.cu[b + 1];
+    const bool run = c0 >= 0 && c1 >= c0 && c1 <= a.T;
+    s.t0 = run ? c0 : 0;
+    s.n_tok = run ? c1 - c0 : 0;
+    s.row = a.rows != nullptr ? a.rows[b] : b;
+    bool ok = run && (s.n_tok == 0 || (s.row >= 0 && s.row < a.c.num_rows && s.n_tok <= a.max_new));
+    int64_t len = 0;
+    if (run && s.n_tok == 0) {
+      s.row = -1;              // nothing new: not looked at
+    } else if (ok) {
+      len = a.c.len[s.row];
+      ok = len >= 0 && len <= a.max_len && len <= (static_cast<int64_t>(a.c.width) << a.c.ps_log2);
+    }
+    if (!ok) {
+      set_device_status(a.status, DEV_BAD_INDEX);
+      len = 0;
+      s.row = -1;
+    }
+    s.key_end = static_cast<int>(len);
+    s.lim = s.key_end - (run ? c1 : 0) + 1;
+    s.tile0 = 0;
+    s.tiles = s.n_tok > 0 ? static_cast<int>((len + 127) / 128) : 0;
+    s.chunk = s.chunks = 0;
+    s.part = -1;
+    segs[b] = s;
+  }
+  // groups: the shared keys as one segment, if the partial rows of both parts fit
+  const int n_groups = a.group > 1 ? a.S / a.group : 0;
+  if (tid == 0)
+    sh_grouped = n_groups > 0 && 2 * a.T * a.c.Hq <= a.l.rows_narrow &&
+                 (a.l.rows_wide == 0 || 2 * a.T * a.c.Hq <= a.l.rows_wide);
+  __syncthreads();
+  const bool grouped = sh_grouped != 0;
+  const int n_segs = a.S + (grouped ? n_groups : 0);
+  if (grouped) {
+    for (int i = tid; i < n_groups; i += kPlanThreads) {
+      int lead = -1;
+      for (int b = i * a.group; b < (i + 1) * a.group; ++b)
+        if (segs[b].row >= 0 && lead < 0) lead = b;
+      int sh_len = lead < 0 ? 0 : a.shared[i];
+      if (sh_len < 0) sh_len = 0;
+      if (lead >= 0 && sh_len > segs[lead].key_end) sh_len = segs[lead].key_end;
+      const int tiles = sh_len / 128;
+      Seg s;
+      s.t0 = a.cu[i * a.group];
+      const int t1 = a.cu[(i + 1) * a.group];
+      const bool run = s.t0 >= 0 && t1 >= s.t0 && t1 <= a.T;
+      if (!run) s.t0 = 0;
+      s.n_tok = run ? t1 - s.t0 : 0;
+      s.row = lead < 0 ? 0 : segs[lead].row;
+      s.lim = INT_MIN;
+      s.tile0 = 0;
+      s.tiles = run && s.n_tok > 0 ? tiles : 0;
+      s.key_end = tiles * 128;
+      s.chunk = s.chunks = 0;
+      s.part = -1;
+      segs[a.S + i] = s;
+      if (s.tiles > 0)
+        for (int b = i * a.group; b < (i + 1) * a.group; ++b) {
+          const int rest = segs[b].tiles - s.tiles;
+          segs[b].tile0 = s.tiles;
+          segs[b].tiles = rest > 0 ? rest : 0;
         }
+    }
+    __syncthreads();
+    for (int b = warp; b < a.S; b += kPlanThreads / 32) {
+      const Seg s = segs[b];
+      for (int i = lane; i < s.n_tok; i += 32) {
+        const int n = s.row < 0 ? 0 : s.lim + s.t0 + i;
+        lims[s.t0 + i] = n < 0 ? 0 : n;
       }
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
-      d *= a.scale;
-      const float mn = fmaxf(m, d);
-      const float f = mn == -INFINITY ? 1.0f : expf(m - mn), p = mn == -INFINITY ? 0.0f : expf(d - mn);
-      m = mn;
-      l = l * f + p;
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) acc[i] = fmaf(acc[i], f, p * v[i]);
     }
   }
-  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  __syncthreads();
+
+  // work of each class, in key tiles of one Q tile (narrow) or pair of them (wide)
+  for (int i = tid; i < n_segs; i += kPlanThreads) {
+    const Seg& s = segs[i];
+    const bool w = is_wide(s, g);
+    const int pairs = w ? (s.n_tok + 2 * qt_of(g, true) - 1) / (2 * qt_of(g, true)) : 1;
+    if (s.tiles > 0) {
+      atomicAdd(&sh_w[w], static_cast<unsigned long long>(a.c.Hkv) * pairs * s.tiles);
+      atomicMax(&sh_max[w], s.tiles);
+    }
+  }
+  __syncthreads();
+  // candidates: warp = (class, k): chunks that make k rounds of jobs over all streams
+  {
+    const int cls = warp >> 4, k = (warp & 15) + 1;
+    const int round = cls ? a.sms : 2 * a.sms;
+    const int longest = sh_max[cls];
+    const unsigned long long W = sh_w[cls];
+    int C = k == 16 ? longest : static_cast<int>((W + static_cast<unsigned long long>(round) * k - 1) /
+                                                 (static_cast<unsigned long long>(round) * k));
+    if (C < (cls ? 8 : 2)) C = cls ? 8 : 2;
+    if (C > longest) C = longest;
+    if (longest > 0) {
+      unsigned long long jobs = 0, rows = 0;
+      for (int i = lane; i < n_segs; i += 32) {
+        const Seg& s = segs[i];
+        if (s.tiles == 0 || is_wide(s, g) != (cls == 1)) continue;
+        const int chunks = (s.tiles + C - 1) / C;
+        const int pairs = cls ? (s.n_tok + 2 * qt_of(g, true) - 1) / (2 * qt_of(g, true)) : 1;
+        jobs += static_cast<unsigned long long>(a.c.Hkv) * pairs * chunks;
+        const bool two = grouped && segs[a.S + (i < a.S ? i / a.group : i - a.S)].tiles > 0;
+        if (chunks > 1 || two) rows += static_cast<unsigned long long>(a.c.Hq) * chunks * s.n_tok;
+      }
 #pragma unroll
-  for (int i = 0; i < kPer; ++i)
-    a.o[(t * a.c.Hq + h) * D + lane + 32 * i] =
-        static_cast<uint16_t>(pack_bf16x2(acc[i] * inv, 0.0f) & 0xFFFFu);
-  if (lane == 0) a.lse[t * a.c.Hq + h] = l > 0.0f ? m + logf(l) : -INFINITY;
+      for (int off = 16; off > 0; off >>= 1) {
+        jobs += __shfl_xor_sync(0xffffffffu, jobs, off);
+        rows += __shfl_xor_sync(0xffffffffu, rows, off);
+      }
+      const unsigned long long cap = cls ? a.l.max_wide : a.l.max_narrow;
+      const unsigned long long most = cls ? a.l.rows_wide : a.l.rows_narrow;
+      if (lane == 0 && jobs <= cap && rows <= most) {
+        // makespan in tiles: whole rounds, and what a job costs beside its tiles
+        const unsigned long long cost = ((jobs + round - 1) / round) * (C + (cls ? 6 : 3));
+        atomicMin(&best[cls], (cost << 25) | static_cast<unsigned long long>(kMaxTiles - C));
+      }
+    }
+  }
+  __syncthreads();
+  if (tid < 2) sh_c[tid] = best[tid] == ~0ull ? kMaxTiles : kMaxTiles - static_cast<int>(best[tid] & 0x1FFFFFF);
+  __syncthreads();
+
+  // chunks, partial rows and jobs of every segment
+  int base[2] = {0, 0};
+  int64_t part[2] = {0, a.l.rows_narrow};
+  for (int i0 = 0; i0 < n_segs; i0 += kPlanThreads) {
+    const int i = i0 + tid;
+    int jobs = 0, rows = 0, w = 0;
+    if (i < n_segs) {
+      Seg& s = segs[i];
+      w = is_wide(s, g) ? 1 : 0;
+      if (s.tiles > 0) {
+        const int C = sh_c[w];
+        s.chunks = (s.tiles + C - 1) / C;
+        s.chunk = (s.tiles + s.chunks - 1) / s.chunks;
+        s.chunks = (s.tiles + s.chunk - 1) / s.chunk;
+        const int pairs = w ? (s.n_tok + 2 * qt_of(g, true) - 1) / (2 * qt_of(g, true)) : 1;
+        jobs = a.c.Hkv * pairs * s.chunks;
+        const bool two = grouped && segs[a.S + (i < a.S ? i / a.group : i - a.S)].tiles > 0;
+        if (s.chunks > 1 || two) rows = a.c.Hq * s.chunks * s.n_tok;
+      }
+    }
+#pragma unroll
+    for (int cls = 0; cls < 2; ++cls) {
+      int total;
+      const int at = plan_scan(w == cls ? jobs : 0, sh, &total);
+      if (i < n_segs) first[cls * (kMaxSegs + 1) + i] = base[cls] + at;
+      base[cls] += total;
+      const int pr = plan_scan(w == cls ? rows : 0, sh, &total);
+      if (i < n_segs && w == cls && rows > 0) segs[i].part = static_cast<int>(part[cls] + pr);
+      part[cls] += total;
+    }
+  }
+  __syncthreads();
+  if (tid == 0) {
+    info->n_jobs[0] = base[0];
+    info->n_jobs[1] = base[1];
+    info->grouped = grouped ? 1 : 0;
+  }
+
+  // the job lists
+#pragma unroll 1
+  for (int cls = 0; cls < 2; ++cls) {
+    Job* jobs = reinterpret_cast<Job*>(a.ws + (cls ? a.l.wide : a.l.narrow));
+    const int* f = first + cls * (kMaxSegs + 1);
+    for (int x = tid; x < base[cls]; x += kPlanThreads) {
+      int lo = 0, hi = n_segs - 1;           // the last segment that starts at or before x
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (f[mid] <= x) lo = mid; else hi = mid - 1;
+      }
+      const Seg s = segs[lo];
+      int y = x - f[lo];
+      Job j;
+      j.row = s.row;
+      j.lim = s.lim;
+      j.key_end = s.key_end;
+      int chunk;
+      if (cls == 0) {
+        // key heads of one chunk side by side: neighbours in memory
+        j.kv = y % a.c.Hkv;
+        chunk = y / a.c.Hkv;
+        j.t0 = s.t0;
+        j.n_tok = s.n_tok;
+      } else {
+        // Q tiles of one (chunk, key head) side by side: they share its K and V through L2;
+        // the last tokens, which see most keys, first
+        const int per = 2 * qt_of(g, true);
+        const int pairs = (s.n_tok + per - 1) / per;
+        const int p = pairs - 1 - y % pairs;
+        y /= pairs;
+        j.kv = y % a.c.Hkv;
+        chunk = y / a.c.Hkv;
+        j.t0 = s.t0 + p * per;
+        j.n_tok = s.n_tok - p * per < per ? s.n_tok - p * per : per;
+      }
+      const int tiles = tiles_of(s, j.t0 + j.n_tok);
+      j.tile0 = s.tile0 + chunk * s.chunk;
+      j.n_tiles = tiles - chunk * s.chunk;
+      j.n_tiles = j.n_tiles < 0 ? 0 : (j.n_tiles > s.chunk ? s.chunk : j.n_tiles);
+      // rows of the partial results: [kv][chunk][token][head of the group]
+      j.part = s.part < 0 ? -1 : s.part + ((j.kv * s.chunks + chunk) * s.n_tok + (j.t0 - s.t0)) * g;
+      jobs[x] = j;
+    }
+  }
 }
+
+// --------------------------------------------------------------------------------------
+template <int D, bool kWide>
+struct Cfg {
+  static constexpr int kBoxes = D / 64;
+  static constexpr int kTile = 128 * D * 2;
+  static constexpr int kQRows = kWide ? 128 : kNarrowRows;
+  static constexpr int kQBox = kQRows * 128;               // bytes of one 64-column box of Q
+  static constexpr int kQTile = kQBox * kBoxes;
+  static constexpr int kN = (kWide ? 2 : 3) * (D == 128 ? 1 : 2);   // K (and V) ring stages
+  static constexpr int kOffK = 2 * kQTile;
+  static constexpr int kOffV = kOffK + kN * kTile;
+  static constexpr int kOffBar = kOffV + kN * kTile;
+  static constexpr int kBarQFull = 0, kBarQEmpty = 1, kBarKFull = 2;
+  static constexpr int kBarKEmpty = kBarKFull + kN;
+  static constexpr int kBarVFull = kBarKEmpty + kN;
+  static constexpr int kBarVEmpty = kBarVFull + kN;
+  static constexpr int kBarSFull = kBarVEmpty + kN;
+  static constexpr int kBarPFull = kBarSFull + 2;          // [stream][half]
+  static constexpr int kBarODone = kBarPFull + 4;
+  static constexpr int kBarOFree = kBarODone + 2;
+  static constexpr int kBarDrain = kBarOFree + 2;
+  static constexpr int kNumBars = kBarDrain + 1;
+  static constexpr int kSmem = kOffBar + kNumBars * 8 + 16 + 1024;
+  __host__ __device__ static constexpr uint32_t col_s(int q) { return 128u * q; }
+  __host__ __device__ static constexpr uint32_t col_o(int q) { return 256u + D * q; }
+};
+
+struct AttnArgs {
+  CacheView c;
+  float scale;
+  int layout;
+  const Job* jobs;
+  const int* n_jobs;
+  const int* lims;
+  float* part_o;
+  float* part_lse;
+  uint16_t* o;
+  float* lse;
+  uint32_t* status;
+};
+
+// The two streams of an item: narrow, jobs 2 i and 2 i + 1; wide, the Q tiles of job i.
+struct Streams {
+  Job j[2];
+  int n[2];         // key tiles of each stream
+};
+__device__ __forceinline__ Job load_job(const Job* p) {
+  Job j;
+  const int4* v = reinterpret_cast<const int4*>(p);
+  const int4 x = __ldcg(v), y = __ldcg(v + 1), z = __ldcg(v + 2);
+  j.t0 = x.x; j.n_tok = x.y; j.row = x.z; j.lim = x.w;
+  j.tile0 = y.x; j.n_tiles = y.y; j.key_end = y.z; j.kv = y.w;
+  j.part = z.x;
+  return j;
+}
+template <bool kWide>
+__device__ __forceinline__ Streams load_streams(const AttnArgs& a, int item, int n_jobs, int qt, int g) {
+  Streams s;
+  if constexpr (kWide) {
+    s.j[0] = load_job(a.jobs + item);
+    s.j[1] = s.j[0];
+    s.n[0] = s.j[0].n_tiles;
+    s.n[1] = s.j[0].n_tok > qt ? s.j[0].n_tiles : 0;
+    s.j[1].t0 += qt;
+    s.j[1].n_tok -= qt;
+    if (s.j[1].part >= 0) s.j[1].part += qt * g;
+    if (s.j[0].n_tok > qt) s.j[0].n_tok = qt;
+  } else {
+    s.j[0] = load_job(a.jobs + 2 * item);
+    s.n[0] = s.j[0].n_tiles;
+    s.n[1] = 0;
+    if (2 * item + 1 < n_jobs) {
+      s.j[1] = load_job(a.jobs + 2 * item + 1);
+      s.n[1] = s.j[1].n_tiles;
+    }
+  }
+  return s;
+}
+
+// The page indices of one stream, 32 ahead in the producer warp's lanes and the next 32 after them.
+struct PageWindow {
+  const int32_t* row;
+  int end;           // pages that hold keys
+  int base, cur, next;
+  __device__ __forceinline__ int fetch(int i, int lane) const {
+    return i + lane < end ? __ldg(row + i + lane) : -1;
+  }
+  __device__ __forceinline__ void start(const CacheView& c, const Job& j, int lane) {
+    row = c.table + static_cast<int64_t>(j.row) * c.width;
+    end = (j.key_end + (1 << c.ps_log2) - 1) >> c.ps_log2;
+    base = (j.tile0 * 128) >> c.ps_log2;
+    cur = fetch(base, lane);
+    next = fetch(base + 32, lane);
+  }
+  // page index i (warp-uniform, not decreasing), its table entry for all lanes
+  __device__ __forceinline__ int get(int i, int lane) {
+    if (i >= base + 32) {
+      base += 32;
+      cur = next;
+      next = fetch(base + 32, lane);
+    }
+    return __shfl_sync(0xffffffffu, cur, i - base);
+  }
+};
+
+template <int D, bool kWide>
+__global__ void __launch_bounds__(kThreads, 1)
+    cache_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                      const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ AttnArgs a) {
+  using C = Cfg<D, kWide>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kNumBars);
+  __shared__ int abort_flag;
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int g = a.c.Hq / a.c.Hkv;
+  const int qt = C::kQRows / g;
+  constexpr int kRowThreads = kWide ? 128 : kNarrowRows;   // softmax threads of a stream
+
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    mbar_init(&bars[C::kBarQFull], 1);
+    mbar_init(&bars[C::kBarQEmpty], 1);
+    for (int i = 0; i < C::kN; ++i) {
+      mbar_init(&bars[C::kBarKFull + i], 1);
+      mbar_init(&bars[C::kBarKEmpty + i], 1);
+      mbar_init(&bars[C::kBarVFull + i], 1);
+      mbar_init(&bars[C::kBarVEmpty + i], 1);
+    }
+    for (int q = 0; q < 2; ++q) {
+      mbar_init(&bars[C::kBarSFull + q], 1);
+      mbar_init(&bars[C::kBarPFull + 2 * q], kRowThreads);
+      mbar_init(&bars[C::kBarPFull + 2 * q + 1], kRowThreads);
+      mbar_init(&bars[C::kBarODone + q], 1);
+      mbar_init(&bars[C::kBarOFree + q], kRowThreads);
+    }
+    mbar_init(&bars[C::kBarDrain], 1);
+    fence_mbar_init();
+  }
+  if (warp == 2) {
+    __syncwarp();
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  volatile int* vabort = &abort_flag;
+
+  pdl_launch_dependents();
+  pdl_wait();                 // the job lists
+  const int n_jobs = __ldcg(a.n_jobs);
+  const int n_items = kWide ? n_jobs : (n_jobs + 1) / 2;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer (whole warp)
+    uint32_t kit = 0, vit = 0, uc = 0;
+    bool ok = true;
+    const int ps = 1 << a.c.ps_log2;
+    const int boxes = ps < 128 ? 128 / ps : 1;
+    const int box_tok = ps < 128 ? ps : 128;
+    // one 128-key tile of K or V, page by page
+    auto load_tile = [&](PageWindow& w, const Job& j, int tile, const CUtensorMap* tm, uint8_t* dst, uint64_t* bar) {
+      const int key0 = 128 * tile;
+      if (lane == 0) mbar_arrive_expect_tx(bar, C::kTile);
+      __syncwarp();
+      for (int p = 0; p < boxes; ++p) {
+        const int key = key0 + p * box_tok;
+        const int i = key >> a.c.ps_log2;
+        int page = w.get(i, lane);
+        if (page < 0 || page >= a.c.num_pages) {
+          if (lane == 0 && i < w.end) set_device_status(a.status, DEV_BAD_INDEX);
+          page = static_cast<int>(a.c.num_pages);      // outside the map: filled with zeros
+        }
+        if (lane < C::kBoxes) {
+          const int slot = key & (ps - 1);
+          tma_load_4d(dst + lane * 16384 + p * box_tok * 128, tm, bar, 64 * lane,
+                      a.layout == 0 ? j.kv : slot, a.layout == 0 ? slot : j.kv, page);
+        }
+      }
+    };
+    for (int it = blockIdx.x; it < n_items && ok; it += gridDim.x) {
+      const Streams s = load_streams<kWide>(a, it, n_jobs, qt, g);
+      const int most = s.n[0] > s.n[1] ? s.n[0] : s.n[1];
+      if (most == 0) continue;
+      PageWindow w[2];
+      w[0].start(a.c, s.j[0], lane);
+      if (!kWide && s.n[1] > 0) w[1].start(a.c, s.j[1], lane);
+      bool q_sent = false;
+      for (int j = 0; j < most && ok; ++j) {
+#pragma unroll
+        for (int q = 0; q < (kWide ? 1 : 2); ++q) {
+          if (!ok || j >= s.n[q]) continue;
+          const uint32_t ks = kit % C::kN;
+          if (kit >= static_cast<uint32_t>(C::kN))
+            ok = __all_sync(0xffffffffu, mbar_wait(&bars[C::kBarKEmpty + ks], ((kit / C::kN) - 1) & 1u, a.status, vabort));
+          if (!ok) break;
+          // the window is read twice for a tile (K, then V): keep the state of the first read
+          PageWindow at = w[q];
+          load_tile(at, s.j[q], s.j[q].tile0 + j, &tm_k, smem + C::kOffK + ks * C::kTile, &bars[C::kBarKFull + ks]);
+          ++kit;
+          if (!q_sent) {
+            // Q goes behind the first K tile: its buffer is free once the last item's scores are done
+            q_sent = true;
+            if (uc > 0) ok = __all_sync(0xffffffffu, mbar_wait(&bars[C::kBarQEmpty], (uc - 1) & 1u, a.status, vabort));
+            if (!ok) break;
+            ++uc;
+            const int nq = (s.n[0] > 0 ? 1 : 0) + (s.n[1] > 0 ? 1 : 0);
+            if (lane == 0) mbar_arrive_expect_tx(&bars[C::kBarQFull], static_cast<uint32_t>(nq * C::kBoxes * 128 * g * qt));
+            __syncwarp();
+            if (lane < 2 * C::kBoxes) {
+              const int qq = lane / C::kBoxes, b = lane % C::kBoxes;
+              if ((qq ? s.n[1] : s.n[0]) > 0)
+                tma_load_3d(smem + qq * C::kQTile + b * C::kQBox, &tm_q, &bars[C::kBarQFull], 64 * b,
+                            (qq ? s.j[1].kv : s.j[0].kv) * g, qq ? s.j[1].t0 : s.j[0].t0);
+            }
+          }
+          const uint32_t vs = vit % C::kN;
+          if (vit >= static_cast<uint32_t>(C::kN))
+            ok = __all_sync(0xffffffffu, mbar_wait(&bars[C::kBarVEmpty + vs], ((vit / C::kN) - 1) & 1u, a.status, vabort));
+          if (!ok) break;
+          load_tile(w[q], s.j[q], s.j[q].tile0 + j, &tm_v, smem + C::kOffV + vs * C::kTile, &bars[C::kBarVFull + vs]);
+          ++vit;
+        }
+      }
+    }
+    if (!ok) {
+      *vabort = 1;
+      // drain this warp's own copies still in flight before the CTA may exit
+      for (uint32_t i = kit > static_cast<uint32_t>(C::kN) ? kit - C::kN : 0u; i < kit; ++i)
+        mbar_wait_ns(&bars[C::kBarKFull + i % C::kN], (i / C::kN) & 1u, 200000000ull);
+      for (uint32_t i = vit > static_cast<uint32_t>(C::kN) ? vit - C::kN : 0u; i < vit; ++i)
+        mbar_wait_ns(&bars[C::kBarVFull + i % C::kN], (i / C::kN) & 1u, 200000000ull);
+      if (uc > 0) mbar_wait_ns(&bars[C::kBarQFull], (uc - 1) & 1u, 200000000ull);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer (converged warp)
+    constexpr uint32_t kIdS = idesc_bf16(128, 128, false, false);
+    constexpr uint32_t kIdPV = idesc_bf16(128, D, false, true);
+    const uint64_t dQ0 = smem_desc(smem_u32(smem), 16, 1024);
+    const uint64_t dK0 = smem_desc(smem_u32(smem + C::kOffK), 16, 1024);
+    const uint64_t dV0 = smem_desc(smem_u32(smem + C::kOffV), 16384, 1024);
+    uint32_t kit = 0, vit = 0, uc = 0;
+    uint32_t pph = 0u;               // bit q: parity of the next p_full waits of stream q
+    uint32_t uq[2] = {0u, 0u};       // jobs done per stream
+    bool ok = true;
+    auto wait = [&](int bar, uint32_t parity) {
+      return mbar_wait_warp<20u>(&bars[bar], parity, a.status, vabort);
+    };
+    auto issue_s = [&](int q, uint32_t kstage) {
+      const uint64_t qa = dQ0 + static_cast<uint64_t>((q * C::kQTile) >> 4);
+      const uint64_t ka = dK0 + static_cast<uint64_t>((kstage * C::kTile) >> 4);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint64_t qo = static_cast<uint64_t>(((kk >> 2) * C::kQBox + (kk & 3) * 32) >> 4);
+        const uint64_t ko = static_cast<uint64_t>(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4);
+        mma_bf16_ss_w(tmem + C::col_s(q), qa + qo, ka + ko, kIdS, kk > 0 ? 1u : 0u);
+      }
+    };
+    auto issue_pv = [&](int q, uint32_t vstage, int h, bool acc) {
+      const uint64_t va = dV0 + static_cast<uint64_t>((vstage * C::kTile) >> 4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int kk = 4 * h + i;
+        mma_bf16_ts_w(tmem + C::col_o(q), tmem + C::col_s(q) + kk * 8,
+                      va + static_cast<uint64_t>((kk * 2048) >> 4), kIdPV, (acc || i > 0) ? 1u : 0u);
+      }
+    };
+    // Clear the V rows from `from` on (behind the sequence's end; whatever they hold must not
+    // meet a probability of zero).
+    auto clear_v = [&](uint32_t vstage, int from) {
+      uint8_t* v = smem + C::kOffV + vstage * C::kTile;
+      for (int i = lane; i < (128 - from) * 8; i += 32)
+#pragma unroll
+        for (int b = 0; b < C::kBoxes; ++b)
+          *reinterpret_cast<uint4*>(v + b * 16384 + from * 128 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+      fence_proxy_async_smem();
+      __syncwarp();
+    };
+    for (int it = blockIdx.x; it < n_items && ok; it += gridDim.x) {
+      const Streams s = load_streams<kWide>(a, it, n_jobs, qt, g);
+      const int most = s.n[0] > s.n[1] ? s.n[0] : s.n[1];
+      if (most == 0) continue;
+      ok = wait(C::kBarQFull, uc & 1u);
+      if (!ok) break;
+      tc_fence_after();
+      // first scores
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        if (!ok || s.n[q] == 0) continue;
+        const uint32_t ks = kit % C::kN;
+        if (!kWide || q == 0) {
+          ok = wait(C::kBarKFull + ks, (kit / C::kN) & 1u);
+          if (!ok) break;
+          tc_fence_after();
+        }
+        issue_s(q, ks);
+        mma_commit_w(&bars[C::kBarSFull + q]);
+        if (!kWide || q == 1 || s.n[1] == 0) {
+          mma_commit_w(&bars[C::kBarKEmpty + ks]);
+          ++kit;
+        }
+      }
+      for (int j = 0; j < most && ok; ++j) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          if (!ok || j >= s.n[q]) continue;
+          const uint32_t vs = vit % C::kN;
+          if (!kWide || q == 0) {
+            ok = wait(C::kBarVFull + vs, (vit / C::kN) & 1u);
+            if (!ok) break;
+            const int left = s.j[q].key_end - 128 * (s.j[q].tile0 + j);
+            if (left < 128) clear_v(vs, left < 0 ? 0 : left);
+          }
+          ok = wait(C::kBarPFull + 2 * q, (pph >> q) & 1u);
+          if (!ok) break;
+          if (j == 0 && uq[q] > 0) {
+            ok = wait(C::kBarOFree + q, (uq[q] - 1) & 1u);
+            if (!ok) break;
+          }
+          tc_fence_after();
+          issue_pv(q, vs, 0, j > 0);
+          ok = wait(C::kBarPFull + 2 * q + 1, (pph >> q) & 1u);
+          if (!ok) break;
+          pph ^= 1u << q;
+          tc_fence_after();
+          issue_pv(q, vs, 1, true);
+          if (j + 1 == s.n[q]) mma_commit_w(&bars[C::kBarODone + q]);
+          if (!kWide || q == 1 || s.n[1] == 0) {
+            mma_commit_w(&bars[C::kBarVEmpty + vs]);
+            ++vit;
+          }
+          if (j + 1 < s.n[q]) {
+            const uint32_t ks = kit % C::kN;
+            if (!kWide || q == 0) {
+              ok = wait(C::kBarKFull + ks, (kit / C::kN) & 1u);
+              if (!ok) break;
+              tc_fence_after();
+            }
+            issue_s(q, ks);
+            mma_commit_w(&bars[C::kBarSFull + q]);
+            if (!kWide || q == 1 || s.n[1] == 0) {
+              mma_commit_w(&bars[C::kBarKEmpty + ks]);
+              ++kit;
+            }
+          }
+        }
+      }
+      if (!ok) break;
+      if (s.n[0] > 0) ++uq[0];
+      if (s.n[1] > 0) ++uq[1];
+      ++uc;
+      mma_commit_w(&bars[C::kBarQEmpty]);
+    }
+    if (!ok) *vabort = 1;
+    // every MMA (and the arrivals committed behind it) has landed before exit
+    mma_commit_w(&bars[C::kBarDrain]);
+    mbar_wait_ns(&bars[C::kBarDrain], 0u, ok ? LS_WAIT_LIMIT_NS : 200000000ull);
+  } else if (warp >= 4 && (kWide || (warp & 3) < kNarrowRows / 32)) {
+    // ------------------------------------------------------------ softmax of stream q
+    const int q = (warp - 4) >> 2;
+    const int quarter = warp & 3;
+    const int row = quarter * 32 + lane;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t colS = C::col_s(q), colO = C::col_o(q);
+    const float c2 = a.scale * kLog2e;
+    uint32_t sph = 0u, uq = 0u;
+    bool ok = true;
+    for (int it = blockIdx.x; it < n_items && ok; it += gridDim.x) {
+      const Streams s = load_streams<kWide>(a, it, n_jobs, qt, g);
+      const Job w = q ? s.j[1] : s.j[0];
+      const int n = q ? s.n[1] : s.n[0];
+      if (n == 0) continue;
+      const int tok = row / g;
+      const bool valid = tok < w.n_tok && row < g * qt;
+      const bool any = __any_sync(0xffffffffu, valid);
+      const int t = w.t0 + tok;
+      // rows that are not used need no mask: what they hold reaches no other row
+      int limit = INT_MAX;
+      if (valid) limit = w.lim == INT_MIN ? __ldcg(a.lims + t) : w.lim + t;
+      limit -= 128 * w.tile0;
+      float m_run = -INFINITY, l = 0.0f;
+      for (int j = 0; j < n; ++j) {
+        ok = mbar_wait_hint<20u>(&bars[C::kBarSFull + q], sph, a.status, vabort);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        sph ^= 1u;
+        if (!any) {               // no row of this warp is used: what it leaves in P reaches none
+          tc_fence_after();
+          tc_fence_before();
+          mbar_arrive(&bars[C::kBarPFull + 2 * q]);
+          mbar_arrive(&bars[C::kBarPFull + 2 * q + 1]);
+          continue;
+        }
+        tc_fence_after();
+        uint32_t sv[4][32];
+        tmem_ld32(lane_base + colS + 0, sv[0]);
+        tmem_ld32(lane_base + colS + 32, sv[1]);
+        tmem_ld32(lane_base + colS + 64, sv[2]);
+        tmem_ld32(lane_base + colS + 96, sv[3]);
+        tmem_ld_wait();
+        const int lim = limit - 128 * j;
+        if (lim < 128) {
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            if (c >= lim) sv[c >> 5][c & 31] = __float_as_uint(-INFINITY);
+        }
+        float mxa = -INFINITY, mxb = -INFINITY, mxc = -INFINITY, mxd = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 128; c += 8) {
+          mxa = fmax3(mxa, __uint_as_float(sv[c >> 5][c & 31]), __uint_as_float(sv[c >> 5][(c + 1) & 31]));
+          mxb = fmax3(mxb, __uint_as_float(sv[c >> 5][(c + 2) & 31]), __uint_as_float(sv[c >> 5][(c + 3) & 31]));
+          mxc = fmax3(mxc, __uint_as_float(sv[c >> 5][(c + 4) & 31]), __uint_as_float(sv[c >> 5][(c + 5) & 31]));
+          mxd = fmax3(mxd, __uint_as_float(sv[c >> 5][(c + 6) & 31]), __uint_as_float(sv[c >> 5][(c + 7) & 31]));
+        }
+        const float mt = fmax3(mxa, mxb, fmaxf(mxc, mxd)) * c2;
+        float factor = 1.0f;
+        bool resc = false;
+        if (m_run == -INFINITY) {
+          m_run = mt;
+        } else if (mt > m_run + kRescaleLog2) {
+          factor = ex2_approx(m_run - mt);
+          l *= factor;
+          m_run = mt;
+          resc = true;
+        }
+        const float neg_m = (m_run == -INFINITY) ? 0.0f : -m_run;
+        const bool any_resc = __any_sync(0xffffffffu, resc);
+        const uint64_t c2x2 = f2_pack(c2, c2), nm2 = f2_pack(neg_m, neg_m);
+        uint64_t rs2[4] = {f2_pack(0.0f, 0.0f), f2_pack(0.0f, 0.0f), f2_pack(0.0f, 0.0f),
+                           f2_pack(0.0f, 0.0f)};
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t pw[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const int c = half * 64 + 2 * i;
+            const uint64_t e = f2_fma(f2_pack(__uint_as_float(sv[c >> 5][c & 31]),
+                                              __uint_as_float(sv[(c + 1) >> 5][(c + 1) & 31])),
+                                      c2x2, nm2);
+            float x0, x1;
+            f2_unpack(e, x0, x1);
+            const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+            rs2[i & 3] = f2_add(rs2[i & 3], f2_pack(p0, p1));
+            pw[i] = pack_bf16x2(p0, p1);
+          }
+          tmem_st32(lane_base + colS + half * 32, pw);
+          if (!any_resc) {
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(&bars[C::kBarPFull + 2 * q + half]);
+          }
+        }
+        float r0, r1, r2, r3;
+        f2_unpack(f2_add(rs2[0], rs2[1]), r0, r1);
+        f2_unpack(f2_add(rs2[2], rs2[3]), r2, r3);
+        l += (r0 + r1) + (r2 + r3);
+        if (any_resc) {
+#pragma unroll
+          for (int cc = 0; cc < D / 32; ++cc) {
+            uint32_t ov[32];
+            tmem_ld32(lane_base + colO + cc * 32, ov);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * factor);
+            tmem_st32(lane_base + colO + cc * 32, ov);
+          }
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(&bars[C::kBarPFull + 2 * q]);
+          mbar_arrive(&bars[C::kBarPFull + 2 * q + 1]);
+        }
+      }
+      if (!ok) break;
+      ok = mbar_wait_hint<20u>(&bars[C::kBarODone + q], uq & 1u, a.status, vabort);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      if (any) {
+        const int hh = row - tok * g;
+        const float inv_l = (l > 0.0f) ? 1.0f / l : 0.0f;
+        const int64_t out = static_cast<int64_t>(t) * a.c.Hq + w.kv * g + hh;
+        const int64_t prow = static_cast<int64_t>(w.part) + row;
+#pragma unroll
+        for (int cc = 0; cc < D / 32; ++cc) {
+          uint32_t ov[32];
+          tmem_ld32(lane_base + colO + cc * 32, ov);
+          tmem_ld_wait();
+          if (!valid) continue;
+          if (w.part < 0) {
+            uint4* dst = reinterpret_cast<uint4*>(a.o + out * D + cc * 32);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              dst[i] = make_uint4(
+                  pack_bf16x2(__uint_as_float(ov[8 * i + 0]) * inv_l, __uint_as_float(ov[8 * i + 1]) * inv_l),
+                  pack_bf16x2(__uint_as_float(ov[8 * i + 2]) * inv_l, __uint_as_float(ov[8 * i + 3]) * inv_l),
+                  pack_bf16x2(__uint_as_float(ov[8 * i + 4]) * inv_l, __uint_as_float(ov[8 * i + 5]) * inv_l),
+                  pack_bf16x2(__uint_as_float(ov[8 * i + 6]) * inv_l, __uint_as_float(ov[8 * i + 7]) * inv_l));
+          } else {
+            float4* dst = reinterpret_cast<float4*>(a.part_o + prow * D + cc * 32);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              dst[i] = make_float4(__uint_as_float(ov[4 * i]) * inv_l, __uint_as_float(ov[4 * i + 1]) * inv_l,
+                                   __uint_as_float(ov[4 * i + 2]) * inv_l, __uint_as_float(ov[4 * i + 3]) * inv_l);
+          }
+        }
+        if (valid) {
+          const float lse2 = l > 0.0f ? m_run + __log2f(l) : -INFINITY;
+          if (w.part < 0)
+            a.lse[out] = lse2 * kLn2;
+          else
+            a.part_lse[prow] = lse2;
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(&bars[C::kBarOFree + q]);
+      ++uq;
+    }
+    if (!ok) *vabort = 1;
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// --------------------------------------------------------------------------------------
+constexpr int kJoinThreads = 128;
+
+struct JoinArgs {
+  int S, group, Hq, Hkv, heads;      // heads: query heads of a block (one key head's)
+  const int32_t* cu;
+  const Info* info;
+  const Seg* segs;
+  const float* part_o;
+  const float* part_lse;
+  uint16_t* o;
+  float* lse;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_constant__ JoinArgs a) {
+  constexpr int kPer = D / 32, kWarps = kJoinThreads / 32;
+  __shared__ float sm[kWarps], sl[kWarps];
+  __shared__ float so[kWarps][D];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int t = blockIdx.x;
+  const int g = a.Hq / a.Hkv;
+  pdl_wait();
+  int b = 0;
+  for (int i0 = 0; i0 < a.S; i0 += kJoinThreads) {
+    const int i = i0 + threadIdx.x;
+    b += __syncthreads_count(i < a.S && a.cu[i + 1] <= t);
+  }
+  if (b >= a.S || t < a.cu[b]) return;
+  // the token's part lists: its own segment, and its group's
+  const Seg* seg[2] = {a.segs + b, a.info->grouped ? a.segs + a.S + b / a.group : nullptr};
+  int n[2] = {0, 0}, base[2], step[2];
+  bool direct = false;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    if (seg[k] == nullptr || seg[k]->tiles == 0) continue;
+    const Seg& s = *seg[k];
+    int tiles = s.tiles;
+    if (is_wide(s, g)) {      // the keys of the token's pair of Q tiles
+      const int per = 2 * qt_of(g, true);
+      int end = s.t0 + ((t - s.t0) / per + 1) * per;
+      if (end > s.t0 + s.n_tok) end = s.t0 + s.n_tok;
+      tiles = tiles_of(s, end);
+    }
+    n[k] = (tiles + s.chunk - 1) / s.chunk;
+    base[k] = s.part + (t - s.t0) * g;
+    step[k] = s.n_tok * g;
+    if (s.part < 0) direct = n[k] > 0;
+  }
+  if (direct) return;
+  const int total = n[0] + n[1];
+  for (int h = blockIdx.y * a.heads; h < (static_cast<int>(blockIdx.y) + 1) * a.heads; ++h) {
+    const int kv = h / g, hh = h - kv * g;
+    float m = -INFINITY, l = 0.0f, acc[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) acc[i] = 0.0f;
+    for (int p = warp; p < total; p += kWarps) {
+      const int k = p < n[0] ? 0 : 1, c = p - (k ? n[0] : 0);
+      const int chunks = k ? seg[1]->chunks : seg[0]->chunks;
+      const int64_t row = static_cast<int64_t>(k ? base[1] : base[0]) +
+                          static_cast<int64_t>(kv * chunks + c) * (k ? step[1] : step[0]) + hh;
+      const float x = __ldcg(a.part_lse + row);
+      float v[kPer];
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) v[i] = __ldcg(a.part_o + row * D + lane + 32 * i);
+      if (x == -INFINITY) continue;
+      const float mn = fmaxf(m, x);
+      const float f = ex2_approx(m - mn), e = ex2_approx(x - mn);
+      m = mn;
+      l = l * f + e;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) acc[i] = acc[i] * f + e * v[i];
+    }
+    if (lane == 0) { sm[warp] = m; sl[warp] = l; }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) so[warp][lane + 32 * i] = acc[i];
+    __syncthreads();
+    float M = sm[0];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) M = fmaxf(M, sm[w]);
+    float L = 0.0f, f[kWarps];
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      f[w] = sm[w] == -INFINITY ? 0.0f : ex2_approx(sm[w] - M);
+      L += f[w] * sl[w];
+    }
+    const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+    const int64_t out = static_cast<int64_t>(t) * a.Hq + h;
+    for (int i = threadIdx.x; i < D; i += kJoinThreads) {
+      float x = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) x += f[w] * so[w][i];
+      a.o[out * D + i] = static_cast<uint16_t>(pack_bf16x2(x * inv, 0.0f) & 0xFFFFu);
+    }
+    if (threadIdx.x == 0) a.lse[out] = L > 0.0f ? (M + __log2f(L)) * kLn2 : -INFINITY;
+    __syncthreads();
+  }
+}
+
+// Launch with programmatic serialisation: the kernel may start while the one before it ends.
+template <class... P, class... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+}
+
+template <int D, bool kWide>
+cudaError_t launch_attn(const CacheAttnArgs& a, const AttnArgs& p, cudaStream_t s) {
+  using C = Cfg<D, kWide>;
+  static bool attr_set[kMaxDeviceCache] = {};
+  const int dev = cached_device_index();
+  if (dev < 0) return cudaErrorInvalidDevice;
+  if (!attr_set[dev]) {
+    cudaError_t e = cudaFuncSetAttribute(cache_attn_kernel<D, kWide>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    attr_set[dev] = true;
+  }
+  return launch_after(cache_attn_kernel<D, kWide>, dim3(static_cast<unsigned>(num_sms())), kThreads,
+                      C::kSmem, s, *a.tm_k, *a.tm_v, kWide ? a.tm_q : a.tm_qn, p);
+}
+
+constexpr size_t kPlanSmem = 2 * (kMaxSegs + 1) * sizeof(int);
 
 }  // namespace
 
-size_t cache_attn_ws_bytes(const CacheView&, int, int64_t, int, int64_t) { return 256; }
+CacheAttnLayout cache_attn_layout(const CacheView& c, int S, int64_t T, int max_new) {
+  CacheAttnLayout l{};
+  const int g = c.Hq / c.Hkv;
+  const int64_t sms = num_sms();
+  // Partial rows: a token in two segments (groups) a few times over, and twelve chunks of a
+  // narrow job, eight of a wide one, a SM.
+  const int64_t tok = T < kMaxSeqs ? T : kMaxSeqs;
+  const bool wide = T > kNarrowRows / g;
+  l.rows_narrow = 3 * tok * c.Hq + sms * 12 * (T * g < kNarrowRows ? T * g : kNarrowRows);
+  l.rows_wide = wide ? 3 * tok * c.Hq + sms * 8 * 256 : 0;
+  // jobs: one a (segment, key head) at least, and the chunks
+  const int64_t segs = S + S / 2;
+  l.max_narrow = segs * c.Hkv + 2 * 16 * sms;
+  // (every token is in one segment or two, each with a last pair of Q tiles that is not full)
+  l.max_wide = wide ? (T / (128 / g) + 2 * segs) * c.Hkv + 16 * sms : 0;
+  (void)max_new;
+  auto put = [&](size_t* at, size_t bytes) {
+    *at = l.total;
+    l.total += (bytes + 255) / 256 * 256;
+  };
+  put(&l.info, sizeof(Info));
+  put(&l.segs, sizeof(Seg) * static_cast<size_t>(segs));
+  put(&l.lims, sizeof(int) * static_cast<size_t>(T));
+  put(&l.narrow, sizeof(Job) * static_cast<size_t>(l.max_narrow));
+  put(&l.wide, sizeof(Job) * static_cast<size_t>(l.max_wide));
+  put(&l.lse, sizeof(float) * static_cast<size_t>(l.rows_narrow + l.rows_wide));
+  put(&l.o, sizeof(float) * static_cast<size_t>(l.rows_narrow + l.rows_wide) * c.D);
+  return l;
+}
 
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, cudaStream_t s) {
-  const unsigned grid = static_cast<unsigned>((a.T * a.c.Hq + kThreads / 32 - 1) / (kThreads / 32));
-  if (a.c.D == 128)
-    cache_attn_warp<128><<<grid, kThreads, 0, s>>>(a);
-  else
-    cache_attn_warp<64><<<grid, kThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  const int g = a.c.Hq / a.c.Hkv;
+  uint8_t* ws = static_cast<uint8_t*>(a.ws);
+  PlanArgs p{};
+  p.c = a.c;
+  p.S = a.S;
+  p.T = a.T;
+  p.rows = a.rows;
+  p.cu = a.cu;
+  p.max_new = a.max_new;
+  p.max_len = a.max_len;
+  p.group = a.group;
+  p.shared = a.shared;
+  p.ws = ws;
+  p.l = cache_attn_layout(a.c, a.S, a.T, a.max_new);
+  p.sms = num_sms();
+  p.status = a.status;
+  cache_plan_kernel<<<1, kPlanThreads, kPlanSmem, s>>>(p);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+
+  const Info* info = reinterpret_cast<const Info*>(ws + p.l.info);
+  AttnArgs k{};
+  k.c = a.c;
+  k.scale = a.scale;
+  k.layout = a.layout;
+  k.lims = reinterpret_cast<const int*>(ws + p.l.lims);
+  k.part_lse = reinterpret_cast<float*>(ws + p.l.lse);
+  k.part_o = reinterpret_cast<float*>(ws + p.l.o);
+  k.o = a.o;
+  k.lse = a.lse;
+  k.status = a.status;
+  k.jobs = reinterpret_cast<const Job*>(ws + p.l.narrow);
+  k.n_jobs = info->n_jobs;
+  e = a.c.D == 128 ? launch_attn<128, false>(a, k, s) : launch_attn<64, false>(a, k, s);
+  if (e != cudaSuccess) return e;
+  // more than 64 rows in a segment: only if the bounds allow it
+  if (static_cast<int64_t>(a.max_new) * a.group > kNarrowRows / g && a.T > kNarrowRows / g) {
+    k.jobs = reinterpret_cast<const Job*>(ws + p.l.wide);
+    k.n_jobs = info->n_jobs + 1;
+    e = a.c.D == 128 ? launch_attn<128, true>(a, k, s) : launch_attn<64, true>(a, k, s);
+    if (e != cudaSuccess) return e;
+  }
+  JoinArgs j{};
+  j.S = a.S;
+  j.group = a.group;
+  j.Hq = a.c.Hq;
+  j.Hkv = a.c.Hkv;
+  j.cu = a.cu;
+  j.info = info;
+  j.segs = reinterpret_cast<const Seg*>(ws + p.l.segs);
+  j.part_o = k.part_o;
+  j.part_lse = k.part_lse;
+  j.o = a.o;
+  j.lse = a.lse;
+  // a block a head while that is a moderate grid, else a block a key head
+  j.heads = a.T * a.c.Hq <= 16384 ? 1 : g;
+  const dim3 grid(static_cast<unsigned>(a.T), static_cast<unsigned>(a.c.Hq / j.heads));
+  return a.c.D == 128 ? launch_after(cache_join_kernel<128>, grid, kJoinThreads, 0, s, j)
+                      : launch_after(cache_join_kernel<64>, grid, kJoinThreads, 0, s, j);
 }
 
 }  // namespace ls

@@ -17,6 +17,7 @@ struct ls_cache_s {
   int page_size, layout;
   float scale;
   ls::CacheView view;
+  CUtensorMap tm_k, tm_v;   // boxes of one head and min(page_size, 128) tokens of one page
 };
 
 namespace {
@@ -109,6 +110,18 @@ ls_status ls_cache_create(const ls_cache_desc* d, ls_cache_t* out) {
   v.table = d->page_table;
   v.len = d->seq_len;
   v.ref = d->refcount;
+  const cuuint64_t D = d->D, H = d->Hkv, ps = d->page_size, N = static_cast<cuuint64_t>(d->num_pages);
+  const cuuint32_t bt = d->page_size < 128 ? d->page_size : 128;
+  const bool nhd = d->layout == LS_CACHE_NHD;
+  const cuuint64_t dims[4] = {D, nhd ? H : ps, nhd ? ps : H, N};
+  const cuuint64_t strides[3] = {D * 2, (nhd ? H : ps) * D * 2, static_cast<cuuint64_t>(d->page_stride) * 2};
+  const cuuint32_t box[4] = {64, nhd ? 1 : bt, nhd ? bt : 1, 1};
+  int st = encode_bf16_map(&h->tm_k, d->k_pages, 4, dims, strides, box);
+  if (st == LS_OK) st = encode_bf16_map(&h->tm_v, d->v_pages, 4, dims, strides, box);
+  if (st != LS_OK) {
+    delete h;
+    return static_cast<ls_status>(st);
+  }
   h->magic = kMagic;
   *out = h;
   return LS_OK;
@@ -271,7 +284,7 @@ ls_status ls_cache_append(ls_cache_t h, const ls_cache_append_desc* d, void* str
 size_t ls_cache_attn_workspace_bytes(ls_cache_t h, int32_t S, int64_t T, int32_t max_new,
                                      int64_t max_len) {
   if (check_cache(h) != LS_OK || S < 1 || T < 1 || max_new < 1 || max_len < 1) return 0;
-  return align_up(cache_attn_ws_bytes(h->view, S, T, max_new, max_len), 256);
+  return cache_attn_layout(h->view, S, T, max_new).total;
 }
 
 ls_status ls_cache_attn(ls_cache_t h, const ls_cache_attn_desc* d, void* workspace,
@@ -315,7 +328,18 @@ ls_status ls_cache_attn(ls_cache_t h, const ls_cache_attn_desc* d, void* workspa
   a.group = d->group;
   a.shared = d->group > 1 ? d->shared_len : nullptr;
   a.ws = workspace;
+  a.tm_k = &h->tm_k;
+  a.tm_v = &h->tm_v;
+  a.layout = h->layout;
   a.status = status;
+  const cuuint32_t g = c.Hq / c.Hkv;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(c.D), static_cast<cuuint64_t>(c.Hq),
+                              static_cast<cuuint64_t>(d->T)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(c.D) * 2, static_cast<cuuint64_t>(d->q_stride) * 2};
+  const cuuint32_t box[3] = {64, g, 128 / g}, boxn[3] = {64, g, 64 / g};
+  st = static_cast<ls_status>(encode_bf16_map(&a.tm_q, d->q, 3, dims, strides, box));
+  if (st == LS_OK) st = static_cast<ls_status>(encode_bf16_map(&a.tm_qn, d->q, 3, dims, strides, boxn));
+  if (st != LS_OK) return st;
   return run_launch(LS_KERNEL_CACHE_ATTN, stream, "cache attention launch",
                     [&](cudaStream_t s) { return launch_cache_attn(a, s); });
 }

@@ -107,10 +107,18 @@ struct CacheAttnArgs {
   void* ws;
   const CUtensorMap* tm_k;    // pages: see ls_cache.cu
   const CUtensorMap* tm_v;
-  CUtensorMap tm_q;           // {64, g, qt} boxes of [T][Hq][D]
+  int layout;                 // 0: [page_size, Hkv, D] inside a page, 1: [Hkv, page_size, D]
+  CUtensorMap tm_q;           // {64, g, 128 / g} boxes of [T][Hq][D]
+  CUtensorMap tm_qn;          // {64, g, 64 / g} boxes
   uint32_t* status;
 };
-size_t cache_attn_ws_bytes(const CacheView& c, int S, int64_t T, int max_new, int64_t max_len);
+// Workspace of a call: sizes come from the host's bounds alone.
+struct CacheAttnLayout {
+  size_t info, segs, lims, narrow, wide, lse, o, total;   // byte offsets, bytes
+  int64_t max_narrow, max_wide;                           // job list capacities
+  int64_t rows_narrow, rows_wide;                         // rows of partial results
+};
+CacheAttnLayout cache_attn_layout(const CacheView& c, int S, int64_t T, int max_new);
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, cudaStream_t s);
 
 }  // namespace ls
