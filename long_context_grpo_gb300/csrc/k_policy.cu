@@ -1,7 +1,25 @@
 // Clipped policy loss with a KL term over packed tokens, forward and backward.
 //
-// policy_rows: one CTA per token row at a time: maximum, sum of exponentials, the token's
-//   scalar chain in fp64 by one thread, then dlogits = g (onehot - softmax).
+//   p = softmax(x), logp = log p_y, d = logp - old, rho = e^d,
+//   term = w (beta kl - min(rho A, clip(rho) A)),  g = d term / d logp,
+//   dlogits = g (onehot_y - p)
+//
+// policy_cluster: the whole row stays in shared memory between the two passes, so HBM sees every
+//   logit once in and once out (4 bytes a logit; bound by HBM).  A cluster of 1, 2, 4 or 8 CTAs
+//   owns one row at a time, each a slice of at most 38 KB, in three buffers: one row waits for its
+//   gradient while its sums are exchanged, the next row's sums are taken, and the third
+//   arrives by bulk copy.
+//   4 or 8 streaming warps: the warp's maximum (packed bf16 maxima), then the sum of exp(x - max) in
+//     fp32, joined across lanes in fp32 pairs; later p g rounded to bf16 and stored.
+//   1 scalar warp: joins the partials, exchanges them with the other CTAs
+//     (distributed shared memory, remote mbarrier arrivals, bounded waits) and joins those in
+//     rank order and decides the clip on d in fp64.  It also owns the up to 7 + 7 logits of a row outside its 16-byte
+//     granules.
+//   1 output warp: issues the copies, writes the token's outputs and its loss term (fp64), off the
+//     row's critical path.
+//   A row whose gradient has another alignment than its logits goes
+//     through shared memory once more and is shifted there.
+// policy_rows: one CTA a row from global memory, for vocabularies beyond eight slices (460,000).
 // policy_reduce: the fp64 sum of the tokens' terms in a fixed order, rounded once.
 #include "ls_internal.h"
 #include "ls_ops.h"
@@ -10,135 +28,681 @@
 namespace ls {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr float kLog2e = 1.4426950408889634f;
 
+__device__ __forceinline__ float bf16_bits(uint32_t h) { return __uint_as_float(h << 16); }
 __device__ __forceinline__ float bf16_at(const uint16_t* x, int64_t i) {
-  return __uint_as_float(static_cast<uint32_t>(x[i]) << 16);
+  return bf16_bits(__ldcg(reinterpret_cast<const unsigned short*>(x) + i));
+}
+__device__ __forceinline__ float lo_bf16(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_bf16(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+__device__ __forceinline__ uint16_t to_bf16(float x) {
+  return static_cast<uint16_t>(pack_bf16x2(x, 0.0f) & 0xFFFFu);
 }
 
-// What the softmax pass of a row needs, and the token's loss term.
-struct TokenGrad {
-  float g;          // d loss / d logp
-  double term;
+// The inputs of one token, its outcome.
+struct Token {
+  int y;
+  float old, ref, A, w;
+  // (derived where they are needed, so that a token loaded ahead is not waited for)
+  __device__ __forceinline__ bool bad(int64_t V) const { return w != 0.0f && (y < 0 || y >= V); }
+  __device__ __forceinline__ bool used(int64_t V) const { return w != 0.0f && y >= 0 && y < V; }
 };
-
-// The token's scalar chain in fp64, its outputs written (all but the gradient row).
-__device__ __forceinline__ TokenGrad policy_token(const PolicyArgs& a, int64_t row, double logp) {
-  const double A = a.adv[row], w = a.weight[row];
-  const double d = logp - static_cast<double>(a.old[row]);
-  const bool clipped = (A > 0.0 && d > a.log_hi) || (A < 0.0 && d < a.log_lo);
-  const double rho_a = exp(d) * A;
-  const double surr = clipped ? (A > 0.0 ? a.clip_hi : a.clip_lo) * A : rho_a;
-  double kl = 0.0, slope = 0.0;
-  if (a.ref != nullptr) {
-    const double r = logp - static_cast<double>(a.ref[row]);
-    if (a.kl == 1) {
-      kl = r;
-      slope = 1.0;
-    } else if (a.kl == 2) {
-      kl = 0.5 * r * r;
-      slope = r;
-    } else {
-      const double em = expm1(-r);
-      kl = em + r;
-      slope = -em;
-    }
-  }
-  TokenGrad t;
-  t.term = w * (a.beta * kl - surr);
-  t.g = static_cast<float>(w * (a.beta * slope - (clipped ? 0.0 : rho_a)));
-  a.clip_mask[row] = clipped ? 1 : 0;
-  if (a.logp_out != nullptr) a.logp_out[row] = static_cast<float>(logp);
-  if (a.kl_out != nullptr) a.kl_out[row] = static_cast<float>(kl);
+__device__ __forceinline__ Token load_token(const PolicyArgs& a, int64_t row) {
+  Token t;
+  t.w = a.weight[row];
+  t.y = a.ids[row];
+  t.old = a.old[row];
+  t.ref = a.ref != nullptr ? a.ref[row] : 0.0f;
+  t.A = a.adv[row];
   return t;
 }
 
+struct TokenLoss {
+  float g;           // d term / d logp
+  bool clipped;
+};
+// The clip is decided on d in fp64; ratio and gradient follow in fp32 (relative error ~2^-22).
+__device__ __forceinline__ TokenLoss token_grad(const PolicyArgs& a, const Token& t, double logp) {
+  TokenLoss o;
+  const double d = logp - static_cast<double>(t.old);
+  o.clipped = (t.A > 0.0f && d > a.log_hi) || (t.A < 0.0f && d < a.log_lo);
+  float slope = 0.0f;
+  if (a.ref != nullptr) {
+    const float r = static_cast<float>(logp - static_cast<double>(t.ref));
+    slope = a.kl == 1 ? 1.0f : (a.kl == 2 ? r : -expm1f(-r));
+  }
+  o.g = t.w * (static_cast<float>(a.beta) * slope - (o.clipped ? 0.0f : expf(static_cast<float>(d)) * t.A));
+  return o;
+}
+// The loss term and the KL estimate in fp64, off the row's critical path: even lanes take the
+// ratio's exponential, odd lanes the KL term's, in one instruction stream.
+__device__ __forceinline__ double token_term(const PolicyArgs& a, const Token& t, double logp, bool clipped,
+                                             int lane, float* kl) {
+  const double d = logp - static_cast<double>(t.old), r = logp - static_cast<double>(t.ref);
+  const double em = expm1((lane & 1) ? -r : d);
+  const double em_d = __shfl_sync(0xffffffffu, em, 0), em_r = __shfl_sync(0xffffffffu, em, 1);
+  const double A = t.A;
+  const double surr = clipped ? (A > 0.0 ? a.clip_hi : a.clip_lo) * A : (em_d + 1.0) * A;
+  double k = 0.0;
+  if (a.ref != nullptr) k = a.kl == 1 ? r : (a.kl == 2 ? 0.5 * r * r : em_r + r);
+  *kl = static_cast<float>(k);
+  return static_cast<double>(t.w) * (a.beta * k - surr);
+}
+
+__device__ __forceinline__ void write_token(const PolicyArgs& a, int64_t row, bool clipped, double logp, float kl,
+                                            double term) {
+  a.clip_mask[row] = clipped ? 1 : 0;
+  if (a.logp_out != nullptr) a.logp_out[row] = static_cast<float>(logp);
+  if (a.kl_out != nullptr) a.kl_out[row] = kl;
+  a.terms[row] = term;
+}
 // A token that is left out (weight 0, or an id outside the vocabulary): zeros.
-__device__ __forceinline__ void policy_no_token(const PolicyArgs& a, int64_t row) {
+__device__ __forceinline__ void write_no_token(const PolicyArgs& a, int64_t row) {
   a.clip_mask[row] = 0;
   if (a.logp_out != nullptr) a.logp_out[row] = 0.0f;
   if (a.kl_out != nullptr) a.kl_out[row] = 0.0f;
   a.terms[row] = 0.0;
 }
 
-__global__ void __launch_bounds__(kThreads) policy_rows(const __grid_constant__ PolicyArgs a) {
-  __shared__ float sh_m[kThreads / 32];
-  __shared__ double sh_s[kThreads / 32];
-  __shared__ float sh_g, sh_lse;
+// log(s): the exponent apart, so that the fp32 logarithm sees [1/2, 1) (absolute error 2^-25).
+__device__ __forceinline__ double log_of(double s) {
+  const int e = ((__double2hiint(s) >> 20) & 0x7FF) - 1022;
+  if (e <= -1022 || e >= 1025) return log(s);      // 0, subnormal, infinite, NaN
+  const float m = static_cast<float>(__hiloint2double((__double2hiint(s) & 0x000FFFFF) | 0x3FE00000, __double2loint(s)));
+  return (static_cast<double>(e) + static_cast<double>(log2f(m))) * 0.69314718055994530942;
+}
+
+// ======================================================================================
+// One CTA a row
+// ======================================================================================
+constexpr int kRowThreads = 512;
+
+__global__ void __launch_bounds__(kRowThreads) policy_rows(const __grid_constant__ PolicyArgs a) {
+  __shared__ float sh_m[kRowThreads / 32];
+  __shared__ double sh_s[kRowThreads / 32];
+  __shared__ float sh_g, sh_ls;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
     const uint16_t* x = a.logits + row * a.ldx;
     uint16_t* d = a.dlogits + row * a.ldd;
-    const int y = a.ids[row];
-    const bool used = a.weight[row] != 0.0f;
-    if (!used || y < 0 || y >= a.V) {
-      for (int64_t i = tid; i < a.V; i += kThreads) d[i] = 0;
+    const Token tok = load_token(a, row);
+    if (!tok.used(a.V)) {
+      for (int64_t i = tid; i < a.V; i += kRowThreads) d[i] = 0;
       if (tid == 0) {
-        if (used) set_device_status(a.status, DEV_BAD_INDEX);
-        policy_no_token(a, row);
+        if (tok.bad(a.V)) set_device_status(a.status, DEV_BAD_INDEX);
+        write_no_token(a, row);
       }
       continue;
     }
     float m = -INFINITY;
-    for (int64_t i = tid; i < a.V; i += kThreads) m = fmaxf(m, bf16_at(x, i));
+    for (int64_t i = tid; i < a.V; i += kRowThreads) m = fmaxf(m, bf16_at(x, i));
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
     if (lane == 0) sh_m[warp] = m;
     __syncthreads();
     m = sh_m[0];
-    for (int w = 1; w < kThreads / 32; ++w) m = fmaxf(m, sh_m[w]);
+    for (int w = 1; w < kRowThreads / 32; ++w) m = fmaxf(m, sh_m[w]);
     double s = 0.0;
-    for (int64_t i = tid; i < a.V; i += kThreads) s += static_cast<double>(expf(bf16_at(x, i) - m));
+    for (int64_t i = tid; i < a.V; i += kRowThreads)
+      s += static_cast<double>(ex2_approx((bf16_at(x, i) - m) * kLog2e));
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
     if (lane == 0) sh_s[warp] = s;
     __syncthreads();
-    if (tid == 0) {
+    if (warp == 0) {
       s = 0.0;
-      for (int w = 0; w < kThreads / 32; ++w) s += sh_s[w];
-      const double lse = static_cast<double>(m) + log(s);
-      const TokenGrad t = policy_token(a, row, static_cast<double>(bf16_at(x, y)) - lse);
-      a.terms[row] = t.term;
-      sh_g = t.g;
-      sh_lse = static_cast<float>(log(s));
+      for (int w = 0; w < kRowThreads / 32; ++w) s += sh_s[w];
+      const double ls = log_of(s);
+      const double logp = static_cast<double>(bf16_at(x, tok.y)) - (static_cast<double>(m) + ls);
+      const TokenLoss o = token_grad(a, tok, logp);
+      float kl;
+      const double term = token_term(a, tok, logp, o.clipped, lane, &kl);
+      if (lane == 0) {
+        write_token(a, row, o.clipped, logp, kl, term);
+        sh_g = o.g;
+        sh_ls = static_cast<float>(ls);
+      }
     }
     __syncthreads();
-    const float g = sh_g, ls = sh_lse;
-    for (int64_t i = tid; i < a.V; i += kThreads) {
-      const float p = expf(bf16_at(x, i) - m - ls);
-      d[i] = static_cast<uint16_t>(pack_bf16x2(g * ((i == y ? 1.0f : 0.0f) - p), 0.0f));
+    const float g = sh_g, ls = sh_ls;
+    for (int64_t i = tid; i < a.V; i += kRowThreads) {
+      const float p = ex2_approx((bf16_at(x, i) - m - ls) * kLog2e);
+      d[i] = to_bf16(g * ((i == tok.y ? 1.0f : 0.0f) - p));
     }
     __syncthreads();
   }
+}
+
+// ======================================================================================
+// A cluster a row, the row in shared memory
+// ======================================================================================
+constexpr int kMaxCluster = 8;
+constexpr int kBufs = 3;                       // slices in shared memory
+constexpr int kSlice2 = 38000;                 // slice bytes with which two CTAs share an SM
+constexpr int kSliceMax = 76000;               // three slices in one CTA's shared memory
+constexpr int kSmallGranules = 512;            // slices up to here: 128 streaming threads
+
+// How a row lies in memory: `head` logits before its first 16-byte granule, `nv` whole granules, then
+// the tail; granules [g0, g0 + n) are this CTA's.
+struct RowSpan {
+  int head, tail, nv, g0, n;
+};
+__device__ __forceinline__ RowSpan row_span(const PolicyArgs& a, int64_t row, int per, int rank) {
+  RowSpan s;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(a.logits + row * a.ldx);
+  s.head = static_cast<int>((16 - (at & 15)) & 15) / 2;
+  if (s.head > a.V) s.head = static_cast<int>(a.V);
+  s.nv = static_cast<int>(a.V - s.head) >> 3;
+  s.tail = static_cast<int>(a.V) - s.head - 8 * s.nv;
+  s.g0 = rank * per;
+  s.n = s.nv - s.g0;
+  s.n = s.n < 0 ? 0 : (s.n > per ? per : s.n);
+  return s;
+}
+
+// The logit outside the granules that a lane owns, or -1.
+__device__ __forceinline__ int64_t edge_index(const RowSpan& s, int64_t V, int lane) {
+  if (lane >= 16 && lane - 16 < s.head) return lane - 16;
+  if (lane >= 24 && lane - 24 < s.tail) return V - s.tail + lane - 24;
+  return -1;
+}
+
+// Sums of exponentials are unevaluated fp32 pairs (about 48 bits): fp64 is slow here, and every
+// join below sits on the row's critical path.
+struct Pair {
+  float hi, lo;
+};
+__device__ __forceinline__ Pair pair_add(Pair a, Pair b) {
+  const float s = a.hi + b.hi;
+  const float bb = s - a.hi;
+  const float err = (a.hi - (s - bb)) + (b.hi - bb);
+  return {s, err + (a.lo + b.lo)};
+}
+// Over the lanes that differ in the bits below kLanes: the maximum of m, and the sum of the parts
+// s relative to it (each given relative to its own m; m a logit, not scaled).  -INF with 0
+// is an empty part.
+template <int kLanes>
+__device__ __forceinline__ void join_lanes(float& m, Pair& s) {
+  float M = m;
+#pragma unroll
+  for (int off = kLanes / 2; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+  const float f = m == -INFINITY ? 1.0f : ex2_approx((m - M) * kLog2e);
+  s.hi *= f;
+  s.lo *= f;
+#pragma unroll
+  for (int off = kLanes / 2; off > 0; off >>= 1) {
+    const Pair o = {__shfl_xor_sync(0xffffffffu, s.hi, off), __shfl_xor_sync(0xffffffffu, s.lo, off)};
+    s = pair_add(s, o);
+  }
+  m = M;
+}
+// log(s): the exponent apart, so that the fp32 logarithm sees [1/2, 1) (absolute error 2^-25).
+__device__ __forceinline__ double log_pair(Pair s) {
+  int e = 0;
+  const float f = frexpf(s.hi, &e);
+  return (static_cast<double>(e) + static_cast<double>(log2f(f) + s.lo / s.hi * kLog2e)) * 0.69314718055994530942;
+}
+
+// Named barriers.  The streaming warps take the sums of row r + 1 before they wait for the gradient
+// of row r, so the parts of row r + 2 come behind the scalar warp's use of those of row r: two
+// ids (row parity).  Nothing holds the scalar and streaming warps back from running ahead of
+// the output warp but the copies that it issues: row r + 3 is requested behind its waits for row
+// r, and the rows at the end, which wait for no copy, are at most three: three ids.
+enum : uint32_t { kBarParts = 1, kBarG = 3, kBarEmpty = 5, kBarOut = 8, kBarCopy = 11 };
+
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Eight logits from word kFirst (and a half, if odd) of two granules on.
+template <int kFirst>
+__device__ __forceinline__ void cut_words(const uint32_t (&w)[8], bool odd, uint32_t (&o)[4]) {
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+    o[u] = odd ? __byte_perm(w[kFirst + u], w[kFirst + u + 1], 0x5432) : w[kFirst + u];
+}
+
+template <int kStream>
+__global__ void __launch_bounds__(kStream + 64, kStream == 256 ? 2 : 4)
+    policy_cluster(const __grid_constant__ PolicyArgs a, int cl, int per) {
+  constexpr int kWarps = kStream / 32;
+  constexpr int kThreads = kStream + 32;        // streaming warps and one other
+  extern __shared__ __align__(128) uint8_t dyn[];
+  __shared__ __align__(8) uint64_t full[kBufs], xbar[2];
+  __shared__ float part[2][kWarps][3];         // a warp's maximum and sum (pair)
+  __shared__ float slot[2][kMaxCluster][3];    // a CTA's, by rank
+  __shared__ float sh_g[2], sh_c[2], sh_gy[2];
+  __shared__ double sh_logp[kBufs];            // for the output warp
+  __shared__ int sh_state[kBufs];                  // 0 left out, 1 used, 2 used and clipped, 3 aborted
+  __shared__ int sh_used[kBufs], sh_y[2];
+  // Set when a bounded wait of this CTA or of a peer gave up: rows are only walked through from
+  // then on, with NaN terms and gradients of zero.
+  __shared__ int cl_abort;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = cl > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int64_t cid = cl > 1 ? cluster_id_x() : blockIdx.x;
+  const int64_t ncl = cl > 1 ? cluster_count_x() : gridDim.x;
+  const int slice = per * 16;
+  volatile int* vabort = &cl_abort;
+  // rows that all lie alike are looked at once
+  const bool alike = a.ldx % 8 == 0;
+
+  if (tid == 0) {
+    cl_abort = 0;
+    for (int i = 0; i < kBufs; ++i) mbar_init(&full[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&xbar[i], static_cast<uint32_t>(cl));
+    fence_mbar_init();
+  }
+  __syncthreads();
+  if (cl > 1) cluster_sync_all();     // peers' barriers are ready before any remote arrival
+  pdl_launch_dependents();
+
+  RowSpan sp = row_span(a, cid, per, rank);
+  if (warp == kWarps) {
+    // ------------------------------------------------------------------ scalar warp
+    // What belongs to the next rows is loaded ahead: a token two rows, its logit and the
+    // logits outside the granules (lanes 16-22 the head's, 24-30 the tail's, on rank 0) one.
+    struct Ahead {
+      Token tok;
+      float xy, edge;
+    };
+    auto token = [&](int64_t row) {
+      Token t = {0, 0.0f, 0.0f, 0.0f, 0.0f};
+      if (row < a.T) t = load_token(a, row);
+      return t;
+    };
+    auto logits = [&](int64_t row, const Token& t) {
+      Ahead r = {t, 0.0f, -INFINITY};
+      if (row < a.T && t.used(a.V)) {
+        const uint16_t* x = a.logits + row * a.ldx;
+        r.xy = bf16_at(x, t.y);
+        if (rank == 0) {
+          const int64_t e = edge_index(alike ? sp : row_span(a, row, per, rank), a.V, lane);
+          if (e >= 0) r.edge = bf16_at(x, e);
+        }
+      }
+      return r;
+    };
+    Ahead now = logits(cid, token(cid));
+    Token next = token(cid + ncl);
+    uint32_t ux = 0;                   // rows exchanged
+    int it = 0, b = 0;
+    for (int64_t row = cid; row < a.T; row += ncl, ++it, b = b == kBufs - 1 ? 0 : b + 1) {
+      const int par = it & 1;
+      const Token t = now.tok;
+      const float xv = now.xy, ev = now.edge;
+      now = logits(row + ncl, next);
+      next = token(row + 2 * ncl);
+      if (!alike) sp = row_span(a, row, per, rank);
+      TokenLoss o;
+      o.g = 0.0f;
+      o.clipped = false;
+      double logp = 0.0;
+      float lse = 0.0f;
+      bool aborted = false;
+      named_barrier_sync(kBarParts + par, kThreads);
+      if (t.used(a.V)) {
+        float m = -INFINITY;
+        Pair s = {0.0f, 0.0f};
+        if (lane < kWarps) {
+          m = part[par][lane][0];
+          s = {part[par][lane][1], part[par][lane][2]};
+        } else if (lane >= 16) {
+          m = ev;                        // a logit outside the granules
+          s.hi = ev == -INFINITY ? 0.0f : 1.0f;
+        }
+        if (rank == 0) join_lanes<32>(m, s); else join_lanes<8>(m, s);
+        // (the shuffles also make sure that xv has arrived: the row may be overwritten in place
+        // once the partials are out)
+        const float x_y = __shfl_sync(0xffffffffu, xv, 0);
+        aborted = *vabort != 0;
+        if (cl > 1 && !aborted) {
+          const int sl = ux & 1;
+          if (lane < cl) {
+            const uint32_t dst = cluster_map(&slot[sl][rank][0], lane);
+            st_cluster_f32(dst, m);
+            st_cluster_f32(dst + 4, s.hi);
+            st_cluster_f32(dst + 8, s.lo);
+            mbar_arrive_remote(cluster_map(&xbar[sl], lane));
+          }
+          __syncwarp();
+          aborted = !mbar_wait_cluster(&xbar[sl], (ux >> 1) & 1u, a.status, vabort);
+          aborted = __any_sync(0xffffffffu, aborted);
+          if (!aborted) {
+            // every CTA joins the same parts the same way
+            const bool in = lane < cl;
+            m = in ? slot[sl][lane][0] : -INFINITY;
+            s = {in ? slot[sl][lane][1] : 0.0f, in ? slot[sl][lane][2] : 0.0f};
+            join_lanes<8>(m, s);
+            m = __shfl_sync(0xffffffffu, m, 0);
+            s = {__shfl_sync(0xffffffffu, s.hi, 0), __shfl_sync(0xffffffffu, s.lo, 0)};
+          }
+        }
+        // the peers' own waits poll their flag
+        if (cl > 1 && aborted && lane < cl) st_cluster_u32(cluster_map(&cl_abort, lane), 1u);
+        ++ux;
+        const double ls = static_cast<double>(m) + log_pair(s);
+        logp = static_cast<double>(x_y) - ls;
+        lse = static_cast<float>(ls);
+        if (!aborted) o = token_grad(a, t, logp);
+      }
+      // -g p = -sign(g) 2^(x log2 e - lse log2 e + log2 |g|)
+      const float c = fmaf(-lse, kLog2e, log2f(fabsf(o.g)));
+      const float gy = o.g * (1.0f - ex2_approx(static_cast<float>(logp) * kLog2e));
+      if (lane == 0) {
+        sh_g[par] = o.g;
+        sh_c[par] = c;
+        sh_gy[par] = gy;
+        sh_y[par] = t.used(a.V) ? t.y - sp.head : -1;
+        sh_logp[b] = logp;
+        sh_state[b] = aborted ? 3 : (!t.used(a.V) ? 0 : (o.clipped ? 2 : 1));
+        __threadfence_block();
+      }
+      __syncwarp();
+      named_barrier_arrive(kBarG + par, kThreads);
+      named_barrier_arrive(kBarOut + b, 64);
+      if (rank == 0) {
+        const int64_t e = edge_index(sp, a.V, lane);
+        if (e >= 0) {
+          float v = 0.0f;
+          if (o.g != 0.0f) v = e == t.y ? gy : copysignf(ex2_approx(fmaf(ev, kLog2e, c)), -o.g);
+          if (o.g != o.g) v = o.g;
+          a.dlogits[row * a.ldd + e] = to_bf16(v);
+        }
+      }
+    }
+  } else if (warp > kWarps) {
+    // ------------------------------------------------------------------ output warp
+    // Requests a row's slice as soon as a buffer is free (three rows ahead of the gradient), and
+    // writes the token's outputs, the loss term in fp64 (slow here) among them.
+    auto request = [&](int64_t row, int b, const Token& t) {
+      if (row >= a.T) return;
+      const bool used = t.used(a.V);
+      const RowSpan rs = alike ? sp : row_span(a, row, per, rank);
+      if (lane == 0) {
+        sh_used[b] = used ? 1 : 0;
+        if (used && rs.n > 0 && !*vabort) {
+          mbar_arrive_expect_tx(&full[b], static_cast<uint32_t>(rs.n) * 16u);
+          bulk_load(dyn + b * slice, a.logits + row * a.ldx + rs.head + 8 * static_cast<int64_t>(rs.g0),
+                    static_cast<uint32_t>(rs.n) * 16u, &full[b]);
+        } else {
+          mbar_arrive(&full[b]);
+        }
+      }
+      __syncwarp();
+    };
+    auto token = [&](int64_t row) {
+      Token t = {0, 0.0f, 0.0f, 0.0f, 0.0f};
+      if (row < a.T) t = load_token(a, row);
+      return t;
+    };
+    Token t0 = token(cid), t1 = token(cid + ncl), t2 = token(cid + 2 * ncl), t3 = token(cid + 3 * ncl);
+    request(cid, 0, t0);
+    request(cid + ncl, 1, t1);
+    request(cid + 2 * ncl, 2, t2);
+    int it = 0, b = 0;
+    for (int64_t row = cid; row < a.T; row += ncl, ++it, b = b == kBufs - 1 ? 0 : b + 1) {
+      named_barrier_sync(kBarOut + b, 64);
+      const double logp = sh_logp[b];
+      const int state = sh_state[b];
+      __syncwarp();
+      named_barrier_sync(kBarEmpty + b, kThreads);
+      request(row + kBufs * ncl, b, t3);
+      const Token t = t0;
+      t0 = t1;
+      t1 = t2;
+      t2 = t3;
+      t3 = token(row + (kBufs + 1) * ncl);
+      if (rank != 0) continue;
+      if (state == 0) {
+        if (lane == 0) {
+          if (t.bad(a.V)) set_device_status(a.status, DEV_BAD_INDEX);
+          write_no_token(a, row);
+        }
+        continue;
+      }
+      float kl;
+      double term = token_term(a, t, logp, state == 2, lane, &kl);
+      double lp = logp;
+      if (state == 3) {
+        term = lp = __longlong_as_double(0x7ff8000000000000ll);
+        kl = static_cast<float>(lp);
+      }
+      if (lane == 0) write_token(a, row, state == 2, lp, kl, term);
+    }
+    if (*vabort) {
+      // copies still in flight land before the CTA may exit: the last request of each buffer
+      for (int i = 0; i < kBufs; ++i)
+        if (it > i) mbar_wait_ns(&full[i], static_cast<uint32_t>((it - 1 - i) / kBufs) & 1u, 200000000ull);
+    }
+  } else {
+    // -------------------------------------------------------------- streaming warps
+    const uint64_t l2 = f2_pack(kLog2e, kLog2e);
+    // Maximum and sum of this CTA's slice of its i-th row: the warp's maximum first, then one
+    // exponential a logit.
+    auto pass1 = [&](int64_t row, int i) {
+      const int bi = i % kBufs, par = i & 1;
+      const int n = alike ? sp.n : row_span(a, row, per, rank).n;
+      const uint4* buf = reinterpret_cast<const uint4*>(dyn + bi * slice);
+      // (after an abort the rows are only walked through, barrier by barrier: every row still
+      // arrives here, without a copy)
+      const bool here = mbar_wait(&full[bi], static_cast<uint32_t>(i / kBufs) & 1u, a.status);
+      if (!here) *vabort = 1;
+      float m = -INFINITY;
+      Pair s = {0.0f, 0.0f};
+      if (here && sh_used[bi] != 0 && !*vabort) {
+        uint32_t mx = 0xFF80FF80u;
+#pragma unroll 4
+        for (int j = tid; j < n; j += kStream) {
+          const uint4 v = buf[j];
+          mx = max_bf16x2(mx, max_bf16x2(max_bf16x2(v.x, v.y), max_bf16x2(v.z, v.w)));
+        }
+        m = fmaxf(lo_bf16(mx), hi_bf16(mx));
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+        const float base = m == -INFINITY ? 0.0f : -m;
+        const uint64_t nb = f2_pack(base, base);
+        uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll 2
+        for (int j = tid; j < n; j += kStream) {
+          const uint4 v = buf[j];
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            float e0, e1;
+            f2_unpack(f2_mul(f2_add(f2_pack(lo_bf16(w[u]), hi_bf16(w[u])), nb), l2), e0, e1);
+            acc[u] = f2_add(acc[u], f2_pack(ex2_approx(e0), ex2_approx(e1)));
+          }
+        }
+        float s0, s1;
+        f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), s0, s1);
+        s.hi = s0 + s1;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1)
+          s = pair_add(s, {__shfl_xor_sync(0xffffffffu, s.hi, off), __shfl_xor_sync(0xffffffffu, s.lo, off)});
+      }
+      if (lane == 0) {
+        part[par][warp][0] = m;
+        part[par][warp][1] = s.hi;
+        part[par][warp][2] = s.lo;
+        __threadfence_block();
+      }
+      __syncwarp();
+      named_barrier_arrive(kBarParts + par, kThreads);
+    };
+    int it = 0;
+    if (cid < a.T) pass1(cid, 0);
+    for (int64_t row = cid; row < a.T; row += ncl, ++it) {
+      const int par = it & 1;
+      uint4* buf = reinterpret_cast<uint4*>(dyn + (it % kBufs) * slice);
+      // the next row's sums while this row's are exchanged
+      if (row + ncl < a.T) pass1(row + ncl, it + 1);
+      named_barrier_sync(kBarG + par, kThreads);
+      const float g = sh_g[par], c = sh_c[par], gy = sh_gy[par];
+      const int y = sh_y[par];
+      if (!alike) sp = row_span(a, row, per, rank);
+      const int yg = y >= 0 ? (y >> 3) - sp.g0 : -1;        // granule of the sampled token
+      uint16_t* d = a.dlogits + row * a.ldd + sp.head + 8 * static_cast<int64_t>(sp.g0);
+      const bool direct = (reinterpret_cast<uintptr_t>(d) & 15) == 0;
+      uint4* d4 = direct ? reinterpret_cast<uint4*>(d) : buf;
+      const uint32_t sign = g > 0.0f ? 0x80008000u : 0u;
+      const uint64_t c2 = f2_pack(c, c);
+      if (g == 0.0f || *vabort) {
+        for (int i = tid; i < sp.n; i += kStream) d4[i] = make_uint4(0u, 0u, 0u, 0u);
+      } else {
+#pragma unroll 2
+        for (int i = tid; i < sp.n; i += kStream) {
+          const uint4 v = buf[i];
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          uint32_t o[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            float e0, e1;
+            f2_unpack(f2_fma(f2_pack(lo_bf16(w[u]), hi_bf16(w[u])), l2, c2), e0, e1);
+            o[u] = pack_bf16x2(ex2_approx(e0), ex2_approx(e1)) ^ sign;
+          }
+          if (i == yg) {
+            const uint32_t h = to_bf16(gy);
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              if (u == (y & 7) >> 1) o[u] = (y & 1) ? (o[u] & 0xFFFFu) | (h << 16) : (o[u] & 0xFFFF0000u) | h;
+          }
+          d4[i] = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+      }
+      if (!direct && sp.n > 0) {
+        // the gradient row lies at another offset from a 16-byte boundary: its granules are cut
+        // from two of the buffer's
+        named_barrier_sync(kBarCopy, kStream);
+        const int n = 8 * sp.n;
+        const int off = static_cast<int>((16 - (reinterpret_cast<uintptr_t>(d) & 15)) & 15) / 2;
+        const int nd = (n - off) >> 3;
+        uint4* to = reinterpret_cast<uint4*>(d + off);
+        for (int i = tid; i < nd; i += kStream) {
+          const uint4 p = buf[i], q = buf[i + 1];
+          const uint32_t w[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
+          uint32_t o[4];
+          switch (off >> 1) {
+            case 0: cut_words<0>(w, off & 1, o); break;
+            case 1: cut_words<1>(w, off & 1, o); break;
+            case 2: cut_words<2>(w, off & 1, o); break;
+            default: cut_words<3>(w, off & 1, o); break;
+          }
+          to[i] = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+        const uint16_t* h = reinterpret_cast<const uint16_t*>(buf);
+        if (tid < off) d[tid] = h[tid];
+        if (tid < n - off - 8 * nd) d[off + 8 * nd + tid] = h[off + 8 * nd + tid];
+        // the next copy into this buffer comes behind the writes above
+        fence_proxy_async_smem();
+      }
+      named_barrier_arrive(kBarEmpty + it % kBufs, kThreads);
+    }
+  }
+  __syncwarp();
+  // No CTA leaves while a peer may still write its shared memory; every wait above is bounded.
+  if (cl > 1) cluster_sync_all();
 }
 
 constexpr int kReduceThreads = 1024;
 
 __global__ void __launch_bounds__(kReduceThreads) policy_reduce(const double* terms, int64_t n,
                                                                float* loss) {
-  __shared__ double sh[kReduceThreads];
+  __shared__ double sh[kReduceThreads / 32];
   const int tid = threadIdx.x;
+  pdl_wait();
   double acc = 0.0;
   for (int64_t i = tid; i < n; i += kReduceThreads) acc += terms[i];
-  sh[tid] = acc;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
+  if ((tid & 31) == 0) sh[tid >> 5] = acc;
   __syncthreads();
-  for (int w = kReduceThreads / 2; w > 0; w >>= 1) {
-    if (tid < w) sh[tid] += sh[tid + w];
-    __syncthreads();
+  if (tid < 32) {
+    acc = sh[tid];
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
+    if (tid == 0) *loss = static_cast<float>(acc);
   }
-  if (tid == 0) *loss = static_cast<float>(sh[0]);
+}
+
+template <int kStream>
+cudaError_t launch_cluster(const PolicyArgs& a, int cl, int per, cudaStream_t s) {
+  constexpr int kThreads = kStream + 64;
+  const int smem = kBufs * per * 16;
+  static bool attr_set[kMaxDeviceCache] = {};
+  const int dev = cached_device_index();
+  if (dev < 0) return cudaErrorInvalidDevice;
+  if (!attr_set[dev]) {
+    cudaError_t e = cudaFuncSetAttribute(policy_cluster<kStream>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kBufs * kSliceMax);
+    if (e != cudaSuccess) return e;
+    attr_set[dev] = true;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(cl);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = cl > 1 ? 1 : 0;
+  int n = 0;
+  if (cl > 1) {
+    cfg.gridDim = dim3(static_cast<unsigned>(num_sms() * cl), 1, 1);
+    if (cudaOccupancyMaxActiveClusters(&n, policy_cluster<kStream>, &cfg) != cudaSuccess || n <= 0) {
+      (void)cudaGetLastError();
+      n = num_sms() / cl;
+    }
+  } else {
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, policy_cluster<kStream>, kThreads,
+                                                      static_cast<size_t>(smem)) != cudaSuccess || n <= 0) {
+      (void)cudaGetLastError();
+      n = 1;
+    }
+    n *= num_sms();
+  }
+  if (n > a.T) n = static_cast<int>(a.T);
+  cfg.gridDim = dim3(static_cast<unsigned>(n * cl), 1, 1);
+  return cudaLaunchKernelEx(&cfg, policy_cluster<kStream>, a, cl, per);
 }
 
 }  // namespace
 
 cudaError_t launch_policy_loss(const PolicyArgs& a, cudaStream_t s) {
-  int64_t grid = static_cast<int64_t>(num_sms()) * 4;
-  if (grid > a.T) grid = a.T;
-  policy_rows<<<static_cast<unsigned>(grid), kThreads, 0, s>>>(a);
-  cudaError_t e = cudaGetLastError();
+  // the fewest CTAs a row whose slices let two of them share an SM
+  const int64_t granules = (a.V + 7) / 8;
+  int cl = 1;
+  while (cl < kMaxCluster && (granules + cl - 1) / cl * 16 > kSlice2) cl *= 2;
+  int64_t per = (granules + cl - 1) / cl;
+  if (per < 1) per = 1;
+  cudaError_t e;
+  if (per * 16 <= kSliceMax) {
+    e = per <= kSmallGranules ? launch_cluster<128>(a, cl, static_cast<int>(per), s)
+                              : launch_cluster<256>(a, cl, static_cast<int>(per), s);
+  } else {
+    int64_t grid = static_cast<int64_t>(num_sms()) * 4;
+    if (grid > a.T) grid = a.T;
+    policy_rows<<<static_cast<unsigned>(grid), kRowThreads, 0, s>>>(a);
+    e = cudaGetLastError();
+  }
   if (e != cudaSuccess) return e;
-  policy_reduce<<<1, kReduceThreads, 0, s>>>(a.terms, a.T, a.loss);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(1);
+  cfg.blockDim = dim3(kReduceThreads);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, policy_reduce, static_cast<const double*>(a.terms), a.T, a.loss);
 }
 
 }  // namespace ls
