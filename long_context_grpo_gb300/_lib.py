@@ -128,8 +128,8 @@ def _load():
                                                 vp, sz, vp]),
         "ls_block_replay_bwd": (ctypes.c_int, [vp, i64, i64, vp, vp, vp, vp, vp, vp, sz, vp]),
         "ls_policy_loss_workspace_bytes": (sz, [i64]),
-        "ls_policy_loss": (ctypes.c_int, [ctypes.POINTER(PolicyLossDesc), vp, sz, vp]),
-        "ls_rope": (ctypes.c_int, [ctypes.POINTER(RopeDesc), vp]),
+        "ls_policy_loss": (ctypes.c_int, [vp, vp, sz, vp]),
+        "ls_rope": (ctypes.c_int, [vp, vp]),
         "ls_rope_freqs": (ctypes.c_int, [i32, ctypes.c_double, i32, ctypes.c_double, i64,
                                          ctypes.c_double, ctypes.c_double, vp, vp]),
         "ls_cache_create": (ctypes.c_int, [ctypes.POINTER(CacheDesc), ctypes.POINTER(vp)]),
@@ -140,9 +140,9 @@ def _load():
         "ls_cache_fork": (ctypes.c_int, [vp, i32, vp, vp, vp, sz, vp]),
         "ls_cache_free": (ctypes.c_int, [vp, i32, vp, vp]),
         "ls_cache_compact": (ctypes.c_int, [vp, vp, vp, vp, sz, vp]),
-        "ls_cache_append": (ctypes.c_int, [vp, ctypes.POINTER(CacheAppendDesc), vp]),
+        "ls_cache_append": (ctypes.c_int, [vp, vp, vp]),
         "ls_cache_attn_workspace_bytes": (sz, [vp, i32, i64, i32, i64]),
-        "ls_cache_attn": (ctypes.c_int, [vp, ctypes.POINTER(CacheAttnDesc), vp, sz, vp]),
+        "ls_cache_attn": (ctypes.c_int, [vp, vp, vp, sz, vp]),
         "ls_get_device_status": (ctypes.c_int, [vp, ctypes.POINTER(ctypes.c_uint32)]),
         "ls_timing_enable": (ctypes.c_int, [ctypes.c_int]),
         "ls_debug_wait_timeout": (ctypes.c_int, [ctypes.c_uint64, vp]),

@@ -6,6 +6,7 @@ stream; outputs and workspaces that are not given are allocated on it.
 from __future__ import annotations
 
 import ctypes
+import struct
 from typing import NamedTuple
 
 import torch
@@ -17,43 +18,65 @@ _SCALING = {"none": 0, "linear": 1, "ramp": 2}
 _LAYOUT = {"NHD": 0, "HND": 1}
 
 
-def _ptr(t, name, dtype, shape=None):
-    """As _lib._ptr, and on the current device (whose stream the call goes to)."""
-    p = b._ptr(t, name, dtype, shape)
-    if t is not None and t.device.index != torch.cuda.current_device():
-        raise ValueError("%s is on %s, the current device is cuda:%d"
-                         % (name, t.device, torch.cuda.current_device()))
-    return p
+# The descriptors of include/longstraw.h as native struct layouts: packing one is several times
+# cheaper than filling a ctypes.Structure, and small calls are bound by the host.
+_POLICY = struct.Struct("@qqqqPPPPPPdddiPPPPP")
+_ROPE = struct.Struct("@qiiiiiiPdPqPqPqPqPq")
+_APPEND = struct.Struct("@iqPPPqPqPqPqPiid")
+_ATTN = struct.Struct("@iqPPiqPqPPiP")
+
+_Tensor = torch.Tensor
+_bf16, _f32, _i32, _i64, _u8 = torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8
 
 
-def _strided(t, name, shape, strides, width):
+def _ptr(t, name, dtype, shape, dev):
+    """Address of a contiguous tensor of this type and shape (None: any) on device `dev`, the
+    current one, whose stream the call goes to."""
+    if (isinstance(t, _Tensor) and t.dtype is dtype and t.get_device() == dev and t.is_contiguous()
+            and (shape is None or t.shape == shape)):
+        return t.data_ptr()
+    b._ptr(t, name, dtype, shape)          # says what is wrong with it
+    if t is None:
+        raise TypeError("%s must be a CUDA tensor" % name)
+    raise ValueError("%s is on %s, the current device is cuda:%d" % (name, t.device, dev))
+
+
+def _opt(t, name, dtype, shape, dev):
+    return 0 if t is None else _ptr(t, name, dtype, shape, dev)
+
+
+def _strided(t, name, shape, strides, width, dev):
     """(pointer, elements between rows) of a bf16 tensor of this shape whose dimensions behind
     the first have these strides; the rows hold `width` values each."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not isinstance(t, _Tensor) or not t.is_cuda:
         raise TypeError("%s must be a CUDA tensor" % name)
-    if t.dtype != torch.bfloat16:
-        raise TypeError("%s must be %s, got %s" % (name, torch.bfloat16, t.dtype))
-    if tuple(t.shape) != shape:
+    if t.dtype is not _bf16:
+        raise TypeError("%s must be %s, got %s" % (name, _bf16, t.dtype))
+    if t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
     st = t.stride()
-    for n, have, want in zip(shape[1:], st[1:], strides):
-        if n > 1 and have != want:
-            raise ValueError("%s must be contiguous behind its first dimension" % name)
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError("%s is on %s, the current device is cuda:%d"
-                         % (name, t.device, torch.cuda.current_device()))
+    if st[1:] != strides:
+        for n, have, want in zip(shape[1:], st[1:], strides):
+            if n > 1 and have != want:
+                raise ValueError("%s must be contiguous behind its first dimension" % name)
+    if t.get_device() != dev:
+        raise ValueError("%s is on %s, the current device is cuda:%d" % (name, t.device, dev))
     # one row: whatever stride torch keeps for it
-    return t.data_ptr(), (st[0] if shape[0] > 1 else max(width, (width + 7) // 8 * 8))
+    return t.data_ptr(), (st[0] if shape[0] > 1 else (width + 7) // 8 * 8)
 
 
-def _heads(t, name, T, H, D):
-    return _strided(t, name, (T, H, D), (D, 1), H * D)
+def _heads(t, name, T, H, D, dev):
+    return _strided(t, name, (T, H, D), (D, 1), H * D, dev)
+
+
+def _raw_stream(dev):
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _host_doubles(x, name):
     """(pointer, count, keep-alive) of float64 values on the host."""
-    if isinstance(x, torch.Tensor):
-        if x.is_cuda or x.dtype != torch.float64 or x.dim() != 1 or not x.is_contiguous():
+    if isinstance(x, _Tensor):
+        if x.is_cuda or x.dtype is not torch.float64 or x.dim() != 1 or not x.is_contiguous():
             raise TypeError("%s must be a contiguous 1-D float64 tensor on the CPU" % name)
         return x.data_ptr(), x.numel(), x
     v = [float(e) for e in x]
@@ -86,26 +109,27 @@ def policy_loss(logits, ids, logp_old, advantages, weights, eps_low=0.2, eps_hig
     if kl not in _KL:
         raise ValueError("kl must be one of %s" % (tuple(_KL),))
     T, V = logits.shape
-    x, ldx = _strided(logits, "logits", (T, V), (1,), V)
-    dev = logits.device
+    dev = torch.cuda.current_device()
+    at = logits.device
+    x, ldx = _strided(logits, "logits", (T, V), (1,), V, dev)
     if dlogits is None:
-        dlogits = torch.empty((T, V), dtype=torch.bfloat16, device=dev)
-    dx, ldd = _strided(dlogits, "dlogits", (T, V), (1,), V)
-    loss = torch.empty(1, dtype=torch.float32, device=dev) if loss is None else loss
-    logp_out = torch.empty(T, dtype=torch.float32, device=dev) if logp_out is None else logp_out
-    kl_out = torch.empty(T, dtype=torch.float32, device=dev) if kl_out is None else kl_out
-    clip_mask = torch.empty(T, dtype=torch.uint8, device=dev) if clip_mask is None else clip_mask
+        dlogits = torch.empty((T, V), dtype=_bf16, device=at)
+    dx, ldd = _strided(dlogits, "dlogits", (T, V), (1,), V, dev)
+    loss = torch.empty(1, dtype=_f32, device=at) if loss is None else loss
+    logp_out = torch.empty(T, dtype=_f32, device=at) if logp_out is None else logp_out
+    kl_out = torch.empty(T, dtype=_f32, device=at) if kl_out is None else kl_out
+    clip_mask = torch.empty(T, dtype=_u8, device=at) if clip_mask is None else clip_mask
     if workspace is None:
-        workspace = torch.empty(max(policy_loss_workspace_bytes(T), 16), dtype=torch.uint8, device=dev)
-    f32 = torch.float32
-    d = b.PolicyLossDesc(
-        T, V, ldx, ldd, x, _ptr(ids, "ids", torch.int32, (T,)), _ptr(logp_old, "logp_old", f32, (T,)),
-        _ptr(logp_ref, "logp_ref", f32, (T,)), _ptr(advantages, "advantages", f32, (T,)),
-        _ptr(weights, "weights", f32, (T,)), float(eps_low), float(eps_high), float(beta), _KL[kl],
-        _ptr(loss, "loss", f32, (1,)), dx, _ptr(clip_mask, "clip_mask", torch.uint8, (T,)),
-        _ptr(logp_out, "logp_out", f32, (T,)), _ptr(kl_out, "kl_out", f32, (T,)))
-    b._check(b._lib().ls_policy_loss(ctypes.byref(d), _ptr(workspace, "workspace", torch.uint8),
-                                     workspace.numel(), b._stream()), "ls_policy_loss")
+        workspace = torch.empty(max(policy_loss_workspace_bytes(T), 16), dtype=_u8, device=at)
+    n = (T,)
+    d = _POLICY.pack(
+        T, V, ldx, ldd, x, _ptr(ids, "ids", _i32, n, dev), _ptr(logp_old, "logp_old", _f32, n, dev),
+        _opt(logp_ref, "logp_ref", _f32, n, dev), _ptr(advantages, "advantages", _f32, n, dev),
+        _ptr(weights, "weights", _f32, n, dev), eps_low, eps_high, beta, _KL[kl],
+        _ptr(loss, "loss", _f32, (1,), dev), dx, _ptr(clip_mask, "clip_mask", _u8, n, dev),
+        _ptr(logp_out, "logp_out", _f32, n, dev), _ptr(kl_out, "kl_out", _f32, n, dev))
+    b._check(b._lib().ls_policy_loss(d, _ptr(workspace, "workspace", _u8, None, dev), workspace.numel(),
+                                     _raw_stream(dev)), "ls_policy_loss")
     return PolicyLoss(loss, dlogits, logp_out, kl_out, clip_mask)
 
 
@@ -133,21 +157,22 @@ def rope(q, k, inv_freq, positions=None, pos0: int = 0, interleaved: bool = Fals
     if not isinstance(some, torch.Tensor) or some.dim() != 3:
         raise TypeError("q or k must be a 3-D CUDA tensor")
     T, _, D = some.shape
+    dev = torch.cuda.current_device()
     f, n, keep = _host_doubles(inv_freq, "inv_freq")
-    d = b.RopeDesc(T=T, D=D, rot_dim=2 * n, interleaved=int(interleaved), inverse=int(inverse),
-                   inv_freq=f, attn_factor=float(attn_factor), pos0=pos0,
-                   positions=_ptr(positions, "positions", torch.int64, (T,)))
+    Hq = Hk = qp = qs = qo = qos = kp = ks = ko = kos = 0
     if q is not None:
-        d.Hq = q.shape[1]
-        d.q, d.q_stride = _heads(q, "q", T, d.Hq, D)
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
-        d.q_out, d.q_out_stride = _heads(q_out, "q_out", T, d.Hq, D)
+        Hq = q.shape[1]
+        qp, qs = _heads(q, "q", T, Hq, D, dev)
+        q_out = torch.empty((T, Hq, D), dtype=_bf16, device=q.device) if q_out is None else q_out
+        qo, qos = _heads(q_out, "q_out", T, Hq, D, dev)
     if k is not None:
-        d.Hk = k.shape[1]
-        d.k, d.k_stride = _heads(k, "k", T, d.Hk, D)
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device) if k_out is None else k_out
-        d.k_out, d.k_out_stride = _heads(k_out, "k_out", T, d.Hk, D)
-    b._check(b._lib().ls_rope(ctypes.byref(d), b._stream()), "ls_rope")
+        Hk = k.shape[1]
+        kp, ks = _heads(k, "k", T, Hk, D, dev)
+        k_out = torch.empty((T, Hk, D), dtype=_bf16, device=k.device) if k_out is None else k_out
+        ko, kos = _heads(k_out, "k_out", T, Hk, D, dev)
+    d = _ROPE.pack(T, Hq, Hk, D, 2 * n, bool(interleaved), bool(inverse), f, attn_factor,
+                   _opt(positions, "positions", _i64, (T,), dev), pos0, qp, qs, qo, qos, kp, ks, ko, kos)
+    b._check(b._lib().ls_rope(d, _raw_stream(dev)), "ls_rope")
     return q_out, k_out
 
 
@@ -173,21 +198,23 @@ class PagedCache:
         N, D = shape[0], shape[3]
         ps, Hkv = (shape[1], shape[2]) if layout == "NHD" else (shape[2], shape[1])
         inner = (shape[2] * D, D, 1)
-        kp, stride = _strided(k_pages, "k_pages", shape, inner, ps * Hkv * D)
-        vp, vstride = _strided(v_pages, "v_pages", shape, inner, ps * Hkv * D)
+        dev = torch.cuda.current_device()
+        kp, stride = _strided(k_pages, "k_pages", shape, inner, ps * Hkv * D, dev)
+        vp, vstride = _strided(v_pages, "v_pages", shape, inner, ps * Hkv * D, dev)
         if stride != vstride:
             raise ValueError("k_pages and v_pages must have the same page stride")
         rows, width = page_table.shape
         self.num_pages, self.page_size, self.Hq, self.Hkv, self.D = N, ps, Hq, Hkv, D
         self.k_pages, self.v_pages = k_pages, v_pages
         self.page_table, self.seq_len, self.refcount = page_table, seq_len, refcount
-        i32 = torch.int32
         d = b.CacheDesc(N, ps, Hq, Hkv, D, _LAYOUT[layout], softmax_scale, stride, kp, vp, rows, width,
-                        _ptr(page_table, "page_table", i32, (rows, width)),
-                        _ptr(seq_len, "seq_len", i32, (rows,)), _ptr(refcount, "refcount", i32, (N,)))
+                        _ptr(page_table, "page_table", _i32, (rows, width), dev),
+                        _ptr(seq_len, "seq_len", _i32, (rows,), dev),
+                        _ptr(refcount, "refcount", _i32, (N,), dev))
         h = ctypes.c_void_p()
         b._check(b._lib().ls_cache_create(ctypes.byref(d), ctypes.byref(h)), "ls_cache_create")
         self._h = h
+        self._pages_bytes = int(b._lib().ls_cache_pages_workspace_bytes(h))
 
     def close(self):
         if getattr(self, "_h", None) is not None and self._h.value is not None:
@@ -200,19 +227,19 @@ class PagedCache:
         except Exception:
             pass
 
-    def _list(self, t, name, n=None):
-        if not isinstance(t, torch.Tensor) or t.dim() != 1:
+    @staticmethod
+    def _list(t, name, dev, n=None):
+        if not isinstance(t, _Tensor) or t.dim() != 1:
             raise TypeError("%s must be a 1-D CUDA tensor" % name)
-        return _ptr(t, name, torch.int32, None if n is None else (n,))
+        return _ptr(t, name, _i32, None if n is None else (n,), dev)
 
-    def _pages_ws(self, workspace):
+    def _pages_ws(self, workspace, dev):
         if workspace is None:
-            workspace = torch.empty(self.pages_workspace_bytes(), dtype=torch.uint8,
-                                    device=self.refcount.device)
-        return workspace
+            workspace = torch.empty(self._pages_bytes, dtype=_u8, device=self.refcount.device)
+        return workspace, _ptr(workspace, "workspace", _u8, None, dev)
 
     def pages_workspace_bytes(self) -> int:
-        return int(b._lib().ls_cache_pages_workspace_bytes(self._h))
+        return self._pages_bytes
 
     def reset(self):
         """Every row empty, every page free."""
@@ -220,32 +247,35 @@ class PagedCache:
 
     def extend(self, rows, add, workspace=None):
         """Lengths of `rows` grow by `add` (int32), with free pages for the new tokens."""
-        ws = self._pages_ws(workspace)
-        b._check(b._lib().ls_cache_extend(
-            self._h, rows.numel(), self._list(rows, "rows"), self._list(add, "add", rows.numel()),
-            _ptr(ws, "workspace", torch.uint8), ws.numel(), b._stream()), "ls_cache_extend")
+        dev = torch.cuda.current_device()
+        ws, wp = self._pages_ws(workspace, dev)
+        n = rows.numel()
+        b._check(b._lib().ls_cache_extend(self._h, n, self._list(rows, "rows", dev), self._list(add, "add", dev, n),
+                                          wp, ws.numel(), _raw_stream(dev)), "ls_cache_extend")
 
     def fork(self, parents, children, workspace=None):
         """Empty rows `children` become copies of rows `parents`: whole pages are shared, a
         part-filled last page is copied."""
-        ws = self._pages_ws(workspace)
-        b._check(b._lib().ls_cache_fork(
-            self._h, parents.numel(), self._list(parents, "parents"),
-            self._list(children, "children", parents.numel()), _ptr(ws, "workspace", torch.uint8),
-            ws.numel(), b._stream()), "ls_cache_fork")
+        dev = torch.cuda.current_device()
+        ws, wp = self._pages_ws(workspace, dev)
+        n = parents.numel()
+        b._check(b._lib().ls_cache_fork(self._h, n, self._list(parents, "parents", dev),
+                                        self._list(children, "children", dev, n), wp, ws.numel(),
+                                        _raw_stream(dev)), "ls_cache_fork")
 
     def free(self, rows):
         """Empties `rows`; pages that no row lists any more become free."""
-        b._check(b._lib().ls_cache_free(self._h, rows.numel(), self._list(rows, "rows"), b._stream()),
+        dev = torch.cuda.current_device()
+        b._check(b._lib().ls_cache_free(self._h, rows.numel(), self._list(rows, "rows", dev), _raw_stream(dev)),
                  "ls_cache_free")
 
     def compact(self, into=None, n_live=None, workspace=None):
         """Moves the live pages together: in place, or into another PagedCache's pool."""
-        ws = self._pages_ws(workspace)
+        dev = torch.cuda.current_device()
+        ws, wp = self._pages_ws(workspace, dev)
         dst = self if into is None else into
-        b._check(b._lib().ls_cache_compact(
-            self._h, dst._h, _ptr(n_live, "n_live", torch.int32, (1,)),
-            _ptr(ws, "workspace", torch.uint8), ws.numel(), b._stream()), "ls_cache_compact")
+        b._check(b._lib().ls_cache_compact(self._h, dst._h, _opt(n_live, "n_live", _i32, (1,), dev), wp, ws.numel(),
+                                           _raw_stream(dev)), "ls_cache_compact")
 
     def append(self, k_new, v_new, cu_new, rows=None, q=None, q_out=None, inv_freq=None,
                interleaved: bool = False, attn_factor: float = 1.0):
@@ -256,21 +286,20 @@ class PagedCache:
             raise TypeError("k_new must be a 3-D CUDA tensor")
         T = k_new.shape[0]
         S = cu_new.numel() - 1
-        d = b.CacheAppendDesc(S=S, T=T, cu_new=self._list(cu_new, "cu_new"),
-                              rows=None if rows is None else self._list(rows, "rows", S),
-                              interleaved=int(interleaved), attn_factor=float(attn_factor))
-        d.k_new, d.k_stride = _heads(k_new, "k_new", T, self.Hkv, self.D)
-        d.v_new, d.v_stride = _heads(v_new, "v_new", T, self.Hkv, self.D)
+        dev = torch.cuda.current_device()
+        kp, ks = _heads(k_new, "k_new", T, self.Hkv, self.D, dev)
+        vp, vs = _heads(v_new, "v_new", T, self.Hkv, self.D, dev)
+        f = n = qp = qs = qo = qos = 0
         keep = None
         if inv_freq is not None:
-            d.inv_freq, n, keep = _host_doubles(inv_freq, "inv_freq")
-            d.rot_dim = 2 * n
+            f, n, keep = _host_doubles(inv_freq, "inv_freq")
         if q is not None:
-            d.q, d.q_stride = _heads(q, "q", T, self.Hq, self.D)
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
-            d.q_out, d.q_out_stride = _heads(q_out, "q_out", T, self.Hq, self.D)
-        b._check(b._lib().ls_cache_append(self._h, ctypes.byref(d), b._stream()), "ls_cache_append")
-        del keep
+            qp, qs = _heads(q, "q", T, self.Hq, self.D, dev)
+            q_out = torch.empty((T, self.Hq, self.D), dtype=_bf16, device=q.device) if q_out is None else q_out
+            qo, qos = _heads(q_out, "q_out", T, self.Hq, self.D, dev)
+        d = _APPEND.pack(S, T, 0 if rows is None else self._list(rows, "rows", dev, S), self._list(cu_new, "cu_new", dev),
+                         kp, ks, vp, vs, qp, qs, qo, qos, f, 2 * n, bool(interleaved), attn_factor)
+        b._check(b._lib().ls_cache_append(self._h, d, _raw_stream(dev)), "ls_cache_append")
         return (q_out if q is not None else None), None
 
     def attn_workspace_bytes(self, S: int, T: int, max_new: int, max_len: int) -> int:
@@ -285,19 +314,19 @@ class PagedCache:
             raise TypeError("q must be a 3-D CUDA tensor")
         T = q.shape[0]
         S = cu_new.numel() - 1
+        dev = torch.cuda.current_device()
         if o is None:
-            o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            o = torch.empty((T, self.Hq, self.D), dtype=_bf16, device=q.device)
         if lse is None:
-            lse = torch.empty((T, self.Hq), dtype=torch.float32, device=q.device)
+            lse = torch.empty((T, self.Hq), dtype=_f32, device=q.device)
         if workspace is None:
-            workspace = torch.empty(max(self.attn_workspace_bytes(S, T, max_new, max_len), 16),
-                                    dtype=torch.uint8, device=q.device)
-        qp, qs = _heads(q, "q", T, self.Hq, self.D)
-        d = b.CacheAttnDesc(
-            S, T, None if rows is None else self._list(rows, "rows", S), self._list(cu_new, "cu_new"),
-            max_new, max_len, qp, qs, _ptr(o, "o", torch.bfloat16, (T, self.Hq, self.D)),
-            _ptr(lse, "lse", torch.float32, (T, self.Hq)), group,
-            None if shared_len is None else self._list(shared_len, "shared_len", S // max(group, 1)))
-        b._check(b._lib().ls_cache_attn(self._h, ctypes.byref(d), _ptr(workspace, "workspace", torch.uint8),
-                                        workspace.numel(), b._stream()), "ls_cache_attn")
+            workspace = torch.empty(max(self.attn_workspace_bytes(S, T, max_new, max_len), 16), dtype=_u8,
+                                    device=q.device)
+        qp, qs = _heads(q, "q", T, self.Hq, self.D, dev)
+        d = _ATTN.pack(S, T, 0 if rows is None else self._list(rows, "rows", dev, S), self._list(cu_new, "cu_new", dev),
+                       max_new, max_len, qp, qs, _ptr(o, "o", _bf16, (T, self.Hq, self.D), dev),
+                       _ptr(lse, "lse", _f32, (T, self.Hq), dev), group,
+                       0 if shared_len is None else self._list(shared_len, "shared_len", dev, S // max(group, 1)))
+        b._check(b._lib().ls_cache_attn(self._h, d, _ptr(workspace, "workspace", _u8, None, dev), workspace.numel(),
+                                        _raw_stream(dev)), "ls_cache_attn")
         return o, lse

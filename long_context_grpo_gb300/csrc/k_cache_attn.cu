@@ -47,6 +47,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleLog2 = 8.0f;
 constexpr int kNarrowRows = 64;
+constexpr int kNarrowRounds = 6;       // rounds of narrow jobs at most
 constexpr int kMaxTiles = 1 << 24;     // 128-key tiles of the longest sequence
 
 // A run of packed tokens over a run of key tiles of one table row.
@@ -109,7 +110,6 @@ __device__ __forceinline__ int plan_scan(int v, int* sh, int* total) {
 }
 
 constexpr int kPlanThreads = 1024;
-constexpr int kMaxSegs = kMaxSeqs + kMaxSeqs / 2;
 
 struct PlanArgs {
   CacheView c;
@@ -128,8 +128,12 @@ struct PlanArgs {
 };
 
 __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const __grid_constant__ PlanArgs a) {
-  extern __shared__ int dyn[];
-  int* first = dyn;                       // jobs of each class before a segment: [2][kMaxSegs + 1]
+  // the segments, and the jobs of each class before a segment
+  extern __shared__ __align__(16) uint8_t dyn[];
+  const int cap = a.S + (a.group > 1 ? a.S / a.group : 0);
+  Seg* segs = reinterpret_cast<Seg*>(dyn);
+  int* first[2] = {reinterpret_cast<int*>(dyn + cap * sizeof(Seg)),
+                   reinterpret_cast<int*>(dyn + cap * sizeof(Seg)) + cap};
   __shared__ int sh[33];
   __shared__ int sh_max[2], sh_c[2], sh_grouped;
   __shared__ unsigned long long sh_w[2];
@@ -137,7 +141,6 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const __grid_c
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = a.c.Hq / a.c.Hkv;
   Info* info = reinterpret_cast<Info*>(a.ws + a.l.info);
-  Seg* segs = reinterpret_cast<Seg*>(a.ws + a.l.segs);
   int* lims = reinterpret_cast<int*>(a.ws + a.l.lims);
   pdl_launch_dependents();
 
@@ -152,10 +155,11 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const __grid_c
   for (int b = tid; b < a.S; b += kPlanThreads) {
     Seg s;
     const int c0 = a.cu[b], c1 = a.cu[b + 1];
+    const int row = a.rows != nullptr ? a.rows[b] : b;
     const bool run = c0 >= 0 && c1 >= c0 && c1 <= a.T;
     s.t0 = run ? c0 : 0;
     s.n_tok = run ? c1 - c0 : 0;
-    s.row = a.rows != nullptr ? a.rows[b] : b;
+    s.row = row;
     bool ok = run && (s.n_tok == 0 || (s.row >= 0 && s.row < a.c.num_rows && s.n_tok <= a.max_new));
     int64_t len = 0;
     if (run && s.n_tok == 0) {
@@ -247,7 +251,7 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const __grid_c
                                                  (static_cast<unsigned long long>(round) * k));
     if (C < (cls ? 8 : 2)) C = cls ? 8 : 2;
     if (C > longest) C = longest;
-    if (longest > 0) {
+    if (longest > 0 && (cls == 1 || k <= kNarrowRounds || k == 16)) {
       unsigned long long jobs = 0, rows = 0;
       for (int i = lane; i < n_segs; i += 32) {
         const Seg& s = segs[i];
@@ -300,7 +304,7 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const __grid_c
     for (int cls = 0; cls < 2; ++cls) {
       int total;
       const int at = plan_scan(w == cls ? jobs : 0, sh, &total);
-      if (i < n_segs) first[cls * (kMaxSegs + 1) + i] = base[cls] + at;
+      if (i < n_segs) first[cls][i] = base[cls] + at;
       base[cls] += total;
       const int pr = plan_scan(w == cls ? rows : 0, sh, &total);
       if (i < n_segs && w == cls && rows > 0) segs[i].part = static_cast<int>(part[cls] + pr);
@@ -314,11 +318,17 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const __grid_c
     info->grouped = grouped ? 1 : 0;
   }
 
+  // for the join
+  {
+    const int4* from = reinterpret_cast<const int4*>(segs);
+    int4* to = reinterpret_cast<int4*>(a.ws + a.l.segs);
+    for (int i = tid; i < n_segs * static_cast<int>(sizeof(Seg) / 16); i += kPlanThreads) to[i] = from[i];
+  }
   // the job lists
 #pragma unroll 1
   for (int cls = 0; cls < 2; ++cls) {
     Job* jobs = reinterpret_cast<Job*>(a.ws + (cls ? a.l.wide : a.l.narrow));
-    const int* f = first + cls * (kMaxSegs + 1);
+    const int* f = first[cls];
     for (int x = tid; x < base[cls]; x += kPlanThreads) {
       int lo = 0, hi = n_segs - 1;           // the last segment that starts at or before x
       while (lo < hi) {
@@ -440,7 +450,7 @@ __device__ __forceinline__ Streams load_streams(const AttnArgs& a, int item, int
   return s;
 }
 
-// The page indices of one stream, 32 ahead in the producer warp's lanes and the next 32 after them.
+// The page indices of one stream: 64 table entries ahead in the producer warp's lanes.
 struct PageWindow {
   const int32_t* row;
   int end;           // pages that hold keys
@@ -455,14 +465,16 @@ struct PageWindow {
     cur = fetch(base, lane);
     next = fetch(base + 32, lane);
   }
-  // page index i (warp-uniform, not decreasing), its table entry for all lanes
-  __device__ __forceinline__ int get(int i, int lane) {
+  // Table entry i + mine of every lane; i is warp-uniform and never falls, mine < 32.
+  __device__ __forceinline__ int get(int i, int mine, int lane) {
     if (i >= base + 32) {
       base += 32;
       cur = next;
       next = fetch(base + 32, lane);
     }
-    return __shfl_sync(0xffffffffu, cur, i - base);
+    const int at = i - base + mine;
+    const int x = __shfl_sync(0xffffffffu, cur, at & 31), y = __shfl_sync(0xffffffffu, next, at & 31);
+    return at < 32 ? x : y;
   }
 };
 
@@ -515,6 +527,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   volatile int* vabort = &abort_flag;
 
+  if (threadIdx.x == 0) {
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+    tma_prefetch_desc(&tm_q);
+  }
   pdl_launch_dependents();
   pdl_wait();                 // the job lists
   const int n_jobs = __ldcg(a.n_jobs);
@@ -527,25 +544,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int ps = 1 << a.c.ps_log2;
     const int boxes = ps < 128 ? 128 / ps : 1;
     const int box_tok = ps < 128 ? ps : 128;
-    // one 128-key tile of K or V, page by page
-    auto load_tile = [&](PageWindow& w, const Job& j, int tile, const CUtensorMap* tm, uint8_t* dst, uint64_t* bar) {
-      const int key0 = 128 * tile;
+    // One 128-key tile: a lane issues one box (64 columns of the tokens of one page); one
+    // lane after the other took 185 clocks a box and held 16-token pages to half the rate.
+    const int my_box = lane / C::kBoxes, my_half = lane % C::kBoxes;
+    auto load_tile = [&](int page, const Job& j, int tile, const CUtensorMap* tm, uint8_t* dst, uint64_t* bar) {
       if (lane == 0) mbar_arrive_expect_tx(bar, C::kTile);
       __syncwarp();
-      for (int p = 0; p < boxes; ++p) {
-        const int key = key0 + p * box_tok;
-        const int i = key >> a.c.ps_log2;
-        int page = w.get(i, lane);
-        if (page < 0 || page >= a.c.num_pages) {
-          if (lane == 0 && i < w.end) set_device_status(a.status, DEV_BAD_INDEX);
-          page = static_cast<int>(a.c.num_pages);      // outside the map: filled with zeros
-        }
-        if (lane < C::kBoxes) {
-          const int slot = key & (ps - 1);
-          tma_load_4d(dst + lane * 16384 + p * box_tok * 128, tm, bar, 64 * lane,
-                      a.layout == 0 ? j.kv : slot, a.layout == 0 ? slot : j.kv, page);
-        }
+      if (my_box < boxes) {
+        const int slot = (128 * tile + my_box * box_tok) & (ps - 1);
+        tma_load_4d(dst + my_half * 16384 + my_box * box_tok * 128, tm, bar, 64 * my_half,
+                    a.layout == 0 ? j.kv : slot, a.layout == 0 ? slot : j.kv, page);
       }
+      __syncwarp();
+    };
+    // The page of this lane's box of a tile; one past the pool (the map's fill: zeros) if it
+    // lies behind the sequence or the entry is none.
+    auto page_of = [&](PageWindow& w, int tile) {
+      const int i = (128 * tile) >> a.c.ps_log2;
+      const int page = w.get(i, my_box, lane);
+      if (page >= 0 && page < a.c.num_pages) return page;
+      if (my_box < boxes && i + my_box < w.end) set_device_status(a.status, DEV_BAD_INDEX);
+      return static_cast<int>(a.c.num_pages);
     };
     for (int it = blockIdx.x; it < n_items && ok; it += gridDim.x) {
       const Streams s = load_streams<kWide>(a, it, n_jobs, qt, g);
@@ -563,9 +582,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (kit >= static_cast<uint32_t>(C::kN))
             ok = __all_sync(0xffffffffu, mbar_wait(&bars[C::kBarKEmpty + ks], ((kit / C::kN) - 1) & 1u, a.status, vabort));
           if (!ok) break;
-          // the window is read twice for a tile (K, then V): keep the state of the first read
-          PageWindow at = w[q];
-          load_tile(at, s.j[q], s.j[q].tile0 + j, &tm_k, smem + C::kOffK + ks * C::kTile, &bars[C::kBarKFull + ks]);
+          const int page = page_of(w[q], s.j[q].tile0 + j);
+          load_tile(page, s.j[q], s.j[q].tile0 + j, &tm_k, smem + C::kOffK + ks * C::kTile, &bars[C::kBarKFull + ks]);
           ++kit;
           if (!q_sent) {
             // Q goes behind the first K tile: its buffer is free once the last item's scores are done
@@ -587,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (vit >= static_cast<uint32_t>(C::kN))
             ok = __all_sync(0xffffffffu, mbar_wait(&bars[C::kBarVEmpty + vs], ((vit / C::kN) - 1) & 1u, a.status, vabort));
           if (!ok) break;
-          load_tile(w[q], s.j[q], s.j[q].tile0 + j, &tm_v, smem + C::kOffV + vs * C::kTile, &bars[C::kBarVFull + vs]);
+          load_tile(page, s.j[q], s.j[q].tile0 + j, &tm_v, smem + C::kOffV + vs * C::kTile, &bars[C::kBarVFull + vs]);
           ++vit;
         }
       }
@@ -896,10 +914,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // --------------------------------------------------------------------------------------
-constexpr int kJoinThreads = 128;
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 
 struct JoinArgs {
-  int S, group, Hq, Hkv, heads;      // heads: query heads of a block (one key head's)
+  int S, group, Hq, Hkv;
+  int64_t T;
   const int32_t* cu;
   const Info* info;
   const Seg* segs;
@@ -909,29 +928,39 @@ struct JoinArgs {
   float* lse;
 };
 
-template <int D>
+// kPer warps join one (token, head) row: 1 with many rows, all of the block's with few rows of many
+// parts.  32 parts at a time: a lane loads one part's log-sum-exp, the warp sets the weights,
+// then the parts' rows are added, their loads independent of one another.
+template <int D, int kPer>
 __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_constant__ JoinArgs a) {
-  constexpr int kPer = D / 32, kWarps = kJoinThreads / 32;
-  __shared__ float sm[kWarps], sl[kWarps];
-  __shared__ float so[kWarps][D];
+  constexpr int kV = D / 32;          // values of a lane
+  __shared__ float sm[kJoinWarps], sl[kJoinWarps];
+  __shared__ float so[kPer > 1 ? kJoinWarps : 1][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int t = blockIdx.x;
   const int g = a.Hq / a.Hkv;
+  const int64_t out = (static_cast<int64_t>(blockIdx.x) * kJoinWarps + warp) / kPer;
   pdl_wait();
-  int b = 0;
-  for (int i0 = 0; i0 < a.S; i0 += kJoinThreads) {
-    const int i = i0 + threadIdx.x;
-    b += __syncthreads_count(i < a.S && a.cu[i + 1] <= t);
+  const int t = static_cast<int>(out / a.Hq), h = static_cast<int>(out - static_cast<int64_t>(t) * a.Hq);
+  if (t >= a.T) return;               // (with kPer > 1 for the whole block)
+  // the entry of token t: the last one that starts at or before it and is not empty
+  int lo = 0, hi = a.S;               // entries [0, lo) end at or before t, [hi, S) do not
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (a.cu[mid + 1] <= t) lo = mid + 1; else hi = mid;
   }
+  const int b = lo;
   if (b >= a.S || t < a.cu[b]) return;
-  // the token's part lists: its own segment, and its group's
-  const Seg* seg[2] = {a.segs + b, a.info->grouped ? a.segs + a.S + b / a.group : nullptr};
-  int n[2] = {0, 0}, base[2], step[2];
+  // the row's part lists: its own segment's, and its group's
+  const int grouped = a.info->grouped;
+  const int kv = h / g, hh = h - kv * g;
+  int n[2] = {0, 0};
+  int64_t first[2] = {0, 0}, step[2] = {0, 0};
   bool direct = false;
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    if (seg[k] == nullptr || seg[k]->tiles == 0) continue;
-    const Seg& s = *seg[k];
+    if (k == 1 && !grouped) continue;
+    const Seg s = a.segs[k == 0 ? b : a.S + b / a.group];
+    if (s.tiles == 0) continue;
     int tiles = s.tiles;
     if (is_wide(s, g)) {      // the keys of the token's pair of Q tiles
       const int per = 2 * qt_of(g, true);
@@ -940,58 +969,76 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
       tiles = tiles_of(s, end);
     }
     n[k] = (tiles + s.chunk - 1) / s.chunk;
-    base[k] = s.part + (t - s.t0) * g;
-    step[k] = s.n_tok * g;
+    step[k] = static_cast<int64_t>(s.n_tok) * g;
+    first[k] = s.part + static_cast<int64_t>(kv) * s.chunks * step[k] + static_cast<int64_t>(t - s.t0) * g + hh;
     if (s.part < 0) direct = n[k] > 0;
   }
   if (direct) return;
   const int total = n[0] + n[1];
-  for (int h = blockIdx.y * a.heads; h < (static_cast<int>(blockIdx.y) + 1) * a.heads; ++h) {
-    const int kv = h / g, hh = h - kv * g;
-    float m = -INFINITY, l = 0.0f, acc[kPer];
+  float m = -INFINITY, l = 0.0f, acc[kV];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) acc[i] = 0.0f;
-    for (int p = warp; p < total; p += kWarps) {
-      const int k = p < n[0] ? 0 : 1, c = p - (k ? n[0] : 0);
-      const int chunks = k ? seg[1]->chunks : seg[0]->chunks;
-      const int64_t row = static_cast<int64_t>(k ? base[1] : base[0]) +
-                          static_cast<int64_t>(kv * chunks + c) * (k ? step[1] : step[0]) + hh;
-      const float x = __ldcg(a.part_lse + row);
-      float v[kPer];
+  for (int i = 0; i < kV; ++i) acc[i] = 0.0f;
+  for (int p0 = (warp % kPer) * 32; p0 < total; p0 += 32 * kPer) {
+    const int p = p0 + lane;
+    const int64_t row = p < n[0] ? first[0] + p * step[0] : first[1] + (p - n[0]) * step[1];
+    const float x = p < total ? __ldcg(a.part_lse + row) : -INFINITY;
+    float mx = x;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) v[i] = __ldcg(a.part_o + row * D + lane + 32 * i);
-      if (x == -INFINITY) continue;
-      const float mn = fmaxf(m, x);
-      const float f = ex2_approx(m - mn), e = ex2_approx(x - mn);
-      m = mn;
-      l = l * f + e;
+    for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+    if (mx == -INFINITY) continue;
+    const float mn = fmaxf(m, mx);
+    const float f = ex2_approx(m - mn);
+    const float w = ex2_approx(x - mn);
+    float ws = w;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) acc[i] = acc[i] * f + e * v[i];
+    for (int off = 16; off > 0; off >>= 1) ws += __shfl_xor_sync(0xffffffffu, ws, off);
+    m = mn;
+    l = l * f + ws;
+#pragma unroll
+    for (int i = 0; i < kV; ++i) acc[i] *= f;
+    const int cnt = total - p0 < 32 ? total - p0 : 32;
+#pragma unroll 4
+    for (int k = 0; k < cnt; ++k) {
+      const float wk = __shfl_sync(0xffffffffu, w, k);
+      const float* src = a.part_o + __shfl_sync(0xffffffffu, row, k) * D + lane * kV;
+      if constexpr (kV == 4) {
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
+        acc[0] = fmaf(wk, v.x, acc[0]);
+        acc[1] = fmaf(wk, v.y, acc[1]);
+        acc[2] = fmaf(wk, v.z, acc[2]);
+        acc[3] = fmaf(wk, v.w, acc[3]);
+      } else {
+        const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
+        acc[0] = fmaf(wk, v.x, acc[0]);
+        acc[1] = fmaf(wk, v.y, acc[1]);
+      }
     }
+  }
+  if constexpr (kPer > 1) {
     if (lane == 0) { sm[warp] = m; sl[warp] = l; }
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) so[warp][lane + 32 * i] = acc[i];
+    for (int i = 0; i < kV; ++i) so[warp][lane * kV + i] = acc[i];
     __syncthreads();
-    float M = sm[0];
+    if (warp > 0) return;
+    m = sm[0];
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) M = fmaxf(M, sm[w]);
-    float L = 0.0f, f[kWarps];
+    for (int w = 1; w < kPer; ++w) m = fmaxf(m, sm[w]);
+    l = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      f[w] = sm[w] == -INFINITY ? 0.0f : ex2_approx(sm[w] - M);
-      L += f[w] * sl[w];
+    for (int i = 0; i < kV; ++i) acc[i] = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kPer; ++w) {
+      const float f = sm[w] == -INFINITY ? 0.0f : ex2_approx(sm[w] - m);
+      l += f * sl[w];
+#pragma unroll
+      for (int i = 0; i < kV; ++i) acc[i] = fmaf(f, so[w][lane * kV + i], acc[i]);
     }
-    const float inv = L > 0.0f ? 1.0f / L : 0.0f;
-    const int64_t out = static_cast<int64_t>(t) * a.Hq + h;
-    for (int i = threadIdx.x; i < D; i += kJoinThreads) {
-      float x = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) x += f[w] * so[w][i];
-      a.o[out * D + i] = static_cast<uint16_t>(pack_bf16x2(x * inv, 0.0f) & 0xFFFFu);
-    }
-    if (threadIdx.x == 0) a.lse[out] = L > 0.0f ? (M + __log2f(L)) * kLn2 : -INFINITY;
-    __syncthreads();
   }
+  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(a.o + out * D) + lane * (kV / 2);
+#pragma unroll
+  for (int i = 0; i < kV / 2; ++i) dst[i] = pack_bf16x2(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+  if (lane == 0) a.lse[out] = l > 0.0f ? (m + __log2f(l)) * kLn2 : -INFINITY;
 }
 
 // Launch with programmatic serialisation: the kernel may start while the one before it ends.
@@ -1026,7 +1073,7 @@ cudaError_t launch_attn(const CacheAttnArgs& a, const AttnArgs& p, cudaStream_t 
                       C::kSmem, s, *a.tm_k, *a.tm_v, kWide ? a.tm_q : a.tm_qn, p);
 }
 
-constexpr size_t kPlanSmem = 2 * (kMaxSegs + 1) * sizeof(int);
+constexpr int kPlanSeg = sizeof(Seg) + 2 * sizeof(int);   // shared memory of a segment
 
 }  // namespace
 
@@ -1077,7 +1124,17 @@ cudaError_t launch_cache_attn(const CacheAttnArgs& a, cudaStream_t s) {
   p.l = cache_attn_layout(a.c, a.S, a.T, a.max_new);
   p.sms = num_sms();
   p.status = a.status;
-  cache_plan_kernel<<<1, kPlanThreads, kPlanSmem, s>>>(p);
+  static bool attr_set[kMaxDeviceCache] = {};
+  const int dev = cached_device_index();
+  if (dev < 0) return cudaErrorInvalidDevice;
+  if (!attr_set[dev]) {
+    cudaError_t e = cudaFuncSetAttribute(cache_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (kMaxSeqs + kMaxSeqs / 2) * kPlanSeg);
+    if (e != cudaSuccess) return e;
+    attr_set[dev] = true;
+  }
+  const int segs = a.S + (a.group > 1 ? a.S / a.group : 0);
+  cache_plan_kernel<<<1, kPlanThreads, static_cast<size_t>(segs) * kPlanSeg, s>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
 
@@ -1115,11 +1172,17 @@ cudaError_t launch_cache_attn(const CacheAttnArgs& a, cudaStream_t s) {
   j.part_lse = k.part_lse;
   j.o = a.o;
   j.lse = a.lse;
-  // a block a head while that is a moderate grid, else a block a key head
-  j.heads = a.T * a.c.Hq <= 16384 ? 1 : g;
-  const dim3 grid(static_cast<unsigned>(a.T), static_cast<unsigned>(a.c.Hq / j.heads));
-  return a.c.D == 128 ? launch_after(cache_join_kernel<128>, grid, kJoinThreads, 0, s, j)
-                      : launch_after(cache_join_kernel<64>, grid, kJoinThreads, 0, s, j);
+  // few rows have many parts each: a block a row; else a warp a row
+  j.T = a.T;
+  const int64_t rows = a.T * a.c.Hq;
+  if (rows <= 8 * num_sms()) {
+    const dim3 grid(static_cast<unsigned>(rows));
+    return a.c.D == 128 ? launch_after(cache_join_kernel<128, kJoinWarps>, grid, kJoinThreads, 0, s, j)
+                        : launch_after(cache_join_kernel<64, kJoinWarps>, grid, kJoinThreads, 0, s, j);
+  }
+  const dim3 grid(static_cast<unsigned>((rows + kJoinWarps - 1) / kJoinWarps));
+  return a.c.D == 128 ? launch_after(cache_join_kernel<128, 1>, grid, kJoinThreads, 0, s, j)
+                      : launch_after(cache_join_kernel<64, 1>, grid, kJoinThreads, 0, s, j);
 }
 
 }  // namespace ls

@@ -21,6 +21,8 @@
 //     through shared memory once more and is shifted there.
 // policy_rows: one CTA a row from global memory, for vocabularies beyond eight slices (460,000).
 // policy_reduce: the fp64 sum of the tokens' terms in a fixed order, rounded once.
+#include <atomic>
+
 #include "ls_internal.h"
 #include "ls_ops.h"
 #include "ptx.cuh"
@@ -653,8 +655,14 @@ cudaError_t launch_cluster(const PolicyArgs& a, int cl, int per, cudaStream_t s)
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = cl > 1 ? 1 : 0;
+  // how many fit the GPU, asked once for a shape of launch
+  static std::atomic<uint64_t> memo[kMaxDeviceCache];
+  const uint64_t key = (static_cast<uint64_t>(cl) << 48) | (static_cast<uint64_t>(per) << 24);
+  const uint64_t seen = memo[dev].load();
   int n = 0;
-  if (cl > 1) {
+  if ((seen & ~0xFFFFFFull) == key) {
+    n = static_cast<int>(seen & 0xFFFFFF);
+  } else if (cl > 1) {
     cfg.gridDim = dim3(static_cast<unsigned>(num_sms() * cl), 1, 1);
     if (cudaOccupancyMaxActiveClusters(&n, policy_cluster<kStream>, &cfg) != cudaSuccess || n <= 0) {
       (void)cudaGetLastError();
@@ -668,6 +676,7 @@ cudaError_t launch_cluster(const PolicyArgs& a, int cl, int per, cudaStream_t s)
     }
     n *= num_sms();
   }
+  memo[dev].store(key | static_cast<uint64_t>(n));
   if (n > a.T) n = static_cast<int>(a.T);
   cfg.gridDim = dim3(static_cast<unsigned>(n * cl), 1, 1);
   return cudaLaunchKernelEx(&cfg, policy_cluster<kStream>, a, cl, per);
