@@ -33,7 +33,6 @@
 // outside the pool read as zeros (the TMA's fill).  P is rounded to bf16 for the tensor cores, the
 // sum is taken before that rounding.  Every wait is bounded as in the replay kernels.
 #include <climits>
-#include <utility>
 
 #include "ls_internal.h"
 #include "ls_ops.h"
@@ -1039,22 +1038,6 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
 #pragma unroll
   for (int i = 0; i < kV / 2; ++i) dst[i] = pack_bf16x2(acc[2 * i] * inv, acc[2 * i + 1] * inv);
   if (lane == 0) a.lse[out] = l > 0.0f ? (m + __log2f(l)) * kLn2 : -INFINITY;
-}
-
-// Launch with programmatic serialisation: the kernel may start while the one before it ends.
-template <class... P, class... A>
-cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A&&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(static_cast<unsigned>(threads));
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
 }
 
 template <int D, bool kWide>

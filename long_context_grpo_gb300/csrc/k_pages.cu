@@ -1,10 +1,10 @@
 // Page management of the cache: extend, fork, free, compact, reset.
 //
 // Free pages are those with count 0.  Allocation takes the lowest ones in list order, so the
-// result is a function of the arrays alone: a scan of the counts writes the free (or live)
-// pages' indices in ascending order, one block decides on every entry of the list (sizes,
-// ranks among the free pages, refusals), and the entries' table rows, counts and page copies
-// run on the whole grid.  Counts change by integer atomics, whose order cannot change them.
+// result is a function of the arrays alone: one block decides on every entry of the list (sizes,
+// ranks among the free pages, refusals) and scans the counts for as many free pages as that
+// takes; then the entries' table rows, counts and page copies run on the whole grid.  Counts
+// change by integer atomics, whose order cannot change them.
 #include "ls_internal.h"
 #include "ls_ops.h"
 #include "ptx.cuh"
@@ -17,7 +17,7 @@ constexpr int kCopyThreads = 256;
 
 // Workspace: a header, the list's plan, one int32 a page.
 struct Plan {
-  int32_t n_free;                     // free pages found (or live pages, compact)
+  int32_t n_moves;                    // compact
   int32_t pad[63];
   int32_t row[kMaxList];              // table row the entry writes; -1: left out
   int32_t from[kMaxList];             // fork: parent row
@@ -55,25 +55,36 @@ __device__ __forceinline__ int block_scan(int v, int* sh /* [33] */, int* total)
   return (warp > 0 ? sh[warp - 1] : 0) + s - v;
 }
 
-// list[] = the pages whose count is 0 (want_free) in ascending order, *n their number.
-__global__ void __launch_bounds__(kScanThreads) free_list_kernel(const int32_t* ref, int64_t pages,
-                                                                int32_t* list, int32_t* n) {
-  __shared__ int sh[33];
+constexpr int kScanPer = 8;          // pages of a thread in one step of a scan
+
+// list[] = the lowest pages whose count is 0, in ascending order, at least `want` of them if there
+// are as many (the scan stops there); returns how many are listed.  Whole block.
+__device__ int scan_free(const int32_t* ref, int64_t pages, int want, int32_t* list, int* sh) {
   int base = 0;
-  for (int64_t p0 = 0; p0 < pages; p0 += kScanThreads) {
-    const int64_t p = p0 + threadIdx.x;
-    const int is = (p < pages && ref[p] == 0) ? 1 : 0;
+  for (int64_t p0 = 0; p0 < pages && base < want; p0 += kScanThreads * kScanPer) {
+    const int64_t p = p0 + threadIdx.x * kScanPer;
+    uint32_t bits = 0;
+    int r[kScanPer];
+#pragma unroll
+    for (int k = 0; k < kScanPer; ++k) r[k] = p + k < pages ? __ldcg(ref + p + k) : 1;
+#pragma unroll
+    for (int k = 0; k < kScanPer; ++k) bits |= r[k] == 0 ? 1u << k : 0u;
     int total;
-    const int at = base + block_scan(is, sh, &total);
-    if (is) list[at] = static_cast<int32_t>(p);
+    int at = base + block_scan(__popc(bits), sh, &total);
+#pragma unroll
+    for (int k = 0; k < kScanPer; ++k)
+      if (bits & (1u << k)) list[at++] = static_cast<int32_t>(p + k);
     base += total;
   }
-  if (threadIdx.x == 0) *n = base;
+  __syncthreads();
+  return base;
 }
 
+// Whether list[i] stands before position i too (the list in shared memory).
 __device__ __forceinline__ bool listed_before(const int32_t* list, int i) {
+  const int x = list[i];
   for (int j = 0; j < i; ++j)
-    if (list[j] == list[i]) return true;
+    if (list[j] == x) return true;
   return false;
 }
 
@@ -84,17 +95,23 @@ __device__ __forceinline__ bool good_len(const CacheView& c, int64_t len) {
 __global__ void __launch_bounds__(kMaxList) extend_plan_kernel(CacheView c, int n,
                                                               const int32_t* rows,
                                                               const int32_t* add, Plan* plan,
-                                                              uint32_t* status) {
+                                                              int32_t* list, uint32_t* status) {
   __shared__ int sh[33];
+  __shared__ int32_t listed[kMaxList];
   const int i = threadIdx.x;
+  pdl_launch_dependents();
   bool ok = false;
-  int row = -1, need = 0, first = 0;
+  int row = -1, more = 0, need = 0, first = 0;
   int64_t len = 0, grown = 0;
   if (i < n) {
-    row = rows[i];
-    if (row >= 0 && row < c.num_rows && add[i] >= 0 && !listed_before(rows, i)) {
-      len = c.len[row];
-      grown = len + add[i];
+    listed[i] = row = rows[i];
+    more = add[i];
+    if (row >= 0 && row < c.num_rows) len = c.len[row];
+  }
+  __syncthreads();
+  if (i < n) {
+    if (row >= 0 && row < c.num_rows && more >= 0 && !listed_before(listed, i)) {
+      grown = len + more;
       if (good_len(c, len) && good_len(c, grown)) {
         ok = true;
         const int64_t ps1 = (1 << c.ps_log2) - 1;
@@ -106,8 +123,9 @@ __global__ void __launch_bounds__(kMaxList) extend_plan_kernel(CacheView c, int 
   }
   int total;
   const int rank = block_scan(ok ? need : 0, sh, &total);
+  const int n_free = scan_free(c.ref, c.num_pages, total, list, sh);
   if (i >= n) return;
-  if (ok && rank + need > plan->n_free) {
+  if (ok && rank + need > n_free) {
     set_device_status(status, DEV_NO_PAGES);
     ok = false;
   }
@@ -121,6 +139,7 @@ __global__ void __launch_bounds__(kMaxList) extend_plan_kernel(CacheView c, int 
 __global__ void __launch_bounds__(kCopyThreads) extend_kernel(CacheView c, const Plan* plan,
                                                              const int32_t* list) {
   const int i = blockIdx.x;
+  pdl_wait();
   const int row = plan->row[i];
   if (row < 0) return;
   const int first = plan->first[i], count = plan->count[i], rank = plan->rank[i];
@@ -134,21 +153,26 @@ __global__ void __launch_bounds__(kCopyThreads) extend_kernel(CacheView c, const
 __global__ void __launch_bounds__(kMaxList) fork_plan_kernel(CacheView c, int n,
                                                             const int32_t* parents,
                                                             const int32_t* children, Plan* plan,
-                                                            uint32_t* status) {
+                                                            int32_t* list, uint32_t* status) {
   __shared__ int sh[33];
+  __shared__ int32_t listed[kMaxList];
   const int i = threadIdx.x;
+  pdl_launch_dependents();
   bool ok = false;
   int child = -1, parent = -1;
   int64_t len = 0;
   if (i < n) {
-    child = children[i];
+    listed[i] = child = children[i];
     parent = parents[i];
-    ok = child >= 0 && child < c.num_rows && parent >= 0 && parent < c.num_rows &&
-         !listed_before(children, i);
+    ok = child >= 0 && child < c.num_rows && parent >= 0 && parent < c.num_rows;
     if (ok) {
       len = c.len[parent];
       ok = c.len[child] == 0 && good_len(c, len) && child != parent;
     }
+  }
+  __syncthreads();
+  if (i < n) {
+    ok = ok && !listed_before(listed, i);
     if (!ok) set_device_status(status, DEV_BAD_INDEX);
   }
   const int full = static_cast<int>(len >> c.ps_log2);
@@ -156,8 +180,9 @@ __global__ void __launch_bounds__(kMaxList) fork_plan_kernel(CacheView c, int n,
   int total;
   // every length above is read before the first one is written below
   const int rank = block_scan(ok && part > 0 ? 1 : 0, sh, &total);
+  const int n_free = scan_free(c.ref, c.num_pages, total, list, sh);
   if (i >= n) return;
-  if (ok && part > 0 && rank >= plan->n_free) {
+  if (ok && part > 0 && rank >= n_free) {
     set_device_status(status, DEV_NO_PAGES);
     ok = false;
   }
@@ -169,52 +194,71 @@ __global__ void __launch_bounds__(kMaxList) fork_plan_kernel(CacheView c, int n,
   if (ok) c.len[child] = static_cast<int32_t>(len);
 }
 
-// The first `tokens` tokens of a page's keys and values, page src to page dst (16-byte units).
-__device__ __forceinline__ void copy_page(const CacheView& sc, const CacheView& dc, int64_t src,
-                                          int64_t dst, int tokens) {
-  const int d8 = sc.D / 8;
-  const int units = tokens * sc.Hkv * d8;
-  const uint4* sk = reinterpret_cast<const uint4*>(sc.k + src * sc.page_stride);
-  const uint4* sv = reinterpret_cast<const uint4*>(sc.v + src * sc.page_stride);
-  uint4* dk = reinterpret_cast<uint4*>(dc.k + dst * dc.page_stride);
-  uint4* dv = reinterpret_cast<uint4*>(dc.v + dst * dc.page_stride);
+// The first `tokens` tokens of a page's keys and values, page src to page dst, in 16-byte units,
+// four of each in flight a thread; this block's share of them is number y of ny.
+__device__ __forceinline__ void copy_tokens(const CacheView& c, int64_t src, int64_t dst, int tokens, int y,
+                                            int ny) {
+  const int d8 = c.D / 8;
+  const int units = tokens * c.Hkv * d8;
+  const uint4* sk = reinterpret_cast<const uint4*>(c.k + src * c.page_stride);
+  const uint4* sv = reinterpret_cast<const uint4*>(c.v + src * c.page_stride);
+  uint4* dk = reinterpret_cast<uint4*>(c.k + dst * c.page_stride);
+  uint4* dv = reinterpret_cast<uint4*>(c.v + dst * c.page_stride);
   const int per_head = tokens * d8;
-  for (int u = threadIdx.x; u < units; u += blockDim.x) {
-    int64_t at = u;
-    if (sc.head_stride > sc.tok_stride) {     // [Hkv, page_size, D]: a run a head
-      const int h = u / per_head;
-      at = h * (sc.head_stride / 8) + (u - h * per_head);
+  const bool runs = c.head_stride > c.tok_stride;     // [Hkv, page_size, D]: a run a head
+  const int step = ny * kCopyThreads;
+  for (int u0 = y * kCopyThreads + threadIdx.x; u0 < units; u0 += 4 * step) {
+    uint4 k[4], v[4];
+    int64_t at[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int u = u0 + x * step;
+      at[x] = u;
+      if (runs) {
+        const int h = u / per_head;
+        at[x] = h * (c.head_stride / 8) + (u - h * per_head);
+      }
+      if (u < units) {
+        k[x] = __ldcs(sk + at[x]);
+        v[x] = __ldcs(sv + at[x]);
+      }
     }
-    dk[at] = sk[at];
-    dv[at] = sv[at];
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      if (u0 + x * step < units) {
+        dk[at[x]] = k[x];
+        dv[at[x]] = v[x];
+      }
   }
 }
 
+// Blocks (pair, y): the pair's table columns and page units are shared out over gridDim.y.
 __global__ void __launch_bounds__(kCopyThreads) fork_kernel(CacheView c, const Plan* plan,
                                                            const int32_t* list, uint32_t* status) {
-  const int i = blockIdx.x;
+  const int i = blockIdx.x, y = blockIdx.y, ny = gridDim.y;
+  pdl_wait();
   const int row = plan->row[i];
   if (row < 0) return;
   const int32_t* src = c.table + static_cast<int64_t>(plan->from[i]) * c.width;
   int32_t* dst = c.table + static_cast<int64_t>(row) * c.width;
   const int full = plan->first[i], part = plan->count[i];
-  for (int j = threadIdx.x; j < full; j += kCopyThreads) {
-    const int page = src[j];
-    dst[j] = page;
-    if (page >= 0 && page < c.num_pages)
-      atomicAdd(c.ref + page, 1);
+  const int page = part > 0 ? list[plan->rank[i]] : -1, from = part > 0 ? src[full] : -1;
+  for (int j = y * kCopyThreads + threadIdx.x; j < full; j += ny * kCopyThreads) {
+    const int p = src[j];
+    dst[j] = p;
+    if (p >= 0 && p < c.num_pages)
+      atomicAdd(c.ref + p, 1);
     else
       set_device_status(status, DEV_BAD_INDEX);
   }
   if (part > 0) {
-    const int page = list[plan->rank[i]], from = src[full];
-    if (threadIdx.x == 0) {
+    if (y == 0 && threadIdx.x == 0) {
       dst[full] = page;
       c.ref[page] = 1;
     }
     if (from >= 0 && from < c.num_pages)
-      copy_page(c, c, from, page, part);
-    else if (threadIdx.x == 0)
+      copy_tokens(c, from, page, part, y, ny);
+    else if (y == 0 && threadIdx.x == 0)
       set_device_status(status, DEV_BAD_INDEX);
   }
 }
@@ -249,92 +293,174 @@ __global__ void __launch_bounds__(kCopyThreads) free_kernel(CacheView c, int n, 
   if (threadIdx.x == 0) c.len[row] = 0;
 }
 
-// to[p] = the page that p moves to (-1: not live); *n_live the number of live pages.
-// Out of place: its rank among the live pages.  In place: p itself below n_live, else the hole
-// of p's rank among the live pages from n_live on.
+// The compaction's workspace behind the plan, int32 [pages] each: to[p], the page that p moves to
+// (-1: not live), and from[m], the source of move m.  Out of place every live page moves, to its
+// rank among them (move m is to page m).  In place the live pages from n_live on move
+// into the holes below, both in ascending order; hole[m], a third list, is move m's target.
+struct Moves {
+  int32_t *to, *from, *hole;
+};
+__host__ __device__ inline Moves moves_of(void* ws, int64_t pages) {
+  int32_t* l = page_list(ws);
+  return {l, l + pages, l + 2 * pages};
+}
+
 __global__ void __launch_bounds__(kScanThreads) compact_plan_kernel(const int32_t* ref, int64_t pages,
-                                                                   int inplace, int32_t* to,
-                                                                   int32_t* n_ws, int32_t* n_live) {
+                                                                   int inplace, Moves mv, Plan* plan,
+                                                                   int32_t* n_live) {
   __shared__ int sh[33];
-  int base = 0;
-  for (int64_t p0 = 0; p0 < pages; p0 += kScanThreads) {
-    const int64_t p = p0 + threadIdx.x;
-    const int is = (p < pages && ref[p] > 0) ? 1 : 0;
+  pdl_launch_dependents();
+  // ranks among the live pages
+  int live = 0;
+  for (int64_t p0 = 0; p0 < pages; p0 += kScanThreads * kScanPer) {
+    const int64_t p = p0 + threadIdx.x * kScanPer;
+    uint32_t bits = 0;
+    int r[kScanPer];
+#pragma unroll
+    for (int k = 0; k < kScanPer; ++k) r[k] = p + k < pages ? __ldcg(ref + p + k) : 0;
+#pragma unroll
+    for (int k = 0; k < kScanPer; ++k) bits |= r[k] > 0 ? 1u << k : 0u;
     int total;
-    const int at = base + block_scan(is, sh, &total);
-    if (p < pages) to[p] = is ? at : -1;
-    base += total;
+    int at = live + block_scan(__popc(bits), sh, &total);
+#pragma unroll
+    for (int k = 0; k < kScanPer; ++k)
+      if (p + k < pages) {
+        const bool is = bits & (1u << k);
+        mv.to[p + k] = is ? at : -1;
+        if (is) mv.from[at++] = static_cast<int32_t>(p + k);
+      }
+    live += total;
   }
-  const int live = base;
   if (threadIdx.x == 0) {
-    *n_ws = live;
     if (n_live != nullptr) *n_live = live;
+    if (!inplace) plan->n_moves = live;
   }
   if (!inplace) return;
   __syncthreads();
-  // A live page q >= live of rank r is mover number r - (live pages below `live`).  The hole
-  // of number m is the m-th page below `live` that is not live; walk both in order, holes
-  // kept as to[hole] = -2 - m until the movers have looked them up.
+  // pages below n_live that are not live: the holes; the live ones there stay
   int holes = 0;
   for (int64_t p0 = 0; p0 < live; p0 += kScanThreads) {
     const int64_t p = p0 + threadIdx.x;
-    const int is = (p < live && to[p] < 0) ? 1 : 0;
+    const int is = (p < live && mv.to[p] < 0) ? 1 : 0;
     int total;
     const int at = holes + block_scan(is, sh, &total);
-    // hole number `at` is kept in the entry of free slot `at` behind the table
-    if (is) to[pages + at] = static_cast<int32_t>(p);
+    if (is) mv.hole[at] = static_cast<int32_t>(p);
     holes += total;
-    if (p < live && !is) to[p] = static_cast<int32_t>(p);
   }
   __syncthreads();
-  const int stay = live - holes;          // live pages below `live`
-  for (int64_t p = live + threadIdx.x; p < pages; p += kScanThreads)
-    if (to[p] >= 0) to[p] = to[pages + (to[p] - stay)];
-}
-
-// A block a source page (grid-stride): its keys and values and its count.
-__global__ void __launch_bounds__(kCopyThreads) compact_copy_kernel(CacheView sc, CacheView dc,
-                                                                   int inplace, const int32_t* to,
-                                                                   const int32_t* n_ws,
-                                                                   uint32_t* status) {
-  const int n = *n_ws;
-  for (int64_t p = blockIdx.x; p < sc.num_pages; p += gridDim.x) {
-    const int d = to[p];
-    if (d < 0 || (inplace && d == p)) continue;
-    if (d >= dc.num_pages) {
-      if (threadIdx.x == 0) set_device_status(status, DEV_NO_PAGES);
-      continue;
-    }
-    copy_page(sc, dc, p, d, 1 << sc.ps_log2);
-    if (threadIdx.x == 0) {
-      dc.ref[d] = sc.ref[p];
-      if (inplace) sc.ref[p] = 0;
-    }
+  const int stay = live - holes;          // live pages below n_live: moves are from[stay ...]
+  for (int64_t p = threadIdx.x; p < pages; p += kScanThreads) {
+    const int rank = mv.to[p];
+    if (rank >= 0) mv.to[p] = rank < stay ? static_cast<int32_t>(p) : mv.hole[rank - stay];
   }
-  if (!inplace)
-    for (int64_t p = n + blockIdx.x * static_cast<int64_t>(kCopyThreads) + threadIdx.x; p < dc.num_pages;
-         p += static_cast<int64_t>(gridDim.x) * kCopyThreads)
-      dc.ref[p] = 0;
+  __syncthreads();
+  // the movers to the front, in their order
+  for (int m0 = 0; m0 < holes; m0 += kScanThreads) {
+    const int m = m0 + threadIdx.x;
+    const int f = m < holes ? mv.from[stay + m] : 0;
+    __syncthreads();
+    if (m < holes) mv.from[m] = f;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) plan->n_moves = holes;
 }
 
-__global__ void __launch_bounds__(kCopyThreads) compact_table_kernel(CacheView sc, CacheView dc,
-                                                                    const int32_t* to,
-                                                                    uint32_t* status) {
+// Copies the moves' keys and values through shared memory by bulk copies (one thread, six
+// 32 KB stages, four loads ahead of the stores: bound by HBM, 2 x the moved bytes), while the
+// block's other threads write the tables, lengths and counts.
+constexpr int kPieces = 32768, kStages = 6, kAhead = 4;
+constexpr int kMoveThreads = 288;
+
+__global__ void __launch_bounds__(kMoveThreads) compact_move_kernel(CacheView sc, CacheView dc, int inplace,
+                                                                   Moves mv, const Plan* plan,
+                                                                   uint32_t* status) {
+  extern __shared__ __align__(128) uint8_t stage[];
+  __shared__ __align__(8) uint64_t full[kStages];
+  const int tid = threadIdx.x;
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) mbar_init(&full[i], 1);
+    fence_mbar_init();
+    // the barriers are used by the bulk copies
+    fence_proxy_async_smem();
+  }
+  __syncthreads();
+  pdl_wait();
+  const int n = plan->n_moves;
+  if (tid >= 256) {
+    if (tid > 256) return;
+    // ---------------------------------------------------------------- the copies
+    const int64_t page_bytes = 2ll * sc.Hkv * sc.D << sc.ps_log2;
+    const int pieces = static_cast<int>((page_bytes + kPieces - 1) / kPieces);
+    const int64_t units = static_cast<int64_t>(n) * 2 * pieces;
+    auto unit = [&](int64_t u, const uint8_t** src, uint8_t** dst) -> uint32_t {
+      const int64_t m = u / (2 * pieces);
+      const int x = static_cast<int>(u - m * 2 * pieces), half = x / pieces, piece = x - half * pieces;
+      const int64_t from = mv.from[m], to = inplace ? mv.hole[m] : m;
+      const int64_t off = static_cast<int64_t>(piece) * kPieces;
+      *src = reinterpret_cast<const uint8_t*>((half ? sc.v : sc.k) + from * sc.page_stride) + off;
+      *dst = to < dc.num_pages ? reinterpret_cast<uint8_t*>((half ? dc.v : dc.k) + to * dc.page_stride) + off : nullptr;
+      const int64_t left = page_bytes - off;
+      return static_cast<uint32_t>(left < kPieces ? left : kPieces);
+    };
+    const int64_t mine = units > blockIdx.x ? (units - blockIdx.x + gridDim.x - 1) / gridDim.x : 0;
+    auto load = [&](int64_t k) {
+      const uint8_t* src;
+      uint8_t* dst;
+      const uint32_t bytes = unit(blockIdx.x + k * gridDim.x, &src, &dst);
+      const int s = static_cast<int>(k % kStages);
+      mbar_arrive_expect_tx(&full[s], bytes);
+      bulk_load(stage + s * kPieces, src, bytes, &full[s]);
+    };
+    for (int64_t k = 0; k < kAhead && k < mine; ++k) load(k);
+    int64_t k = 0;
+    for (; k < mine; ++k) {
+      const int s = static_cast<int>(k % kStages);
+      if (!mbar_wait(&full[s], static_cast<uint32_t>(k / kStages) & 1u, status)) break;
+      const uint8_t* src;
+      uint8_t* dst;
+      const uint32_t bytes = unit(blockIdx.x + k * gridDim.x, &src, &dst);
+      fence_proxy_async_smem();
+      if (dst != nullptr) bulk_store(dst, stage + s * kPieces, bytes);
+      bulk_commit();
+      if (k + kAhead < mine) {
+        // its stage was stored kStages - kAhead groups ago
+        bulk_wait_read<kStages - kAhead>();
+        load(k + kAhead);
+      }
+    }
+    // every copy has landed before the block ends (after a wait that gave up: the loads, bounded)
+    if (k < mine)
+      for (int64_t j = k; j < mine && j < k + kAhead; ++j)
+        mbar_wait_ns(&full[j % kStages], static_cast<uint32_t>(j / kStages) & 1u, 200000000ull);
+    bulk_wait_all();
+    return;
+  }
+  // ------------------------------------------------------- tables, lengths and counts
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * 256;
+  const int64_t i0 = blockIdx.x * 256ll + tid;
   const int64_t total = static_cast<int64_t>(sc.num_rows) * sc.width;
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * kCopyThreads;
-  const int64_t i0 = blockIdx.x * static_cast<int64_t>(kCopyThreads) + threadIdx.x;
   for (int64_t i = i0; i < total; i += stride) {
     const int page = sc.table[i];
     int d = -1;
     if (page >= 0 && page < sc.num_pages) {
-      d = to[page];
+      d = mv.to[page];
       if (d >= dc.num_pages) d = -1;
     } else if (page >= sc.num_pages) {
       set_device_status(status, DEV_BAD_INDEX);
     }
     dc.table[i] = d;
   }
-  for (int64_t i = i0; i < sc.num_rows; i += stride) dc.len[i] = sc.len[i];
+  if (!inplace) {
+    for (int64_t i = i0; i < sc.num_rows; i += stride) dc.len[i] = sc.len[i];
+    for (int64_t p = i0; p < dc.num_pages; p += stride) dc.ref[p] = p < n ? sc.ref[mv.from[p]] : 0;
+    if (i0 == 0 && n > dc.num_pages) set_device_status(status, DEV_NO_PAGES);
+  } else {
+    for (int64_t m = i0; m < n; m += stride) {
+      const int from = mv.from[m];
+      sc.ref[mv.hole[m]] = sc.ref[from];
+      sc.ref[from] = 0;
+    }
+  }
 }
 
 __global__ void __launch_bounds__(kCopyThreads) reset_kernel(CacheView c) {
@@ -353,9 +479,9 @@ unsigned wide_grid(int64_t items) {
 
 }  // namespace
 
-// The page list doubles as the compaction's map (num_pages) and its holes (num_pages).
+// Behind the plan: the list of free pages, or the compaction's three lists.
 size_t cache_pages_ws_bytes(int64_t num_pages) {
-  return sizeof(Plan) + static_cast<size_t>(num_pages) * 2 * sizeof(int32_t);
+  return sizeof(Plan) + static_cast<size_t>(num_pages) * 3 * sizeof(int32_t);
 }
 
 cudaError_t launch_cache_reset(const CacheView& c, cudaStream_t s) {
@@ -368,19 +494,24 @@ cudaError_t launch_cache_reset(const CacheView& c, cudaStream_t s) {
 cudaError_t launch_cache_extend(const CacheView& c, int n, const int32_t* rows, const int32_t* add,
                                 void* ws, uint32_t* status, cudaStream_t s) {
   Plan* plan = static_cast<Plan*>(ws);
-  free_list_kernel<<<1, kScanThreads, 0, s>>>(c.ref, c.num_pages, page_list(ws), &plan->n_free);
-  extend_plan_kernel<<<1, kMaxList, 0, s>>>(c, n, rows, add, plan, status);
-  extend_kernel<<<static_cast<unsigned>(n), kCopyThreads, 0, s>>>(c, plan, page_list(ws));
-  return cudaGetLastError();
+  extend_plan_kernel<<<1, kMaxList, 0, s>>>(c, n, rows, add, plan, page_list(ws), status);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_after(extend_kernel, dim3(static_cast<unsigned>(n)), kCopyThreads, 0, s, c,
+                      static_cast<const Plan*>(plan), static_cast<const int32_t*>(page_list(ws)));
 }
 
 cudaError_t launch_cache_fork(const CacheView& c, int n, const int32_t* parents,
                               const int32_t* children, void* ws, uint32_t* status, cudaStream_t s) {
   Plan* plan = static_cast<Plan*>(ws);
-  free_list_kernel<<<1, kScanThreads, 0, s>>>(c.ref, c.num_pages, page_list(ws), &plan->n_free);
-  fork_plan_kernel<<<1, kMaxList, 0, s>>>(c, n, parents, children, plan, status);
-  fork_kernel<<<static_cast<unsigned>(n), kCopyThreads, 0, s>>>(c, plan, page_list(ws), status);
-  return cudaGetLastError();
+  fork_plan_kernel<<<1, kMaxList, 0, s>>>(c, n, parents, children, plan, page_list(ws), status);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  // enough blocks to fill the GPU, while each has a few hundred units
+  int ny = 4 * num_sms() / n;
+  ny = ny < 1 ? 1 : (ny > 16 ? 16 : ny);
+  return launch_after(fork_kernel, dim3(static_cast<unsigned>(n), static_cast<unsigned>(ny)), kCopyThreads, 0, s, c,
+                      static_cast<const Plan*>(plan), static_cast<const int32_t*>(page_list(ws)), status);
 }
 
 cudaError_t launch_cache_free(const CacheView& c, int n, const int32_t* rows, uint32_t* status,
@@ -391,16 +522,22 @@ cudaError_t launch_cache_free(const CacheView& c, int n, const int32_t* rows, ui
 
 cudaError_t launch_cache_compact(const CacheView& src, const CacheView& dst, bool inplace,
                                  int32_t* n_live, void* ws, uint32_t* status, cudaStream_t s) {
+  static bool attr_set[kMaxDeviceCache] = {};
+  const int dev = cached_device_index();
+  if (dev < 0) return cudaErrorInvalidDevice;
+  if (!attr_set[dev]) {
+    cudaError_t e = cudaFuncSetAttribute(compact_move_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kStages * kPieces);
+    if (e != cudaSuccess) return e;
+    attr_set[dev] = true;
+  }
   Plan* plan = static_cast<Plan*>(ws);
-  int32_t* to = page_list(ws);
-  compact_plan_kernel<<<1, kScanThreads, 0, s>>>(src.ref, src.num_pages, inplace ? 1 : 0, to,
-                                                 &plan->n_free, n_live);
-  compact_copy_kernel<<<wide_grid(src.num_pages), kCopyThreads, 0, s>>>(src, dst, inplace ? 1 : 0, to,
-                                                                        &plan->n_free, status);
-  const int64_t n = static_cast<int64_t>(src.num_rows) * src.width;
-  compact_table_kernel<<<wide_grid((n + kCopyThreads - 1) / kCopyThreads), kCopyThreads, 0, s>>>(
-      src, dst, to, status);
-  return cudaGetLastError();
+  const Moves mv = moves_of(ws, src.num_pages);
+  compact_plan_kernel<<<1, kScanThreads, 0, s>>>(src.ref, src.num_pages, inplace ? 1 : 0, mv, plan, n_live);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_after(compact_move_kernel, dim3(static_cast<unsigned>(num_sms())), kMoveThreads, kStages * kPieces, s,
+                      src, dst, inplace ? 1 : 0, mv, static_cast<const Plan*>(plan), status);
 }
 
 }  // namespace ls

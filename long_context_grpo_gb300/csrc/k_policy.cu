@@ -702,16 +702,7 @@ cudaError_t launch_policy_loss(const PolicyArgs& a, cudaStream_t s) {
     e = cudaGetLastError();
   }
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(1);
-  cfg.blockDim = dim3(kReduceThreads);
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, policy_reduce, static_cast<const double*>(a.terms), a.T, a.loss);
+  return launch_after(policy_reduce, dim3(1), kReduceThreads, 0, s, static_cast<const double*>(a.terms), a.T, a.loss);
 }
 
 }  // namespace ls
