@@ -10,7 +10,7 @@
 //   tokens over its keys, or, for a group with shared pages, all the group's tokens over the
 //   shared keys (read once) and each sequence's over the rest.  Key runs are split into
 //   chunks so that the tile counts of all SMs come out even (the chunk length with the least
-//   estimated makespan of 15 candidates); a segment of more than one chunk, or a token in two
+//   estimated makespan of 16 candidates); a segment of more than one chunk, or a token in two
 //   segments, leaves partial results.  Output: lists of jobs.
 //
 // cache_attn_kernel<D, wide> (persistent, 384 threads).  Warp 0 feeds Q, K and V by TMA (pages
@@ -46,7 +46,6 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleLog2 = 8.0f;
 constexpr int kNarrowRows = 64;
-constexpr int kNarrowRounds = 6;       // rounds of narrow jobs at most
 constexpr int kMaxTiles = 1 << 24;     // 128-key tiles of the longest sequence
 
 // A run of packed tokens over a run of key tiles of one table row.
@@ -83,7 +82,8 @@ __device__ __forceinline__ int tiles_of(const Seg& s, int t_end) {
   return n < s.tiles ? n : s.tiles;
 }
 
-__device__ __forceinline__ int plan_scan(int v, int* sh, int* total) {
+// (not inlined: the planning kernel runs once through its code, so its size is its time)
+__device__ __noinline__ int plan_scan(int v, int* sh, int* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int s = v;
 #pragma unroll
@@ -133,8 +133,9 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const __grid_c
   Seg* segs = reinterpret_cast<Seg*>(dyn);
   int* first[2] = {reinterpret_cast<int*>(dyn + cap * sizeof(Seg)),
                    reinterpret_cast<int*>(dyn + cap * sizeof(Seg)) + cap};
-  __shared__ int sh[33];
+  __shared__ int sh[66];
   __shared__ int sh_max[2], sh_c[2], sh_grouped;
+  __shared__ int sh_base[2], sh_part[2];
   __shared__ unsigned long long sh_w[2];
   __shared__ unsigned long long best[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -145,6 +146,8 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const __grid_c
 
   if (tid < 2) {
     sh_max[tid] = 0;
+    sh_base[tid] = 0;
+    sh_part[tid] = tid ? static_cast<int>(a.l.rows_narrow) : 0;
     sh_w[tid] = 0;
     best[tid] = ~0ull;
   }
@@ -242,15 +245,18 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const __grid_c
   __syncthreads();
   // candidates: warp = (class, k): chunks that make k rounds of jobs over all streams
   {
-    const int cls = warp >> 4, k = (warp & 15) + 1;
+    const int cls = warp >> 4, v = warp & 15;
+    // wide: 15 round counts; narrow: five, each with chunks an eighth and a quarter longer too (a
+    // few short sequences then stay whole); and no split
+    const int k = cls ? v + 1 : v / 3 + 1, more = cls ? 0 : v % 3;
     const int round = cls ? a.sms : 2 * a.sms;
     const int longest = sh_max[cls];
     const unsigned long long W = sh_w[cls];
-    int C = k == 16 ? longest : static_cast<int>((W + static_cast<unsigned long long>(round) * k - 1) /
-                                                 (static_cast<unsigned long long>(round) * k));
+    const unsigned long long per = 8ull * round * k;
+    int C = v == 15 ? longest : static_cast<int>((W * (8 + more) + per - 1) / per);
     if (C < (cls ? 8 : 2)) C = cls ? 8 : 2;
     if (C > longest) C = longest;
-    if (longest > 0 && (cls == 1 || k <= kNarrowRounds || k == 16)) {
+    if (longest > 0) {
       unsigned long long jobs = 0, rows = 0;
       for (int i = lane; i < n_segs; i += 32) {
         const Seg& s = segs[i];
@@ -280,8 +286,7 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const __grid_c
   __syncthreads();
 
   // chunks, partial rows and jobs of every segment
-  int base[2] = {0, 0};
-  int64_t part[2] = {0, a.l.rows_narrow};
+  int rows_total;
   for (int i0 = 0; i0 < n_segs; i0 += kPlanThreads) {
     const int i = i0 + tid;
     int jobs = 0, rows = 0, w = 0;
@@ -299,21 +304,24 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const __grid_c
         if (s.chunks > 1 || two) rows = a.c.Hq * s.chunks * s.n_tok;
       }
     }
-#pragma unroll
+#pragma unroll 1
     for (int cls = 0; cls < 2; ++cls) {
       int total;
       const int at = plan_scan(w == cls ? jobs : 0, sh, &total);
-      if (i < n_segs) first[cls][i] = base[cls] + at;
-      base[cls] += total;
-      const int pr = plan_scan(w == cls ? rows : 0, sh, &total);
-      if (i < n_segs && w == cls && rows > 0) segs[i].part = static_cast<int>(part[cls] + pr);
-      part[cls] += total;
+      if (i < n_segs) first[cls][i] = sh_base[cls] + at;
+      const int pr = plan_scan(w == cls ? rows : 0, sh + 33, &rows_total);
+      if (i < n_segs && w == cls && rows > 0) segs[i].part = sh_part[cls] + pr;
+      __syncthreads();
+      if (tid == 0) {
+        sh_base[cls] += total;
+        sh_part[cls] += rows_total;
+      }
     }
   }
   __syncthreads();
   if (tid == 0) {
-    info->n_jobs[0] = base[0];
-    info->n_jobs[1] = base[1];
+    info->n_jobs[0] = sh_base[0];
+    info->n_jobs[1] = sh_base[1];
     info->grouped = grouped ? 1 : 0;
   }
 
@@ -328,7 +336,8 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const __grid_c
   for (int cls = 0; cls < 2; ++cls) {
     Job* jobs = reinterpret_cast<Job*>(a.ws + (cls ? a.l.wide : a.l.narrow));
     const int* f = first[cls];
-    for (int x = tid; x < base[cls]; x += kPlanThreads) {
+    const int n_jobs = sh_base[cls];
+    for (int x = tid; x < n_jobs; x += kPlanThreads) {
       int lo = 0, hi = n_segs - 1;           // the last segment that starts at or before x
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
