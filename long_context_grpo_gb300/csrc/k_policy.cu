@@ -9,11 +9,12 @@
 //   owns one row at a time, each a slice of at most 38 KB, in three buffers: one row waits for its
 //   gradient while its sums are exchanged, the next row's sums are taken, and the third
 //   arrives by bulk copy.
-//   4 or 8 streaming warps: the warp's maximum (packed bf16 maxima), then the sum of exp(x - max) in
-//     fp32, joined across lanes in fp32 pairs; later p g rounded to bf16 and stored.
+//   4 or 8 streaming warps: the sum of exp(x - m) in fp32, m the maximum of a thread's first eight
+//     logits (the true one if that overflows), joined across lanes in fp32 pairs; later p g
+//     rounded to bf16 and stored.  One exponential a logit and pass.
 //   1 scalar warp: joins the partials, exchanges them with the other CTAs
 //     (distributed shared memory, remote mbarrier arrivals, bounded waits) and joins those in
-//     rank order and decides the clip on d in fp64.  It also owns the up to 7 + 7 logits of a row outside its 16-byte
+//     rank order and decides the clip.  It also owns the up to 7 + 7 logits of a row outside its 16-byte
 //     granules.
 //   1 output warp: issues the copies, writes the token's outputs and its loss term (fp64), off the
 //     row's critical path.
@@ -60,21 +61,53 @@ __device__ __forceinline__ Token load_token(const PolicyArgs& a, int64_t row) {
   return t;
 }
 
+// Unevaluated sums of two fp32 values, about 48 bits: an fp64 instruction holds its pipe for
+// tens of cycles here, and a dozen of them in a row's critical path cost more than all the rest.
+struct Pair {
+  float hi, lo;
+};
+__device__ __forceinline__ Pair two_sum(float a, float b) {
+  const float s = a + b, bb = s - a;
+  return {s, (a - (s - bb)) + (b - bb)};
+}
+__device__ __forceinline__ Pair pair_add(Pair a, Pair b) {
+  const Pair s = two_sum(a.hi, b.hi);
+  return {s.hi, s.lo + (a.lo + b.lo)};
+}
+__device__ __forceinline__ double to_double(Pair a) { return static_cast<double>(a.hi) + static_cast<double>(a.lo); }
+// log(s), s >= 0: the exponent apart, so that the fp32 logarithm sees [1/2, 1) (absolute error
+// below 2^-24); exponent x log 2 is exact in its upper part (16 bits of log 2).
+__device__ __forceinline__ Pair log_pair(Pair s) {
+  constexpr float kLn2Hi = 0.693145751953125f, kLn2Lo = 1.4286068203094172e-06f;
+  int e = 0;
+  const float f = frexpf(s.hi, &e);
+  const float rest = logf(f) + s.lo / s.hi;
+  const float k = static_cast<float>(e);
+  Pair r = two_sum(k * kLn2Hi, rest);
+  r.lo = fmaf(k, kLn2Lo, r.lo);
+  return r;
+}
+// Whether a > b.
+__device__ __forceinline__ bool above(Pair a, Pair b) {
+  const Pair d = pair_add(a, {-b.hi, -b.lo});
+  return d.hi + d.lo > 0.0f;
+}
+
 struct TokenLoss {
   float g;           // d term / d logp
   bool clipped;
 };
-// The clip is decided on d in fp64; ratio and gradient follow in fp32 (relative error ~2^-22).
-__device__ __forceinline__ TokenLoss token_grad(const PolicyArgs& a, const Token& t, double logp) {
+// The clip is decided on the pair d; ratio and gradient follow in fp32 (relative error ~2^-22).
+__device__ __forceinline__ TokenLoss token_grad(const PolicyArgs& a, const Token& t, Pair logp) {
   TokenLoss o;
-  const double d = logp - static_cast<double>(t.old);
-  o.clipped = (t.A > 0.0f && d > a.log_hi) || (t.A < 0.0f && d < a.log_lo);
+  const Pair d = pair_add(logp, {-t.old, 0.0f});
+  o.clipped = (t.A > 0.0f && above(d, {a.log_hi[0], a.log_hi[1]})) || (t.A < 0.0f && above({a.log_lo[0], a.log_lo[1]}, d));
   float slope = 0.0f;
   if (a.ref != nullptr) {
-    const float r = static_cast<float>(logp - static_cast<double>(t.ref));
-    slope = a.kl == 1 ? 1.0f : (a.kl == 2 ? r : -expm1f(-r));
+    const Pair r = pair_add(logp, {-t.ref, 0.0f});
+    slope = a.kl == 1 ? 1.0f : (a.kl == 2 ? r.hi + r.lo : -expm1f(-(r.hi + r.lo)));
   }
-  o.g = t.w * (static_cast<float>(a.beta) * slope - (o.clipped ? 0.0f : expf(static_cast<float>(d)) * t.A));
+  o.g = t.w * (static_cast<float>(a.beta) * slope - (o.clipped ? 0.0f : expf(d.hi + d.lo) * t.A));
   return o;
 }
 // The loss term and the KL estimate in fp64, off the row's critical path: even lanes take the
@@ -105,14 +138,6 @@ __device__ __forceinline__ void write_no_token(const PolicyArgs& a, int64_t row)
   if (a.logp_out != nullptr) a.logp_out[row] = 0.0f;
   if (a.kl_out != nullptr) a.kl_out[row] = 0.0f;
   a.terms[row] = 0.0;
-}
-
-// log(s): the exponent apart, so that the fp32 logarithm sees [1/2, 1) (absolute error 2^-25).
-__device__ __forceinline__ double log_of(double s) {
-  const int e = ((__double2hiint(s) >> 20) & 0x7FF) - 1022;
-  if (e <= -1022 || e >= 1025) return log(s);      // 0, subnormal, infinite, NaN
-  const float m = static_cast<float>(__hiloint2double((__double2hiint(s) & 0x000FFFFF) | 0x3FE00000, __double2loint(s)));
-  return (static_cast<double>(e) + static_cast<double>(log2f(m))) * 0.69314718055994530942;
 }
 
 // ======================================================================================
@@ -155,15 +180,17 @@ __global__ void __launch_bounds__(kRowThreads) policy_rows(const __grid_constant
     if (warp == 0) {
       s = 0.0;
       for (int w = 0; w < kRowThreads / 32; ++w) s += sh_s[w];
-      const double ls = log_of(s);
-      const double logp = static_cast<double>(bf16_at(x, tok.y)) - (static_cast<double>(m) + ls);
-      const TokenLoss o = token_grad(a, tok, logp);
+      const float s_hi = static_cast<float>(s);
+      const Pair ls = log_pair({s_hi, static_cast<float>(s - static_cast<double>(s_hi))});
+      const Pair lp = pair_add(two_sum(bf16_at(x, tok.y), -m), {-ls.hi, -ls.lo});
+      const TokenLoss o = token_grad(a, tok, lp);
+      const double logp = to_double(lp);
       float kl;
       const double term = token_term(a, tok, logp, o.clipped, lane, &kl);
       if (lane == 0) {
         write_token(a, row, o.clipped, logp, kl, term);
         sh_g = o.g;
-        sh_ls = static_cast<float>(ls);
+        sh_ls = ls.hi + ls.lo;
       }
     }
     __syncthreads();
@@ -210,17 +237,6 @@ __device__ __forceinline__ int64_t edge_index(const RowSpan& s, int64_t V, int l
   return -1;
 }
 
-// Sums of exponentials are unevaluated fp32 pairs (about 48 bits): fp64 is slow here, and every
-// join below sits on the row's critical path.
-struct Pair {
-  float hi, lo;
-};
-__device__ __forceinline__ Pair pair_add(Pair a, Pair b) {
-  const float s = a.hi + b.hi;
-  const float bb = s - a.hi;
-  const float err = (a.hi - (s - bb)) + (b.hi - bb);
-  return {s, err + (a.lo + b.lo)};
-}
 // Over the lanes that differ in the bits below kLanes: the maximum of m, and the sum of the parts
 // s relative to it (each given relative to its own m; m a logit, not scaled).  -INF with 0
 // is an empty part.
@@ -239,13 +255,6 @@ __device__ __forceinline__ void join_lanes(float& m, Pair& s) {
   }
   m = M;
 }
-// log(s): the exponent apart, so that the fp32 logarithm sees [1/2, 1) (absolute error 2^-25).
-__device__ __forceinline__ double log_pair(Pair s) {
-  int e = 0;
-  const float f = frexpf(s.hi, &e);
-  return (static_cast<double>(e) + static_cast<double>(log2f(f) + s.lo / s.hi * kLog2e)) * 0.69314718055994530942;
-}
-
 // Named barriers.  The streaming warps take the sums of row r + 1 before they wait for the gradient
 // of row r, so the parts of row r + 2 come behind the scalar warp's use of those of row r: two
 // ids (row parity).  Nothing holds the scalar and streaming warps back from running ahead of
@@ -257,6 +266,10 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
+}
+__device__ __forceinline__ float granule_max(const uint4& v) {
+  const uint32_t m = max_bf16x2(max_bf16x2(v.x, v.y), max_bf16x2(v.z, v.w));
+  return fmaxf(lo_bf16(m), hi_bf16(m));
 }
 
 // Eight logits from word kFirst (and a half, if odd) of two granules on.
@@ -277,7 +290,7 @@ __global__ void __launch_bounds__(kStream + 64, kStream == 256 ? 2 : 4)
   __shared__ float part[2][kWarps][3];         // a warp's maximum and sum (pair)
   __shared__ float slot[2][kMaxCluster][3];    // a CTA's, by rank
   __shared__ float sh_g[2], sh_c[2], sh_gy[2];
-  __shared__ double sh_logp[kBufs];            // for the output warp
+  __shared__ float sh_logp[kBufs][2];          // for the output warp (pair)
   __shared__ int sh_state[kBufs];                  // 0 left out, 1 used, 2 used and clipped, 3 aborted
   __shared__ int sh_used[kBufs], sh_y[2];
   // Set when a bounded wait of this CTA or of a peer gave up: rows are only walked through from
@@ -343,7 +356,7 @@ __global__ void __launch_bounds__(kStream + 64, kStream == 256 ? 2 : 4)
       TokenLoss o;
       o.g = 0.0f;
       o.clipped = false;
-      double logp = 0.0;
+      Pair logp = {0.0f, 0.0f};
       float lse = 0.0f;
       bool aborted = false;
       named_barrier_sync(kBarParts + par, kThreads);
@@ -357,7 +370,7 @@ __global__ void __launch_bounds__(kStream + 64, kStream == 256 ? 2 : 4)
           m = ev;                        // a logit outside the granules
           s.hi = ev == -INFINITY ? 0.0f : 1.0f;
         }
-        if (rank == 0) join_lanes<32>(m, s); else join_lanes<8>(m, s);
+        if (kWarps > 8 || rank == 0) join_lanes<32>(m, s); else join_lanes<8>(m, s);
         // (the shuffles also make sure that xv has arrived: the row may be overwritten in place
         // once the partials are out)
         const float x_y = __shfl_sync(0xffffffffu, xv, 0);
@@ -387,22 +400,22 @@ __global__ void __launch_bounds__(kStream + 64, kStream == 256 ? 2 : 4)
         // the peers' own waits poll their flag
         if (cl > 1 && aborted && lane < cl) st_cluster_u32(cluster_map(&cl_abort, lane), 1u);
         ++ux;
-        const double ls = static_cast<double>(m) + log_pair(s);
-        logp = static_cast<double>(x_y) - ls;
-        lse = static_cast<float>(ls);
+        const Pair ls = log_pair(s);
+        logp = pair_add(two_sum(x_y, -m), {-ls.hi, -ls.lo});
+        lse = m + (ls.hi + ls.lo);
         if (!aborted) o = token_grad(a, t, logp);
       }
       // -g p = -sign(g) 2^(x log2 e - lse log2 e + log2 |g|)
       const float c = fmaf(-lse, kLog2e, log2f(fabsf(o.g)));
-      const float gy = o.g * (1.0f - ex2_approx(static_cast<float>(logp) * kLog2e));
+      const float gy = o.g * (1.0f - ex2_approx((logp.hi + logp.lo) * kLog2e));
       if (lane == 0) {
         sh_g[par] = o.g;
         sh_c[par] = c;
         sh_gy[par] = gy;
         sh_y[par] = t.used(a.V) ? t.y - sp.head : -1;
-        sh_logp[b] = logp;
+        sh_logp[b][0] = logp.hi;
+        sh_logp[b][1] = logp.lo;
         sh_state[b] = aborted ? 3 : (!t.used(a.V) ? 0 : (o.clipped ? 2 : 1));
-        __threadfence_block();
       }
       __syncwarp();
       named_barrier_arrive(kBarG + par, kThreads);
@@ -449,7 +462,7 @@ __global__ void __launch_bounds__(kStream + 64, kStream == 256 ? 2 : 4)
     int it = 0, b = 0;
     for (int64_t row = cid; row < a.T; row += ncl, ++it, b = b == kBufs - 1 ? 0 : b + 1) {
       named_barrier_sync(kBarOut + b, 64);
-      const double logp = sh_logp[b];
+      const Pair lp2 = {sh_logp[b][0], sh_logp[b][1]};
       const int state = sh_state[b];
       __syncwarp();
       named_barrier_sync(kBarEmpty + b, kThreads);
@@ -468,8 +481,8 @@ __global__ void __launch_bounds__(kStream + 64, kStream == 256 ? 2 : 4)
         continue;
       }
       float kl;
-      double term = token_term(a, t, logp, state == 2, lane, &kl);
-      double lp = logp;
+      double lp = to_double(lp2);
+      double term = token_term(a, t, lp, state == 2, lane, &kl);
       if (state == 3) {
         term = lp = __longlong_as_double(0x7ff8000000000000ll);
         kl = static_cast<float>(lp);
@@ -484,8 +497,26 @@ __global__ void __launch_bounds__(kStream + 64, kStream == 256 ? 2 : 4)
   } else {
     // -------------------------------------------------------------- streaming warps
     const uint64_t l2 = f2_pack(kLog2e, kLog2e);
-    // Maximum and sum of this CTA's slice of its i-th row: the warp's maximum first, then one
-    // exponential a logit.
+    auto slice_sum = [&](const uint4* buf, int n, int from, float m) {
+      const float base = m == -INFINITY ? 0.0f : -m;
+      const uint64_t nb = f2_pack(base, base);
+      uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll 4
+      for (int j = from; j < n; j += kStream) {
+        const uint4 v = buf[j];
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          float e0, e1;
+          f2_unpack(f2_mul(f2_add(f2_pack(lo_bf16(w[u]), hi_bf16(w[u])), nb), l2), e0, e1);
+          acc[u] = f2_add(acc[u], f2_pack(ex2_approx(e0), ex2_approx(e1)));
+        }
+      }
+      float s0, s1;
+      f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), s0, s1);
+      return s0 + s1;
+    };
+    // Sum of exponentials of this CTA's slice of its i-th row.
     auto pass1 = [&](int64_t row, int i) {
       const int bi = i % kBufs, par = i & 1;
       const int n = alike ? sp.n : row_span(a, row, per, rank).n;
@@ -497,41 +528,26 @@ __global__ void __launch_bounds__(kStream + 64, kStream == 256 ? 2 : 4)
       float m = -INFINITY;
       Pair s = {0.0f, 0.0f};
       if (here && sh_used[bi] != 0 && !*vabort) {
-        uint32_t mx = 0xFF80FF80u;
-#pragma unroll 4
-        for (int j = tid; j < n; j += kStream) {
-          const uint4 v = buf[j];
-          mx = max_bf16x2(mx, max_bf16x2(max_bf16x2(v.x, v.y), max_bf16x2(v.z, v.w)));
+        // Relative to the maximum of the thread's first granule; if a later logit is so much
+        // larger that the sum leaves [0, 2^100), or nothing in it is finite, once more relative
+        // to the warp's true maximum.
+        m = tid < n ? granule_max(buf[tid]) : -INFINITY;
+        float sum = slice_sum(buf, n, tid, m);
+        const bool odd = tid < n && (m == -INFINITY || !(sum < 1.2676506e30f));
+        if (__any_sync(0xffffffffu, odd)) {
+          m = -INFINITY;
+          for (int j = tid; j < n; j += kStream) m = fmaxf(m, granule_max(buf[j]));
+#pragma unroll
+          for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+          sum = slice_sum(buf, n, tid, m);
         }
-        m = fmaxf(lo_bf16(mx), hi_bf16(mx));
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-        const float base = m == -INFINITY ? 0.0f : -m;
-        const uint64_t nb = f2_pack(base, base);
-        uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
-#pragma unroll 2
-        for (int j = tid; j < n; j += kStream) {
-          const uint4 v = buf[j];
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            float e0, e1;
-            f2_unpack(f2_mul(f2_add(f2_pack(lo_bf16(w[u]), hi_bf16(w[u])), nb), l2), e0, e1);
-            acc[u] = f2_add(acc[u], f2_pack(ex2_approx(e0), ex2_approx(e1)));
-          }
-        }
-        float s0, s1;
-        f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), s0, s1);
-        s.hi = s0 + s1;
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1)
-          s = pair_add(s, {__shfl_xor_sync(0xffffffffu, s.hi, off), __shfl_xor_sync(0xffffffffu, s.lo, off)});
+        s.hi = sum;
+        join_lanes<32>(m, s);
       }
       if (lane == 0) {
         part[par][warp][0] = m;
         part[par][warp][1] = s.hi;
         part[par][warp][2] = s.lo;
-        __threadfence_block();
       }
       __syncwarp();
       named_barrier_arrive(kBarParts + par, kThreads);
@@ -547,7 +563,6 @@ __global__ void __launch_bounds__(kStream + 64, kStream == 256 ? 2 : 4)
       const float g = sh_g[par], c = sh_c[par], gy = sh_gy[par];
       const int y = sh_y[par];
       if (!alike) sp = row_span(a, row, per, rank);
-      const int yg = y >= 0 ? (y >> 3) - sp.g0 : -1;        // granule of the sampled token
       uint16_t* d = a.dlogits + row * a.ldd + sp.head + 8 * static_cast<int64_t>(sp.g0);
       const bool direct = (reinterpret_cast<uintptr_t>(d) & 15) == 0;
       uint4* d4 = direct ? reinterpret_cast<uint4*>(d) : buf;
@@ -556,7 +571,7 @@ __global__ void __launch_bounds__(kStream + 64, kStream == 256 ? 2 : 4)
       if (g == 0.0f || *vabort) {
         for (int i = tid; i < sp.n; i += kStream) d4[i] = make_uint4(0u, 0u, 0u, 0u);
       } else {
-#pragma unroll 2
+#pragma unroll 4
         for (int i = tid; i < sp.n; i += kStream) {
           const uint4 v = buf[i];
           const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -567,15 +582,13 @@ __global__ void __launch_bounds__(kStream + 64, kStream == 256 ? 2 : 4)
             f2_unpack(f2_fma(f2_pack(lo_bf16(w[u]), hi_bf16(w[u])), l2, c2), e0, e1);
             o[u] = pack_bf16x2(ex2_approx(e0), ex2_approx(e1)) ^ sign;
           }
-          if (i == yg) {
-            const uint32_t h = to_bf16(gy);
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-              if (u == (y & 7) >> 1) o[u] = (y & 1) ? (o[u] & 0xFFFFu) | (h << 16) : (o[u] & 0xFFFF0000u) | h;
-          }
           d4[i] = make_uint4(o[0], o[1], o[2], o[3]);
         }
       }
+      // the sampled token's column, by the thread that wrote its granule
+      const int yl = y - 8 * sp.g0;
+      if (y >= 0 && yl >= 0 && yl < 8 * sp.n && (yl >> 3) % kStream == tid && g != 0.0f)
+        reinterpret_cast<uint16_t*>(d4)[yl] = to_bf16(gy);
       if (!direct && sp.n > 0) {
         // the gradient row lies at another offset from a 16-byte boundary: its granules are cut
         // from two of the buffer's

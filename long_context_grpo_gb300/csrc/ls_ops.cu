@@ -61,8 +61,11 @@ ls_status ls_policy_loss(const ls_policy_loss_desc* d, void* workspace, size_t w
   a.weight = d->weights;
   a.clip_lo = 1.0 - d->eps_low;
   a.clip_hi = 1.0 + d->eps_high;
-  a.log_lo = std::log(a.clip_lo);
-  a.log_hi = std::log(a.clip_hi);
+  const double lo = std::log(a.clip_lo), hi = std::log(a.clip_hi);
+  a.log_lo[0] = static_cast<float>(lo);
+  a.log_lo[1] = static_cast<float>(lo - a.log_lo[0]);
+  a.log_hi[0] = static_cast<float>(hi);
+  a.log_hi[1] = static_cast<float>(hi - a.log_hi[0]);
   a.beta = d->beta;
   a.kl = d->kl;
   a.loss = d->loss;

@@ -18,7 +18,7 @@ struct PolicyArgs {
   const float* adv;
   const float* weight;
   double clip_lo, clip_hi;    // 1 - eps_low, 1 + eps_high
-  double log_lo, log_hi;      // their logarithms
+  float log_lo[2], log_hi[2]; // their logarithms, each as a sum of two
   double beta;
   int kl;                     // ls_kl_kind
   float* loss;
