@@ -4,24 +4,27 @@
 //   term = w (beta kl - min(rho A, clip(rho) A)),  g = d term / d logp,
 //   dlogits = g (onehot_y - p)
 //
-// policy_cluster: the whole row stays in shared memory between the two passes, so HBM sees every
-//   logit once in and once out (4 bytes a logit; bound by HBM).  A cluster of 1, 2, 4 or 8 CTAs
-//   owns one row at a time, each a slice of at most 38 KB, in three buffers: one row waits for its
-//   gradient while its sums are exchanged, the next row's sums are taken, and the third
-//   arrives by bulk copy.
-//   4 or 8 streaming warps: the sum of exp(x - m) in fp32, m the maximum of a thread's first eight
+// Rows are read from HBM once and gradients written once (4 bytes a logit; bound by HBM).
+//
+// policy_warp<n>: V <= 256 n.  A warp a row, the row in registers: no block-wide step at all.
+// policy_cluster: larger rows stay in shared memory between the two passes.  A cluster of 1, 2, 4
+//   or 8 CTAs owns one row at a time, each a slice of at most 76 KB, in three buffers: one row
+//   waits for its gradient while its sums are exchanged, the next row's sums are taken, and the
+//   third arrives by bulk copy.  The exchange takes about 4 us whatever the slice, so the fewest
+//   CTAs a row are the fastest (slices of 76 KB against 38 KB, two CTAs an SM then:
+//   4,096 x 151,936 388 against 457 us).
+//   8 streaming warps: the sum of exp(x - m) in fp32, m the maximum of a thread's first eight
 //     logits (the true one if that overflows), joined across lanes in fp32 pairs; later p g
 //     rounded to bf16 and stored.  One exponential a logit and pass.
-//   1 scalar warp: joins the partials, exchanges them with the other CTAs
-//     (distributed shared memory, remote mbarrier arrivals, bounded waits) and joins those in
-//     rank order and decides the clip.  It also owns the up to 7 + 7 logits of a row outside its 16-byte
-//     granules.
-//   1 output warp: issues the copies, writes the token's outputs and its loss term (fp64), off the
-//     row's critical path.
-//   A row whose gradient has another alignment than its logits goes
-//     through shared memory once more and is shifted there.
-// policy_rows: one CTA a row from global memory, for vocabularies beyond eight slices (460,000).
-// policy_reduce: the fp64 sum of the tokens' terms in a fixed order, rounded once.
+//   1 scalar warp: joins the partials, exchanges them with the other CTAs (distributed shared
+//     memory, remote mbarrier arrivals, bounded waits), joins those in rank order and decides
+//     the clip.  It also owns the up to 7 + 7 logits of a row outside its 16-byte granules.
+//   1 copy warp: requests a row's slice as soon as a buffer is free.
+//   A row whose gradient has another alignment than its logits goes through shared memory once
+//   more and is shifted there.
+// policy_rows: one CTA a row from global memory, for vocabularies beyond eight slices (304,000).
+// policy_finish: a thread a token: its outputs and its loss term in fp64 (an fp64 instruction of one
+//   lane costs as much as one of 32 tokens), and their sum in a fixed order, rounded once.
 #include <atomic>
 
 #include "ls_internal.h"
@@ -74,7 +77,6 @@ __device__ __forceinline__ Pair pair_add(Pair a, Pair b) {
   const Pair s = two_sum(a.hi, b.hi);
   return {s.hi, s.lo + (a.lo + b.lo)};
 }
-__device__ __forceinline__ double to_double(Pair a) { return static_cast<double>(a.hi) + static_cast<double>(a.lo); }
 // log(s), s >= 0: the exponent apart, so that the fp32 logarithm sees [1/2, 1) (absolute error
 // below 2^-24); exponent x log 2 is exact in its upper part (16 bits of log 2).
 __device__ __forceinline__ Pair log_pair(Pair s) {
@@ -110,34 +112,12 @@ __device__ __forceinline__ TokenLoss token_grad(const PolicyArgs& a, const Token
   o.g = t.w * (static_cast<float>(a.beta) * slope - (o.clipped ? 0.0f : expf(d.hi + d.lo) * t.A));
   return o;
 }
-// The loss term and the KL estimate in fp64, off the row's critical path: even lanes take the
-// ratio's exponential, odd lanes the KL term's, in one instruction stream.
-__device__ __forceinline__ double token_term(const PolicyArgs& a, const Token& t, double logp, bool clipped,
-                                             int lane, float* kl) {
-  const double d = logp - static_cast<double>(t.old), r = logp - static_cast<double>(t.ref);
-  const double em = expm1((lane & 1) ? -r : d);
-  const double em_d = __shfl_sync(0xffffffffu, em, 0), em_r = __shfl_sync(0xffffffffu, em, 1);
-  const double A = t.A;
-  const double surr = clipped ? (A > 0.0 ? a.clip_hi : a.clip_lo) * A : (em_d + 1.0) * A;
-  double k = 0.0;
-  if (a.ref != nullptr) k = a.kl == 1 ? r : (a.kl == 2 ? 0.5 * r * r : em_r + r);
-  *kl = static_cast<float>(k);
-  return static_cast<double>(t.w) * (a.beta * k - surr);
+// What the row kernels leave for policy_finish.
+__device__ __forceinline__ void leave_logp(const PolicyArgs& a, int64_t row, Pair logp) {
+  a.logp_pair[row] = make_float2(logp.hi, logp.lo);
 }
-
-__device__ __forceinline__ void write_token(const PolicyArgs& a, int64_t row, bool clipped, double logp, float kl,
-                                            double term) {
-  a.clip_mask[row] = clipped ? 1 : 0;
-  if (a.logp_out != nullptr) a.logp_out[row] = static_cast<float>(logp);
-  if (a.kl_out != nullptr) a.kl_out[row] = kl;
-  a.terms[row] = term;
-}
-// A token that is left out (weight 0, or an id outside the vocabulary): zeros.
-__device__ __forceinline__ void write_no_token(const PolicyArgs& a, int64_t row) {
-  a.clip_mask[row] = 0;
-  if (a.logp_out != nullptr) a.logp_out[row] = 0.0f;
-  if (a.kl_out != nullptr) a.kl_out[row] = 0.0f;
-  a.terms[row] = 0.0;
+__device__ __forceinline__ void reset_counter(const PolicyArgs& a) {
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.counter = 0u;
 }
 
 // ======================================================================================
@@ -150,16 +130,14 @@ __global__ void __launch_bounds__(kRowThreads) policy_rows(const __grid_constant
   __shared__ double sh_s[kRowThreads / 32];
   __shared__ float sh_g, sh_ls;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  reset_counter(a);
+  pdl_launch_dependents();
   for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
     const uint16_t* x = a.logits + row * a.ldx;
     uint16_t* d = a.dlogits + row * a.ldd;
     const Token tok = load_token(a, row);
     if (!tok.used(a.V)) {
       for (int64_t i = tid; i < a.V; i += kRowThreads) d[i] = 0;
-      if (tid == 0) {
-        if (tok.bad(a.V)) set_device_status(a.status, DEV_BAD_INDEX);
-        write_no_token(a, row);
-      }
       continue;
     }
     float m = -INFINITY;
@@ -184,11 +162,8 @@ __global__ void __launch_bounds__(kRowThreads) policy_rows(const __grid_constant
       const Pair ls = log_pair({s_hi, static_cast<float>(s - static_cast<double>(s_hi))});
       const Pair lp = pair_add(two_sum(bf16_at(x, tok.y), -m), {-ls.hi, -ls.lo});
       const TokenLoss o = token_grad(a, tok, lp);
-      const double logp = to_double(lp);
-      float kl;
-      const double term = token_term(a, tok, logp, o.clipped, lane, &kl);
       if (lane == 0) {
-        write_token(a, row, o.clipped, logp, kl, term);
+        leave_logp(a, row, lp);
         sh_g = o.g;
         sh_ls = ls.hi + ls.lo;
       }
@@ -208,9 +183,8 @@ __global__ void __launch_bounds__(kRowThreads) policy_rows(const __grid_constant
 // ======================================================================================
 constexpr int kMaxCluster = 8;
 constexpr int kBufs = 3;                       // slices in shared memory
-constexpr int kSlice2 = 38000;                 // slice bytes with which two CTAs share an SM
-constexpr int kSliceMax = 76000;               // three slices in one CTA's shared memory
-constexpr int kSmallGranules = 512;            // slices up to here: 128 streaming threads
+constexpr int kSliceMax = 76000;               // bytes: three slices in one CTA's shared memory
+constexpr int kStream = 256;                   // streaming threads
 
 // How a row lies in memory: `head` logits before its first 16-byte granule, `nv` whole granules, then
 // the tail; granules [g0, g0 + n) are this CTA's.
@@ -255,12 +229,13 @@ __device__ __forceinline__ void join_lanes(float& m, Pair& s) {
   }
   m = M;
 }
+
 // Named barriers.  The streaming warps take the sums of row r + 1 before they wait for the gradient
 // of row r, so the parts of row r + 2 come behind the scalar warp's use of those of row r: two
-// ids (row parity).  Nothing holds the scalar and streaming warps back from running ahead of
-// the output warp but the copies that it issues: row r + 3 is requested behind its waits for row
-// r, and the rows at the end, which wait for no copy, are at most three: three ids.
-enum : uint32_t { kBarParts = 1, kBarG = 3, kBarEmpty = 5, kBarOut = 8, kBarCopy = 11 };
+// ids (row parity).  Nothing holds the streaming warps back from running ahead of the copy warp
+// but the copies that it issues: row r + 3 is requested behind its wait for row r, and the rows
+// at the end, which wait for no copy, are at most three: three ids.
+enum : uint32_t { kBarParts = 1, kBarG = 3, kBarEmpty = 5, kBarCopy = 8 };
 
 __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
@@ -280,8 +255,31 @@ __device__ __forceinline__ void cut_words(const uint32_t (&w)[8], bool odd, uint
     o[u] = odd ? __byte_perm(w[kFirst + u], w[kFirst + u + 1], 0x5432) : w[kFirst + u];
 }
 
-template <int kStream>
-__global__ void __launch_bounds__(kStream + 64, kStream == 256 ? 2 : 4)
+// n granules of a buffer to a row that does not start on a 16-byte boundary: its whole granules
+// are cut from two of the buffer's, its ends written one by one.  Threads tid of threads.
+__device__ __forceinline__ void shift_row(uint16_t* d, const uint4* buf, int n, int tid, int threads) {
+  if (n == 0) return;
+  const int off = static_cast<int>((16 - (reinterpret_cast<uintptr_t>(d) & 15)) & 15) / 2;   // 1 .. 7
+  const int nd = n - 1;
+  uint4* to = reinterpret_cast<uint4*>(d + off);
+  for (int i = tid; i < nd; i += threads) {
+    const uint4 p = buf[i], q = buf[i + 1];
+    const uint32_t w[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
+    uint32_t o[4];
+    switch (off >> 1) {
+      case 0: cut_words<0>(w, off & 1, o); break;
+      case 1: cut_words<1>(w, off & 1, o); break;
+      case 2: cut_words<2>(w, off & 1, o); break;
+      default: cut_words<3>(w, off & 1, o); break;
+    }
+    to[i] = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+  const uint16_t* h = reinterpret_cast<const uint16_t*>(buf);
+  if (tid < off) d[tid] = h[tid];
+  if (tid < 8 - off) d[off + 8 * nd + tid] = h[off + 8 * nd + tid];
+}
+
+__global__ void __launch_bounds__(kStream + 64, 2)
     policy_cluster(const __grid_constant__ PolicyArgs a, int cl, int per) {
   constexpr int kWarps = kStream / 32;
   constexpr int kThreads = kStream + 32;        // streaming warps and one other
@@ -290,8 +288,6 @@ __global__ void __launch_bounds__(kStream + 64, kStream == 256 ? 2 : 4)
   __shared__ float part[2][kWarps][3];         // a warp's maximum and sum (pair)
   __shared__ float slot[2][kMaxCluster][3];    // a CTA's, by rank
   __shared__ float sh_g[2], sh_c[2], sh_gy[2];
-  __shared__ float sh_logp[kBufs][2];          // for the output warp (pair)
-  __shared__ int sh_state[kBufs];                  // 0 left out, 1 used, 2 used and clipped, 3 aborted
   __shared__ int sh_used[kBufs], sh_y[2];
   // Set when a bounded wait of this CTA or of a peer gave up: rows are only walked through from
   // then on, with NaN terms and gradients of zero.
@@ -314,6 +310,7 @@ __global__ void __launch_bounds__(kStream + 64, kStream == 256 ? 2 : 4)
   }
   __syncthreads();
   if (cl > 1) cluster_sync_all();     // peers' barriers are ready before any remote arrival
+  reset_counter(a);
   pdl_launch_dependents();
 
   RowSpan sp = row_span(a, cid, per, rank);
@@ -345,8 +342,8 @@ __global__ void __launch_bounds__(kStream + 64, kStream == 256 ? 2 : 4)
     Ahead now = logits(cid, token(cid));
     Token next = token(cid + ncl);
     uint32_t ux = 0;                   // rows exchanged
-    int it = 0, b = 0;
-    for (int64_t row = cid; row < a.T; row += ncl, ++it, b = b == kBufs - 1 ? 0 : b + 1) {
+    int it = 0;
+    for (int64_t row = cid; row < a.T; row += ncl, ++it) {
       const int par = it & 1;
       const Token t = now.tok;
       const float xv = now.xy, ev = now.edge;
@@ -413,14 +410,14 @@ __global__ void __launch_bounds__(kStream + 64, kStream == 256 ? 2 : 4)
         sh_c[par] = c;
         sh_gy[par] = gy;
         sh_y[par] = t.used(a.V) ? t.y - sp.head : -1;
-        sh_logp[b][0] = logp.hi;
-        sh_logp[b][1] = logp.lo;
-        sh_state[b] = aborted ? 3 : (!t.used(a.V) ? 0 : (o.clipped ? 2 : 1));
       }
       __syncwarp();
       named_barrier_arrive(kBarG + par, kThreads);
-      named_barrier_arrive(kBarOut + b, 64);
       if (rank == 0) {
+        if (lane == 0 && t.used(a.V)) {
+          const float nan = __int_as_float(0x7fc00000);
+          leave_logp(a, row, aborted ? Pair{nan, nan} : logp);
+        }
         const int64_t e = edge_index(sp, a.V, lane);
         if (e >= 0) {
           float v = 0.0f;
@@ -431,9 +428,8 @@ __global__ void __launch_bounds__(kStream + 64, kStream == 256 ? 2 : 4)
       }
     }
   } else if (warp > kWarps) {
-    // ------------------------------------------------------------------ output warp
-    // Requests a row's slice as soon as a buffer is free (three rows ahead of the gradient), and
-    // writes the token's outputs, the loss term in fp64 (slow here) among them.
+    // -------------------------------------------------------------------- copy warp
+    // Requests a row's slice as soon as a buffer is free (three rows ahead of the gradient).
     auto request = [&](int64_t row, int b, const Token& t) {
       if (row >= a.T) return;
       const bool used = t.used(a.V);
@@ -455,39 +451,16 @@ __global__ void __launch_bounds__(kStream + 64, kStream == 256 ? 2 : 4)
       if (row < a.T) t = load_token(a, row);
       return t;
     };
-    Token t0 = token(cid), t1 = token(cid + ncl), t2 = token(cid + 2 * ncl), t3 = token(cid + 3 * ncl);
+    const Token t0 = token(cid), t1 = token(cid + ncl), t2 = token(cid + 2 * ncl);
+    Token next = token(cid + 3 * ncl);
     request(cid, 0, t0);
     request(cid + ncl, 1, t1);
     request(cid + 2 * ncl, 2, t2);
     int it = 0, b = 0;
     for (int64_t row = cid; row < a.T; row += ncl, ++it, b = b == kBufs - 1 ? 0 : b + 1) {
-      named_barrier_sync(kBarOut + b, 64);
-      const Pair lp2 = {sh_logp[b][0], sh_logp[b][1]};
-      const int state = sh_state[b];
-      __syncwarp();
       named_barrier_sync(kBarEmpty + b, kThreads);
-      request(row + kBufs * ncl, b, t3);
-      const Token t = t0;
-      t0 = t1;
-      t1 = t2;
-      t2 = t3;
-      t3 = token(row + (kBufs + 1) * ncl);
-      if (rank != 0) continue;
-      if (state == 0) {
-        if (lane == 0) {
-          if (t.bad(a.V)) set_device_status(a.status, DEV_BAD_INDEX);
-          write_no_token(a, row);
-        }
-        continue;
-      }
-      float kl;
-      double lp = to_double(lp2);
-      double term = token_term(a, t, lp, state == 2, lane, &kl);
-      if (state == 3) {
-        term = lp = __longlong_as_double(0x7ff8000000000000ll);
-        kl = static_cast<float>(lp);
-      }
-      if (lane == 0) write_token(a, row, state == 2, lp, kl, term);
+      request(row + kBufs * ncl, b, next);
+      next = token(row + (kBufs + 1) * ncl);
     }
     if (*vabort) {
       // copies still in flight land before the CTA may exit: the last request of each buffer
@@ -593,25 +566,7 @@ __global__ void __launch_bounds__(kStream + 64, kStream == 256 ? 2 : 4)
         // the gradient row lies at another offset from a 16-byte boundary: its granules are cut
         // from two of the buffer's
         named_barrier_sync(kBarCopy, kStream);
-        const int n = 8 * sp.n;
-        const int off = static_cast<int>((16 - (reinterpret_cast<uintptr_t>(d) & 15)) & 15) / 2;
-        const int nd = (n - off) >> 3;
-        uint4* to = reinterpret_cast<uint4*>(d + off);
-        for (int i = tid; i < nd; i += kStream) {
-          const uint4 p = buf[i], q = buf[i + 1];
-          const uint32_t w[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
-          uint32_t o[4];
-          switch (off >> 1) {
-            case 0: cut_words<0>(w, off & 1, o); break;
-            case 1: cut_words<1>(w, off & 1, o); break;
-            case 2: cut_words<2>(w, off & 1, o); break;
-            default: cut_words<3>(w, off & 1, o); break;
-          }
-          to[i] = make_uint4(o[0], o[1], o[2], o[3]);
-        }
-        const uint16_t* h = reinterpret_cast<const uint16_t*>(buf);
-        if (tid < off) d[tid] = h[tid];
-        if (tid < n - off - 8 * nd) d[off + 8 * nd + tid] = h[off + 8 * nd + tid];
+        shift_row(d, buf, sp.n, tid, kStream);
         // the next copy into this buffer comes behind the writes above
         fence_proxy_async_smem();
       }
@@ -623,28 +578,199 @@ __global__ void __launch_bounds__(kStream + 64, kStream == 256 ? 2 : 4)
   if (cl > 1) cluster_sync_all();
 }
 
-constexpr int kReduceThreads = 1024;
+// ======================================================================================
+// A warp a row, the row in registers
+// ======================================================================================
+constexpr int kWarpThreads = 256;
 
-__global__ void __launch_bounds__(kReduceThreads) policy_reduce(const double* terms, int64_t n,
-                                                               float* loss) {
-  __shared__ double sh[kReduceThreads / 32];
-  const int tid = threadIdx.x;
-  pdl_wait();
-  double acc = 0.0;
-  for (int64_t i = tid; i < n; i += kReduceThreads) acc += terms[i];
+// n granules of 16 bytes from registers (granule i in v[i / 32] of lane i % 32) to a row that is
+// aligned, or through the warp's shared memory to one that is not.
+template <int kG>
+__device__ __forceinline__ void store_row(uint16_t* d, const uint4 (&v)[kG], int n, uint4* buf, int lane) {
+  if ((reinterpret_cast<uintptr_t>(d) & 15) == 0) {
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
-  if ((tid & 31) == 0) sh[tid >> 5] = acc;
-  __syncthreads();
-  if (tid < 32) {
-    acc = sh[tid];
+    for (int k = 0; k < kG; ++k)
+      if (lane + 32 * k < n) __stcs(reinterpret_cast<uint4*>(d) + lane + 32 * k, v[k]);
+    return;
+  }
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
-    if (tid == 0) *loss = static_cast<float>(acc);
+  for (int k = 0; k < kG; ++k)
+    if (lane + 32 * k < n) buf[lane + 32 * k] = v[k];
+  __syncwarp();
+  shift_row(d, buf, n, lane, 32);
+  __syncwarp();
+}
+
+template <int kG>
+__global__ void __launch_bounds__(kWarpThreads, kG > 4 ? 2 : 4) policy_warp(const __grid_constant__ PolicyArgs a) {
+  extern __shared__ __align__(128) uint8_t dyn[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint4* buf = reinterpret_cast<uint4*>(dyn) + warp * 32 * kG;     // only for unaligned gradients
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * (kWarpThreads / 32);
+  const int64_t first = blockIdx.x * static_cast<int64_t>(kWarpThreads / 32) + warp;
+  reset_counter(a);
+  pdl_launch_dependents();
+  Token next = {0, 0.0f, 0.0f, 0.0f, 0.0f};
+  if (first < a.T) next = load_token(a, first);
+  const uint64_t l2 = f2_pack(kLog2e, kLog2e);
+  for (int64_t row = first; row < a.T; row += stride) {
+    const Token t = next;
+    if (row + stride < a.T) next = load_token(a, row + stride);
+    const RowSpan sp = row_span(a, row, 32 * kG, 0);
+    const uint16_t* x = a.logits + row * a.ldx;
+    uint16_t* d = a.dlogits + row * a.ldd;
+    const int64_t e = edge_index(sp, a.V, lane);
+    uint4 v[kG];
+    if (!t.used(a.V)) {
+#pragma unroll
+      for (int k = 0; k < kG; ++k) v[k] = make_uint4(0u, 0u, 0u, 0u);
+      store_row(d + sp.head, v, sp.n, buf, lane);
+      if (e >= 0) d[e] = 0;
+      continue;
+    }
+    const uint4* x4 = reinterpret_cast<const uint4*>(x + sp.head);
+#pragma unroll
+    for (int k = 0; k < kG; ++k)
+      v[k] = lane + 32 * k < sp.n ? __ldcs(x4 + lane + 32 * k)
+                                  : make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);
+    const float xy = bf16_at(x, t.y);
+    const float ev = e >= 0 ? bf16_at(x, e) : -INFINITY;
+    float m = ev;
+#pragma unroll
+    for (int k = 0; k < kG; ++k) m = fmaxf(m, granule_max(v[k]));
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    const float base = m == -INFINITY ? 0.0f : -m;
+    const uint64_t nb = f2_pack(base, base);
+    uint64_t acc[4] = {f2_pack(ex2_approx((ev + base) * kLog2e), 0.0f), 0ull, 0ull, 0ull};
+#pragma unroll
+    for (int k = 0; k < kG; ++k) {
+      const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        float e0, e1;
+        f2_unpack(f2_mul(f2_add(f2_pack(lo_bf16(w[u]), hi_bf16(w[u])), nb), l2), e0, e1);
+        acc[u] = f2_add(acc[u], f2_pack(ex2_approx(e0), ex2_approx(e1)));
+      }
+    }
+    float s0, s1;
+    f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), s0, s1);
+    Pair s = two_sum(s0, s1);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+      s = pair_add(s, {__shfl_xor_sync(0xffffffffu, s.hi, off), __shfl_xor_sync(0xffffffffu, s.lo, off)});
+    const Pair ls = log_pair(s);
+    const Pair logp = pair_add(two_sum(xy, -m), {-ls.hi, -ls.lo});
+    const TokenLoss o = token_grad(a, t, logp);
+    if (lane == 0) leave_logp(a, row, logp);
+    const float c = fmaf(-(m + (ls.hi + ls.lo)), kLog2e, log2f(fabsf(o.g)));
+    const float gy = o.g * (1.0f - ex2_approx((logp.hi + logp.lo) * kLog2e));
+    const uint32_t sign = o.g > 0.0f ? 0x80008000u : 0u;
+    const uint64_t c2 = f2_pack(c, c);
+#pragma unroll
+    for (int k = 0; k < kG; ++k) {
+      const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+      uint32_t r[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        float e0, e1;
+        f2_unpack(f2_fma(f2_pack(lo_bf16(w[u]), hi_bf16(w[u])), l2, c2), e0, e1);
+        r[u] = o.g == 0.0f ? 0u : pack_bf16x2(ex2_approx(e0), ex2_approx(e1)) ^ sign;
+      }
+      v[k] = make_uint4(r[0], r[1], r[2], r[3]);
+    }
+    store_row(d + sp.head, v, sp.n, buf, lane);
+    if (e >= 0) {
+      float w = 0.0f;
+      if (o.g != 0.0f) w = copysignf(ex2_approx(fmaf(ev, kLog2e, c)), -o.g);
+      if (o.g != o.g) w = o.g;
+      d[e] = to_bf16(w);
+    }
+    // the sampled token's column, behind the lane's own store of its granule
+    __syncwarp();
+    if (lane == 0 && o.g != 0.0f) d[t.y] = to_bf16(gy);
   }
 }
 
-template <int kStream>
+// ======================================================================================
+// The tokens' outputs and the loss
+// ======================================================================================
+constexpr int kFinishThreads = 128;
+
+__global__ void __launch_bounds__(kFinishThreads) policy_finish(const __grid_constant__ PolicyArgs a) {
+  __shared__ double sh[kFinishThreads / 32];
+  __shared__ unsigned sh_last;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_wait();
+  double sum = 0.0;
+  for (int64_t row = blockIdx.x * static_cast<int64_t>(kFinishThreads) + tid; row < a.T;
+       row += static_cast<int64_t>(gridDim.x) * kFinishThreads) {
+    const Token t = load_token(a, row);
+    float logp_out = 0.0f, kl_out = 0.0f;
+    bool clipped = false;
+    if (t.bad(a.V)) set_device_status(a.status, DEV_BAD_INDEX);
+    if (t.used(a.V)) {
+      const float2 p = __ldcg(a.logp_pair + row);
+      const Pair lp = {p.x, p.y};
+      clipped = token_grad(a, t, lp).clipped;
+      const double logp = static_cast<double>(p.x) + static_cast<double>(p.y);
+      const double A = t.A, r = logp - static_cast<double>(t.ref);
+      const double surr = clipped ? (A > 0.0 ? a.clip_hi : a.clip_lo) * A
+                                  : exp(logp - static_cast<double>(t.old)) * A;
+      double kl = 0.0;
+      if (a.ref != nullptr) kl = a.kl == 1 ? r : (a.kl == 2 ? 0.5 * r * r : expm1(-r) + r);
+      sum += static_cast<double>(t.w) * (a.beta * kl - surr);
+      logp_out = static_cast<float>(logp);
+      kl_out = static_cast<float>(kl);
+    }
+    a.clip_mask[row] = clipped ? 1 : 0;
+    if (a.logp_out != nullptr) a.logp_out[row] = logp_out;
+    if (a.kl_out != nullptr) a.kl_out[row] = kl_out;
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+  if (lane == 0) sh[warp] = sum;
+  __syncthreads();
+  if (tid == 0) {
+    for (int w = 1; w < kFinishThreads / 32; ++w) sum += sh[w];
+    a.partial[blockIdx.x] = sum;
+    __threadfence();
+    sh_last = atomicAdd(a.counter, 1u) == gridDim.x - 1 ? 1u : 0u;
+  }
+  __syncthreads();
+  // the last block adds the blocks' sums in their order: the same result whichever block it is
+  if (!sh_last || warp > 0) return;
+  __threadfence();
+  sum = 0.0;
+  for (int i = lane; i < static_cast<int>(gridDim.x); i += 32) sum += __ldcg(a.partial + i);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+  if (lane == 0) *a.loss = static_cast<float>(sum);
+}
+
+template <int kG>
+cudaError_t launch_warp(const PolicyArgs& a, cudaStream_t s) {
+  constexpr int kRows = kWarpThreads / 32;
+  // the shifting buffer only where some gradient row is not aligned as its logits are
+  const bool shift = (a.ldx - a.ldd) % 8 != 0 ||
+                     (reinterpret_cast<uintptr_t>(a.logits) - reinterpret_cast<uintptr_t>(a.dlogits)) % 16 != 0;
+  const int smem = shift ? kRows * 32 * kG * 16 : 0;
+  static bool attr_set[kMaxDeviceCache] = {};
+  const int dev = cached_device_index();
+  if (dev < 0) return cudaErrorInvalidDevice;
+  if (!attr_set[dev]) {
+    cudaError_t e = cudaFuncSetAttribute(policy_warp<kG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kRows * 32 * kG * 16);
+    if (e != cudaSuccess) return e;
+    attr_set[dev] = true;
+  }
+  int64_t grid = (a.T + kRows - 1) / kRows;
+  const int64_t most = static_cast<int64_t>(num_sms()) * 8;
+  if (grid > most) grid = most;
+  policy_warp<kG><<<static_cast<unsigned>(grid), kWarpThreads, static_cast<size_t>(smem), s>>>(a);
+  return cudaGetLastError();
+}
+
 cudaError_t launch_cluster(const PolicyArgs& a, int cl, int per, cudaStream_t s) {
   constexpr int kThreads = kStream + 64;
   const int smem = kBufs * per * 16;
@@ -652,7 +778,7 @@ cudaError_t launch_cluster(const PolicyArgs& a, int cl, int per, cudaStream_t s)
   const int dev = cached_device_index();
   if (dev < 0) return cudaErrorInvalidDevice;
   if (!attr_set[dev]) {
-    cudaError_t e = cudaFuncSetAttribute(policy_cluster<kStream>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e = cudaFuncSetAttribute(policy_cluster, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          kBufs * kSliceMax);
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
@@ -677,12 +803,12 @@ cudaError_t launch_cluster(const PolicyArgs& a, int cl, int per, cudaStream_t s)
     n = static_cast<int>(seen & 0xFFFFFF);
   } else if (cl > 1) {
     cfg.gridDim = dim3(static_cast<unsigned>(num_sms() * cl), 1, 1);
-    if (cudaOccupancyMaxActiveClusters(&n, policy_cluster<kStream>, &cfg) != cudaSuccess || n <= 0) {
+    if (cudaOccupancyMaxActiveClusters(&n, policy_cluster, &cfg) != cudaSuccess || n <= 0) {
       (void)cudaGetLastError();
       n = num_sms() / cl;
     }
   } else {
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, policy_cluster<kStream>, kThreads,
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, policy_cluster, kThreads,
                                                       static_cast<size_t>(smem)) != cudaSuccess || n <= 0) {
       (void)cudaGetLastError();
       n = 1;
@@ -692,30 +818,38 @@ cudaError_t launch_cluster(const PolicyArgs& a, int cl, int per, cudaStream_t s)
   memo[dev].store(key | static_cast<uint64_t>(n));
   if (n > a.T) n = static_cast<int>(a.T);
   cfg.gridDim = dim3(static_cast<unsigned>(n * cl), 1, 1);
-  return cudaLaunchKernelEx(&cfg, policy_cluster<kStream>, a, cl, per);
+  return cudaLaunchKernelEx(&cfg, policy_cluster, a, cl, per);
 }
 
 }  // namespace
 
 cudaError_t launch_policy_loss(const PolicyArgs& a, cudaStream_t s) {
-  // the fewest CTAs a row whose slices let two of them share an SM
   const int64_t granules = (a.V + 7) / 8;
-  int cl = 1;
-  while (cl < kMaxCluster && (granules + cl - 1) / cl * 16 > kSlice2) cl *= 2;
-  int64_t per = (granules + cl - 1) / cl;
-  if (per < 1) per = 1;
   cudaError_t e;
-  if (per * 16 <= kSliceMax) {
-    e = per <= kSmallGranules ? launch_cluster<128>(a, cl, static_cast<int>(per), s)
-                              : launch_cluster<256>(a, cl, static_cast<int>(per), s);
+  if (a.V <= 1024) {
+    e = launch_warp<4>(a, s);
+  } else if (a.V <= 2048) {
+    e = launch_warp<8>(a, s);
+  } else if (a.V <= 4096) {
+    e = launch_warp<16>(a, s);
   } else {
-    int64_t grid = static_cast<int64_t>(num_sms()) * 4;
-    if (grid > a.T) grid = a.T;
-    policy_rows<<<static_cast<unsigned>(grid), kRowThreads, 0, s>>>(a);
-    e = cudaGetLastError();
+    // the fewest CTAs a row
+    int cl = 1;
+    while (cl < kMaxCluster && (granules + cl - 1) / cl * 16 > kSliceMax) cl *= 2;
+    const int64_t per = (granules + cl - 1) / cl;
+    if (per * 16 <= kSliceMax) {
+      e = launch_cluster(a, cl, static_cast<int>(per), s);
+    } else {
+      int64_t grid = static_cast<int64_t>(num_sms()) * 4;
+      if (grid > a.T) grid = a.T;
+      policy_rows<<<static_cast<unsigned>(grid), kRowThreads, 0, s>>>(a);
+      e = cudaGetLastError();
+    }
   }
   if (e != cudaSuccess) return e;
-  return launch_after(policy_reduce, dim3(1), kReduceThreads, 0, s, static_cast<const double*>(a.terms), a.T, a.loss);
+  int64_t grid = (a.T + kFinishThreads - 1) / kFinishThreads;
+  if (grid > kMaxPartials) grid = kMaxPartials;
+  return launch_after(policy_finish, dim3(static_cast<unsigned>(grid)), kFinishThreads, 0, s, a);
 }
 
 }  // namespace ls

@@ -9,9 +9,10 @@
 // range reduction on the device.  A block computes the cosines and sines of its tokens once, in
 // shared memory, and every head of the token uses them.
 //
-// Bound by HBM: 2 bytes read and 2 written a value.  Vector path: 16-byte accesses, eight
-// pairs of the half layout (or four interleaved ones) an item.  Element path for rows that are
-// not 16-byte aligned or rot_dim not a multiple of 16 (8 interleaved).
+// Bound by HBM: 2 bytes read and 2 written a value.  Vector path: 16-byte accesses, four in flight
+// a thread; a thread keeps its place in the head and walks the heads of the block's tokens.
+// Element path for rows that are not 16-byte aligned or rot_dim not a multiple of 16 (8
+// interleaved).
 #include "ls_internal.h"
 #include "ls_ops.h"
 #include "ptx.cuh"
@@ -20,7 +21,9 @@ namespace ls {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxTok = 8;      // tokens of a block
+constexpr int kMaxTok = 32;     // tokens of a block at most
+constexpr int kBlocks = 4;      // blocks of an SM
+constexpr int kFly = 4;         // items of a thread in flight
 
 __device__ __forceinline__ float bf(uint32_t w, int hi) {
   return __uint_as_float(hi ? (w & 0xFFFF0000u) : (w << 16));
@@ -86,9 +89,83 @@ __device__ __forceinline__ Place place_of(const RopeArgs& a, int64_t t, int h, i
   return p;
 }
 
+// Walks the (token, head) pairs of a block, `step` heads at a time: no divisions in the loop.
+struct Walk {
+  int tok, head;
+  __device__ __forceinline__ void next(int step, int H) {
+    head += step;
+    while (head >= H) {
+      head -= H;
+      ++tok;
+    }
+  }
+};
+
+// One 16-byte chunk (kPair: chunk c of the first half with its partner in the second) of kFly heads
+// at a time, loads first.  kTurn: rotated by the chunk's angles; else copied.
+template <bool kTurn, bool kPair>
+__device__ __forceinline__ void chunks(const RopeArgs& a, const Token* tok, const float2* cs, int64_t t0, int nt,
+                                       int h_first, int h_count, int c, int partner, int first, int step) {
+  const int half = a.rot >> 1;
+  Walk w = {0, first};
+  w.next(0, h_count);
+  while (w.tok < nt) {
+    uint4 x[kFly], y[kFly];
+    uint16_t* dst[kFly];
+    int at[kFly];
+#pragma unroll
+    for (int f = 0; f < kFly; ++f) {
+      at[f] = -1;
+      dst[f] = nullptr;
+      if (w.tok < nt) {
+        const int64_t page = tok[w.tok].page;
+        const Place p = place_of(a, t0 + w.tok, h_first + w.head, page);
+        if (page >= 0 && (kTurn || p.src != p.dst)) {
+          at[f] = w.tok;
+          dst[f] = p.dst + c;
+          x[f] = __ldcs(reinterpret_cast<const uint4*>(p.src + c));
+          if (kPair) y[f] = __ldcs(reinterpret_cast<const uint4*>(p.src + c + partner));
+        }
+        w.next(step, h_count);
+      }
+    }
+#pragma unroll
+    for (int f = 0; f < kFly; ++f) {
+      if (at[f] < 0) continue;
+      if constexpr (!kTurn) {
+        *reinterpret_cast<uint4*>(dst[f]) = x[f];
+      } else if constexpr (kPair) {
+        const float4* t = reinterpret_cast<const float4*>(cs + at[f] * half + c);
+        const uint32_t wx[4] = {x[f].x, x[f].y, x[f].z, x[f].w}, wy[4] = {y[f].x, y[f].y, y[f].z, y[f].w};
+        uint32_t ox[4], oy[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const float4 r = t[u];        // cos, sin of two pairs
+          const float x0 = bf(wx[u], 0), x1 = bf(wx[u], 1), y0 = bf(wy[u], 0), y1 = bf(wy[u], 1);
+          ox[u] = pack_bf16x2(x0 * r.x - y0 * r.y, x1 * r.z - y1 * r.w);
+          oy[u] = pack_bf16x2(y0 * r.x + x0 * r.y, y1 * r.z + x1 * r.w);
+        }
+        *reinterpret_cast<uint4*>(dst[f]) = make_uint4(ox[0], ox[1], ox[2], ox[3]);
+        *reinterpret_cast<uint4*>(dst[f] + partner) = make_uint4(oy[0], oy[1], oy[2], oy[3]);
+      } else {
+        const float2* t = cs + at[f] * half + (c >> 1);
+        const uint32_t wx[4] = {x[f].x, x[f].y, x[f].z, x[f].w};
+        uint32_t o[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const float2 r = t[u];
+          const float x0 = bf(wx[u], 0), y0 = bf(wx[u], 1);
+          o[u] = pack_bf16x2(x0 * r.x - y0 * r.y, y0 * r.x + x0 * r.y);
+        }
+        *reinterpret_cast<uint4*>(dst[f]) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+    }
+  }
+}
+
 template <bool kVec>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a, int tb) {
-  __shared__ float2 cs[kMaxTok][kMaxRot];
+__global__ void __launch_bounds__(kThreads, kBlocks) rope_kernel(const __grid_constant__ RopeArgs a, int tb) {
+  extern __shared__ __align__(16) float2 cs[];      // [token][pair]: cosine, sine
   __shared__ Token tok[kMaxTok];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int half = a.rot >> 1;
@@ -112,68 +189,32 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     const float x = static_cast<float>(static_cast<int32_t>(turn >> 32)) * 4.656612873077393e-10f;
     float s, c;
     sincospif(x, &s, &c);
-    cs[k][p] = make_float2(c * a.factor, (a.inverse ? -s : s) * a.factor);
+    cs[i] = make_float2(c * a.factor, (a.inverse ? -s : s) * a.factor);
   }
   __syncthreads();
 
   const int H = a.Hq + a.Hk + (a.append ? a.Hk : 0);
   const int Hr = a.rot > 0 ? a.Hq + a.Hk : 0;       // heads that are rotated
   if constexpr (kVec) {
+    // A thread keeps its chunk of a head and walks the heads: rotated chunks (pairs of them in
+    // the half layout) and the copied rest of the rotated heads, then the heads that are copied.
     const int n8 = a.D / 8;
     const int nr = a.interleaved ? a.rot / 8 : a.rot / 16;
-    const int per = Hr * (nr + (a.D - a.rot) / 8) + (H - Hr) * n8;
-    for (int i = tid; i < nt * per; i += kThreads) {
-      const int k = i / per;
-      int j = i - k * per;
-      const int64_t page = tok[k].page;
-      if (page < 0) continue;
-      const int rot_items = Hr * nr;
-      if (j < rot_items) {
-        const int h = j / nr, c = j - h * nr;
-        const Place p = place_of(a, t0 + k, h, page);
-        if (a.interleaved) {
-          const uint4 v = *reinterpret_cast<const uint4*>(p.src + 8 * c);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-          uint32_t o[4];
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const float2 t = cs[k][4 * c + u];
-            const float x = bf(w[u], 0), y = bf(w[u], 1);
-            o[u] = pack_bf16x2(x * t.x - y * t.y, y * t.x + x * t.y);
-          }
-          *reinterpret_cast<uint4*>(p.dst + 8 * c) = make_uint4(o[0], o[1], o[2], o[3]);
-        } else {
-          const uint4 vx = *reinterpret_cast<const uint4*>(p.src + 8 * c);
-          const uint4 vy = *reinterpret_cast<const uint4*>(p.src + half + 8 * c);
-          const uint32_t wx[4] = {vx.x, vx.y, vx.z, vx.w}, wy[4] = {vy.x, vy.y, vy.z, vy.w};
-          uint32_t ox[4], oy[4];
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const float2 t0v = cs[k][8 * c + 2 * u], t1v = cs[k][8 * c + 2 * u + 1];
-            const float x0 = bf(wx[u], 0), x1 = bf(wx[u], 1), y0 = bf(wy[u], 0), y1 = bf(wy[u], 1);
-            ox[u] = pack_bf16x2(x0 * t0v.x - y0 * t0v.y, x1 * t1v.x - y1 * t1v.y);
-            oy[u] = pack_bf16x2(y0 * t0v.x + x0 * t0v.y, y1 * t1v.x + x1 * t1v.y);
-          }
-          *reinterpret_cast<uint4*>(p.dst + 8 * c) = make_uint4(ox[0], ox[1], ox[2], ox[3]);
-          *reinterpret_cast<uint4*>(p.dst + half + 8 * c) = make_uint4(oy[0], oy[1], oy[2], oy[3]);
-        }
-        continue;
+    const int per = nr + (a.D - a.rot) / 8;
+    if (Hr > 0) {
+      const int groups = kThreads / per, first = tid / per, j = tid - first * per;
+      if (first < groups) {
+        if (j >= nr)
+          chunks<false, false>(a, tok, cs, t0, nt, 0, Hr, a.rot + 8 * (j - nr), 0, first, groups);
+        else if (a.interleaved)
+          chunks<true, false>(a, tok, cs, t0, nt, 0, Hr, 8 * j, 0, first, groups);
+        else
+          chunks<true, true>(a, tok, cs, t0, nt, 0, Hr, 8 * j, half, first, groups);
       }
-      j -= rot_items;
-      // values behind the rotated part, then the heads that are only copied
-      const int np = (a.D - a.rot) / 8;
-      int h, c;
-      if (j < Hr * np) {
-        h = j / np;
-        c = a.rot / 8 + (j - h * np);
-      } else {
-        j -= Hr * np;
-        h = Hr + j / n8;
-        c = j - (h - Hr) * n8;
-      }
-      const Place p = place_of(a, t0 + k, h, page);
-      if (p.src != p.dst)
-        *reinterpret_cast<uint4*>(p.dst + 8 * c) = *reinterpret_cast<const uint4*>(p.src + 8 * c);
+    }
+    if (H > Hr) {
+      const int groups = kThreads / n8, first = tid / n8, j = tid - first * n8;
+      if (first < groups) chunks<false, false>(a, tok, cs, t0, nt, Hr, H - Hr, 8 * j, 0, first, groups);
     }
   } else {
     // element path: pair items, then single values
@@ -187,7 +228,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
         const int h = j / half, c = j - h * half;
         const Place p = place_of(a, t0 + k, h, page);
         const int ix = a.interleaved ? 2 * c : c, iy = a.interleaved ? 2 * c + 1 : c + half;
-        const float2 t = cs[k][c];
+        const float2 t = cs[k * half + c];
         const float x = bf(p.src[ix], 0), y = bf(p.src[iy], 0);
         p.dst[ix] = to_bf16(x * t.x - y * t.y);
         p.dst[iy] = to_bf16(y * t.x + x * t.y);
@@ -224,14 +265,16 @@ cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s) {
     vec = vec && vec_ok(a.v, a.vs);   // pages are 16-byte aligned
   else if (a.Hk > 0)
     vec = vec && vec_ok(a.ko, a.kos);
-  // a few tokens a block once there are enough of them to fill the GPU
-  int tb = static_cast<int>(a.T / (static_cast<int64_t>(num_sms()) * 8));
-  tb = tb < 1 ? 1 : (tb > kMaxTok ? kMaxTok : tb);
+  // one wave of blocks, however many tokens each takes
+  const int64_t wave = static_cast<int64_t>(num_sms()) * kBlocks;
+  int64_t tb = (a.T + wave - 1) / wave;
+  if (tb > kMaxTok) tb = kMaxTok;
   const unsigned grid = static_cast<unsigned>((a.T + tb - 1) / tb);
+  const size_t smem = static_cast<size_t>(tb) * (a.rot / 2) * sizeof(float2);
   if (vec)
-    rope_kernel<true><<<grid, kThreads, 0, s>>>(a, tb);
+    rope_kernel<true><<<grid, kThreads, smem, s>>>(a, static_cast<int>(tb));
   else
-    rope_kernel<false><<<grid, kThreads, 0, s>>>(a, tb);
+    rope_kernel<false><<<grid, kThreads, smem, s>>>(a, static_cast<int>(tb));
   return cudaGetLastError();
 }
 

@@ -16,7 +16,7 @@ extern "C" {
 
 size_t ls_policy_loss_workspace_bytes(int64_t T) {
   if (T < 1) return 0;
-  return align_up(static_cast<size_t>(T) * sizeof(double), 256);
+  return align_up(static_cast<size_t>(T) * sizeof(float2), 256) + kMaxPartials * sizeof(double) + 256;
 }
 
 ls_status ls_policy_loss(const ls_policy_loss_desc* d, void* workspace, size_t workspace_bytes,
@@ -73,7 +73,11 @@ ls_status ls_policy_loss(const ls_policy_loss_desc* d, void* workspace, size_t w
   a.clip_mask = d->clip_mask;
   a.logp_out = d->logp_out;
   a.kl_out = d->kl_out;
-  a.terms = static_cast<double*>(workspace);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.logp_pair = reinterpret_cast<float2*>(ws);
+  ws += align_up(static_cast<size_t>(d->T) * sizeof(float2), 256);
+  a.partial = reinterpret_cast<double*>(ws);
+  a.counter = reinterpret_cast<unsigned*>(ws + kMaxPartials * sizeof(double));
   a.status = status;
   cudaError_t e;
   {

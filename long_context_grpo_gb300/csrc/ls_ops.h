@@ -26,9 +26,12 @@ struct PolicyArgs {
   uint8_t* clip_mask;
   float* logp_out;            // or nullptr
   float* kl_out;              // or nullptr
-  double* terms;              // workspace [T]
+  float2* logp_pair;          // workspace [T]: log-probabilities as sums of two
+  double* partial;            // workspace [kMaxPartials]
+  unsigned* counter;          // workspace
   uint32_t* status;
 };
+constexpr int kMaxPartials = 512;
 cudaError_t launch_policy_loss(const PolicyArgs& a, cudaStream_t s);
 
 // ----- paged cache

@@ -43,7 +43,7 @@ def _check(r, o, w, eps_low, eps_high):
 
 
 SHAPES = [(1, 1, 0), (3, 7, 0), (5, 31, 1), (17, 1024, 0), (33, 1001, 3), (9, 4096, 8), (300, 264, 0), (4, 32000, 0),
-          (3, 50257, 7), (2, 151936, 64), (2, 151937, 0), (1, 200000, 0)]
+          (3, 50257, 7), (2, 151936, 64), (2, 151937, 0), (1, 200000, 0), (700, 1000, 1), (300, 4093, 2), (5, 38001, 1), (1, 310001, 0)]
 
 
 @pytest.mark.gpu
