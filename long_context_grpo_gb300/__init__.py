@@ -18,5 +18,6 @@ def __getattr__(name):
         return getattr(_lib, name)
     if name in _OPS:
         from . import _ops
-        return getattr(_ops, name)
+        globals()[name] = getattr(_ops, name)      # found without this function from now on
+        return globals()[name]
     raise AttributeError(name)

@@ -9,8 +9,9 @@
 // range reduction on the device.  A block computes the cosines and sines of its tokens once, in
 // shared memory, and every head of the token uses them.
 //
-// Bound by HBM: 2 bytes read and 2 written a value.  Vector path: 16-byte accesses, four in flight
-// a thread; a thread keeps its place in the head and walks the heads of the block's tokens.
+// Bound by HBM: 2 bytes read and 2 written a value.  Vector path: 16-byte accesses; a thread
+// keeps its place in the head and walks the heads of the block's tokens (two or four accesses in
+// flight a thread, with fewer blocks an SM, measured slower: 98 us and more against 92).
 // Element path for rows that are not 16-byte aligned or rot_dim not a multiple of 16 (8
 // interleaved).
 #include "ls_internal.h"
@@ -21,9 +22,8 @@ namespace ls {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxTok = 32;     // tokens of a block at most
-constexpr int kBlocks = 4;      // blocks of an SM
-constexpr int kFly = 4;         // items of a thread in flight
+constexpr int kMaxTok = 2;      // tokens of a block at most
+constexpr int kBlocks = 8;      // blocks of an SM
 
 __device__ __forceinline__ float bf(uint32_t w, int hi) {
   return __uint_as_float(hi ? (w & 0xFFFF0000u) : (w << 16));
@@ -101,64 +101,47 @@ struct Walk {
   }
 };
 
-// One 16-byte chunk (kPair: chunk c of the first half with its partner in the second) of kFly heads
-// at a time, loads first.  kTurn: rotated by the chunk's angles; else copied.
+// One 16-byte chunk (kPair: chunk c of the first half with its partner in the second) of the heads
+// that this thread walks.  kTurn: rotated by the chunk's angles; else copied.
 template <bool kTurn, bool kPair>
 __device__ __forceinline__ void chunks(const RopeArgs& a, const Token* tok, const float2* cs, int64_t t0, int nt,
                                        int h_first, int h_count, int c, int partner, int first, int step) {
   const int half = a.rot >> 1;
   Walk w = {0, first};
-  w.next(0, h_count);
-  while (w.tok < nt) {
-    uint4 x[kFly], y[kFly];
-    uint16_t* dst[kFly];
-    int at[kFly];
+  for (w.next(0, h_count); w.tok < nt; w.next(step, h_count)) {
+    const int64_t page = tok[w.tok].page;
+    if (page < 0) continue;
+    const Place p = place_of(a, t0 + w.tok, h_first + w.head, page);
+    if (!kTurn && p.src == p.dst) continue;
+    const uint4 x = *reinterpret_cast<const uint4*>(p.src + c);
+    if constexpr (!kTurn) {
+      *reinterpret_cast<uint4*>(p.dst + c) = x;
+    } else if constexpr (kPair) {
+      const uint4 y = *reinterpret_cast<const uint4*>(p.src + c + partner);
+      const float4* t = reinterpret_cast<const float4*>(cs + w.tok * half + c);
+      const uint32_t wx[4] = {x.x, x.y, x.z, x.w}, wy[4] = {y.x, y.y, y.z, y.w};
+      uint32_t ox[4], oy[4];
 #pragma unroll
-    for (int f = 0; f < kFly; ++f) {
-      at[f] = -1;
-      dst[f] = nullptr;
-      if (w.tok < nt) {
-        const int64_t page = tok[w.tok].page;
-        const Place p = place_of(a, t0 + w.tok, h_first + w.head, page);
-        if (page >= 0 && (kTurn || p.src != p.dst)) {
-          at[f] = w.tok;
-          dst[f] = p.dst + c;
-          x[f] = __ldcs(reinterpret_cast<const uint4*>(p.src + c));
-          if (kPair) y[f] = __ldcs(reinterpret_cast<const uint4*>(p.src + c + partner));
-        }
-        w.next(step, h_count);
+      for (int u = 0; u < 4; ++u) {
+        const float4 r = t[u];        // cos, sin of two pairs
+        const float x0 = bf(wx[u], 0), x1 = bf(wx[u], 1), y0 = bf(wy[u], 0), y1 = bf(wy[u], 1);
+        ox[u] = pack_bf16x2(x0 * r.x - y0 * r.y, x1 * r.z - y1 * r.w);
+        oy[u] = pack_bf16x2(y0 * r.x + x0 * r.y, y1 * r.z + x1 * r.w);
       }
-    }
+      *reinterpret_cast<uint4*>(p.dst + c) = make_uint4(ox[0], ox[1], ox[2], ox[3]);
+      *reinterpret_cast<uint4*>(p.dst + c + partner) = make_uint4(oy[0], oy[1], oy[2], oy[3]);
+    } else {
+      const float4* t = reinterpret_cast<const float4*>(cs + w.tok * half + (c >> 1));
+      const uint32_t wx[4] = {x.x, x.y, x.z, x.w};
+      uint32_t o[4];
 #pragma unroll
-    for (int f = 0; f < kFly; ++f) {
-      if (at[f] < 0) continue;
-      if constexpr (!kTurn) {
-        *reinterpret_cast<uint4*>(dst[f]) = x[f];
-      } else if constexpr (kPair) {
-        const float4* t = reinterpret_cast<const float4*>(cs + at[f] * half + c);
-        const uint32_t wx[4] = {x[f].x, x[f].y, x[f].z, x[f].w}, wy[4] = {y[f].x, y[f].y, y[f].z, y[f].w};
-        uint32_t ox[4], oy[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const float4 r = t[u];        // cos, sin of two pairs
-          const float x0 = bf(wx[u], 0), x1 = bf(wx[u], 1), y0 = bf(wy[u], 0), y1 = bf(wy[u], 1);
-          ox[u] = pack_bf16x2(x0 * r.x - y0 * r.y, x1 * r.z - y1 * r.w);
-          oy[u] = pack_bf16x2(y0 * r.x + x0 * r.y, y1 * r.z + x1 * r.w);
-        }
-        *reinterpret_cast<uint4*>(dst[f]) = make_uint4(ox[0], ox[1], ox[2], ox[3]);
-        *reinterpret_cast<uint4*>(dst[f] + partner) = make_uint4(oy[0], oy[1], oy[2], oy[3]);
-      } else {
-        const float2* t = cs + at[f] * half + (c >> 1);
-        const uint32_t wx[4] = {x[f].x, x[f].y, x[f].z, x[f].w};
-        uint32_t o[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const float2 r = t[u];
-          const float x0 = bf(wx[u], 0), y0 = bf(wx[u], 1);
-          o[u] = pack_bf16x2(x0 * r.x - y0 * r.y, y0 * r.x + x0 * r.y);
-        }
-        *reinterpret_cast<uint4*>(dst[f]) = make_uint4(o[0], o[1], o[2], o[3]);
+      for (int u = 0; u < 2; ++u) {
+        const float4 r = t[u];
+        const float x0 = bf(wx[2 * u], 0), y0 = bf(wx[2 * u], 1), x1 = bf(wx[2 * u + 1], 0), y1 = bf(wx[2 * u + 1], 1);
+        o[2 * u] = pack_bf16x2(x0 * r.x - y0 * r.y, y0 * r.x + x0 * r.y);
+        o[2 * u + 1] = pack_bf16x2(x1 * r.z - y1 * r.w, y1 * r.z + x1 * r.w);
       }
+      *reinterpret_cast<uint4*>(p.dst + c) = make_uint4(o[0], o[1], o[2], o[3]);
     }
   }
 }
@@ -265,10 +248,9 @@ cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s) {
     vec = vec && vec_ok(a.v, a.vs);   // pages are 16-byte aligned
   else if (a.Hk > 0)
     vec = vec && vec_ok(a.ko, a.kos);
-  // one wave of blocks, however many tokens each takes
-  const int64_t wave = static_cast<int64_t>(num_sms()) * kBlocks;
-  int64_t tb = (a.T + wave - 1) / wave;
-  if (tb > kMaxTok) tb = kMaxTok;
+  // two tokens share a block's prologue once that leaves four waves of blocks (14,000 tokens
+  // appended: 92 us, with one 103; 3,000 rotated: 19 us either way)
+  const int64_t tb = a.T >= static_cast<int64_t>(num_sms()) * kBlocks * 4 * kMaxTok ? kMaxTok : 1;
   const unsigned grid = static_cast<unsigned>((a.T + tb - 1) / tb);
   const size_t smem = static_cast<size_t>(tb) * (a.rot / 2) * sizeof(float2);
   if (vec)
