@@ -57,7 +57,7 @@ struct Seg {
   int key_end;      // keys from here on are not read
   int chunk, chunks;
   int part;         // first row of its partial results; -1: written to the output
-  int pad[2];
+  int jobs, rows;   // jobs and partial rows of it (planning); a group's shared length before that
 };
 // One (key head, chunk) of a segment, for one Q tile (narrow) or two (wide).
 struct Job {
@@ -82,33 +82,15 @@ __device__ __forceinline__ int tiles_of(const Seg& s, int t_end) {
   return n < s.tiles ? n : s.tiles;
 }
 
-// (not inlined: the planning kernel runs once through its code, so its size is its time)
-__device__ __noinline__ int plan_scan(int v, int* sh, int* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int s = v;
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int u = __shfl_up_sync(0xffffffffu, s, off);
-    if (lane >= off) s += u;
-  }
-  __syncthreads();
-  if (lane == 31) sh[warp] = s;
-  __syncthreads();
-  if (warp == 0) {
-    int w = sh[lane];
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, w, off);
-      if (lane >= off) w += u;
-    }
-    sh[lane] = w;
-  }
-  __syncthreads();
-  *total = sh[31];
-  return (warp > 0 ? sh[warp - 1] : 0) + s - v;
+// x / d for 0 <= x < 2^24, inv = 1 / d (an integer division takes a hundred cycles).
+__device__ __forceinline__ int quick_div(int x, int d, float inv) {
+  int q = static_cast<int>(static_cast<float>(x) * inv);
+  const int r = x - q * d;
+  q += r >= d ? 1 : 0;
+  return r < 0 ? q - 1 : q;
 }
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 512, kPlanWarps = kPlanThreads / 32, kCandidates = 16;
 
 struct PlanArgs {
   CacheView c;
@@ -133,10 +115,9 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const __grid_c
   Seg* segs = reinterpret_cast<Seg*>(dyn);
   int* first[2] = {reinterpret_cast<int*>(dyn + cap * sizeof(Seg)),
                    reinterpret_cast<int*>(dyn + cap * sizeof(Seg)) + cap};
-  __shared__ int sh[66];
   __shared__ int sh_max[2], sh_c[2], sh_grouped;
-  __shared__ int sh_base[2], sh_part[2];
-  __shared__ unsigned long long sh_w[2];
+  __shared__ int sh_base[2];
+  __shared__ float sh_work[2][kPlanWarps];
   __shared__ unsigned long long best[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = a.c.Hq / a.c.Hkv;
@@ -146,9 +127,6 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const __grid_c
 
   if (tid < 2) {
     sh_max[tid] = 0;
-    sh_base[tid] = 0;
-    sh_part[tid] = tid ? static_cast<int>(a.l.rows_narrow) : 0;
-    sh_w[tid] = 0;
     best[tid] = ~0ull;
   }
   __syncthreads();
@@ -158,6 +136,7 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const __grid_c
     Seg s;
     const int c0 = a.cu[b], c1 = a.cu[b + 1];
     const int row = a.rows != nullptr ? a.rows[b] : b;
+    const int shared = a.group > 1 && b % a.group == 0 ? a.shared[b / a.group] : 0;
     const bool run = c0 >= 0 && c1 >= c0 && c1 <= a.T;
     s.t0 = run ? c0 : 0;
     s.n_tok = run ? c1 - c0 : 0;
@@ -181,6 +160,8 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const __grid_c
     s.tiles = s.n_tok > 0 ? static_cast<int>((len + 127) / 128) : 0;
     s.chunk = s.chunks = 0;
     s.part = -1;
+    s.jobs = 0;
+    s.rows = shared;
     segs[b] = s;
   }
   // groups: the shared keys as one segment, if the partial rows of both parts fit
@@ -191,20 +172,24 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const __grid_c
   __syncthreads();
   const bool grouped = sh_grouped != 0;
   const int n_segs = a.S + (grouped ? n_groups : 0);
+  // whether segment i's tokens are in two segments
+  auto in_two = [&](int i) {
+    return grouped && segs[a.S + (i < a.S ? i / a.group : i - a.S)].tiles > 0;
+  };
   if (grouped) {
     for (int i = tid; i < n_groups; i += kPlanThreads) {
       int lead = -1;
       for (int b = i * a.group; b < (i + 1) * a.group; ++b)
         if (segs[b].row >= 0 && lead < 0) lead = b;
-      int sh_len = lead < 0 ? 0 : a.shared[i];
+      int sh_len = lead < 0 ? 0 : segs[i * a.group].rows;
       if (sh_len < 0) sh_len = 0;
       if (lead >= 0 && sh_len > segs[lead].key_end) sh_len = segs[lead].key_end;
       const int tiles = sh_len / 128;
       Seg s;
-      s.t0 = a.cu[i * a.group];
-      const int t1 = a.cu[(i + 1) * a.group];
-      const bool run = s.t0 >= 0 && t1 >= s.t0 && t1 <= a.T;
-      if (!run) s.t0 = 0;
+      const Seg& tail = segs[(i + 1) * a.group - 1];
+      s.t0 = segs[i * a.group].t0;
+      const int t1 = tail.t0 + tail.n_tok;
+      const bool run = t1 >= s.t0;
       s.n_tok = run ? t1 - s.t0 : 0;
       s.row = lead < 0 ? 0 : segs[lead].row;
       s.lim = INT_MIN;
@@ -213,6 +198,7 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const __grid_c
       s.key_end = tiles * 128;
       s.chunk = s.chunks = 0;
       s.part = -1;
+      s.jobs = s.rows = 0;
       segs[a.S + i] = s;
       if (s.tiles > 0)
         for (int b = i * a.group; b < (i + 1) * a.group; ++b) {
@@ -232,91 +218,122 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const __grid_c
   }
   __syncthreads();
 
-  // work of each class, in key tiles of one Q tile (narrow) or pair of them (wide)
-  for (int i = tid; i < n_segs; i += kPlanThreads) {
-    const Seg& s = segs[i];
-    const bool w = is_wide(s, g);
-    const int pairs = w ? (s.n_tok + 2 * qt_of(g, true) - 1) / (2 * qt_of(g, true)) : 1;
-    if (s.tiles > 0) {
-      atomicAdd(&sh_w[w], static_cast<unsigned long long>(a.c.Hkv) * pairs * s.tiles);
-      atomicMax(&sh_max[w], s.tiles);
+  // work of each class, in key tiles of one Q tile (narrow) or pair of them (wide); the estimates
+  // are in fp32 (64-bit integers take microseconds here)
+  const int qn = qt_of(g, false), per_pair = 2 * qt_of(g, true);
+  {
+    float work[2] = {0.0f, 0.0f};
+    int longest[2] = {0, 0};
+    for (int i = tid; i < n_segs; i += kPlanThreads) {
+      const int tiles = segs[i].tiles, n = segs[i].n_tok;
+      const int w = n > qn ? 1 : 0;
+      const float x = static_cast<float>(w ? (n + per_pair - 1) / per_pair : 1) * static_cast<float>(a.c.Hkv * tiles);
+      work[0] += w ? 0.0f : x;
+      work[1] += w ? x : 0.0f;
+      if (w) longest[1] = max(longest[1], tiles); else longest[0] = max(longest[0], tiles);
+    }
+    if (warp * 32 < n_segs) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) {
+          work[c] += __shfl_xor_sync(0xffffffffu, work[c], off);
+          longest[c] = max(longest[c], __shfl_xor_sync(0xffffffffu, longest[c], off));
+        }
+        if (lane == 0) {
+          sh_work[c][warp] = work[c];
+          atomicMax(&sh_max[c], longest[c]);
+        }
+      }
     }
   }
   __syncthreads();
-  // candidates: warp = (class, k): chunks that make k rounds of jobs over all streams
-  {
-    const int cls = warp >> 4, v = warp & 15;
+  // candidates, a warp each: chunks that make k rounds of jobs over all streams
+#pragma unroll 1
+  for (int x = warp; x < 2 * kCandidates; x += kPlanWarps) {
+    const int cls = x / kCandidates, v = x % kCandidates;
+    const int longest = sh_max[cls];
+    if (longest == 0) continue;
     // wide: 15 round counts; narrow: five, each with chunks an eighth and a quarter longer too (a
     // few short sequences then stay whole); and no split
-    const int k = cls ? v + 1 : v / 3 + 1, more = cls ? 0 : v % 3;
-    const int round = cls ? a.sms : 2 * a.sms;
-    const int longest = sh_max[cls];
-    const unsigned long long W = sh_w[cls];
-    const unsigned long long per = 8ull * round * k;
-    int C = v == 15 ? longest : static_cast<int>((W * (8 + more) + per - 1) / per);
-    if (C < (cls ? 8 : 2)) C = cls ? 8 : 2;
-    if (C > longest) C = longest;
-    if (longest > 0) {
-      unsigned long long jobs = 0, rows = 0;
-      for (int i = lane; i < n_segs; i += 32) {
-        const Seg& s = segs[i];
-        if (s.tiles == 0 || is_wide(s, g) != (cls == 1)) continue;
-        const int chunks = (s.tiles + C - 1) / C;
-        const int pairs = cls ? (s.n_tok + 2 * qt_of(g, true) - 1) / (2 * qt_of(g, true)) : 1;
-        jobs += static_cast<unsigned long long>(a.c.Hkv) * pairs * chunks;
-        const bool two = grouped && segs[a.S + (i < a.S ? i / a.group : i - a.S)].tiles > 0;
-        if (chunks > 1 || two) rows += static_cast<unsigned long long>(a.c.Hq) * chunks * s.n_tok;
-      }
+    const float round = static_cast<float>(cls ? a.sms : 2 * a.sms);
+    const float rounds = static_cast<float>(cls ? v + 1 : v / 3 + 1), more = cls ? 1.0f : 1.0f + 0.125f * (v % 3);
+    float W = 0.0f;
+    for (int w = 0; w < kPlanWarps && w * 32 < n_segs; ++w) W += sh_work[cls][w];
+    const float Cf = ceilf(__fdividef(W * more, round * rounds));
+    int C = v == kCandidates - 1 || Cf >= static_cast<float>(longest) ? longest : static_cast<int>(Cf);
+    const int least = cls ? 8 : 2;
+    C = C < least ? least : C;
+    C = C > longest ? longest : C;
+    const float inv = __fdividef(1.0f, static_cast<float>(C));
+    float jobs = 0.0f, rows = 0.0f;
+    for (int i = lane; i < n_segs; i += 32) {
+      const int tiles = segs[i].tiles, n = segs[i].n_tok;
+      if (tiles == 0 || (n > qn) != (cls == 1)) continue;
+      const float chunks = ceilf(static_cast<float>(tiles) * inv);
+      const float pairs = static_cast<float>(cls ? (n + per_pair - 1) / per_pair : 1);
+      jobs += static_cast<float>(a.c.Hkv) * pairs * chunks;
+      if (chunks > 1.0f || in_two(i)) rows += static_cast<float>(a.c.Hq) * chunks * static_cast<float>(n);
+    }
 #pragma unroll
-      for (int off = 16; off > 0; off >>= 1) {
-        jobs += __shfl_xor_sync(0xffffffffu, jobs, off);
-        rows += __shfl_xor_sync(0xffffffffu, rows, off);
-      }
-      const unsigned long long cap = cls ? a.l.max_wide : a.l.max_narrow;
-      const unsigned long long most = cls ? a.l.rows_wide : a.l.rows_narrow;
-      if (lane == 0 && jobs <= cap && rows <= most) {
-        // makespan in tiles: whole rounds, and what a job costs beside its tiles
-        const unsigned long long cost = ((jobs + round - 1) / round) * (C + (cls ? 6 : 3));
-        atomicMin(&best[cls], (cost << 25) | static_cast<unsigned long long>(kMaxTiles - C));
-      }
+    for (int off = 16; off > 0; off >>= 1) {
+      jobs += __shfl_xor_sync(0xffffffffu, jobs, off);
+      rows += __shfl_xor_sync(0xffffffffu, rows, off);
+    }
+    // (the capacities with the estimates' rounding to spare; without a split they suffice exactly)
+    const float cap = 0.999f * static_cast<float>(cls ? a.l.max_wide : a.l.max_narrow);
+    const float most = 0.999f * static_cast<float>(cls ? a.l.rows_wide : a.l.rows_narrow);
+    if (lane == 0 && (v == kCandidates - 1 || (jobs <= cap && rows <= most))) {
+      // makespan in tiles: whole rounds, and what a job costs beside its tiles; equal ones: the
+      // longer chunks
+      const float cost = ceilf(__fdividef(jobs, round)) * static_cast<float>(C + (cls ? 6 : 3));
+      atomicMin(&best[cls], (static_cast<unsigned long long>(__float_as_uint(cost)) << 25) |
+                                static_cast<unsigned long long>(kMaxTiles - C));
     }
   }
   __syncthreads();
   if (tid < 2) sh_c[tid] = best[tid] == ~0ull ? kMaxTiles : kMaxTiles - static_cast<int>(best[tid] & 0x1FFFFFF);
   __syncthreads();
 
-  // chunks, partial rows and jobs of every segment
-  int rows_total;
-  for (int i0 = 0; i0 < n_segs; i0 += kPlanThreads) {
-    const int i = i0 + tid;
-    int jobs = 0, rows = 0, w = 0;
-    if (i < n_segs) {
-      Seg& s = segs[i];
-      w = is_wide(s, g) ? 1 : 0;
-      if (s.tiles > 0) {
-        const int C = sh_c[w];
-        s.chunks = (s.tiles + C - 1) / C;
-        s.chunk = (s.tiles + s.chunks - 1) / s.chunks;
-        s.chunks = (s.tiles + s.chunk - 1) / s.chunk;
-        const int pairs = w ? (s.n_tok + 2 * qt_of(g, true) - 1) / (2 * qt_of(g, true)) : 1;
-        jobs = a.c.Hkv * pairs * s.chunks;
-        const bool two = grouped && segs[a.S + (i < a.S ? i / a.group : i - a.S)].tiles > 0;
-        if (s.chunks > 1 || two) rows = a.c.Hq * s.chunks * s.n_tok;
-      }
-    }
+  // chunks, jobs and partial rows of every segment
+  for (int i = tid; i < n_segs; i += kPlanThreads) {
+    Seg& s = segs[i];
+    const int w = s.n_tok > qn ? 1 : 0;
+    s.jobs = s.rows = 0;
+    if (s.tiles == 0) continue;
+    const int C = sh_c[w];
+    s.chunks = (s.tiles + C - 1) / C;
+    s.chunk = (s.tiles + s.chunks - 1) / s.chunks;
+    s.chunks = (s.tiles + s.chunk - 1) / s.chunk;
+    s.jobs = a.c.Hkv * (w ? (s.n_tok + per_pair - 1) / per_pair : 1) * s.chunks;
+    if (s.chunks > 1 || in_two(i)) s.rows = a.c.Hq * s.chunks * s.n_tok;
+  }
+  __syncthreads();
+  // their exclusive sums: a warp each for the jobs and the rows of the two classes
+  if (warp < 4) {
+    const int cls = warp & 1;
+    const bool of_rows = warp >= 2;
+    int base = of_rows && cls ? static_cast<int>(a.l.rows_narrow) : 0;
 #pragma unroll 1
-    for (int cls = 0; cls < 2; ++cls) {
-      int total;
-      const int at = plan_scan(w == cls ? jobs : 0, sh, &total);
-      if (i < n_segs) first[cls][i] = sh_base[cls] + at;
-      const int pr = plan_scan(w == cls ? rows : 0, sh + 33, &rows_total);
-      if (i < n_segs && w == cls && rows > 0) segs[i].part = sh_part[cls] + pr;
-      __syncthreads();
-      if (tid == 0) {
-        sh_base[cls] += total;
-        sh_part[cls] += rows_total;
+    for (int i0 = 0; i0 < n_segs; i0 += 32) {
+      const int i = i0 + lane;
+      int v = 0;
+      if (i < n_segs && (segs[i].n_tok > qn) == (cls == 1)) v = of_rows ? segs[i].rows : segs[i].jobs;
+      int s = v;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, s, off);
+        if (lane >= off) s += u;
       }
+      if (i < n_segs) {
+        if (!of_rows)
+          first[cls][i] = base + s - v;
+        else if (v > 0)
+          segs[i].part = base + s - v;
+      }
+      base += __shfl_sync(0xffffffffu, s, 31);
     }
+    if (!of_rows && lane == 0) sh_base[cls] = base;
   }
   __syncthreads();
   if (tid == 0) {
@@ -337,6 +354,8 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const __grid_c
     Job* jobs = reinterpret_cast<Job*>(a.ws + (cls ? a.l.wide : a.l.narrow));
     const int* f = first[cls];
     const int n_jobs = sh_base[cls];
+    const float inv_kv = 1.0f / static_cast<float>(a.c.Hkv);
+    const bool quick = n_jobs < 1 << 24;
     for (int x = tid; x < n_jobs; x += kPlanThreads) {
       int lo = 0, hi = n_segs - 1;           // the last segment that starts at or before x
       while (lo < hi) {
@@ -352,21 +371,20 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const __grid_c
       int chunk;
       if (cls == 0) {
         // key heads of one chunk side by side: neighbours in memory
-        j.kv = y % a.c.Hkv;
-        chunk = y / a.c.Hkv;
+        chunk = quick ? quick_div(y, a.c.Hkv, inv_kv) : y / a.c.Hkv;
+        j.kv = y - chunk * a.c.Hkv;
         j.t0 = s.t0;
         j.n_tok = s.n_tok;
       } else {
         // Q tiles of one (chunk, key head) side by side: they share its K and V through L2;
         // the last tokens, which see most keys, first
-        const int per = 2 * qt_of(g, true);
-        const int pairs = (s.n_tok + per - 1) / per;
+        const int pairs = (s.n_tok + per_pair - 1) / per_pair;
         const int p = pairs - 1 - y % pairs;
         y /= pairs;
-        j.kv = y % a.c.Hkv;
-        chunk = y / a.c.Hkv;
-        j.t0 = s.t0 + p * per;
-        j.n_tok = s.n_tok - p * per < per ? s.n_tok - p * per : per;
+        chunk = quick ? quick_div(y, a.c.Hkv, inv_kv) : y / a.c.Hkv;
+        j.kv = y - chunk * a.c.Hkv;
+        j.t0 = s.t0 + p * per_pair;
+        j.n_tok = s.n_tok - p * per_pair < per_pair ? s.n_tok - p * per_pair : per_pair;
       }
       const int tiles = tiles_of(s, j.t0 + j.n_tok);
       j.tile0 = s.tile0 + chunk * s.chunk;
@@ -374,7 +392,10 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const __grid_c
       j.n_tiles = j.n_tiles < 0 ? 0 : (j.n_tiles > s.chunk ? s.chunk : j.n_tiles);
       // rows of the partial results: [kv][chunk][token][head of the group]
       j.part = s.part < 0 ? -1 : s.part + ((j.kv * s.chunks + chunk) * s.n_tok + (j.t0 - s.t0)) * g;
-      jobs[x] = j;
+      int4* out = reinterpret_cast<int4*>(jobs + x);
+      out[0] = make_int4(j.t0, j.n_tok, j.row, j.lim);
+      out[1] = make_int4(j.tile0, j.n_tiles, j.key_end, j.kv);
+      out[2] = make_int4(j.part, 0, 0, 0);
     }
   }
 }
@@ -543,6 +564,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_launch_dependents();
   pdl_wait();                 // the job lists
   const int n_jobs = __ldcg(a.n_jobs);
+  // (the first jobs' line is on its way meanwhile)
+  prefetch_l1(a.jobs + (kWide ? 1 : 2) * blockIdx.x);
   const int n_items = kWide ? n_jobs : (n_jobs + 1) / 2;
 
   if (warp == 0) {
@@ -937,12 +960,11 @@ struct JoinArgs {
 };
 
 // kPer warps join one (token, head) row: 1 with many rows, all of the block's with few rows of many
-// parts.  32 parts at a time: a lane loads one part's log-sum-exp, the warp sets the weights,
-// then the parts' rows are added, their loads independent of one another.
+// parts.  32 parts at a time: a lane loads one part's log-sum-exp, the warp sets the weights
+// (every warp of the row the same), then adds every kPer-th part's row, loads independent.
 template <int D, int kPer>
 __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_constant__ JoinArgs a) {
   constexpr int kV = D / 32;          // values of a lane
-  __shared__ float sm[kJoinWarps], sl[kJoinWarps];
   __shared__ float so[kPer > 1 ? kJoinWarps : 1][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = a.Hq / a.Hkv;
@@ -986,7 +1008,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
   float m = -INFINITY, l = 0.0f, acc[kV];
 #pragma unroll
   for (int i = 0; i < kV; ++i) acc[i] = 0.0f;
-  for (int p0 = (warp % kPer) * 32; p0 < total; p0 += 32 * kPer) {
+  for (int p0 = 0; p0 < total; p0 += 32) {
     const int p = p0 + lane;
     const int64_t row = p < n[0] ? first[0] + p * step[0] : first[1] + (p - n[0]) * step[1];
     const float x = p < total ? __ldcg(a.part_lse + row) : -INFINITY;
@@ -1006,7 +1028,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
     for (int i = 0; i < kV; ++i) acc[i] *= f;
     const int cnt = total - p0 < 32 ? total - p0 : 32;
 #pragma unroll 4
-    for (int k = 0; k < cnt; ++k) {
+    for (int k = warp % kPer; k < cnt; k += kPer) {
       const float wk = __shfl_sync(0xffffffffu, w, k);
       const float* src = a.part_o + __shfl_sync(0xffffffffu, row, k) * D + lane * kV;
       if constexpr (kV == 4) {
@@ -1023,24 +1045,14 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
     }
   }
   if constexpr (kPer > 1) {
-    if (lane == 0) { sm[warp] = m; sl[warp] = l; }
 #pragma unroll
     for (int i = 0; i < kV; ++i) so[warp][lane * kV + i] = acc[i];
     __syncthreads();
     if (warp > 0) return;
-    m = sm[0];
 #pragma unroll
-    for (int w = 1; w < kPer; ++w) m = fmaxf(m, sm[w]);
-    l = 0.0f;
+    for (int w = 1; w < kPer; ++w)
 #pragma unroll
-    for (int i = 0; i < kV; ++i) acc[i] = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kPer; ++w) {
-      const float f = sm[w] == -INFINITY ? 0.0f : ex2_approx(sm[w] - m);
-      l += f * sl[w];
-#pragma unroll
-      for (int i = 0; i < kV; ++i) acc[i] = fmaf(f, so[w][lane * kV + i], acc[i]);
-    }
+      for (int i = 0; i < kV; ++i) acc[i] += so[w][lane * kV + i];
   }
   const float inv = l > 0.0f ? 1.0f / l : 0.0f;
   uint32_t* dst = reinterpret_cast<uint32_t*>(a.o + out * D) + lane * (kV / 2);
