@@ -701,6 +701,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = wait(C::kBarQFull, uc & 1u);
       if (!ok) break;
       tc_fence_after();
+      // Q is free for the next item once the last scores are taken
+      int scores = s.n[0] + s.n[1];
       // first scores
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
@@ -713,6 +715,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         issue_s(q, ks);
         mma_commit_w(&bars[C::kBarSFull + q]);
+        if (--scores == 0) mma_commit_w(&bars[C::kBarQEmpty]);
         if (!kWide || q == 1 || s.n[1] == 0) {
           mma_commit_w(&bars[C::kBarKEmpty + ks]);
           ++kit;
@@ -756,6 +759,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             issue_s(q, ks);
             mma_commit_w(&bars[C::kBarSFull + q]);
+            if (--scores == 0) mma_commit_w(&bars[C::kBarQEmpty]);
             if (!kWide || q == 1 || s.n[1] == 0) {
               mma_commit_w(&bars[C::kBarKEmpty + ks]);
               ++kit;
@@ -767,7 +771,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (s.n[0] > 0) ++uq[0];
       if (s.n[1] > 0) ++uq[1];
       ++uc;
-      mma_commit_w(&bars[C::kBarQEmpty]);
     }
     if (!ok) *vabort = 1;
     // every MMA (and the arrivals committed behind it) has landed before exit

@@ -11,14 +11,15 @@
 //   or 8 CTAs owns one row at a time, each a slice of at most 76 KB, in three buffers: one row
 //   waits for its gradient while its sums are exchanged, the next row's sums are taken, and the
 //   third arrives by bulk copy.  The exchange takes about 4 us whatever the slice, so the fewest
-//   CTAs a row are the fastest (slices of 76 KB against 38 KB, two CTAs an SM then:
-//   4,096 x 151,936 388 against 457 us).
-//   8 streaming warps: the sum of exp(x - m) in fp32, m the maximum of a thread's first eight
+//   CTAs a row are the fastest (slices of 76 KB against 38 KB with two CTAs an SM:
+//   4,096 x 151,936 388 against 457 us), and two rows' exchanges overlap (5,341 x 50,256 184
+//   against 260 us).
+//   4 or 8 streaming warps: the sum of exp(x - m) in fp32, m the maximum of a thread's first eight
 //     logits (the true one if that overflows), joined across lanes in fp32 pairs; later p g
 //     rounded to bf16 and stored.  One exponential a logit and pass.
-//   1 scalar warp: joins the partials, exchanges them with the other CTAs (distributed shared
-//     memory, remote mbarrier arrivals, bounded waits), joins those in rank order and decides
-//     the clip.  It also owns the up to 7 + 7 logits of a row outside its 16-byte granules.
+//   2 scalar warps, every other row each: join the partials, exchange them with the other CTAs (distributed
+//     shared memory, remote mbarrier arrivals, bounded waits), join those in rank order and decide
+//     the clip.  They also own the up to 7 + 7 logits of a row outside its 16-byte granules.
 //   1 copy warp: requests a row's slice as soon as a buffer is free.
 //   A row whose gradient has another alignment than its logits goes through shared memory once
 //   more and is shifted there.
@@ -182,9 +183,11 @@ __global__ void __launch_bounds__(kRowThreads) policy_rows(const __grid_constant
 // A cluster a row, the row in shared memory
 // ======================================================================================
 constexpr int kMaxCluster = 8;
-constexpr int kBufs = 3;                       // slices in shared memory
+constexpr int kMaxBufs = 4;                    // slices in shared memory (three or four)
 constexpr int kSliceMax = 76000;               // bytes: three slices in one CTA's shared memory
-constexpr int kStream = 256;                   // streaming threads
+constexpr int kSlice4 = 57000;                 // four
+constexpr int kSlice2 = 38000;                 // three, and two such CTAs on an SM
+constexpr int kSliceSmall = 26000;             // up to here: 128 streaming threads, four CTAs an SM
 
 // How a row lies in memory: `head` logits before its first 16-byte granule, `nv` whole granules, then
 // the tail; granules [g0, g0 + n) are this CTA's.
@@ -230,12 +233,13 @@ __device__ __forceinline__ void join_lanes(float& m, Pair& s) {
   m = M;
 }
 
-// Named barriers.  The streaming warps take the sums of row r + 1 before they wait for the gradient
-// of row r, so the parts of row r + 2 come behind the scalar warp's use of those of row r: two
-// ids (row parity).  Nothing holds the streaming warps back from running ahead of the copy warp
-// but the copies that it issues: row r + 3 is requested behind its wait for row r, and the rows
-// at the end, which wait for no copy, are at most three: three ids.
-enum : uint32_t { kBarParts = 1, kBarG = 3, kBarEmpty = 5, kBarCopy = 8 };
+// Named barriers.  With nb buffers the streaming warps take the sums of row r + nb - 2 before they
+// wait for the gradient of row r, so at most nb - 1 <= 3 rows' parts are waiting for the scalar
+// warp, and as many gradients for the streaming warps: three ids each.  Nothing holds the
+// streaming warps back from running ahead of the copy warp but the copies that it issues: row
+// r + nb is requested behind its wait for row r, and the rows at the end, which wait for no
+// copy, are at most nb: nb <= 4 ids.
+enum : uint32_t { kBarParts = 1, kBarG = 4, kBarEmpty = 7, kBarCopy = 11 };
 
 __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
@@ -279,16 +283,17 @@ __device__ __forceinline__ void shift_row(uint16_t* d, const uint4* buf, int n, 
   if (tid < 8 - off) d[off + 8 * nd + tid] = h[off + 8 * nd + tid];
 }
 
-__global__ void __launch_bounds__(kStream + 64, 2)
-    policy_cluster(const __grid_constant__ PolicyArgs a, int cl, int per) {
+template <int kStream>
+__global__ void __launch_bounds__(kStream + 96, kStream == 128 ? 4 : 3)
+    policy_cluster(const __grid_constant__ PolicyArgs a, int cl, int per, int nb) {
   constexpr int kWarps = kStream / 32;
   constexpr int kThreads = kStream + 32;        // streaming warps and one other
   extern __shared__ __align__(128) uint8_t dyn[];
-  __shared__ __align__(8) uint64_t full[kBufs], xbar[2];
-  __shared__ float part[2][kWarps][3];         // a warp's maximum and sum (pair)
-  __shared__ float slot[2][kMaxCluster][3];    // a CTA's, by rank
-  __shared__ float sh_g[2], sh_c[2], sh_gy[2];
-  __shared__ int sh_used[kBufs], sh_y[2];
+  __shared__ __align__(8) uint64_t full[kMaxBufs], xbar[4];
+  __shared__ float part[3][kWarps][3];         // a warp's maximum and sum (pair)
+  __shared__ float slot[4][kMaxCluster][3];    // a CTA's, by rank
+  __shared__ float sh_g[3], sh_c[3], sh_gy[3];
+  __shared__ int sh_used[kMaxBufs], sh_y[3];
   // Set when a bounded wait of this CTA or of a peer gave up: rows are only walked through from
   // then on, with NaN terms and gradients of zero.
   __shared__ int cl_abort;
@@ -304,8 +309,8 @@ __global__ void __launch_bounds__(kStream + 64, 2)
 
   if (tid == 0) {
     cl_abort = 0;
-    for (int i = 0; i < kBufs; ++i) mbar_init(&full[i], 1);
-    for (int i = 0; i < 2; ++i) mbar_init(&xbar[i], static_cast<uint32_t>(cl));
+    for (int i = 0; i < nb; ++i) mbar_init(&full[i], 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&xbar[i], static_cast<uint32_t>(cl));
     fence_mbar_init();
   }
   __syncthreads();
@@ -314,10 +319,13 @@ __global__ void __launch_bounds__(kStream + 64, 2)
   pdl_launch_dependents();
 
   RowSpan sp = row_span(a, cid, per, rank);
-  if (warp == kWarps) {
-    // ------------------------------------------------------------------ scalar warp
-    // What belongs to the next rows is loaded ahead: a token two rows, its logit and the
+  if (warp == kWarps || warp == kWarps + 1) {
+    // ----------------------------------------------------------------- scalar warps
+    // Each takes every other row, so that two rows' exchanges overlap (one alone takes 3.7 us a
+    // row).  What belongs to the next rows is loaded ahead: a token two rows, its logit and the
     // logits outside the granules (lanes 16-22 the head's, 24-30 the tail's, on rank 0) one.
+    const int who = warp - kWarps;
+    const int64_t first = cid + who * ncl, step = 2 * ncl;
     struct Ahead {
       Token tok;
       float xy, edge;
@@ -339,16 +347,15 @@ __global__ void __launch_bounds__(kStream + 64, 2)
       }
       return r;
     };
-    Ahead now = logits(cid, token(cid));
-    Token next = token(cid + ncl);
+    Ahead now = logits(first, token(first));
+    Token next = token(first + step);
     uint32_t ux = 0;                   // rows exchanged
-    int it = 0;
-    for (int64_t row = cid; row < a.T; row += ncl, ++it) {
-      const int par = it & 1;
+    int par = who;                     // row modulo 3
+    for (int64_t row = first; row < a.T; row += step, par = par == 0 ? 2 : par - 1) {
       const Token t = now.tok;
       const float xv = now.xy, ev = now.edge;
-      now = logits(row + ncl, next);
-      next = token(row + 2 * ncl);
+      now = logits(row + step, next);
+      next = token(row + 2 * step);
       if (!alike) sp = row_span(a, row, per, rank);
       TokenLoss o;
       o.g = 0.0f;
@@ -373,7 +380,7 @@ __global__ void __launch_bounds__(kStream + 64, 2)
         const float x_y = __shfl_sync(0xffffffffu, xv, 0);
         aborted = *vabort != 0;
         if (cl > 1 && !aborted) {
-          const int sl = ux & 1;
+          const int sl = 2 * who + (ux & 1);
           if (lane < cl) {
             const uint32_t dst = cluster_map(&slot[sl][rank][0], lane);
             st_cluster_f32(dst, m);
@@ -427,9 +434,9 @@ __global__ void __launch_bounds__(kStream + 64, 2)
         }
       }
     }
-  } else if (warp > kWarps) {
+  } else if (warp == kWarps + 2) {
     // -------------------------------------------------------------------- copy warp
-    // Requests a row's slice as soon as a buffer is free (three rows ahead of the gradient).
+    // Requests a row's slice as soon as a buffer is free.
     auto request = [&](int64_t row, int b, const Token& t) {
       if (row >= a.T) return;
       const bool used = t.used(a.V);
@@ -451,21 +458,18 @@ __global__ void __launch_bounds__(kStream + 64, 2)
       if (row < a.T) t = load_token(a, row);
       return t;
     };
-    const Token t0 = token(cid), t1 = token(cid + ncl), t2 = token(cid + 2 * ncl);
-    Token next = token(cid + 3 * ncl);
-    request(cid, 0, t0);
-    request(cid + ncl, 1, t1);
-    request(cid + 2 * ncl, 2, t2);
+    for (int i = 0; i < nb; ++i) request(cid + i * ncl, i, token(cid + i * ncl));
+    Token next = token(cid + nb * ncl);
     int it = 0, b = 0;
-    for (int64_t row = cid; row < a.T; row += ncl, ++it, b = b == kBufs - 1 ? 0 : b + 1) {
+    for (int64_t row = cid; row < a.T; row += ncl, ++it, b = b == nb - 1 ? 0 : b + 1) {
       named_barrier_sync(kBarEmpty + b, kThreads);
-      request(row + kBufs * ncl, b, next);
-      next = token(row + (kBufs + 1) * ncl);
+      request(row + nb * ncl, b, next);
+      next = token(row + (nb + 1) * ncl);
     }
     if (*vabort) {
       // copies still in flight land before the CTA may exit: the last request of each buffer
-      for (int i = 0; i < kBufs; ++i)
-        if (it > i) mbar_wait_ns(&full[i], static_cast<uint32_t>((it - 1 - i) / kBufs) & 1u, 200000000ull);
+      for (int i = 0; i < nb; ++i)
+        if (it > i) mbar_wait_ns(&full[i], static_cast<uint32_t>((it - 1 - i) / nb) & 1u, 200000000ull);
     }
   } else {
     // -------------------------------------------------------------- streaming warps
@@ -490,13 +494,15 @@ __global__ void __launch_bounds__(kStream + 64, 2)
       return s0 + s1;
     };
     // Sum of exponentials of this CTA's slice of its i-th row.
-    auto pass1 = [&](int64_t row, int i) {
-      const int bi = i % kBufs, par = i & 1;
+    int sum_buf = 0, sum_par = 0;      // of the next row to be summed
+    uint32_t sum_phase = 0u;
+    auto pass1 = [&](int64_t row) {
+      const int bi = sum_buf, par = sum_par;
       const int n = alike ? sp.n : row_span(a, row, per, rank).n;
       const uint4* buf = reinterpret_cast<const uint4*>(dyn + bi * slice);
       // (after an abort the rows are only walked through, barrier by barrier: every row still
       // arrives here, without a copy)
-      const bool here = mbar_wait(&full[bi], static_cast<uint32_t>(i / kBufs) & 1u, a.status);
+      const bool here = mbar_wait(&full[bi], sum_phase, a.status);
       if (!here) *vabort = 1;
       float m = -INFINITY;
       Pair s = {0.0f, 0.0f};
@@ -524,14 +530,17 @@ __global__ void __launch_bounds__(kStream + 64, 2)
       }
       __syncwarp();
       named_barrier_arrive(kBarParts + par, kThreads);
+      sum_par = par == 2 ? 0 : par + 1;
+      sum_buf = bi == nb - 1 ? 0 : bi + 1;
+      sum_phase ^= bi == nb - 1 ? 1u : 0u;
     };
-    int it = 0;
-    if (cid < a.T) pass1(cid, 0);
-    for (int64_t row = cid; row < a.T; row += ncl, ++it) {
-      const int par = it & 1;
-      uint4* buf = reinterpret_cast<uint4*>(dyn + (it % kBufs) * slice);
-      // the next row's sums while this row's are exchanged
-      if (row + ncl < a.T) pass1(row + ncl, it + 1);
+    int b = 0, par = 0;
+    const int64_t ahead = (nb - 2) * ncl;
+    for (int64_t row = cid; row < cid + ahead && row < a.T; row += ncl) pass1(row);
+    for (int64_t row = cid; row < a.T; row += ncl, b = b == nb - 1 ? 0 : b + 1, par = par == 2 ? 0 : par + 1) {
+      uint4* buf = reinterpret_cast<uint4*>(dyn + b * slice);
+      // later rows' sums while this row's are exchanged
+      if (row + ahead < a.T) pass1(row + ahead);
       named_barrier_sync(kBarG + par, kThreads);
       const float g = sh_g[par], c = sh_c[par], gy = sh_gy[par];
       const int y = sh_y[par];
@@ -570,7 +579,7 @@ __global__ void __launch_bounds__(kStream + 64, 2)
         // the next copy into this buffer comes behind the writes above
         fence_proxy_async_smem();
       }
-      named_barrier_arrive(kBarEmpty + it % kBufs, kThreads);
+      named_barrier_arrive(kBarEmpty + b, kThreads);
     }
   }
   __syncwarp();
@@ -771,15 +780,19 @@ cudaError_t launch_warp(const PolicyArgs& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
+template <int kStream>
 cudaError_t launch_cluster(const PolicyArgs& a, int cl, int per, cudaStream_t s) {
-  constexpr int kThreads = kStream + 64;
-  const int smem = kBufs * per * 16;
+  constexpr int kThreads = kStream + 96;
+  // four buffers (two rows of sums ahead) where the exchange or the SM's one CTA leaves room for
+  // them
+  const int nb = per * 16 <= kSlice4 && (cl > 1 || per * 16 > kSlice2) ? 4 : 3;
+  const int smem = nb * per * 16;
   static bool attr_set[kMaxDeviceCache] = {};
   const int dev = cached_device_index();
   if (dev < 0) return cudaErrorInvalidDevice;
   if (!attr_set[dev]) {
-    cudaError_t e = cudaFuncSetAttribute(policy_cluster, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kBufs * kSliceMax);
+    cudaError_t e = cudaFuncSetAttribute(policy_cluster<kStream>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         3 * kSliceMax);
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
   }
@@ -803,12 +816,12 @@ cudaError_t launch_cluster(const PolicyArgs& a, int cl, int per, cudaStream_t s)
     n = static_cast<int>(seen & 0xFFFFFF);
   } else if (cl > 1) {
     cfg.gridDim = dim3(static_cast<unsigned>(num_sms() * cl), 1, 1);
-    if (cudaOccupancyMaxActiveClusters(&n, policy_cluster, &cfg) != cudaSuccess || n <= 0) {
+    if (cudaOccupancyMaxActiveClusters(&n, policy_cluster<kStream>, &cfg) != cudaSuccess || n <= 0) {
       (void)cudaGetLastError();
       n = num_sms() / cl;
     }
   } else {
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, policy_cluster, kThreads,
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, policy_cluster<kStream>, kThreads,
                                                       static_cast<size_t>(smem)) != cudaSuccess || n <= 0) {
       (void)cudaGetLastError();
       n = 1;
@@ -818,7 +831,7 @@ cudaError_t launch_cluster(const PolicyArgs& a, int cl, int per, cudaStream_t s)
   memo[dev].store(key | static_cast<uint64_t>(n));
   if (n > a.T) n = static_cast<int>(a.T);
   cfg.gridDim = dim3(static_cast<unsigned>(n * cl), 1, 1);
-  return cudaLaunchKernelEx(&cfg, policy_cluster, a, cl, per);
+  return cudaLaunchKernelEx(&cfg, policy_cluster<kStream>, a, cl, per, nb);
 }
 
 }  // namespace
@@ -832,13 +845,16 @@ cudaError_t launch_policy_loss(const PolicyArgs& a, cudaStream_t s) {
     e = launch_warp<8>(a, s);
   } else if (a.V <= 4096) {
     e = launch_warp<16>(a, s);
+
   } else {
     // the fewest CTAs a row
     int cl = 1;
     while (cl < kMaxCluster && (granules + cl - 1) / cl * 16 > kSliceMax) cl *= 2;
     const int64_t per = (granules + cl - 1) / cl;
     if (per * 16 <= kSliceMax) {
-      e = launch_cluster(a, cl, static_cast<int>(per), s);
+      // (33,554 x 8,000: 185 us with 128 streaming threads, 211 with 256; 16,777 x 16,000: 180, 174)
+      e = per * 16 <= kSliceSmall ? launch_cluster<128>(a, cl, static_cast<int>(per), s)
+                                  : launch_cluster<256>(a, cl, static_cast<int>(per), s);
     } else {
       int64_t grid = static_cast<int64_t>(num_sms()) * 4;
       if (grid > a.T) grid = a.T;
