@@ -447,7 +447,7 @@ size_t ls_cache_pages_workspace_bytes(ls_cache_t h);
  * ls_cache_free -- drops the rows' pages (those that no row lists any more become free) and
  *   empties the rows.
  * ls_cache_compact -- moves the live pages of src together.  dst a handle over another pool of
- *   the same page shape, layout and table shape: live pages go to dst pages 0 .. n-1 in
+ *   the same page shape, layout and table shape, in other memory: live pages go to dst pages 0 .. n-1 in
  *   ascending order, dst's table, lengths and counts are written from src's; src keeps its
  *   state.  Pages beyond dst's pool set the device status (4 in the word) and are listed as -1.
  *   dst = src: in place, live pages from n on move into the holes below, in ascending order;
@@ -476,7 +476,8 @@ ls_status ls_cache_compact(ls_cache_t src, ls_cache_t dst, int32_t* n_live, void
  *   k_new + t k_stride + h D; q likewise with Hq heads (NULL: no queries; then q_out is
  *   ignored), q_out may be q.  inv_freq HOST, rot_dim / 2 doubles, or NULL: no rotation (and q must be
  *   NULL).  Tokens at a negative position are left out.  Pages of several rows must not be
- *   appended to (ls_cache_fork copies the page that a row grows into).
+ *   appended to (ls_cache_fork copies the page that a row grows into), nor one row by two
+ *   entries.
  *
  * ls_cache_attn -- attention of the new tokens over their sequences' pages, their own keys
  *   included (append first): token at position p sees keys 0 .. p,

@@ -114,22 +114,36 @@ def policy_loss(logits, ids, logp_old, advantages, weights, eps_low=0.2, eps_hig
     x, ldx = _strided(logits, "logits", (T, V), (1,), V, dev)
     if dlogits is None:
         dlogits = torch.empty((T, V), dtype=_bf16, device=at)
-    dx, ldd = _strided(dlogits, "dlogits", (T, V), (1,), V, dev)
-    loss = torch.empty(1, dtype=_f32, device=at) if loss is None else loss
-    logp_out = torch.empty(T, dtype=_f32, device=at) if logp_out is None else logp_out
-    kl_out = torch.empty(T, dtype=_f32, device=at) if kl_out is None else kl_out
-    clip_mask = torch.empty(T, dtype=_u8, device=at) if clip_mask is None else clip_mask
-    if workspace is None:
-        workspace = torch.empty(max(policy_loss_workspace_bytes(T), 16), dtype=_u8, device=at)
+        dx, ldd = dlogits.data_ptr(), V
+    else:
+        dx, ldd = _strided(dlogits, "dlogits", (T, V), (1,), V, dev)
     n = (T,)
+    if clip_mask is None:
+        clip_mask = torch.empty(n, dtype=_u8, device=at)
+        cm = clip_mask.data_ptr()
+    else:
+        cm = _ptr(clip_mask, "clip_mask", _u8, n, dev)
+    nbytes = b._lib().ls_policy_loss_workspace_bytes(T)
+    if loss is None and logp_out is None and kl_out is None and workspace is None:
+        # one allocation for the workspace and the small outputs (small calls are host-bound)
+        buf = torch.empty(nbytes // 4 + 1 + 2 * T, dtype=_f32, device=at)
+        workspace, loss, logp_out, kl_out = buf.split_with_sizes((nbytes // 4, 1, T, T))
+        wp = buf.data_ptr()
+        sp, lp, kp = wp + nbytes, wp + nbytes + 4, wp + nbytes + 4 + 4 * T
+    else:
+        loss = torch.empty(1, dtype=_f32, device=at) if loss is None else loss
+        logp_out = torch.empty(n, dtype=_f32, device=at) if logp_out is None else logp_out
+        kl_out = torch.empty(n, dtype=_f32, device=at) if kl_out is None else kl_out
+        if workspace is None:
+            workspace = torch.empty(max(nbytes, 16), dtype=_u8, device=at)
+        wp, nbytes = _ptr(workspace, "workspace", _u8, None, dev), workspace.numel()
+        sp = _ptr(loss, "loss", _f32, (1,), dev)
+        lp, kp = _ptr(logp_out, "logp_out", _f32, n, dev), _ptr(kl_out, "kl_out", _f32, n, dev)
     d = _POLICY.pack(
         T, V, ldx, ldd, x, _ptr(ids, "ids", _i32, n, dev), _ptr(logp_old, "logp_old", _f32, n, dev),
         _opt(logp_ref, "logp_ref", _f32, n, dev), _ptr(advantages, "advantages", _f32, n, dev),
-        _ptr(weights, "weights", _f32, n, dev), eps_low, eps_high, beta, _KL[kl],
-        _ptr(loss, "loss", _f32, (1,), dev), dx, _ptr(clip_mask, "clip_mask", _u8, n, dev),
-        _ptr(logp_out, "logp_out", _f32, n, dev), _ptr(kl_out, "kl_out", _f32, n, dev))
-    b._check(b._lib().ls_policy_loss(d, _ptr(workspace, "workspace", _u8, None, dev), workspace.numel(),
-                                     _raw_stream(dev)), "ls_policy_loss")
+        _ptr(weights, "weights", _f32, n, dev), eps_low, eps_high, beta, _KL[kl], sp, dx, cm, lp, kp)
+    b._check(b._lib().ls_policy_loss(d, wp, nbytes, _raw_stream(dev)), "ls_policy_loss")
     return PolicyLoss(loss, dlogits, logp_out, kl_out, clip_mask)
 
 
@@ -163,13 +177,19 @@ def rope(q, k, inv_freq, positions=None, pos0: int = 0, interleaved: bool = Fals
     if q is not None:
         Hq = q.shape[1]
         qp, qs = _heads(q, "q", T, Hq, D, dev)
-        q_out = torch.empty((T, Hq, D), dtype=_bf16, device=q.device) if q_out is None else q_out
-        qo, qos = _heads(q_out, "q_out", T, Hq, D, dev)
+        if q_out is None:
+            q_out = torch.empty((T, Hq, D), dtype=_bf16, device=q.device)
+            qo, qos = q_out.data_ptr(), Hq * D
+        else:
+            qo, qos = _heads(q_out, "q_out", T, Hq, D, dev)
     if k is not None:
         Hk = k.shape[1]
         kp, ks = _heads(k, "k", T, Hk, D, dev)
-        k_out = torch.empty((T, Hk, D), dtype=_bf16, device=k.device) if k_out is None else k_out
-        ko, kos = _heads(k_out, "k_out", T, Hk, D, dev)
+        if k_out is None:
+            k_out = torch.empty((T, Hk, D), dtype=_bf16, device=k.device)
+            ko, kos = k_out.data_ptr(), Hk * D
+        else:
+            ko, kos = _heads(k_out, "k_out", T, Hk, D, dev)
     d = _ROPE.pack(T, Hq, Hk, D, 2 * n, bool(interleaved), bool(inverse), f, attn_factor,
                    _opt(positions, "positions", _i64, (T,), dev), pos0, qp, qs, qo, qos, kp, ks, ko, kos)
     b._check(b._lib().ls_rope(d, _raw_stream(dev)), "ls_rope")
@@ -295,8 +315,11 @@ class PagedCache:
             f, n, keep = _host_doubles(inv_freq, "inv_freq")
         if q is not None:
             qp, qs = _heads(q, "q", T, self.Hq, self.D, dev)
-            q_out = torch.empty((T, self.Hq, self.D), dtype=_bf16, device=q.device) if q_out is None else q_out
-            qo, qos = _heads(q_out, "q_out", T, self.Hq, self.D, dev)
+            if q_out is None:
+                q_out = torch.empty((T, self.Hq, self.D), dtype=_bf16, device=q.device)
+                qo, qos = q_out.data_ptr(), self.Hq * self.D
+            else:
+                qo, qos = _heads(q_out, "q_out", T, self.Hq, self.D, dev)
         d = _APPEND.pack(S, T, 0 if rows is None else self._list(rows, "rows", dev, S), self._list(cu_new, "cu_new", dev),
                          kp, ks, vp, vs, qp, qs, qo, qos, f, 2 * n, bool(interleaved), attn_factor)
         b._check(b._lib().ls_cache_append(self._h, d, _raw_stream(dev)), "ls_cache_append")
@@ -315,17 +338,23 @@ class PagedCache:
         T = q.shape[0]
         S = cu_new.numel() - 1
         dev = torch.cuda.current_device()
+        at = q.device
         if o is None:
-            o = torch.empty((T, self.Hq, self.D), dtype=_bf16, device=q.device)
+            o = torch.empty((T, self.Hq, self.D), dtype=_bf16, device=at)
+            op = o.data_ptr()
+        else:
+            op = _ptr(o, "o", _bf16, (T, self.Hq, self.D), dev)
         if lse is None:
-            lse = torch.empty((T, self.Hq), dtype=_f32, device=q.device)
+            lse = torch.empty((T, self.Hq), dtype=_f32, device=at)
+            lp = lse.data_ptr()
+        else:
+            lp = _ptr(lse, "lse", _f32, (T, self.Hq), dev)
         if workspace is None:
             workspace = torch.empty(max(self.attn_workspace_bytes(S, T, max_new, max_len), 16), dtype=_u8,
-                                    device=q.device)
+                                    device=at)
         qp, qs = _heads(q, "q", T, self.Hq, self.D, dev)
         d = _ATTN.pack(S, T, 0 if rows is None else self._list(rows, "rows", dev, S), self._list(cu_new, "cu_new", dev),
-                       max_new, max_len, qp, qs, _ptr(o, "o", _bf16, (T, self.Hq, self.D), dev),
-                       _ptr(lse, "lse", _f32, (T, self.Hq), dev), group,
+                       max_new, max_len, qp, qs, op, lp, group,
                        0 if shared_len is None else self._list(shared_len, "shared_len", dev, S // max(group, 1)))
         b._check(b._lib().ls_cache_attn(self._h, d, _ptr(workspace, "workspace", _u8, None, dev), workspace.numel(),
                                         _raw_stream(dev)), "ls_cache_attn")

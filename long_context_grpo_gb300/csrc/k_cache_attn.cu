@@ -1084,7 +1084,7 @@ constexpr int kPlanSeg = sizeof(Seg) + 2 * sizeof(int);   // shared memory of a 
 
 }  // namespace
 
-CacheAttnLayout cache_attn_layout(const CacheView& c, int S, int64_t T, int max_new) {
+CacheAttnLayout cache_attn_layout(const CacheView& c, int S, int64_t T) {
   CacheAttnLayout l{};
   const int g = c.Hq / c.Hkv;
   const int64_t sms = num_sms();
@@ -1099,7 +1099,6 @@ CacheAttnLayout cache_attn_layout(const CacheView& c, int S, int64_t T, int max_
   l.max_narrow = segs * c.Hkv + 2 * 16 * sms;
   // (every token is in one segment or two, each with a last pair of Q tiles that is not full)
   l.max_wide = wide ? (T / (128 / g) + 2 * segs) * c.Hkv + 16 * sms : 0;
-  (void)max_new;
   auto put = [&](size_t* at, size_t bytes) {
     *at = l.total;
     l.total += (bytes + 255) / 256 * 256;
@@ -1128,7 +1127,7 @@ cudaError_t launch_cache_attn(const CacheAttnArgs& a, cudaStream_t s) {
   p.group = a.group;
   p.shared = a.shared;
   p.ws = ws;
-  p.l = cache_attn_layout(a.c, a.S, a.T, a.max_new);
+  p.l = cache_attn_layout(a.c, a.S, a.T);
   p.sms = num_sms();
   p.status = a.status;
   static bool attr_set[kMaxDeviceCache] = {};

@@ -235,11 +235,14 @@ __device__ __forceinline__ void join_lanes(float& m, Pair& s) {
 
 // Named barriers.  With nb buffers the streaming warps take the sums of row r + nb - 2 before they
 // wait for the gradient of row r, so at most nb - 1 <= 3 rows' parts are waiting for the scalar
-// warp, and as many gradients for the streaming warps: three ids each.  Nothing holds the
+// warps, and as many gradients for the streaming warps.  Row r uses id r modulo 4: an even
+// number, so that an id belongs to one of the two scalar warps (of three ids the warp that
+// is ahead could take the parts that the other one has not come to yet).  Nothing holds the
 // streaming warps back from running ahead of the copy warp but the copies that it issues: row
 // r + nb is requested behind its wait for row r, and the rows at the end, which wait for no
 // copy, are at most nb: nb <= 4 ids.
-enum : uint32_t { kBarParts = 1, kBarG = 4, kBarEmpty = 7, kBarCopy = 11 };
+enum : uint32_t { kBarParts = 1, kBarG = 5, kBarEmpty = 9, kBarCopy = 13 };
+constexpr int kRing = 4;            // rows whose parts and gradients are kept apart
 
 __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
@@ -290,10 +293,10 @@ __global__ void __launch_bounds__(kStream + 96, kStream == 128 ? 4 : 3)
   constexpr int kThreads = kStream + 32;        // streaming warps and one other
   extern __shared__ __align__(128) uint8_t dyn[];
   __shared__ __align__(8) uint64_t full[kMaxBufs], xbar[4];
-  __shared__ float part[3][kWarps][3];         // a warp's maximum and sum (pair)
+  __shared__ float part[kRing][kWarps][3];         // a warp's maximum and sum (pair)
   __shared__ float slot[4][kMaxCluster][3];    // a CTA's, by rank
-  __shared__ float sh_g[3], sh_c[3], sh_gy[3];
-  __shared__ int sh_used[kMaxBufs], sh_y[3];
+  __shared__ float sh_g[kRing], sh_c[kRing], sh_gy[kRing];
+  __shared__ int sh_used[kMaxBufs], sh_y[kRing];
   // Set when a bounded wait of this CTA or of a peer gave up: rows are only walked through from
   // then on, with NaN terms and gradients of zero.
   __shared__ int cl_abort;
@@ -350,8 +353,8 @@ __global__ void __launch_bounds__(kStream + 96, kStream == 128 ? 4 : 3)
     Ahead now = logits(first, token(first));
     Token next = token(first + step);
     uint32_t ux = 0;                   // rows exchanged
-    int par = who;                     // row modulo 3
-    for (int64_t row = first; row < a.T; row += step, par = par == 0 ? 2 : par - 1) {
+    int par = who;                     // row modulo kRing
+    for (int64_t row = first; row < a.T; row += step, par = (par + 2) % kRing) {
       const Token t = now.tok;
       const float xv = now.xy, ev = now.edge;
       now = logits(row + step, next);
@@ -530,14 +533,14 @@ __global__ void __launch_bounds__(kStream + 96, kStream == 128 ? 4 : 3)
       }
       __syncwarp();
       named_barrier_arrive(kBarParts + par, kThreads);
-      sum_par = par == 2 ? 0 : par + 1;
+      sum_par = (par + 1) % kRing;
       sum_buf = bi == nb - 1 ? 0 : bi + 1;
       sum_phase ^= bi == nb - 1 ? 1u : 0u;
     };
     int b = 0, par = 0;
     const int64_t ahead = (nb - 2) * ncl;
     for (int64_t row = cid; row < cid + ahead && row < a.T; row += ncl) pass1(row);
-    for (int64_t row = cid; row < a.T; row += ncl, b = b == nb - 1 ? 0 : b + 1, par = par == 2 ? 0 : par + 1) {
+    for (int64_t row = cid; row < a.T; row += ncl, b = b == nb - 1 ? 0 : b + 1, par = (par + 1) % kRing) {
       uint4* buf = reinterpret_cast<uint4*>(dyn + b * slice);
       // later rows' sums while this row's are exchanged
       if (row + ahead < a.T) pass1(row + ahead);

@@ -284,7 +284,7 @@ ls_status ls_cache_append(ls_cache_t h, const ls_cache_append_desc* d, void* str
 size_t ls_cache_attn_workspace_bytes(ls_cache_t h, int32_t S, int64_t T, int32_t max_new,
                                      int64_t max_len) {
   if (check_cache(h) != LS_OK || S < 1 || T < 1 || max_new < 1 || max_len < 1) return 0;
-  return cache_attn_layout(h->view, S, T, max_new).total;
+  return cache_attn_layout(h->view, S, T).total;
 }
 
 ls_status ls_cache_attn(ls_cache_t h, const ls_cache_attn_desc* d, void* workspace,

@@ -121,7 +121,7 @@ struct CacheAttnLayout {
   int64_t max_narrow, max_wide;                           // job list capacities
   int64_t rows_narrow, rows_wide;                         // rows of partial results
 };
-CacheAttnLayout cache_attn_layout(const CacheView& c, int S, int64_t T, int max_new);
+CacheAttnLayout cache_attn_layout(const CacheView& c, int S, int64_t T);
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, cudaStream_t s);
 
 }  // namespace ls

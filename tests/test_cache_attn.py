@@ -56,7 +56,7 @@ def check(cache, table, lens, n_new, q, o, lse, layout, rows=None, scale=None, c
         assert np.array_equal(np.isneginf(gl), none)
         assert (go[none] == 0).all()
         assert (np.abs(go - wo) <= 2 ** -8 * (np.abs(wo) + wa) + 2 ** -14 * wa + 1e-30).all(), (b, np.abs(go - wo).max())
-        assert (np.abs(gl - wl)[~none] <= 2 ** -20 * np.abs(wl[~none]) + 2e-5).all()
+        assert (np.abs(gl[~none] - wl[~none]) <= 2 ** -20 * np.abs(wl[~none]) + 2e-5).all()
         at += n
 
 
@@ -224,6 +224,38 @@ def test_far_pages_of_a_large_pool():
     c.fork(i(), i())
     c.compact()
     assert torch.equal(both[0, 0], k) and c.page_table[1, 0] == 0
+    assert ls.device_status() == (0, 0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout,ps", [("NHD", 16), ("HND", 32), ("NHD", 256), ("HND", 128)])
+@pytest.mark.parametrize("n", [1, 90])
+def test_pages_apart_from_one_another(layout, ps, n):
+    """A page stride that is no multiple of the page or its rows: the gaps are left as they were."""
+    import long_context_grpo_gb300 as ls
+    Hkv, D, N = 3, 64, 40
+    size = ps * Hkv * D
+    inner = (ps, Hkv, D) if layout == "NHD" else (Hkv, ps, D)
+    raw = [torch.full((N, size + 8), 9.0, device="cuda").to(torch.bfloat16) for _ in range(2)]
+    k, v = (x[:, :size].unflatten(1, inner) for x in raw)
+    k.copy_(torch.randn(k.shape, device="cuda"))
+    v.copy_(torch.randn(v.shape, device="cuda"))
+    L = 2 * ps + 130
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    width = -(-L // ps)
+    table = torch.from_numpy(np.random.default_rng(ps).permutation(N)[:2 * width].reshape(2, width).astype(np.int32)).cuda()
+    ref = torch.bincount(table.flatten().long(), minlength=N).int()
+    c = ls.PagedCache(k, v, table, i32(L, L - 7), ref, Hq=6, layout=layout)
+    kn, vn = (torch.randn(2 * n, Hkv, D, device="cuda").to(torch.bfloat16) for _ in range(2))
+    c.append(kn, vn, cu([n, n]))
+    q = torch.randn(2 * n, 6, D, device="cuda").to(torch.bfloat16)
+    o, lse = c.attn(q, cu([n, n]), max_new=n, max_len=L)
+    check(c, table.cpu().numpy(), [L, L - 7], [n, n], q, o, lse, layout)
+    before = [sequence(x, table[0].cpu().numpy(), L, layout) for x in (k, v)]
+    c.compact()
+    for x, y in zip((k, v), before):
+        assert np.array_equal(sequence(x, c.page_table[0].cpu().numpy(), L, layout), y)
+    assert all((x[:, size:] == 9).all() for x in raw)
     assert ls.device_status() == (0, 0)
 
 

@@ -62,6 +62,52 @@ def test_against_float64(T, V, pad, kl):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,V,pad", [(20000, 600, 1), (9000, 3000, 0), (12000, 5000, 1), (9000, 8000, 0), (5000, 17001, 0),
+                                     (4000, 32000, 8), (3000, 45000, 1), (1500, 75000, 0), (1200, 100000, 64),
+                                     (1000, 151936, 1), (700, 300000, 0)])
+@pytest.mark.parametrize("masked", [0.0, 0.5, 0.97])
+def test_many_rows_a_block_with_tokens_left_out(T, V, pad, masked):
+    """Every row of long runs against float64 on the GPU, twice: rows that are left out let some of a
+    block's warps run ahead of others."""
+    import long_context_grpo_gb300 as ls
+    g = torch.Generator(device="cuda").manual_seed(T + V)
+    x = (torch.randn(T, V + pad, generator=g, device="cuda", dtype=torch.bfloat16) * 2)[:, :V]
+    ids = torch.randint(0, V, (T,), generator=g, device="cuda", dtype=torch.int32)
+    lp = ls.token_logp(x.contiguous(), ids)
+    old, ref = (lp + 0.25 * torch.randn(T, generator=g, device="cuda") for _ in range(2))
+    adv = torch.randn(T, generator=g, device="cuda")
+    w = (torch.rand(T, generator=g, device="cuda") >= masked).float() / T
+    call = lambda: ls.policy_loss(x, ids, old, adv, w, eps_low=0.2, eps_high=0.28, logp_ref=ref, beta=0.05, kl="k2")  # noqa: E731
+    r, again = call(), call()
+    assert all(torch.equal(a, b) for a, b in zip(r, again)) and ls.device_status() == (0, 0)
+    loss = 0.0
+    for a in range(0, T, 500):
+        i = slice(a, a + 500)
+        soft = torch.log_softmax(x[i].double(), 1)
+        y = ids[i].long()[:, None]
+        logp = soft.gather(1, y)[:, 0]
+        d, A, used = logp - old[i].double(), adv[i].double(), w[i] != 0
+        rho, kd = d.exp(), logp - ref[i].double()
+        clip = ((A > 0) & (d > np.log(1.28))) | ((A < 0) & (d < np.log(0.8)))
+        gt = torch.where(used, w[i].double() * (0.05 * kd - torch.where(clip, 0.0, rho * A)), 0.0)
+        surr = torch.where(clip, rho.clamp(0.8, 1.28) * A, rho * A)
+        loss += float((w[i].double() * (0.05 * kd * kd / 2 - surr)).sum())
+        near = ((d - np.log(1.28)).abs() < 1e-6) | ((d - np.log(0.8)).abs() < 1e-6)
+        p = soft.exp_()
+        want = -gt[:, None] * p
+        want.scatter_add_(1, y, gt[:, None])
+        # g is the difference of two fp32 terms, each within 2^-21 of itself (an exponential, two
+        # products); where they cancel that is all of g's error, and it scales the whole row
+        off = w[i].double() * (0.05 * kd.abs() + (rho * A).abs()) * 2 ** -20
+        hot = torch.zeros_like(p).scatter_(1, y, 1.0)
+        tol = want.abs() * (2 ** -8 + 2 ** -16) + gt.abs()[:, None] * p * 2 ** -16 + off[:, None] * (p + hot) * 1.01 + 1e-36
+        assert bool((((r.dlogits[i].double() - want).abs() <= tol).all(1) | near).all())
+        assert torch.equal(r.clip_mask[i].bool() | near, (clip & used) | near)
+        assert bool(((r.logp[i].double() - logp * used).abs() <= 2e-6).all())
+    assert abs(r.loss.item() - loss) <= 1e-5 * float((w.double() * rho.max()).sum()) + 1e-6
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("V,pad", [(1024, 0), (1000, 16), (333, 2)])
 def test_gradient_in_place_of_the_logits_and_untouched_padding(V, pad):
     import long_context_grpo_gb300 as ls
