@@ -446,10 +446,11 @@ struct Streams {
   Job j[2];
   int n[2];         // key tiles of each stream
 };
+// (through L1: the producer loads a job one item ahead, the other warps of the SM then find it there)
 __device__ __forceinline__ Job load_job(const Job* p) {
   Job j;
   const int4* v = reinterpret_cast<const int4*>(p);
-  const int4 x = __ldcg(v), y = __ldcg(v + 1), z = __ldcg(v + 2);
+  const int4 x = v[0], y = v[1], z = v[2];
   j.t0 = x.x; j.n_tok = x.y; j.row = x.z; j.lim = x.w;
   j.tile0 = y.x; j.n_tiles = y.y; j.key_end = y.z; j.kv = y.w;
   j.part = z.x;
@@ -458,6 +459,8 @@ __device__ __forceinline__ Job load_job(const Job* p) {
 template <bool kWide>
 __device__ __forceinline__ Streams load_streams(const AttnArgs& a, int item, int n_jobs, int qt, int g) {
   Streams s;
+  s.n[0] = s.n[1] = 0;
+  if (item >= (kWide ? n_jobs : (n_jobs + 1) / 2)) return s;
   if constexpr (kWide) {
     s.j[0] = load_job(a.jobs + item);
     s.j[1] = s.j[0];
@@ -470,7 +473,6 @@ __device__ __forceinline__ Streams load_streams(const AttnArgs& a, int item, int
   } else {
     s.j[0] = load_job(a.jobs + 2 * item);
     s.n[0] = s.j[0].n_tiles;
-    s.n[1] = 0;
     if (2 * item + 1 < n_jobs) {
       s.j[1] = load_job(a.jobs + 2 * item + 1);
       s.n[1] = s.j[1].n_tiles;
@@ -597,13 +599,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (my_box < boxes && i + my_box < w.end) set_device_status(a.status, DEV_BAD_INDEX);
       return static_cast<int>(a.c.num_pages);
     };
+    // the next item's jobs and first pages are loaded while this one's tiles are
+    Streams next = load_streams<kWide>(a, blockIdx.x, n_jobs, qt, g);
+    PageWindow next_w[2];
+    auto start_windows = [&]() {
+      if (next.n[0] > 0) next_w[0].start(a.c, next.j[0], lane);
+      if (!kWide && next.n[1] > 0) next_w[1].start(a.c, next.j[1], lane);
+    };
+    start_windows();
     for (int it = blockIdx.x; it < n_items && ok; it += gridDim.x) {
-      const Streams s = load_streams<kWide>(a, it, n_jobs, qt, g);
+      const Streams s = next;
+      PageWindow w[2] = {next_w[0], next_w[1]};
+      next = load_streams<kWide>(a, it + static_cast<int>(gridDim.x), n_jobs, qt, g);
+      start_windows();
       const int most = s.n[0] > s.n[1] ? s.n[0] : s.n[1];
       if (most == 0) continue;
-      PageWindow w[2];
-      w[0].start(a.c, s.j[0], lane);
-      if (!kWide && s.n[1] > 0) w[1].start(a.c, s.j[1], lane);
       bool q_sent = false;
       for (int j = 0; j < most && ok; ++j) {
 #pragma unroll
@@ -917,11 +927,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                   pack_bf16x2(__uint_as_float(ov[8 * i + 4]) * inv_l, __uint_as_float(ov[8 * i + 5]) * inv_l),
                   pack_bf16x2(__uint_as_float(ov[8 * i + 6]) * inv_l, __uint_as_float(ov[8 * i + 7]) * inv_l));
           } else {
-            float4* dst = reinterpret_cast<float4*>(a.part_o + prow * D + cc * 32);
+            float* dst = a.part_o + prow * D + cc * 32;
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              dst[i] = make_float4(__uint_as_float(ov[4 * i]) * inv_l, __uint_as_float(ov[4 * i + 1]) * inv_l,
-                                   __uint_as_float(ov[4 * i + 2]) * inv_l, __uint_as_float(ov[4 * i + 3]) * inv_l);
+            for (int i = 0; i < 4; ++i) {
+              float v[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(ov[8 * i + e]) * inv_l;
+              st_global_v8(dst + 8 * i, v);
+            }
           }
         }
         if (valid) {
@@ -1110,12 +1123,14 @@ CacheAttnLayout cache_attn_layout(const CacheView& c, int S, int64_t T) {
   put(&l.wide, sizeof(Job) * static_cast<size_t>(l.max_wide));
   put(&l.lse, sizeof(float) * static_cast<size_t>(l.rows_narrow + l.rows_wide));
   put(&l.o, sizeof(float) * static_cast<size_t>(l.rows_narrow + l.rows_wide) * c.D);
+  l.total += 256;      // offsets are from the workspace's first 256-byte boundary
   return l;
 }
 
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, cudaStream_t s) {
   const int g = a.c.Hq / a.c.Hkv;
-  uint8_t* ws = static_cast<uint8_t*>(a.ws);
+  // (the layout has room for the alignment)
+  uint8_t* ws = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(a.ws) + 255) & ~static_cast<uintptr_t>(255));
   PlanArgs p{};
   p.c = a.c;
   p.S = a.S;
