@@ -42,6 +42,12 @@ namespace ls {
 namespace {
 
 constexpr int kThreads = 384;
+// Registers of a thread: the launch gives all 168 a thread (checked); the softmax warpgroups, which hold a row of
+// 128 scores, take what the control warpgroup leaves (without the split 108 bytes of a softmax
+// thread spill: 1,024 tokens over 131,072 keys 1,966 us instead of 1,915, 12 sequences' groups
+// 51.3 instead of 47.4).
+constexpr int kRegsLaunch = 168, kRegsControl = 112, kRegsSoftmax = 192;
+static_assert(kRegsControl + 2 * kRegsSoftmax <= 3 * kRegsLaunch, "more than the launch gives");
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleLog2 = 8.0f;
@@ -439,6 +445,9 @@ struct AttnArgs {
   uint16_t* o;
   float* lse;
   uint32_t* status;
+  // o starts on a 32-byte boundary: stores of whole sectors (8 x 1,000 tokens without a past 224 us,
+  // 234 with halves; a 16-byte boundary is enough for the halves)
+  bool o_whole;
 };
 
 // The two streams of an item: narrow, jobs 2 i and 2 i + 1; wide, the Q tiles of job i.
@@ -479,6 +488,48 @@ __device__ __forceinline__ Streams load_streams(const AttnArgs& a, int item, int
     }
   }
   return s;
+}
+
+// Stream q of an item (n_tiles = 0: none).
+template <bool kWide>
+__device__ __forceinline__ Job load_stream(const AttnArgs& a, int item, int q, int n_jobs, int qt, int g) {
+  const int at = kWide ? item : 2 * item + q;
+  Job j;
+  j.n_tiles = 0;
+  if (at >= n_jobs) return j;
+  j = load_job(a.jobs + at);
+  if (kWide && q == 1) {
+    if (j.n_tok <= qt) j.n_tiles = 0;
+    j.t0 += qt;
+    j.n_tok -= qt;
+    if (j.part >= 0) j.part += qt * g;
+  } else if (kWide && j.n_tok > qt) {
+    j.n_tok = qt;
+  }
+  return j;
+}
+// What the MMA warp needs of an item: the key tiles of its streams, and their keys from the first
+// tile's first key on.
+struct Runs {
+  int n[2], keys[2];
+};
+template <bool kWide>
+__device__ __forceinline__ Runs load_runs(const AttnArgs& a, int item, int n_jobs, int qt) {
+  Runs r;
+  r.n[0] = r.n[1] = r.keys[0] = r.keys[1] = 0;
+#pragma unroll
+  for (int q = 0; q < (kWide ? 1 : 2); ++q) {
+    const int at = kWide ? item : 2 * item + q;
+    if (at >= n_jobs) continue;
+    const int4 y = reinterpret_cast<const int4*>(a.jobs + at)[1];
+    r.n[q] = y.y;
+    r.keys[q] = y.z - 128 * y.x;
+    if (kWide) {
+      r.n[1] = reinterpret_cast<const int4*>(a.jobs + at)[0].y > qt ? y.y : 0;
+      r.keys[1] = r.keys[0];
+    }
+  }
+  return r;
 }
 
 // The page indices of one stream: 64 table entries ahead in the producer warp's lanes.
@@ -566,373 +617,388 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_launch_dependents();
   pdl_wait();                 // the job lists
   const int n_jobs = __ldcg(a.n_jobs);
-  // (the first jobs' line is on its way meanwhile)
-  prefetch_l1(a.jobs + (kWide ? 1 : 2) * blockIdx.x);
   const int n_items = kWide ? n_jobs : (n_jobs + 1) / 2;
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ TMA producer (whole warp)
-    uint32_t kit = 0, vit = 0, uc = 0;
-    bool ok = true;
-    const int ps = 1 << a.c.ps_log2;
-    const int boxes = ps < 128 ? 128 / ps : 1;
-    const int box_tok = ps < 128 ? ps : 128;
-    // One 128-key tile: a lane issues one box (64 columns of the tokens of one page); one
-    // lane after the other took 185 clocks a box and held 16-token pages to half the rate.
-    const int my_box = lane / C::kBoxes, my_half = lane % C::kBoxes;
-    auto load_tile = [&](int page, const Job& j, int tile, const CUtensorMap* tm, uint8_t* dst, uint64_t* bar) {
-      if (lane == 0) mbar_arrive_expect_tx(bar, C::kTile);
-      __syncwarp();
-      if (my_box < boxes) {
-        const int slot = (128 * tile + my_box * box_tok) & (ps - 1);
-        tma_load_4d(dst + my_half * 16384 + my_box * box_tok * 128, tm, bar, 64 * my_half,
-                    a.layout == 0 ? j.kv : slot, a.layout == 0 ? slot : j.kv, page);
-      }
-      __syncwarp();
-    };
-    // The page of this lane's box of a tile; one past the pool (the map's fill: zeros) if it
-    // lies behind the sequence or the entry is none.
-    auto page_of = [&](PageWindow& w, int tile) {
-      const int i = (128 * tile) >> a.c.ps_log2;
-      const int page = w.get(i, my_box, lane);
-      if (page >= 0 && page < a.c.num_pages) return page;
-      if (my_box < boxes && i + my_box < w.end) set_device_status(a.status, DEV_BAD_INDEX);
-      return static_cast<int>(a.c.num_pages);
-    };
-    // the next item's jobs and first pages are loaded while this one's tiles are
-    Streams next = load_streams<kWide>(a, blockIdx.x, n_jobs, qt, g);
-    PageWindow next_w[2];
-    auto start_windows = [&]() {
-      if (next.n[0] > 0) next_w[0].start(a.c, next.j[0], lane);
-      if (!kWide && next.n[1] > 0) next_w[1].start(a.c, next.j[1], lane);
-    };
-    start_windows();
-    for (int it = blockIdx.x; it < n_items && ok; it += gridDim.x) {
-      const Streams s = next;
-      PageWindow w[2] = {next_w[0], next_w[1]};
-      next = load_streams<kWide>(a, it + static_cast<int>(gridDim.x), n_jobs, qt, g);
+  if (warp < 4) {
+    setreg_dec<kRegsControl>();
+    if (warp == 0) {
+      // ------------------------------------------------------------ TMA producer (whole warp)
+      uint32_t kit = 0, vit = 0, uc = 0;
+      bool ok = true;
+      const int ps = 1 << a.c.ps_log2;
+      const int boxes = ps < 128 ? 128 / ps : 1;
+      const int box_tok = ps < 128 ? ps : 128;
+      // One 128-key tile: a lane issues one box (64 columns of the tokens of one page); one
+      // lane after the other took 185 clocks a box and held 16-token pages to half the rate.
+      const int my_box = lane / C::kBoxes, my_half = lane % C::kBoxes;
+      auto load_tile = [&](int page, const Job& j, int tile, const CUtensorMap* tm, uint8_t* dst, uint64_t* bar) {
+        if (lane == 0) mbar_arrive_expect_tx(bar, C::kTile);
+        __syncwarp();
+        if (my_box < boxes) {
+          const int slot = (128 * tile + my_box * box_tok) & (ps - 1);
+          tma_load_4d(dst + my_half * 16384 + my_box * box_tok * 128, tm, bar, 64 * my_half,
+                      a.layout == 0 ? j.kv : slot, a.layout == 0 ? slot : j.kv, page);
+        }
+        __syncwarp();
+      };
+      // The page of this lane's box of a tile; one past the pool (the map's fill: zeros) if it
+      // lies behind the sequence or the entry is none.
+      auto page_of = [&](PageWindow& w, int tile) {
+        const int i = (128 * tile) >> a.c.ps_log2;
+        const int page = w.get(i, my_box, lane);
+        if (page >= 0 && page < a.c.num_pages) return page;
+        if (my_box < boxes && i + my_box < w.end) set_device_status(a.status, DEV_BAD_INDEX);
+        return static_cast<int>(a.c.num_pages);
+      };
+      // the next item's jobs and first pages are loaded while this one's tiles are
+      Streams next = load_streams<kWide>(a, blockIdx.x, n_jobs, qt, g);
+      PageWindow next_w[2];
+      auto start_windows = [&]() {
+        if (next.n[0] > 0) next_w[0].start(a.c, next.j[0], lane);
+        if (!kWide && next.n[1] > 0) next_w[1].start(a.c, next.j[1], lane);
+      };
       start_windows();
-      const int most = s.n[0] > s.n[1] ? s.n[0] : s.n[1];
-      if (most == 0) continue;
-      bool q_sent = false;
-      for (int j = 0; j < most && ok; ++j) {
+      for (int it = blockIdx.x; it < n_items && ok; it += gridDim.x) {
+        const Streams s = next;
+        PageWindow w[2] = {next_w[0], next_w[1]};
+        next = load_streams<kWide>(a, it + static_cast<int>(gridDim.x), n_jobs, qt, g);
+        start_windows();
+        const int most = s.n[0] > s.n[1] ? s.n[0] : s.n[1];
+        if (most == 0) continue;
+        bool q_sent = false;
+        for (int j = 0; j < most && ok; ++j) {
 #pragma unroll
-        for (int q = 0; q < (kWide ? 1 : 2); ++q) {
-          if (!ok || j >= s.n[q]) continue;
-          const uint32_t ks = kit % C::kN;
-          if (kit >= static_cast<uint32_t>(C::kN))
-            ok = __all_sync(0xffffffffu, mbar_wait(&bars[C::kBarKEmpty + ks], ((kit / C::kN) - 1) & 1u, a.status, vabort));
-          if (!ok) break;
-          const int page = page_of(w[q], s.j[q].tile0 + j);
-          load_tile(page, s.j[q], s.j[q].tile0 + j, &tm_k, smem + C::kOffK + ks * C::kTile, &bars[C::kBarKFull + ks]);
-          ++kit;
-          if (!q_sent) {
-            // Q goes behind the first K tile: its buffer is free once the last item's scores are done
-            q_sent = true;
-            if (uc > 0) ok = __all_sync(0xffffffffu, mbar_wait(&bars[C::kBarQEmpty], (uc - 1) & 1u, a.status, vabort));
+          for (int q = 0; q < (kWide ? 1 : 2); ++q) {
+            if (!ok || j >= s.n[q]) continue;
+            const uint32_t ks = kit % C::kN;
+            if (kit >= static_cast<uint32_t>(C::kN))
+              ok = __all_sync(0xffffffffu, mbar_wait(&bars[C::kBarKEmpty + ks], ((kit / C::kN) - 1) & 1u, a.status, vabort));
             if (!ok) break;
-            ++uc;
-            const int nq = (s.n[0] > 0 ? 1 : 0) + (s.n[1] > 0 ? 1 : 0);
-            if (lane == 0) mbar_arrive_expect_tx(&bars[C::kBarQFull], static_cast<uint32_t>(nq * C::kBoxes * 128 * g * qt));
-            __syncwarp();
-            if (lane < 2 * C::kBoxes) {
-              const int qq = lane / C::kBoxes, b = lane % C::kBoxes;
-              if ((qq ? s.n[1] : s.n[0]) > 0)
-                tma_load_3d(smem + qq * C::kQTile + b * C::kQBox, &tm_q, &bars[C::kBarQFull], 64 * b,
-                            (qq ? s.j[1].kv : s.j[0].kv) * g, qq ? s.j[1].t0 : s.j[0].t0);
+            const int page = page_of(w[q], s.j[q].tile0 + j);
+            load_tile(page, s.j[q], s.j[q].tile0 + j, &tm_k, smem + C::kOffK + ks * C::kTile, &bars[C::kBarKFull + ks]);
+            ++kit;
+            if (!q_sent) {
+              // Q goes behind the first K tile: its buffer is free once the last item's scores are done
+              q_sent = true;
+              if (uc > 0) ok = __all_sync(0xffffffffu, mbar_wait(&bars[C::kBarQEmpty], (uc - 1) & 1u, a.status, vabort));
+              if (!ok) break;
+              ++uc;
+              const int nq = (s.n[0] > 0 ? 1 : 0) + (s.n[1] > 0 ? 1 : 0);
+              if (lane == 0) mbar_arrive_expect_tx(&bars[C::kBarQFull], static_cast<uint32_t>(nq * C::kBoxes * 128 * g * qt));
+              __syncwarp();
+              if (lane < 2 * C::kBoxes) {
+                const int qq = lane / C::kBoxes, b = lane % C::kBoxes;
+                if ((qq ? s.n[1] : s.n[0]) > 0)
+                  tma_load_3d(smem + qq * C::kQTile + b * C::kQBox, &tm_q, &bars[C::kBarQFull], 64 * b,
+                              (qq ? s.j[1].kv : s.j[0].kv) * g, qq ? s.j[1].t0 : s.j[0].t0);
+              }
             }
-          }
-          const uint32_t vs = vit % C::kN;
-          if (vit >= static_cast<uint32_t>(C::kN))
-            ok = __all_sync(0xffffffffu, mbar_wait(&bars[C::kBarVEmpty + vs], ((vit / C::kN) - 1) & 1u, a.status, vabort));
-          if (!ok) break;
-          load_tile(page, s.j[q], s.j[q].tile0 + j, &tm_v, smem + C::kOffV + vs * C::kTile, &bars[C::kBarVFull + vs]);
-          ++vit;
-        }
-      }
-    }
-    if (!ok) {
-      *vabort = 1;
-      // drain this warp's own copies still in flight before the CTA may exit
-      for (uint32_t i = kit > static_cast<uint32_t>(C::kN) ? kit - C::kN : 0u; i < kit; ++i)
-        mbar_wait_ns(&bars[C::kBarKFull + i % C::kN], (i / C::kN) & 1u, 200000000ull);
-      for (uint32_t i = vit > static_cast<uint32_t>(C::kN) ? vit - C::kN : 0u; i < vit; ++i)
-        mbar_wait_ns(&bars[C::kBarVFull + i % C::kN], (i / C::kN) & 1u, 200000000ull);
-      if (uc > 0) mbar_wait_ns(&bars[C::kBarQFull], (uc - 1) & 1u, 200000000ull);
-    }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer (converged warp)
-    constexpr uint32_t kIdS = idesc_bf16(128, 128, false, false);
-    constexpr uint32_t kIdPV = idesc_bf16(128, D, false, true);
-    const uint64_t dQ0 = smem_desc(smem_u32(smem), 16, 1024);
-    const uint64_t dK0 = smem_desc(smem_u32(smem + C::kOffK), 16, 1024);
-    const uint64_t dV0 = smem_desc(smem_u32(smem + C::kOffV), 16384, 1024);
-    uint32_t kit = 0, vit = 0, uc = 0;
-    uint32_t pph = 0u;               // bit q: parity of the next p_full waits of stream q
-    uint32_t uq[2] = {0u, 0u};       // jobs done per stream
-    bool ok = true;
-    auto wait = [&](int bar, uint32_t parity) {
-      return mbar_wait_warp<20u>(&bars[bar], parity, a.status, vabort);
-    };
-    auto issue_s = [&](int q, uint32_t kstage) {
-      const uint64_t qa = dQ0 + static_cast<uint64_t>((q * C::kQTile) >> 4);
-      const uint64_t ka = dK0 + static_cast<uint64_t>((kstage * C::kTile) >> 4);
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint64_t qo = static_cast<uint64_t>(((kk >> 2) * C::kQBox + (kk & 3) * 32) >> 4);
-        const uint64_t ko = static_cast<uint64_t>(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4);
-        mma_bf16_ss_w(tmem + C::col_s(q), qa + qo, ka + ko, kIdS, kk > 0 ? 1u : 0u);
-      }
-    };
-    auto issue_pv = [&](int q, uint32_t vstage, int h, bool acc) {
-      const uint64_t va = dV0 + static_cast<uint64_t>((vstage * C::kTile) >> 4);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int kk = 4 * h + i;
-        mma_bf16_ts_w(tmem + C::col_o(q), tmem + C::col_s(q) + kk * 8,
-                      va + static_cast<uint64_t>((kk * 2048) >> 4), kIdPV, (acc || i > 0) ? 1u : 0u);
-      }
-    };
-    // Clear the V rows from `from` on (behind the sequence's end; whatever they hold must not
-    // meet a probability of zero).
-    auto clear_v = [&](uint32_t vstage, int from) {
-      uint8_t* v = smem + C::kOffV + vstage * C::kTile;
-      for (int i = lane; i < (128 - from) * 8; i += 32)
-#pragma unroll
-        for (int b = 0; b < C::kBoxes; ++b)
-          *reinterpret_cast<uint4*>(v + b * 16384 + from * 128 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
-      fence_proxy_async_smem();
-      __syncwarp();
-    };
-    for (int it = blockIdx.x; it < n_items && ok; it += gridDim.x) {
-      const Streams s = load_streams<kWide>(a, it, n_jobs, qt, g);
-      const int most = s.n[0] > s.n[1] ? s.n[0] : s.n[1];
-      if (most == 0) continue;
-      ok = wait(C::kBarQFull, uc & 1u);
-      if (!ok) break;
-      tc_fence_after();
-      // Q is free for the next item once the last scores are taken
-      int scores = s.n[0] + s.n[1];
-      // first scores
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        if (!ok || s.n[q] == 0) continue;
-        const uint32_t ks = kit % C::kN;
-        if (!kWide || q == 0) {
-          ok = wait(C::kBarKFull + ks, (kit / C::kN) & 1u);
-          if (!ok) break;
-          tc_fence_after();
-        }
-        issue_s(q, ks);
-        mma_commit_w(&bars[C::kBarSFull + q]);
-        if (--scores == 0) mma_commit_w(&bars[C::kBarQEmpty]);
-        if (!kWide || q == 1 || s.n[1] == 0) {
-          mma_commit_w(&bars[C::kBarKEmpty + ks]);
-          ++kit;
-        }
-      }
-      for (int j = 0; j < most && ok; ++j) {
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          if (!ok || j >= s.n[q]) continue;
-          const uint32_t vs = vit % C::kN;
-          if (!kWide || q == 0) {
-            ok = wait(C::kBarVFull + vs, (vit / C::kN) & 1u);
+            const uint32_t vs = vit % C::kN;
+            if (vit >= static_cast<uint32_t>(C::kN))
+              ok = __all_sync(0xffffffffu, mbar_wait(&bars[C::kBarVEmpty + vs], ((vit / C::kN) - 1) & 1u, a.status, vabort));
             if (!ok) break;
-            const int left = s.j[q].key_end - 128 * (s.j[q].tile0 + j);
-            if (left < 128) clear_v(vs, left < 0 ? 0 : left);
-          }
-          ok = wait(C::kBarPFull + 2 * q, (pph >> q) & 1u);
-          if (!ok) break;
-          if (j == 0 && uq[q] > 0) {
-            ok = wait(C::kBarOFree + q, (uq[q] - 1) & 1u);
-            if (!ok) break;
-          }
-          tc_fence_after();
-          issue_pv(q, vs, 0, j > 0);
-          ok = wait(C::kBarPFull + 2 * q + 1, (pph >> q) & 1u);
-          if (!ok) break;
-          pph ^= 1u << q;
-          tc_fence_after();
-          issue_pv(q, vs, 1, true);
-          if (j + 1 == s.n[q]) mma_commit_w(&bars[C::kBarODone + q]);
-          if (!kWide || q == 1 || s.n[1] == 0) {
-            mma_commit_w(&bars[C::kBarVEmpty + vs]);
+            load_tile(page, s.j[q], s.j[q].tile0 + j, &tm_v, smem + C::kOffV + vs * C::kTile, &bars[C::kBarVFull + vs]);
             ++vit;
           }
-          if (j + 1 < s.n[q]) {
-            const uint32_t ks = kit % C::kN;
-            if (!kWide || q == 0) {
-              ok = wait(C::kBarKFull + ks, (kit / C::kN) & 1u);
-              if (!ok) break;
-              tc_fence_after();
-            }
-            issue_s(q, ks);
-            mma_commit_w(&bars[C::kBarSFull + q]);
-            if (--scores == 0) mma_commit_w(&bars[C::kBarQEmpty]);
-            if (!kWide || q == 1 || s.n[1] == 0) {
-              mma_commit_w(&bars[C::kBarKEmpty + ks]);
-              ++kit;
-            }
-          }
         }
       }
-      if (!ok) break;
-      if (s.n[0] > 0) ++uq[0];
-      if (s.n[1] > 0) ++uq[1];
-      ++uc;
-    }
-    if (!ok) *vabort = 1;
-    // every MMA (and the arrivals committed behind it) has landed before exit
-    mma_commit_w(&bars[C::kBarDrain]);
-    mbar_wait_ns(&bars[C::kBarDrain], 0u, ok ? LS_WAIT_LIMIT_NS : 200000000ull);
-  } else if (warp >= 4 && (kWide || (warp & 3) < kNarrowRows / 32)) {
-    // ------------------------------------------------------------ softmax of stream q
-    const int q = (warp - 4) >> 2;
-    const int quarter = warp & 3;
-    const int row = quarter * 32 + lane;
-    const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    const uint32_t colS = C::col_s(q), colO = C::col_o(q);
-    const float c2 = a.scale * kLog2e;
-    uint32_t sph = 0u, uq = 0u;
-    bool ok = true;
-    for (int it = blockIdx.x; it < n_items && ok; it += gridDim.x) {
-      const Streams s = load_streams<kWide>(a, it, n_jobs, qt, g);
-      const Job w = q ? s.j[1] : s.j[0];
-      const int n = q ? s.n[1] : s.n[0];
-      if (n == 0) continue;
-      const int tok = row / g;
-      const bool valid = tok < w.n_tok && row < g * qt;
-      const bool any = __any_sync(0xffffffffu, valid);
-      const int t = w.t0 + tok;
-      // rows that are not used need no mask: what they hold reaches no other row
-      int limit = INT_MAX;
-      if (valid) limit = w.lim == INT_MIN ? __ldcg(a.lims + t) : w.lim + t;
-      limit -= 128 * w.tile0;
-      float m_run = -INFINITY, l = 0.0f;
-      for (int j = 0; j < n; ++j) {
-        ok = mbar_wait_hint<20u>(&bars[C::kBarSFull + q], sph, a.status, vabort);
-        ok = __all_sync(0xffffffffu, ok);
+      if (!ok) {
+        *vabort = 1;
+        // drain this warp's own copies still in flight before the CTA may exit
+        for (uint32_t i = kit > static_cast<uint32_t>(C::kN) ? kit - C::kN : 0u; i < kit; ++i)
+          mbar_wait_ns(&bars[C::kBarKFull + i % C::kN], (i / C::kN) & 1u, 200000000ull);
+        for (uint32_t i = vit > static_cast<uint32_t>(C::kN) ? vit - C::kN : 0u; i < vit; ++i)
+          mbar_wait_ns(&bars[C::kBarVFull + i % C::kN], (i / C::kN) & 1u, 200000000ull);
+        if (uc > 0) mbar_wait_ns(&bars[C::kBarQFull], (uc - 1) & 1u, 200000000ull);
+      }
+    } else if (warp == 1) {
+      // ------------------------------------------------------------ MMA issuer (converged warp)
+      constexpr uint32_t kIdS = idesc_bf16(128, 128, false, false);
+      constexpr uint32_t kIdPV = idesc_bf16(128, D, false, true);
+      const uint64_t dQ0 = smem_desc(smem_u32(smem), 16, 1024);
+      const uint64_t dK0 = smem_desc(smem_u32(smem + C::kOffK), 16, 1024);
+      const uint64_t dV0 = smem_desc(smem_u32(smem + C::kOffV), 16384, 1024);
+      uint32_t kit = 0, vit = 0, uc = 0;
+      uint32_t pph = 0u;               // bit q: parity of the next p_full waits of stream q
+      uint32_t uq[2] = {0u, 0u};       // jobs done per stream
+      bool ok = true;
+      auto wait = [&](int bar, uint32_t parity) {
+        return mbar_wait_warp<20u>(&bars[bar], parity, a.status, vabort);
+      };
+      auto issue_s = [&](int q, uint32_t kstage) {
+        const uint64_t qa = dQ0 + static_cast<uint64_t>((q * C::kQTile) >> 4);
+        const uint64_t ka = dK0 + static_cast<uint64_t>((kstage * C::kTile) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint64_t qo = static_cast<uint64_t>(((kk >> 2) * C::kQBox + (kk & 3) * 32) >> 4);
+          const uint64_t ko = static_cast<uint64_t>(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4);
+          mma_bf16_ss_w(tmem + C::col_s(q), qa + qo, ka + ko, kIdS, kk > 0 ? 1u : 0u);
+        }
+      };
+      auto issue_pv = [&](int q, uint32_t vstage, int h, bool acc) {
+        const uint64_t va = dV0 + static_cast<uint64_t>((vstage * C::kTile) >> 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int kk = 4 * h + i;
+          mma_bf16_ts_w(tmem + C::col_o(q), tmem + C::col_s(q) + kk * 8,
+                        va + static_cast<uint64_t>((kk * 2048) >> 4), kIdPV, (acc || i > 0) ? 1u : 0u);
+        }
+      };
+      // Clear the V rows from `from` on (behind the sequence's end; whatever they hold must not
+      // meet a probability of zero).
+      auto clear_v = [&](uint32_t vstage, int from) {
+        uint8_t* v = smem + C::kOffV + vstage * C::kTile;
+        for (int i = lane; i < (128 - from) * 8; i += 32)
+#pragma unroll
+          for (int b = 0; b < C::kBoxes; ++b)
+            *reinterpret_cast<uint4*>(v + b * 16384 + from * 128 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async_smem();
+        __syncwarp();
+      };
+      Runs next = load_runs<kWide>(a, blockIdx.x, n_jobs, qt);
+      for (int it = blockIdx.x; it < n_items && ok; it += gridDim.x) {
+        const Runs s = next;
+        next = load_runs<kWide>(a, it + static_cast<int>(gridDim.x), n_jobs, qt);
+        const int most = s.n[0] > s.n[1] ? s.n[0] : s.n[1];
+        if (most == 0) continue;
+        ok = wait(C::kBarQFull, uc & 1u);
         if (!ok) break;
-        sph ^= 1u;
-        if (!any) {               // no row of this warp is used: what it leaves in P reaches none
-          tc_fence_after();
-          tc_fence_before();
-          mbar_arrive(&bars[C::kBarPFull + 2 * q]);
-          mbar_arrive(&bars[C::kBarPFull + 2 * q + 1]);
-          continue;
-        }
         tc_fence_after();
-        uint32_t sv[4][32];
-        tmem_ld32(lane_base + colS + 0, sv[0]);
-        tmem_ld32(lane_base + colS + 32, sv[1]);
-        tmem_ld32(lane_base + colS + 64, sv[2]);
-        tmem_ld32(lane_base + colS + 96, sv[3]);
-        tmem_ld_wait();
-        const int lim = limit - 128 * j;
-        if (lim < 128) {
+        // Q is free for the next item once the last scores are taken
+        int scores = s.n[0] + s.n[1];
+        // first scores
 #pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (c >= lim) sv[c >> 5][c & 31] = __float_as_uint(-INFINITY);
-        }
-        float mxa = -INFINITY, mxb = -INFINITY, mxc = -INFINITY, mxd = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < 128; c += 8) {
-          mxa = fmax3(mxa, __uint_as_float(sv[c >> 5][c & 31]), __uint_as_float(sv[c >> 5][(c + 1) & 31]));
-          mxb = fmax3(mxb, __uint_as_float(sv[c >> 5][(c + 2) & 31]), __uint_as_float(sv[c >> 5][(c + 3) & 31]));
-          mxc = fmax3(mxc, __uint_as_float(sv[c >> 5][(c + 4) & 31]), __uint_as_float(sv[c >> 5][(c + 5) & 31]));
-          mxd = fmax3(mxd, __uint_as_float(sv[c >> 5][(c + 6) & 31]), __uint_as_float(sv[c >> 5][(c + 7) & 31]));
-        }
-        const float mt = fmax3(mxa, mxb, fmaxf(mxc, mxd)) * c2;
-        float factor = 1.0f;
-        bool resc = false;
-        if (m_run == -INFINITY) {
-          m_run = mt;
-        } else if (mt > m_run + kRescaleLog2) {
-          factor = ex2_approx(m_run - mt);
-          l *= factor;
-          m_run = mt;
-          resc = true;
-        }
-        const float neg_m = (m_run == -INFINITY) ? 0.0f : -m_run;
-        const bool any_resc = __any_sync(0xffffffffu, resc);
-        const uint64_t c2x2 = f2_pack(c2, c2), nm2 = f2_pack(neg_m, neg_m);
-        uint64_t rs2[4] = {f2_pack(0.0f, 0.0f), f2_pack(0.0f, 0.0f), f2_pack(0.0f, 0.0f),
-                           f2_pack(0.0f, 0.0f)};
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t pw[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const int c = half * 64 + 2 * i;
-            const uint64_t e = f2_fma(f2_pack(__uint_as_float(sv[c >> 5][c & 31]),
-                                              __uint_as_float(sv[(c + 1) >> 5][(c + 1) & 31])),
-                                      c2x2, nm2);
-            float x0, x1;
-            f2_unpack(e, x0, x1);
-            const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-            rs2[i & 3] = f2_add(rs2[i & 3], f2_pack(p0, p1));
-            pw[i] = pack_bf16x2(p0, p1);
+        for (int q = 0; q < 2; ++q) {
+          if (!ok || s.n[q] == 0) continue;
+          const uint32_t ks = kit % C::kN;
+          if (!kWide || q == 0) {
+            ok = wait(C::kBarKFull + ks, (kit / C::kN) & 1u);
+            if (!ok) break;
+            tc_fence_after();
           }
-          tmem_st32(lane_base + colS + half * 32, pw);
-          if (!any_resc) {
+          issue_s(q, ks);
+          mma_commit_w(&bars[C::kBarSFull + q]);
+          if (--scores == 0) mma_commit_w(&bars[C::kBarQEmpty]);
+          if (!kWide || q == 1 || s.n[1] == 0) {
+            mma_commit_w(&bars[C::kBarKEmpty + ks]);
+            ++kit;
+          }
+        }
+        for (int j = 0; j < most && ok; ++j) {
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            if (!ok || j >= s.n[q]) continue;
+            const uint32_t vs = vit % C::kN;
+            if (!kWide || q == 0) {
+              ok = wait(C::kBarVFull + vs, (vit / C::kN) & 1u);
+              if (!ok) break;
+              const int left = s.keys[q] - 128 * j;
+              if (left < 128) clear_v(vs, left < 0 ? 0 : left);
+            }
+            ok = wait(C::kBarPFull + 2 * q, (pph >> q) & 1u);
+            if (!ok) break;
+            if (j == 0 && uq[q] > 0) {
+              ok = wait(C::kBarOFree + q, (uq[q] - 1) & 1u);
+              if (!ok) break;
+            }
+            tc_fence_after();
+            issue_pv(q, vs, 0, j > 0);
+            ok = wait(C::kBarPFull + 2 * q + 1, (pph >> q) & 1u);
+            if (!ok) break;
+            pph ^= 1u << q;
+            tc_fence_after();
+            issue_pv(q, vs, 1, true);
+            if (j + 1 == s.n[q]) mma_commit_w(&bars[C::kBarODone + q]);
+            if (!kWide || q == 1 || s.n[1] == 0) {
+              mma_commit_w(&bars[C::kBarVEmpty + vs]);
+              ++vit;
+            }
+            if (j + 1 < s.n[q]) {
+              const uint32_t ks = kit % C::kN;
+              if (!kWide || q == 0) {
+                ok = wait(C::kBarKFull + ks, (kit / C::kN) & 1u);
+                if (!ok) break;
+                tc_fence_after();
+              }
+              issue_s(q, ks);
+              mma_commit_w(&bars[C::kBarSFull + q]);
+              if (--scores == 0) mma_commit_w(&bars[C::kBarQEmpty]);
+              if (!kWide || q == 1 || s.n[1] == 0) {
+                mma_commit_w(&bars[C::kBarKEmpty + ks]);
+                ++kit;
+              }
+            }
+          }
+        }
+        if (!ok) break;
+        if (s.n[0] > 0) ++uq[0];
+        if (s.n[1] > 0) ++uq[1];
+        ++uc;
+      }
+      if (!ok) *vabort = 1;
+      // every MMA (and the arrivals committed behind it) has landed before exit
+      mma_commit_w(&bars[C::kBarDrain]);
+      mbar_wait_ns(&bars[C::kBarDrain], 0u, ok ? LS_WAIT_LIMIT_NS : 200000000ull);
+    }
+  } else {
+    setreg_inc<kRegsSoftmax>();
+    if (kWide || (warp & 3) < kNarrowRows / 32) {
+      // ------------------------------------------------------------ softmax of stream q
+      const int q = (warp - 4) >> 2;
+      const int quarter = warp & 3;
+      const int row = quarter * 32 + lane;
+      const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+      const uint32_t colS = C::col_s(q), colO = C::col_o(q);
+      const float c2 = a.scale * kLog2e;
+      const int tok = row / g;
+      uint32_t sph = 0u, uq = 0u;
+      bool ok = true;
+      for (int it = blockIdx.x; it < n_items && ok; it += gridDim.x) {
+        const Job w = load_stream<kWide>(a, it, q, n_jobs, qt, g);
+        const int n = w.n_tiles;
+        if (n == 0) continue;
+        const bool valid = tok < w.n_tok && row < g * qt;
+        const bool any = __any_sync(0xffffffffu, valid);
+        const int t = w.t0 + tok;
+        // rows that are not used need no mask: what they hold reaches no other row
+        int limit = INT_MAX;
+        if (valid) limit = w.lim == INT_MIN ? __ldcg(a.lims + t) : w.lim + t;
+        limit -= 128 * w.tile0;
+        float m_run = -INFINITY, l = 0.0f;
+        for (int j = 0; j < n; ++j) {
+          ok = mbar_wait_hint<20u>(&bars[C::kBarSFull + q], sph, a.status, vabort);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          sph ^= 1u;
+          if (!any) {               // no row of this warp is used: what it leaves in P reaches none
+            tc_fence_after();
+            tc_fence_before();
+            mbar_arrive(&bars[C::kBarPFull + 2 * q]);
+            mbar_arrive(&bars[C::kBarPFull + 2 * q + 1]);
+            continue;
+          }
+          tc_fence_after();
+          uint32_t sv[4][32];
+          tmem_ld32(lane_base + colS + 0, sv[0]);
+          tmem_ld32(lane_base + colS + 32, sv[1]);
+          tmem_ld32(lane_base + colS + 64, sv[2]);
+          tmem_ld32(lane_base + colS + 96, sv[3]);
+          tmem_ld_wait();
+          const int lim = limit - 128 * j;
+          if (lim < 128) {
+#pragma unroll
+            for (int c = 0; c < 128; ++c)
+              if (c >= lim) sv[c >> 5][c & 31] = __float_as_uint(-INFINITY);
+          }
+          float mxa = -INFINITY, mxb = -INFINITY, mxc = -INFINITY, mxd = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 128; c += 8) {
+            mxa = fmax3(mxa, __uint_as_float(sv[c >> 5][c & 31]), __uint_as_float(sv[c >> 5][(c + 1) & 31]));
+            mxb = fmax3(mxb, __uint_as_float(sv[c >> 5][(c + 2) & 31]), __uint_as_float(sv[c >> 5][(c + 3) & 31]));
+            mxc = fmax3(mxc, __uint_as_float(sv[c >> 5][(c + 4) & 31]), __uint_as_float(sv[c >> 5][(c + 5) & 31]));
+            mxd = fmax3(mxd, __uint_as_float(sv[c >> 5][(c + 6) & 31]), __uint_as_float(sv[c >> 5][(c + 7) & 31]));
+          }
+          const float mt = fmax3(mxa, mxb, fmaxf(mxc, mxd)) * c2;
+          float factor = 1.0f;
+          bool resc = false;
+          if (m_run == -INFINITY) {
+            m_run = mt;
+          } else if (mt > m_run + kRescaleLog2) {
+            factor = ex2_approx(m_run - mt);
+            l *= factor;
+            m_run = mt;
+            resc = true;
+          }
+          const float neg_m = (m_run == -INFINITY) ? 0.0f : -m_run;
+          const bool any_resc = __any_sync(0xffffffffu, resc);
+          const uint64_t c2x2 = f2_pack(c2, c2), nm2 = f2_pack(neg_m, neg_m);
+          uint64_t rs2[4] = {f2_pack(0.0f, 0.0f), f2_pack(0.0f, 0.0f), f2_pack(0.0f, 0.0f),
+                             f2_pack(0.0f, 0.0f)};
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint32_t pw[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const int c = half * 64 + 2 * i;
+              const uint64_t e = f2_fma(f2_pack(__uint_as_float(sv[c >> 5][c & 31]),
+                                                __uint_as_float(sv[(c + 1) >> 5][(c + 1) & 31])),
+                                        c2x2, nm2);
+              float x0, x1;
+              f2_unpack(e, x0, x1);
+              const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+              rs2[i & 3] = f2_add(rs2[i & 3], f2_pack(p0, p1));
+              pw[i] = pack_bf16x2(p0, p1);
+            }
+            tmem_st32(lane_base + colS + half * 32, pw);
+            if (!any_resc) {
+              tmem_st_wait();
+              tc_fence_before();
+              mbar_arrive(&bars[C::kBarPFull + 2 * q + half]);
+            }
+          }
+          float r0, r1, r2, r3;
+          f2_unpack(f2_add(rs2[0], rs2[1]), r0, r1);
+          f2_unpack(f2_add(rs2[2], rs2[3]), r2, r3);
+          l += (r0 + r1) + (r2 + r3);
+          if (any_resc) {
+#pragma unroll
+            for (int cc = 0; cc < D / 32; ++cc) {
+              uint32_t ov[32];
+              tmem_ld32(lane_base + colO + cc * 32, ov);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * factor);
+              tmem_st32(lane_base + colO + cc * 32, ov);
+            }
             tmem_st_wait();
             tc_fence_before();
-            mbar_arrive(&bars[C::kBarPFull + 2 * q + half]);
+            mbar_arrive(&bars[C::kBarPFull + 2 * q]);
+            mbar_arrive(&bars[C::kBarPFull + 2 * q + 1]);
           }
         }
-        float r0, r1, r2, r3;
-        f2_unpack(f2_add(rs2[0], rs2[1]), r0, r1);
-        f2_unpack(f2_add(rs2[2], rs2[3]), r2, r3);
-        l += (r0 + r1) + (r2 + r3);
-        if (any_resc) {
-#pragma unroll
-          for (int cc = 0; cc < D / 32; ++cc) {
-            uint32_t ov[32];
-            tmem_ld32(lane_base + colO + cc * 32, ov);
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * factor);
-            tmem_st32(lane_base + colO + cc * 32, ov);
-          }
-          tmem_st_wait();
-          tc_fence_before();
-          mbar_arrive(&bars[C::kBarPFull + 2 * q]);
-          mbar_arrive(&bars[C::kBarPFull + 2 * q + 1]);
-        }
-      }
-      if (!ok) break;
-      ok = mbar_wait_hint<20u>(&bars[C::kBarODone + q], uq & 1u, a.status, vabort);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      tc_fence_after();
-      if (any) {
+        if (!ok) break;
+        ok = mbar_wait_hint<20u>(&bars[C::kBarODone + q], uq & 1u, a.status, vabort);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
         const int hh = row - tok * g;
         const float inv_l = (l > 0.0f) ? 1.0f / l : 0.0f;
         const int64_t out = static_cast<int64_t>(t) * a.c.Hq + w.kv * g + hh;
         const int64_t prow = static_cast<int64_t>(w.part) + row;
 #pragma unroll
-        for (int cc = 0; cc < D / 32; ++cc) {
-          uint32_t ov[32];
-          tmem_ld32(lane_base + colO + cc * 32, ov);
+        for (int cc = 0; cc < D / 64; ++cc) {
+          uint32_t ov[2][32];
+          tmem_ld32(lane_base + colO + cc * 64, ov[0]);
+          tmem_ld32(lane_base + colO + cc * 64 + 32, ov[1]);
           tmem_ld_wait();
+          if (cc + 1 == D / 64) {       // the next job's products may go to TMEM during the stores
+            tc_fence_before();
+            mbar_arrive(&bars[C::kBarOFree + q]);
+          }
           if (!valid) continue;
           if (w.part < 0) {
-            uint4* dst = reinterpret_cast<uint4*>(a.o + out * D + cc * 32);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              dst[i] = make_uint4(
-                  pack_bf16x2(__uint_as_float(ov[8 * i + 0]) * inv_l, __uint_as_float(ov[8 * i + 1]) * inv_l),
-                  pack_bf16x2(__uint_as_float(ov[8 * i + 2]) * inv_l, __uint_as_float(ov[8 * i + 3]) * inv_l),
-                  pack_bf16x2(__uint_as_float(ov[8 * i + 4]) * inv_l, __uint_as_float(ov[8 * i + 5]) * inv_l),
-                  pack_bf16x2(__uint_as_float(ov[8 * i + 6]) * inv_l, __uint_as_float(ov[8 * i + 7]) * inv_l));
-          } else {
-            float* dst = a.part_o + prow * D + cc * 32;
+            uint16_t* dst = a.o + out * D + cc * 64;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              float v[8];
+              uint32_t p[8];
 #pragma unroll
-              for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(ov[8 * i + e]) * inv_l;
+              for (int e = 0; e < 8; ++e)
+                p[e] = pack_bf16x2(__uint_as_float(ov[i >> 1][16 * (i & 1) + 2 * e]) * inv_l,
+                                   __uint_as_float(ov[i >> 1][16 * (i & 1) + 2 * e + 1]) * inv_l);
+              if (a.o_whole) {
+                st_global_v8(dst + 16 * i, p);
+              } else {
+                reinterpret_cast<uint4*>(dst + 16 * i)[0] = make_uint4(p[0], p[1], p[2], p[3]);
+                reinterpret_cast<uint4*>(dst + 16 * i)[1] = make_uint4(p[4], p[5], p[6], p[7]);
+              }
+            }
+          } else {
+            float* dst = a.part_o + prow * D + cc * 64;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              uint32_t v[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) v[e] = __float_as_uint(__uint_as_float(ov[i >> 2][8 * (i & 3) + e]) * inv_l);
               st_global_v8(dst + 8 * i, v);
             }
           }
@@ -944,12 +1010,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           else
             a.part_lse[prow] = lse2;
         }
+        ++uq;
       }
-      tc_fence_before();
-      mbar_arrive(&bars[C::kBarOFree + q]);
-      ++uq;
+      if (!ok) *vabort = 1;
     }
-    if (!ok) *vabort = 1;
   }
 
   tc_fence_before();
@@ -1087,6 +1151,11 @@ cudaError_t launch_attn(const CacheAttnArgs& a, const AttnArgs& p, cudaStream_t 
     cudaError_t e = cudaFuncSetAttribute(cache_attn_kernel<D, kWide>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
+    // the register split is of what the launch gives
+    cudaFuncAttributes f;
+    e = cudaFuncGetAttributes(&f, cache_attn_kernel<D, kWide>);
+    if (e != cudaSuccess) return e;
+    if (f.numRegs < kRegsLaunch) return cudaErrorLaunchOutOfResources;
     attr_set[dev] = true;
   }
   return launch_after(cache_attn_kernel<D, kWide>, dim3(static_cast<unsigned>(num_sms())), kThreads,
@@ -1168,6 +1237,7 @@ cudaError_t launch_cache_attn(const CacheAttnArgs& a, cudaStream_t s) {
   k.part_lse = reinterpret_cast<float*>(ws + p.l.lse);
   k.part_o = reinterpret_cast<float*>(ws + p.l.o);
   k.o = a.o;
+  k.o_whole = reinterpret_cast<uintptr_t>(a.o) % 32 == 0;
   k.lse = a.lse;
   k.status = a.status;
   k.jobs = reinterpret_cast<const Job*>(ws + p.l.narrow);

@@ -138,6 +138,24 @@ def test_a_group_with_tokens_inside_the_shared_part():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n,L", [(1, 90), (120, 700), (2, 9000)])
+@pytest.mark.parametrize("skip", [8, 16, 24])
+def test_output_on_any_16_byte_boundary(D, n, L, skip):
+    """`o` inside a larger tensor: the same bits, and nothing beside it is written."""
+    make, table = build([L] * 3, 64, 2, D, seed=L)
+    c = make(8)
+    q = torch.randn(3 * n, 8, D, device="cuda").to(torch.bfloat16)
+    want, lse = c.attn(q, cu([n] * 3), max_new=n, max_len=L)
+    check(c, table, [L] * 3, [n] * 3, q, want, lse, "NHD")
+    room = torch.full((want.numel() + 64,), 7.0, dtype=torch.bfloat16, device="cuda")
+    o = room[skip:skip + want.numel()].view(want.shape)
+    c.attn(q, cu([n] * 3), max_new=n, max_len=L, o=o)
+    assert torch.equal(o, want)
+    assert bool((room[:skip] == 7).all()) and bool((room[skip + want.numel():] == 7).all())
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("n", [1, 33])
 def test_rows_scale_strides_and_tokens_that_see_nothing(n):
     """Rows in any order and twice, q rows of a wider tensor, packed rows that no entry owns, a length below
