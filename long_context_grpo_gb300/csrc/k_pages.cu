@@ -5,6 +5,8 @@
 // ranks among the free pages, refusals) and scans the counts for as many free pages as that
 // takes; then the entries' table rows, counts and page copies run on the whole grid.  Counts
 // change by integer atomics, whose order cannot change them.
+#include <climits>
+
 #include "ls_internal.h"
 #include "ls_ops.h"
 #include "ptx.cuh"
@@ -29,23 +31,24 @@ __host__ __device__ inline int32_t* page_list(void* ws) {
   return reinterpret_cast<int32_t*>(static_cast<char*>(ws) + sizeof(Plan));
 }
 
-// Exclusive sum over the block of one int a thread; *total for all.
-__device__ __forceinline__ int block_scan(int v, int* sh /* [33] */, int* total) {
+// Exclusive sum over the block of one number a thread; *total for all.
+template <class N>
+__device__ __forceinline__ N block_scan(N v, N* sh /* [33] */, N* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int s = v;
+  N s = v;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
-    const int u = __shfl_up_sync(0xffffffffu, s, off);
+    const N u = __shfl_up_sync(0xffffffffu, s, off);
     if (lane >= off) s += u;
   }
   __syncthreads();
   if (lane == 31) sh[warp] = s;
   __syncthreads();
   if (warp == 0) {
-    int w = lane < static_cast<int>(blockDim.x >> 5) ? sh[lane] : 0;
+    N w = lane < static_cast<int>(blockDim.x >> 5) ? sh[lane] : 0;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, w, off);
+      const N u = __shfl_up_sync(0xffffffffu, w, off);
       if (lane >= off) w += u;
     }
     sh[lane] = w;
@@ -97,6 +100,7 @@ __global__ void __launch_bounds__(kMaxList) extend_plan_kernel(CacheView c, int 
                                                               const int32_t* add, Plan* plan,
                                                               int32_t* list, uint32_t* status) {
   __shared__ int sh[33];
+  __shared__ int64_t sums[33];
   __shared__ int32_t listed[kMaxList];
   const int i = threadIdx.x;
   pdl_launch_dependents();
@@ -121,9 +125,10 @@ __global__ void __launch_bounds__(kMaxList) extend_plan_kernel(CacheView c, int 
     }
     if (!ok) set_device_status(status, DEV_BAD_INDEX);
   }
-  int total;
-  const int rank = block_scan(ok ? need : 0, sh, &total);
-  const int n_free = scan_free(c.ref, c.num_pages, total, list, sh);
+  // (an entry may ask for 2^27 pages: the sum of a list passes 32 bits)
+  int64_t total;
+  const int64_t rank = block_scan<int64_t>(ok ? need : 0, sums, &total);
+  const int n_free = scan_free(c.ref, c.num_pages, static_cast<int>(total < INT_MAX ? total : INT_MAX), list, sh);
   if (i >= n) return;
   if (ok && rank + need > n_free) {
     set_device_status(status, DEV_NO_PAGES);
@@ -132,7 +137,7 @@ __global__ void __launch_bounds__(kMaxList) extend_plan_kernel(CacheView c, int 
   plan->row[i] = ok ? row : -1;
   plan->first[i] = first;
   plan->count[i] = need;
-  plan->rank[i] = rank;
+  plan->rank[i] = static_cast<int32_t>(rank);     // (fits if the entry is not left out)
   if (ok) c.len[row] = static_cast<int32_t>(grown);
 }
 

@@ -322,3 +322,20 @@ def test_refusals_of_a_live_handle():
         assert at(**kw) == 1, kw
     assert at(S=2049) == 2 and at(q=0x1008) == 4 and at(q_stride=260) == 4 and at(wsb=0) == 8
     assert ls.device_status() == (0, 0)
+
+
+@pytest.mark.gpu
+def test_a_list_that_asks_for_more_than_2_31_pages():
+    """17 rows that each ask for all their 2^27 - 1 table columns: none fits, nothing changes; a row that fits
+    before them is served."""
+    import long_context_grpo_gb300 as ls
+    width, rows, ps = (1 << 27) - 1, 18, 16
+    k = torch.zeros(40, 2, ps, 1, 64, dtype=torch.bfloat16, device="cuda")
+    table = torch.full((rows, width), -1, dtype=torch.int32, device="cuda")
+    c = ls.PagedCache(k[:, 0], k[:, 1], table, torch.zeros(rows, dtype=torch.int32, device="cuda"),
+                      torch.zeros(40, dtype=torch.int32, device="cuda"), Hq=1)
+    c.extend(torch.arange(rows, dtype=torch.int32, device="cuda"),
+             torch.tensor([20] + [width * ps] * (rows - 1), dtype=torch.int32, device="cuda"))
+    assert ls.device_status() == (7, 4)
+    assert c.seq_len.tolist() == [20] + [0] * (rows - 1) and int(c.refcount.sum()) == 2
+    assert table[0, :3].tolist() == [0, 1, -1] and int(table[1:, :64].max()) == -1
