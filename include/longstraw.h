@@ -438,8 +438,9 @@ size_t ls_cache_pages_workspace_bytes(ls_cache_t h);
  * its later entries set the device status and are left out.
  *
  * ls_cache_extend -- seq_len[rows[i]] += add[i], with pages for the new tokens.  An entry that
- *   does not fit its table row, or that the free pages left do not cover, is left out (its row
- *   unchanged) and sets the device status (4 in the word for want of pages).
+ *   does not fit its table row, or that the free pages left behind the entries before it (those
+ *   left out for want of pages included) do not cover, is left out (its row unchanged) and sets
+ *   the device status (4 in the word for want of pages).
  * ls_cache_fork -- row children[i] becomes a copy of row parents[i]: whole pages are shared, a
  *   part-filled last page is copied into a free page of its own (its filled tokens only), so
  *   both rows can grow.  A child must be empty (length 0) and no parent of this call that
@@ -465,7 +466,8 @@ ls_status ls_cache_compact(ls_cache_t src, ls_cache_t dst, int32_t* n_live, void
 /*
  * The new tokens of S sequences, packed: entry b owns packed rows cu_new[b] .. cu_new[b+1]-1
  * (cu_new device int32 [S + 1], cu_new[0] >= 0, non-decreasing; an entry may have none and is
- * then not looked at; packed rows that no entry owns are left as they were) and is table row
+ * then not looked at; packed rows that no entry owns are left as they were; offsets that fall or
+ * leave 0 .. T set the device status, and attention then does no entry) and is table row
  * rows[b] (rows device int32 [S], or NULL: row b).  seq_len counts the new tokens already (ls_cache_extend comes first):
  * token i of n new ones of a sequence of length L is at position L - n + i.
  * 1 <= S <= 2048, T >= 1 packed rows.

@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const __grid_c
   Seg* segs = reinterpret_cast<Seg*>(dyn);
   int* first[2] = {reinterpret_cast<int*>(dyn + cap * sizeof(Seg)),
                    reinterpret_cast<int*>(dyn + cap * sizeof(Seg)) + cap};
-  __shared__ int sh_max[2], sh_c[2], sh_grouped;
+  __shared__ int sh_max[2], sh_c[2], sh_grouped, sh_bad;
   __shared__ int sh_base[2];
   __shared__ float sh_work[2][kPlanWarps];
   __shared__ unsigned long long best[2];
@@ -135,6 +135,7 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const __grid_c
     sh_max[tid] = 0;
     best[tid] = ~0ull;
   }
+  if (tid == 0) sh_bad = 0;
   __syncthreads();
 
   // the entries: tokens, table row, length
@@ -144,6 +145,7 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const __grid_c
     const int row = a.rows != nullptr ? a.rows[b] : b;
     const int shared = a.group > 1 && b % a.group == 0 ? a.shared[b / a.group] : 0;
     const bool run = c0 >= 0 && c1 >= c0 && c1 <= a.T;
+    if (!run) sh_bad = 1;
     s.t0 = run ? c0 : 0;
     s.n_tok = run ? c1 - c0 : 0;
     s.row = row;
@@ -176,7 +178,12 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const __grid_c
     sh_grouped = n_groups > 0 && 2 * a.T * a.c.Hq <= a.l.rows_narrow &&
                  (a.l.rows_wide == 0 || 2 * a.T * a.c.Hq <= a.l.rows_wide);
   __syncthreads();
-  const bool grouped = sh_grouped != 0;
+  const bool grouped = sh_grouped != 0 && sh_bad == 0;
+  if (sh_bad != 0) {
+    // offsets that fall: the runs may overlap, and their jobs pass the lists; no entry is done
+    for (int b = tid; b < a.S; b += kPlanThreads) segs[b].n_tok = segs[b].tiles = 0;
+    __syncthreads();
+  }
   const int n_segs = a.S + (grouped ? n_groups : 0);
   // whether segment i's tokens are in two segments
   auto in_two = [&](int i) {
@@ -271,7 +278,9 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const __grid_c
     const int least = cls ? 8 : 2;
     C = C < least ? least : C;
     C = C > longest ? longest : C;
-    const float inv = __fdividef(1.0f, static_cast<float>(C));
+    // (fp32 quotients of up to 2^20 tiles are on the right side of an integer, or above it; more
+    // tiles than that are rounded up by a millionth, so that the capacities hold)
+    const float inv = __fdividef(longest < 1 << 20 ? 1.0f : 1.000001f, static_cast<float>(C));
     float jobs = 0.0f, rows = 0.0f;
     for (int i = lane; i < n_segs; i += 32) {
       const int tiles = segs[i].tiles, n = segs[i].n_tok;

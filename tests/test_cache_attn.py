@@ -220,6 +220,31 @@ def test_wild_rows_lengths_and_pages_are_reported(n):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("group", [1, 4])
+@pytest.mark.parametrize("offsets", ["falls", "saw", "negative", "past"])
+def test_offsets_that_are_not_a_partition_are_refused(offsets, group):
+    """Runs that overlap would make more jobs than the workspace's lists hold: no entry is done."""
+    import long_context_grpo_gb300 as ls
+    S, n, L = 64, 40, 300
+    make, table = build([L] * S, 64, 2, 64, seed=5)
+    c = make(8)
+    T = S * n
+    q = torch.randn(T, 8, 64, device="cuda").to(torch.bfloat16)
+    at = {"falls": [n * b - (200 if b == 30 else 0) for b in range(S + 1)], "saw": [T * (b % 2) for b in range(S + 1)],
+          "negative": [-1] + [n * b for b in range(1, S + 1)], "past": [n * b for b in range(S)] + [T + 1]}[offsets]
+    at = torch.tensor(at, dtype=torch.int32, device="cuda")
+    sl = torch.full((S // group,), 64, dtype=torch.int32, device="cuda") if group > 1 else None
+    o, lse = c.attn(q, at, max_new=T, max_len=L, group=group, shared_len=sl)
+    assert ls.device_status() == (7, 2)
+    own = torch.zeros(T, dtype=torch.bool, device="cuda")
+    own[:n] = offsets in ("falls", "past")
+    assert not o[own].any() and torch.isneginf(lse[own]).all()
+    want = c.attn(q, cu([n] * S), max_new=n, max_len=L)
+    check(c, table, [L] * S, [n] * S, q, *want, "NHD")
+    assert ls.device_status() == (0, 0)
+
+
+@pytest.mark.gpu
 def test_far_pages_of_a_large_pool():
     """Element offsets past 2^32: the last pages of a 9 GB pool."""
     import long_context_grpo_gb300 as ls
