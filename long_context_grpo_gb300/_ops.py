@@ -168,7 +168,10 @@ def rope(q, k, inv_freq, positions=None, pos0: int = 0, interleaved: bool = Fals
     inv_freq, token t at positions[t] (int64) or pos0 + t.  inverse=True is the gradient:
     give it d loss / d output.  q_out / k_out may be the inputs.  Returns (q_out, k_out)."""
     some = q if q is not None else k
-    if not isinstance(some, torch.Tensor) or some.dim() != 3:
+    for t in (some, k):
+        if t is not None and (not isinstance(t, torch.Tensor) or t.dim() != 3):
+            raise TypeError("q and k must be 3-D CUDA tensors")
+    if some is None:
         raise TypeError("q or k must be a 3-D CUDA tensor")
     T, _, D = some.shape
     dev = torch.cuda.current_device()
@@ -269,25 +272,24 @@ class PagedCache:
         """Lengths of `rows` grow by `add` (int32), with free pages for the new tokens."""
         dev = torch.cuda.current_device()
         ws, wp = self._pages_ws(workspace, dev)
-        n = rows.numel()
-        b._check(b._lib().ls_cache_extend(self._h, n, self._list(rows, "rows", dev), self._list(add, "add", dev, n),
-                                          wp, ws.numel(), _raw_stream(dev)), "ls_cache_extend")
+        rp, n = self._list(rows, "rows", dev), rows.numel()
+        b._check(b._lib().ls_cache_extend(self._h, n, rp, self._list(add, "add", dev, n), wp, ws.numel(),
+                                          _raw_stream(dev)), "ls_cache_extend")
 
     def fork(self, parents, children, workspace=None):
         """Empty rows `children` become copies of rows `parents`: whole pages are shared, a
         part-filled last page is copied."""
         dev = torch.cuda.current_device()
         ws, wp = self._pages_ws(workspace, dev)
-        n = parents.numel()
-        b._check(b._lib().ls_cache_fork(self._h, n, self._list(parents, "parents", dev),
-                                        self._list(children, "children", dev, n), wp, ws.numel(),
+        pp, n = self._list(parents, "parents", dev), parents.numel()
+        b._check(b._lib().ls_cache_fork(self._h, n, pp, self._list(children, "children", dev, n), wp, ws.numel(),
                                         _raw_stream(dev)), "ls_cache_fork")
 
     def free(self, rows):
         """Empties `rows`; pages that no row lists any more become free."""
         dev = torch.cuda.current_device()
-        b._check(b._lib().ls_cache_free(self._h, rows.numel(), self._list(rows, "rows", dev), _raw_stream(dev)),
-                 "ls_cache_free")
+        rp = self._list(rows, "rows", dev)
+        b._check(b._lib().ls_cache_free(self._h, rows.numel(), rp, _raw_stream(dev)), "ls_cache_free")
 
     def compact(self, into=None, n_live=None, workspace=None):
         """Moves the live pages together: in place, or into another PagedCache's pool."""
@@ -305,8 +307,8 @@ class PagedCache:
         if not isinstance(k_new, torch.Tensor) or k_new.dim() != 3:
             raise TypeError("k_new must be a 3-D CUDA tensor")
         T = k_new.shape[0]
-        S = cu_new.numel() - 1
         dev = torch.cuda.current_device()
+        cp, S = self._list(cu_new, "cu_new", dev), cu_new.numel() - 1
         kp, ks = _heads(k_new, "k_new", T, self.Hkv, self.D, dev)
         vp, vs = _heads(v_new, "v_new", T, self.Hkv, self.D, dev)
         f = n = qp = qs = qo = qos = 0
@@ -320,7 +322,7 @@ class PagedCache:
                 qo, qos = q_out.data_ptr(), self.Hq * self.D
             else:
                 qo, qos = _heads(q_out, "q_out", T, self.Hq, self.D, dev)
-        d = _APPEND.pack(S, T, 0 if rows is None else self._list(rows, "rows", dev, S), self._list(cu_new, "cu_new", dev),
+        d = _APPEND.pack(S, T, 0 if rows is None else self._list(rows, "rows", dev, S), cp,
                          kp, ks, vp, vs, qp, qs, qo, qos, f, 2 * n, bool(interleaved), attn_factor)
         b._check(b._lib().ls_cache_append(self._h, d, _raw_stream(dev)), "ls_cache_append")
         return (q_out if q is not None else None), None
@@ -336,8 +338,8 @@ class PagedCache:
         if not isinstance(q, torch.Tensor) or q.dim() != 3:
             raise TypeError("q must be a 3-D CUDA tensor")
         T = q.shape[0]
-        S = cu_new.numel() - 1
         dev = torch.cuda.current_device()
+        cp, S = self._list(cu_new, "cu_new", dev), cu_new.numel() - 1
         at = q.device
         if o is None:
             o = torch.empty((T, self.Hq, self.D), dtype=_bf16, device=at)
@@ -353,7 +355,7 @@ class PagedCache:
             workspace = torch.empty(max(self.attn_workspace_bytes(S, T, max_new, max_len), 16), dtype=_u8,
                                     device=at)
         qp, qs = _heads(q, "q", T, self.Hq, self.D, dev)
-        d = _ATTN.pack(S, T, 0 if rows is None else self._list(rows, "rows", dev, S), self._list(cu_new, "cu_new", dev),
+        d = _ATTN.pack(S, T, 0 if rows is None else self._list(rows, "rows", dev, S), cp,
                        max_new, max_len, qp, qs, op, lp, group,
                        0 if shared_len is None else self._list(shared_len, "shared_len", dev, S // max(group, 1)))
         b._check(b._lib().ls_cache_attn(self._h, d, _ptr(workspace, "workspace", _u8, None, dev), workspace.numel(),

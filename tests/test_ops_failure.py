@@ -45,3 +45,20 @@ def test_kernel_times_of_the_group_operators():
     finally:
         ls.timing_enable(False)
     assert got["rope"][1] == 1 and got["rope"][0] > 0 and got["cache_attn"][1] == 0
+
+
+@pytest.mark.gpu
+def test_lists_and_flat_tensors_are_refused_by_name():
+    import long_context_grpo_gb300 as ls
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    both = torch.randn(8, 2, 16, 1, 64, device="cuda").to(torch.bfloat16)
+    c = ls.PagedCache(both[:, 0], both[:, 1], i32([0, 0], [0, 0]), i32(0, 0), i32(*[0] * 8), Hq=2)
+    x = torch.randn(4, 2, 64, device="cuda").to(torch.bfloat16)
+    kv = x[:, :1].contiguous()
+    f, _ = ls.rope_freqs(64)
+    for name, fn in [("rows", lambda: c.extend([0], [4])), ("parents", lambda: c.fork([0], [1])), ("rows", lambda: c.free([0])),
+                     ("cu_new", lambda: c.append(kv, kv, [0, 4])), ("cu_new", lambda: c.attn(x, [0, 4], 4, 4)),
+                     ("q and k", lambda: ls.rope(x, kv.view(-1), f)), ("q or k", lambda: ls.rope(None, None, f)),
+                     ("rows", lambda: c.free(i32([0, 1]).view(1, 2)))]:
+        with pytest.raises(TypeError, match=name):
+            fn()
