@@ -60,36 +60,70 @@ __device__ __forceinline__ N block_scan(N v, N* sh /* [33] */, N* total) {
 
 constexpr int kScanPer = 8;          // pages of a thread in one step of a scan
 
+// The counts of a thread's pages in one step of a scan.
+struct Counts {
+  int r[kScanPer];
+};
+__device__ __forceinline__ Counts load_counts(const int32_t* ref, int64_t pages, int64_t p0) {
+  const int64_t p = p0 + threadIdx.x * kScanPer;
+  Counts c;
+#pragma unroll
+  for (int k = 0; k < kScanPer; ++k) c.r[k] = p + k < pages ? __ldcg(ref + p + k) : 1;
+  return c;
+}
+
 // list[] = the lowest pages whose count is 0, in ascending order, at least `want` of them if there
-// are as many (the scan stops there); returns how many are listed.  Whole block.
-__device__ int scan_free(const int32_t* ref, int64_t pages, int want, int32_t* list, int* sh) {
+// are as many (the scan stops there); returns how many are listed.  Whole block; c: the first
+// step's counts (loaded while the list is read).
+__device__ int scan_free(Counts c, const int32_t* ref, int64_t pages, int want, int32_t* list, int* sh) {
   int base = 0;
   for (int64_t p0 = 0; p0 < pages && base < want; p0 += kScanThreads * kScanPer) {
-    const int64_t p = p0 + threadIdx.x * kScanPer;
+    if (p0 > 0) c = load_counts(ref, pages, p0);
     uint32_t bits = 0;
-    int r[kScanPer];
 #pragma unroll
-    for (int k = 0; k < kScanPer; ++k) r[k] = p + k < pages ? __ldcg(ref + p + k) : 1;
-#pragma unroll
-    for (int k = 0; k < kScanPer; ++k) bits |= r[k] == 0 ? 1u << k : 0u;
+    for (int k = 0; k < kScanPer; ++k) bits |= c.r[k] == 0 ? 1u << k : 0u;
     int total;
     int at = base + block_scan(__popc(bits), sh, &total);
 #pragma unroll
     for (int k = 0; k < kScanPer; ++k)
-      if (bits & (1u << k)) list[at++] = static_cast<int32_t>(p + k);
+      if (bits & (1u << k)) list[at++] = static_cast<int32_t>(p0 + threadIdx.x * kScanPer + k);
     base += total;
   }
   __syncthreads();
   return base;
 }
 
-// Whether list[i] stands before position i too (the list in shared memory).
-__device__ __forceinline__ bool listed_before(const int32_t* list, int i) {
-  const int x = list[i];
-  for (int j = 0; j < i; ++j)
-    if (list[j] == x) return true;
-  return false;
-}
+// The first position of every row of a list: a hash table of twice as many slots as entries, so
+// that an entry costs a few probes instead of a comparison with every earlier one.  (With this, the
+// first counts loaded ahead and the entries' plan read at once 128 rows are freed and forked in
+// 14.5 us, without in 18.7.)  clear, sync, put, sync, first.
+struct FirstAt {
+  int32_t key[2 * kMaxList], at[2 * kMaxList];
+  __device__ __forceinline__ void clear() {
+    for (int i = threadIdx.x; i < 2 * kMaxList; i += blockDim.x) {
+      key[i] = -1;
+      at[i] = kMaxList;
+    }
+  }
+  static __device__ __forceinline__ uint32_t slot_of(int32_t row) {
+    return (static_cast<uint32_t>(row) * 2654435761u >> 16) % (2 * kMaxList);
+  }
+  // (rows are not negative)
+  __device__ __forceinline__ void put(int32_t row, int i) {
+    uint32_t x = slot_of(row);
+    for (int n = 0; n < 2 * kMaxList; ++n, x = (x + 1) % (2 * kMaxList)) {
+      const int32_t k = atomicCAS(&key[x], -1, row);
+      if (k != -1 && k != row) continue;
+      atomicMin(&at[x], i);
+      return;
+    }
+  }
+  __device__ __forceinline__ int first(int32_t row) const {
+    uint32_t x = slot_of(row);
+    for (int n = 0; n < 2 * kMaxList && key[x] != row; ++n) x = (x + 1) % (2 * kMaxList);
+    return at[x];
+  }
+};
 
 __device__ __forceinline__ bool good_len(const CacheView& c, int64_t len) {
   return len >= 0 && len <= (static_cast<int64_t>(c.width) << c.ps_log2);
@@ -101,20 +135,25 @@ __global__ void __launch_bounds__(kMaxList) extend_plan_kernel(CacheView c, int 
                                                               int32_t* list, uint32_t* status) {
   __shared__ int sh[33];
   __shared__ int64_t sums[33];
-  __shared__ int32_t listed[kMaxList];
+  __shared__ FirstAt listed;
   const int i = threadIdx.x;
   pdl_launch_dependents();
+  const Counts counts = load_counts(c.ref, c.num_pages, 0);
+  listed.clear();
   bool ok = false;
   int row = -1, more = 0, need = 0, first = 0;
   int64_t len = 0, grown = 0;
   if (i < n) {
-    listed[i] = row = rows[i];
+    row = rows[i];
     more = add[i];
-    if (row >= 0 && row < c.num_rows) len = c.len[row];
+    if (row < 0 || row >= c.num_rows) row = -1;
+    if (row >= 0) len = c.len[row];
   }
   __syncthreads();
+  if (row >= 0) listed.put(row, i);
+  __syncthreads();
   if (i < n) {
-    if (row >= 0 && row < c.num_rows && more >= 0 && !listed_before(listed, i)) {
+    if (row >= 0 && more >= 0 && listed.first(row) == i) {
       grown = len + more;
       if (good_len(c, len) && good_len(c, grown)) {
         ok = true;
@@ -128,7 +167,7 @@ __global__ void __launch_bounds__(kMaxList) extend_plan_kernel(CacheView c, int 
   // (an entry may ask for 2^27 pages: the sum of a list passes 32 bits)
   int64_t total;
   const int64_t rank = block_scan<int64_t>(ok ? need : 0, sums, &total);
-  const int n_free = scan_free(c.ref, c.num_pages, static_cast<int>(total < INT_MAX ? total : INT_MAX), list, sh);
+  const int n_free = scan_free(counts, c.ref, c.num_pages, static_cast<int>(total < INT_MAX ? total : INT_MAX), list, sh);
   if (i >= n) return;
   if (ok && rank + need > n_free) {
     set_device_status(status, DEV_NO_PAGES);
@@ -145,9 +184,8 @@ __global__ void __launch_bounds__(kCopyThreads) extend_kernel(CacheView c, const
                                                              const int32_t* list) {
   const int i = blockIdx.x;
   pdl_wait();
-  const int row = plan->row[i];
+  const int row = plan->row[i], first = plan->first[i], count = plan->count[i], rank = plan->rank[i];
   if (row < 0) return;
-  const int first = plan->first[i], count = plan->count[i], rank = plan->rank[i];
   for (int j = threadIdx.x; j < count; j += kCopyThreads) {
     const int page = list[rank + j];
     c.table[static_cast<int64_t>(row) * c.width + first + j] = page;
@@ -160,14 +198,16 @@ __global__ void __launch_bounds__(kMaxList) fork_plan_kernel(CacheView c, int n,
                                                             const int32_t* children, Plan* plan,
                                                             int32_t* list, uint32_t* status) {
   __shared__ int sh[33];
-  __shared__ int32_t listed[kMaxList];
+  __shared__ FirstAt listed;
   const int i = threadIdx.x;
   pdl_launch_dependents();
+  const Counts counts = load_counts(c.ref, c.num_pages, 0);
+  listed.clear();
   bool ok = false;
   int child = -1, parent = -1;
   int64_t len = 0;
   if (i < n) {
-    listed[i] = child = children[i];
+    child = children[i];
     parent = parents[i];
     ok = child >= 0 && child < c.num_rows && parent >= 0 && parent < c.num_rows;
     if (ok) {
@@ -176,8 +216,11 @@ __global__ void __launch_bounds__(kMaxList) fork_plan_kernel(CacheView c, int n,
     }
   }
   __syncthreads();
+  const bool row = child >= 0 && child < c.num_rows;
+  if (row) listed.put(child, i);
+  __syncthreads();
   if (i < n) {
-    ok = ok && !listed_before(listed, i);
+    ok = ok && row && listed.first(child) == i;
     if (!ok) set_device_status(status, DEV_BAD_INDEX);
   }
   const int full = static_cast<int>(len >> c.ps_log2);
@@ -185,7 +228,7 @@ __global__ void __launch_bounds__(kMaxList) fork_plan_kernel(CacheView c, int n,
   int total;
   // every length above is read before the first one is written below
   const int rank = block_scan(ok && part > 0 ? 1 : 0, sh, &total);
-  const int n_free = scan_free(c.ref, c.num_pages, total, list, sh);
+  const int n_free = scan_free(counts, c.ref, c.num_pages, total, list, sh);
   if (i >= n) return;
   if (ok && part > 0 && rank >= n_free) {
     set_device_status(status, DEV_NO_PAGES);
@@ -242,12 +285,13 @@ __global__ void __launch_bounds__(kCopyThreads) fork_kernel(CacheView c, const P
                                                            const int32_t* list, uint32_t* status) {
   const int i = blockIdx.x, y = blockIdx.y, ny = gridDim.y;
   pdl_wait();
-  const int row = plan->row[i];
+  // (in one round of loads: each costs 0.6 us here)
+  const int row = plan->row[i], parent = plan->from[i], full = plan->first[i], part = plan->count[i];
+  const int rank = plan->rank[i];
   if (row < 0) return;
-  const int32_t* src = c.table + static_cast<int64_t>(plan->from[i]) * c.width;
+  const int32_t* src = c.table + static_cast<int64_t>(parent) * c.width;
   int32_t* dst = c.table + static_cast<int64_t>(row) * c.width;
-  const int full = plan->first[i], part = plan->count[i];
-  const int page = part > 0 ? list[plan->rank[i]] : -1, from = part > 0 ? src[full] : -1;
+  const int page = part > 0 ? list[rank] : -1, from = part > 0 ? src[full] : -1;
   for (int j = y * kCopyThreads + threadIdx.x; j < full; j += ny * kCopyThreads) {
     const int p = src[j];
     dst[j] = p;

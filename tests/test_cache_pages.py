@@ -339,3 +339,30 @@ def test_a_list_that_asks_for_more_than_2_31_pages():
     assert ls.device_status() == (7, 4)
     assert c.seq_len.tolist() == [20] + [0] * (rows - 1) and int(c.refcount.sum()) == 2
     assert table[0, :3].tolist() == [0, 1, -1] and int(table[1:, :64].max()) == -1
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,spread", [(1024, 1), (3000, 1), (70000, 17), (1024 * 64, 64)])
+def test_lists_of_1024_entries_with_rows_listed_again(rows, spread):
+    """Every position of the longest list: later entries of a row are left out, wherever they stand."""
+    import long_context_grpo_gb300 as ls
+    rng = np.random.default_rng(rows)
+    c = cache_of(make(4000, 16, 1, 64, rows, 3), 1)
+    c.reset()
+    m = host(c)
+    some = rng.permutation(rows // spread)[:700] * spread        # (rows that fall into few slots of a table too)
+    lst = np.concatenate([some[:500], rng.choice(some, 524)])
+    rng.shuffle(lst)
+    add = rng.integers(0, 49, 1024)
+    c.extend(i32(*lst), i32(*add))
+    m.extend(lst, add)
+    assert ls.device_status() == (7, 2)
+    same(c, m)
+    empty = np.nonzero(m.len == 0)[0]
+    kids = rng.choice(empty[:600], 1024)
+    full = np.nonzero(m.len > 0)[0]
+    parents = rng.choice(full, 1024)
+    c.fork(i32(*parents), i32(*kids))
+    m.fork(parents, kids)
+    assert ls.device_status() == (7, 2)
+    same(c, m)
