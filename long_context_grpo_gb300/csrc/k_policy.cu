@@ -8,9 +8,9 @@
 //
 // policy_warp<n>: V <= 256 n.  A warp a row, the row in registers: no block-wide step at all.
 // policy_cluster: larger rows stay in shared memory between the two passes.  A cluster of 1, 2, 4
-//   or 8 CTAs owns one row at a time, each a slice of at most 76 KB, in three buffers: one row
-//   waits for its gradient while its sums are exchanged, the next row's sums are taken, and the
-//   third arrives by bulk copy.  The exchange takes about 4 us whatever the slice, so the fewest
+//   or 8 CTAs owns one row at a time, each a slice of at most 76 KB, in three or four buffers: one
+//   row (or two) waits for its gradient while its sums are exchanged, the next row's sums are taken,
+//   and the last arrives by bulk copy.  The exchange takes about 4 us whatever the slice, so the fewest
 //   CTAs a row are the fastest (slices of 76 KB against 38 KB with two CTAs an SM:
 //   4,096 x 151,936 388 against 457 us), and two rows' exchanges overlap (5,341 x 50,256 184
 //   against 260 us).
@@ -848,7 +848,6 @@ cudaError_t launch_policy_loss(const PolicyArgs& a, cudaStream_t s) {
     e = launch_warp<8>(a, s);
   } else if (a.V <= 4096) {
     e = launch_warp<16>(a, s);
-
   } else {
     // the fewest CTAs a row
     int cl = 1;
