@@ -100,7 +100,14 @@ __device__ __forceinline__ int quick_div(int x, int d, float inv) {
   return r < 0 ? q - 1 : q;
 }
 
-constexpr int kPlanThreads = 512, kPlanWarps = kPlanThreads / 32, kCandidates = 16;
+// ceil(x / d), x and d counts of tiles or tokens.
+__device__ __forceinline__ int ceil_div(int x, int d) {
+  if (x >= 1 << 20) return static_cast<int>((static_cast<int64_t>(x) + d - 1) / d);
+  return quick_div(x + d - 1, d, __fdividef(1.0f, static_cast<float>(d)));
+}
+
+constexpr int kPlanThreads = 512, kPlanWarps = kPlanThreads / 32;
+constexpr int kCandidates = 16;      // of each class: one warp's lanes for both
 
 struct PlanArgs {
   CacheView c;
@@ -128,17 +135,14 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const __grid_c
   __shared__ int sh_max[2], sh_c[2], sh_grouped, sh_bad;
   __shared__ int sh_base[2];
   __shared__ float sh_work[2][kPlanWarps];
-  __shared__ unsigned long long best[2];
+  __shared__ unsigned long long cost_of[2 * kCandidates];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = a.c.Hq / a.c.Hkv;
   Info* info = reinterpret_cast<Info*>(a.ws + a.l.info);
   int* lims = reinterpret_cast<int*>(a.ws + a.l.lims);
   pdl_launch_dependents();
 
-  if (tid < 2) {
-    sh_max[tid] = 0;
-    best[tid] = ~0ull;
-  }
+  if (tid < 2) sh_max[tid] = 0;
   if (tid == 0) sh_bad = 0;
   __syncthreads();
 
@@ -190,14 +194,15 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const __grid_c
   }
   const int n_segs = a.S + (grouped ? n_groups : 0);
   // whether segment i's tokens are in two segments
+  const float inv_group = __fdividef(1.0f, static_cast<float>(a.group));
   auto in_two = [&](int i) {
-    return grouped && segs[a.S + (i < a.S ? i / a.group : i - a.S)].tiles > 0;
+    return grouped && segs[a.S + (i < a.S ? quick_div(i, a.group, inv_group) : i - a.S)].tiles > 0;
   };
   if (grouped) {
     for (int i = tid; i < n_groups; i += kPlanThreads) {
       int lead = -1;
-      for (int b = i * a.group; b < (i + 1) * a.group; ++b)
-        if (segs[b].row >= 0 && lead < 0) lead = b;
+      for (int b = i * a.group; b < (i + 1) * a.group && lead < 0; ++b)
+        if (segs[b].row >= 0) lead = b;
       int sh_len = lead < 0 ? 0 : segs[i * a.group].rows;
       if (sh_len < 0) sh_len = 0;
       if (lead >= 0 && sh_len > segs[lead].key_end) sh_len = segs[lead].key_end;
@@ -217,16 +222,16 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const __grid_c
       s.part = -1;
       s.jobs = s.rows = 0;
       segs[a.S + i] = s;
-      if (s.tiles > 0)
-        for (int b = i * a.group; b < (i + 1) * a.group; ++b) {
-          const int rest = segs[b].tiles - s.tiles;
-          segs[b].tile0 = s.tiles;
-          segs[b].tiles = rest > 0 ? rest : 0;
-        }
     }
     __syncthreads();
     for (int b = warp; b < a.S; b += kPlanThreads / 32) {
       const Seg s = segs[b];
+      const int shared = segs[a.S + quick_div(b, a.group, inv_group)].tiles;
+      __syncwarp();
+      if (lane == 0 && shared > 0) {
+        segs[b].tile0 = shared;
+        segs[b].tiles = s.tiles > shared ? s.tiles - shared : 0;
+      }
       for (int i = lane; i < s.n_tok; i += 32) {
         const int n = s.row < 0 ? 0 : s.lim + s.t0 + i;
         lims[s.t0 + i] = n < 0 ? 0 : n;
@@ -244,19 +249,18 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const __grid_c
     for (int i = tid; i < n_segs; i += kPlanThreads) {
       const int tiles = segs[i].tiles, n = segs[i].n_tok;
       const int w = n > qn ? 1 : 0;
-      const float x = static_cast<float>(w ? (n + per_pair - 1) / per_pair : 1) * static_cast<float>(a.c.Hkv * tiles);
+      const float x = static_cast<float>(w ? ceil_div(n, per_pair) : 1) * static_cast<float>(a.c.Hkv * tiles);
       work[0] += w ? 0.0f : x;
       work[1] += w ? x : 0.0f;
       if (w) longest[1] = max(longest[1], tiles); else longest[0] = max(longest[0], tiles);
+      segs[i].jobs = in_two(i) ? 1 : 0;      // (until the jobs are counted)
     }
     if (warp * 32 < n_segs) {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) {
-          work[c] += __shfl_xor_sync(0xffffffffu, work[c], off);
-          longest[c] = max(longest[c], __shfl_xor_sync(0xffffffffu, longest[c], off));
-        }
+        for (int off = 16; off > 0; off >>= 1) work[c] += __shfl_xor_sync(0xffffffffu, work[c], off);
+        longest[c] = __reduce_max_sync(0xffffffffu, longest[c]);
         if (lane == 0) {
           sh_work[c][warp] = work[c];
           atomicMax(&sh_max[c], longest[c]);
@@ -270,6 +274,7 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const __grid_c
   for (int x = warp; x < 2 * kCandidates; x += kPlanWarps) {
     const int cls = x / kCandidates, v = x % kCandidates;
     const int longest = sh_max[cls];
+    if (lane == 0) cost_of[x] = ~0ull;
     if (longest == 0) continue;
     // wide: 15 round counts; narrow: five, each with chunks an eighth and a quarter longer too (a
     // few short sequences then stay whole); and no split
@@ -283,8 +288,7 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const __grid_c
     C = C < least ? least : C;
     C = C > longest ? longest : C;
     // the longest segment's chunks all alike
-    const int of = (longest + C - 1) / C;
-    C = (longest + of - 1) / of;
+    C = ceil_div(longest, ceil_div(longest, C));
     // (fp32 quotients of up to 2^20 tiles are on the right side of an integer, or above it; more
     // tiles than that are rounded up by a millionth, so that the capacities hold)
     const float inv = __fdividef(longest < 1 << 20 ? 1.0f : 1.000001f, static_cast<float>(C));
@@ -293,9 +297,9 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const __grid_c
       const int tiles = segs[i].tiles, n = segs[i].n_tok;
       if (tiles == 0 || (n > qn) != (cls == 1)) continue;
       const float chunks = ceilf(static_cast<float>(tiles) * inv);
-      const float pairs = static_cast<float>(cls ? (n + per_pair - 1) / per_pair : 1);
+      const float pairs = static_cast<float>(cls ? ceil_div(n, per_pair) : 1);
       jobs += static_cast<float>(a.c.Hkv) * pairs * chunks;
-      if (chunks > 1.0f || in_two(i)) rows += static_cast<float>(a.c.Hq) * chunks * static_cast<float>(n);
+      if (chunks > 1.0f || segs[i].jobs != 0) rows += static_cast<float>(a.c.Hq) * chunks * static_cast<float>(n);
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
@@ -312,26 +316,35 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const __grid_c
       // chunks
       const float cost = ceilf(__fdividef(jobs, round)) * (static_cast<float>(C) + (cls ? 4.5f : 3.0f)) +
                          rows * (cls ? 1.1e-4f : 7e-5f);
-      atomicMin(&best[cls], (static_cast<unsigned long long>(__float_as_uint(cost)) << 25) |
-                                static_cast<unsigned long long>(kMaxTiles - C));
+      cost_of[x] = (static_cast<unsigned long long>(__float_as_uint(cost)) << 25) |
+                   static_cast<unsigned long long>(kMaxTiles - C);
     }
   }
   __syncthreads();
-  if (tid < 2) sh_c[tid] = best[tid] == ~0ull ? kMaxTiles : kMaxTiles - static_cast<int>(best[tid] & 0x1FFFFFF);
+  if (warp == 0) {
+    unsigned long long best = cost_of[lane];
+#pragma unroll
+    for (int off = kCandidates / 2; off > 0; off >>= 1) {
+      const unsigned long long u = __shfl_xor_sync(0xffffffffu, best, off);
+      best = u < best ? u : best;
+    }
+    if (lane % kCandidates == 0)
+      sh_c[lane / kCandidates] = best == ~0ull ? kMaxTiles : kMaxTiles - static_cast<int>(best & 0x1FFFFFF);
+  }
   __syncthreads();
 
   // chunks, jobs and partial rows of every segment
   for (int i = tid; i < n_segs; i += kPlanThreads) {
     Seg& s = segs[i];
     const int w = s.n_tok > qn ? 1 : 0;
+    const bool two = s.jobs != 0;
     s.jobs = s.rows = 0;
     if (s.tiles == 0) continue;
-    const int C = sh_c[w];
-    s.chunks = (s.tiles + C - 1) / C;
-    s.chunk = (s.tiles + s.chunks - 1) / s.chunks;
-    s.chunks = (s.tiles + s.chunk - 1) / s.chunk;
-    s.jobs = a.c.Hkv * (w ? (s.n_tok + per_pair - 1) / per_pair : 1) * s.chunks;
-    if (s.chunks > 1 || in_two(i)) s.rows = a.c.Hq * s.chunks * s.n_tok;
+    s.chunks = ceil_div(s.tiles, sh_c[w]);
+    s.chunk = ceil_div(s.tiles, s.chunks);
+    s.chunks = ceil_div(s.tiles, s.chunk);
+    s.jobs = a.c.Hkv * (w ? ceil_div(s.n_tok, per_pair) : 1) * s.chunks;
+    if (s.chunks > 1 || two) s.rows = a.c.Hq * s.chunks * s.n_tok;
   }
   __syncthreads();
   // their exclusive sums: a warp each for the jobs and the rows of the two classes
