@@ -10,7 +10,8 @@
 // shared memory, and every head of the token uses them.
 //
 // Bound by HBM: 2 bytes read and 2 written a value (14,000 tokens appended: 89 us, 6.3 TB/s; 3,001
-// tokens of 48 heads turned: 16.5 us, 4.5 TB/s, two and a half waves of blocks).  Vector path: 16-byte accesses; a thread
+// tokens of 48 heads turned: 22.5 us if they are not in L2, 16 if they are, in two and a half waves
+// of blocks).  Vector path: 16-byte accesses; a thread
 // keeps its place in the head and walks the heads of the block's tokens (two or four accesses in
 // flight a thread, with fewer blocks an SM, measured slower: 98 us and more against 92).
 // Element path for rows that are not 16-byte aligned or rot_dim not a multiple of 16 (8
@@ -73,15 +74,16 @@ struct Place {
   const uint16_t* src;
   uint16_t* dst;
 };
+template <bool kAppend>
 __device__ __forceinline__ Place place_of(const RopeArgs& a, int64_t t, int h, int64_t page) {
   Place p;
   if (h < a.Hq) {
     p.src = a.q + t * a.qs + h * a.D;
     p.dst = a.qo + t * a.qos + h * a.D;
-  } else if (h < a.Hq + a.Hk) {
+  } else if (!kAppend || h < a.Hq + a.Hk) {
     const int hk = h - a.Hq;
     p.src = a.k + t * a.ks + hk * a.D;
-    p.dst = a.append ? a.c.k + page + hk * a.c.head_stride : a.ko + t * a.kos + hk * a.D;
+    p.dst = kAppend && a.append ? a.c.k + page + hk * a.c.head_stride : a.ko + t * a.kos + hk * a.D;
   } else {
     const int hk = h - a.Hq - a.Hk;
     p.src = a.v + t * a.vs + hk * a.D;
@@ -102,23 +104,46 @@ struct Walk {
   }
 };
 
+// What a thread reads of one (token, head): a 16-byte chunk and, with kPair, its partner.
+struct Chunk {
+  uint4 x, y;
+};
+template <bool kPair>
+__device__ __forceinline__ void load_chunk(Chunk* v, const uint16_t* src, int partner) {
+  v->x = *reinterpret_cast<const uint4*>(src);
+  if constexpr (kPair) v->y = *reinterpret_cast<const uint4*>(src + partner);
+}
+
 // One 16-byte chunk (kPair: chunk c of the first half with its partner in the second) of the heads
-// that this thread walks.  kTurn: rotated by the chunk's angles; else copied.
-template <bool kTurn, bool kPair>
-__device__ __forceinline__ void chunks(const RopeArgs& a, const Token* tok, const float2* cs, int64_t t0, int nt,
+// that this thread walks.  kTurn: rotated by the chunk's angles; else copied.  kLoaded: v is the
+// first of them, loaded by first_chunk before the angles were there.
+template <bool kPair>
+__device__ __forceinline__ void first_chunk(Chunk* v, const RopeArgs& a, int64_t t0, int nt, int h_first, int h_count,
+                                            int c, int partner, int first) {
+  Walk w = {0, first};
+  w.next(0, h_count);
+  if (w.tok < nt) load_chunk<kPair>(v, place_of<false>(a, t0 + w.tok, h_first + w.head, 0).src + c, partner);
+}
+template <bool kTurn, bool kPair, bool kLoaded>
+__device__ __forceinline__ void chunks(Chunk ahead, const RopeArgs& a, const Token* tok, const float2* cs, int64_t t0, int nt,
                                        int h_first, int h_count, int c, int partner, int first, int step) {
   const int half = a.rot >> 1;
+  bool loaded = kLoaded;
   Walk w = {0, first};
   for (w.next(0, h_count); w.tok < nt; w.next(step, h_count)) {
-    const int64_t page = tok[w.tok].page;
+    const bool have = loaded;
+    loaded = false;
+    const int64_t page = kLoaded ? 0 : tok[w.tok].page;     // (an append's; it loads nothing ahead)
     if (page < 0) continue;
-    const Place p = place_of(a, t0 + w.tok, h_first + w.head, page);
+    const Place p = place_of<!kLoaded>(a, t0 + w.tok, h_first + w.head, page);
     if (!kTurn && p.src == p.dst) continue;
-    const uint4 x = *reinterpret_cast<const uint4*>(p.src + c);
+    if (!have) load_chunk<kPair>(&ahead, p.src + c, partner);
+    const Chunk& v = ahead;
+    const uint4 x = v.x;
     if constexpr (!kTurn) {
       *reinterpret_cast<uint4*>(p.dst + c) = x;
     } else if constexpr (kPair) {
-      const uint4 y = *reinterpret_cast<const uint4*>(p.src + c + partner);
+      const uint4 y = v.y;
       const float4* t = reinterpret_cast<const float4*>(cs + w.tok * half + c);
       const uint32_t wx[4] = {x.x, x.y, x.z, x.w}, wy[4] = {y.x, y.y, y.z, y.w};
       uint32_t ox[4], oy[4];
@@ -147,7 +172,7 @@ __device__ __forceinline__ void chunks(const RopeArgs& a, const Token* tok, cons
   }
 }
 
-template <bool kVec>
+template <bool kVec, bool kAhead>
 __global__ void __launch_bounds__(kThreads, kBlocks) rope_kernel(const __grid_constant__ RopeArgs a, int tb) {
   extern __shared__ __align__(16) float2 cs[];      // [token][pair]: cosine, sine
   __shared__ Token tok[kMaxTok];
@@ -155,6 +180,27 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rope_kernel(const __grid_co
   const int half = a.rot >> 1;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tb;
   const int nt = static_cast<int>(a.T - t0 < tb ? a.T - t0 : tb);
+
+  // A thread keeps its chunk of a head and walks the heads: rotated chunks (pairs of them in
+  // the half layout) and the copied rest of the rotated heads, then the heads that are copied.
+  // With kAhead the first chunk is on its way while the angles are computed (3,001 tokens that
+  // are not in L2: 22.5 us, without 24.6; an append reads the page table first and gains nothing:
+  // 92 us, without 91).
+  Chunk v = {};
+  if constexpr (kAhead) {
+    const int nr = a.interleaved ? a.rot / 8 : a.rot / 16;
+    const int per = nr + (a.D - a.rot) / 8;
+    const int groups = kThreads / per, first = tid / per, j = tid - first * per;
+    const int Hr = a.Hq + a.Hk;
+    if (first < groups) {
+      if (j >= nr)
+        first_chunk<false>(&v, a, t0, nt, 0, Hr, a.rot + 8 * (j - nr), 0, first);
+      else if (a.interleaved)
+        first_chunk<false>(&v, a, t0, nt, 0, Hr, 8 * j, 0, first);
+      else
+        first_chunk<true>(&v, a, t0, nt, 0, Hr, 8 * j, half, first);
+    }
+  }
 
   if (a.append) {
     for (int i = warp; i < nt; i += kThreads / 32) {
@@ -180,25 +226,23 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rope_kernel(const __grid_co
   const int H = a.Hq + a.Hk + (a.append ? a.Hk : 0);
   const int Hr = a.rot > 0 ? a.Hq + a.Hk : 0;       // heads that are rotated
   if constexpr (kVec) {
-    // A thread keeps its chunk of a head and walks the heads: rotated chunks (pairs of them in
-    // the half layout) and the copied rest of the rotated heads, then the heads that are copied.
-    const int n8 = a.D / 8;
     const int nr = a.interleaved ? a.rot / 8 : a.rot / 16;
     const int per = nr + (a.D - a.rot) / 8;
     if (Hr > 0) {
       const int groups = kThreads / per, first = tid / per, j = tid - first * per;
       if (first < groups) {
         if (j >= nr)
-          chunks<false, false>(a, tok, cs, t0, nt, 0, Hr, a.rot + 8 * (j - nr), 0, first, groups);
+          chunks<false, false, kAhead>(v, a, tok, cs, t0, nt, 0, Hr, a.rot + 8 * (j - nr), 0, first, groups);
         else if (a.interleaved)
-          chunks<true, false>(a, tok, cs, t0, nt, 0, Hr, 8 * j, 0, first, groups);
+          chunks<true, false, kAhead>(v, a, tok, cs, t0, nt, 0, Hr, 8 * j, 0, first, groups);
         else
-          chunks<true, true>(a, tok, cs, t0, nt, 0, Hr, 8 * j, half, first, groups);
+          chunks<true, true, kAhead>(v, a, tok, cs, t0, nt, 0, Hr, 8 * j, half, first, groups);
       }
     }
     if (H > Hr) {
+      const int n8 = a.D / 8;
       const int groups = kThreads / n8, first = tid / n8, j = tid - first * n8;
-      if (first < groups) chunks<false, false>(a, tok, cs, t0, nt, Hr, H - Hr, 8 * j, 0, first, groups);
+      if (first < groups) chunks<false, false, false>(v, a, tok, cs, t0, nt, Hr, H - Hr, 8 * j, 0, first, groups);
     }
   } else {
     // element path: pair items, then single values
@@ -210,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rope_kernel(const __grid_co
       if (page < 0) continue;
       if (j < Hr * half) {
         const int h = j / half, c = j - h * half;
-        const Place p = place_of(a, t0 + k, h, page);
+        const Place p = place_of<true>(a, t0 + k, h, page);
         const int ix = a.interleaved ? 2 * c : c, iy = a.interleaved ? 2 * c + 1 : c + half;
         const float2 t = cs[k * half + c];
         const float x = bf(p.src[ix], 0), y = bf(p.src[iy], 0);
@@ -229,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rope_kernel(const __grid_co
         h = Hr + j / a.D;
         c = j - (h - Hr) * a.D;
       }
-      const Place p = place_of(a, t0 + k, h, page);
+      const Place p = place_of<true>(a, t0 + k, h, page);
       if (p.src != p.dst) p.dst[c] = p.src[c];
     }
   }
@@ -254,10 +298,12 @@ cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s) {
   const int64_t tb = a.T >= static_cast<int64_t>(num_sms()) * kBlocks * 4 * kMaxTok ? kMaxTok : 1;
   const unsigned grid = static_cast<unsigned>((a.T + tb - 1) / tb);
   const size_t smem = static_cast<size_t>(tb) * (a.rot / 2) * sizeof(float2);
-  if (vec)
-    rope_kernel<true><<<grid, kThreads, smem, s>>>(a, static_cast<int>(tb));
+  if (vec && !a.append)
+    rope_kernel<true, true><<<grid, kThreads, smem, s>>>(a, static_cast<int>(tb));
+  else if (vec)
+    rope_kernel<true, false><<<grid, kThreads, smem, s>>>(a, static_cast<int>(tb));
   else
-    rope_kernel<false><<<grid, kThreads, smem, s>>>(a, static_cast<int>(tb));
+    rope_kernel<false, false><<<grid, kThreads, smem, s>>>(a, static_cast<int>(tb));
   return cudaGetLastError();
 }
 
