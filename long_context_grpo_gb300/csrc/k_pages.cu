@@ -7,7 +7,7 @@
 // change by integer atomics, whose order cannot change them.
 //
 // Few rows: bound by launches and by rounds of dependent loads (0.6 us each; 128 rows freed and
-// forked from 8 of 33,000 tokens: 14.5 us for 18 MB).  Compaction: bound by HBM (4.2 GB moved
+// forked from 8 of 33,000 tokens: 12.3 us for 18 MB).  Compaction: bound by HBM (4.2 GB moved
 // between pools in 646 us, 6.5 TB/s).
 #include <climits>
 
@@ -98,9 +98,9 @@ __device__ int scan_free(Counts c, const int32_t* ref, int64_t pages, int want, 
 }
 
 // The first position of every row of a list: a hash table of twice as many slots as entries, so
-// that an entry costs a few probes instead of a comparison with every earlier one.  (With this, the
-// first counts loaded ahead and the entries' plan read at once 128 rows are freed and forked in
-// 14.5 us, without in 18.7.)  clear, sync, put, sync, first.
+// that an entry costs a few probes instead of a comparison with every earlier one.  (This, the first
+// counts loaded ahead and the entries' plan read at once save 4 us of a fork of 128 rows.)
+// clear, sync, put, sync, first.
 struct FirstAt {
   int32_t key[2 * kMaxList], at[2 * kMaxList];
   __device__ __forceinline__ void clear() {
@@ -322,21 +322,21 @@ __global__ void __launch_bounds__(kCopyThreads) free_kernel(CacheView c, int n, 
   const int row = rows[i];
   int dup = 0;
   for (int j = threadIdx.x; j < i; j += kCopyThreads) dup |= rows[j] == row;
+  const bool in = row >= 0 && row < c.num_rows;
+  int32_t* t = c.table + static_cast<int64_t>(in ? row : 0) * c.width;
+  // the length and the first pages in one round of loads
+  const int64_t len = in ? c.len[row] : -1;
+  int next = in && threadIdx.x < c.width ? t[threadIdx.x] : -1;
   dup = __syncthreads_or(dup);
-  if (row < 0 || row >= c.num_rows || dup) {
+  if (!in || dup || !good_len(c, len)) {
     if (threadIdx.x == 0) set_device_status(status, DEV_BAD_INDEX);
     return;
   }
-  const int64_t len = c.len[row];
-  if (!good_len(c, len)) {
-    if (threadIdx.x == 0) set_device_status(status, DEV_BAD_INDEX);
-    return;
-  }
-  int32_t* t = c.table + static_cast<int64_t>(row) * c.width;
   const int pages = static_cast<int>((len + (1 << c.ps_log2) - 1) >> c.ps_log2);
   for (int j = threadIdx.x; j < pages; j += kCopyThreads) {
-    const int page = t[j];
+    const int page = next;
     t[j] = -1;
+    if (j + kCopyThreads < pages) next = t[j + kCopyThreads];
     if (page >= 0 && page < c.num_pages)
       atomicSub(c.ref + page, 1);
     else
@@ -560,7 +560,8 @@ cudaError_t launch_cache_fork(const CacheView& c, int n, const int32_t* parents,
   fork_plan_kernel<<<1, kMaxList, 0, s>>>(c, n, parents, children, plan, page_list(ws), status);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  // enough blocks to fill the GPU, while each has a few hundred units
+  // enough blocks to fill the GPU, while each has a few hundred units (128 rows freed and forked:
+  // 12.3 us; with half as many blocks 14.1, with twice as many 12.4)
   int ny = 4 * num_sms() / n;
   ny = ny < 1 ? 1 : (ny > 16 ? 16 : ny);
   return launch_after(fork_kernel, dim3(static_cast<unsigned>(n), static_cast<unsigned>(ny)), kCopyThreads, 0, s, c,
