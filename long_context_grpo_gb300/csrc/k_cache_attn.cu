@@ -151,6 +151,8 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const __grid_c
     Seg s;
     const int c0 = a.cu[b], c1 = a.cu[b + 1];
     const int row = a.rows != nullptr ? a.rows[b] : b;
+    // (loaded beside the offsets)
+    const int64_t held = row >= 0 && row < a.c.num_rows ? a.c.len[row] : -1;
     const int shared = a.group > 1 && b % a.group == 0 ? a.shared[b / a.group] : 0;
     const bool run = c0 >= 0 && c1 >= c0 && c1 <= a.T;
     if (!run) sh_bad = 1;
@@ -162,7 +164,7 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const __grid_c
     if (run && s.n_tok == 0) {
       s.row = -1;              // nothing new: not looked at
     } else if (ok) {
-      len = a.c.len[s.row];
+      len = held;
       ok = len >= 0 && len <= a.max_len && len <= (static_cast<int64_t>(a.c.width) << a.c.ps_log2);
     }
     if (!ok) {
@@ -1081,17 +1083,18 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = a.Hq / a.Hkv;
   const int64_t out = (static_cast<int64_t>(blockIdx.x) * kJoinWarps + warp) / kPer;
-  pdl_wait();
   const int t = static_cast<int>(out / a.Hq), h = static_cast<int>(out - static_cast<int64_t>(t) * a.Hq);
-  if (t >= a.T) return;               // (with kPer > 1 for the whole block)
-  // the entry of token t: the last one that starts at or before it and is not empty
-  int lo = 0, hi = a.S;               // entries [0, lo) end at or before t, [hi, S) do not
+  // the entry of token t: the last one that starts at or before it and is not empty (the offsets
+  // are the caller's: found while the kernel before drains)
+  int lo = 0, hi = t < a.T ? a.S : 0; // entries [0, lo) end at or before t, [hi, S) do not
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
     if (a.cu[mid + 1] <= t) lo = mid + 1; else hi = mid;
   }
   const int b = lo;
-  if (b >= a.S || t < a.cu[b]) return;
+  const bool mine = t < a.T && b < a.S && t >= a.cu[b];
+  pdl_wait();
+  if (!mine) return;                  // (with kPer > 1 for the whole block)
   // the row's part lists: its own segment's, and its group's
   const int grouped = a.info->grouped;
   const int kv = h / g, hh = h - kv * g;
