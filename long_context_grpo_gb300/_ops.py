@@ -124,21 +124,27 @@ def policy_loss(logits, ids, logp_old, advantages, weights, eps_low=0.2, eps_hig
     else:
         cm = _ptr(clip_mask, "clip_mask", _u8, n, dev)
     nbytes = b._lib().ls_policy_loss_workspace_bytes(T)
-    if loss is None and logp_out is None and kl_out is None and workspace is None:
-        # one allocation for the workspace and the small outputs (small calls are host-bound)
-        buf = torch.empty(nbytes // 4 + 1 + 2 * T, dtype=_f32, device=at)
-        workspace, loss, logp_out, kl_out = buf.split_with_sizes((nbytes // 4, 1, T, T))
-        wp = buf.data_ptr()
-        sp, lp, kp = wp + nbytes, wp + nbytes + 4, wp + nbytes + 4 + 4 * T
+    # (one allocation an output: views of a fresh tensor cost the host more than its allocation)
+    if loss is None:
+        loss = torch.empty(1, dtype=_f32, device=at)
+        sp = loss.data_ptr()
     else:
-        loss = torch.empty(1, dtype=_f32, device=at) if loss is None else loss
-        logp_out = torch.empty(n, dtype=_f32, device=at) if logp_out is None else logp_out
-        kl_out = torch.empty(n, dtype=_f32, device=at) if kl_out is None else kl_out
-        if workspace is None:
-            workspace = torch.empty(max(nbytes, 16), dtype=_u8, device=at)
-        wp, nbytes = _ptr(workspace, "workspace", _u8, None, dev), workspace.numel()
         sp = _ptr(loss, "loss", _f32, (1,), dev)
-        lp, kp = _ptr(logp_out, "logp_out", _f32, n, dev), _ptr(kl_out, "kl_out", _f32, n, dev)
+    if logp_out is None:
+        logp_out = torch.empty(n, dtype=_f32, device=at)
+        lp = logp_out.data_ptr()
+    else:
+        lp = _ptr(logp_out, "logp_out", _f32, n, dev)
+    if kl_out is None:
+        kl_out = torch.empty(n, dtype=_f32, device=at)
+        kp = kl_out.data_ptr()
+    else:
+        kp = _ptr(kl_out, "kl_out", _f32, n, dev)
+    if workspace is None:
+        workspace = torch.empty(max(nbytes, 16), dtype=_u8, device=at)
+        wp = workspace.data_ptr()
+    else:
+        wp, nbytes = _ptr(workspace, "workspace", _u8, None, dev), workspace.numel()
     d = _POLICY.pack(
         T, V, ldx, ldd, x, _ptr(ids, "ids", _i32, n, dev), _ptr(logp_old, "logp_old", _f32, n, dev),
         _opt(logp_ref, "logp_ref", _f32, n, dev), _ptr(advantages, "advantages", _f32, n, dev),

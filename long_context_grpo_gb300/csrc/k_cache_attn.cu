@@ -27,7 +27,7 @@
 //     Q takes 16 KB instead of 32, which leaves room for three K and three V tiles in flight
 //     (192 KB an SM).  M = 128 MMAs with most rows idle still take less than half the time that
 //     the tile's 64 KB take from HBM; bound by HBM (40 sequences of up to 65,000 keys: 829 us for
-//     5.7 GB, all of the measured copy rate; 8 responses that share 32,768 of 34,000 keys: 47 us
+//     5.7 GB, all of the measured copy rate; 8 responses that share 32,768 of 34,000 keys: 46 us
 //     for 173 MB, of which the plan and the join, latency both, are about ten).
 //
 // cache_join_kernel.  Combines a token's partial results in chunk order (deterministic), and
