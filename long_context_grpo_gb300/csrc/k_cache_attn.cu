@@ -1231,8 +1231,13 @@ CacheAttnLayout cache_attn_layout(const CacheView& c, int S, int64_t T) {
   return l;
 }
 
+// Whether the bounds allow more than 64 rows in a segment.
+bool cache_attn_wide(const CacheView& c, int64_t T, int max_new, int group) {
+  const int tokens = kNarrowRows / (c.Hq / c.Hkv);
+  return static_cast<int64_t>(max_new) * group > tokens && T > tokens;
+}
+
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, cudaStream_t s) {
-  const int g = a.c.Hq / a.c.Hkv;
   // (the layout has room for the alignment)
   uint8_t* ws = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(a.ws) + 255) & ~static_cast<uintptr_t>(255));
   PlanArgs p{};
@@ -1279,8 +1284,7 @@ cudaError_t launch_cache_attn(const CacheAttnArgs& a, cudaStream_t s) {
   k.n_jobs = info->n_jobs;
   e = a.c.D == 128 ? launch_attn<128, false>(a, k, s) : launch_attn<64, false>(a, k, s);
   if (e != cudaSuccess) return e;
-  // more than 64 rows in a segment: only if the bounds allow it
-  if (static_cast<int64_t>(a.max_new) * a.group > kNarrowRows / g && a.T > kNarrowRows / g) {
+  if (a.wide) {
     k.jobs = reinterpret_cast<const Job*>(ws + p.l.wide);
     k.n_jobs = info->n_jobs + 1;
     e = a.c.D == 128 ? launch_attn<128, true>(a, k, s) : launch_attn<64, true>(a, k, s);

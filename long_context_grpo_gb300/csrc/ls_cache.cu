@@ -337,7 +337,8 @@ ls_status ls_cache_attn(ls_cache_t h, const ls_cache_attn_desc* d, void* workspa
                               static_cast<cuuint64_t>(d->T)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(c.D) * 2, static_cast<cuuint64_t>(d->q_stride) * 2};
   const cuuint32_t box[3] = {64, g, 128 / g}, boxn[3] = {64, g, 64 / g};
-  st = static_cast<ls_status>(encode_bf16_map(&a.tm_q, d->q, 3, dims, strides, box));
+  a.wide = cache_attn_wide(c, d->T, d->max_new, d->group);
+  if (a.wide) st = static_cast<ls_status>(encode_bf16_map(&a.tm_q, d->q, 3, dims, strides, box));
   if (st == LS_OK) st = static_cast<ls_status>(encode_bf16_map(&a.tm_qn, d->q, 3, dims, strides, boxn));
   if (st != LS_OK) return st;
   return run_launch(LS_KERNEL_CACHE_ATTN, stream, "cache attention launch",

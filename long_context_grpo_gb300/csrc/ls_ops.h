@@ -111,7 +111,8 @@ struct CacheAttnArgs {
   const CUtensorMap* tm_k;    // pages: see ls_cache.cu
   const CUtensorMap* tm_v;
   int layout;                 // 0: [page_size, Hkv, D] inside a page, 1: [Hkv, page_size, D]
-  CUtensorMap tm_q;           // {64, g, 128 / g} boxes of [T][Hq][D]
+  bool wide;                  // cache_attn_wide of the bounds
+  CUtensorMap tm_q;           // {64, g, 128 / g} boxes of [T][Hq][D]; with wide only
   CUtensorMap tm_qn;          // {64, g, 64 / g} boxes
   uint32_t* status;
 };
@@ -122,6 +123,7 @@ struct CacheAttnLayout {
   int64_t rows_narrow, rows_wide;                         // rows of partial results
 };
 CacheAttnLayout cache_attn_layout(const CacheView& c, int S, int64_t T);
+bool cache_attn_wide(const CacheView& c, int64_t T, int max_new, int group);
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, cudaStream_t s);
 
 }  // namespace ls
