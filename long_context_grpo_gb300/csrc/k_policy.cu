@@ -713,11 +713,13 @@ __global__ void __launch_bounds__(kFinishThreads) policy_finish(const __grid_con
   __shared__ double sh[kFinishThreads / 32];
   __shared__ unsigned sh_last;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t first = blockIdx.x * static_cast<int64_t>(kFinishThreads) + tid;
+  Token t = {0, 0.0f, 0.0f, 0.0f, 0.0f};
+  if (first < a.T) t = load_token(a, first);     // (while the rows are still at work)
   pdl_wait();
   double sum = 0.0;
-  for (int64_t row = blockIdx.x * static_cast<int64_t>(kFinishThreads) + tid; row < a.T;
-       row += static_cast<int64_t>(gridDim.x) * kFinishThreads) {
-    const Token t = load_token(a, row);
+  for (int64_t row = first; row < a.T; row += static_cast<int64_t>(gridDim.x) * kFinishThreads) {
+    if (row != first) t = load_token(a, row);
     float logp_out = 0.0f, kl_out = 0.0f;
     bool clipped = false;
     if (t.bad(a.V)) set_device_status(a.status, DEV_BAD_INDEX);
