@@ -312,6 +312,7 @@ int64_t ls_grpo_loss_noalloc_max_rows(void);
  * Any V, strides and 2-byte alignment of the rows are right; rows that are 16-byte aligned
  * (a stride that is a multiple of 8) are fast.  Precision as in ls_grpo_loss: compensated fp32
  * row sums, the loss terms in fp64; the clip decision is taken on d with its rounding error.
+ * Infinite values follow the formulas: a sampled logit of -inf has rho = 0, logp_old = -inf rho = inf.
  * A row left unfinished by a bounded wait that gave up (LS_ERR_TIMEOUT) gets NaN outputs, so
  * that *loss is NaN, and a zero gradient.
  */

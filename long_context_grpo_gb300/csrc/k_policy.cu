@@ -70,9 +70,11 @@ __device__ __forceinline__ Token load_token(const PolicyArgs& a, int64_t row) {
 struct Pair {
   float hi, lo;
 };
+// (an infinite sum has no rounding error: the differences would be infinity - infinity, and a
+// sampled token whose logit is -inf, or an infinite logp_old, would turn into NaN)
 __device__ __forceinline__ Pair two_sum(float a, float b) {
   const float s = a + b, bb = s - a;
-  return {s, (a - (s - bb)) + (b - bb)};
+  return {s, fabsf(s) == INFINITY ? 0.0f : (a - (s - bb)) + (b - bb)};
 }
 __device__ __forceinline__ Pair pair_add(Pair a, Pair b) {
   const Pair s = two_sum(a.hi, b.hi);

@@ -245,3 +245,54 @@ def test_two_graphs_of_one_shape_and_repeatability():
     torch.cuda.synchronize()
     for a, b in zip(want, outs):
         assert all(torch.equal(u, v) for u, v in zip(a, b))
+
+
+INF = float("inf")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,V,pad", [(6, 500, 0), (6, 1001, 3), (6, 5000, 0), (6, 38001, 1), (6, 310001, 0)])
+@pytest.mark.parametrize("kl", ["none", "k1", "k2", "k3"])
+@pytest.mark.parametrize("what", ["sampled", "old -inf", "old +inf", "ref -inf", "ref +inf"])
+def test_infinite_log_probabilities(T, V, pad, kl, what):
+    """A sampled token whose logit is -inf, and infinite log-probabilities given, with both signs of A:
+    infinities and NaN are where the float64 definition has them, finite outputs have its values."""
+    import long_context_grpo_gb300 as ls
+    if "ref" in what and kl == "none":
+        pytest.skip("no reference without a KL term")
+    wide, ids, old, ref, adv, w = _inputs(T, V, seed=V, masked=0.0, pad=pad)
+    adv = adv.abs() + 0.1
+    adv[1::2] *= -1                                    # rows 0, 2, .. A > 0; 1, 3, .. A < 0
+    for t in (2, 3):
+        if what == "sampled":
+            wide[t, int(ids[t])] = -INF
+        else:
+            (old if "old" in what else ref)[t] = -INF if "-" in what else INF
+    beta = 0.0 if kl == "none" else 0.05
+    with np.errstate(all="ignore"):
+        o = ref_loss(wide[:, :V], ids, old, adv, w, 0.2, 0.28, ref, beta, kl)
+    r = ls.policy_loss(wide.cuda()[:, :V], ids.cuda(), old.cuda(), adv.cuda(), w.cuda(), eps_low=0.2, eps_high=0.28,
+                       logp_ref=None if kl == "none" else ref.cuda(), beta=beta, kl=kl)
+    assert np.array_equal(r.clip_mask.cpu().numpy().astype(bool), o["clip"])
+
+    def same(got, want, tol):
+        got, want = (np.asarray(x, dtype=np.float64) for x in (got.double().cpu().numpy(), want))
+        fin = np.isfinite(want)
+        assert np.array_equal(np.isnan(got), np.isnan(want)) and np.array_equal(got[~fin & ~np.isnan(want)], want[~fin & ~np.isnan(want)])
+        assert (np.abs(got[fin] - want[fin]) <= tol[fin]).all()
+
+    with np.errstate(all="ignore"):
+        same(r.logp, o["logp"], 2 ** -23 * np.abs(o["logp"]) + 2e-6)
+        same(r.kl, o["kl"], 1e-5 * np.abs(o["kl"]) + 4e-6)
+        same(r.loss, [o["loss"]], np.array([1e-5 * np.abs(o["terms"]).sum() + 1e-12]))
+        # (as in test_many_rows_a_block_with_tokens_left_out: the fp32 terms that g is the difference of)
+        A, rw = adv.double().numpy(), w.double().numpy()
+        rk = o["logp"] - ref.double().numpy()
+        slope = {"none": np.zeros(T), "k1": np.ones(T), "k2": rk, "k3": -np.expm1(-rk)}[kl]
+        off = rw * (beta * np.abs(slope) + np.where(o["clip"], 0.0, np.exp(o["d"]) * np.abs(A))) * 2 ** -20
+        hot = np.zeros_like(o["p"])
+        hot[np.arange(T), ids.numpy()] = 1.0
+        want = o["g"][:, None] * (hot - o["p"])       # as one product: -g p + g is inf - inf at a sampled -inf logit
+        same(r.dlogits, want, np.abs(want) * (2 ** -8 + 2 ** -16) + np.abs(o["g"])[:, None] * o["p"] * 2 ** -16 +
+             off[:, None] * (o["p"] + hot) * 1.01 + 1e-36)
+    assert ls.device_status() == (0, 0)
