@@ -213,7 +213,10 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const __grid_c
       const Seg& tail = segs[(i + 1) * a.group - 1];
       s.t0 = segs[i * a.group].t0;
       const int t1 = tail.t0 + tail.n_tok;
-      const bool run = t1 >= s.t0;
+      // (an entry above max_new is refused but its tokens are among these: more of them than the
+      // bounds allow could be wide where the host, by the bounds, launches no wide kernel; the
+      // group's entries then read their keys for themselves)
+      const bool run = t1 >= s.t0 && t1 - s.t0 <= static_cast<int64_t>(a.max_new) * a.group;
       s.n_tok = run ? t1 - s.t0 : 0;
       s.row = lead < 0 ? 0 : segs[lead].row;
       s.lim = INT_MIN;

@@ -406,3 +406,30 @@ def test_captured_decode_replayed_as_the_sequences_grow():
         if i % 13 == 0 or i == 39:
             check(c, c.page_table.cpu().numpy(), now, [1] * S, qr, o, lse, "NHD")
     assert ls.device_status() == (0, 0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("group,max_new,over", [(8, 1, 10), (4, 1, 20), (4, 1, 5), (4, 3, 40), (2, 1, 300)])
+def test_an_entry_over_the_bound_spoils_none_of_its_group(D, group, max_new, over):
+    """Its tokens count among the group's, which may pass what the call's bounds allow a segment of shared
+    keys: the others' outputs are theirs all the same, and the next group's."""
+    import long_context_grpo_gb300 as ls
+    shared, S = 1280, 2 * group
+    lens = [shared + 400 + 3 * b for b in range(S)]
+    make, table = build(lens, 64, 2, D, seed=over, shared=shared, group=group, junk=float("nan"))
+    c = make(8)
+    new = [over if b == group - 1 else max_new for b in range(S)]
+    T = sum(new)
+    q = torch.randn(T, 8, D, device="cuda").to(torch.bfloat16)
+    sl = torch.full((2,), shared, dtype=torch.int32, device="cuda")
+    ws = torch.full((c.attn_workspace_bytes(S, T, max_new, max(lens)),), 0xFF, dtype=torch.uint8, device="cuda")
+    o, lse = c.attn(q, cu(new), max_new=max_new, max_len=max(lens), group=group, shared_len=sl, workspace=ws)
+    assert ls.device_status() == (7, 2)
+    at = sum(new[:group - 1])
+    bad = slice(at, at + over)
+    assert not o[bad].any() and torch.isneginf(lse[bad]).all()
+    keep = torch.ones(T, dtype=torch.bool, device="cuda")
+    keep[bad] = False
+    rows = [b for b in range(S) if b != group - 1]
+    check(c, table, lens, [max_new] * (S - 1), q[keep], o[keep], lse[keep], "NHD", rows=rows)
