@@ -490,6 +490,8 @@ ls_status ls_cache_compact(ls_cache_t src, ls_cache_t dst, int32_t* n_live, void
  *   sees no key (position < 0) gets o = 0, lse = -inf.  What lies in a page behind its
  *   sequence's length may be anything (NaN as well).  One pass over the keys with the running
  *   maximum and sum in fp32; long sequences are split over CTAs and joined in a fixed order.
+ *   A NaN in a query or in a key that it sees gives NaN for o and lse; NaN or infinite values v_j
+ *   also reach the call's tokens before j that attend the same 128 keys (0 x NaN).
  *   max_new, max_len: host bounds on the new tokens and the length of any entry; an entry
  *   above them sets the device status and gets o = 0, lse = -inf.
  *   group, shared_len: with group > 1 (S a multiple of it) the entries come in groups that

@@ -999,7 +999,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         tc_fence_after();
         const int hh = row - tok * g;
-        const float inv_l = (l > 0.0f) ? 1.0f / l : 0.0f;
+        // (only a sum of zero is of no key; a NaN one is of a NaN score, and stays)
+        const float inv_l = l == 0.0f ? 0.0f : 1.0f / l;
         const int64_t out = static_cast<int64_t>(t) * a.c.Hq + w.kv * g + hh;
         const int64_t prow = static_cast<int64_t>(w.part) + row;
 #pragma unroll
@@ -1041,7 +1042,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (valid) {
-          const float lse2 = l > 0.0f ? m_run + __log2f(l) : -INFINITY;
+          const float lse2 = l == 0.0f ? -INFINITY : m_run + __log2f(l);
           if (w.part < 0)
             a.lse[out] = lse2 * kLn2;
           else
@@ -1133,7 +1134,8 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
     float mx = x;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-    if (mx == -INFINITY) continue;
+    // (the maximum drops a NaN part, its weight does not)
+    if (mx == -INFINITY && !__any_sync(0xffffffffu, x != x)) continue;
     const float mn = fmaxf(m, mx);
     const float f = ex2_approx(m - mn);
     const float w = ex2_approx(x - mn);
@@ -1172,11 +1174,11 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
 #pragma unroll
       for (int i = 0; i < kV; ++i) acc[i] += so[w][lane * kV + i];
   }
-  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   uint32_t* dst = reinterpret_cast<uint32_t*>(a.o + out * D) + lane * (kV / 2);
 #pragma unroll
   for (int i = 0; i < kV / 2; ++i) dst[i] = pack_bf16x2(acc[2 * i] * inv, acc[2 * i + 1] * inv);
-  if (lane == 0) a.lse[out] = l > 0.0f ? (m + __log2f(l)) * kLn2 : -INFINITY;
+  if (lane == 0) a.lse[out] = l == 0.0f ? -INFINITY : (m + __log2f(l)) * kLn2;
 }
 
 template <int D, bool kWide>

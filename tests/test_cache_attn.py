@@ -433,3 +433,36 @@ def test_an_entry_over_the_bound_spoils_none_of_its_group(D, group, max_new, ove
     keep[bad] = False
     rows = [b for b in range(S) if b != group - 1]
     check(c, table, lens, [max_new] * (S - 1), q[keep], o[keep], lse[keep], "NHD", rows=rows)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,L", [(1, 90), (3, 40000), (70, 300), (70, 40000)])
+@pytest.mark.parametrize("group", [1, 2])
+@pytest.mark.parametrize("where", ["query", "last key", "first key"])
+def test_a_poisoned_query_or_key_reaches_the_rows_that_see_it(where, group, n, L):
+    """NaN outputs for these, in short and in split sequences, of their own and shared; the same bits as
+    without it for all others."""
+    import long_context_grpo_gb300 as ls
+    Hq, Hkv = 8, 2
+    shared = 64 if group > 1 and L < 256 else (L // 2 // 128 * 128 if group > 1 else 0)
+    make, table = build([L] * 2, 64, Hkv, 128, seed=L, shared=shared, group=group)
+    c = make(Hq)
+    q = torch.randn(2 * n, Hq, 128, device="cuda").to(torch.bfloat16)
+    sl = torch.tensor([shared], dtype=torch.int32, device="cuda") if group > 1 else None
+    call = lambda: c.attn(q, cu([n] * 2), max_new=n, max_len=L, group=group, shared_len=sl)  # noqa: E731
+    want = call()
+    sees = torch.zeros(2 * n, Hq, dtype=torch.bool, device="cuda")
+    if where == "query":
+        q[n // 2, 5, 17] = float("nan")
+        sees[n // 2, 5] = True
+    else:
+        # a key of key head 1: of the middle new token, or the prompt's first one (in shared pages both entries')
+        pos = L - n + n // 2 if where == "last key" else 0
+        c.k_pages[int(table[0, pos // 64]), pos % 64, 1, 3] = float("nan")
+        sees[n // 2 if pos else 0:n, 4:] = True
+        if pos < shared:
+            sees[n:, 4:] = True
+    o, lse = call()
+    assert torch.isnan(o[sees]).all() and torch.isnan(lse[sees]).all()
+    assert torch.equal(o[~sees], want[0][~sees]) and torch.equal(lse[~sees], want[1][~sees])
+    assert ls.device_status() == (0, 0)
