@@ -468,7 +468,7 @@ ls_status ls_cache_compact(ls_cache_t src, ls_cache_t dst, int32_t* n_live, void
  * The new tokens of S sequences, packed: entry b owns packed rows cu_new[b] .. cu_new[b+1]-1
  * (cu_new device int32 [S + 1], cu_new[0] >= 0, non-decreasing; an entry may have none and is
  * then not looked at; packed rows that no entry owns are left as they were; offsets that fall or
- * leave 0 .. T set the device status, and attention then does no entry) and is table row
+ * leave 0 .. T set the device status, and the call then does no entry) and is table row
  * rows[b] (rows device int32 [S], or NULL: row b).  seq_len counts the new tokens already (ls_cache_extend comes first):
  * token i of n new ones of a sequence of length L is at position L - n + i.
  * 1 <= S <= 2048, T >= 1 packed rows.

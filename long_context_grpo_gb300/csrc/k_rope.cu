@@ -44,11 +44,20 @@ __device__ __forceinline__ Token locate(const RopeArgs& a, int64_t t, int lane) 
   Token r;
   r.pos = 0;
   r.page = -1;
-  // the entry of row t: the number of entries that end at or before it
+  // the entry of row t: the number of entries that end at or before it (lower half); and the
+  // number of offsets that fall or leave 0 .. T (upper half), with which the count means nothing
   int b = 0;
-  for (int i = lane; i < a.S; i += 32) b += (a.cu[i + 1] <= t) ? 1 : 0;
+  for (int i = lane; i < a.S; i += 32) {
+    const int start = a.cu[i], end = a.cu[i + 1];
+    b += end <= t ? 1 : 0;
+    if (end < start || end > a.T || start < 0) b += 1 << 16;
+  }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) b += __shfl_xor_sync(0xffffffffu, b, off);
+  if (b >= 1 << 16) {
+    if (lane == 0) set_device_status(a.status, DEV_BAD_INDEX);
+    return r;
+  }
   if (b >= a.S || t < a.cu[b]) return r;
   const int row = a.rows != nullptr ? a.rows[b] : b;
   if (row < 0 || row >= a.c.num_rows) {
@@ -56,6 +65,10 @@ __device__ __forceinline__ Token locate(const RopeArgs& a, int64_t t, int lane) 
     return r;
   }
   const int64_t len = a.c.len[row];
+  if (len < 0 || len > (static_cast<int64_t>(a.c.width) << a.c.ps_log2)) {
+    if (lane == 0) set_device_status(a.status, DEV_BAD_INDEX);
+    return r;
+  }
   r.pos = len - (a.cu[b + 1] - t);
   if (r.pos < 0) return r;
   const int64_t j = r.pos >> a.c.ps_log2;

@@ -466,3 +466,53 @@ def test_a_poisoned_query_or_key_reaches_the_rows_that_see_it(where, group, n, L
     assert torch.isnan(o[sees]).all() and torch.isnan(lse[sees]).all()
     assert torch.equal(o[~sees], want[0][~sees]) and torch.equal(lse[~sees], want[1][~sees])
     assert ls.device_status() == (0, 0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rotated", [False, True])
+def test_append_refuses_offsets_that_are_not_a_partition_and_wild_lengths(rotated):
+    """Rows whose tables list pages behind their ends: nothing is written there (nor anywhere by offsets that
+    fall or leave the packed rows), and the device status says so."""
+    import long_context_grpo_gb300 as ls
+    S, T, ps = 4, 60, 16
+    make, table = build([160] * S, ps, 2, 64, seed=8)
+    c = make(4)
+    k, v = (torch.randn(T, 2, 64, device="cuda").to(torch.bfloat16) for _ in range(2))
+    q = torch.randn(T, 4, 64, device="cuda").to(torch.bfloat16)
+    f = ls.rope_freqs(64)[0]
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    lens = i32(*[100] * S)
+
+    def call(offsets):
+        before, q_out = c.k_pages.clone(), torch.full_like(q, 7.0)
+        if rotated:
+            c.append(k, v, offsets, q=q, q_out=q_out, inv_freq=f)
+        else:
+            c.append(k, v, offsets)
+        return before, q_out
+
+    for offsets in ((0, 50, 10, 30, 60), (0, 60, 0, 60, 60), (-1, 10, 20, 30, 60), (0, 10, 20, 30, 61), (5, 4, 4, 4, 60)):
+        c.seq_len.copy_(lens)
+        before, q_out = call(i32(*offsets))
+        assert ls.device_status() == (7, 2), offsets
+        assert torch.equal(c.k_pages, before) and bool((q_out == 7).all()), offsets
+    for wild in (-1, -(1 << 31), 161, 1 << 30, (1 << 31) - 1):
+        c.seq_len.copy_(lens)
+        c.seq_len[1] = wild
+        before, q_out = call(i32(0, 5, 25, 25, 60))
+        assert ls.device_status() == (7, 2), wild
+        want = before.clone()
+        for b, t0, n in ((0, 0, 5), (3, 25, 35)):
+            pos = torch.arange(100 - n, 100, device="cuda")
+            kb, qb = k[t0:t0 + n], q[t0:t0 + n]
+            if rotated:
+                qb, kb = ls.rope(qb, kb, f, positions=pos)
+                assert torch.equal(q_out[t0:t0 + n], qb)
+            for j, p in enumerate(pos.tolist()):
+                want[int(table[b, p // ps]), p % ps] = kb[j]
+        assert torch.equal(c.k_pages, want) and bool((q_out[5:25] == 7).all()), wild
+    # an entry that has nothing new is not looked at
+    c.seq_len.copy_(lens)
+    c.seq_len[1] = -5
+    call(i32(0, 5, 5, 25, 60))
+    assert ls.device_status() == (0, 0)
