@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kMaxList) extend_plan_kernel(CacheView c, int 
   const int64_t rank = block_scan<int64_t>(ok ? need : 0, sums, &total);
   const int n_free = scan_free(counts, c.ref, c.num_pages, static_cast<int>(total < INT_MAX ? total : INT_MAX), list, sh);
   if (i >= n) return;
-  if (ok && rank + need > n_free) {
+  if (ok && need > 0 && rank + need > n_free) {
     set_device_status(status, DEV_NO_PAGES);
     ok = false;
   }

@@ -366,3 +366,18 @@ def test_lists_of_1024_entries_with_rows_listed_again(rows, spread):
     m.fork(parents, kids)
     assert ls.device_status() == (7, 2)
     same(c, m)
+
+
+@pytest.mark.gpu
+def test_a_row_that_grows_within_its_page_needs_none():
+    """Behind an entry that went without pages, an entry that needs none is done."""
+    import long_context_grpo_gb300 as ls
+    c = cache_of(make(4, 16, 1, 64, 4, 4), 1)
+    c.reset()
+    m = host(c)
+    for rows, add, bits in (((0, 1), (20, 5), 0), ((2, 0, 1, 3), (40, 12, 11, 0), 4), ((1, 2, 0), (1, 16, 0), 4), ((3, 2), (1, 0), 4)):
+        c.extend(i32(*rows), i32(*add))
+        m.extend(rows, add)
+        same(c, m)
+        assert ls.device_status() == ((7, bits) if bits else (0, 0)), rows
+    assert c.seq_len.tolist() == [32, 17, 0, 0]
