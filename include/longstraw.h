@@ -313,8 +313,9 @@ int64_t ls_grpo_loss_noalloc_max_rows(void);
  * (a stride that is a multiple of 8) are fast.  Precision as in ls_grpo_loss: compensated fp32
  * row sums, the loss terms in fp64; the clip decision is taken on d with its rounding error.
  * Infinite values follow the formulas: a sampled logit of -inf has rho = 0, logp_old = -inf rho = inf.
- * A row left unfinished by a bounded wait that gave up (LS_ERR_TIMEOUT) gets NaN outputs, so
- * that *loss is NaN, and a zero gradient.
+ * After a bounded wait that gave up (LS_ERR_TIMEOUT) the tokens that share its thread-block
+ * cluster have NaN for logp_out and kl_out, so that *loss is NaN, and gradients that may be zero in
+ * whole or in part; all others are as they should be.
  */
 typedef enum { LS_KL_NONE = 0, LS_KL_K1 = 1, LS_KL_K2 = 2, LS_KL_K3 = 3 } ls_kl_kind;
 typedef struct {
@@ -651,6 +652,13 @@ ls_status ls_timing_read(double* total_ms, int64_t* launches, int n);
  * usable.
  */
 ls_status ls_debug_wait_timeout(uint64_t limit_ns, void* stream);
+
+/*
+ * The bounded waits of ls_policy_loss launched from now on give up after limit_ns (test aid; at most
+ * 10 s; 0: a wait that is not over already gives up at once; negative: the usual 4 s).
+ * Process-wide.
+ */
+ls_status ls_debug_wait_limit(int64_t limit_ns);
 
 /*
  * Launch-failure injection (test aid for the error paths; no GPU fault is involved).

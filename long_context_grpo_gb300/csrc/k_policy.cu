@@ -288,6 +288,16 @@ __device__ __forceinline__ void shift_row(uint16_t* d, const uint4* buf, int n, 
   if (tid < 8 - off) d[off + 8 * nd + tid] = h[off + 8 * nd + tid];
 }
 
+// Zeros to n granules of a row that does not start on a 16-byte boundary.
+__device__ __forceinline__ void zero_row(uint16_t* d, int n, int tid, int threads) {
+  if (n == 0) return;
+  const int off = static_cast<int>((16 - (reinterpret_cast<uintptr_t>(d) & 15)) & 15) / 2;   // 1 .. 7
+  uint4* to = reinterpret_cast<uint4*>(d + off);
+  for (int i = tid; i < n - 1; i += threads) to[i] = make_uint4(0u, 0u, 0u, 0u);
+  if (tid < off) d[tid] = 0;
+  if (tid < 8 - off) d[off + 8 * (n - 1) + tid] = 0;
+}
+
 template <int kStream>
 __global__ void __launch_bounds__(kStream + 96, kStream == 128 ? 4 : 3)
     policy_cluster(const __grid_constant__ PolicyArgs a, int cl, int per, int nb) {
@@ -300,7 +310,8 @@ __global__ void __launch_bounds__(kStream + 96, kStream == 128 ? 4 : 3)
   __shared__ float sh_g[kRing], sh_c[kRing], sh_gy[kRing];
   __shared__ int sh_used[kMaxBufs], sh_y[kRing];
   // Set when a bounded wait of this CTA or of a peer gave up: rows are only walked through from
-  // then on, with NaN terms and gradients of zero.
+  // then on, barrier by barrier, with gradients of zero, and nothing is copied any more.  Every
+  // decision on it is a vote of the warp (its lanes may see it at different times).
   __shared__ int cl_abort;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -383,7 +394,7 @@ __global__ void __launch_bounds__(kStream + 96, kStream == 128 ? 4 : 3)
         // (the shuffles also make sure that xv has arrived: the row may be overwritten in place
         // once the partials are out)
         const float x_y = __shfl_sync(0xffffffffu, xv, 0);
-        aborted = *vabort != 0;
+        aborted = __any_sync(0xffffffffu, *vabort != 0);
         if (cl > 1 && !aborted) {
           const int sl = 2 * who + (ux & 1);
           if (lane < cl) {
@@ -394,8 +405,7 @@ __global__ void __launch_bounds__(kStream + 96, kStream == 128 ? 4 : 3)
             mbar_arrive_remote(cluster_map(&xbar[sl], lane));
           }
           __syncwarp();
-          aborted = !mbar_wait_cluster(&xbar[sl], (ux >> 1) & 1u, a.status, vabort);
-          aborted = __any_sync(0xffffffffu, aborted);
+          aborted = __any_sync(0xffffffffu, !mbar_wait_limit<true>(&xbar[sl], (ux >> 1) & 1u, a.status, vabort, a.wait_ns));
           if (!aborted) {
             // every CTA joins the same parts the same way
             const bool in = lane < cl;
@@ -426,10 +436,7 @@ __global__ void __launch_bounds__(kStream + 96, kStream == 128 ? 4 : 3)
       __syncwarp();
       named_barrier_arrive(kBarG + par, kThreads);
       if (rank == 0) {
-        if (lane == 0 && t.used(a.V)) {
-          const float nan = __int_as_float(0x7fc00000);
-          leave_logp(a, row, aborted ? Pair{nan, nan} : logp);
-        }
+        if (lane == 0 && t.used(a.V)) leave_logp(a, row, logp);
         const int64_t e = edge_index(sp, a.V, lane);
         if (e >= 0) {
           float v = 0.0f;
@@ -441,14 +448,18 @@ __global__ void __launch_bounds__(kStream + 96, kStream == 128 ? 4 : 3)
     }
   } else if (warp == kWarps + 2) {
     // -------------------------------------------------------------------- copy warp
-    // Requests a row's slice as soon as a buffer is free.
+    // Requests a row's slice as soon as a buffer is free.  After an abort nothing more is requested:
+    // the buffer's last phase may not be complete, and nobody waits for another one.  (A streaming
+    // warp that gave up on a row's phase has set the flag before it let the row's buffer go.)
+    int sent = 0;                        // rows requested
     auto request = [&](int64_t row, int b, const Token& t) {
-      if (row >= a.T) return;
+      if (row >= a.T || __any_sync(0xffffffffu, *vabort != 0)) return;
+      ++sent;
       const bool used = t.used(a.V);
       const RowSpan rs = alike ? sp : row_span(a, row, per, rank);
       if (lane == 0) {
         sh_used[b] = used ? 1 : 0;
-        if (used && rs.n > 0 && !*vabort) {
+        if (used && rs.n > 0) {
           mbar_arrive_expect_tx(&full[b], static_cast<uint32_t>(rs.n) * 16u);
           bulk_load(dyn + b * slice, a.logits + row * a.ldx + rs.head + 8 * static_cast<int64_t>(rs.g0),
                     static_cast<uint32_t>(rs.n) * 16u, &full[b]);
@@ -465,8 +476,8 @@ __global__ void __launch_bounds__(kStream + 96, kStream == 128 ? 4 : 3)
     };
     for (int i = 0; i < nb; ++i) request(cid + i * ncl, i, token(cid + i * ncl));
     Token next = token(cid + nb * ncl);
-    int it = 0, b = 0;
-    for (int64_t row = cid; row < a.T; row += ncl, ++it, b = b == nb - 1 ? 0 : b + 1) {
+    int b = 0;
+    for (int64_t row = cid; row < a.T; row += ncl, b = b == nb - 1 ? 0 : b + 1) {
       named_barrier_sync(kBarEmpty + b, kThreads);
       request(row + nb * ncl, b, next);
       next = token(row + (nb + 1) * ncl);
@@ -474,7 +485,7 @@ __global__ void __launch_bounds__(kStream + 96, kStream == 128 ? 4 : 3)
     if (*vabort) {
       // copies still in flight land before the CTA may exit: the last request of each buffer
       for (int i = 0; i < nb; ++i)
-        if (it > i) mbar_wait_ns(&full[i], static_cast<uint32_t>((it - 1 - i) / nb) & 1u, 200000000ull);
+        if (sent > i) mbar_wait_ns(&full[i], static_cast<uint32_t>((sent - 1 - i) / nb) & 1u, 200000000ull);
     }
   } else {
     // -------------------------------------------------------------- streaming warps
@@ -501,17 +512,18 @@ __global__ void __launch_bounds__(kStream + 96, kStream == 128 ? 4 : 3)
     // Sum of exponentials of this CTA's slice of its i-th row.
     int sum_buf = 0, sum_par = 0;      // of the next row to be summed
     uint32_t sum_phase = 0u;
+    bool dead = false;                 // this warp has given up on the copies
     auto pass1 = [&](int64_t row) {
       const int bi = sum_buf, par = sum_par;
       const int n = alike ? sp.n : row_span(a, row, per, rank).n;
       const uint4* buf = reinterpret_cast<const uint4*>(dyn + bi * slice);
-      // (after an abort the rows are only walked through, barrier by barrier: every row still
-      // arrives here, without a copy)
-      const bool here = mbar_wait(&full[bi], sum_phase, a.status);
-      if (!here) *vabort = 1;
+      if (!dead && !__all_sync(0xffffffffu, mbar_wait_limit<false>(&full[bi], sum_phase, a.status, vabort, a.wait_ns))) {
+        dead = true;
+        *vabort = 1;
+      }
       float m = -INFINITY;
       Pair s = {0.0f, 0.0f};
-      if (here && sh_used[bi] != 0 && !*vabort) {
+      if (!dead && sh_used[bi] != 0) {
         // Relative to the maximum of the thread's first granule; if a later logit is so much
         // larger that the sum leaves [0, 2^100), or nothing in it is finite, once more relative
         // to the warp's true maximum.
@@ -553,10 +565,15 @@ __global__ void __launch_bounds__(kStream + 96, kStream == 128 ? 4 : 3)
       uint16_t* d = a.dlogits + row * a.ldd + sp.head + 8 * static_cast<int64_t>(sp.g0);
       const bool direct = (reinterpret_cast<uintptr_t>(d) & 15) == 0;
       uint4* d4 = direct ? reinterpret_cast<uint4*>(d) : buf;
+      // (a row with g != 0 has its slice in the buffer, whoever gave up on a later one)
       const uint32_t sign = g > 0.0f ? 0x80008000u : 0u;
       const uint64_t c2 = f2_pack(c, c);
-      if (g == 0.0f || *vabort) {
-        for (int i = tid; i < sp.n; i += kStream) d4[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (g == 0.0f) {
+        if (direct) {
+          for (int i = tid; i < sp.n; i += kStream) d4[i] = make_uint4(0u, 0u, 0u, 0u);
+        } else {
+          zero_row(d, sp.n, tid, kStream);     // (a copy given up on may still be landing in the buffer)
+        }
       } else {
 #pragma unroll 4
         for (int i = tid; i < sp.n; i += kStream) {
@@ -576,7 +593,7 @@ __global__ void __launch_bounds__(kStream + 96, kStream == 128 ? 4 : 3)
       const int yl = y - 8 * sp.g0;
       if (y >= 0 && yl >= 0 && yl < 8 * sp.n && (yl >> 3) % kStream == tid && g != 0.0f)
         reinterpret_cast<uint16_t*>(d4)[yl] = to_bf16(gy);
-      if (!direct && sp.n > 0) {
+      if (!direct && sp.n > 0 && g != 0.0f) {
         // the gradient row lies at another offset from a 16-byte boundary: its granules are cut
         // from two of the buffer's
         named_barrier_sync(kBarCopy, kStream);
@@ -584,12 +601,27 @@ __global__ void __launch_bounds__(kStream + 96, kStream == 128 ? 4 : 3)
         // the next copy into this buffer comes behind the writes above
         fence_proxy_async_smem();
       }
-      named_barrier_arrive(kBarEmpty + b, kThreads);
+      // (a warp that waits for no copies any more would run ahead of the copy warp: it waits for it here)
+      if (dead)
+        named_barrier_sync(kBarEmpty + b, kThreads);
+      else
+        named_barrier_arrive(kBarEmpty + b, kThreads);
     }
   }
   __syncwarp();
-  // No CTA leaves while a peer may still write its shared memory; every wait above is bounded.
-  if (cl > 1) cluster_sync_all();
+  __syncthreads();
+  if (cl > 1) {
+    // a wait that gave up behind the last exchange is known to the whole cluster too
+    if (tid < cl && *vabort) st_cluster_u32(cluster_map(&cl_abort, tid), 1u);
+    __syncwarp();
+    // no CTA leaves while a peer may still write its shared memory; every wait above is bounded
+    cluster_sync_all();
+  }
+  // Which of the cluster's rows are whole is not known then: none of them counts, and the loss is NaN.
+  if (rank == 0 && *vabort) {
+    const float nan = __int_as_float(0x7fc00000);
+    for (int64_t row = cid + tid * ncl; row < a.T; row += (kStream + 96) * ncl) leave_logp(a, row, {nan, nan});
+  }
 }
 
 // ======================================================================================

@@ -40,6 +40,10 @@ bool injected_failure() {
   return false;
 }
 
+// ----- limit of the bounded waits that take it from the launch (ls_debug_wait_limit)
+std::atomic<uint64_t> g_wait_limit{LS_WAIT_LIMIT_NS};
+uint64_t wait_limit_ns() { return g_wait_limit.load(); }
+
 namespace {
 
 constexpr uint32_t kMagic = 0x4c535046u;  // "LSPF"
@@ -805,6 +809,12 @@ ls_status ls_debug_wait_timeout(uint64_t limit_ns, void* stream) {
   if (st != LS_OK) return st;
   cudaError_t e = injected_failure() ? cudaErrorLaunchFailure : launch_wait_timeout(limit_ns, status, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? LS_OK : cuda_fail(e, "wait-timeout self test launch");
+}
+
+ls_status ls_debug_wait_limit(int64_t limit_ns) {
+  if (limit_ns > 10000000000ll) return LS_ERR_INVALID_ARGUMENT;
+  g_wait_limit.store(limit_ns < 0 ? LS_WAIT_LIMIT_NS : static_cast<uint64_t>(limit_ns));
+  return LS_OK;
 }
 
 ls_status ls_debug_fail_launch(int64_t after) {

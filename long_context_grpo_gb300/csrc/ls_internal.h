@@ -184,5 +184,8 @@ int launch_failed(cudaError_t e, const char* what);
 // True when the launch attempt about to be made is the one ls_debug_fail_launch armed: the
 // caller then skips the launch and reports a launch failure.
 bool injected_failure();
+// Nanoseconds after which a bounded wait of a kernel that takes its limit from the launch gives up
+// (ls_debug_wait_limit).
+uint64_t wait_limit_ns();
 
 }  // namespace ls

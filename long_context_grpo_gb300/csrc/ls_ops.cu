@@ -79,6 +79,7 @@ ls_status ls_policy_loss(const ls_policy_loss_desc* d, void* workspace, size_t w
   a.partial = reinterpret_cast<double*>(ws);
   a.counter = reinterpret_cast<unsigned*>(ws + kMaxPartials * sizeof(double));
   a.status = status;
+  a.wait_ns = wait_limit_ns();
   cudaError_t e;
   {
     LaunchTimer t(LS_KERNEL_POLICY_LOSS, static_cast<cudaStream_t>(stream));

@@ -30,6 +30,7 @@ struct PolicyArgs {
   double* partial;            // workspace [kMaxPartials]
   unsigned* counter;          // workspace
   uint32_t* status;
+  uint64_t wait_ns;           // limit of a bounded wait
 };
 constexpr int kMaxPartials = 512;
 cudaError_t launch_policy_loss(const PolicyArgs& a, cudaStream_t s);

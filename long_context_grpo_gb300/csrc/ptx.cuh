@@ -154,6 +154,64 @@ __device__ __forceinline__ bool mbar_wait_hint(uint64_t* bar, uint32_t parity, u
   }
 }
 
+// A wait whose limit the launch gives (0: a phase that is not complete yet gives up at once); it
+// also gives up, without recording a timeout, once *abort is set, by this CTA or by a peer.  The
+// threads of a warp may come back with different answers: a vote goes before anything that the
+// warp does together.  kCluster: acquire over the cluster, for arrivals of its other CTAs.
+template <bool kCluster>
+__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  if constexpr (kCluster)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+  return ok != 0u;
+}
+template <bool kCluster>
+__device__ __forceinline__ bool mbar_try_wait_in(uint64_t* bar, uint32_t parity) {
+  if constexpr (!kCluster) {
+    return mbar_try_wait(bar, parity);
+  } else {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0u;
+  }
+}
+template <bool kCluster>
+__device__ __forceinline__ bool mbar_wait_limit(uint64_t* bar, uint32_t parity, uint32_t* status,
+                                                volatile int* abort, uint64_t limit) {
+  if (limit == 0 ? mbar_test_wait<kCluster>(bar, parity) : mbar_try_wait_in<kCluster>(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t i = 0;; ++i) {
+    if ((i & 63u) == 0u) {
+      if (*abort) return false;
+      if (globaltimer_ns() - t0 >= limit) {
+        set_device_status(status, DEV_WAIT_TIMEOUT);
+        return false;
+      }
+    }
+    if (mbar_try_wait_in<kCluster>(bar, parity)) return true;
+  }
+}
+
 // Same wait with a caller-chosen limit (used on teardown after an abort).
 __device__ __forceinline__ bool mbar_wait_ns(uint64_t* bar, uint32_t parity, uint64_t limit) {
   const uint64_t t0 = globaltimer_ns();

@@ -62,3 +62,56 @@ def test_lists_and_flat_tensors_are_refused_by_name():
                      ("rows", lambda: c.free(i32([0, 1]).view(1, 2)))]:
         with pytest.raises(TypeError, match=name):
             fn()
+
+
+def test_wait_limit_of_the_operators_is_validated_on_the_host():
+    from long_context_grpo_gb300 import build as lsbuild
+    lsbuild.build()
+    from long_context_grpo_gb300 import _lib as b
+    L = b._lib()
+    assert L.ls_debug_wait_limit(10_000_000_001) == 1
+    assert L.ls_debug_wait_limit(10_000_000_000) == 0 and L.ls_debug_wait_limit(0) == 0
+    assert L.ls_debug_wait_limit(-1) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,V,pad,shift", [(3000, 5000, 0, 0), (1500, 32000, 0, 0), (1500, 32003, 1, 3), (700, 50257, 7, 0),
+                                           (500, 151936, 0, 0), (300, 151937, 1, 5), (200, 300001, 0, 1)])
+@pytest.mark.parametrize("limit", [0, 1, 1000, 5000, 20000])
+def test_policy_loss_waits_that_give_up(T, V, pad, shift, limit):
+    """A short limit runs out while copies and exchanges are under way: the call reports it, the tokens that
+    are not NaN are right, the loss is NaN, and the next call is as ever.  Cluster sizes 1, 2, 4 and 8; gradient
+    rows on the logits' alignment and `shift` elements beside it; a third of the tokens left out."""
+    import long_context_grpo_gb300 as ls
+    from long_context_grpo_gb300 import _lib as b
+    L = b._lib()
+    g = torch.Generator(device="cuda").manual_seed(V)
+    x = (torch.randn(T, V + pad, generator=g, device="cuda", dtype=torch.bfloat16) * 2)[:, :V]
+    ids = torch.randint(0, V, (T,), generator=g, device="cuda", dtype=torch.int32)
+    old = -torch.rand(T, generator=g, device="cuda") * 20
+    adv = torch.randn(T, generator=g, device="cuda")
+    w = (torch.rand(T, generator=g, device="cuda") >= 1 / 3).float() / T
+    w[0] = 1 / T
+    room = torch.empty(T * (V + 8) + 16, dtype=torch.bfloat16, device="cuda")
+    d = room[shift:shift + T * (V + pad)].view(T, V + pad)[:, :V]
+    call = lambda: ls.policy_loss(x, ids, old, adv, w, dlogits=d)  # noqa: E731
+    want = call()
+    grad = want.dlogits.clone()
+    assert ls.device_status() == (0, 0)
+    for _ in range(3):
+        try:
+            assert L.ls_debug_wait_limit(limit) == 0
+            r = call()
+            torch.cuda.synchronize()
+        finally:
+            L.ls_debug_wait_limit(-1)
+        status = ls.device_status()
+        lost = torch.isnan(r.logp)
+        assert status == ((6, 1) if lost.any() else status) and status in ((0, 0), (6, 1))
+        assert limit > 0 or lost.any()
+        assert not lost[w == 0].any() and torch.isnan(r.loss).item() == lost.any().item()
+        assert torch.equal(r.logp[~lost], want.logp[~lost]) and torch.equal(r.clip_mask[~lost], want.clip_mask[~lost])
+        assert torch.equal(r.dlogits[~lost], grad[~lost])
+        r = call()
+        assert torch.equal(r.loss, want.loss) and torch.equal(r.dlogits, grad) and torch.equal(r.logp, want.logp)
+        assert ls.device_status() == (0, 0)
