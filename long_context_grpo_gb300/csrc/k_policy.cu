@@ -70,11 +70,9 @@ __device__ __forceinline__ Token load_token(const PolicyArgs& a, int64_t row) {
 struct Pair {
   float hi, lo;
 };
-// (an infinite sum has no rounding error: the differences would be infinity - infinity, and a
-// sampled token whose logit is -inf, or an infinite logp_old, would turn into NaN)
 __device__ __forceinline__ Pair two_sum(float a, float b) {
   const float s = a + b, bb = s - a;
-  return {s, fabsf(s) == INFINITY ? 0.0f : (a - (s - bb)) + (b - bb)};
+  return {s, (a - (s - bb)) + (b - bb)};
 }
 __device__ __forceinline__ Pair pair_add(Pair a, Pair b) {
   const Pair s = two_sum(a.hi, b.hi);
@@ -92,9 +90,17 @@ __device__ __forceinline__ Pair log_pair(Pair s) {
   r.lo = fmaf(k, kLn2Lo, r.lo);
   return r;
 }
+// The sum of two log-probabilities, which may be infinite: an infinite sum has no rounding error
+// (its parts' differences are infinity - infinity: a sampled token whose logit is -inf, or an
+// infinite logp_old, would turn into NaN).
+__device__ __forceinline__ Pair log_add(Pair a, Pair b) {
+  Pair s = pair_add(a, b);
+  if (fabsf(s.hi) == INFINITY) s.lo = 0.0f;
+  return s;
+}
 // Whether a > b.
 __device__ __forceinline__ bool above(Pair a, Pair b) {
-  const Pair d = pair_add(a, {-b.hi, -b.lo});
+  const Pair d = log_add(a, {-b.hi, -b.lo});
   return d.hi + d.lo > 0.0f;
 }
 
@@ -105,11 +111,11 @@ struct TokenLoss {
 // The clip is decided on the pair d; ratio and gradient follow in fp32 (relative error ~2^-22).
 __device__ __forceinline__ TokenLoss token_grad(const PolicyArgs& a, const Token& t, Pair logp) {
   TokenLoss o;
-  const Pair d = pair_add(logp, {-t.old, 0.0f});
+  const Pair d = log_add(logp, {-t.old, 0.0f});
   o.clipped = (t.A > 0.0f && above(d, {a.log_hi[0], a.log_hi[1]})) || (t.A < 0.0f && above({a.log_lo[0], a.log_lo[1]}, d));
   float slope = 0.0f;
   if (a.ref != nullptr) {
-    const Pair r = pair_add(logp, {-t.ref, 0.0f});
+    const Pair r = log_add(logp, {-t.ref, 0.0f});
     slope = a.kl == 1 ? 1.0f : (a.kl == 2 ? r.hi + r.lo : -expm1f(-(r.hi + r.lo)));
   }
   o.g = t.w * (static_cast<float>(a.beta) * slope - (o.clipped ? 0.0f : expf(d.hi + d.lo) * t.A));
@@ -163,7 +169,7 @@ __global__ void __launch_bounds__(kRowThreads) policy_rows(const __grid_constant
       for (int w = 0; w < kRowThreads / 32; ++w) s += sh_s[w];
       const float s_hi = static_cast<float>(s);
       const Pair ls = log_pair({s_hi, static_cast<float>(s - static_cast<double>(s_hi))});
-      const Pair lp = pair_add(two_sum(bf16_at(x, tok.y), -m), {-ls.hi, -ls.lo});
+      const Pair lp = log_add(two_sum(bf16_at(x, tok.y), -m), {-ls.hi, -ls.lo});
       const TokenLoss o = token_grad(a, tok, lp);
       if (lane == 0) {
         leave_logp(a, row, lp);
@@ -420,7 +426,7 @@ __global__ void __launch_bounds__(kStream + 96, kStream == 128 ? 4 : 3)
         if (cl > 1 && aborted && lane < cl) st_cluster_u32(cluster_map(&cl_abort, lane), 1u);
         ++ux;
         const Pair ls = log_pair(s);
-        logp = pair_add(two_sum(x_y, -m), {-ls.hi, -ls.lo});
+        logp = log_add(two_sum(x_y, -m), {-ls.hi, -ls.lo});
         lse = m + (ls.hi + ls.lo);
         if (!aborted) o = token_grad(a, t, logp);
       }
@@ -706,7 +712,7 @@ __global__ void __launch_bounds__(kWarpThreads, kG > 4 ? 2 : 4) policy_warp(cons
     for (int off = 16; off > 0; off >>= 1)
       s = pair_add(s, {__shfl_xor_sync(0xffffffffu, s.hi, off), __shfl_xor_sync(0xffffffffu, s.lo, off)});
     const Pair ls = log_pair(s);
-    const Pair logp = pair_add(two_sum(xy, -m), {-ls.hi, -ls.lo});
+    const Pair logp = log_add(two_sum(xy, -m), {-ls.hi, -ls.lo});
     const TokenLoss o = token_grad(a, t, logp);
     if (lane == 0) leave_logp(a, row, logp);
     const float c = fmaf(-(m + (ls.hi + ls.lo)), kLog2e, log2f(fabsf(o.g)));
