@@ -739,15 +739,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (!ok) {
-        *vabort = 1;
-        // drain this warp's own copies still in flight before the CTA may exit
-        for (uint32_t i = kit > static_cast<uint32_t>(C::kN) ? kit - C::kN : 0u; i < kit; ++i)
-          mbar_wait_ns(&bars[C::kBarKFull + i % C::kN], (i / C::kN) & 1u, 200000000ull);
-        for (uint32_t i = vit > static_cast<uint32_t>(C::kN) ? vit - C::kN : 0u; i < vit; ++i)
-          mbar_wait_ns(&bars[C::kBarVFull + i % C::kN], (i / C::kN) & 1u, 200000000ull);
-        if (uc > 0) mbar_wait_ns(&bars[C::kBarQFull], (uc - 1) & 1u, 200000000ull);
-      }
+      if (!ok) *vabort = 1;
+      // This warp's own copies still in flight land before the CTA may exit: also where all are
+      // sent, since another warp may give up while the last are on their way.
+#pragma unroll 1
+      for (uint32_t i = kit > static_cast<uint32_t>(C::kN) ? kit - C::kN : 0u; i < kit; ++i)
+        mbar_wait_ns(&bars[C::kBarKFull + i % C::kN], (i / C::kN) & 1u, 200000000ull);
+#pragma unroll 1
+      for (uint32_t i = vit > static_cast<uint32_t>(C::kN) ? vit - C::kN : 0u; i < vit; ++i)
+        mbar_wait_ns(&bars[C::kBarVFull + i % C::kN], (i / C::kN) & 1u, 200000000ull);
+      if (uc > 0) mbar_wait_ns(&bars[C::kBarQFull], (uc - 1) & 1u, 200000000ull);
     } else if (warp == 1) {
       // ------------------------------------------------------------ MMA issuer (converged warp)
       constexpr uint32_t kIdS = idesc_bf16(128, 128, false, false);
@@ -875,7 +876,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) *vabort = 1;
       // every MMA (and the arrivals committed behind it) has landed before exit
       mma_commit_w(&bars[C::kBarDrain]);
-      mbar_wait_ns(&bars[C::kBarDrain], 0u, ok ? LS_WAIT_LIMIT_NS : 200000000ull);
+      mbar_wait_ns(&bars[C::kBarDrain], 0u, ok ? 4000000000ull : 200000000ull);
     }
   } else {
     setreg_inc<kRegsSoftmax>();

@@ -24,6 +24,15 @@ enum : uint32_t {
 #ifndef LS_WAIT_LIMIT_NS
 #define LS_WAIT_LIMIT_NS 4000000000ull
 #endif
+// ... and looks at the clock and at its CTA's abort flag every so many polls (a power of two).
+#ifndef LS_WAIT_POLLS
+#define LS_WAIT_POLLS 64u
+#endif
+// A poll suspends the thread until the phase is complete or the hardware's own limit (far longer than
+// any wait of a healthy run) has passed; "test_wait" does not, so that a test can let waits run out.
+#ifndef LS_WAIT_POLL
+#define LS_WAIT_POLL "try_wait"
+#endif
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -65,7 +74,7 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier." LS_WAIT_POLL ".parity.shared::cta.b64 p, [%1], %2;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
       : "r"(smem_u32(bar)), "r"(parity)
@@ -95,7 +104,7 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint32
   const uint64_t t0 = globaltimer_ns();
   for (uint32_t i = 1;; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 63u) == 0u) {
+    if ((i & (LS_WAIT_POLLS - 1u)) == 0u) {
       if (*abort) return false;
       if (globaltimer_ns() - t0 > LS_WAIT_LIMIT_NS) {
         set_device_status(status, DEV_WAIT_TIMEOUT);
@@ -109,7 +118,7 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint32
 // at most kHintNs nanoseconds before it polls again (0: the hardware's own limit).
 template <uint32_t kHintNs>
 __device__ __forceinline__ bool mbar_try_wait_hint(uint64_t* bar, uint32_t parity) {
-  if constexpr (kHintNs == 0u) {
+  if constexpr (kHintNs == 0u || sizeof(LS_WAIT_POLL) != sizeof("try_wait")) {
     return mbar_try_wait(bar, parity);
   } else {
     uint32_t ok;
@@ -144,7 +153,7 @@ __device__ __forceinline__ bool mbar_wait_hint(uint64_t* bar, uint32_t parity, u
   const uint64_t t0 = globaltimer_ns();
   for (uint32_t i = 1;; ++i) {
     if (mbar_try_wait_hint<kHintNs>(bar, parity)) return true;
-    if ((i & 63u) == 0u) {
+    if ((i & (LS_WAIT_POLLS - 1u)) == 0u) {
       if (*abort) return false;
       if (globaltimer_ns() - t0 > LS_WAIT_LIMIT_NS) {
         set_device_status(status, DEV_WAIT_TIMEOUT);

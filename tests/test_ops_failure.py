@@ -115,3 +115,54 @@ def test_policy_loss_waits_that_give_up(T, V, pad, shift, limit):
         r = call()
         assert torch.equal(r.loss, want.loss) and torch.equal(r.dlogits, grad) and torch.equal(r.logp, want.logp)
         assert ls.device_status() == (0, 0)
+
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("polls", [1, 64])
+def test_cache_attention_waits_that_give_up(tmp_path, polls):
+    """A library whose attention waits give up after a few polls, unless they are over by then: every call
+    returns, the copies in flight have landed (the calls follow one another on the same shared memory), the
+    status says so, and the context stays usable."""
+    import subprocess
+    import sys
+    from pathlib import Path
+    script = """
+import sys
+from long_context_grpo_gb300 import build as lb
+lb.BUILD_DIR, lb.LIB = sys.argv[1] + "/obj", sys.argv[1] + "/lib.so"
+lb.FLAGS = lb.FLAGS + ["-DLS_WAIT_LIMIT_NS=0ull", "-DLS_WAIT_POLLS=%su" % sys.argv[2], '-DLS_WAIT_POLL="test_wait"']
+lb.build(force=True)
+import torch
+import long_context_grpo_gb300 as ls
+assert ls.library_path == lb.LIB
+i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")
+ps, Hq, Hkv, total = 64, 16, 4, 0
+for S, n, lens, group in ((20, 1, 6000, 1), (8, 1, 9000, 8), (3, 200, 6000, 1), (1, 300, 30000, 1), (4, 40, 5000, 2)):
+    for D in (64, 128):
+        pages, shared = -(-lens // ps), lens // 2 // 128 * 128
+        table = torch.arange(S * pages, dtype=torch.int32, device="cuda").view(S, pages)
+        for x in range(S):
+            table[x, :shared // ps] = table[x - x % group, :shared // ps]
+        both = torch.randn(S * pages, 2, ps, Hkv, D, device="cuda").to(torch.bfloat16)
+        c = ls.PagedCache(both[:, 0], both[:, 1], table, i32(*[lens] * S), i32(*[1] * (S * pages)), Hq=Hq)
+        q = torch.randn(S * n, Hq, D, device="cuda").to(torch.bfloat16)
+        sl = i32(*[shared] * (S // group)) if group > 1 else None
+        gave_up = 0
+        for _ in range(20):
+            o, lse = c.attn(q, i32(*[n * x for x in range(S + 1)]), max_new=n, max_len=lens, group=group, shared_len=sl)
+            torch.cuda.synchronize()
+            status = ls.device_status()
+            assert status in ((0, 0), (6, 1)), status
+            gave_up += status == (6, 1)
+        print(S, n, D, gave_up, "of 20")
+        total += gave_up
+x = torch.ones(1 << 20, device="cuda")
+assert x.sum().item() == 1 << 20
+assert total > 0 or sys.argv[2] != "1"
+print("all returned")
+"""
+    root = Path(__file__).resolve().parent.parent
+    r = subprocess.run([sys.executable, "-c", script, str(tmp_path), str(polls)], cwd=root, capture_output=True, text=True, timeout=300)
+    print(r.stdout)
+    assert r.returncode == 0 and "all returned" in r.stdout, r.stdout + r.stderr
