@@ -454,7 +454,8 @@ size_t ls_cache_pages_workspace_bytes(ls_cache_t h);
  *   ascending order, dst's table, lengths and counts are written from src's; src keeps its
  *   state.  Pages beyond dst's pool set the device status (4 in the word) and are listed as -1.
  *   dst = src: in place, live pages from n on move into the holes below, in ascending order;
- *   listed pages are renamed, the pages they left become free.  n_live: device int32 [1], may
+ *   listed pages are renamed, the pages they left become free.  What a table holds behind its row's
+ *   length is no listed page: renamed if it is a live one, -1 if not, never reported.  n_live: device int32 [1], may
  *   be NULL: the number n of live pages.
  */
 ls_status ls_cache_extend(ls_cache_t h, int32_t n, const int32_t* rows, const int32_t* add,

@@ -498,11 +498,16 @@ __global__ void __launch_bounds__(kMoveThreads) compact_move_kernel(CacheView sc
     if (page >= 0 && page < sc.num_pages) {
       d = mv.to[page];
       if (d >= dc.num_pages) d = -1;
-    } else if (page >= sc.num_pages) {
-      set_device_status(status, DEV_BAD_INDEX);
+    } else {
+      // no page: reported where the row's length makes it one that is listed
+      const int64_t row = i <= UINT_MAX ? static_cast<unsigned>(i) / static_cast<unsigned>(sc.width) : i / sc.width;
+      const int64_t len = sc.len[row];
+      if (good_len(sc, len) && (i - row * sc.width) << sc.ps_log2 < len) set_device_status(status, DEV_BAD_INDEX);
     }
     dc.table[i] = d;
   }
+  for (int64_t i = i0; i < sc.num_rows; i += stride)
+    if (!good_len(sc, sc.len[i])) set_device_status(status, DEV_BAD_INDEX);
   if (!inplace) {
     for (int64_t i = i0; i < sc.num_rows; i += stride) dc.len[i] = sc.len[i];
     for (int64_t p = i0; p < dc.num_pages; p += stride) dc.ref[p] = p < n ? sc.ref[mv.from[p]] : 0;

@@ -381,3 +381,34 @@ def test_a_row_that_grows_within_its_page_needs_none():
         same(c, m)
         assert ls.device_status() == ((7, bits) if bits else (0, 0)), rows
     assert c.seq_len.tolist() == [32, 17, 0, 0]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("into", [False, True])
+def test_compaction_judges_the_listed_pages(into):
+    """What a table holds behind a row's length is not listed (it becomes -1); a page outside the pool within
+    the length, on either side, and a length outside the table are reported."""
+    import long_context_grpo_gb300 as ls
+    for page, column, length, bits in ((1 << 30, 2, 20, 0), (6, 2, 32, 0), (-5, 2, 20, 0), (-1, 1, 20, 2), (-9, 0, 1, 2), (6, 1, 17, 2),
+                                       (1 << 30, 2, 33, 2), (-1, 2, 33, 2), (-1, 2, 49, 2), (-1, 2, -1, 2), (-1, 2, 1 << 30, 2)):
+        k, v, table, length_, ref = make(6, 16, 2, 64, 3, 3)
+        table.copy_(torch.tensor([[1, 4, -1], [5, 3, -1], [-1, -1, -1]], dtype=torch.int32))
+        table[1, column] = page
+        length_.copy_(i32(30, length, 0))
+        ref.zero_()
+        pages = [1, 4] + [p for p in table[1].tolist() if 0 <= p < 6]
+        ref[pages] = 1
+        c = cache_of((k, v, table, length_, ref), 2)
+        d = cache_of(make(6, 16, 2, 64, 3, 3), 2) if into else c
+        m = host(c)
+        k0 = k.clone()
+        c.compact(into=d if into else None)
+        assert ls.device_status() == ((7, bits) if bits else (0, 0)), (page, column, length)
+        live = [p for p in range(6) if m.ref[p]]
+        assert d.refcount.tolist() == [1] * len(live) + [0] * (6 - len(live))
+        want, got = m.table, d.page_table.cpu().numpy()
+        for r in range(3):
+            for j in range(3):
+                p = int(want[r, j])
+                assert (got[r, j] == -1) if not 0 <= p < 6 else torch.equal(d.k_pages[int(got[r, j])], k0[p])
+        assert torch.equal(d.seq_len, c.seq_len)
