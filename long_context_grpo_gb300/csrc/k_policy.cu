@@ -27,6 +27,7 @@
 // policy_finish: a thread a token: its outputs and its loss term in fp64 (an fp64 instruction of one
 //   lane costs as much as one of 32 tokens), and their sum in a fixed order, rounded once.
 #include <atomic>
+#include <type_traits>
 
 #include "ls_internal.h"
 #include "ls_ops.h"
@@ -190,6 +191,11 @@ __global__ void __launch_bounds__(kRowThreads) policy_rows(const __grid_constant
 // ======================================================================================
 // A cluster a row, the row in shared memory
 // ======================================================================================
+// Rows whose log-sum-exp is at most this far from zero fold it into one constant of the gradient's
+// exponent: rounded to fp32 (twice) it costs the probability 2^-14 at most.  Farther ones subtract
+// the row's maximum from each logit first, as the sums do, or the rounding would pass bf16's half
+// step at 1e5 (4,096 x 151,936: 389 us near zero, 394 with the subtraction).
+constexpr float kNear = 512.0f;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxBufs = 4;                    // slices in shared memory (three or four)
 constexpr int kSliceMax = 76000;               // bytes: three slices in one CTA's shared memory
@@ -313,7 +319,7 @@ __global__ void __launch_bounds__(kStream + 96, kStream == 128 ? 4 : 3)
   __shared__ __align__(8) uint64_t full[kMaxBufs], xbar[4];
   __shared__ float part[kRing][kWarps][3];         // a warp's maximum and sum (pair)
   __shared__ float slot[4][kMaxCluster][3];    // a CTA's, by rank
-  __shared__ float sh_g[kRing], sh_c[kRing], sh_gy[kRing];
+  __shared__ __align__(16) float4 sh_turn[kRing];   // g, -base, c, g (1 - p) of a row
   __shared__ int sh_used[kMaxBufs], sh_y[kRing];
   // Set when a bounded wait of this CTA or of a peer gave up: rows are only walked through from
   // then on, barrier by barrier, with gradients of zero, and nothing is copied any more.  Every
@@ -383,7 +389,7 @@ __global__ void __launch_bounds__(kStream + 96, kStream == 128 ? 4 : 3)
       o.g = 0.0f;
       o.clipped = false;
       Pair logp = {0.0f, 0.0f};
-      float lse = 0.0f;
+      float base = 0.0f, rest = 0.0f;      // their sum is the row's log-sum-exp
       bool aborted = false;
       named_barrier_sync(kBarParts + par, kThreads);
       if (t.used(a.V)) {
@@ -427,16 +433,18 @@ __global__ void __launch_bounds__(kStream + 96, kStream == 128 ? 4 : 3)
         ++ux;
         const Pair ls = log_pair(s);
         logp = log_add(two_sum(x_y, -m), {-ls.hi, -ls.lo});
-        lse = m + (ls.hi + ls.lo);
+        rest = m + (ls.hi + ls.lo);
+        if (!(fabsf(rest) <= kNear)) {
+          base = m;
+          rest = ls.hi + ls.lo;
+        }
         if (!aborted) o = token_grad(a, t, logp);
       }
-      // -g p = -sign(g) 2^(x log2 e - lse log2 e + log2 |g|)
-      const float c = fmaf(-lse, kLog2e, log2f(fabsf(o.g)));
+      // -g p = -sign(g) 2^((x - base) log2 e - rest log2 e + log2 |g|), base = 0 for rows near zero
+      const float c = fmaf(-rest, kLog2e, log2f(fabsf(o.g)));
       const float gy = o.g * (1.0f - ex2_approx((logp.hi + logp.lo) * kLog2e));
       if (lane == 0) {
-        sh_g[par] = o.g;
-        sh_c[par] = c;
-        sh_gy[par] = gy;
+        sh_turn[par] = make_float4(o.g, -base, c, gy);
         sh_y[par] = t.used(a.V) ? t.y - sp.head : -1;
       }
       __syncwarp();
@@ -446,7 +454,7 @@ __global__ void __launch_bounds__(kStream + 96, kStream == 128 ? 4 : 3)
         const int64_t e = edge_index(sp, a.V, lane);
         if (e >= 0) {
           float v = 0.0f;
-          if (o.g != 0.0f) v = e == t.y ? gy : copysignf(ex2_approx(fmaf(ev, kLog2e, c)), -o.g);
+          if (o.g != 0.0f) v = e == t.y ? gy : copysignf(ex2_approx(fmaf(ev - base, kLog2e, c)), -o.g);
           if (o.g != o.g) v = o.g;
           a.dlogits[row * a.ldd + e] = to_bf16(v);
         }
@@ -565,7 +573,8 @@ __global__ void __launch_bounds__(kStream + 96, kStream == 128 ? 4 : 3)
       // later rows' sums while this row's are exchanged
       if (row + ahead < a.T) pass1(row + ahead);
       named_barrier_sync(kBarG + par, kThreads);
-      const float g = sh_g[par], c = sh_c[par], gy = sh_gy[par];
+      const float4 tn = sh_turn[par];
+      const float g = tn.x, nm = tn.y, c = tn.z, gy = tn.w;
       const int y = sh_y[par];
       if (!alike) sp = row_span(a, row, per, rank);
       uint16_t* d = a.dlogits + row * a.ldd + sp.head + 8 * static_cast<int64_t>(sp.g0);
@@ -573,7 +582,7 @@ __global__ void __launch_bounds__(kStream + 96, kStream == 128 ? 4 : 3)
       uint4* d4 = direct ? reinterpret_cast<uint4*>(d) : buf;
       // (a row with g != 0 has its slice in the buffer, whoever gave up on a later one)
       const uint32_t sign = g > 0.0f ? 0x80008000u : 0u;
-      const uint64_t c2 = f2_pack(c, c);
+      const uint64_t c2 = f2_pack(c, c), nm2 = f2_pack(nm, nm);
       if (g == 0.0f) {
         if (direct) {
           for (int i = tid; i < sp.n; i += kStream) d4[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -581,19 +590,27 @@ __global__ void __launch_bounds__(kStream + 96, kStream == 128 ? 4 : 3)
           zero_row(d, sp.n, tid, kStream);     // (a copy given up on may still be landing in the buffer)
         }
       } else {
+        const auto turn = [&](auto far) {
 #pragma unroll 4
-        for (int i = tid; i < sp.n; i += kStream) {
-          const uint4 v = buf[i];
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-          uint32_t o[4];
+          for (int i = tid; i < sp.n; i += kStream) {
+            const uint4 v = buf[i];
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            uint32_t o[4];
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            float e0, e1;
-            f2_unpack(f2_fma(f2_pack(lo_bf16(w[u]), hi_bf16(w[u])), l2, c2), e0, e1);
-            o[u] = pack_bf16x2(ex2_approx(e0), ex2_approx(e1)) ^ sign;
+            for (int u = 0; u < 4; ++u) {
+              float e0, e1;
+              uint64_t x = f2_pack(lo_bf16(w[u]), hi_bf16(w[u]));
+              if constexpr (decltype(far)::value) x = f2_add(x, nm2);
+              f2_unpack(f2_fma(x, l2, c2), e0, e1);
+              o[u] = pack_bf16x2(ex2_approx(e0), ex2_approx(e1)) ^ sign;
+            }
+            d4[i] = make_uint4(o[0], o[1], o[2], o[3]);
           }
-          d4[i] = make_uint4(o[0], o[1], o[2], o[3]);
-        }
+        };
+        if (nm == 0.0f)
+          turn(std::false_type{});
+        else
+          turn(std::true_type{});
       }
       // the sampled token's column, by the thread that wrote its granule
       const int yl = y - 8 * sp.g0;
@@ -715,7 +732,7 @@ __global__ void __launch_bounds__(kWarpThreads, kG > 4 ? 2 : 4) policy_warp(cons
     const Pair logp = log_add(two_sum(xy, -m), {-ls.hi, -ls.lo});
     const TokenLoss o = token_grad(a, t, logp);
     if (lane == 0) leave_logp(a, row, logp);
-    const float c = fmaf(-(m + (ls.hi + ls.lo)), kLog2e, log2f(fabsf(o.g)));
+    const float c = fmaf(-(ls.hi + ls.lo), kLog2e, log2f(fabsf(o.g)));
     const float gy = o.g * (1.0f - ex2_approx((logp.hi + logp.lo) * kLog2e));
     const uint32_t sign = o.g > 0.0f ? 0x80008000u : 0u;
     const uint64_t c2 = f2_pack(c, c);
@@ -726,7 +743,7 @@ __global__ void __launch_bounds__(kWarpThreads, kG > 4 ? 2 : 4) policy_warp(cons
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         float e0, e1;
-        f2_unpack(f2_fma(f2_pack(lo_bf16(w[u]), hi_bf16(w[u])), l2, c2), e0, e1);
+        f2_unpack(f2_fma(f2_add(f2_pack(lo_bf16(w[u]), hi_bf16(w[u])), nb), l2, c2), e0, e1);
         r[u] = o.g == 0.0f ? 0u : pack_bf16x2(ex2_approx(e0), ex2_approx(e1)) ^ sign;
       }
       v[k] = make_uint4(r[0], r[1], r[2], r[3]);
@@ -734,7 +751,7 @@ __global__ void __launch_bounds__(kWarpThreads, kG > 4 ? 2 : 4) policy_warp(cons
     store_row(d + sp.head, v, sp.n, buf, lane);
     if (e >= 0) {
       float w = 0.0f;
-      if (o.g != 0.0f) w = copysignf(ex2_approx(fmaf(ev, kLog2e, c)), -o.g);
+      if (o.g != 0.0f) w = copysignf(ex2_approx(fmaf(ev + base, kLog2e, c)), -o.g);
       if (o.g != o.g) w = o.g;
       d[e] = to_bf16(w);
     }

@@ -296,3 +296,27 @@ def test_infinite_log_probabilities(T, V, pad, kl, what):
         same(r.dlogits, want, np.abs(want) * (2 ** -8 + 2 ** -16) + np.abs(o["g"])[:, None] * o["p"] * 2 ** -16 +
              off[:, None] * (o["p"] + hot) * 1.01 + 1e-36)
     assert ls.device_status() == (0, 0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,V,pad", [(8, 500, 0), (8, 1001, 3), (8, 5001, 0), (8, 38001, 1), (4, 310001, 0)])
+@pytest.mark.parametrize("size", [1e4, 1e5, 3e7, 2e38])
+def test_logits_far_from_zero(T, V, pad, size):
+    """Equal logits far from zero share the probability; the rest, whole steps of bf16 below, have none."""
+    import long_context_grpo_gb300 as ls
+    g = torch.Generator().manual_seed(V)
+    wide = (torch.randn(T, V + pad, generator=g) * 0.01 - 1).clamp(max=-0.9).mul(size).to(torch.bfloat16)
+    wide[T // 2:] = (wide[T // 2:].float() + size).to(torch.bfloat16)       # these rows around zero
+    top = torch.rand(T, V + pad, generator=g) < 0.02
+    top[:, V // 3] = True
+    level = torch.tensor([size, -size / 4] * (T // 2)).to(torch.bfloat16)[:, None]
+    level[T // 2:] = torch.tensor(size).to(torch.bfloat16)
+    wide = torch.where(top, level, wide)
+    ids = torch.stack([top[t, :V].nonzero()[0, 0] for t in range(T)]).int()
+    x = wide[:, :V]
+    logp = torch.log_softmax(x.double(), 1).gather(1, ids.long()[:, None])[:, 0]
+    old, adv, w = (logp + 0.05).float(), torch.randn(T, generator=g), torch.full((T,), 1.0 / T)
+    o = ref_loss(x, ids, old, adv, w, 0.2, 0.2)
+    assert np.isfinite(o["dlogits"]).all() and (np.abs(o["dlogits"]) > 0).sum() > T
+    r = ls.policy_loss(wide.cuda()[:, :V], ids.cuda(), old.cuda(), adv.cuda(), w.cuda())
+    _check(r, o, w, 0.2, 0.2)
