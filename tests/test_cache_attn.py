@@ -516,3 +516,26 @@ def test_append_refuses_offsets_that_are_not_a_partition_and_wild_lengths(rotate
     c.seq_len[1] = -5
     call(i32(0, 5, 5, 25, 60))
     assert ls.device_status() == (0, 0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,L", [(1, 30000), (3, 9999), (60, 20000), (300, 5000)])
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 1, 128), (32, 8, 64)])
+def test_another_split_of_the_same_sequence(n, L, Hq, Hkv, D):
+    """Alone and beside others a sequence is cut into other chunks: the same values either way."""
+    import long_context_grpo_gb300 as ls
+    lens = [L] + [L - 171 * b for b in range(1, 24)]
+    make, table = build(lens, 64, Hkv, D, seed=n)
+    c = make(Hq)
+    q = torch.randn(24 * n, Hq, D, device="cuda").to(torch.bfloat16)
+    for S in (1, 2, 5, 24):
+        o, lse = c.attn(q[:S * n], cu([n] * S), max_new=n, max_len=L)
+        check(c, table, lens[:1], [n], q[:n], o[:n], lse[:n], "NHD")
+        if S == 1:
+            alone = o.clone(), lse.clone()
+            again = c.attn(q[:n], cu([n]), max_new=4 * n, max_len=8 * L)
+            assert torch.equal(o, again[0]) and torch.equal(lse, again[1])      # bounds move no split
+        # twice the rounding of the probabilities (2^-8 of a weighted mean of |v|, below 1 here) and of o
+        assert bool(((o[:n].double() - alone[0].double()).abs() <= 2 ** -7 + 2 ** -7 * alone[0].double().abs()).all())
+        assert torch.allclose(lse[:n], alone[1], atol=4e-5, rtol=2 ** -20)
+    assert ls.device_status() == (0, 0)
