@@ -201,7 +201,8 @@ constexpr int kMaxBufs = 4;                    // slices in shared memory (three
 constexpr int kSliceMax = 76000;               // bytes: three slices in one CTA's shared memory
 constexpr int kSlice4 = 57000;                 // four
 constexpr int kSlice2 = 38000;                 // three, and two such CTAs on an SM
-constexpr int kSliceSmall = 26000;             // up to here: 128 streaming threads, four CTAs an SM
+constexpr int kSliceSmall = 26000;             // up to here: 128 streaming threads; four CTAs an SM to
+                                               // 18,700 bytes, three to 25,200
 
 // How a row lies in memory: `head` logits before its first 16-byte granule, `nv` whole granules, then
 // the tail; granules [g0, g0 + n) are this CTA's.
@@ -314,6 +315,7 @@ template <int kStream>
 __global__ void __launch_bounds__(kStream + 96, kStream == 128 ? 4 : 3)
     policy_cluster(const __grid_constant__ PolicyArgs a, int cl, int per, int nb) {
   constexpr int kWarps = kStream / 32;
+  static_assert(kWarps <= 8, "a scalar warp joins the warps' parts over eight lanes");
   constexpr int kThreads = kStream + 32;        // streaming warps and one other
   extern __shared__ __align__(128) uint8_t dyn[];
   __shared__ __align__(8) uint64_t full[kMaxBufs], xbar[4];
@@ -402,7 +404,7 @@ __global__ void __launch_bounds__(kStream + 96, kStream == 128 ? 4 : 3)
           m = ev;                        // a logit outside the granules
           s.hi = ev == -INFINITY ? 0.0f : 1.0f;
         }
-        if (kWarps > 8 || rank == 0) join_lanes<32>(m, s); else join_lanes<8>(m, s);
+        if (rank == 0) join_lanes<32>(m, s); else join_lanes<8>(m, s);
         // (the shuffles also make sure that xv has arrived: the row may be overwritten in place
         // once the partials are out)
         const float x_y = __shfl_sync(0xffffffffu, xv, 0);
