@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rope_kernel(const __grid_co
     }
   }
 
-  if (a.append) {
+  if (!kAhead && a.append) {              // (an append loads nothing ahead)
     for (int i = warp; i < nt; i += kThreads / 32) {
       const Token r = locate(a, t0 + i, lane);
       if (lane == 0) tok[i] = r;
@@ -236,8 +236,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rope_kernel(const __grid_co
   }
   __syncthreads();
 
-  const int H = a.Hq + a.Hk + (a.append ? a.Hk : 0);
-  const int Hr = a.rot > 0 ? a.Hq + a.Hk : 0;       // heads that are rotated
+  const int H = a.Hq + a.Hk + (!kAhead && a.append ? a.Hk : 0);
+  const int Hr = kAhead || a.rot > 0 ? a.Hq + a.Hk : 0;       // heads that are rotated
   if constexpr (kVec) {
     const int nr = a.interleaved ? a.rot / 8 : a.rot / 16;
     const int per = nr + (a.D - a.rot) / 8;
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rope_kernel(const __grid_co
           chunks<true, true, kAhead>(v, a, tok, cs, t0, nt, 0, Hr, 8 * j, half, first, groups);
       }
     }
-    if (H > Hr) {
+    if (!kAhead && H > Hr) {
       const int n8 = a.D / 8;
       const int groups = kThreads / n8, first = tid / n8, j = tid - first * n8;
       if (first < groups) chunks<false, false, false>(v, a, tok, cs, t0, nt, Hr, H - Hr, 8 * j, 0, first, groups);
