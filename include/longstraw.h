@@ -391,7 +391,9 @@ ls_status ls_rope_freqs(int32_t rot_dim, double theta, int32_t scaling, double f
 /*
  * Paged cache (review section 3-2 (2), physical pages of the prompt's keys and values; the
  * prompt as state shared by the group, section 2): keys and values of one attention layer in
- * pages of page_size tokens.  Row r of the page table lists the pages of sequence r, page j
+ * pages of page_size tokens.  A model has a cache a layer, each with a page table, lengths and
+ * counts of its own: fork and compact move the pages of their handle alone, so that layers cannot
+ * share these arrays, and extend, fork, free and compact are called for every layer.  Row r of the page table lists the pages of sequence r, page j
  * holding its tokens j page_size .. (j + 1) page_size - 1; seq_len[r] is its length; several
  * rows may list the same page, refcount[p] of them.  A page is free iff its count is 0.
  * All of it is device memory of the caller, borrowed until ls_cache_destroy:
@@ -492,6 +494,8 @@ ls_status ls_cache_compact(ls_cache_t src, ls_cache_t dst, int32_t* n_live, void
  *   sees no key (position < 0) gets o = 0, lse = -inf.  What lies in a page behind its
  *   sequence's length may be anything (NaN as well).  One pass over the keys with the running
  *   maximum and sum in fp32; long sequences are split over CTAs and joined in a fixed order.
+ *   Probabilities are rounded to bf16, the values' type, before they meet the values, as in
+ *   ls_replay_fwd; the sum that divides them is taken before that.
  *   A NaN in a query or in a key that it sees gives NaN for o and lse; NaN or infinite values v_j
  *   also reach the call's tokens before j that attend the same 128 keys (0 x NaN).
  *   max_new, max_len: host bounds on the new tokens and the length of any entry; an entry
@@ -501,7 +505,9 @@ ls_status ls_cache_compact(ls_cache_t src, ls_cache_t dst, int32_t* n_live, void
  *   first shared_len[i] tokens (device int32 [S / group]), which are then read once for the
  *   whole group.  The result is that without it.  group = 1, shared_len = NULL: no sharing.
  *   workspace device, 16-byte aligned, >= ls_cache_attn_workspace_bytes(h, S, T, max_new,
- *   max_len) bytes (whatever the group).
+ *   max_len) bytes (whatever the group).  Most of it is room for partial results, 4 D + 4 bytes a
+ *   row: up to 6 min(T, 2048) Hq rows and a fixed number an SM (1,024 tokens of 40 heads of 128:
+ *   350 MB); layers and calls on one stream can share one.
  */
 typedef struct {
   int32_t S;

@@ -211,8 +211,9 @@ class PagedCache:
     k_pages, v_pages: bf16 [pages, page_size, Hkv, D] ("NHD") or [pages, Hkv, page_size, D]
     ("HND"), contiguous behind the first dimension (both may be views of one pool).
     page_table int32 [rows, width], seq_len int32 [rows], refcount int32 [pages].  All are
-    borrowed and must outlive the handle; reset() makes every row empty.  Calls are ordered
-    on one stream.  See include/longstraw.h for each call's contract.
+    borrowed and must outlive the handle; reset() makes every row empty.  Every layer of a model
+    has a handle and table, lengths and counts of its own.  Calls are ordered on one stream.  See
+    include/longstraw.h for each call's contract.
     """
 
     def __init__(self, k_pages, v_pages, page_table, seq_len, refcount, Hq: int, layout: str = "NHD",

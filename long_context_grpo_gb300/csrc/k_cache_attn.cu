@@ -20,22 +20,25 @@
 //   more than 2^8).
 //   wide: segments of more than 64 rows.  The two streams are two 128-row Q tiles that use
 //     the same K and V tiles; bound by the softmax's latency between a tile's two products and,
-//     on long calls, by the power limit (1,024 tokens of 40 heads over 131,072 keys: 1.87 ms,
-//     1,460 TFLOP/s of 1,930 measured; over 16,384 keys 308 us, 1,080 TFLOP/s).
+//     on long calls, by the power limit (1,024 tokens of 40 heads over 131,072 keys: 1.87-1.93 ms
+//     in a graph, 1.96 a call: 1,400-1,460 TFLOP/s of 1,930 measured; over 16,384 keys 308 us,
+//     1,080 TFLOP/s).
 //   narrow: at most 64 rows (a token or a few per sequence).  The two streams are two
 //     independent jobs with K/V tiles of their own, so one's softmax hides the other's loads;
 //     Q takes 16 KB instead of 32, which leaves room for three K and three V tiles in flight
 //     (192 KB an SM).  M = 128 MMAs with most rows idle still take less than half the time that
 //     the tile's 64 KB take from HBM; bound by HBM (40 sequences of up to 65,000 keys: 829 us for
-//     5.7 GB, all of the measured copy rate; 8 responses that share 32,768 of 34,000 keys: 46 us
+//     5.7 GB, 94 % of the 7.35 TB/s of a kernel that only reads; 8 responses that share 32,768 of 34,000 keys: 46 us
 //     for 173 MB, of which the plan and the join, latency both, are about ten).
 //
 // cache_join_kernel.  Combines a token's partial results in chunk order (deterministic), and
 //   writes zeros for tokens that see no key.
 //
 // V rows behind a sequence's end are cleared in shared memory before the MMA (0 x NaN); pages
-// outside the pool read as zeros (the TMA's fill).  P is rounded to bf16 for the tensor cores, the
-// sum is taken before that rounding.  Every wait is bounded as in the replay kernels.
+// outside the pool read as zeros (the TMA's fill).  P is rounded to bf16, the type of V, for the
+// tensor cores (one kind of operand a product; P in two parts would double that product); the sum is
+// taken before that rounding.  The outputs' error against float64 is 0.0023 relative, that of fp32
+// probabilities 0.0017, most of both the output's own rounding.  Every wait is bounded as in the replay kernels.
 #include <climits>
 
 #include "ls_internal.h"

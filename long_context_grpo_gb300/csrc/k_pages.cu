@@ -7,7 +7,7 @@
 // change by integer atomics, whose order cannot change them.
 //
 // Few rows: bound by launches and by rounds of dependent loads (0.6 us each; 128 rows freed and
-// forked from 8 of 33,000 tokens: 12.3 us for 18 MB).  Compaction: bound by HBM (4.2 GB moved
+// forked from 8 of 33,000 tokens: 12.3-14.4 us for 18 MB).  Compaction: bound by HBM (4.2 GB moved
 // between pools in 646 us, 6.5 TB/s).
 #include <climits>
 

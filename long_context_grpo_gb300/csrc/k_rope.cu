@@ -10,7 +10,7 @@
 // shared memory, and every head of the token uses them.
 //
 // Bound by HBM: 2 bytes read and 2 written a value (14,000 tokens appended: 89 us, 6.3 TB/s; 3,001
-// tokens of 48 heads turned: 22.5 us if they are not in L2, 16 if they are, in two and a half waves
+// tokens of 48 heads turned: 22.5 us if they are not in L2, 17 if they are, in two and a half waves
 // of blocks).  Vector path: 16-byte accesses; a thread
 // keeps its place in the head and walks the heads of the block's tokens (two or four accesses in
 // flight a thread, with fewer blocks an SM, measured slower: 98 us and more against 92).
