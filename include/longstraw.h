@@ -314,8 +314,8 @@ int64_t ls_grpo_loss_noalloc_max_rows(void);
  * row sums, the loss terms in fp64; the clip decision is taken on d with its rounding error.
  * Infinite values follow the formulas: a sampled logit of -inf has rho = 0, logp_old = -inf rho = inf.
  * After a bounded wait that gave up (LS_ERR_TIMEOUT) the tokens that share its thread-block
- * cluster have NaN for logp_out and kl_out, so that *loss is NaN, and gradients that may be zero in
- * whole or in part; all others are as they should be.
+ * cluster have NaN for logp_out (and for kl_out with a KL term), so that *loss is NaN, and gradients
+ * that may be zero in whole or in part; all others are as they should be.
  */
 typedef enum { LS_KL_NONE = 0, LS_KL_K1 = 1, LS_KL_K2 = 2, LS_KL_K3 = 3 } ls_kl_kind;
 typedef struct {
