@@ -548,6 +548,26 @@ ls_status ls_cache_attn(ls_cache_t h, const ls_cache_attn_desc* d, void* workspa
                         size_t workspace_bytes, void* stream);
 
 /*
+ * ls_cache_attn_window -- ls_cache_attn through a sliding window, for windowed layers: the token at
+ *   position p sees the keys j <= p with j > p - window or j < sinks, that is the last `window` keys
+ *   up to its own and the sequence's first `sinks`.  window >= 1, sinks >= 0; either may pass the
+ *   longest sequence.  Only pages with keys in sight are looked at: table entries of others, pages
+ *   that lie before the window and hold none of the first tokens, may be anything (-1 once a caller
+ *   has given the page away).  All else as ls_cache_attn, but for two things: NaN or
+ *   infinite values v_j also reach tokens of the call that no longer see them, if an earlier token of
+ *   the same entry, at most 128 before, does (0 x NaN); and with group > 1 every entry reads the
+ *   keys that it sees for itself (the windows of a group's entries are a few thousand keys, which
+ *   stay in L2).
+ *   workspace device, 16-byte aligned, >= ls_cache_attn_window_workspace_bytes of the same bounds
+ *   (0 for bounds that the call refuses): lists of jobs, and room for partial results where long
+ *   windows of few tokens are split, at most 2^19 rows of 4 D + 4 bytes.
+ */
+size_t ls_cache_attn_window_workspace_bytes(ls_cache_t h, int32_t S, int64_t T, int32_t max_new,
+                                            int64_t max_len, int64_t window, int64_t sinks);
+ls_status ls_cache_attn_window(ls_cache_t h, const ls_cache_attn_desc* d, int64_t window, int64_t sinks,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Context-parallel prompt sharding (LongStraw review, section 3-2 (2) "Physical page
  * ownership": each rank owns a slice of the prompt's K/V pages; local attention results are
  * combined by a cross-rank log-sum-exp and output merge).  Every shard is its own handle

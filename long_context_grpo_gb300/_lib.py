@@ -143,6 +143,8 @@ def _load():
         "ls_cache_append": (ctypes.c_int, [vp, vp, vp]),
         "ls_cache_attn_workspace_bytes": (sz, [vp, i32, i64, i32, i64]),
         "ls_cache_attn": (ctypes.c_int, [vp, vp, vp, sz, vp]),
+        "ls_cache_attn_window_workspace_bytes": (sz, [vp, i32, i64, i32, i64, i64, i64]),
+        "ls_cache_attn_window": (ctypes.c_int, [vp, vp, i64, i64, vp, sz, vp]),
         "ls_get_device_status": (ctypes.c_int, [vp, ctypes.POINTER(ctypes.c_uint32)]),
         "ls_timing_enable": (ctypes.c_int, [ctypes.c_int]),
         "ls_debug_wait_timeout": (ctypes.c_int, [ctypes.c_uint64, vp]),

@@ -334,14 +334,20 @@ class PagedCache:
         b._check(b._lib().ls_cache_append(self._h, d, _raw_stream(dev)), "ls_cache_append")
         return (q_out if q is not None else None), None
 
-    def attn_workspace_bytes(self, S: int, T: int, max_new: int, max_len: int) -> int:
+    def attn_workspace_bytes(self, S: int, T: int, max_new: int, max_len: int, window: int = None,
+                             sinks: int = 0) -> int:
+        if window is not None:
+            return int(b._lib().ls_cache_attn_window_workspace_bytes(self._h, S, T, max_new, max_len, window, sinks))
         return int(b._lib().ls_cache_attn_workspace_bytes(self._h, S, T, max_new, max_len))
 
     def attn(self, q, cu_new, max_new: int, max_len: int, rows=None, group: int = 1,
-             shared_len=None, o=None, lse=None, workspace=None):
+             shared_len=None, o=None, lse=None, workspace=None, window: int = None, sinks: int = 0):
         """Attention of the new tokens q [T, Hq, D] over their sequences' pages, causal within
         the sequence (append first).  group > 1: runs of `group` entries share their first
-        shared_len[i] tokens' pages, which are read once.  Returns (o, lse)."""
+        shared_len[i] tokens' pages, which are read once.  window: a token sees the last `window`
+        keys up to its own and the first `sinks` of its sequence.  Returns (o, lse)."""
+        if window is None and sinks != 0:
+            raise ValueError("sinks are of a window")
         if not isinstance(q, torch.Tensor) or q.dim() != 3:
             raise TypeError("q must be a 3-D CUDA tensor")
         T = q.shape[0]
@@ -359,12 +365,16 @@ class PagedCache:
         else:
             lp = _ptr(lse, "lse", _f32, (T, self.Hq), dev)
         if workspace is None:
-            workspace = torch.empty(max(self.attn_workspace_bytes(S, T, max_new, max_len), 16), dtype=_u8,
-                                    device=at)
+            workspace = torch.empty(max(self.attn_workspace_bytes(S, T, max_new, max_len, window, sinks), 16),
+                                    dtype=_u8, device=at)
         qp, qs = _heads(q, "q", T, self.Hq, self.D, dev)
         d = _ATTN.pack(S, T, 0 if rows is None else self._list(rows, "rows", dev, S), cp,
                        max_new, max_len, qp, qs, op, lp, group,
                        0 if shared_len is None else self._list(shared_len, "shared_len", dev, S // max(group, 1)))
-        b._check(b._lib().ls_cache_attn(self._h, d, _ptr(workspace, "workspace", _u8, None, dev), workspace.numel(),
-                                        _raw_stream(dev)), "ls_cache_attn")
+        wp = _ptr(workspace, "workspace", _u8, None, dev)
+        if window is None:
+            b._check(b._lib().ls_cache_attn(self._h, d, wp, workspace.numel(), _raw_stream(dev)), "ls_cache_attn")
+        else:
+            b._check(b._lib().ls_cache_attn_window(self._h, d, window, sinks, wp, workspace.numel(),
+                                                   _raw_stream(dev)), "ls_cache_attn_window")
         return o, lse

@@ -40,6 +40,7 @@
 // taken before that rounding.  The outputs' error against float64 is 0.0023 relative, that of fp32
 // probabilities 0.0017, most of both the output's own rounding.  Every wait is bounded as in the replay kernels.
 #include <climits>
+#include <type_traits>
 
 #include "ls_internal.h"
 #include "ls_ops.h"
@@ -77,7 +78,9 @@ struct Job {
   int t0, n_tok, row, lim;
   int tile0, n_tiles, key_end, kv;
   int part;         // row of its first token's first head among the partial rows; -1: output
-  int pad[3];
+  // of a window (tile0 and n_tiles count the tiles in sight): the first st of them are the first
+  // tiles of the row, the others lie `shift` further; lo: the window's first key of the first token
+  int st, shift, lo;
 };
 struct Info {
   int n_jobs[2];    // narrow, wide
@@ -447,6 +450,158 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const __grid_c
 }
 
 // --------------------------------------------------------------------------------------
+// Attention through a window: the token with L keys up to its own sees the last `keys` of them and the
+// row's first `sinks`.  What a Q tile's tokens see is bounded by the window, so no plan is needed:
+// every Q tile's tiles in sight are cut into `chunks` equal parts, jobs are numbered by (Q tile, chunk,
+// key head), and each CTA works its own out at its start.  Q tiles: a sequence's tokens (narrow), or
+// numbered so that a sequence's are found without a sum over those before it (wide): sequence b's start at
+// cu[b] / per + b, per the tokens of a pair of Q tiles; at most one of them is empty.
+struct Window {
+  int keys, sinks;
+  int S;
+  int64_t T;
+  const int32_t* rows;
+  const int32_t* cu;
+  int max_new;
+  int64_t max_len;
+  int chunks;       // of this class
+  int n_jobs;
+  Job* jobs;
+  int* bad;         // workspace: offsets that fall
+};
+
+// A Q tile's tokens, its sequence and the tiles that it sees.
+struct Sight {
+  int t0, n_tok, row;
+  int lim;          // token t sees keys below lim + t
+  int key_end, lo;
+  int st, shift;
+  int tiles;        // in sight; 0: none
+};
+
+// The Q tile of sequence b that starts at token t0 (behind the sequence: none); what is refused is
+// reported to status, if there is one.
+__device__ __forceinline__ Sight window_sight(const CacheView& c, const Window& w, int b, int t0, int per, bool wide,
+                                              uint32_t* status) {
+  Sight s;
+  const int c0 = w.cu[b], c1 = w.cu[b + 1];
+  s.t0 = t0;
+  s.n_tok = s.tiles = s.st = s.shift = s.key_end = s.lo = s.lim = 0;
+  s.row = 0;
+  const int n = c1 - c0;
+  if (t0 >= c1) return s;
+  if (n > w.max_new && status != nullptr) set_device_status(status, DEV_BAD_INDEX);
+  if (n > w.max_new || (n > kNarrowRows / (c.Hq / c.Hkv)) != wide) return s;
+  const int row = w.rows != nullptr ? w.rows[b] : b;
+  int64_t len = row >= 0 && row < c.num_rows ? c.len[row] : -1;
+  if (len < 0 || len > w.max_len || len > (static_cast<int64_t>(c.width) << c.ps_log2)) {
+    if (status != nullptr) set_device_status(status, DEV_BAD_INDEX);
+    return s;
+  }
+  s.row = row;
+  s.n_tok = c1 - t0 < per ? c1 - t0 : per;
+  s.lim = static_cast<int>(len) - c1 + 1;
+  const int first = s.lim + t0, last = first + s.n_tok - 1;   // keys that the first and the last token see
+  if (last <= 0) return s;
+  s.key_end = last;
+  s.lo = first > w.keys ? first - w.keys : 0;
+  const int tile0 = s.lo >> 7, tile1 = (last - 1) / 128 + 1;
+  const int sinks = w.sinks < last ? w.sinks : last;
+  s.st = (sinks + 127) >> 7;
+  if (s.st > tile0) s.st = tile0;
+  s.shift = tile0 - s.st;
+  s.tiles = s.st + tile1 - tile0;
+  return s;
+}
+
+// Chunk length of a Q tile with this many tiles in sight.
+__device__ __forceinline__ int window_chunk(int tiles, int chunks) { return (tiles + chunks - 1) / chunks; }
+
+template <bool kWide>
+__device__ __forceinline__ Job window_job(const CacheView& c, const Window& w, int x, uint32_t* status) {
+  const int g = c.Hq / c.Hkv;
+  int kv, chunk, b, t0;
+  const int per = kWide ? 2 * (128 / g) : kNarrowRows / g;
+  if constexpr (kWide) {
+    // Q tiles of one (chunk, key head) side by side: their windows overlap
+    const int slots = w.n_jobs / (c.Hkv * w.chunks);
+    const int slot = x % slots;
+    x /= slots;
+    kv = x % c.Hkv;
+    chunk = x / c.Hkv;
+    int lo = 0, hi = w.S - 1;           // the last sequence that starts at or before the slot
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (w.cu[mid] / per + mid <= slot) lo = mid; else hi = mid - 1;
+    }
+    b = lo;
+    const int tile = slot - (w.cu[b] / per + b);
+    const int64_t at = w.cu[b] + static_cast<int64_t>(tile) * per;
+    t0 = tile < 0 || at >= w.cu[b + 1] ? INT_MAX : static_cast<int>(at);
+  } else {
+    // key heads of one chunk side by side: neighbours in memory
+    kv = x % c.Hkv;
+    x /= c.Hkv;
+    chunk = x % w.chunks;
+    b = x / w.chunks;
+    t0 = w.cu[b];
+  }
+  const Sight s = window_sight(c, w, b, t0, per, kWide, status);
+  Job j;
+  j.t0 = s.t0;
+  j.n_tok = s.n_tok;
+  j.row = s.row;
+  j.lim = s.lim;
+  j.key_end = s.key_end;
+  j.kv = kv;
+  j.st = s.st;
+  j.shift = s.shift;
+  j.lo = s.lo;
+  j.part = -1;
+  j.tile0 = j.n_tiles = 0;
+  if (s.tiles > 0) {
+    const int len = window_chunk(s.tiles, w.chunks);
+    j.tile0 = chunk * len;
+    j.n_tiles = s.tiles - j.tile0;
+    j.n_tiles = j.n_tiles < 0 ? 0 : (j.n_tiles > len ? len : j.n_tiles);
+    // rows of the partial results: [chunk][kv][token][head of the group]
+    if (s.tiles > len) j.part = static_cast<int>(((static_cast<int64_t>(chunk) * c.Hkv + kv) * w.T + s.t0) * g);
+  }
+  return j;
+}
+
+// The start of a CTA: whether the offsets hold, and the jobs of its items.  Returns the number of jobs.
+template <bool kWide>
+__device__ __forceinline__ int window_start(const CacheView& c, const Window& w, uint32_t* status) {
+  bool bad = false;
+  for (int b = threadIdx.x; b < w.S; b += kThreads) {
+    const int c0 = w.cu[b], c1 = w.cu[b + 1];
+    bad = bad || c0 < 0 || c1 < c0 || c1 > w.T;
+  }
+  bad = __syncthreads_or(bad);
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    *w.bad = bad ? 1 : 0;
+    if (bad) set_device_status(status, DEV_BAD_INDEX);
+  }
+  if (bad) return 0;
+  constexpr int kPer = kWide ? 1 : 2;
+  for (int64_t i = blockIdx.x + static_cast<int64_t>(threadIdx.x / kPer) * gridDim.x;; i += static_cast<int64_t>(kThreads / kPer) * gridDim.x) {
+    const int64_t x = i * kPer + threadIdx.x % kPer;
+    if (x >= w.n_jobs) break;
+    const Job j = window_job<kWide>(c, w, static_cast<int>(x), status);
+    int4* out = reinterpret_cast<int4*>(w.jobs + x);
+    out[0] = make_int4(j.t0, j.n_tok, j.row, j.lim);
+    out[1] = make_int4(j.tile0, j.n_tiles, j.key_end, j.kv);
+    out[2] = make_int4(j.part, j.st, j.shift, j.lo);
+  }
+  __syncthreads();
+  return w.n_jobs;
+}
+
+// The row's tile that tile v in sight is.
+__device__ __forceinline__ int window_tile(int v, int st, int shift) { return v < st ? v : v + shift; }
+
+// --------------------------------------------------------------------------------------
 template <int D, bool kWide>
 struct Cfg {
   static constexpr int kBoxes = D / 64;
@@ -488,6 +643,7 @@ struct AttnArgs {
   // o starts on a 32-byte boundary: stores of whole sectors (8 x 1,000 tokens without a past 224 us,
   // 234 with halves; a 16-byte boundary is enough for the halves)
   bool o_whole;
+  Window w;
 };
 
 // The two streams of an item: narrow, jobs 2 i and 2 i + 1; wide, the Q tiles of job i.
@@ -502,7 +658,7 @@ __device__ __forceinline__ Job load_job(const Job* p) {
   const int4 x = v[0], y = v[1], z = v[2];
   j.t0 = x.x; j.n_tok = x.y; j.row = x.z; j.lim = x.w;
   j.tile0 = y.x; j.n_tiles = y.y; j.key_end = y.z; j.kv = y.w;
-  j.part = z.x;
+  j.part = z.x; j.st = z.y; j.shift = z.z; j.lo = z.w;
   return j;
 }
 template <bool kWide>
@@ -552,8 +708,9 @@ __device__ __forceinline__ Job load_stream(const AttnArgs& a, int item, int q, i
 // tile's first key on.
 struct Runs {
   int n[2], keys[2];
+  int tile0[2], st[2], shift[2], lo[2];     // of a window; keys are counted from the row's first then
 };
-template <bool kWide>
+template <bool kWide, bool kWin>
 __device__ __forceinline__ Runs load_runs(const AttnArgs& a, int item, int n_jobs, int qt) {
   Runs r;
   r.n[0] = r.n[1] = r.keys[0] = r.keys[1] = 0;
@@ -563,7 +720,14 @@ __device__ __forceinline__ Runs load_runs(const AttnArgs& a, int item, int n_job
     if (at >= n_jobs) continue;
     const int4 y = reinterpret_cast<const int4*>(a.jobs + at)[1];
     r.n[q] = y.y;
-    r.keys[q] = y.z - 128 * y.x;
+    r.keys[q] = y.z - (kWin ? 0 : 128 * y.x);
+    if constexpr (kWin) {
+      const int4 z = reinterpret_cast<const int4*>(a.jobs + at)[2];
+      r.tile0[q] = y.x;
+      r.st[q] = z.y;
+      r.shift[q] = z.z;
+      r.lo[q] = z.w;
+    }
     if (kWide) {
       r.n[1] = reinterpret_cast<const int4*>(a.jobs + at)[0].y > qt ? y.y : 0;
       r.keys[1] = r.keys[0];
@@ -600,7 +764,42 @@ struct PageWindow {
   }
 };
 
-template <int D, bool kWide>
+// The same for a job of a window, whose tiles leap from the first ones to the window's: the entries
+// behind the leap are on their way from the start.  (A tile's pages never cross the end of 32 entries: both
+// start at a tile.)
+struct LeapingPages {
+  const int32_t* row;
+  int end;
+  int base, nbase, cur, next;
+  __device__ __forceinline__ int fetch(int i, int lane) const {
+    return i + lane < end ? __ldg(row + i + lane) : -1;
+  }
+  __device__ __forceinline__ void start(const CacheView& c, const Job& j, int lane) {
+    row = c.table + static_cast<int64_t>(j.row) * c.width;
+    end = (j.key_end + (1 << c.ps_log2) - 1) >> c.ps_log2;
+    base = (window_tile(j.tile0, j.st, j.shift) * 128) >> c.ps_log2;
+    nbase = j.tile0 < j.st && j.tile0 + j.n_tiles > j.st ? (window_tile(j.st, j.st, j.shift) * 128) >> c.ps_log2
+                                                        : base + 32;
+    cur = fetch(base, lane);
+    next = fetch(nbase, lane);
+  }
+  __device__ __forceinline__ int get(int i, int mine, int lane) {
+    if (i >= base + 32) {
+      if (i >= nbase && i < nbase + 32) {
+        base = nbase;
+        cur = next;
+      } else {
+        base = i;
+        cur = fetch(base, lane);
+      }
+      nbase = base + 32;
+      next = fetch(nbase, lane);
+    }
+    return __shfl_sync(0xffffffffu, cur, (i - base + mine) & 31);
+  }
+};
+
+template <int D, bool kWide, bool kWin>
 __global__ void __launch_bounds__(kThreads, 1)
     cache_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                       const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ AttnArgs a) {
@@ -655,8 +854,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tm_q);
   }
   pdl_launch_dependents();
-  pdl_wait();                 // the job lists
-  const int n_jobs = __ldcg(a.n_jobs);
+  int n_jobs;
+  if constexpr (kWin) {
+    n_jobs = window_start<kWide>(a.c, a.w, a.status);
+    pdl_wait();               // the narrow kernel, for the join that waits for this one
+  } else {
+    pdl_wait();               // the job lists
+    n_jobs = __ldcg(a.n_jobs);
+  }
   const int n_items = kWide ? n_jobs : (n_jobs + 1) / 2;
 
   if (warp < 4) {
@@ -683,16 +888,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       // The page of this lane's box of a tile; one past the pool (the map's fill: zeros) if it
       // lies behind the sequence or the entry is none.
-      auto page_of = [&](PageWindow& w, int tile) {
+      using Pages = std::conditional_t<kWin, LeapingPages, PageWindow>;
+      auto page_of = [&](Pages& w, const Job& job, int tile) {
         const int i = (128 * tile) >> a.c.ps_log2;
         const int page = w.get(i, my_box, lane);
+        if constexpr (kWin) {
+          // pages that none of the job's tokens sees are not looked at: their place holds zeros
+          const int64_t at = static_cast<int64_t>(i + my_box) << a.c.ps_log2;
+          if (at + ps <= job.lo && at >= a.w.sinks) return static_cast<int>(a.c.num_pages);
+        }
         if (page >= 0 && page < a.c.num_pages) return page;
         if (my_box < boxes && i + my_box < w.end) set_device_status(a.status, DEV_BAD_INDEX);
         return static_cast<int>(a.c.num_pages);
       };
       // the next item's jobs and first pages are loaded while this one's tiles are
       Streams next = load_streams<kWide>(a, blockIdx.x, n_jobs, qt, g);
-      PageWindow next_w[2];
+      Pages next_w[2];
       auto start_windows = [&]() {
         if (next.n[0] > 0) next_w[0].start(a.c, next.j[0], lane);
         if (!kWide && next.n[1] > 0) next_w[1].start(a.c, next.j[1], lane);
@@ -700,7 +911,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       start_windows();
       for (int it = blockIdx.x; it < n_items && ok; it += gridDim.x) {
         const Streams s = next;
-        PageWindow w[2] = {next_w[0], next_w[1]};
+        Pages w[2] = {next_w[0], next_w[1]};
         next = load_streams<kWide>(a, it + static_cast<int>(gridDim.x), n_jobs, qt, g);
         start_windows();
         const int most = s.n[0] > s.n[1] ? s.n[0] : s.n[1];
@@ -714,8 +925,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (kit >= static_cast<uint32_t>(C::kN))
               ok = __all_sync(0xffffffffu, mbar_wait(&bars[C::kBarKEmpty + ks], ((kit / C::kN) - 1) & 1u, a.status, vabort));
             if (!ok) break;
-            const int page = page_of(w[q], s.j[q].tile0 + j);
-            load_tile(page, s.j[q], s.j[q].tile0 + j, &tm_k, smem + C::kOffK + ks * C::kTile, &bars[C::kBarKFull + ks]);
+            const int tile = kWin ? window_tile(s.j[q].tile0 + j, s.j[q].st, s.j[q].shift) : s.j[q].tile0 + j;
+            const int page = page_of(w[q], s.j[q], tile);
+            load_tile(page, s.j[q], tile, &tm_k, smem + C::kOffK + ks * C::kTile, &bars[C::kBarKFull + ks]);
             ++kit;
             if (!q_sent) {
               // Q goes behind the first K tile: its buffer is free once the last item's scores are done
@@ -737,7 +949,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (vit >= static_cast<uint32_t>(C::kN))
               ok = __all_sync(0xffffffffu, mbar_wait(&bars[C::kBarVEmpty + vs], ((vit / C::kN) - 1) & 1u, a.status, vabort));
             if (!ok) break;
-            load_tile(page, s.j[q], s.j[q].tile0 + j, &tm_v, smem + C::kOffV + vs * C::kTile, &bars[C::kBarVFull + vs]);
+            load_tile(page, s.j[q], tile, &tm_v, smem + C::kOffV + vs * C::kTile, &bars[C::kBarVFull + vs]);
             ++vit;
           }
         }
@@ -785,21 +997,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                         va + static_cast<uint64_t>((kk * 2048) >> 4), kIdPV, (acc || i > 0) ? 1u : 0u);
         }
       };
-      // Clear the V rows from `from` on (behind the sequence's end; whatever they hold must not
-      // meet a probability of zero).
-      auto clear_v = [&](uint32_t vstage, int from) {
+      // Clear the V rows from `from` to `to` (behind the sequence's end, or out of sight; whatever they
+      // hold must not meet a probability of zero).
+      auto clear_v = [&](uint32_t vstage, int from, int to) {
         uint8_t* v = smem + C::kOffV + vstage * C::kTile;
-        for (int i = lane; i < (128 - from) * 8; i += 32)
+        for (int i = lane; i < (to - from) * 8; i += 32)
 #pragma unroll
           for (int b = 0; b < C::kBoxes; ++b)
             *reinterpret_cast<uint4*>(v + b * 16384 + from * 128 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
         fence_proxy_async_smem();
         __syncwarp();
       };
-      Runs next = load_runs<kWide>(a, blockIdx.x, n_jobs, qt);
+      Runs next = load_runs<kWide, kWin>(a, blockIdx.x, n_jobs, qt);
       for (int it = blockIdx.x; it < n_items && ok; it += gridDim.x) {
         const Runs s = next;
-        next = load_runs<kWide>(a, it + static_cast<int>(gridDim.x), n_jobs, qt);
+        next = load_runs<kWide, kWin>(a, it + static_cast<int>(gridDim.x), n_jobs, qt);
         const int most = s.n[0] > s.n[1] ? s.n[0] : s.n[1];
         if (most == 0) continue;
         ok = wait(C::kBarQFull, uc & 1u);
@@ -833,8 +1045,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!kWide || q == 0) {
               ok = wait(C::kBarVFull + vs, (vit / C::kN) & 1u);
               if (!ok) break;
-              const int left = s.keys[q] - 128 * j;
-              if (left < 128) clear_v(vs, left < 0 ? 0 : left);
+              if constexpr (kWin) {
+                const int at = 128 * window_tile(s.tile0[q] + j, s.st[q], s.shift[q]);
+                const int left = s.keys[q] - at, lo = s.lo[q] - at, first = a.w.sinks - at;
+                if (lo > 0 && lo > first) clear_v(vs, first < 0 ? 0 : first, lo < 128 ? lo : 128);
+                if (left < 128) clear_v(vs, left < 0 ? 0 : left, 128);
+              } else {
+                const int left = s.keys[q] - 128 * j;
+                if (left < 128) clear_v(vs, left < 0 ? 0 : left, 128);
+              }
             }
             ok = wait(C::kBarPFull + 2 * q, (pph >> q) & 1u);
             if (!ok) break;
@@ -903,8 +1122,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int t = w.t0 + tok;
         // rows that are not used need no mask: what they hold reaches no other row
         int limit = INT_MAX;
-        if (valid) limit = w.lim == INT_MIN ? __ldcg(a.lims + t) : w.lim + t;
-        limit -= 128 * w.tile0;
+        int low = 0;                // of a window: its first key
+        if constexpr (kWin) {
+          if (valid) limit = w.lim + t;
+          if (valid && limit > a.w.keys) low = limit - a.w.keys;
+        } else {
+          if (valid) limit = w.lim == INT_MIN ? __ldcg(a.lims + t) : w.lim + t;
+          limit -= 128 * w.tile0;
+        }
         float m_run = -INFINITY, l = 0.0f;
         for (int j = 0; j < n; ++j) {
           ok = mbar_wait_hint<20u>(&bars[C::kBarSFull + q], sph, a.status, vabort);
@@ -925,11 +1150,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld32(lane_base + colS + 64, sv[2]);
           tmem_ld32(lane_base + colS + 96, sv[3]);
           tmem_ld_wait();
-          const int lim = limit - 128 * j;
-          if (lim < 128) {
+          if constexpr (kWin) {
+            const int at = 128 * window_tile(w.tile0 + j, w.st, w.shift);
+            const int lim = limit - at, lo = low - at, first = a.w.sinks - at;
+            if (lim < 128 || (lo > 0 && lo > first)) {
 #pragma unroll
-            for (int c = 0; c < 128; ++c)
-              if (c >= lim) sv[c >> 5][c & 31] = __float_as_uint(-INFINITY);
+              for (int c = 0; c < 128; ++c)
+                if (c >= lim || (c < lo && c >= first)) sv[c >> 5][c & 31] = __float_as_uint(-INFINITY);
+            }
+          } else {
+            const int lim = limit - 128 * j;
+            if (lim < 128) {
+#pragma unroll
+              for (int c = 0; c < 128; ++c)
+                if (c >= lim) sv[c >> 5][c & 31] = __float_as_uint(-INFINITY);
+            }
           }
           float mxa = -INFINITY, mxb = -INFINITY, mxc = -INFINITY, mxd = -INFINITY;
 #pragma unroll
@@ -1079,12 +1314,16 @@ struct JoinArgs {
   const float* part_lse;
   uint16_t* o;
   float* lse;
+  // of a window
+  CacheView c;
+  Window w;
+  int chunks_wide;
 };
 
 // kPer warps join one (token, head) row: 1 with many rows, all of the block's with few rows of many
 // parts.  32 parts at a time: a lane loads one part's log-sum-exp, the warp sets the weights
 // (every warp of the row the same), then adds every kPer-th part's row, loads independent.
-template <int D, int kPer>
+template <int D, int kPer, bool kWin>
 __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_constant__ JoinArgs a) {
   constexpr int kV = D / 32;          // values of a lane
   __shared__ float so[kPer > 1 ? kJoinWarps : 1][D];
@@ -1104,11 +1343,26 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
   pdl_wait();
   if (!mine) return;                  // (with kPer > 1 for the whole block)
   // the row's part lists: its own segment's, and its group's
-  const int grouped = a.info->grouped;
+  const int grouped = kWin ? 0 : a.info->grouped;
   const int kv = h / g, hh = h - kv * g;
   int n[2] = {0, 0};
   int64_t first[2] = {0, 0}, step[2] = {0, 0};
   bool direct = false;
+  if constexpr (kWin) {
+    const int c0 = a.cu[b];
+    const bool wide = a.cu[b + 1] - c0 > kNarrowRows / g;
+    const int per = wide ? 2 * (128 / g) : kNarrowRows / g;
+    if (*a.w.bad == 0) {
+      const Sight s = window_sight(a.c, a.w, b, c0 + (t - c0) / per * per, per, wide, nullptr);
+      if (s.tiles > 0) {
+        const int len = window_chunk(s.tiles, wide ? a.chunks_wide : a.w.chunks);
+        n[0] = (s.tiles + len - 1) / len;
+        direct = n[0] == 1;
+        step[0] = a.T * a.Hq;
+        first[0] = (kv * a.T + t) * g + hh;
+      }
+    }
+  } else {
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     if (k == 1 && !grouped) continue;
@@ -1125,6 +1379,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
     step[k] = static_cast<int64_t>(s.n_tok) * g;
     first[k] = s.part + static_cast<int64_t>(kv) * s.chunks * step[k] + static_cast<int64_t>(t - s.t0) * g + hh;
     if (s.part < 0) direct = n[k] > 0;
+  }
   }
   if (direct) return;
   const int total = n[0] + n[1];
@@ -1185,25 +1440,46 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
   if (lane == 0) a.lse[out] = l == 0.0f ? -INFINITY : (m + __log2f(l)) * kLn2;
 }
 
-template <int D, bool kWide>
+template <int D, bool kWide, bool kWin>
 cudaError_t launch_attn(const CacheAttnArgs& a, const AttnArgs& p, cudaStream_t s) {
   using C = Cfg<D, kWide>;
   static bool attr_set[kMaxDeviceCache] = {};
   const int dev = cached_device_index();
   if (dev < 0) return cudaErrorInvalidDevice;
   if (!attr_set[dev]) {
-    cudaError_t e = cudaFuncSetAttribute(cache_attn_kernel<D, kWide>,
+    cudaError_t e = cudaFuncSetAttribute(cache_attn_kernel<D, kWide, kWin>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     // the register split is of what the launch gives
     cudaFuncAttributes f;
-    e = cudaFuncGetAttributes(&f, cache_attn_kernel<D, kWide>);
+    e = cudaFuncGetAttributes(&f, cache_attn_kernel<D, kWide, kWin>);
     if (e != cudaSuccess) return e;
     if (f.numRegs < kRegsLaunch) return cudaErrorLaunchOutOfResources;
     attr_set[dev] = true;
   }
-  return launch_after(cache_attn_kernel<D, kWide>, dim3(static_cast<unsigned>(num_sms())), kThreads,
-                      C::kSmem, s, *a.tm_k, *a.tm_v, kWide ? a.tm_q : a.tm_qn, p);
+  const dim3 grid(static_cast<unsigned>(num_sms()));
+  if constexpr (kWin && !kWide) {   // the call's first kernel reads what kernels before the call wrote
+    cache_attn_kernel<D, kWide, kWin><<<grid, kThreads, C::kSmem, s>>>(*a.tm_k, *a.tm_v, a.tm_qn, p);
+    return cudaGetLastError();
+  } else {
+    return launch_after(cache_attn_kernel<D, kWide, kWin>, grid, kThreads, C::kSmem, s, *a.tm_k, *a.tm_v,
+                        kWide ? a.tm_q : a.tm_qn, p);
+  }
+}
+
+template <bool kWin>
+cudaError_t launch_join(const CacheAttnArgs& a, const JoinArgs& j, cudaStream_t s) {
+  // few rows have many parts each: a block a row; else a warp a row (2,048 rows of a group of 8 over
+  // 34,000 keys 48.1 against 49.3 us for the call; 3,200 rows of 20 sequences 96.1 against 93.7)
+  const int64_t rows = a.T * a.c.Hq;
+  if (rows <= 16 * num_sms()) {
+    const dim3 grid(static_cast<unsigned>(rows));
+    return a.c.D == 128 ? launch_after(cache_join_kernel<128, kJoinWarps, kWin>, grid, kJoinThreads, 0, s, j)
+                        : launch_after(cache_join_kernel<64, kJoinWarps, kWin>, grid, kJoinThreads, 0, s, j);
+  }
+  const dim3 grid(static_cast<unsigned>((rows + kJoinWarps - 1) / kJoinWarps));
+  return a.c.D == 128 ? launch_after(cache_join_kernel<128, 1, kWin>, grid, kJoinThreads, 0, s, j)
+                      : launch_after(cache_join_kernel<64, 1, kWin>, grid, kJoinThreads, 0, s, j);
 }
 
 constexpr int kPlanSeg = sizeof(Seg) + 2 * sizeof(int);   // shared memory of a segment
@@ -1291,12 +1567,12 @@ cudaError_t launch_cache_attn(const CacheAttnArgs& a, cudaStream_t s) {
   k.status = a.status;
   k.jobs = reinterpret_cast<const Job*>(ws + p.l.narrow);
   k.n_jobs = info->n_jobs;
-  e = a.c.D == 128 ? launch_attn<128, false>(a, k, s) : launch_attn<64, false>(a, k, s);
+  e = a.c.D == 128 ? launch_attn<128, false, false>(a, k, s) : launch_attn<64, false, false>(a, k, s);
   if (e != cudaSuccess) return e;
   if (a.wide) {
     k.jobs = reinterpret_cast<const Job*>(ws + p.l.wide);
     k.n_jobs = info->n_jobs + 1;
-    e = a.c.D == 128 ? launch_attn<128, true>(a, k, s) : launch_attn<64, true>(a, k, s);
+    e = a.c.D == 128 ? launch_attn<128, true, false>(a, k, s) : launch_attn<64, true, false>(a, k, s);
     if (e != cudaSuccess) return e;
   }
   JoinArgs j{};
@@ -1311,18 +1587,124 @@ cudaError_t launch_cache_attn(const CacheAttnArgs& a, cudaStream_t s) {
   j.part_lse = k.part_lse;
   j.o = a.o;
   j.lse = a.lse;
-  // few rows have many parts each: a block a row; else a warp a row (2,048 rows of a group of 8 over
-  // 34,000 keys 48.1 against 49.3 us for the call; 3,200 rows of 20 sequences 96.1 against 93.7)
   j.T = a.T;
-  const int64_t rows = a.T * a.c.Hq;
-  if (rows <= 16 * num_sms()) {
-    const dim3 grid(static_cast<unsigned>(rows));
-    return a.c.D == 128 ? launch_after(cache_join_kernel<128, kJoinWarps>, grid, kJoinThreads, 0, s, j)
-                        : launch_after(cache_join_kernel<64, kJoinWarps>, grid, kJoinThreads, 0, s, j);
+  return launch_join<false>(a, j, s);
+}
+
+namespace {
+
+// Chunks of every Q tile of a class, from the bounds alone: the number with the least estimated makespan,
+// in tiles as in the plan above (whole rounds of jobs, what a job costs beside its tiles, the
+// partial rows written and read).
+int window_chunks(int64_t tiles, int64_t jobs, int64_t streams, int64_t rows, bool wide) {
+  int best = 1;
+  double least = 0.0;
+  for (int n = 1; n <= tiles && n <= kMaxWindowChunks; ++n) {
+    if (n > 1 && n * rows > kMaxWindowRows) break;
+    const double len = static_cast<double>((tiles + n - 1) / n);
+    const double rounds = static_cast<double>((jobs * n + streams - 1) / streams);
+    const double cost = rounds * (len + (wide ? 4.5 : 3.0)) + (n > 1 ? n * rows * (wide ? 1.1e-4 : 7e-5) : 0.0);
+    if (n == 1 || cost < least) {
+      best = n;
+      least = cost;
+    }
   }
-  const dim3 grid(static_cast<unsigned>((rows + kJoinWarps - 1) / kJoinWarps));
-  return a.c.D == 128 ? launch_after(cache_join_kernel<128, 1>, grid, kJoinThreads, 0, s, j)
-                      : launch_after(cache_join_kernel<64, 1>, grid, kJoinThreads, 0, s, j);
+  return best;
+}
+
+}  // namespace
+
+CacheWindowLayout cache_window_layout(const CacheView& c, int S, int64_t T, int max_new, int64_t max_len, int64_t window,
+                                      int64_t sinks) {
+  CacheWindowLayout l{};
+  const int g = c.Hq / c.Hkv;
+  const int64_t sms = num_sms();
+  l.keys = static_cast<int>(window < max_len ? window : max_len);
+  l.sinks = static_cast<int>(sinks < max_len ? sinks : max_len);
+  const int64_t all = (max_len + 127) / 128;
+  // tiles in sight of n tokens at most
+  auto in_sight = [&](int64_t n) {
+    const int64_t t = (l.keys + n - 2) / 128 + 2 + (l.sinks + 127) / 128;
+    return t < all ? t : all;
+  };
+  const int64_t qn = kNarrowRows / g, per = 2 * (128 / g);
+  const bool wide = cache_attn_wide(c, T, max_new, 1);
+  const int64_t most = T < max_new ? T : max_new;
+  l.chunks[0] = window_chunks(in_sight(most < qn ? most : qn), static_cast<int64_t>(S) * c.Hkv, 2 * sms, T * c.Hq, false);
+  l.jobs[0] = static_cast<int64_t>(S) * c.Hkv * l.chunks[0];
+  if (wide) {
+    const int64_t slots = T / per + S;
+    l.chunks[1] = window_chunks(in_sight(most < per ? most : per), slots * c.Hkv, sms, T * c.Hq, true);
+    l.jobs[1] = slots * c.Hkv * l.chunks[1];
+  }
+  const int n = l.chunks[0] > l.chunks[1] ? l.chunks[0] : l.chunks[1];
+  const int64_t rows = n > 1 ? n * T * c.Hq : 0;
+  l.ok = l.jobs[0] < INT_MAX / 2 && l.jobs[1] < INT_MAX / 2;
+  auto put = [&](size_t* at, size_t bytes) {
+    *at = l.total;
+    l.total += (bytes + 255) / 256 * 256;
+  };
+  put(&l.bad, sizeof(int));
+  put(&l.list[0], sizeof(Job) * static_cast<size_t>(l.jobs[0]));
+  put(&l.list[1], sizeof(Job) * static_cast<size_t>(l.jobs[1]));
+  put(&l.lse, sizeof(float) * static_cast<size_t>(rows));
+  put(&l.o, sizeof(float) * static_cast<size_t>(rows) * c.D);
+  l.total += 256;      // offsets are from the workspace's first 256-byte boundary
+  return l;
+}
+
+cudaError_t launch_cache_window(const CacheAttnArgs& a, const CacheWindowLayout& l, cudaStream_t s) {
+  uint8_t* ws = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(a.ws) + 255) & ~static_cast<uintptr_t>(255));
+  AttnArgs k{};
+  k.c = a.c;
+  k.scale = a.scale;
+  k.layout = a.layout;
+  k.part_lse = reinterpret_cast<float*>(ws + l.lse);
+  k.part_o = reinterpret_cast<float*>(ws + l.o);
+  k.o = a.o;
+  k.o_whole = reinterpret_cast<uintptr_t>(a.o) % 32 == 0;
+  k.lse = a.lse;
+  k.status = a.status;
+  Window& w = k.w;
+  w.keys = l.keys;
+  w.sinks = l.sinks;
+  w.S = a.S;
+  w.T = a.T;
+  w.rows = a.rows;
+  w.cu = a.cu;
+  w.max_new = a.max_new;
+  w.max_len = a.max_len;
+  w.bad = reinterpret_cast<int*>(ws + l.bad);
+  auto set_class = [&](int cls) {
+    w.chunks = l.chunks[cls];
+    w.n_jobs = static_cast<int>(l.jobs[cls]);
+    w.jobs = reinterpret_cast<Job*>(ws + l.list[cls]);
+    k.jobs = w.jobs;
+  };
+  set_class(0);
+  cudaError_t e = a.c.D == 128 ? launch_attn<128, false, true>(a, k, s) : launch_attn<64, false, true>(a, k, s);
+  if (e != cudaSuccess) return e;
+  if (a.wide) {
+    set_class(1);
+    e = a.c.D == 128 ? launch_attn<128, true, true>(a, k, s) : launch_attn<64, true, true>(a, k, s);
+    if (e != cudaSuccess) return e;
+  }
+  set_class(0);
+  JoinArgs j{};
+  j.S = a.S;
+  j.group = 1;
+  j.Hq = a.c.Hq;
+  j.Hkv = a.c.Hkv;
+  j.T = a.T;
+  j.cu = a.cu;
+  j.part_o = k.part_o;
+  j.part_lse = k.part_lse;
+  j.o = a.o;
+  j.lse = a.lse;
+  j.c = a.c;
+  j.w = w;
+  j.chunks_wide = l.chunks[1];
+  return launch_join<true>(a, j, s);
 }
 
 }  // namespace ls

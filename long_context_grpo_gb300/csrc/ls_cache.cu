@@ -49,6 +49,9 @@ ls_status run_launch(int kernel, void* stream, const char* what, F launch) {
   return e == cudaSuccess ? LS_OK : static_cast<ls_status>(launch_failed(e, what));
 }
 
+ls_status attn_impl(ls_cache_t h, const ls_cache_attn_desc* d, const int64_t* sight, void* workspace,
+                    size_t workspace_bytes, void* stream);
+
 ls_status check_pages_ws(ls_cache_t h, const void* ws, size_t bytes) {
   if (ws == nullptr || bytes < ls_cache_pages_workspace_bytes(h)) return LS_ERR_WORKSPACE;
   return aligned16(ws) ? LS_OK : LS_ERR_MISALIGNED;
@@ -287,9 +290,34 @@ size_t ls_cache_attn_workspace_bytes(ls_cache_t h, int32_t S, int64_t T, int32_t
   return cache_attn_layout(h->view, S, T).total;
 }
 
+size_t ls_cache_attn_window_workspace_bytes(ls_cache_t h, int32_t S, int64_t T, int32_t max_new,
+                                            int64_t max_len, int64_t window, int64_t sinks) {
+  if (check_cache(h) != LS_OK || S < 1 || T < 1 || max_new < 1 || max_len < 1 || window < 1 || sinks < 0 ||
+      S > kMaxSeqs || T >= (int64_t(1) << 31) || max_len >= (int64_t(1) << 31))
+    return 0;
+  return cache_window_layout(h->view, S, T, max_new, max_len, window, sinks).total;
+}
+
 ls_status ls_cache_attn(ls_cache_t h, const ls_cache_attn_desc* d, void* workspace,
                         size_t workspace_bytes, void* stream) {
   NvtxRange nvtx_range("ls_cache_attn");
+  return attn_impl(h, d, nullptr, workspace, workspace_bytes, stream);
+}
+
+ls_status ls_cache_attn_window(ls_cache_t h, const ls_cache_attn_desc* d, int64_t window, int64_t sinks,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+  NvtxRange nvtx_range("ls_cache_attn_window");
+  const int64_t sight[2] = {window, sinks};
+  return attn_impl(h, d, sight, workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"
+
+namespace {
+
+// Attention of new tokens; sight: window and first tokens, or null.
+ls_status attn_impl(ls_cache_t h, const ls_cache_attn_desc* d, const int64_t* sight, void* workspace,
+                    size_t workspace_bytes, void* stream) {
   ls_status st = check_cache(h);
   if (st != LS_OK) return st;
   if (d == nullptr || d->cu_new == nullptr || d->q == nullptr || d->o == nullptr || d->lse == nullptr)
@@ -303,7 +331,16 @@ ls_status ls_cache_attn(ls_cache_t h, const ls_cache_attn_desc* d, void* workspa
     return LS_ERR_UNSUPPORTED;
   if (d->q_stride < static_cast<int64_t>(c.Hq) * c.D) return LS_ERR_INVALID_ARGUMENT;
   if (d->q_stride >= (int64_t(1) << 38)) return LS_ERR_UNSUPPORTED;
-  const size_t need = ls_cache_attn_workspace_bytes(h, d->S, d->T, d->max_new, d->max_len);
+  CacheWindowLayout layout{};
+  size_t need = 0;
+  if (sight != nullptr) {
+    if (sight[0] < 1 || sight[1] < 0) return LS_ERR_INVALID_ARGUMENT;
+    layout = cache_window_layout(c, d->S, d->T, d->max_new, d->max_len, sight[0], sight[1]);
+    if (!layout.ok) return LS_ERR_UNSUPPORTED;
+    need = layout.total;
+  } else {
+    need = ls_cache_attn_workspace_bytes(h, d->S, d->T, d->max_new, d->max_len);
+  }
   if (workspace == nullptr || workspace_bytes < need) return LS_ERR_WORKSPACE;
   if (!aligned16(d->q) || !aligned16(d->o) || d->q_stride % 8 != 0 || !aligned16(workspace) ||
       !aligned_n(d->lse, 4) || !aligned_n(d->rows, 4) || !aligned_n(d->cu_new, 4) ||
@@ -337,12 +374,13 @@ ls_status ls_cache_attn(ls_cache_t h, const ls_cache_attn_desc* d, void* workspa
                               static_cast<cuuint64_t>(d->T)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(c.D) * 2, static_cast<cuuint64_t>(d->q_stride) * 2};
   const cuuint32_t box[3] = {64, g, 128 / g}, boxn[3] = {64, g, 64 / g};
-  a.wide = cache_attn_wide(c, d->T, d->max_new, d->group);
+  a.wide = cache_attn_wide(c, d->T, d->max_new, sight != nullptr ? 1 : d->group);
   if (a.wide) st = static_cast<ls_status>(encode_bf16_map(&a.tm_q, d->q, 3, dims, strides, box));
   if (st == LS_OK) st = static_cast<ls_status>(encode_bf16_map(&a.tm_qn, d->q, 3, dims, strides, boxn));
   if (st != LS_OK) return st;
-  return run_launch(LS_KERNEL_CACHE_ATTN, stream, "cache attention launch",
-                    [&](cudaStream_t s) { return launch_cache_attn(a, s); });
+  return run_launch(LS_KERNEL_CACHE_ATTN, stream, "cache attention launch", [&](cudaStream_t s) {
+    return sight != nullptr ? launch_cache_window(a, layout, s) : launch_cache_attn(a, s);
+  });
 }
 
-}  // extern "C"
+}  // namespace

@@ -126,5 +126,19 @@ struct CacheAttnLayout {
 CacheAttnLayout cache_attn_layout(const CacheView& c, int S, int64_t T);
 bool cache_attn_wide(const CacheView& c, int64_t T, int max_new, int group);
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, cudaStream_t s);
+// Through a window (a.group and a.shared are not used): Q tiles' chunks, jobs and workspace, from the
+// host's bounds alone; [0] narrow, [1] wide.
+constexpr int kMaxWindowChunks = 64;
+constexpr int64_t kMaxWindowRows = int64_t(1) << 19;       // of partial results
+struct CacheWindowLayout {
+  int keys, sinks;            // clipped to the longest sequence
+  int chunks[2];
+  int64_t jobs[2];
+  bool ok;                    // the jobs can be counted
+  size_t bad, list[2], lse, o, total;
+};
+CacheWindowLayout cache_window_layout(const CacheView& c, int S, int64_t T, int max_new, int64_t max_len, int64_t window,
+                                      int64_t sinks);
+cudaError_t launch_cache_window(const CacheAttnArgs& a, const CacheWindowLayout& l, cudaStream_t s);
 
 }  // namespace ls

@@ -103,15 +103,20 @@ def sequence(pages, table_row, length, layout):
     return y[:length]
 
 
-def attend(q, k, v, scale):
+def attend(q, k, v, scale, window=None, sinks=0):
     """Attention of the last len(q) tokens of one sequence, causal: (o, lse, sum p |v|).
-    q [n, Hq, D]; k, v [L, Hkv, D]."""
+    q [n, Hq, D]; k, v [L, Hkv, D].  window: only the last `window` keys up to a token's own and the first
+    `sinks`; keys and values that nobody sees may be anything."""
     n, Hq, D = q.shape
     L, Hkv = k.shape[0], k.shape[1]
     g = Hq // Hkv
     o, a = np.zeros((n, Hq, D)), np.zeros((n, Hq, D))
     lse = np.full((n, Hq), -np.inf)
     hidden = np.arange(L)[None] > (L - n + np.arange(n))[:, None]
+    if window is not None:
+        back = (L - n + np.arange(n))[:, None] - np.arange(L)[None]
+        hidden |= (back >= window) & (np.arange(L) >= sinks)[None]
+        v = np.where(hidden.all(0)[:, None, None], 0.0, v)
     some = ~hidden.all(1) if L else np.zeros(n, dtype=bool)
     for h in range(Hq if some.any() else 0):
         s = np.where(hidden, -np.inf, q[:, h] @ k[:, h // g].T * scale)[some]
