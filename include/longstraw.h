@@ -560,7 +560,7 @@ ls_status ls_cache_attn(ls_cache_t h, const ls_cache_attn_desc* d, void* workspa
  *   stay in L2).
  *   workspace device, 16-byte aligned, >= ls_cache_attn_window_workspace_bytes of the same bounds
  *   (0 for bounds that the call refuses): lists of jobs, and room for partial results where long
- *   windows of few tokens are split, at most 2^19 rows of 4 D + 4 bytes.
+ *   windows of few tokens are split, at most 2^20 rows of 4 D + 4 bytes.
  */
 size_t ls_cache_attn_window_workspace_bytes(ls_cache_t h, int32_t S, int64_t T, int32_t max_new,
                                             int64_t max_len, int64_t window, int64_t sinks);

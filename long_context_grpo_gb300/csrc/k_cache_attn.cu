@@ -451,11 +451,11 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const __grid_c
 
 // --------------------------------------------------------------------------------------
 // Attention through a window: the token with L keys up to its own sees the last `keys` of them and the
-// row's first `sinks`.  What a Q tile's tokens see is bounded by the window, so no plan is needed:
-// every Q tile's tiles in sight are cut into `chunks` equal parts, jobs are numbered by (Q tile, chunk,
-// key head), and each CTA works its own out at its start.  Q tiles: a sequence's tokens (narrow), or
-// numbered so that a sequence's are found without a sum over those before it (wide): sequence b's start at
-// cu[b] / per + b, per the tokens of a pair of Q tiles; at most one of them is empty.
+// row's first `sinks`.  What a Q tile's tokens see is bounded by the window, so no plan is needed: a
+// unit is a Q tile and a key head, the first `whole` units are a job each, the others are cut into
+// `chunks` jobs of as many tiles, and each CTA works its own jobs out at its start.  Q tiles: a sequence's
+// tokens (narrow), or numbered so that a sequence's are found without a sum over those before it (wide):
+// sequence b's start at cu[b] / per + b, per the tokens of a pair of Q tiles; at most one of them is empty.
 struct Window {
   int keys, sinks;
   int S;
@@ -464,8 +464,9 @@ struct Window {
   const int32_t* cu;
   int max_new;
   int64_t max_len;
-  int chunks;       // of this class
-  int n_jobs;
+  int units, whole, chunks, n_jobs;     // of this class
+  int unit_rows;    // partial rows of a chunk
+  int part0;        // the class's first partial row
   Job* jobs;
   int* bad;         // workspace: offsets that fall
 };
@@ -517,18 +518,17 @@ __device__ __forceinline__ Sight window_sight(const CacheView& c, const Window& 
 // Chunk length of a Q tile with this many tiles in sight.
 __device__ __forceinline__ int window_chunk(int tiles, int chunks) { return (tiles + chunks - 1) / chunks; }
 
+// Unit u: its key head, and what its Q tile sees.
 template <bool kWide>
-__device__ __forceinline__ Job window_job(const CacheView& c, const Window& w, int x, uint32_t* status) {
+__device__ __forceinline__ Sight window_unit(const CacheView& c, const Window& w, int u, int* kv, uint32_t* status) {
   const int g = c.Hq / c.Hkv;
-  int kv, chunk, b, t0;
   const int per = kWide ? 2 * (128 / g) : kNarrowRows / g;
+  int b, t0;
   if constexpr (kWide) {
-    // Q tiles of one (chunk, key head) side by side: their windows overlap
-    const int slots = w.n_jobs / (c.Hkv * w.chunks);
-    const int slot = x % slots;
-    x /= slots;
-    kv = x % c.Hkv;
-    chunk = x / c.Hkv;
+    // Q tiles of one key head side by side: their windows overlap
+    const int slots = w.units / c.Hkv;
+    *kv = u / slots;
+    const int slot = u - *kv * slots;
     int lo = 0, hi = w.S - 1;           // the last sequence that starts at or before the slot
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
@@ -539,33 +539,41 @@ __device__ __forceinline__ Job window_job(const CacheView& c, const Window& w, i
     const int64_t at = w.cu[b] + static_cast<int64_t>(tile) * per;
     t0 = tile < 0 || at >= w.cu[b + 1] ? INT_MAX : static_cast<int>(at);
   } else {
-    // key heads of one chunk side by side: neighbours in memory
-    kv = x % c.Hkv;
-    x /= c.Hkv;
-    chunk = x % w.chunks;
-    b = x / w.chunks;
+    // key heads of one sequence side by side: neighbours in memory
+    b = u / c.Hkv;
+    *kv = u - b * c.Hkv;
     t0 = w.cu[b];
   }
-  const Sight s = window_sight(c, w, b, t0, per, kWide, status);
+  return window_sight(c, w, b, t0, per, kWide, status);
+}
+
+template <bool kWide>
+__device__ __forceinline__ Job window_job(const CacheView& c, const Window& w, int x, uint32_t* status) {
+  int u = x, chunk = 0;
+  if (x >= w.whole) {
+    // chunks of all units side by side
+    const int cut = w.units - w.whole;
+    chunk = (x - w.whole) / cut;
+    u = w.whole + (x - w.whole) - chunk * cut;
+  }
   Job j;
+  const Sight s = window_unit<kWide>(c, w, u, &j.kv, status);
   j.t0 = s.t0;
   j.n_tok = s.n_tok;
   j.row = s.row;
   j.lim = s.lim;
   j.key_end = s.key_end;
-  j.kv = kv;
   j.st = s.st;
   j.shift = s.shift;
   j.lo = s.lo;
   j.part = -1;
   j.tile0 = j.n_tiles = 0;
   if (s.tiles > 0) {
-    const int len = window_chunk(s.tiles, w.chunks);
+    const int len = x < w.whole ? s.tiles : window_chunk(s.tiles, w.chunks);
     j.tile0 = chunk * len;
     j.n_tiles = s.tiles - j.tile0;
     j.n_tiles = j.n_tiles < 0 ? 0 : (j.n_tiles > len ? len : j.n_tiles);
-    // rows of the partial results: [chunk][kv][token][head of the group]
-    if (s.tiles > len) j.part = static_cast<int>(((static_cast<int64_t>(chunk) * c.Hkv + kv) * w.T + s.t0) * g);
+    if (s.tiles > len) j.part = w.part0 + (x - w.whole) * w.unit_rows;
   }
   return j;
 }
@@ -622,7 +630,8 @@ struct Cfg {
   static constexpr int kBarODone = kBarPFull + 4;
   static constexpr int kBarOFree = kBarODone + 2;
   static constexpr int kBarDrain = kBarOFree + 2;
-  static constexpr int kNumBars = kBarDrain + 1;
+  static constexpr int kBarVClean = kBarDrain + 1;         // of a window
+  static constexpr int kNumBars = kBarVClean + kN;
   static constexpr int kSmem = kOffBar + kNumBars * 8 + 16 + 1024;
   __host__ __device__ static constexpr uint32_t col_s(int q) { return 128u * q; }
   __host__ __device__ static constexpr uint32_t col_o(int q) { return 256u + D * q; }
@@ -704,13 +713,40 @@ __device__ __forceinline__ Job load_stream(const AttnArgs& a, int item, int q, i
   }
   return j;
 }
+// The columns of tile j of a window's job that a row (token `tok` of its Q tile) sees: below lim, and not
+// in [first, low).
+struct Mask {
+  int lim, low, first;
+};
+// The lowest n bits, n clipped to 0 .. 32.
+__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u); }
+template <bool kWide>
+__device__ __forceinline__ Mask load_mask(const AttnArgs& a, int item, int q, int j, int qt, int tok) {
+  const Job* p = a.jobs + (kWide ? item : 2 * item + q);
+  int t0, n_tok, row, lim, tile0, part, st, shift, lo;
+  // (volatile: not the values that the loop's start loaded)
+  asm volatile("ld.global.v4.s32 {%0, %1, %2, %3}, [%4];" : "=r"(t0), "=r"(n_tok), "=r"(row), "=r"(lim) : "l"(p));
+  asm volatile("ld.global.s32 %0, [%1];" : "=r"(tile0) : "l"(&p->tile0));
+  asm volatile("ld.global.v4.s32 {%0, %1, %2, %3}, [%4];" : "=r"(part), "=r"(st), "=r"(shift), "=r"(lo) : "l"(&p->part));
+  if (kWide && q == 1) {
+    t0 += qt;
+    n_tok -= qt;
+  }
+  const int at = 128 * window_tile(tile0 + j, st, shift), limit = lim + t0 + tok;
+  Mask m;
+  // (rows that are not used need no mask: what they hold reaches no other row)
+  m.lim = tok < n_tok ? limit - at : 128;
+  m.low = (limit > a.w.keys ? limit - a.w.keys : 0) - at;
+  m.first = a.w.sinks - at;
+  return m;
+}
+
 // What the MMA warp needs of an item: the key tiles of its streams, and their keys from the first
 // tile's first key on.
 struct Runs {
   int n[2], keys[2];
-  int tile0[2], st[2], shift[2], lo[2];     // of a window; keys are counted from the row's first then
 };
-template <bool kWide, bool kWin>
+template <bool kWide>
 __device__ __forceinline__ Runs load_runs(const AttnArgs& a, int item, int n_jobs, int qt) {
   Runs r;
   r.n[0] = r.n[1] = r.keys[0] = r.keys[1] = 0;
@@ -720,14 +756,7 @@ __device__ __forceinline__ Runs load_runs(const AttnArgs& a, int item, int n_job
     if (at >= n_jobs) continue;
     const int4 y = reinterpret_cast<const int4*>(a.jobs + at)[1];
     r.n[q] = y.y;
-    r.keys[q] = y.z - (kWin ? 0 : 128 * y.x);
-    if constexpr (kWin) {
-      const int4 z = reinterpret_cast<const int4*>(a.jobs + at)[2];
-      r.tile0[q] = y.x;
-      r.st[q] = z.y;
-      r.shift[q] = z.z;
-      r.lo[q] = z.w;
-    }
+    r.keys[q] = y.z - 128 * y.x;
     if (kWide) {
       r.n[1] = reinterpret_cast<const int4*>(a.jobs + at)[0].y > qt ? y.y : 0;
       r.keys[1] = r.keys[0];
@@ -835,6 +864,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars[C::kBarOFree + q], kRowThreads);
     }
     mbar_init(&bars[C::kBarDrain], 1);
+    if constexpr (kWin)
+      for (int i = 0; i < C::kN; ++i) mbar_init(&bars[C::kBarVClean + i], 2);
     fence_mbar_init();
   }
   if (warp == 2) {
@@ -997,21 +1028,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                         va + static_cast<uint64_t>((kk * 2048) >> 4), kIdPV, (acc || i > 0) ? 1u : 0u);
         }
       };
-      // Clear the V rows from `from` to `to` (behind the sequence's end, or out of sight; whatever they
-      // hold must not meet a probability of zero).
-      auto clear_v = [&](uint32_t vstage, int from, int to) {
+      // Clear the V rows from `from` on (behind the sequence's end; whatever they hold must not
+      // meet a probability of zero).
+      auto clear_v = [&](uint32_t vstage, int from) {
         uint8_t* v = smem + C::kOffV + vstage * C::kTile;
-        for (int i = lane; i < (to - from) * 8; i += 32)
+        for (int i = lane; i < (128 - from) * 8; i += 32)
 #pragma unroll
           for (int b = 0; b < C::kBoxes; ++b)
             *reinterpret_cast<uint4*>(v + b * 16384 + from * 128 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
         fence_proxy_async_smem();
         __syncwarp();
       };
-      Runs next = load_runs<kWide, kWin>(a, blockIdx.x, n_jobs, qt);
+      Runs next = load_runs<kWide>(a, blockIdx.x, n_jobs, qt);
       for (int it = blockIdx.x; it < n_items && ok; it += gridDim.x) {
         const Runs s = next;
-        next = load_runs<kWide, kWin>(a, it + static_cast<int>(gridDim.x), n_jobs, qt);
+        next = load_runs<kWide>(a, it + static_cast<int>(gridDim.x), n_jobs, qt);
         const int most = s.n[0] > s.n[1] ? s.n[0] : s.n[1];
         if (most == 0) continue;
         ok = wait(C::kBarQFull, uc & 1u);
@@ -1045,14 +1076,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!kWide || q == 0) {
               ok = wait(C::kBarVFull + vs, (vit / C::kN) & 1u);
               if (!ok) break;
-              if constexpr (kWin) {
-                const int at = 128 * window_tile(s.tile0[q] + j, s.st[q], s.shift[q]);
-                const int left = s.keys[q] - at, lo = s.lo[q] - at, first = a.w.sinks - at;
-                if (lo > 0 && lo > first) clear_v(vs, first < 0 ? 0 : first, lo < 128 ? lo : 128);
-                if (left < 128) clear_v(vs, left < 0 ? 0 : left, 128);
+              if constexpr (kWin) {      // cleared by the warps beside this one
+                ok = wait(C::kBarVClean + vs, (vit / C::kN) & 1u);
+                if (!ok) break;
               } else {
                 const int left = s.keys[q] - 128 * j;
-                if (left < 128) clear_v(vs, left < 0 ? 0 : left, 128);
+                if (left < 128) clear_v(vs, left < 0 ? 0 : left);
               }
             }
             ok = wait(C::kBarPFull + 2 * q, (pph >> q) & 1u);
@@ -1099,6 +1128,43 @@ __global__ void __launch_bounds__(kThreads, 1)
       // every MMA (and the arrivals committed behind it) has landed before exit
       mma_commit_w(&bars[C::kBarDrain]);
       mbar_wait_ns(&bars[C::kBarDrain], 0u, ok ? 4000000000ull : 200000000ull);
+    } else if constexpr (kWin) {
+      // ------------------------------------------------------------ warps 2 and 3: V rows out of sight
+      // Rows that none of the job's tokens sees (before the window, behind the first tokens, behind the
+      // last token's own) are cleared: whatever they hold must not meet a probability of zero.  At most
+      // three tiles of a job have any; here they cost the MMA warp nothing (4 us a job in its own path).
+      uint32_t vit = 0;
+      bool ok = true;
+      for (int it = blockIdx.x; it < n_items && ok; it += gridDim.x) {
+        const Streams s = load_streams<kWide>(a, it, n_jobs, qt, g);
+        const int most = s.n[0] > s.n[1] ? s.n[0] : s.n[1];
+        for (int j = 0; j < most && ok; ++j) {
+#pragma unroll
+          for (int q = 0; q < (kWide ? 1 : 2); ++q) {
+            if (!ok || j >= s.n[q]) continue;
+            const uint32_t vs = vit % C::kN;
+            ok = __all_sync(0xffffffffu, mbar_wait(&bars[C::kBarVFull + vs], (vit / C::kN) & 1u, a.status, vabort));
+            if (!ok) break;
+            ++vit;
+            const int at = 128 * window_tile(s.j[q].tile0 + j, s.j[q].st, s.j[q].shift);
+            const int end = s.j[q].key_end - at, first = a.w.sinks - at, lo = s.j[q].lo - at;
+            if (end < 128 || (lo > 0 && lo > first)) {
+              uint8_t* v = smem + C::kOffV + vs * C::kTile;
+              for (int i = 32 * (warp - 2) + lane; i < 128 * 8; i += 64) {
+                const int r = i >> 3;
+                if (r < end && (r >= lo || r < first)) continue;
+#pragma unroll
+                for (int b = 0; b < C::kBoxes; ++b)
+                  *reinterpret_cast<uint4*>(v + b * 16384 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+              }
+              fence_proxy_async_smem();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[C::kBarVClean + vs]);
+          }
+        }
+      }
+      if (!ok) *vabort = 1;
     }
   } else {
     setreg_inc<kRegsSoftmax>();
@@ -1122,10 +1188,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int t = w.t0 + tok;
         // rows that are not used need no mask: what they hold reaches no other row
         int limit = INT_MAX;
-        int low = 0;                // of a window: its first key
+        int clear0 = 0, clear1 = 0;  // of a window: all the job's tokens see the whole of tiles [clear0, clear1)
         if constexpr (kWin) {
-          if (valid) limit = w.lim + t;
-          if (valid && limit > a.w.keys) low = limit - a.w.keys;
+          const int first = w.lim + w.t0, last = first + w.n_tok - 1;
+          if (last > a.w.keys) clear0 = ((last - a.w.keys + 127) >> 7) - w.shift - w.tile0;
+          clear1 = (first >> 7) - w.shift - w.tile0;
         } else {
           if (valid) limit = w.lim == INT_MIN ? __ldcg(a.lims + t) : w.lim + t;
           limit -= 128 * w.tile0;
@@ -1151,12 +1218,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld32(lane_base + colS + 96, sv[3]);
           tmem_ld_wait();
           if constexpr (kWin) {
-            const int at = 128 * window_tile(w.tile0 + j, w.st, w.shift);
-            const int lim = limit - at, lo = low - at, first = a.w.sinks - at;
-            if (lim < 128 || (lo > 0 && lo > first)) {
+            // what the mask needs is loaded again for the few tiles that it cuts (held through the loop it
+            // costs the softmax its registers: 4 chunks of 1,775 tokens 720 us)
+            if (j < clear0 || j >= clear1) {
+              const Mask m = load_mask<kWide>(a, it, q, j, qt, tok);
 #pragma unroll
-              for (int c = 0; c < 128; ++c)
-                if (c >= lim || (c < lo && c >= first)) sv[c >> 5][c & 31] = __float_as_uint(-INFINITY);
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t seen = below(m.lim - 32 * i) & (~below(m.low - 32 * i) | below(m.first - 32 * i));
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                  if (!(seen & (1u << c))) sv[i][c] = __float_as_uint(-INFINITY);
+              }
             }
           } else {
             const int lim = limit - 128 * j;
@@ -1314,16 +1386,12 @@ struct JoinArgs {
   const float* part_lse;
   uint16_t* o;
   float* lse;
-  // of a window
-  CacheView c;
-  Window w;
-  int chunks_wide;
 };
 
 // kPer warps join one (token, head) row: 1 with many rows, all of the block's with few rows of many
 // parts.  32 parts at a time: a lane loads one part's log-sum-exp, the warp sets the weights
 // (every warp of the row the same), then adds every kPer-th part's row, loads independent.
-template <int D, int kPer, bool kWin>
+template <int D, int kPer>
 __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_constant__ JoinArgs a) {
   constexpr int kV = D / 32;          // values of a lane
   __shared__ float so[kPer > 1 ? kJoinWarps : 1][D];
@@ -1343,26 +1411,11 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
   pdl_wait();
   if (!mine) return;                  // (with kPer > 1 for the whole block)
   // the row's part lists: its own segment's, and its group's
-  const int grouped = kWin ? 0 : a.info->grouped;
+  const int grouped = a.info->grouped;
   const int kv = h / g, hh = h - kv * g;
   int n[2] = {0, 0};
   int64_t first[2] = {0, 0}, step[2] = {0, 0};
   bool direct = false;
-  if constexpr (kWin) {
-    const int c0 = a.cu[b];
-    const bool wide = a.cu[b + 1] - c0 > kNarrowRows / g;
-    const int per = wide ? 2 * (128 / g) : kNarrowRows / g;
-    if (*a.w.bad == 0) {
-      const Sight s = window_sight(a.c, a.w, b, c0 + (t - c0) / per * per, per, wide, nullptr);
-      if (s.tiles > 0) {
-        const int len = window_chunk(s.tiles, wide ? a.chunks_wide : a.w.chunks);
-        n[0] = (s.tiles + len - 1) / len;
-        direct = n[0] == 1;
-        step[0] = a.T * a.Hq;
-        first[0] = (kv * a.T + t) * g + hh;
-      }
-    }
-  } else {
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     if (k == 1 && !grouped) continue;
@@ -1379,7 +1432,6 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
     step[k] = static_cast<int64_t>(s.n_tok) * g;
     first[k] = s.part + static_cast<int64_t>(kv) * s.chunks * step[k] + static_cast<int64_t>(t - s.t0) * g + hh;
     if (s.part < 0) direct = n[k] > 0;
-  }
   }
   if (direct) return;
   const int total = n[0] + n[1];
@@ -1440,6 +1492,133 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
   if (lane == 0) a.lse[out] = l == 0.0f ? -INFINITY : (m + __log2f(l)) * kLn2;
 }
 
+// The end of a call through a window.  The first blocks write the tokens that see no key, a thread a
+// token; the others join the partial results of the units that were cut, kPer warps a row, in chunk
+// order.  Nothing is done for rows that the attention kernels have written.
+struct WindowJoinArgs {
+  CacheView c;
+  Window w[2];                    // narrow, wide
+  int token_blocks;
+  int64_t rows[2];                // partial rows of a chunk of all units that are cut
+  const float* part_o;
+  const float* part_lse;
+  uint16_t* o;
+  float* lse;
+};
+
+template <int D, int kPer>
+__global__ void __launch_bounds__(kJoinThreads) window_join_kernel(const __grid_constant__ WindowJoinArgs a) {
+  constexpr int kV = D / 32;          // values of a lane
+  __shared__ float so[kPer > 1 ? kJoinWarps : 1][D];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = a.c.Hq / a.c.Hkv;
+  if (static_cast<int>(blockIdx.x) < a.token_blocks) {
+    const Window& w = a.w[0];
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * kJoinThreads + threadIdx.x;
+    int lo = 0, hi = t < w.T ? w.S : 0; // entries [0, lo) end at or before t, [hi, S) do not
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (w.cu[mid + 1] <= t) lo = mid + 1; else hi = mid;
+    }
+    bool empty = false;
+    if (t < w.T && lo < w.S && t >= w.cu[lo]) {
+      const int c0 = w.cu[lo], n = w.cu[lo + 1] - c0;
+      const bool wide = n > kNarrowRows / g;
+      const int per = wide ? 2 * (128 / g) : kNarrowRows / g;
+      const int t0 = c0 + (static_cast<int>(t) - c0) / per * per;
+      empty = window_sight(a.c, w, lo, t0, per, wide, nullptr).tiles == 0;
+    }
+    pdl_wait();
+    if (*w.bad != 0) empty = t < w.T && lo < w.S && t >= w.cu[lo];
+    uint32_t todo = __ballot_sync(0xffffffffu, empty);
+    const int64_t first = t - lane;
+    while (todo != 0) {
+      const int64_t at = first + __ffs(todo) - 1;
+      todo &= todo - 1;
+      for (int i = lane; i < a.c.Hq * D / 8; i += 32)
+        reinterpret_cast<uint4*>(a.o + at * a.c.Hq * D)[i] = make_uint4(0u, 0u, 0u, 0u);
+      for (int h = lane; h < a.c.Hq; h += 32) a.lse[at * a.c.Hq + h] = -INFINITY;
+    }
+    return;
+  }
+  int64_t x = ((static_cast<int64_t>(blockIdx.x) - a.token_blocks) * kJoinWarps + warp) / kPer;
+  const int cls = x < a.rows[0] ? 0 : 1;
+  if (cls == 1) x -= a.rows[0];
+  Sight s;
+  s.tiles = 0;
+  int kv = 0, unit = 0, row = 0;
+  const Window& w = a.w[cls];
+  if (x < a.rows[cls]) {
+    unit = static_cast<int>(x / w.unit_rows);
+    row = static_cast<int>(x - static_cast<int64_t>(unit) * w.unit_rows);
+    s = cls ? window_unit<true>(a.c, w, w.whole + unit, &kv, nullptr) : window_unit<false>(a.c, w, w.whole + unit, &kv, nullptr);
+  }
+  pdl_wait();
+  const int tok = row / g;
+  if (s.tiles == 0 || tok >= s.n_tok || *w.bad != 0) return;         // (with kPer > 1 for the whole block)
+  const int len = window_chunk(s.tiles, w.chunks);
+  const int total = (s.tiles + len - 1) / len;
+  if (total == 1) return;
+  const int64_t first = static_cast<int64_t>(w.part0) + static_cast<int64_t>(unit) * w.unit_rows + row;
+  const int64_t step = static_cast<int64_t>(w.units - w.whole) * w.unit_rows;
+  const int64_t out = (static_cast<int64_t>(s.t0) + tok) * a.c.Hq + kv * g + (row - tok * g);
+  float m = -INFINITY, l = 0.0f, acc[kV];
+#pragma unroll
+  for (int i = 0; i < kV; ++i) acc[i] = 0.0f;
+  for (int p0 = 0; p0 < total; p0 += 32) {
+    const int p = p0 + lane;
+    const int64_t part = first + p * step;
+    const float v = p < total ? __ldcg(a.part_lse + part) : -INFINITY;
+    float mx = v;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+    // (the maximum drops a NaN part, its weight does not)
+    if (mx == -INFINITY && !__any_sync(0xffffffffu, v != v)) continue;
+    const float mn = fmaxf(m, mx);
+    const float f = ex2_approx(m - mn);
+    const float e = ex2_approx(v - mn);
+    float ws = e;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) ws += __shfl_xor_sync(0xffffffffu, ws, off);
+    m = mn;
+    l = l * f + ws;
+#pragma unroll
+    for (int i = 0; i < kV; ++i) acc[i] *= f;
+    const int cnt = total - p0 < 32 ? total - p0 : 32;
+#pragma unroll 4
+    for (int k = warp % kPer; k < cnt; k += kPer) {
+      const float wk = __shfl_sync(0xffffffffu, e, k);
+      const float* src = a.part_o + (first + (p0 + k) * step) * D + lane * kV;
+      if constexpr (kV == 4) {
+        const float4 y = __ldcg(reinterpret_cast<const float4*>(src));
+        acc[0] = fmaf(wk, y.x, acc[0]);
+        acc[1] = fmaf(wk, y.y, acc[1]);
+        acc[2] = fmaf(wk, y.z, acc[2]);
+        acc[3] = fmaf(wk, y.w, acc[3]);
+      } else {
+        const float2 y = __ldcg(reinterpret_cast<const float2*>(src));
+        acc[0] = fmaf(wk, y.x, acc[0]);
+        acc[1] = fmaf(wk, y.y, acc[1]);
+      }
+    }
+  }
+  if constexpr (kPer > 1) {
+#pragma unroll
+    for (int i = 0; i < kV; ++i) so[warp][lane * kV + i] = acc[i];
+    __syncthreads();
+    if (warp > 0) return;
+#pragma unroll
+    for (int k = 1; k < kPer; ++k)
+#pragma unroll
+      for (int i = 0; i < kV; ++i) acc[i] += so[k][lane * kV + i];
+  }
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(a.o + out * D) + lane * (kV / 2);
+#pragma unroll
+  for (int i = 0; i < kV / 2; ++i) dst[i] = pack_bf16x2(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+  if (lane == 0) a.lse[out] = l == 0.0f ? -INFINITY : (m + __log2f(l)) * kLn2;
+}
+
 template <int D, bool kWide, bool kWin>
 cudaError_t launch_attn(const CacheAttnArgs& a, const AttnArgs& p, cudaStream_t s) {
   using C = Cfg<D, kWide>;
@@ -1465,21 +1644,6 @@ cudaError_t launch_attn(const CacheAttnArgs& a, const AttnArgs& p, cudaStream_t 
     return launch_after(cache_attn_kernel<D, kWide, kWin>, grid, kThreads, C::kSmem, s, *a.tm_k, *a.tm_v,
                         kWide ? a.tm_q : a.tm_qn, p);
   }
-}
-
-template <bool kWin>
-cudaError_t launch_join(const CacheAttnArgs& a, const JoinArgs& j, cudaStream_t s) {
-  // few rows have many parts each: a block a row; else a warp a row (2,048 rows of a group of 8 over
-  // 34,000 keys 48.1 against 49.3 us for the call; 3,200 rows of 20 sequences 96.1 against 93.7)
-  const int64_t rows = a.T * a.c.Hq;
-  if (rows <= 16 * num_sms()) {
-    const dim3 grid(static_cast<unsigned>(rows));
-    return a.c.D == 128 ? launch_after(cache_join_kernel<128, kJoinWarps, kWin>, grid, kJoinThreads, 0, s, j)
-                        : launch_after(cache_join_kernel<64, kJoinWarps, kWin>, grid, kJoinThreads, 0, s, j);
-  }
-  const dim3 grid(static_cast<unsigned>((rows + kJoinWarps - 1) / kJoinWarps));
-  return a.c.D == 128 ? launch_after(cache_join_kernel<128, 1, kWin>, grid, kJoinThreads, 0, s, j)
-                      : launch_after(cache_join_kernel<64, 1, kWin>, grid, kJoinThreads, 0, s, j);
 }
 
 constexpr int kPlanSeg = sizeof(Seg) + 2 * sizeof(int);   // shared memory of a segment
@@ -1587,29 +1751,47 @@ cudaError_t launch_cache_attn(const CacheAttnArgs& a, cudaStream_t s) {
   j.part_lse = k.part_lse;
   j.o = a.o;
   j.lse = a.lse;
+  // few rows have many parts each: a block a row; else a warp a row (2,048 rows of a group of 8 over
+  // 34,000 keys 48.1 against 49.3 us for the call; 3,200 rows of 20 sequences 96.1 against 93.7)
   j.T = a.T;
-  return launch_join<false>(a, j, s);
+  const int64_t rows = a.T * a.c.Hq;
+  if (rows <= 16 * num_sms()) {
+    const dim3 grid(static_cast<unsigned>(rows));
+    return a.c.D == 128 ? launch_after(cache_join_kernel<128, kJoinWarps>, grid, kJoinThreads, 0, s, j)
+                        : launch_after(cache_join_kernel<64, kJoinWarps>, grid, kJoinThreads, 0, s, j);
+  }
+  const dim3 grid(static_cast<unsigned>((rows + kJoinWarps - 1) / kJoinWarps));
+  return a.c.D == 128 ? launch_after(cache_join_kernel<128, 1>, grid, kJoinThreads, 0, s, j)
+                      : launch_after(cache_join_kernel<64, 1>, grid, kJoinThreads, 0, s, j);
 }
 
 namespace {
 
-// Chunks of every Q tile of a class, from the bounds alone: the number with the least estimated makespan,
-// in tiles as in the plan above (whole rounds of jobs, what a job costs beside its tiles, the
-// partial rows written and read).
-int window_chunks(int64_t tiles, int64_t jobs, int64_t streams, int64_t rows, bool wide) {
-  int best = 1;
-  double least = 0.0;
-  for (int n = 1; n <= tiles && n <= kMaxWindowChunks; ++n) {
-    if (n > 1 && n * rows > kMaxWindowRows) break;
-    const double len = static_cast<double>((tiles + n - 1) / n);
-    const double rounds = static_cast<double>((jobs * n + streams - 1) / streams);
-    const double cost = rounds * (len + (wide ? 4.5 : 3.0)) + (n > 1 ? n * rows * (wide ? 1.1e-4 : 7e-5) : 0.0);
-    if (n == 1 || cost < least) {
-      best = n;
-      least = cost;
+// How the units of a class become jobs, from the bounds alone: the first `whole` as they are, the others
+// in `chunks`, with the least estimated makespan in tiles as in the plan above (whole rounds of jobs, what
+// a job costs beside its tiles, the partial rows written and read).  Either all are cut, or those that
+// would make the last round (1,248 jobs on 152 streams: eight rounds and a bit, not nine).
+struct WindowCut {
+  int64_t whole;
+  int chunks;
+};
+WindowCut window_cut(int64_t tiles, int64_t units, int64_t streams, int64_t unit_rows, bool wide) {
+  WindowCut best{units, 1};
+  const double more = wide ? 4.5 : 3.0;
+  double least = static_cast<double>((units + streams - 1) / streams) * (tiles + more);
+  for (int64_t rounds = units / streams;; rounds = 0) {
+    const int64_t cut = units - rounds * streams;
+    for (int n = 2; n <= tiles && n <= kMaxWindowChunks && cut > 0 && cut * n * unit_rows <= kMaxWindowRows; ++n) {
+      const double len = static_cast<double>((tiles + n - 1) / n);
+      const double cost = rounds * (tiles + more) + static_cast<double>((cut * n + streams - 1) / streams) * (len + more) +
+                          cut * n * unit_rows * (wide ? 1.1e-4 : 7e-5);
+      if (cost < least) {
+        best = {rounds * streams, n};
+        least = cost;
+      }
     }
+    if (rounds == 0) return best;
   }
-  return best;
 }
 
 }  // namespace
@@ -1627,19 +1809,22 @@ CacheWindowLayout cache_window_layout(const CacheView& c, int S, int64_t T, int 
     const int64_t t = (l.keys + n - 2) / 128 + 2 + (l.sinks + 127) / 128;
     return t < all ? t : all;
   };
-  const int64_t qn = kNarrowRows / g, per = 2 * (128 / g);
-  const bool wide = cache_attn_wide(c, T, max_new, 1);
+  const int64_t per[2] = {kNarrowRows / g, 2 * (128 / g)};
   const int64_t most = T < max_new ? T : max_new;
-  l.chunks[0] = window_chunks(in_sight(most < qn ? most : qn), static_cast<int64_t>(S) * c.Hkv, 2 * sms, T * c.Hq, false);
-  l.jobs[0] = static_cast<int64_t>(S) * c.Hkv * l.chunks[0];
-  if (wide) {
-    const int64_t slots = T / per + S;
-    l.chunks[1] = window_chunks(in_sight(most < per ? most : per), slots * c.Hkv, sms, T * c.Hq, true);
-    l.jobs[1] = slots * c.Hkv * l.chunks[1];
+  int64_t rows = 0;
+  l.ok = true;
+  for (int cls = 0; cls < (cache_attn_wide(c, T, max_new, 1) ? 2 : 1); ++cls) {
+    const int64_t tok = most < per[cls] ? most : per[cls];
+    l.units[cls] = (cls ? T / per[1] + S : static_cast<int64_t>(S)) * c.Hkv;
+    l.unit_rows[cls] = static_cast<int>(tok * g);
+    const WindowCut cut = window_cut(in_sight(tok), l.units[cls], cls ? sms : 2 * sms, tok * g, cls == 1);
+    l.whole[cls] = cut.whole;
+    l.chunks[cls] = cut.chunks;
+    l.jobs[cls] = cut.whole + (l.units[cls] - cut.whole) * cut.chunks;
+    l.part0[cls] = rows;
+    if (cut.chunks > 1) rows += (l.units[cls] - cut.whole) * cut.chunks * tok * g;
+    l.ok = l.ok && l.jobs[cls] < INT_MAX / 2;
   }
-  const int n = l.chunks[0] > l.chunks[1] ? l.chunks[0] : l.chunks[1];
-  const int64_t rows = n > 1 ? n * T * c.Hq : 0;
-  l.ok = l.jobs[0] < INT_MAX / 2 && l.jobs[1] < INT_MAX / 2;
   auto put = [&](size_t* at, size_t bytes) {
     *at = l.total;
     l.total += (bytes + 255) / 256 * 256;
@@ -1675,36 +1860,45 @@ cudaError_t launch_cache_window(const CacheAttnArgs& a, const CacheWindowLayout&
   w.max_new = a.max_new;
   w.max_len = a.max_len;
   w.bad = reinterpret_cast<int*>(ws + l.bad);
-  auto set_class = [&](int cls) {
+  Window both[2];
+  for (int cls = 0; cls < 2; ++cls) {
+    w.units = static_cast<int>(l.units[cls]);
+    w.whole = static_cast<int>(l.whole[cls]);
     w.chunks = l.chunks[cls];
     w.n_jobs = static_cast<int>(l.jobs[cls]);
+    w.unit_rows = l.unit_rows[cls];
+    w.part0 = static_cast<int>(l.part0[cls]);
     w.jobs = reinterpret_cast<Job*>(ws + l.list[cls]);
     k.jobs = w.jobs;
-  };
-  set_class(0);
-  cudaError_t e = a.c.D == 128 ? launch_attn<128, false, true>(a, k, s) : launch_attn<64, false, true>(a, k, s);
-  if (e != cudaSuccess) return e;
-  if (a.wide) {
-    set_class(1);
-    e = a.c.D == 128 ? launch_attn<128, true, true>(a, k, s) : launch_attn<64, true, true>(a, k, s);
+    both[cls] = w;
+    if (cls == 1 && !a.wide) break;
+    cudaError_t e;
+    if (cls == 0)
+      e = a.c.D == 128 ? launch_attn<128, false, true>(a, k, s) : launch_attn<64, false, true>(a, k, s);
+    else
+      e = a.c.D == 128 ? launch_attn<128, true, true>(a, k, s) : launch_attn<64, true, true>(a, k, s);
     if (e != cudaSuccess) return e;
   }
-  set_class(0);
-  JoinArgs j{};
-  j.S = a.S;
-  j.group = 1;
-  j.Hq = a.c.Hq;
-  j.Hkv = a.c.Hkv;
-  j.T = a.T;
-  j.cu = a.cu;
+  WindowJoinArgs j{};
+  j.c = a.c;
+  j.token_blocks = static_cast<int>((a.T + kJoinThreads - 1) / kJoinThreads);
+  for (int cls = 0; cls < 2; ++cls) {
+    j.w[cls] = both[cls];
+    j.rows[cls] = l.chunks[cls] > 1 ? (l.units[cls] - l.whole[cls]) * l.unit_rows[cls] : 0;
+  }
   j.part_o = k.part_o;
   j.part_lse = k.part_lse;
   j.o = a.o;
   j.lse = a.lse;
-  j.c = a.c;
-  j.w = w;
-  j.chunks_wide = l.chunks[1];
-  return launch_join<true>(a, j, s);
+  const int64_t rows = j.rows[0] + j.rows[1];
+  if (rows <= 16 * num_sms()) {       // few rows have many parts each: a block a row
+    const dim3 grid(static_cast<unsigned>(j.token_blocks + rows));
+    return a.c.D == 128 ? launch_after(window_join_kernel<128, kJoinWarps>, grid, kJoinThreads, 0, s, j)
+                        : launch_after(window_join_kernel<64, kJoinWarps>, grid, kJoinThreads, 0, s, j);
+  }
+  const dim3 grid(static_cast<unsigned>(j.token_blocks + (rows + kJoinWarps - 1) / kJoinWarps));
+  return a.c.D == 128 ? launch_after(window_join_kernel<128, 1>, grid, kJoinThreads, 0, s, j)
+                      : launch_after(window_join_kernel<64, 1>, grid, kJoinThreads, 0, s, j);
 }
 
 }  // namespace ls

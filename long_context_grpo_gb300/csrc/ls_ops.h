@@ -132,8 +132,8 @@ constexpr int kMaxWindowChunks = 64;
 constexpr int64_t kMaxWindowRows = int64_t(1) << 19;       // of partial results
 struct CacheWindowLayout {
   int keys, sinks;            // clipped to the longest sequence
-  int chunks[2];
-  int64_t jobs[2];
+  int chunks[2], unit_rows[2];
+  int64_t units[2], whole[2], jobs[2], part0[2];
   bool ok;                    // the jobs can be counted
   size_t bad, list[2], lse, o, total;
 };
