@@ -745,8 +745,12 @@ __device__ __forceinline__ Mask load_mask(const AttnArgs& a, int item, int q, in
 // tile's first key on.
 struct Runs {
   int n[2], keys[2];
+  int whole0[2], whole1[2];     // of a window: tiles without rows to be cleared
 };
-template <bool kWide>
+// Of a window's job: no row of its tiles [whole0, whole1) is out of sight of all its tokens.
+__device__ __forceinline__ int window_whole0(int tile0, int st, int lo) { return lo > 0 ? st + 1 - tile0 : 0; }
+__device__ __forceinline__ int window_whole1(int tile0, int key_end, int shift) { return (key_end >> 7) - shift - tile0; }
+template <bool kWide, bool kWin>
 __device__ __forceinline__ Runs load_runs(const AttnArgs& a, int item, int n_jobs, int qt) {
   Runs r;
   r.n[0] = r.n[1] = r.keys[0] = r.keys[1] = 0;
@@ -757,6 +761,11 @@ __device__ __forceinline__ Runs load_runs(const AttnArgs& a, int item, int n_job
     const int4 y = reinterpret_cast<const int4*>(a.jobs + at)[1];
     r.n[q] = y.y;
     r.keys[q] = y.z - 128 * y.x;
+    if constexpr (kWin) {
+      const int4 z = reinterpret_cast<const int4*>(a.jobs + at)[2];
+      r.whole0[q] = window_whole0(y.x, z.y, z.w);
+      r.whole1[q] = window_whole1(y.x, y.z, z.z);
+    }
     if (kWide) {
       r.n[1] = reinterpret_cast<const int4*>(a.jobs + at)[0].y > qt ? y.y : 0;
       r.keys[1] = r.keys[0];
@@ -854,7 +863,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars[C::kBarKFull + i], 1);
       mbar_init(&bars[C::kBarKEmpty + i], 1);
       mbar_init(&bars[C::kBarVFull + i], 1);
-      mbar_init(&bars[C::kBarVEmpty + i], 1);
+      mbar_init(&bars[C::kBarVEmpty + i], kWin ? 3 : 1);
     }
     for (int q = 0; q < 2; ++q) {
       mbar_init(&bars[C::kBarSFull + q], 1);
@@ -1004,6 +1013,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t dV0 = smem_desc(smem_u32(smem + C::kOffV), 16384, 1024);
       uint32_t kit = 0, vit = 0, uc = 0;
       uint32_t pph = 0u;               // bit q: parity of the next p_full waits of stream q
+      uint32_t cph = 0u;               // bit i: parity of the next wait for the cleared V tile of stage i
       uint32_t uq[2] = {0u, 0u};       // jobs done per stream
       bool ok = true;
       auto wait = [&](int bar, uint32_t parity) {
@@ -1039,10 +1049,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_proxy_async_smem();
         __syncwarp();
       };
-      Runs next = load_runs<kWide>(a, blockIdx.x, n_jobs, qt);
+      Runs next = load_runs<kWide, kWin>(a, blockIdx.x, n_jobs, qt);
       for (int it = blockIdx.x; it < n_items && ok; it += gridDim.x) {
         const Runs s = next;
-        next = load_runs<kWide>(a, it + static_cast<int>(gridDim.x), n_jobs, qt);
+        next = load_runs<kWide, kWin>(a, it + static_cast<int>(gridDim.x), n_jobs, qt);
         const int most = s.n[0] > s.n[1] ? s.n[0] : s.n[1];
         if (most == 0) continue;
         ok = wait(C::kBarQFull, uc & 1u);
@@ -1076,9 +1086,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!kWide || q == 0) {
               ok = wait(C::kBarVFull + vs, (vit / C::kN) & 1u);
               if (!ok) break;
-              if constexpr (kWin) {      // cleared by the warps beside this one
-                ok = wait(C::kBarVClean + vs, (vit / C::kN) & 1u);
-                if (!ok) break;
+              if constexpr (kWin) {
+                if (j < s.whole0[q] || j >= s.whole1[q]) {      // cleared by the warps beside this one
+                  ok = wait(C::kBarVClean + vs, (cph >> vs) & 1u);
+                  if (!ok) break;
+                  cph ^= 1u << vs;
+                }
               } else {
                 const int left = s.keys[q] - 128 * j;
                 if (left < 128) clear_v(vs, left < 0 ? 0 : left);
@@ -1131,8 +1144,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if constexpr (kWin) {
       // ------------------------------------------------------------ warps 2 and 3: V rows out of sight
       // Rows that none of the job's tokens sees (before the window, behind the first tokens, behind the
-      // last token's own) are cleared: whatever they hold must not meet a probability of zero.  At most
-      // three tiles of a job have any; here they cost the MMA warp nothing (4 us a job in its own path).
+      // last token's own) are cleared: whatever they hold must not meet a probability of zero.  Few
+      // tiles of a job have any; here they cost the MMA warp nothing (4 us a job in its own path), which
+      // waits for these tiles alone.  A stage is free for its next tile once these warps have seen it too.
       uint32_t vit = 0;
       bool ok = true;
       for (int it = blockIdx.x; it < n_items && ok; it += gridDim.x) {
@@ -1146,9 +1160,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = __all_sync(0xffffffffu, mbar_wait(&bars[C::kBarVFull + vs], (vit / C::kN) & 1u, a.status, vabort));
             if (!ok) break;
             ++vit;
-            const int at = 128 * window_tile(s.j[q].tile0 + j, s.j[q].st, s.j[q].shift);
-            const int end = s.j[q].key_end - at, first = a.w.sinks - at, lo = s.j[q].lo - at;
-            if (end < 128 || (lo > 0 && lo > first)) {
+            if (j < window_whole0(s.j[q].tile0, s.j[q].st, s.j[q].lo) ||
+                j >= window_whole1(s.j[q].tile0, s.j[q].key_end, s.j[q].shift)) {
+              const int at = 128 * window_tile(s.j[q].tile0 + j, s.j[q].st, s.j[q].shift);
+              const int end = s.j[q].key_end - at, first = a.w.sinks - at, lo = s.j[q].lo - at;
               uint8_t* v = smem + C::kOffV + vs * C::kTile;
               for (int i = 32 * (warp - 2) + lane; i < 128 * 8; i += 64) {
                 const int r = i >> 3;
@@ -1158,9 +1173,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                   *reinterpret_cast<uint4*>(v + b * 16384 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
               }
               fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&bars[C::kBarVClean + vs]);
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[C::kBarVClean + vs]);
+            if (lane == 0) mbar_arrive(&bars[C::kBarVEmpty + vs]);
           }
         }
       }
