@@ -105,6 +105,18 @@ typedef struct {
  */
 ls_status ls_prefix_prepare(const ls_prefix_desc* desc, ls_prefix_t* out, void* stream);
 
+/*
+ * ls_prefix_set_window -- the handle's layer is windowed: from now on its replays' queries see the last
+ * `window` keys up to their own and the sequence's first `sinks` (the sequence: prompt and response; query
+ * t of a response has position P + t and sees the keys j <= P + t with j > P + t - window or j < sinks).
+ * Holds for ls_replay_fwd/bwd, the packed and the blockwise replay (there the position is prefix_len + t); the
+ * softmax, its gradients and the accumulators are as without it, with the other keys left out: they
+ * are neither read nor, in the accumulators, written.  A forward and its backward have to be made
+ * under the same window.  The prompt-only calls return LS_ERR_UNSUPPORTED.  window >= 1 and sinks >= 0,
+ * either may pass the sequence; window = 0 with sinks = 0 takes the window away.
+ */
+ls_status ls_prefix_set_window(ls_prefix_t h, int64_t window, int64_t sinks);
+
 /* Release the handle's host metadata.  Does not touch device memory. NULL is a no-op. */
 ls_status ls_prefix_destroy(ls_prefix_t h);
 

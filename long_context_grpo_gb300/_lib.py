@@ -101,6 +101,7 @@ def _load():
     sig = {
         "ls_prefix_prepare": (ctypes.c_int, [ctypes.POINTER(PrefixDesc), ctypes.POINTER(vp), vp]),
         "ls_prefix_destroy": (ctypes.c_int, [vp]),
+        "ls_prefix_set_window": (ctypes.c_int, [vp, i64, i64]),
         "ls_replay_fwd": (ctypes.c_int, [vp, i64, vp, vp, vp, vp, vp, vp]),
         "ls_replay_bwd_workspace_bytes": (sz, [vp, i64]),
         "ls_replay_bwd": (ctypes.c_int, [vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
@@ -202,10 +203,12 @@ class Prefix:
     """Resident prompt K/V of one attention layer and its fp32 gradient accumulators.
 
     The tensors are borrowed: they must outlive the handle, and k/v are never written.
-    Creating the handle zeroes dk_acc / dv_acc on the current stream.
+    Creating the handle zeroes dk_acc / dv_acc on the current stream.  window: the layer is
+    windowed, a query sees the last `window` keys up to its own and the sequence's first `sinks`.
     """
 
-    def __init__(self, k_prefix, v_prefix, dk_acc, dv_acc, Hq: int, softmax_scale: float = 0.0):
+    def __init__(self, k_prefix, v_prefix, dk_acc, dv_acc, Hq: int, softmax_scale: float = 0.0,
+                 window: int = 0, sinks: int = 0):
         L = _lib()
         P, Hkv, D = k_prefix.shape
         self.P, self.Hq, self.Hkv, self.D = P, Hq, Hkv, D
@@ -219,6 +222,13 @@ class Prefix:
         _check(L.ls_prefix_prepare(ctypes.byref(d), ctypes.byref(h), _stream()), "ls_prefix_prepare")
         self._h = h
         self.dk_acc, self.dv_acc = dk_acc, dv_acc
+        if window != 0 or sinks != 0:
+            self.set_window(window, sinks)
+
+    def set_window(self, window: int, sinks: int = 0):
+        """A sliding window for the replays from now on (window = 0: none); a forward and its
+        backward have to be made under the same one."""
+        _check(_lib().ls_prefix_set_window(self._h, window, sinks), "ls_prefix_set_window")
 
     def close(self):
         if getattr(self, "_h", None) is not None and self._h.value is not None:

@@ -33,10 +33,12 @@
 // warp 2 TMEM owner, warps 4-11 two softmax warpgroups; warpgroup w owns tile columns
 // [64 w, 64 w + 64).  Every wait is bounded (status word + clean exit on timeout).
 //
-// Instantiations <D, kPacked, kNoSuffix> as in the forward: packed responses (a prompt tile
+// Instantiations <D, kPacked, kNoSuffix, kWindow> as in the forward: packed responses (a prompt tile
 // then sweeps the Q tiles of every response before its single read-modify-write; Q rows past
 // a response's end carry +inf row statistics), or prompt keys only (context-parallel
 // shards).
+#include <climits>
+
 #include "ls_internal.h"
 #include "ptx.cuh"
 
@@ -97,15 +99,81 @@ struct KvUnit {
   int b;      // suffix tiles: response
   int f0;     // first flat 128-row Q tile that sees the tile
   int n;      // number of Q tiles
+  int t_end;  // of a window: queries from here on see none of the tile's keys
 };
+
+// Through a window: the Q tiles of response b that see a prompt tile, and the walk over all that do.
+__device__ __forceinline__ int window_q_tiles(const KvUnit& w, const AttnShape& sh, const Varlen& vl, int b) {
+  const int R = vl.row0[b + 1] - vl.row0[b];
+  const int t = R < w.t_end ? R : w.t_end;
+  return t <= 0 ? 0 : (t + sh.qt - 1) / sh.qt;
+}
+struct QWalk {
+  int b, i, n;     // tile i of the n of response b
+  __device__ __forceinline__ void start(const KvUnit& w, const AttnShape& sh, const Varlen& vl) {
+    b = w.b;
+    i = w.f0 - vl.qt0[b];
+    n = w.prompt ? window_q_tiles(w, sh, vl, b) : i + w.n;
+    while (i >= n && b + 1 < vl.G) skip(w, sh, vl);
+  }
+  __device__ __forceinline__ void skip(const KvUnit& w, const AttnShape& sh, const Varlen& vl) {
+    ++b;
+    i = 0;
+    n = window_q_tiles(w, sh, vl, b);
+  }
+  __device__ __forceinline__ void next(const KvUnit& w, const AttnShape& sh, const Varlen& vl) {
+    ++i;
+    while (i >= n && w.prompt && b + 1 < vl.G) skip(w, sh, vl);
+  }
+};
+// Key tiles of one kv head that any query sees.
+__host__ __device__ inline int window_kv_tiles(const AttnShape& sh, const Varlen& vl) {
+  const PromptTiles pt = prompt_tiles(sh, 0);
+  return pt.first + pt.n_pt - pt.second + vl.kt0[vl.G];
+}
 
 // Flat unit u -> (kv head, 128-key tile).  A prompt tile is seen by every Q tile of every
 // packed response; a suffix tile of response b by that response's tiles from the first
 // one holding a query at or after its first key.
-template <bool kPacked, bool kNoSuffix>
+template <bool kPacked, bool kNoSuffix, bool kWindow>
 __device__ __forceinline__ KvUnit make_kv_unit(int u, const AttnShape& sh, const Varlen& vl) {
   const int n_pt = static_cast<int>((sh.P + 127) / 128);
   KvUnit w;
+  if constexpr (kWindow) {
+    const PromptTiles pt = prompt_tiles(sh, 0);
+    const int n_p = pt.first + n_pt - pt.second, n_all = n_p + vl.kt0[vl.G];
+    w.kv = u / n_all;
+    const int j = u - w.kv * n_all;
+    w.prompt = j < n_p;
+    int64_t last;      // the tile's last key and its first one, counted from the prompt's end
+    if (w.prompt) {
+      w.key0 = 128 * (j < pt.first ? j : j - pt.first + pt.second);
+      w.base = 0;
+      w.R = 0;
+      w.b = 0;
+      w.f0 = 0;
+      last = w.key0 + 127 < sh.P - 1 ? w.key0 + 127 - sh.P : -1;
+    } else {
+      const int x = j - n_p;
+      w.b = varlen_find(vl.kt0, vl.G, x);
+      w.key0 = 128 * (x - vl.kt0[w.b]);
+      w.base = vl.row0[w.b];
+      w.R = vl.row0[w.b + 1] - w.base;
+      w.f0 = vl.qt0[w.b] + w.key0 / sh.qt;
+      last = w.key0 + 127 < w.R - 1 ? w.key0 + 127 : w.R - 1;
+    }
+    // query t sees key k, counted from the prompt's end, while t - k < window; the first tokens always
+    const bool always = (w.prompt ? 0 : sh.P) + w.key0 < sh.sinks;
+    const int64_t end = last + sh.window;
+    w.t_end = always || end > INT_MAX ? INT_MAX : static_cast<int>(end);
+    w.n = 0;
+    if (w.prompt) {
+      for (int b = 0; b < vl.G; ++b) w.n += window_q_tiles(w, sh, vl, b);
+    } else {
+      w.n = window_q_tiles(w, sh, vl, w.b) - w.key0 / sh.qt;
+    }
+    return w;
+  }
   if constexpr (!kPacked) {
     // one response: base 0, length sh.R (kNoSuffix: prompt key tiles only)
     const int n_st = kNoSuffix ? 0 : static_cast<int>((sh.R + 127) / 128);
@@ -144,7 +212,7 @@ __device__ __forceinline__ KvUnit make_kv_unit(int u, const AttnShape& sh, const
   return w;
 }
 
-template <int D, bool kPacked, bool kNoSuffix>
+template <int D, bool kPacked, bool kNoSuffix, bool kWindow>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_kp,
                          const __grid_constant__ CUtensorMap tm_vp,
@@ -166,7 +234,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n_qt = kPacked ? vl.qt0[vl.G] : static_cast<int>((sh.R + sh.qt - 1) / sh.qt);
-  const int n_units = sh.Hkv * (static_cast<int>((sh.P + 127) / 128) +
+  const int n_units = kWindow ? sh.Hkv * window_kv_tiles(sh, vl)
+                              : sh.Hkv * (static_cast<int>((sh.P + 127) / 128) +
                                 (kPacked ? vl.kt0[vl.G]
                                          : (kNoSuffix ? 0 : static_cast<int>((sh.R + 127) / 128))));
   const int rows_used = sh.g * sh.qt;   // rows of a 128-row tile that TMA fills
@@ -233,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t qit = 0, uc = 0, q_sent = 0;
       bool ok = true, kv_pending = false;
       for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x, ++uc) {
-        const KvUnit w = make_kv_unit<kPacked, kNoSuffix>(u, sh, vl);
+        const KvUnit w = make_kv_unit<kPacked, kNoSuffix, kWindow>(u, sh, vl);
         kv_pending = false;
         if (uc > 0) ok = mbar_wait_hint<kHintDkdvProducer>(&bars[C::kBarKVEmpty], (uc - 1) & 1u, status, vabort);
         if (!ok) break;
@@ -246,10 +315,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         kv_pending = true;
         int rb = w.prompt ? 0 : w.b;   // response of the current Q tile
+        QWalk walk;
+        if constexpr (kWindow) walk.start(w, sh, vl);
         for (int li = 0; li < w.n && ok; ++li, ++qit) {
           const int f = w.f0 + li;
           int qrow = f * sh.qt;         // packed row of the tile
-          if constexpr (kPacked) {
+          if constexpr (kWindow) {
+            qrow = vl.row0[walk.b] + walk.i * sh.qt;
+            walk.next(w, sh, vl);
+          } else if constexpr (kPacked) {
             while (f >= vl.qt0[rb + 1]) ++rb;
             qrow = vl.row0[rb] + (f - vl.qt0[rb]) * sh.qt;
           }
@@ -345,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       };
       for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x, ++uc) {
-        const KvUnit w = make_kv_unit<kPacked, kNoSuffix>(u, sh, vl);
+        const KvUnit w = make_kv_unit<kPacked, kNoSuffix, kWindow>(u, sh, vl);
         ok = mbar_wait_hint<kHintDkdvMma>(&bars[C::kBarKVFull], uc & 1u, status, vabort);
         if (!ok) break;
         tc_fence_after();
@@ -391,11 +465,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t qit = 0u, uc = 0u, n_tiles = 0u;
     bool ok = true;
     for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x, ++uc) {
-      const KvUnit w = make_kv_unit<kPacked, kNoSuffix>(u, sh, vl);
+      const KvUnit w = make_kv_unit<kPacked, kNoSuffix, kWindow>(u, sh, vl);
       const int key = w.key0 + row;
+      QWalk walk;
+      int key_end = INT_MAX;       // of a window: queries from here on do not see the key
+      if constexpr (kWindow) {
+        walk.start(w, sh, vl);
+        const int64_t from_end = key - (w.prompt ? sh.P : 0);
+        if (sh.P + from_end >= sh.sinks && from_end + sh.window < INT_MAX)
+          key_end = static_cast<int>(from_end + sh.window);
+      }
       for (int li = 0; li < w.n; ++li, ++n_tiles) {
         // row statistics of this Q tile: every thread reads the same 1 KB (L1 broadcast)
-        const float* rs = rowstats + (static_cast<int64_t>(w.kv) * n_qt + w.f0 + li) * 256;
+        const float* rs = rowstats + (static_cast<int64_t>(w.kv) * n_qt +
+                                      (kWindow ? vl.qt0[walk.b] + walk.i : w.f0 + li)) * 256;
         const float4* lse4 = reinterpret_cast<const float4*>(rs) + wg * 16;   // rows 64 wg ..
         const float4* dlt4 = reinterpret_cast<const float4*>(rs + 128) + wg * 16;
         // the next Q tile's row statistics (8 lines of 128 B) into L1 a step ahead, so that
@@ -444,7 +527,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         // causal suffix: rows r < lo of the tile see only suffix keys < this key
-        if (!w.prompt) {
+        if constexpr (kWindow) {
+          // and behind the window: the rows of queries from key_end on
+          const int t0 = walk.i * sh.qt;
+          walk.next(w, sh, vl);
+          if (key_end < t0 + sh.qt) {
+            const int hi = key_end <= t0 ? 0 : sh.g * (key_end - t0);
+#pragma unroll
+            for (int i = 0; i < 64; ++i)
+              if (wg * 64 + i >= hi) p[i] = 0.0f;
+          }
+          const int d = key - t0;
+          const int lo = w.prompt || d <= 0 ? 0 : (d >= sh.qt ? 128 : sh.g * d);
+          if (lo > wg * 64) {
+#pragma unroll
+            for (int i = 0; i < 64; ++i)
+              if (wg * 64 + i < lo) p[i] = 0.0f;
+          }
+        } else if (!w.prompt) {
           const int v = sh.g * (key - (w.f0 + li - (kPacked ? vl.qt0[w.b] : 0)) * sh.qt);
           const int lo = v < 0 ? 0 : (v > 128 ? 128 : v);
           if (lo > wg * 64) {
@@ -588,7 +688,18 @@ struct QUnit {
   int t0;      // first query of the tile (response-local)
   int n_pt;    // prompt 128-key steps
   int n;       // total steps
+  // of a window: n_pt counts the prompt tiles in sight, the first `first` of which are the prompt's first
+  // and the others lie `leap` further; likewise the suffix tiles behind them
+  int first, leap, sfirst, sleap;
 };
+
+// Step j of a unit through a window: whether its tile is the prompt's, and which one.
+__device__ __forceinline__ int window_step(const QUnit& w, int j, bool* pre) {
+  *pre = j < w.n_pt;
+  if (*pre) return j < w.first ? j : j + w.leap;
+  j -= w.n_pt;
+  return j < w.sfirst ? j : j + w.sleap;
+}
 
 // One response (base 0, length sh.R): flat unit u -> (kv head, 128-row Q tile).
 __device__ __forceinline__ QUnit make_q_unit(int u, const AttnShape& sh, int n_qt) {
@@ -622,9 +733,28 @@ __device__ __forceinline__ QUnit make_q_unit_packed(int u, const AttnShape& sh, 
   return w;
 }
 
-template <bool kPacked, bool kNoSuffix>
+// The same through a window: the key tiles that the unit's queries see.
+__device__ __forceinline__ QUnit make_q_unit_window(int u, const AttnShape& sh, const Varlen& vl) {
+  QUnit w = make_q_unit_packed(u, sh, vl);
+  const int n_st = w.n - w.n_pt;
+  const PromptTiles pt = prompt_tiles(sh, w.t0);
+  w.first = pt.first;
+  w.leap = pt.second - pt.first;
+  w.n_pt = pt.n_pt - w.leap;
+  const int64_t lo = w.t0 - sh.window + 1;
+  const int s0 = lo <= 0 ? 0 : static_cast<int>(lo / 128);
+  const int64_t s = (sh.sinks - sh.P + 127) / 128;     // (first tokens past the prompt)
+  w.sfirst = s <= 0 ? 0 : (s < s0 ? static_cast<int>(s) : s0);
+  w.sleap = s0 - w.sfirst;
+  w.n = w.n_pt + n_st - w.sleap;
+  return w;
+}
+
+template <bool kPacked, bool kNoSuffix, bool kWindow>
 __device__ __forceinline__ QUnit pick_q_unit(int u, const AttnShape& sh, int n_qt, const Varlen& vl) {
-  if constexpr (kPacked) {
+  if constexpr (kWindow) {
+    return make_q_unit_window(u, sh, vl);
+  } else if constexpr (kPacked) {
     return make_q_unit_packed(u, sh, vl);
   } else {
     QUnit w = make_q_unit(u, sh, n_qt);
@@ -633,7 +763,7 @@ __device__ __forceinline__ QUnit pick_q_unit(int u, const AttnShape& sh, int n_q
   }
 }
 
-template <int D, bool kPacked, bool kNoSuffix>
+template <int D, bool kPacked, bool kNoSuffix, bool kWindow>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_kp,
                        const __grid_constant__ CUtensorMap tm_vp,
@@ -701,7 +831,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t kit = 0, uc = 0, k_sent = 0;
       bool ok = true, q_sent = false;
       for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x, ++uc) {
-        const QUnit w = pick_q_unit<kPacked, kNoSuffix>(u, sh, n_qt, vl);
+        const QUnit w = pick_q_unit<kPacked, kNoSuffix, kWindow>(u, sh, n_qt, vl);
         q_sent = false;
         if (uc > 0) ok = mbar_wait_hint<kHintDqProducer>(&bars[C::kBarQEmpty], (uc - 1) & 1u, status, vabort);
         if (!ok) break;
@@ -715,8 +845,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                       w.kv * sh.g, (kPacked ? w.base : 0) + w.t0);
         }
         for (int j = 0; j < w.n && ok; ++j, ++kit) {
-          const bool pre = j < w.n_pt;
-          const int key0 = pre ? 128 * j : (kPacked ? w.base : 0) + 128 * (j - w.n_pt);
+          bool pre = j < w.n_pt;
+          int key0 = pre ? 128 * j : (kPacked ? w.base : 0) + 128 * (j - w.n_pt);
+          if constexpr (kWindow) {
+            const int tile = window_step(w, j, &pre);
+            key0 = (pre ? 0 : w.base) + 128 * tile;
+          }
           const uint32_t sk = kit % C::kNK, sv = kit % C::kNV;
           if (kit >= static_cast<uint32_t>(C::kNK))
             ok = mbar_wait_hint<kHintDqProducer>(&bars[C::kBarKEmpty + sk], ((kit / C::kNK) - 1) & 1u, status, vabort);
@@ -804,7 +938,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (c == 1) mma_commit_w(&bars[C::kBarKEmpty + sk]);
       };
       for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x, ++uc) {
-        const QUnit w = pick_q_unit<kPacked, kNoSuffix>(u, sh, n_qt, vl);
+        const QUnit w = pick_q_unit<kPacked, kNoSuffix, kWindow>(u, sh, n_qt, vl);
         ok = mbar_wait_hint<kHintDqMma>(&bars[C::kBarQTmem], uc & 1u, status, vabort);
         if (!ok) break;
         tc_fence_after();
@@ -849,7 +983,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t uc = 0u, n_steps = 0u;
     bool ok = true;
     for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x, ++uc) {
-      const QUnit w = pick_q_unit<kPacked, kNoSuffix>(u, sh, n_qt, vl);
+      const QUnit w = pick_q_unit<kPacked, kNoSuffix, kWindow>(u, sh, n_qt, vl);
       const int t = w.t0 + row / sh.g;
       const int hg = row % sh.g;
       const bool valid = (row < sh.g * sh.qt) && (kPacked ? t < w.R : t < sh.R);
@@ -885,14 +1019,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&bars[C::kBarQTmem]);
         mbar_arrive(&bars[C::kBarQEmpty]);
       }
+      // of a window: keys from here on, counted from the prompt's end, are in sight of all the tile's queries
+      int whole = 0;
+      if constexpr (kWindow) {
+        const int t_end = w.t0 + sh.qt < w.R ? w.t0 + sh.qt : w.R;
+        whole = clip_int(t_end - sh.window);
+      }
       for (int j = 0; j < w.n; ++j, ++n_steps) {
         ok = mbar_wait_hint<kHintDqSoftmax>(&bars[C::kBarSFull], n_steps & 1u, status, vabort);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
         // valid key columns of this row in this step
-        int lim = 128;
-        if (j < w.n_pt) {
+        int lim = 128, low = 0, first = 0;
+        if constexpr (kWindow) {
+          bool pre;
+          const int tile = window_step(w, j, &pre);
+          // first key of the tile, counted from the prompt's end
+          const int64_t at = 128ll * tile - (pre ? sh.P : 0);
+          if (pre) {
+            if (at > -128) lim = static_cast<int>(-at);
+          } else {
+            const int v = t - 128 * tile + 1;
+            lim = v < 0 ? 0 : (v > 128 ? 128 : v);
+          }
+          if (at < whole) {     // keys before this row's window, but for the first tokens
+            low = clip_int(t - sh.window + 1 - at);
+            first = clip_int(sh.sinks - sh.P - at);
+          }
+        } else if (j < w.n_pt) {
           const int64_t rem = sh.P - 128ll * j;
           if (rem < 128) lim = static_cast<int>(rem);
         } else {
@@ -927,6 +1082,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 64; ++i)
             if (wg * 64 + i >= lim) p[i] = 0.0f;
+        }
+        if constexpr (kWindow) {
+          if (low > 0) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t seen = ~low_bits(low - wg * 64 - 32 * h) | low_bits(first - wg * 64 - 32 * h);
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (!(seen & (1u << i))) p[32 * h + i] = 0.0f;
+            }
+          }
         }
         // ---- dS from dP; packed dS replaces the fp32 dP chunk just read
         ok = mbar_wait_hint<kHintDqSoftmax>(&bars[C::kBarDPFull], n_steps & 1u, status, vabort);
@@ -1000,7 +1166,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D, bool kPacked, bool kNoSuffix = false>
+template <int D, bool kPacked, bool kNoSuffix = false, bool kWindow = false>
 cudaError_t launch_dkdv_d(const BwdArgs& a, cudaStream_t s) {
   using C = DkdvCfg<D>;
   // the shared-memory opt-in is per device: remember it per device index
@@ -1008,22 +1174,23 @@ cudaError_t launch_dkdv_d(const BwdArgs& a, cudaStream_t s) {
   const int dev = cached_device_index();
   if (dev < 0) return cudaErrorInvalidDevice;
   if (!attr_set[dev]) {
-    cudaError_t e = cudaFuncSetAttribute(attn_bwd_dkdv_kernel<D, kPacked, kNoSuffix>,
+    cudaError_t e = cudaFuncSetAttribute(attn_bwd_dkdv_kernel<D, kPacked, kNoSuffix, kWindow>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
   }
   const int64_t n_units =
-      static_cast<int64_t>(a.sh.Hkv) * ((a.sh.P + 127) / 128 + (kNoSuffix ? 0 : a.vl.kt0[a.vl.G]));
+      static_cast<int64_t>(a.sh.Hkv) * (kWindow ? window_kv_tiles(a.sh, a.vl)
+                                                : (a.sh.P + 127) / 128 + (kNoSuffix ? 0 : a.vl.kt0[a.vl.G]));
   int grid = num_sms();
   if (n_units < grid) grid = static_cast<int>(n_units);
-  attn_bwd_dkdv_kernel<D, kPacked, kNoSuffix><<<grid, kThreads, C::kSmem, s>>>(
+  attn_bwd_dkdv_kernel<D, kPacked, kNoSuffix, kWindow><<<grid, kThreads, C::kSmem, s>>>(
       *a.tm_kp, *a.tm_vp, a.tm_ks, a.tm_vs, a.tm_q, a.tm_do, a.sh, a.rowstats, a.dk_acc,
       a.dv_acc, a.dk_suf, a.dv_suf, a.suffix_to_acc, a.vl, a.status);
   return cudaGetLastError();
 }
 
-template <int D, bool kPacked, bool kNoSuffix = false>
+template <int D, bool kPacked, bool kNoSuffix = false, bool kWindow = false>
 cudaError_t launch_dq_d(const BwdArgs& a, cudaStream_t s) {
   using C = DqCfg<D>;
   // the shared-memory opt-in is per device: remember it per device index
@@ -1031,7 +1198,7 @@ cudaError_t launch_dq_d(const BwdArgs& a, cudaStream_t s) {
   const int dev = cached_device_index();
   if (dev < 0) return cudaErrorInvalidDevice;
   if (!attr_set[dev]) {
-    cudaError_t e = cudaFuncSetAttribute(attn_bwd_dq_kernel<D, kPacked, kNoSuffix>,
+    cudaError_t e = cudaFuncSetAttribute(attn_bwd_dq_kernel<D, kPacked, kNoSuffix, kWindow>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
@@ -1039,7 +1206,7 @@ cudaError_t launch_dq_d(const BwdArgs& a, cudaStream_t s) {
   const int64_t n_units = static_cast<int64_t>(a.sh.Hkv) * a.vl.qt0[a.vl.G];
   int grid = num_sms();
   if (n_units < grid) grid = static_cast<int>(n_units);
-  attn_bwd_dq_kernel<D, kPacked, kNoSuffix><<<grid, kThreads, C::kSmem, s>>>(*a.tm_kp, *a.tm_vp, a.tm_ks, a.tm_vs,
+  attn_bwd_dq_kernel<D, kPacked, kNoSuffix, kWindow><<<grid, kThreads, C::kSmem, s>>>(*a.tm_kp, *a.tm_vp, a.tm_ks, a.tm_vs,
                                                         a.tm_q, a.tm_do, a.sh, a.rowstats, a.dq,
                                                         a.vl, a.status);
   return cudaGetLastError();
@@ -1049,12 +1216,16 @@ cudaError_t launch_dq_d(const BwdArgs& a, cudaStream_t s) {
 
 cudaError_t launch_attn_bwd_dkdv(const BwdArgs& a, cudaStream_t s) {
   if (a.no_suffix) return a.sh.D == 128 ? launch_dkdv_d<128, false, true>(a, s) : launch_dkdv_d<64, false, true>(a, s);
+  if (a.sh.window > 0)
+    return a.sh.D == 128 ? launch_dkdv_d<128, true, false, true>(a, s) : launch_dkdv_d<64, true, false, true>(a, s);
   if (a.vl.G > 1) return a.sh.D == 128 ? launch_dkdv_d<128, true>(a, s) : launch_dkdv_d<64, true>(a, s);
   return a.sh.D == 128 ? launch_dkdv_d<128, false>(a, s) : launch_dkdv_d<64, false>(a, s);
 }
 
 cudaError_t launch_attn_bwd_dq(const BwdArgs& a, cudaStream_t s) {
   if (a.no_suffix) return a.sh.D == 128 ? launch_dq_d<128, false, true>(a, s) : launch_dq_d<64, false, true>(a, s);
+  if (a.sh.window > 0)
+    return a.sh.D == 128 ? launch_dq_d<128, true, false, true>(a, s) : launch_dq_d<64, true, false, true>(a, s);
   if (a.vl.G > 1) return a.sh.D == 128 ? launch_dq_d<128, true>(a, s) : launch_dq_d<64, true>(a, s);
   return a.sh.D == 128 ? launch_dq_d<128, false>(a, s) : launch_dq_d<64, false>(a, s);
 }

@@ -20,10 +20,12 @@
 // consecutive queries x the g query heads that share the kv head, so one K/V tile feeds
 // 2 x 128 rows of MMA.  Units are ordered kv-head-major so the CTAs running at the same
 // time stream the same prompt K/V through L2.
-// Instantiations: <D, kPacked, kNoSuffix>.  kPacked: several responses packed along the
+// Instantiations: <D, kPacked, kNoSuffix, kWindow>.  kPacked: several responses packed along the
 // token axis (units, Q rows and suffix keys offset by the response's packed row; each
 // response sees the prompt and only its own causal suffix).  kNoSuffix: prompt keys only
-// (one shard of a context-parallel prompt).  <D, false, false> is the one-response replay.
+// (one shard of a context-parallel prompt).  kWindow (with kPacked, any number of responses): a unit
+// visits only the key tiles that its queries see through a sliding window, the sequence's first
+// tokens' among them.  <D, false, false, false> is the one-response replay.
 // Every wait is bounded; on a timeout the CTA records it in the status word, drains its
 // in-flight copies and MMAs, frees TMEM and exits.
 #include "ls_internal.h"
@@ -79,7 +81,18 @@ struct Unit {
   bool has1;     // Q tile 1 exists
   int n_pt;      // prompt key tiles
   int n_kt;      // total key tiles
+  // of a window: n_pt counts the prompt tiles in sight, the first `first` of which are the prompt's first
+  // and the others lie `leap` further; likewise the suffix tiles behind them
+  int first, leap, sfirst, sleap;
 };
+
+// Step j of a unit through a window: whether its tile is the prompt's, and which one.
+__device__ __forceinline__ int window_step(const Unit& w, int j, bool* pre) {
+  *pre = j < w.n_pt;
+  if (*pre) return j < w.first ? j : j + w.leap;
+  j -= w.n_pt;
+  return j < w.sfirst ? j : j + w.sleap;
+}
 
 // Flat unit u -> (kv head, pair of Q tiles) of one response (base 0, length sh.R); kv-major
 // so concurrently running CTAs stream the same prompt K/V.
@@ -119,10 +132,29 @@ __device__ __forceinline__ Unit make_unit_packed(int u, const AttnShape& sh, con
   return w;
 }
 
+// The same through a window: the key tiles that the unit's queries see.
+__device__ __forceinline__ Unit make_unit_window(int u, const AttnShape& sh, const Varlen& vl) {
+  Unit w = make_unit_packed(u, sh, vl);
+  const int n_st = w.n_kt - w.n_pt;
+  const PromptTiles pt = prompt_tiles(sh, w.t0);
+  w.first = pt.first;
+  w.leap = pt.second - pt.first;
+  w.n_pt = pt.n_pt - w.leap;
+  const int64_t lo = w.t0 - sh.window + 1;
+  const int s0 = lo <= 0 ? 0 : static_cast<int>(lo / 128);
+  const int64_t s = (sh.sinks - sh.P + 127) / 128;     // (first tokens past the prompt)
+  w.sfirst = s <= 0 ? 0 : (s < s0 ? static_cast<int>(s) : s0);
+  w.sleap = s0 - w.sfirst;
+  w.n_kt = w.n_pt + n_st - w.sleap;
+  return w;
+}
+
 // kNoSuffix: the queries see the prompt keys only (one shard of a context-parallel prompt).
-template <bool kPacked, bool kNoSuffix>
+template <bool kPacked, bool kNoSuffix, bool kWindow>
 __device__ __forceinline__ Unit pick_unit(int u, const AttnShape& sh, int n_pairs, const Varlen& vl) {
-  if constexpr (kPacked) {
+  if constexpr (kWindow) {
+    return make_unit_window(u, sh, vl);
+  } else if constexpr (kPacked) {
     return make_unit_packed(u, sh, vl);
   } else {
     Unit w = make_unit(u, sh, n_pairs);
@@ -131,7 +163,7 @@ __device__ __forceinline__ Unit pick_unit(int u, const AttnShape& sh, int n_pair
   }
 }
 
-template <int D, bool kPacked, bool kNoSuffix>
+template <int D, bool kPacked, bool kNoSuffix, bool kWindow>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_kp,
                     const __grid_constant__ CUtensorMap tm_vp,
@@ -198,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t kit = 0, vit = 0, uc = 0;
       bool ok = true;
       for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x, ++uc) {
-        const Unit w = pick_unit<kPacked, kNoSuffix>(u, sh, n_pairs, vl);
+        const Unit w = pick_unit<kPacked, kNoSuffix, kWindow>(u, sh, n_pairs, vl);
         if (uc > 0) ok = mbar_wait_hint<kHintFwdProducer>(&bars[C::kBarQEmpty], (uc - 1) & 1u, status);
         if (!ok) break;
         const int nq = w.has1 ? 2 : 1;
@@ -209,8 +241,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_3d(smem + C::kOffQ + q * C::kTile + b * 16384, &tm_q, &bars[C::kBarQFull],
                         64 * b, w.kv * sh.g, (kPacked ? w.base : 0) + w.t0 + q * sh.qt);
         for (int j = 0; j < w.n_kt && ok; ++j) {
-          const bool pre = j < w.n_pt;
-          const int key0 = pre ? 128 * j : (kPacked ? w.base : 0) + 128 * (j - w.n_pt);
+          bool pre = j < w.n_pt;
+          int key0 = pre ? 128 * j : (kPacked ? w.base : 0) + 128 * (j - w.n_pt);
+          if constexpr (kWindow) {
+            const int tile = window_step(w, j, &pre);
+            key0 = (pre ? 0 : w.base) + 128 * tile;
+          }
           {
             const uint32_t s = kit % C::kNK;
             if (kit >= static_cast<uint32_t>(C::kNK))
@@ -286,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
 
       for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x, ++uc) {
-        const Unit w = pick_unit<kPacked, kNoSuffix>(u, sh, n_pairs, vl);
+        const Unit w = pick_unit<kPacked, kNoSuffix, kWindow>(u, sh, n_pairs, vl);
         const int nq = w.has1 ? 2 : 1;
         ok = mbar_wait_warp<kHintFwdMma>(&bars[C::kBarQFull], uc & 1u, status, vabort);
         if (!ok) break;
@@ -363,10 +399,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t sph = 0u, uq = 0u;
     bool ok = true;
     for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x) {
-      const Unit w = pick_unit<kPacked, kNoSuffix>(u, sh, n_pairs, vl);
+      const Unit w = pick_unit<kPacked, kNoSuffix, kWindow>(u, sh, n_pairs, vl);
       if (q == 1 && !w.has1) continue;
       const int t = w.t0 + q * sh.qt + row / sh.g;
       float m_run = -INFINITY, l = 0.0f;
+      // of a window: keys from here on, counted from the prompt's end, are in sight of all the tile's queries
+      int whole = 0;
+      if constexpr (kWindow) {
+        const int t_end = w.t0 + (q + 1) * sh.qt < w.R ? w.t0 + (q + 1) * sh.qt : w.R;
+        whole = clip_int(t_end - sh.window);
+      }
       for (int j = 0; j < w.n_kt; ++j) {
         ok = mbar_wait_hint<kHintFwdSoftmax>(&bars[C::kBarSFull + q], sph, status, vabort);
         ok = __all_sync(0xffffffffu, ok);
@@ -381,7 +423,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld_wait();
         // valid key columns of this row in this tile
         int lim = 128;
-        if (j < w.n_pt) {
+        if constexpr (kWindow) {
+          bool pre;
+          const int tile = window_step(w, j, &pre);
+          // first key of the tile, counted from the prompt's end
+          const int64_t at = 128ll * tile - (pre ? sh.P : 0);
+          if (pre) {
+            if (at > -128) lim = static_cast<int>(-at);
+          } else {
+            const int v = t - 128 * tile + 1;
+            lim = v < 0 ? 0 : (v > 128 ? 128 : v);
+          }
+          if (at < whole) {
+            // keys before this row's window, but for the first tokens
+            const int low = clip_int(t - sh.window + 1 - at), first = clip_int(sh.sinks - sh.P - at);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t seen = ~low_bits(low - 32 * i) | low_bits(first - 32 * i);
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if (!(seen & (1u << c))) sv[i][c] = __float_as_uint(-INFINITY);
+            }
+          }
+        } else if (j < w.n_pt) {
           const int64_t rem = sh.P - 128ll * j;
           if (rem < 128) lim = static_cast<int>(rem);
         } else {
@@ -513,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D, bool kPacked, bool kNoSuffix = false>
+template <int D, bool kPacked, bool kNoSuffix = false, bool kWindow = false>
 cudaError_t launch_fwd_d(const FwdArgs& a, cudaStream_t s) {
   using C = FwdCfg<D>;
   // the shared-memory opt-in is per device: remember it per device index
@@ -521,7 +585,7 @@ cudaError_t launch_fwd_d(const FwdArgs& a, cudaStream_t s) {
   const int dev = cached_device_index();
   if (dev < 0) return cudaErrorInvalidDevice;
   if (!attr_set[dev]) {
-    cudaError_t e = cudaFuncSetAttribute(attn_fwd_kernel<D, kPacked, kNoSuffix>,
+    cudaError_t e = cudaFuncSetAttribute(attn_fwd_kernel<D, kPacked, kNoSuffix, kWindow>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
@@ -529,7 +593,7 @@ cudaError_t launch_fwd_d(const FwdArgs& a, cudaStream_t s) {
   const int64_t n_units = static_cast<int64_t>(a.sh.Hkv) * a.vl.pair0[a.vl.G];
   int grid = num_sms();
   if (n_units < grid) grid = static_cast<int>(n_units);
-  attn_fwd_kernel<D, kPacked, kNoSuffix><<<grid, kThreads, C::kSmem, s>>>(
+  attn_fwd_kernel<D, kPacked, kNoSuffix, kWindow><<<grid, kThreads, C::kSmem, s>>>(
       *a.tm_kp, *a.tm_vp, a.tm_q, a.tm_ks, a.tm_vs, a.sh, a.vl, a.o, a.lse, a.status);
   return cudaGetLastError();
 }
@@ -538,6 +602,8 @@ cudaError_t launch_fwd_d(const FwdArgs& a, cudaStream_t s) {
 
 cudaError_t launch_attn_fwd(const FwdArgs& a, cudaStream_t s) {
   if (a.no_suffix) return a.sh.D == 128 ? launch_fwd_d<128, false, true>(a, s) : launch_fwd_d<64, false, true>(a, s);
+  if (a.sh.window > 0)
+    return a.sh.D == 128 ? launch_fwd_d<128, true, false, true>(a, s) : launch_fwd_d<64, true, false, true>(a, s);
   if (a.vl.G > 1) return a.sh.D == 128 ? launch_fwd_d<128, true>(a, s) : launch_fwd_d<64, true>(a, s);
   return a.sh.D == 128 ? launch_fwd_d<128, false>(a, s) : launch_fwd_d<64, false>(a, s);
 }

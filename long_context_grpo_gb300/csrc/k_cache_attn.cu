@@ -718,8 +718,6 @@ __device__ __forceinline__ Job load_stream(const AttnArgs& a, int item, int q, i
 struct Mask {
   int lim, low, first;
 };
-// The lowest n bits, n clipped to 0 .. 32.
-__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u); }
 template <bool kWide>
 __device__ __forceinline__ Mask load_mask(const AttnArgs& a, int item, int q, int j, int qt, int tok) {
   const Job* p = a.jobs + (kWide ? item : 2 * item + q);
@@ -1240,7 +1238,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const Mask m = load_mask<kWide>(a, it, q, j, qt, tok);
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                const uint32_t seen = below(m.lim - 32 * i) & (~below(m.low - 32 * i) | below(m.first - 32 * i));
+                const uint32_t seen = low_bits(m.lim - 32 * i) & (~low_bits(m.low - 32 * i) | low_bits(m.first - 32 * i));
 #pragma unroll
                 for (int c = 0; c < 32; ++c)
                   if (!(seen & (1u << c))) sv[i][c] = __float_as_uint(-INFINITY);

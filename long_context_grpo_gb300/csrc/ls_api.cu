@@ -507,6 +507,18 @@ ls_status ls_prefix_prepare(const ls_prefix_desc* d, ls_prefix_t* out, void* str
   return LS_OK;
 }
 
+ls_status ls_prefix_set_window(ls_prefix_t h, int64_t window, int64_t sinks) {
+  NvtxRange nvtx_range("ls_prefix_set_window");
+  ls_status st = check_handle(h);
+  if (st != LS_OK) return st;
+  if (window < 0 || sinks < 0 || (window == 0 && sinks != 0)) return LS_ERR_INVALID_ARGUMENT;
+  // (a prompt and a response together have fewer keys)
+  const int64_t all = int64_t(1) << 32;
+  h->shape.window = window < all ? window : all;
+  h->shape.sinks = sinks < all ? sinks : all;
+  return LS_OK;
+}
+
 ls_status ls_prefix_destroy(ls_prefix_t h) {
   if (h == nullptr) return LS_OK;
   if (h->magic != kMagic) return LS_ERR_NOT_PREPARED;
@@ -678,6 +690,7 @@ ls_status ls_replay_fwd_prompt_only(ls_prefix_t h, int64_t R, const void* q, voi
   NvtxRange nvtx_range("ls_replay_fwd_prompt_only");
   ls_status st = check_handle(h);
   if (st != LS_OK) return st;
+  if (h->shape.window > 0) return LS_ERR_UNSUPPORTED;   // a shard does not know where its keys are
   if (R < 1) return LS_ERR_INVALID_ARGUMENT;
   const int64_t cu[2] = {0, R};
   return replay_fwd_impl(h, h->shape.P, 1, cu, q, h->k_prefix, h->v_prefix, o, lse, stream, 1);
@@ -689,6 +702,7 @@ ls_status ls_replay_bwd_prompt_only(ls_prefix_t h, int64_t R, const void* q, con
   NvtxRange nvtx_range("ls_replay_bwd_prompt_only");
   ls_status st = check_handle(h);
   if (st != LS_OK) return st;
+  if (h->shape.window > 0) return LS_ERR_UNSUPPORTED;   // a shard does not know where its keys are
   if (R < 1) return LS_ERR_INVALID_ARGUMENT;
   const int64_t cu[2] = {0, R};
   return replay_bwd_impl(h, h->shape.P, 1, cu, q, h->k_prefix, h->v_prefix, o, lse, d_out, dq,

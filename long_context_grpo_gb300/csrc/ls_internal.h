@@ -84,7 +84,33 @@ struct AttnShape {
   int Hq, Hkv, D, g;
   float scale;
   int qt;        // queries per 128-row tile (= 128 / g)
+  // Sliding window: query t sees the last `window` keys up to its own (0: all of them) and the
+  // sequence's first `sinks`.  Both are at most 2^32.
+  int64_t window, sinks;
 };
+
+// The prompt's 128-key tiles that any query sees: [0, first) and [second, n_pt).
+struct PromptTiles {
+  int first, second, n_pt;
+};
+// Those that queries t0 and later see; below: keys, counted from the prompt's end, that query t0 has no more
+// in sight.
+__host__ __device__ inline PromptTiles prompt_tiles(const AttnShape& sh, int64_t t0) {
+  PromptTiles w;
+  w.n_pt = static_cast<int>((sh.P + 127) / 128);
+  const int64_t lo = sh.P + t0 - sh.window + 1;
+  w.second = lo >= sh.P ? w.n_pt : (lo <= 0 ? 0 : static_cast<int>(lo / 128));
+  const int64_t s = sh.sinks < sh.P ? sh.sinks : sh.P;
+  w.first = static_cast<int>((s + 127) / 128);
+  if (w.first > w.second) w.first = w.second;
+  return w;
+}
+// x clipped to the range of int with room for sums with tile sizes.
+__host__ __device__ inline int clip_int(int64_t x) {
+  return static_cast<int>(x < -(int64_t(1) << 30) ? -(int64_t(1) << 30) : (x > (int64_t(1) << 30) ? int64_t(1) << 30 : x));
+}
+// The lowest n bits, n clipped to 0 .. 32.
+__host__ __device__ inline uint32_t low_bits(int n) { return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u); }
 
 // Responses packed along the token axis: response b owns packed rows row0[b] .. row0[b+1]-1
 // of Q/dO/O/dQ/LSE and of the suffix K/V, and sees the prompt and, causally, its own rows
