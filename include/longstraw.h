@@ -352,6 +352,61 @@ ls_status ls_policy_loss(const ls_policy_loss_desc* d, void* workspace, size_t w
                          void* stream);
 
 /*
+ * ls_token_scores -- what a rollout and its scoring answer for every token row t of logits x [T, V]
+ * with given id y_t, at a temperature (review section 2-1 step 2): with z_v = x_v / temperature
+ *     lse[t] = log sum_v exp(z_v);  logp[t] = z_y - lse;  entropy[t] = - sum_v p_v log p_v, p_v = exp(z_v - lse)
+ *     top_ids[t, i], top_logp[t, i]: the `top` largest logits' ids, largest first, equal ones the lowest
+ *     id first, and their log-probabilities
+ *   logits   device bf16, row t at logits + t logits_stride (elements, >= V)
+ *   ids      device int32 [T] (an id outside [0, V) sets the device status; its logp is 0)
+ *   logp     device fp32 [T]; lse, entropy device fp32 [T], may be NULL
+ *   top      0 .. min(V, 64); with top > 0 top_ids device int32, top_logp device fp32 [T, top] and
+ *            V <= 2^23 (else LS_ERR_UNSUPPORTED)
+ * Logits of -inf (masked) have p = 0 and add nothing to the entropy; they are alternatives only where fewer
+ * than `top` others are left, with log-probability -inf.  A row that holds a NaN or +inf, or nothing
+ * but -inf, has NaN for all its values and -1 for its top_ids.  One read of the logits; sums in
+ * compensated fp32, the logarithm in fp64.  Any V, stride and 2-byte alignment of the rows are right;
+ * 16-byte aligned rows (a stride that is a multiple of 8) are fast.
+ *
+ * ls_token_scores_bwd -- the gradient: d loss / d logits from d loss / d logp (d_logp) and d loss / d entropy
+ * (d_entropy), device fp32 [T], either may be NULL; logp, lse and entropy (may be NULL without d_entropy) as
+ * ls_token_scores gave them for these logits, ids and temperature:
+ *     dlogits[t,v] = (d_logp (1[v = y] - p_v) - d_entropy p_v (log p_v + entropy)) / temperature
+ *   dlogits  device bf16, row t at dlogits + t dlogits_stride; columns past V are left as they were.  May
+ *            be the logits themselves (same pointer and stride).
+ * A row whose two gradients are 0 is left out: its inputs are not looked at, its gradient is 0.  So is the
+ * gradient of a row whose id is outside [0, V), with the device status set.
+ */
+typedef struct {
+  int64_t T, V;
+  int64_t logits_stride;
+  const void* logits;
+  const int32_t* ids;
+  double temperature;
+  int32_t top;
+  float* logp;
+  float* lse;
+  float* entropy;
+  int32_t* top_ids;
+  float* top_logp;
+} ls_token_scores_desc;
+ls_status ls_token_scores(const ls_token_scores_desc* d, void* stream);
+typedef struct {
+  int64_t T, V;
+  int64_t logits_stride, dlogits_stride;
+  const void* logits;
+  const int32_t* ids;
+  double temperature;
+  const float* logp;
+  const float* lse;
+  const float* entropy;
+  const float* d_logp;
+  const float* d_entropy;
+  void* dlogits;
+} ls_token_scores_bwd_desc;
+ls_status ls_token_scores_bwd(const ls_token_scores_bwd_desc* d, void* stream);
+
+/*
  * ls_rope -- rotary positions of queries and keys, and the gradient through them.  With
  * angle a_i = position_t * inv_freq[i] and factor f = attn_factor, every pair (x, y) of the
  * first rot_dim values of a head becomes

@@ -52,6 +52,23 @@ class PolicyLossDesc(ctypes.Structure):
                 ("kl_out", ctypes.c_void_p)]
 
 
+class TokenScoresDesc(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("V", ctypes.c_int64), ("logits_stride", ctypes.c_int64),
+                ("logits", ctypes.c_void_p), ("ids", ctypes.c_void_p), ("temperature", ctypes.c_double),
+                ("top", ctypes.c_int32), ("logp", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+                ("entropy", ctypes.c_void_p), ("top_ids", ctypes.c_void_p),
+                ("top_logp", ctypes.c_void_p)]
+
+
+class TokenScoresBwdDesc(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("V", ctypes.c_int64), ("logits_stride", ctypes.c_int64),
+                ("dlogits_stride", ctypes.c_int64), ("logits", ctypes.c_void_p),
+                ("ids", ctypes.c_void_p), ("temperature", ctypes.c_double),
+                ("logp", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("entropy", ctypes.c_void_p),
+                ("d_logp", ctypes.c_void_p), ("d_entropy", ctypes.c_void_p),
+                ("dlogits", ctypes.c_void_p)]
+
+
 class RopeDesc(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int64), ("Hq", ctypes.c_int32), ("Hk", ctypes.c_int32),
                 ("D", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
@@ -130,6 +147,8 @@ def _load():
         "ls_block_replay_bwd": (ctypes.c_int, [vp, i64, i64, vp, vp, vp, vp, vp, vp, sz, vp]),
         "ls_policy_loss_workspace_bytes": (sz, [i64]),
         "ls_policy_loss": (ctypes.c_int, [vp, vp, sz, vp]),
+        "ls_token_scores": (ctypes.c_int, [vp, vp]),
+        "ls_token_scores_bwd": (ctypes.c_int, [vp, vp]),
         "ls_rope": (ctypes.c_int, [vp, vp]),
         "ls_rope_freqs": (ctypes.c_int, [i32, ctypes.c_double, i32, ctypes.c_double, i64,
                                          ctypes.c_double, ctypes.c_double, vp, vp]),

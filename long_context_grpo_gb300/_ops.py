@@ -21,6 +21,8 @@ _LAYOUT = {"NHD": 0, "HND": 1}
 # The descriptors of include/longstraw.h as native struct layouts: packing one is several times
 # cheaper than filling a ctypes.Structure, and small calls are bound by the host.
 _POLICY = struct.Struct("@qqqqPPPPPPdddiPPPPP")
+_SCORES = struct.Struct("@qqqPPdiPPPPP")
+_SCORES_BWD = struct.Struct("@qqqqPPdPPPPPP")
 _ROPE = struct.Struct("@qiiiiiiPdPqPqPqPqPq")
 _APPEND = struct.Struct("@iqPPPqPqPqPqPiid")
 _ATTN = struct.Struct("@iqPPiqPqPPiP")
@@ -151,6 +153,67 @@ def policy_loss(logits, ids, logp_old, advantages, weights, eps_low=0.2, eps_hig
         _ptr(weights, "weights", _f32, n, dev), eps_low, eps_high, beta, _KL[kl], sp, dx, cm, lp, kp)
     b._check(b._lib().ls_policy_loss(d, wp, nbytes, _raw_stream(dev)), "ls_policy_loss")
     return PolicyLoss(loss, dlogits, logp_out, kl_out, clip_mask)
+
+
+class TokenScores(NamedTuple):
+    logp: torch.Tensor        # fp32 [T]
+    lse: torch.Tensor         # fp32 [T]
+    entropy: torch.Tensor     # fp32 [T]
+    top_ids: torch.Tensor     # int32 [T, top]
+    top_logp: torch.Tensor    # fp32 [T, top]
+
+
+def token_scores(logits, ids, top: int = 0, temperature: float = 1.0, logp=None, lse=None, entropy=None,
+                 top_ids=None, top_logp=None) -> TokenScores:
+    """Log-probabilities of the given ids, log-sum-exp and entropy of every row of logits / temperature,
+    and the `top` most likely ids with their log-probabilities (largest first, equal ones the lowest
+    id first).  logits: bf16 [T, V], rows may be strided."""
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
+        raise TypeError("logits must be a 2-D CUDA tensor")
+    T, V = logits.shape
+    dev = torch.cuda.current_device()
+    at = logits.device
+    x, ldx = _strided(logits, "logits", (T, V), (1,), V, dev)
+    n, nt = (T,), (T, max(top, 0))
+    if logp is None:
+        logp = torch.empty(n, dtype=_f32, device=at)
+    if lse is None:
+        lse = torch.empty(n, dtype=_f32, device=at)
+    if entropy is None:
+        entropy = torch.empty(n, dtype=_f32, device=at)
+    if top_ids is None:
+        top_ids = torch.empty(nt, dtype=_i32, device=at)
+    if top_logp is None:
+        top_logp = torch.empty(nt, dtype=_f32, device=at)
+    d = _SCORES.pack(T, V, ldx, x, _ptr(ids, "ids", _i32, n, dev), temperature, top, _ptr(logp, "logp", _f32, n, dev),
+                     _ptr(lse, "lse", _f32, n, dev), _ptr(entropy, "entropy", _f32, n, dev),
+                     _ptr(top_ids, "top_ids", _i32, nt, dev), _ptr(top_logp, "top_logp", _f32, nt, dev))
+    b._check(b._lib().ls_token_scores(d, _raw_stream(dev)), "ls_token_scores")
+    return TokenScores(logp, lse, entropy, top_ids, top_logp)
+
+
+def token_scores_bwd(logits, ids, logp, lse, entropy=None, d_logp=None, d_entropy=None, temperature: float = 1.0,
+                     dlogits=None):
+    """d loss / d logits from d loss / d logp and d loss / d entropy (fp32 [T], either may be None) with what
+    token_scores gave for the same logits, ids and temperature.  dlogits may be the logits themselves; a
+    row whose two gradients are 0 is left out (its inputs are not looked at)."""
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
+        raise TypeError("logits must be a 2-D CUDA tensor")
+    T, V = logits.shape
+    dev = torch.cuda.current_device()
+    x, ldx = _strided(logits, "logits", (T, V), (1,), V, dev)
+    if dlogits is None:
+        dlogits = torch.empty((T, V), dtype=_bf16, device=logits.device)
+        dx, ldd = dlogits.data_ptr(), V
+    else:
+        dx, ldd = _strided(dlogits, "dlogits", (T, V), (1,), V, dev)
+    n = (T,)
+    d = _SCORES_BWD.pack(T, V, ldx, ldd, x, _ptr(ids, "ids", _i32, n, dev), temperature,
+                         _ptr(logp, "logp", _f32, n, dev), _ptr(lse, "lse", _f32, n, dev),
+                         _opt(entropy, "entropy", _f32, n, dev), _opt(d_logp, "d_logp", _f32, n, dev),
+                         _opt(d_entropy, "d_entropy", _f32, n, dev), dx)
+    b._check(b._lib().ls_token_scores_bwd(d, _raw_stream(dev)), "ls_token_scores_bwd")
+    return dlogits
 
 
 def rope_freqs(rot_dim: int, theta: float = 10000.0, scaling: str = "none", factor: float = 1.0,

@@ -1,0 +1,511 @@
+// Scores of given tokens (review section 2-1 step 2, old- and reference-policy scoring, with what a
+// rollout answers beside it): log-probability, log-sum-exp, entropy and the most likely alternatives of
+// every row at a temperature t, and the gradient through the first and the third.
+//
+//   lse = log sum_v exp(x_v / t),  logp = x_y / t - lse,  p_v = exp(x_v / t - lse)
+//   entropy = - sum_v p_v log p_v = log S - (sum_v e_v z_v) / S,  z_v = (x_v - max) / t, e_v = exp(z_v), S = sum e_v
+//   d x_v = (d_logp (1[v = y] - p_v) - d_entropy p_v (log p_v + entropy)) / t
+//
+// scores_kernel: a CTA a row, or a cluster of them where there are few rows, each with a slice; one read
+//   of the row.  A thread keeps a running maximum, how many logits equal it, the compensated sum of
+//   the others' exponentials and sum e z (fp32, joined across the CTA; the last logarithm in fp64): a
+//   token with nearly all of the probability keeps the digits of what is left.  For the alternatives the largest logit of every 32
+//   neighbours stays in shared memory: the k best logits of a row (ties to the lowest index) lie in the k
+//   groups with the largest maxima (ties to the lowest group), so that only these are looked at again.
+//   Proof: were one of them in another group, each of the k groups before that one would hold a
+//   logit before it.
+// scores_bwd_kernel: one pass, a block 8,192 logits of a row.
+#include <type_traits>
+
+#include "ls_internal.h"
+#include "ls_ops.h"
+#include "ptx.cuh"
+
+namespace ls {
+namespace {
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kUnroll = 4;                        // 4 x 8 logits a thread and step
+constexpr int kStep = kThreads * 8 * kUnroll;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr double kLn2 = 0.69314718055994530942;
+constexpr uint32_t kNegInf2 = 0xFF80FF80u;
+
+__device__ __forceinline__ float lo_bf16(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_bf16(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// Largest of two pairs; a NaN stays.
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Whole numbers in the order of bf16 values, -0 as 0; +inf is 0xFF80, and NaN (as max2 leaves it) above.
+__device__ __forceinline__ uint32_t order(uint32_t bits) {
+  bits = bits == 0x8000u ? 0u : bits;
+  return bits & 0x8000u ? 0xFFFFu - bits : bits | 0x8000u;
+}
+__device__ __forceinline__ float value_of(uint32_t ord) {
+  return __uint_as_float((ord & 0x8000u ? ord & 0x7FFFu : 0xFFFFu - ord) << 16);
+}
+
+// hi + lo += t, with the exact error of the fp32 addition kept in lo.
+__device__ __forceinline__ void two_sum_acc(float& hi, float& lo, float t) {
+  const float s = hi + t;
+  const float b = s - hi;
+  lo += (hi - (s - b)) + (t - b);
+  hi = s;
+}
+
+// Eight logits of a row from index i on (a multiple of 8); -inf past the end.
+template <bool kVec>
+__device__ __forceinline__ uint4 load8(const uint16_t* x, int64_t i, int64_t end) {
+  if (kVec && i + 8 <= end) return __ldg(reinterpret_cast<const uint4*>(x + i));
+  uint32_t w[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t a = i + 2 * k < end ? x[i + 2 * k] : 0xFF80u, b = i + 2 * k + 1 < end ? x[i + 2 * k + 1] : 0xFF80u;
+    w[k] = a | (b << 16);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// What a CTA knows of its slice: largest logit (as a whole number), sum, sum e z, its best logits.
+struct Slice {
+  uint32_t top;
+  float ones, hi, lo, e;
+};
+constexpr int kMaxCluster = 8;
+
+template <bool kVec, bool kTop>
+__global__ void __launch_bounds__(kThreads) scores_kernel(const __grid_constant__ ScoresArgs a) {
+  extern __shared__ __align__(16) uint8_t dyn[];
+  __shared__ uint32_t sh_max[kWarps];
+  __shared__ float sh_sum[kWarps][4];
+  __shared__ Slice sh_slice[kMaxCluster];
+  __shared__ uint32_t sh_key[kThreads];
+  __shared__ uint32_t sh_low, sh_cut, sh_n[2];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int parts = a.parts;
+  const int64_t row = blockIdx.x / parts;
+  const int part = parts > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const uint16_t* x = a.logits + row * a.ldx;
+  const int64_t begin = part * a.slice;
+  const int64_t end = begin + a.slice < a.V ? begin + a.slice : a.V;
+  const int len = end > begin ? static_cast<int>(end - begin) : 0;
+
+  if (parts > 1) cluster_arrive();       // (the first CTA has started before the others write to it)
+
+  // the given token's logit is on its way while the row is read
+  int y = -1;
+  float xy = 0.0f;
+  if (tid == 0 && part == 0) {
+    y = a.ids[row];
+    if (y < 0 || y >= a.V) {
+      set_device_status(a.status, DEV_BAD_INDEX);
+      y = -1;
+    } else {
+      xy = lo_bf16(x[y]);
+    }
+  }
+
+  uint16_t* groups = reinterpret_cast<uint16_t*>(dyn);
+  float m = -INFINITY, ones = 0.0f, hi = 0.0f, lo = 0.0f, e = 0.0f;
+  uint32_t top2 = kNegInf2;
+  const uint64_t c2 = f2_pack(a.scale2, a.scale2);
+  for (int base = 0; base < len; base += kStep) {
+    uint4 v[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) v[u] = load8<kVec>(x, begin + base + u * kThreads * 8 + tid * 8, end);
+    uint32_t g[kUnroll / 2];      // the largest of each eight, two a register
+#pragma unroll
+    for (int u = 0; u < kUnroll; u += 2) {
+      const uint32_t p = max2(max2(v[u].x, v[u].y), max2(v[u].z, v[u].w));
+      const uint32_t q = max2(max2(v[u + 1].x, v[u + 1].y), max2(v[u + 1].z, v[u + 1].w));
+      g[u / 2] = max2(__byte_perm(p, q, 0x5410), __byte_perm(p, q, 0x7632));
+    }
+    if constexpr (kTop) {
+      // of 32 neighbours: four lanes together
+#pragma unroll
+      for (int i = 0; i < kUnroll / 2; ++i) {
+        g[i] = max2(g[i], __shfl_xor_sync(0xffffffffu, g[i], 1));
+        g[i] = max2(g[i], __shfl_xor_sync(0xffffffffu, g[i], 2));
+      }
+      const int u = tid & 3;
+      const uint32_t w = u & 2 ? g[1] : g[0];
+      const int at = (base + u * kThreads * 8 + tid * 8) >> 5;
+      if (at * 32 < len) groups[at] = static_cast<uint16_t>(u & 1 ? w >> 16 : w & 0xFFFFu);
+    }
+    const uint32_t t2 = max2(g[0], g[1]);
+    top2 = max2(top2, t2);
+    const float cm = fmaxf(lo_bf16(t2), hi_bf16(t2));
+    if (cm > m) {
+      // z falls by d for all before: e^z by f, sum e z to f (sum e z + d sum e)
+      const float d = fmaxf((m - cm) * a.scale2, -1000.0f), f = ex2_approx(d);
+      two_sum_acc(hi, lo, ones);
+      e = f * fmaf(d, hi, e);
+      hi *= f;
+      lo *= f;
+      ones = 0.0f;
+      m = cm;
+    }
+    const uint64_t m2 = f2_pack(m, m);
+    uint64_t s2[2] = {f2_pack(0.0f, 0.0f), f2_pack(0.0f, 0.0f)}, e2[2] = {s2[0], s2[0]};
+    // peak: the maximum is among these; its exponentials, 1 each, are counted and not added
+    auto add = [&](auto peak) {
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float z0, z1;
+          f2_unpack(f2_mul(f2_sub(f2_pack(lo_bf16(w[k]), hi_bf16(w[k])), m2), c2), z0, z1);
+          // (below: exponents of nothing, and -inf - -inf; 0 x -1000 is 0 where 0 x -inf is not)
+          z0 = fmaxf(z0, -1000.0f);
+          z1 = fmaxf(z1, -1000.0f);
+          float p0 = ex2_approx(z0), p1 = ex2_approx(z1);
+          if constexpr (decltype(peak)::value) {
+            if (lo_bf16(w[k]) == m) {
+              ones += 1.0f;
+              p0 = 0.0f;
+            }
+            if (hi_bf16(w[k]) == m) {
+              ones += 1.0f;
+              p1 = 0.0f;
+            }
+          }
+          const uint64_t p = f2_pack(p0, p1);
+          s2[k & 1] = f2_add(s2[k & 1], p);
+          e2[k & 1] = f2_fma(p, f2_pack(z0, z1), e2[k & 1]);
+        }
+      }
+    };
+    if (__any_sync(0xffffffffu, cm == m)) add(std::true_type{}); else add(std::false_type{});
+    float s0, s1, e0, e1;
+    f2_unpack(f2_add(s2[0], s2[1]), s0, s1);
+    f2_unpack(f2_add(e2[0], e2[1]), e0, e1);
+    two_sum_acc(hi, lo, s0 + s1);
+    e += e0 + e1;
+  }
+
+  // the slice's maximum, and the sums relative to it
+  uint32_t top = max(order(top2 & 0xFFFFu), order(top2 >> 16));
+  top = __reduce_max_sync(0xffffffffu, top);
+  if (lane == 0) sh_max[warp] = top;
+  if (tid == 0) {
+    sh_low = 0u;
+    sh_cut = 0u;
+    sh_n[0] = sh_n[1] = 0u;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) top = max(top, sh_max[w]);
+  {
+    const float peak = value_of(top);
+    if (m != peak) {
+      const float d = fmaxf((m - peak) * a.scale2, -1000.0f), f = ex2_approx(d);
+      two_sum_acc(hi, lo, ones);
+      e = f * fmaf(d, hi, e);
+      hi *= f;
+      lo *= f;
+      ones = 0.0f;
+    }
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    const float h = __shfl_xor_sync(0xffffffffu, hi, off);
+    lo += __shfl_xor_sync(0xffffffffu, lo, off);
+    two_sum_acc(hi, lo, h);
+    e += __shfl_xor_sync(0xffffffffu, e, off);
+    ones += __shfl_xor_sync(0xffffffffu, ones, off);
+  }
+  if (lane == 0) {
+    sh_sum[warp][0] = hi;
+    sh_sum[warp][1] = lo;
+    sh_sum[warp][2] = e;
+    sh_sum[warp][3] = ones;
+  }
+
+  unsigned long long* best = nullptr;        // [parts][top]: the slices' best logits, in order
+  if constexpr (kTop) {
+    const int k = a.top;
+    const int n = (len + 31) >> 5;
+    uint8_t* at = dyn + ((static_cast<size_t>(a.slice) + 31) / 32 * 2 + 15) / 16 * 16;
+    best = reinterpret_cast<unsigned long long*>(at);
+    at += static_cast<size_t>(parts) * k * 8;
+    unsigned long long* found = reinterpret_cast<unsigned long long*>(at);       // [32 k]
+    uint32_t* list = reinterpret_cast<uint32_t*>(found + 32 * k);                // [k groups of a thread]
+    uint32_t* chosen = list + static_cast<size_t>(k) * ((a.slice / 32 + kThreads) / kThreads);
+    // groups as whole numbers: maximum, then the lowest index; 0: none
+    auto key = [&](int g) { return (order(groups[g]) << 16) | (0xFFFFu - static_cast<uint32_t>(g)); };
+    uint32_t mine = 0u;
+    for (int g = tid; g < n; g += kThreads) mine = max(mine, key(g));
+    sh_key[tid] = mine;
+    if (tid < k) best[part * k + tid] = 0ull;
+    __syncthreads();
+    // the k threads with the largest groups hold the k largest groups
+    int rank = 0;
+    for (int i = 0; i < kThreads; i += 4) {
+      const uint4 o = *reinterpret_cast<const uint4*>(sh_key + i);
+      rank += (o.x > mine) + (o.y > mine) + (o.z > mine) + (o.w > mine);
+    }
+    if (rank == k - 1) sh_low = mine;
+    __syncthreads();
+    if (rank < k && mine > 0u) {
+      const uint32_t low = sh_low;
+      for (int g = tid; g < n; g += kThreads) {
+        const uint32_t o = key(g);
+        if (o >= low) list[atomicAdd(&sh_n[0], 1u)] = o;
+      }
+    }
+    __syncthreads();
+    const int listed = static_cast<int>(sh_n[0]);
+    for (int i = tid; i < listed; i += kThreads) {
+      const uint32_t o = list[i];
+      int r = 0;
+      for (int j = 0; j < listed; ++j) r += list[j] > o;
+      if (r < k) chosen[r] = 0xFFFFu - (o & 0xFFFFu);
+      if (r == k - 1) sh_cut = o >> 16;       // nothing below the last group's maximum is among the best
+    }
+    __syncthreads();
+    const int groups_chosen = listed < k ? listed : k;
+    const uint32_t cut = sh_cut;
+    for (int r = warp; r < groups_chosen; r += kWarps) {
+      const int i = static_cast<int>(chosen[r]) * 32 + lane;
+      if (i >= len) continue;
+      const uint32_t o = order(x[begin + i]);
+      if (o >= cut)
+        found[atomicAdd(&sh_n[1], 1u)] =
+            (static_cast<unsigned long long>(o) << 32) | (0xFFFFFFFFull - static_cast<unsigned long long>(begin + i));
+    }
+    __syncthreads();
+    const int count = static_cast<int>(sh_n[1]);
+    for (int i = tid; i < count; i += kThreads) {
+      const unsigned long long o = found[i];
+      int r = 0;
+      for (int j = 0; j < count; ++j) r += found[j] > o;
+      if (r < k) best[part * k + r] = o;
+    }
+  }
+  if (parts > 1) cluster_wait();
+  __syncthreads();
+  if (tid == 0) {
+    Slice s;
+    s.top = top;
+    s.ones = s.hi = s.lo = s.e = 0.0f;
+    for (int w = 0; w < kWarps; ++w) {
+      two_sum_acc(s.hi, s.lo, sh_sum[w][0]);
+      s.lo += sh_sum[w][1];
+      s.e += sh_sum[w][2];
+      s.ones += sh_sum[w][3];
+    }
+    if (part == 0) {
+      sh_slice[0] = s;
+    } else {
+      const uint32_t to = cluster_map(&sh_slice[part], 0);
+      st_cluster_u32(to, s.top);
+      st_cluster_f32(to + 4, s.ones);
+      st_cluster_f32(to + 8, s.hi);
+      st_cluster_f32(to + 12, s.lo);
+      st_cluster_f32(to + 16, s.e);
+    }
+  }
+  if (parts > 1) {
+    if (kTop && part > 0 && tid < a.top) {
+      const unsigned long long o = best[part * a.top + tid];
+      const uint32_t to = cluster_map(&best[part * a.top + tid], 0);
+      st_cluster_u32(to, static_cast<uint32_t>(o));
+      st_cluster_u32(to + 4, static_cast<uint32_t>(o >> 32));
+    }
+    cluster_sync_all();
+    if (part > 0) return;
+  } else {
+    __syncthreads();
+  }
+
+  // the row: the slices joined in order
+  __shared__ double sh_lns;
+  __shared__ uint32_t sh_top;
+  if (tid == 0) {
+    uint32_t all = 0u;
+    for (int i = 0; i < parts; ++i) all = max(all, sh_slice[i].top);
+    const float peak = value_of(all);
+    float n = 0.0f, h = 0.0f, l = 0.0f, w = 0.0f;
+    for (int i = 0; i < parts; ++i) {
+      Slice s = sh_slice[i];
+      if (s.top == all) {
+        n += s.ones;
+        two_sum_acc(h, l, s.hi);
+        l += s.lo;
+        w += s.e;
+      } else {
+        const float d = fmaxf((value_of(s.top) - peak) * a.scale2, -1000.0f), f = ex2_approx(d);
+        two_sum_acc(s.hi, s.lo, s.ones);
+        two_sum_acc(h, l, s.hi * f);
+        l += s.lo * f;
+        w += f * fmaf(d, s.hi, s.e);
+      }
+    }
+    // a NaN or an infinite logit, or none that is larger than -inf: no distribution
+    const bool none = all >= 0xFF80u || all <= 0x007Fu;
+    const double rest = static_cast<double>(h) + static_cast<double>(l), S = n + rest;
+    const double lns = none ? static_cast<double>(NAN) : log1p(n - 1.0 + rest);
+    sh_lns = lns;
+    sh_top = all;
+    a.logp[row] = y < 0 ? 0.0f : static_cast<float>((static_cast<double>(xy) - peak) * a.scale - lns);
+    if (a.lse != nullptr) a.lse[row] = static_cast<float>(peak * a.scale + lns);
+    if (a.entropy != nullptr) {
+      const double ent = lns - kLn2 * w / S;
+      a.entropy[row] = ent < 0.0 ? 0.0f : static_cast<float>(ent);
+    }
+  }
+  if constexpr (kTop) {
+    __syncthreads();
+    const int k = a.top, all = parts * k;
+    const bool none = sh_top >= 0xFF80u || sh_top <= 0x007Fu;
+    if (none) {
+      if (tid < k) {
+        a.top_ids[row * k + tid] = -1;
+        a.top_logp[row * k + tid] = NAN;
+      }
+      return;
+    }
+    for (int i = tid; i < all; i += kThreads) {
+      const unsigned long long o = best[i];
+      int r = i;
+      if (parts > 1) {
+        r = 0;
+        for (int j = 0; j < all; ++j) r += best[j] > o;
+      }
+      if (r >= k || o == 0ull) continue;
+      a.top_ids[row * k + r] = static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(o));
+      a.top_logp[row * k + r] =
+          static_cast<float>((static_cast<double>(value_of(static_cast<uint32_t>(o >> 32))) - value_of(sh_top)) * a.scale - sh_lns);
+    }
+  }
+}
+
+// --------------------------------------------------------------------------------------
+template <bool kVec>
+__global__ void __launch_bounds__(kThreads) scores_bwd_kernel(const __grid_constant__ ScoresBwdArgs a) {
+  const int tid = threadIdx.x;
+  const int64_t row = blockIdx.y + static_cast<int64_t>(blockIdx.z) * a.rows_y;
+  if (row >= a.T) return;
+  const int64_t begin = static_cast<int64_t>(blockIdx.x) * kStep;
+  const uint16_t* x = a.logits + row * a.ldx;
+  uint16_t* out = a.dlogits + row * a.ldd;
+  float dl = a.d_logp != nullptr ? a.d_logp[row] : 0.0f, de = a.d_entropy != nullptr ? a.d_entropy[row] : 0.0f;
+  const int y = a.ids[row];
+  const bool wild = y < 0 || y >= a.V;
+  if (wild && begin == 0 && tid == 0) set_device_status(a.status, DEV_BAD_INDEX);
+  // a row that nothing is asked of is not looked at
+  const bool zero = wild || (dl == 0.0f && de == 0.0f);
+  const float lse2 = zero ? 0.0f : a.lse[row] * kLog2e;
+  const float ent = zero || a.d_entropy == nullptr ? 0.0f : a.entropy[row];
+  dl *= a.scale;
+  de *= a.scale;
+  // d = -p (dl + de (log p + entropy)) = -p (k0 + k1 z), z = log2 p (a row without a distribution stays NaN)
+  const float k0 = fmaf(de, ent, dl) + (lse2 - lse2), k1 = de * static_cast<float>(kLn2);
+  float own = 0.0f;
+  if (!zero && y >= begin && y < begin + kStep) {
+    // 1 - p from the log-probability itself: exact where p is close to 1
+    const float lp = a.logp[row];
+    own = -expm1f(lp) * dl;
+    if (de != 0.0f) own -= de * expf(lp) * (fmaxf(lp, -1000.0f) + ent);
+  }
+  uint4 v[kUnroll];
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    const int64_t i = begin + u * kThreads * 8 + tid * 8;
+    v[u] = make_uint4(0u, 0u, 0u, 0u);
+    if (!zero && i < a.V) v[u] = kVec ? __ldcs(reinterpret_cast<const uint4*>(x + i)) : load8<false>(x, i, a.V);
+  }
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    const int64_t i = begin + u * kThreads * 8 + tid * 8;
+    if (i >= a.V) continue;
+    const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+    uint32_t o[4] = {0u, 0u, 0u, 0u};
+    if (!zero) {
+      const int at = y >= i && y < i + 8 ? static_cast<int>(y - i) : -1;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float z0 = fmaxf(fmaf(lo_bf16(w[k]), a.scale2, -lse2), -1000.0f);
+        const float z1 = fmaxf(fmaf(hi_bf16(w[k]), a.scale2, -lse2), -1000.0f);
+        float d0 = -ex2_approx(z0) * fmaf(k1, z0, k0), d1 = -ex2_approx(z1) * fmaf(k1, z1, k0);
+        if (at == 2 * k) d0 = own;
+        if (at == 2 * k + 1) d1 = own;
+        o[k] = pack_bf16x2(d0, d1);
+      }
+    }
+    if (kVec) {
+      __stcs(reinterpret_cast<uint4*>(out + i), make_uint4(o[0], o[1], o[2], o[3]));
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (i + k < a.V) out[i + k] = static_cast<uint16_t>(k & 1 ? o[k / 2] >> 16 : o[k / 2] & 0xFFFFu);
+    }
+  }
+}
+
+bool vec_ok(const void* p, int64_t stride) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride % 8 == 0; }
+
+template <bool kVec, bool kTop>
+cudaError_t launch_scores_t(const ScoresArgs& a, size_t smem, cudaStream_t s) {
+  static bool attr_set[kMaxDeviceCache] = {};
+  const int dev = cached_device_index();
+  if (dev < 0) return cudaErrorInvalidDevice;
+  if (!attr_set[dev]) {
+    cudaError_t e = cudaFuncSetAttribute(scores_kernel<kVec, kTop>, cudaFuncAttributeMaxDynamicSharedMemorySize, kScoresSmem);
+    if (e != cudaSuccess) return e;
+    attr_set[dev] = true;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(a.parts);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(a.T * a.parts));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.parts > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, scores_kernel<kVec, kTop>, a);
+}
+
+}  // namespace
+
+cudaError_t launch_scores(const ScoresArgs& args, cudaStream_t s) {
+  ScoresArgs a = args;
+  // a cluster a row while the rows alone leave SMs without a CTA, and slices are worth it
+  const int64_t sms = num_sms();
+  a.parts = 1;
+  while (a.parts < kMaxCluster && (a.T * a.parts < 2 * sms || a.V / a.parts > kMaxScoresSlice) && a.V / a.parts > kStep)
+    a.parts *= 2;
+  a.slice = (a.V + a.parts - 1) / a.parts;
+  a.slice = (a.slice + 31) / 32 * 32;
+  const bool vec = vec_ok(a.logits, a.ldx);
+  if (a.top == 0) return vec ? launch_scores_t<true, false>(a, 0, s) : launch_scores_t<false, false>(a, 0, s);
+  const size_t k = static_cast<size_t>(a.top);
+  size_t smem = ((static_cast<size_t>(a.slice) + 31) / 32 * 2 + 15) / 16 * 16;
+  smem += k * a.parts * 8 + 32 * k * 8 + k * ((a.slice / 32 + kThreads) / kThreads) * 4 + k * 4;
+  if (smem > kScoresSmem) return cudaErrorInvalidValue;
+  return vec ? launch_scores_t<true, true>(a, smem, s) : launch_scores_t<false, true>(a, smem, s);
+}
+
+cudaError_t launch_scores_bwd(const ScoresBwdArgs& args, cudaStream_t s) {
+  ScoresBwdArgs a = args;
+  a.rows_y = a.T < 65535 ? static_cast<int>(a.T) : 65535;
+  const dim3 grid(static_cast<unsigned>((a.V + kStep - 1) / kStep), static_cast<unsigned>(a.rows_y),
+                  static_cast<unsigned>((a.T + a.rows_y - 1) / a.rows_y));
+  const bool vec = vec_ok(a.logits, a.ldx) && vec_ok(a.dlogits, a.ldd) && a.V % 8 == 0;
+  if (vec)
+    scores_bwd_kernel<true><<<grid, kThreads, 0, s>>>(a);
+  else
+    scores_bwd_kernel<false><<<grid, kThreads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace ls

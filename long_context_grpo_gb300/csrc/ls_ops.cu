@@ -89,6 +89,89 @@ ls_status ls_policy_loss(const ls_policy_loss_desc* d, void* workspace, size_t w
   return e == cudaSuccess ? LS_OK : static_cast<ls_status>(launch_failed(e, "policy loss launch"));
 }
 
+ls_status ls_token_scores(const ls_token_scores_desc* d, void* stream) {
+  NvtxRange nvtx_range("ls_token_scores");
+  if (d == nullptr || d->logits == nullptr || d->ids == nullptr || d->logp == nullptr) return LS_ERR_INVALID_ARGUMENT;
+  if (d->T < 1 || d->V < 1 || d->logits_stride < d->V || d->top < 0 || d->top > d->V) return LS_ERR_INVALID_ARGUMENT;
+  if (!(d->temperature > 0.0) || !std::isfinite(d->temperature) || !std::isfinite(1.0 / d->temperature))
+    return LS_ERR_INVALID_ARGUMENT;
+  if (d->top > 0 && (d->top_ids == nullptr || d->top_logp == nullptr)) return LS_ERR_INVALID_ARGUMENT;
+  if (d->top > kMaxTop || (d->top > 0 && d->V > kMaxScoresVocab) || d->T >= (int64_t(1) << 28) ||
+      d->V >= (int64_t(1) << 31) || d->logits_stride >= (int64_t(1) << 31))
+    return LS_ERR_UNSUPPORTED;
+  if (!aligned_n(d->logits, 2) || !aligned_n(d->ids, 4) || !aligned_n(d->logp, 4) || !aligned_n(d->lse, 4) ||
+      !aligned_n(d->entropy, 4) || !aligned_n(d->top_ids, 4) || !aligned_n(d->top_logp, 4))
+    return LS_ERR_MISALIGNED;
+  uint32_t* status = nullptr;
+  ls_status st = static_cast<ls_status>(enter_call(stream, &status));
+  if (st != LS_OK) return st;
+  ScoresArgs a{};
+  a.T = d->T;
+  a.V = d->V;
+  a.ldx = d->logits_stride;
+  a.logits = static_cast<const uint16_t*>(d->logits);
+  a.ids = d->ids;
+  a.scale = 1.0 / d->temperature;
+  a.scale2 = static_cast<float>(1.4426950408889634074 / d->temperature);
+  a.top = d->top;
+  a.logp = d->logp;
+  a.lse = d->lse;
+  a.entropy = d->entropy;
+  a.top_ids = d->top_ids;
+  a.top_logp = d->top_logp;
+  a.status = status;
+  cudaError_t e;
+  {
+    LaunchTimer t(LS_KERNEL_TOKEN_LOGP, static_cast<cudaStream_t>(stream));
+    e = injected_failure() ? cudaErrorLaunchFailure : launch_scores(a, static_cast<cudaStream_t>(stream));
+  }
+  return e == cudaSuccess ? LS_OK : static_cast<ls_status>(launch_failed(e, "token scores launch"));
+}
+
+ls_status ls_token_scores_bwd(const ls_token_scores_bwd_desc* d, void* stream) {
+  NvtxRange nvtx_range("ls_token_scores_bwd");
+  if (d == nullptr || d->logits == nullptr || d->ids == nullptr || d->logp == nullptr || d->lse == nullptr ||
+      d->dlogits == nullptr)
+    return LS_ERR_INVALID_ARGUMENT;
+  if (d->d_logp == nullptr && d->d_entropy == nullptr) return LS_ERR_INVALID_ARGUMENT;
+  if (d->d_entropy != nullptr && d->entropy == nullptr) return LS_ERR_INVALID_ARGUMENT;
+  if (d->T < 1 || d->V < 1 || d->logits_stride < d->V || d->dlogits_stride < d->V) return LS_ERR_INVALID_ARGUMENT;
+  if (!(d->temperature > 0.0) || !std::isfinite(d->temperature) || !std::isfinite(1.0 / d->temperature))
+    return LS_ERR_INVALID_ARGUMENT;
+  if (d->logits == d->dlogits && d->logits_stride != d->dlogits_stride) return LS_ERR_INVALID_ARGUMENT;
+  if (d->T >= (int64_t(1) << 28) || d->V >= (int64_t(1) << 31) || d->logits_stride >= (int64_t(1) << 31) ||
+      d->dlogits_stride >= (int64_t(1) << 31))
+    return LS_ERR_UNSUPPORTED;
+  if (!aligned_n(d->logits, 2) || !aligned_n(d->dlogits, 2) || !aligned_n(d->ids, 4) || !aligned_n(d->logp, 4) ||
+      !aligned_n(d->lse, 4) || !aligned_n(d->entropy, 4) || !aligned_n(d->d_logp, 4) || !aligned_n(d->d_entropy, 4))
+    return LS_ERR_MISALIGNED;
+  uint32_t* status = nullptr;
+  ls_status st = static_cast<ls_status>(enter_call(stream, &status));
+  if (st != LS_OK) return st;
+  ScoresBwdArgs a{};
+  a.T = d->T;
+  a.V = d->V;
+  a.ldx = d->logits_stride;
+  a.ldd = d->dlogits_stride;
+  a.logits = static_cast<const uint16_t*>(d->logits);
+  a.ids = d->ids;
+  a.logp = d->logp;
+  a.lse = d->lse;
+  a.entropy = d->entropy;
+  a.d_logp = d->d_logp;
+  a.d_entropy = d->d_entropy;
+  a.scale = static_cast<float>(1.0 / d->temperature);
+  a.scale2 = static_cast<float>(1.4426950408889634074 / d->temperature);
+  a.dlogits = static_cast<uint16_t*>(d->dlogits);
+  a.status = status;
+  cudaError_t e;
+  {
+    LaunchTimer t(LS_KERNEL_TOKEN_LOGP, static_cast<cudaStream_t>(stream));
+    e = injected_failure() ? cudaErrorLaunchFailure : launch_scores_bwd(a, static_cast<cudaStream_t>(stream));
+  }
+  return e == cudaSuccess ? LS_OK : static_cast<ls_status>(launch_failed(e, "token scores gradient launch"));
+}
+
 ls_status ls_rope(const ls_rope_desc* d, void* stream) {
   NvtxRange nvtx_range("ls_rope");
   if (d == nullptr || d->inv_freq == nullptr) return LS_ERR_INVALID_ARGUMENT;

@@ -35,6 +35,44 @@ struct PolicyArgs {
 constexpr int kMaxPartials = 512;
 cudaError_t launch_policy_loss(const PolicyArgs& a, cudaStream_t s);
 
+// ----- scores of given tokens (k_scores.cu)
+constexpr int kMaxTop = 64;
+constexpr int kScoresSmem = 160 * 1024;
+constexpr int64_t kMaxScoresSlice = int64_t(1) << 20;      // logits of a CTA with alternatives
+constexpr int64_t kMaxScoresVocab = 8 * kMaxScoresSlice;
+struct ScoresArgs {
+  int64_t T, V, ldx;
+  const uint16_t* logits;     // bf16, row t at logits + t * ldx
+  const int32_t* ids;
+  double scale;               // 1 / temperature
+  float scale2;               // log2 e / temperature
+  int top;
+  float* logp;
+  float* lse;                 // or nullptr
+  float* entropy;             // or nullptr
+  int32_t* top_ids;           // [T][top]
+  float* top_logp;
+  uint32_t* status;
+  int parts;                  // CTAs of a row, logits of each (set by the launch)
+  int64_t slice;
+};
+cudaError_t launch_scores(const ScoresArgs& a, cudaStream_t s);
+struct ScoresBwdArgs {
+  int64_t T, V, ldx, ldd;
+  const uint16_t* logits;
+  const int32_t* ids;
+  const float* logp;
+  const float* lse;
+  const float* entropy;       // or nullptr without d_entropy
+  const float* d_logp;        // or nullptr
+  const float* d_entropy;     // or nullptr
+  float scale, scale2;
+  uint16_t* dlogits;          // row t at dlogits + t * ldd; may be the logits
+  uint32_t* status;
+  int rows_y;                 // rows of the grid's second dimension (set by the launch)
+};
+cudaError_t launch_scores_bwd(const ScoresBwdArgs& a, cudaStream_t s);
+
 // ----- paged cache
 struct CacheView {
   uint16_t* k;
