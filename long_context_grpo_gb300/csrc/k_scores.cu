@@ -41,6 +41,12 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
   return r;
 }
 
+__device__ __forceinline__ float warp_max(float x) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // Whole numbers in the order of bf16 values, -0 as 0; +inf is 0xFF80, and NaN (as max2 leaves it) above.
 __device__ __forceinline__ uint32_t order(uint32_t bits) {
   bits = bits == 0x8000u ? 0u : bits;
@@ -69,6 +75,93 @@ __device__ __forceinline__ uint4 load8(const uint16_t* x, int64_t i, int64_t end
     w[k] = a | (b << 16);
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Sums are kept of 2^z, z = x scale2 - r, r = m scale2 rounded, m the largest logit of theirs: one fused
+// product and difference an exponent, right to 2^-24 of it.  The logits that equal m are counted instead, 1 each
+// (m's own z is only the rounding of r).  Where r is past kFar, or m is -inf, z is (x - m) scale2: any two
+// logits there differ by more than fp32's exponents hold.
+constexpr float kFar = 1e30f;
+__device__ __forceinline__ float reference(float m, float scale2) { return m * scale2; }
+
+// Sums with the largest logit m and reference r, for a larger one.
+__device__ __forceinline__ void rebase(float to, float scale2, float m, float& r, float& ones, float& hi, float& lo, float& e) {
+  const float next = reference(to, scale2);
+  const bool near = fabsf(r) < kFar && fabsf(next) < kFar;
+  if (near) {                        // the counted ones join the sum
+    const float z = fmaf(m, scale2, -r);
+    e = fmaf(ones, z, e);
+    two_sum_acc(hi, lo, ones * fmaf(z, 0.69314718f, 1.0f));
+  }
+  // z falls by d for all, 2^z by f, sum 2^z z to f (sum 2^z z + d sum 2^z)
+  const float d = near ? fmaxf(r - next, -1000.0f) : -1000.0f, f = ex2_approx(d);
+  e = f * fmaf(d, hi, e);
+  hi *= f;
+  lo *= f;
+  ones = 0.0f;
+  r = next;
+}
+
+// Sum and sum e z of a thread's chunk.  kPeak: without the exponentials of logits that equal m, which are
+// counted; kFarOff: r is out of range.
+template <bool kPeak, bool kFarOff>
+__device__ __forceinline__ void add_chunk(const uint4 (&v)[kUnroll], float m, float r, float scale2, float& ones, float& s,
+                                          float& es) {
+  const uint64_t c2 = f2_pack(scale2, scale2), r2 = f2_pack(-r, -r);
+  uint64_t s2[2] = {f2_pack(0.0f, 0.0f), f2_pack(0.0f, 0.0f)}, e2[2] = {s2[0], s2[0]};
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint64_t x = f2_pack(lo_bf16(w[k]), hi_bf16(w[k]));
+      uint64_t z;
+      if constexpr (kFarOff) {
+        // (below: exponents of nothing, and -inf - -inf)
+        z = f2_pack(fmaxf((lo_bf16(w[k]) - m) * scale2, -1000.0f), fmaxf((hi_bf16(w[k]) - m) * scale2, -1000.0f));
+      } else {
+        z = f2_fma(x, c2, r2);
+      }
+      float z0, z1;
+      f2_unpack(z, z0, z1);
+      float p0 = ex2_approx(z0), p1 = ex2_approx(z1);
+      if constexpr (kPeak) {
+        if (lo_bf16(w[k]) == m) {
+          ones += 1.0f;
+          p0 = 0.0f;
+        }
+        if (hi_bf16(w[k]) == m) {
+          ones += 1.0f;
+          p1 = 0.0f;
+        }
+      }
+      const uint64_t p = f2_pack(p0, p1);
+      s2[k & 1] = f2_add(s2[k & 1], p);
+      e2[k & 1] = f2_fma(p, z, e2[k & 1]);
+    }
+  }
+  float s0, s1, e0, e1;
+  f2_unpack(f2_add(s2[0], s2[1]), s0, s1);
+  f2_unpack(f2_add(e2[0], e2[1]), e0, e1);
+  s = s0 + s1;
+  es = e0 + e1;
+}
+
+// Sum e z of a chunk that holds logits of -inf (or so low that their z is): 0 x -1000 is 0 where 0 x -inf is not.
+__device__ __forceinline__ float chunk_entropy(const uint4 (&v)[kUnroll], float m, float r, float scale2) {
+  float es = 0.0f;
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float x0 = lo_bf16(w[k]), x1 = hi_bf16(w[k]);
+      const float z0 = fmaxf(fmaf(x0, scale2, -r), -1000.0f), z1 = fmaxf(fmaf(x1, scale2, -r), -1000.0f);
+      if (x0 != m) es = fmaf(ex2_approx(z0), z0, es);
+      if (x1 != m) es = fmaf(ex2_approx(z1), z1, es);
+    }
+  }
+  return es;
 }
 
 // What a CTA knows of its slice: largest logit (as a whole number), sum, sum e z, its best logits.
@@ -111,9 +204,8 @@ __global__ void __launch_bounds__(kThreads) scores_kernel(const __grid_constant_
   }
 
   uint16_t* groups = reinterpret_cast<uint16_t*>(dyn);
-  float m = -INFINITY, ones = 0.0f, hi = 0.0f, lo = 0.0f, e = 0.0f;
+  float m = -INFINITY, r = -INFINITY, ones = 0.0f, hi = 0.0f, lo = 0.0f, e = 0.0f;
   uint32_t top2 = kNegInf2;
-  const uint64_t c2 = f2_pack(a.scale2, a.scale2);
   for (int base = 0; base < len; base += kStep) {
     uint4 v[kUnroll];
 #pragma unroll
@@ -139,54 +231,24 @@ __global__ void __launch_bounds__(kThreads) scores_kernel(const __grid_constant_
     }
     const uint32_t t2 = max2(g[0], g[1]);
     top2 = max2(top2, t2);
-    const float cm = fmaxf(lo_bf16(t2), hi_bf16(t2));
+    // (one maximum a warp: a lane's own would grow in most steps of some lane)
+    const float cm = warp_max(fmaxf(lo_bf16(t2), hi_bf16(t2)));
     if (cm > m) {
-      // z falls by d for all before: e^z by f, sum e z to f (sum e z + d sum e)
-      const float d = fmaxf((m - cm) * a.scale2, -1000.0f), f = ex2_approx(d);
-      two_sum_acc(hi, lo, ones);
-      e = f * fmaf(d, hi, e);
-      hi *= f;
-      lo *= f;
-      ones = 0.0f;
+      rebase(cm, a.scale2, m, r, ones, hi, lo, e);
       m = cm;
     }
-    const uint64_t m2 = f2_pack(m, m);
-    uint64_t s2[2] = {f2_pack(0.0f, 0.0f), f2_pack(0.0f, 0.0f)}, e2[2] = {s2[0], s2[0]};
     // peak: the maximum is among these; its exponentials, 1 each, are counted and not added
-    auto add = [&](auto peak) {
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          float z0, z1;
-          f2_unpack(f2_mul(f2_sub(f2_pack(lo_bf16(w[k]), hi_bf16(w[k])), m2), c2), z0, z1);
-          // (below: exponents of nothing, and -inf - -inf; 0 x -1000 is 0 where 0 x -inf is not)
-          z0 = fmaxf(z0, -1000.0f);
-          z1 = fmaxf(z1, -1000.0f);
-          float p0 = ex2_approx(z0), p1 = ex2_approx(z1);
-          if constexpr (decltype(peak)::value) {
-            if (lo_bf16(w[k]) == m) {
-              ones += 1.0f;
-              p0 = 0.0f;
-            }
-            if (hi_bf16(w[k]) == m) {
-              ones += 1.0f;
-              p1 = 0.0f;
-            }
-          }
-          const uint64_t p = f2_pack(p0, p1);
-          s2[k & 1] = f2_add(s2[k & 1], p);
-          e2[k & 1] = f2_fma(p, f2_pack(z0, z1), e2[k & 1]);
-        }
-      }
-    };
-    if (__any_sync(0xffffffffu, cm == m)) add(std::true_type{}); else add(std::false_type{});
-    float s0, s1, e0, e1;
-    f2_unpack(f2_add(s2[0], s2[1]), s0, s1);
-    f2_unpack(f2_add(e2[0], e2[1]), e0, e1);
-    two_sum_acc(hi, lo, s0 + s1);
-    e += e0 + e1;
+    float s, es;
+    if (!(fabsf(r) < kFar)) {
+      add_chunk<true, true>(v, m, r, a.scale2, ones, s, es);
+    } else if (cm == m) {
+      add_chunk<true, false>(v, m, r, a.scale2, ones, s, es);
+    } else {
+      add_chunk<false, false>(v, m, r, a.scale2, ones, s, es);
+    }
+    if (!(es == es)) es = chunk_entropy(v, m, r, a.scale2);     // 0 x -inf
+    two_sum_acc(hi, lo, s);
+    e += es;
   }
 
   // the slice's maximum, and the sums relative to it
@@ -203,14 +265,7 @@ __global__ void __launch_bounds__(kThreads) scores_kernel(const __grid_constant_
   for (int w = 0; w < kWarps; ++w) top = max(top, sh_max[w]);
   {
     const float peak = value_of(top);
-    if (m != peak) {
-      const float d = fmaxf((m - peak) * a.scale2, -1000.0f), f = ex2_approx(d);
-      two_sum_acc(hi, lo, ones);
-      e = f * fmaf(d, hi, e);
-      hi *= f;
-      lo *= f;
-      ones = 0.0f;
-    }
+    if (m != peak) rebase(peak, a.scale2, m, r, ones, hi, lo, e);
   }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) {
@@ -334,29 +389,28 @@ __global__ void __launch_bounds__(kThreads) scores_kernel(const __grid_constant_
     float n = 0.0f, h = 0.0f, l = 0.0f, w = 0.0f;
     for (int i = 0; i < parts; ++i) {
       Slice s = sh_slice[i];
-      if (s.top == all) {
-        n += s.ones;
-        two_sum_acc(h, l, s.hi);
-        l += s.lo;
-        w += s.e;
-      } else {
-        const float d = fmaxf((value_of(s.top) - peak) * a.scale2, -1000.0f), f = ex2_approx(d);
-        two_sum_acc(s.hi, s.lo, s.ones);
-        two_sum_acc(h, l, s.hi * f);
-        l += s.lo * f;
-        w += f * fmaf(d, s.hi, s.e);
-      }
+      const float from = value_of(s.top);
+      float base = reference(from, a.scale2);
+      if (from != peak) rebase(peak, a.scale2, from, base, s.ones, s.hi, s.lo, s.e);
+      n += s.ones;
+      two_sum_acc(h, l, s.hi);
+      l += s.lo;
+      w += s.e;
     }
     // a NaN or an infinite logit, or none that is larger than -inf: no distribution
     const bool none = all >= 0xFF80u || all <= 0x007Fu;
-    const double rest = static_cast<double>(h) + static_cast<double>(l), S = n + rest;
+    // the reference's rounding goes out again: z from the peak itself is z + off
+    const float base = reference(peak, a.scale2);
+    const double off = fabsf(base) < kFar ? static_cast<double>(base) - static_cast<double>(peak) * a.scale2 : 0.0;
+    const double back = fabs(off) < 0x1p-12 ? 1.0 + off * kLn2 : exp2(off);
+    const double rest = (static_cast<double>(h) + static_cast<double>(l)) * back, S = n + rest;
     const double lns = none ? static_cast<double>(NAN) : log1p(n - 1.0 + rest);
     sh_lns = lns;
     sh_top = all;
     a.logp[row] = y < 0 ? 0.0f : static_cast<float>((static_cast<double>(xy) - peak) * a.scale - lns);
     if (a.lse != nullptr) a.lse[row] = static_cast<float>(peak * a.scale + lns);
     if (a.entropy != nullptr) {
-      const double ent = lns - kLn2 * w / S;
+      const double ent = lns - kLn2 * (w * back + off * rest) / S;
       a.entropy[row] = ent < 0.0 ? 0.0f : static_cast<float>(ent);
     }
   }
