@@ -14,7 +14,7 @@
 //   groups with the largest maxima (ties to the lowest group), so that only these are looked at again.
 //   Proof: were one of them in another group, each of the k groups before that one would hold a
 //   logit before it.
-// scores_bwd_kernel: one pass, a block 8,192 logits of a row.
+// scores_bwd_kernel: one pass, a block 4,096 logits of a row.
 #include <type_traits>
 
 #include "ls_internal.h"
@@ -24,7 +24,7 @@
 namespace ls {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kThreads = 128, kWarps = kThreads / 32;
 constexpr int kUnroll = 4;                        // 4 x 8 logits a thread and step
 constexpr int kStep = kThreads * 8 * kUnroll;
 constexpr float kLog2e = 1.4426950408889634f;
