@@ -456,6 +456,45 @@ ls_status ls_rope_freqs(int32_t rot_dim, double theta, int32_t scaling, double f
                         double* attn_factor);
 
 /*
+ * ls_norm_rope -- norms of queries and keys, a head each, with the rotation in the same pass.  For every
+ * head x of D values, r = 1 / sqrt(mean x^2 + eps) and n_i = x_i r (w_i + weight_offset); n is then turned as by
+ * ls_rope (d->inverse has to be 0).  inv_freq NULL with rot_dim 0: norms alone.  All of it in fp32,
+ * rounded once.  Tensors, strides, positions and limits as in ls_rope; the outputs may be the inputs.
+ *   q_weight, k_weight  device [D], bf16 or fp32 (weight_fp32 for both); NULL: 1, without the offset
+ *   eps > 0.  A head with an infinity or NaN gives NaN or what the formula gives; a head of zeros gives 0.
+ * Rows that are 16-byte aligned with D and rot_dim multiples of 16 are fast.
+ *
+ * ls_norm_rope_bwd -- the gradient: d->q, d->k are d loss / d output, d->q_out, d->k_out receive d loss / d
+ * input (they may be d->q, d->k), g->q_in, g->k_in are the forward pass's inputs.  With u = (dy turned back)
+ * (w + weight_offset): dx = r (u - x r^2 mean(u x)).  dq_weight, dk_weight: device fp32 [D], written: the sum of
+ * (dy turned back) x r over tokens and heads, in a fixed order; NULL: not wanted.
+ * workspace: device, 16-byte aligned, >= ls_norm_rope_bwd_workspace_bytes(T, D); may be NULL without
+ * weight gradients.
+ *
+ * ls_cache_append_norm -- ls_cache_append with the norms on the way: keys (and queries) are normed, then
+ * turned; values are copied.  Here queries may come without inv_freq (norms alone).
+ */
+typedef struct {
+  const void* q_weight;
+  const void* k_weight;
+  int32_t weight_fp32;
+  double weight_offset;
+  double eps;
+} ls_head_norm;
+typedef struct {
+  const void* q_in;
+  int64_t q_in_stride;
+  const void* k_in;
+  int64_t k_in_stride;
+  float* dq_weight;
+  float* dk_weight;
+} ls_head_norm_grad;
+ls_status ls_norm_rope(const ls_rope_desc* d, const ls_head_norm* n, void* stream);
+size_t ls_norm_rope_bwd_workspace_bytes(int64_t T, int32_t D);
+ls_status ls_norm_rope_bwd(const ls_rope_desc* d, const ls_head_norm* n, const ls_head_norm_grad* g,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Paged cache (review section 3-2 (2), physical pages of the prompt's keys and values; the
  * prompt as state shared by the group, section 2): keys and values of one attention layer in
  * pages of page_size tokens.  A model has a cache a layer, each with a page table, lengths and
@@ -594,6 +633,8 @@ typedef struct {
   double attn_factor;
 } ls_cache_append_desc;
 ls_status ls_cache_append(ls_cache_t h, const ls_cache_append_desc* d, void* stream);
+ls_status ls_cache_append_norm(ls_cache_t h, const ls_cache_append_desc* d, const ls_head_norm* norm,
+                               void* stream);
 
 typedef struct {
   int32_t S;

@@ -10,7 +10,8 @@ _BINDING = ("Prefix", "grpo_loss", "grpo_loss_workspace_bytes", "device_status",
             "LongStrawError", "library_path", "STATUS_NAMES", "timing_enable", "timing_read", "token_logp",
             "KERNEL_NAMES", "attn_merge", "sum_bf16", "bf16_to_f32", "f32_to_bf16")
 _OPS = ("policy_loss", "PolicyLoss", "policy_loss_workspace_bytes", "rope", "rope_freqs", "PagedCache",
-        "token_scores", "TokenScores", "token_scores_bwd")
+        "token_scores", "TokenScores", "token_scores_bwd", "norm_rope", "norm_rope_bwd", "NormRopeGrads",
+        "norm_rope_bwd_workspace_bytes")
 
 
 def __getattr__(name):

@@ -81,6 +81,18 @@ class RopeDesc(ctypes.Structure):
                 ("k_out", ctypes.c_void_p), ("k_out_stride", ctypes.c_int64)]
 
 
+class HeadNorm(ctypes.Structure):
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+                ("weight_fp32", ctypes.c_int32), ("weight_offset", ctypes.c_double),
+                ("eps", ctypes.c_double)]
+
+
+class HeadNormGrad(ctypes.Structure):
+    _fields_ = [("q_in", ctypes.c_void_p), ("q_in_stride", ctypes.c_int64),
+                ("k_in", ctypes.c_void_p), ("k_in_stride", ctypes.c_int64),
+                ("dq_weight", ctypes.c_void_p), ("dk_weight", ctypes.c_void_p)]
+
+
 class CacheDesc(ctypes.Structure):
     _fields_ = [("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int32),
                 ("Hq", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("D", ctypes.c_int32),
@@ -150,6 +162,9 @@ def _load():
         "ls_token_scores": (ctypes.c_int, [vp, vp]),
         "ls_token_scores_bwd": (ctypes.c_int, [vp, vp]),
         "ls_rope": (ctypes.c_int, [vp, vp]),
+        "ls_norm_rope": (ctypes.c_int, [vp, vp, vp]),
+        "ls_norm_rope_bwd_workspace_bytes": (sz, [i64, i32]),
+        "ls_norm_rope_bwd": (ctypes.c_int, [vp, vp, vp, vp, sz, vp]),
         "ls_rope_freqs": (ctypes.c_int, [i32, ctypes.c_double, i32, ctypes.c_double, i64,
                                          ctypes.c_double, ctypes.c_double, vp, vp]),
         "ls_cache_create": (ctypes.c_int, [ctypes.POINTER(CacheDesc), ctypes.POINTER(vp)]),
@@ -161,6 +176,7 @@ def _load():
         "ls_cache_free": (ctypes.c_int, [vp, i32, vp, vp]),
         "ls_cache_compact": (ctypes.c_int, [vp, vp, vp, vp, sz, vp]),
         "ls_cache_append": (ctypes.c_int, [vp, vp, vp]),
+        "ls_cache_append_norm": (ctypes.c_int, [vp, vp, vp, vp]),
         "ls_cache_attn_workspace_bytes": (sz, [vp, i32, i64, i32, i64]),
         "ls_cache_attn": (ctypes.c_int, [vp, vp, vp, sz, vp]),
         "ls_cache_attn_window_workspace_bytes": (sz, [vp, i32, i64, i32, i64, i64, i64]),

@@ -24,6 +24,8 @@ _POLICY = struct.Struct("@qqqqPPPPPPdddiPPPPP")
 _SCORES = struct.Struct("@qqqPPdiPPPPP")
 _SCORES_BWD = struct.Struct("@qqqqPPdPPPPPP")
 _ROPE = struct.Struct("@qiiiiiiPdPqPqPqPqPq")
+_NORM = struct.Struct("@PPidd")
+_NORM_GRAD = struct.Struct("@PqPqPP")
 _APPEND = struct.Struct("@iqPPPqPqPqPqPiid")
 _ATTN = struct.Struct("@iqPPiqPqPPiP")
 
@@ -268,6 +270,103 @@ def rope(q, k, inv_freq, positions=None, pos0: int = 0, interleaved: bool = Fals
     return q_out, k_out
 
 
+def _norm(q_weight, k_weight, eps, weight_offset, D, dev):
+    """The packed norm of heads: weights bf16 or fp32 [D], both of one type."""
+    kind = _bf16
+    for w in (q_weight, k_weight):
+        if isinstance(w, _Tensor) and w.dtype is _f32:
+            kind = _f32
+    return _NORM.pack(_opt(q_weight, "q_weight", kind, (D,), dev), _opt(k_weight, "k_weight", kind, (D,), dev),
+                      kind is _f32, weight_offset, eps)
+
+
+def _rope_desc(q, k, inv_freq, positions, pos0, interleaved, attn_factor, q_out, k_out, dev):
+    """(packed descriptor, q_out, k_out, T, D, keep-alive) of a rotation, inv_freq None: of none."""
+    some = q if q is not None else k
+    for t in (some, k):
+        if t is not None and (not isinstance(t, _Tensor) or t.dim() != 3):
+            raise TypeError("q and k must be 3-D CUDA tensors")
+    if some is None:
+        raise TypeError("q or k must be a 3-D CUDA tensor")
+    T, _, D = some.shape
+    f, n, keep = (0, 0, None) if inv_freq is None else _host_doubles(inv_freq, "inv_freq")
+    Hq = Hk = qp = qs = qo = qos = kp = ks = ko = kos = 0
+    if q is not None:
+        Hq = q.shape[1]
+        qp, qs = _heads(q, "q", T, Hq, D, dev)
+        if q_out is None:
+            q_out = torch.empty((T, Hq, D), dtype=_bf16, device=q.device)
+            qo, qos = q_out.data_ptr(), Hq * D
+        else:
+            qo, qos = _heads(q_out, "q_out", T, Hq, D, dev)
+    if k is not None:
+        Hk = k.shape[1]
+        kp, ks = _heads(k, "k", T, Hk, D, dev)
+        if k_out is None:
+            k_out = torch.empty((T, Hk, D), dtype=_bf16, device=k.device)
+            ko, kos = k_out.data_ptr(), Hk * D
+        else:
+            ko, kos = _heads(k_out, "k_out", T, Hk, D, dev)
+    d = _ROPE.pack(T, Hq, Hk, D, 2 * n, bool(interleaved), False, f, attn_factor,
+                   _opt(positions, "positions", _i64, (T,), dev), pos0, qp, qs, qo, qos, kp, ks, ko, kos)
+    return d, q_out, k_out, T, D, keep
+
+
+def norm_rope(q, k, q_weight, k_weight, inv_freq=None, eps: float = 1e-6, positions=None, pos0: int = 0,
+              interleaved: bool = False, attn_factor: float = 1.0, weight_offset: float = 0.0, q_out=None, k_out=None):
+    """Norms of q [T, Hq, D] and k [T, Hk, D] (bf16; either may be None; rows may be strided views), a head
+    each: x / sqrt(mean x^2 + eps) * (weight + weight_offset), turned by their positions as rope() does it in the
+    same pass (inv_freq None: norms alone).  Weights: bf16 or fp32 [D], None: 1.  q_out / k_out may be the
+    inputs.  Returns (q_out, k_out)."""
+    dev = torch.cuda.current_device()
+    d, q_out, k_out, _, D, keep = _rope_desc(q, k, inv_freq, positions, pos0, interleaved, attn_factor, q_out, k_out, dev)
+    b._check(b._lib().ls_norm_rope(d, _norm(q_weight, k_weight, eps, weight_offset, D, dev), _raw_stream(dev)),
+             "ls_norm_rope")
+    return q_out, k_out
+
+
+class NormRopeGrads(NamedTuple):
+    dq: torch.Tensor          # bf16 [T, Hq, D]
+    dk: torch.Tensor          # bf16 [T, Hk, D]
+    dq_weight: torch.Tensor   # fp32 [D], None without q or its weight
+    dk_weight: torch.Tensor   # fp32 [D], likewise
+
+
+def norm_rope_bwd_workspace_bytes(T: int, D: int) -> int:
+    return int(b._lib().ls_norm_rope_bwd_workspace_bytes(T, D))
+
+
+def norm_rope_bwd(dq, dk, q, k, q_weight, k_weight, inv_freq=None, eps: float = 1e-6, positions=None, pos0: int = 0,
+                  interleaved: bool = False, attn_factor: float = 1.0, weight_offset: float = 0.0, dq_out=None,
+                  dk_out=None, workspace=None) -> NormRopeGrads:
+    """Gradients of norm_rope(): dq, dk are d loss / d its outputs, q, k its inputs.  dq_out / dk_out may be
+    dq / dk.  Weight gradients are fp32 sums over tokens and heads (None for a weight that is None)."""
+    dev = torch.cuda.current_device()
+    if (dq is None) != (q is None) or (dk is None) != (k is None):
+        raise TypeError("dq comes with q, and dk with k")
+    d, dq_out, dk_out, T, D, keep = _rope_desc(dq, dk, inv_freq, positions, pos0, interleaved, attn_factor, dq_out, dk_out,
+                                               dev)
+    qp = qs = kp = ks = 0
+    dwq = dwk = None
+    if q is not None:
+        qp, qs = _heads(q, "q", T, dq.shape[1], D, dev)
+        if q_weight is not None:
+            dwq = torch.empty(D, dtype=_f32, device=q.device)
+    if k is not None:
+        kp, ks = _heads(k, "k", T, dk.shape[1], D, dev)
+        if k_weight is not None:
+            dwk = torch.empty(D, dtype=_f32, device=k.device)
+    wp = nbytes = 0
+    if dwq is not None or dwk is not None:
+        if workspace is None:
+            workspace = torch.empty(norm_rope_bwd_workspace_bytes(T, D), dtype=_u8, device=(q if q is not None else k).device)
+        wp, nbytes = _ptr(workspace, "workspace", _u8, None, dev), workspace.numel()
+    g = _NORM_GRAD.pack(qp, qs, kp, ks, 0 if dwq is None else dwq.data_ptr(), 0 if dwk is None else dwk.data_ptr())
+    b._check(b._lib().ls_norm_rope_bwd(d, _norm(q_weight, k_weight, eps, weight_offset, D, dev), g, wp, nbytes,
+                                       _raw_stream(dev)), "ls_norm_rope_bwd")
+    return NormRopeGrads(dq_out, dk_out, dwq, dwk)
+
+
 class PagedCache:
     """Keys and values of one attention layer in pages that sequences may share.
 
@@ -370,10 +469,14 @@ class PagedCache:
                                            _raw_stream(dev)), "ls_cache_compact")
 
     def append(self, k_new, v_new, cu_new, rows=None, q=None, q_out=None, inv_freq=None,
-               interleaved: bool = False, attn_factor: float = 1.0):
+               interleaved: bool = False, attn_factor: float = 1.0, q_weight=None, k_weight=None,
+               norm_eps: float = None, weight_offset: float = 0.0):
         """Writes the last new tokens of each sequence (packed by cu_new, int32 [S + 1]; lengths
         already extended) into their pages, rotated with inv_freq on the way, and rotates q
-        [T, Hq, D] in the same pass.  Returns (q_out, None) or, without q, (None, None)."""
+        [T, Hq, D] in the same pass.  norm_eps: keys and queries are normed first, a head each, with
+        these weights (as norm_rope does it).  Returns (q_out, None) or, without q, (None, None)."""
+        if norm_eps is None and (q_weight is not None or k_weight is not None):
+            raise ValueError("weights are of a norm: norm_eps is missing")
         if not isinstance(k_new, torch.Tensor) or k_new.dim() != 3:
             raise TypeError("k_new must be a 3-D CUDA tensor")
         T = k_new.shape[0]
@@ -394,7 +497,11 @@ class PagedCache:
                 qo, qos = _heads(q_out, "q_out", T, self.Hq, self.D, dev)
         d = _APPEND.pack(S, T, 0 if rows is None else self._list(rows, "rows", dev, S), cp,
                          kp, ks, vp, vs, qp, qs, qo, qos, f, 2 * n, bool(interleaved), attn_factor)
-        b._check(b._lib().ls_cache_append(self._h, d, _raw_stream(dev)), "ls_cache_append")
+        if norm_eps is None:
+            b._check(b._lib().ls_cache_append(self._h, d, _raw_stream(dev)), "ls_cache_append")
+        else:
+            n = _norm(q_weight, k_weight, norm_eps, weight_offset, self.D, dev)
+            b._check(b._lib().ls_cache_append_norm(self._h, d, n, _raw_stream(dev)), "ls_cache_append_norm")
         return (q_out if q is not None else None), None
 
     def attn_workspace_bytes(self, S: int, T: int, max_new: int, max_len: int, window: int = None,

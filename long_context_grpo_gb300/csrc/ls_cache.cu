@@ -51,6 +51,7 @@ ls_status run_launch(int kernel, void* stream, const char* what, F launch) {
 
 ls_status attn_impl(ls_cache_t h, const ls_cache_attn_desc* d, const int64_t* sight, void* workspace,
                     size_t workspace_bytes, void* stream);
+ls_status append_impl(ls_cache_t h, const ls_cache_append_desc* d, const ls_head_norm* norm, void* stream);
 
 ls_status check_pages_ws(ls_cache_t h, const void* ws, size_t bytes) {
   if (ws == nullptr || bytes < ls_cache_pages_workspace_bytes(h)) return LS_ERR_WORKSPACE;
@@ -234,6 +235,48 @@ ls_status ls_cache_compact(ls_cache_t src, ls_cache_t dst, int32_t* n_live, void
 
 ls_status ls_cache_append(ls_cache_t h, const ls_cache_append_desc* d, void* stream) {
   NvtxRange nvtx_range("ls_cache_append");
+  return append_impl(h, d, nullptr, stream);
+}
+
+ls_status ls_cache_append_norm(ls_cache_t h, const ls_cache_append_desc* d, const ls_head_norm* norm, void* stream) {
+  NvtxRange nvtx_range("ls_cache_append_norm");
+  if (norm == nullptr) return check_cache(h) != LS_OK ? LS_ERR_NOT_PREPARED : LS_ERR_INVALID_ARGUMENT;
+  return append_impl(h, d, norm, stream);
+}
+
+size_t ls_cache_attn_workspace_bytes(ls_cache_t h, int32_t S, int64_t T, int32_t max_new,
+                                     int64_t max_len) {
+  if (check_cache(h) != LS_OK || S < 1 || T < 1 || max_new < 1 || max_len < 1) return 0;
+  return cache_attn_layout(h->view, S, T).total;
+}
+
+size_t ls_cache_attn_window_workspace_bytes(ls_cache_t h, int32_t S, int64_t T, int32_t max_new,
+                                            int64_t max_len, int64_t window, int64_t sinks) {
+  if (check_cache(h) != LS_OK || S < 1 || T < 1 || max_new < 1 || max_len < 1 || window < 1 || sinks < 0 ||
+      S > kMaxSeqs || T >= (int64_t(1) << 31) || max_len >= (int64_t(1) << 31))
+    return 0;
+  return cache_window_layout(h->view, S, T, max_new, max_len, window, sinks).total;
+}
+
+ls_status ls_cache_attn(ls_cache_t h, const ls_cache_attn_desc* d, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+  NvtxRange nvtx_range("ls_cache_attn");
+  return attn_impl(h, d, nullptr, workspace, workspace_bytes, stream);
+}
+
+ls_status ls_cache_attn_window(ls_cache_t h, const ls_cache_attn_desc* d, int64_t window, int64_t sinks,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+  NvtxRange nvtx_range("ls_cache_attn_window");
+  const int64_t sight[2] = {window, sinks};
+  return attn_impl(h, d, sight, workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"
+
+namespace {
+
+// norm: the heads' norms on the way, or null.
+ls_status append_impl(ls_cache_t h, const ls_cache_append_desc* d, const ls_head_norm* norm, void* stream) {
   ls_status st = check_cache(h);
   if (st != LS_OK) return st;
   if (d == nullptr || d->cu_new == nullptr || d->k_new == nullptr || d->v_new == nullptr)
@@ -243,11 +286,16 @@ ls_status ls_cache_append(ls_cache_t h, const ls_cache_append_desc* d, void* str
   const CacheView& c = h->view;
   const int64_t nk = static_cast<int64_t>(c.Hkv) * c.D, nq = static_cast<int64_t>(c.Hq) * c.D;
   if (d->k_stride < nk || d->v_stride < nk) return LS_ERR_INVALID_ARGUMENT;
-  RopeArgs a{};
+  NormArgs n{};
+  if (norm != nullptr) {
+    st = static_cast<ls_status>(head_norm_args(norm, &n));
+    if (st != LS_OK) return st;
+  }
+  RopeArgs& a = n.r;
   if (d->inv_freq != nullptr) {
     if (d->rot_dim < 2 || d->rot_dim > c.D || d->rot_dim % 2 != 0) return LS_ERR_INVALID_ARGUMENT;
     if (!rope_turns(d->inv_freq, d->rot_dim, d->attn_factor, &a)) return LS_ERR_INVALID_ARGUMENT;
-  } else if (d->q != nullptr) {
+  } else if (d->q != nullptr && norm == nullptr) {
     return LS_ERR_INVALID_ARGUMENT;
   }
   if (d->q != nullptr) {
@@ -281,39 +329,8 @@ ls_status ls_cache_append(ls_cache_t h, const ls_cache_append_desc* d, void* str
   a.c = c;
   a.status = status;
   return run_launch(LS_KERNEL_CACHE_APPEND, stream, "cache append launch",
-                    [&](cudaStream_t s) { return launch_rope(a, s); });
+                    [&](cudaStream_t s) { return norm != nullptr ? launch_norm_rope(n, s) : launch_rope(a, s); });
 }
-
-size_t ls_cache_attn_workspace_bytes(ls_cache_t h, int32_t S, int64_t T, int32_t max_new,
-                                     int64_t max_len) {
-  if (check_cache(h) != LS_OK || S < 1 || T < 1 || max_new < 1 || max_len < 1) return 0;
-  return cache_attn_layout(h->view, S, T).total;
-}
-
-size_t ls_cache_attn_window_workspace_bytes(ls_cache_t h, int32_t S, int64_t T, int32_t max_new,
-                                            int64_t max_len, int64_t window, int64_t sinks) {
-  if (check_cache(h) != LS_OK || S < 1 || T < 1 || max_new < 1 || max_len < 1 || window < 1 || sinks < 0 ||
-      S > kMaxSeqs || T >= (int64_t(1) << 31) || max_len >= (int64_t(1) << 31))
-    return 0;
-  return cache_window_layout(h->view, S, T, max_new, max_len, window, sinks).total;
-}
-
-ls_status ls_cache_attn(ls_cache_t h, const ls_cache_attn_desc* d, void* workspace,
-                        size_t workspace_bytes, void* stream) {
-  NvtxRange nvtx_range("ls_cache_attn");
-  return attn_impl(h, d, nullptr, workspace, workspace_bytes, stream);
-}
-
-ls_status ls_cache_attn_window(ls_cache_t h, const ls_cache_attn_desc* d, int64_t window, int64_t sinks,
-                               void* workspace, size_t workspace_bytes, void* stream) {
-  NvtxRange nvtx_range("ls_cache_attn_window");
-  const int64_t sight[2] = {window, sinks};
-  return attn_impl(h, d, sight, workspace, workspace_bytes, stream);
-}
-
-}  // extern "C"
-
-namespace {
 
 // Attention of new tokens; sight: window and first tokens, or null.
 ls_status attn_impl(ls_cache_t h, const ls_cache_attn_desc* d, const int64_t* sight, void* workspace,

@@ -12,6 +12,25 @@
 
 using namespace ls;
 
+namespace ls {
+
+// Checks of the norm's part, and its arguments.
+int head_norm_args(const ls_head_norm* n, NormArgs* a) {
+  if (n == nullptr || !(n->eps > 0.0) || !std::isfinite(n->eps) || !std::isfinite(n->weight_offset) ||
+      !(static_cast<float>(n->eps) > 0.0f) || !std::isfinite(static_cast<float>(n->weight_offset)))
+    return LS_ERR_INVALID_ARGUMENT;
+  if (!aligned_n(n->q_weight, n->weight_fp32 ? 4 : 2) || !aligned_n(n->k_weight, n->weight_fp32 ? 4 : 2))
+    return LS_ERR_MISALIGNED;
+  a->wq = n->q_weight;
+  a->wk = n->k_weight;
+  a->w_fp32 = n->weight_fp32 != 0;
+  a->offset = static_cast<float>(n->weight_offset);
+  a->eps = static_cast<float>(n->eps);
+  return LS_OK;
+}
+
+}  // namespace ls
+
 extern "C" {
 
 size_t ls_policy_loss_workspace_bytes(int64_t T) {
@@ -172,13 +191,20 @@ ls_status ls_token_scores_bwd(const ls_token_scores_bwd_desc* d, void* stream) {
   return e == cudaSuccess ? LS_OK : static_cast<ls_status>(launch_failed(e, "token scores gradient launch"));
 }
 
-ls_status ls_rope(const ls_rope_desc* d, void* stream) {
-  NvtxRange nvtx_range("ls_rope");
-  if (d == nullptr || d->inv_freq == nullptr) return LS_ERR_INVALID_ARGUMENT;
+}  // extern "C"
+
+namespace {
+
+// The checks of a rotation, and its arguments but the status word; alone: without a rotation (rot_dim 0 and no
+// frequencies) there is something left to do.
+ls_status rope_args(const ls_rope_desc* d, bool alone, RopeArgs* out) {
+  if (d == nullptr) return LS_ERR_INVALID_ARGUMENT;
+  const bool turns = !alone || d->inv_freq != nullptr;
+  if (turns && d->inv_freq == nullptr) return LS_ERR_INVALID_ARGUMENT;
   if (d->T < 1 || d->Hq < 0 || d->Hk < 0 || d->Hq + d->Hk < 1) return LS_ERR_INVALID_ARGUMENT;
   if (d->Hq > 65536 || d->Hk > 65536 || d->T >= (int64_t(1) << 31)) return LS_ERR_UNSUPPORTED;
   if (d->D < 2 || d->D > 2 * kMaxRot || d->D % 2 != 0) return LS_ERR_UNSUPPORTED;
-  if (d->rot_dim < 2 || d->rot_dim > d->D || d->rot_dim % 2 != 0) return LS_ERR_INVALID_ARGUMENT;
+  if (turns ? (d->rot_dim < 2 || d->rot_dim > d->D || d->rot_dim % 2 != 0) : d->rot_dim != 0) return LS_ERR_INVALID_ARGUMENT;
   if ((d->Hq > 0 && (d->q == nullptr || d->q_out == nullptr)) ||
       (d->Hk > 0 && (d->k == nullptr || d->k_out == nullptr)))
     return LS_ERR_INVALID_ARGUMENT;
@@ -192,11 +218,8 @@ ls_status ls_rope(const ls_rope_desc* d, void* stream) {
   if (!aligned_n(d->q, 2) || !aligned_n(d->q_out, 2) || !aligned_n(d->k, 2) ||
       !aligned_n(d->k_out, 2) || !aligned_n(d->positions, 8))
     return LS_ERR_MISALIGNED;
-  RopeArgs a{};
-  if (!rope_turns(d->inv_freq, d->rot_dim, d->attn_factor, &a)) return LS_ERR_INVALID_ARGUMENT;
-  uint32_t* status = nullptr;
-  ls_status st = static_cast<ls_status>(enter_call(stream, &status));
-  if (st != LS_OK) return st;
+  RopeArgs& a = *out;
+  if (turns && !rope_turns(d->inv_freq, d->rot_dim, d->attn_factor, &a)) return LS_ERR_INVALID_ARGUMENT;
   a.T = d->T;
   a.Hq = d->Hq;
   a.Hk = d->Hk;
@@ -213,6 +236,21 @@ ls_status ls_rope(const ls_rope_desc* d, void* stream) {
   a.ks = d->k_stride;
   a.ko = static_cast<uint16_t*>(d->k_out);
   a.kos = d->k_out_stride;
+  return LS_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+ls_status ls_rope(const ls_rope_desc* d, void* stream) {
+  NvtxRange nvtx_range("ls_rope");
+  RopeArgs a{};
+  ls_status st = rope_args(d, false, &a);
+  if (st != LS_OK) return st;
+  uint32_t* status = nullptr;
+  st = static_cast<ls_status>(enter_call(stream, &status));
+  if (st != LS_OK) return st;
   a.status = status;
   cudaError_t e;
   {
@@ -220,6 +258,68 @@ ls_status ls_rope(const ls_rope_desc* d, void* stream) {
     e = injected_failure() ? cudaErrorLaunchFailure : launch_rope(a, static_cast<cudaStream_t>(stream));
   }
   return e == cudaSuccess ? LS_OK : static_cast<ls_status>(launch_failed(e, "rotary launch"));
+}
+
+ls_status ls_norm_rope(const ls_rope_desc* d, const ls_head_norm* n, void* stream) {
+  NvtxRange nvtx_range("ls_norm_rope");
+  NormArgs a{};
+  if (d != nullptr && d->inverse != 0) return LS_ERR_INVALID_ARGUMENT;
+  ls_status st = rope_args(d, true, &a.r);
+  if (st == LS_OK) st = static_cast<ls_status>(head_norm_args(n, &a));
+  if (st != LS_OK) return st;
+  uint32_t* status = nullptr;
+  st = static_cast<ls_status>(enter_call(stream, &status));
+  if (st != LS_OK) return st;
+  a.r.status = status;
+  cudaError_t e;
+  {
+    LaunchTimer t(LS_KERNEL_ROPE, static_cast<cudaStream_t>(stream));
+    e = injected_failure() ? cudaErrorLaunchFailure : launch_norm_rope(a, static_cast<cudaStream_t>(stream));
+  }
+  return e == cudaSuccess ? LS_OK : static_cast<ls_status>(launch_failed(e, "norm and rotary launch"));
+}
+
+size_t ls_norm_rope_bwd_workspace_bytes(int64_t T, int32_t D) {
+  if (T < 1 || D < 2 || D > 2 * kMaxRot) return 0;
+  return align_up(static_cast<size_t>(norm_rope_bwd_blocks(T)) * 2 * D * sizeof(float), 256);
+}
+
+ls_status ls_norm_rope_bwd(const ls_rope_desc* d, const ls_head_norm* n, const ls_head_norm_grad* g, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  NvtxRange nvtx_range("ls_norm_rope_bwd");
+  NormArgs a{};
+  if (g == nullptr || (d != nullptr && d->inverse != 0)) return LS_ERR_INVALID_ARGUMENT;
+  ls_status st = rope_args(d, true, &a.r);
+  if (st == LS_OK) st = static_cast<ls_status>(head_norm_args(n, &a));
+  if (st != LS_OK) return st;
+  if ((d->Hq > 0 && (g->q_in == nullptr || g->q_in_stride < static_cast<int64_t>(d->Hq) * d->D)) ||
+      (d->Hk > 0 && (g->k_in == nullptr || g->k_in_stride < static_cast<int64_t>(d->Hk) * d->D)))
+    return LS_ERR_INVALID_ARGUMENT;
+  // (a weight's gradient is of heads that are there)
+  if ((d->Hq == 0 && g->dq_weight != nullptr) || (d->Hk == 0 && g->dk_weight != nullptr)) return LS_ERR_INVALID_ARGUMENT;
+  const bool sums = g->dq_weight != nullptr || g->dk_weight != nullptr;
+  if (sums && (workspace == nullptr || workspace_bytes < ls_norm_rope_bwd_workspace_bytes(d->T, d->D)))
+    return LS_ERR_WORKSPACE;
+  if (!aligned_n(g->q_in, 2) || !aligned_n(g->k_in, 2) || !aligned_n(g->dq_weight, 4) || !aligned_n(g->dk_weight, 4) ||
+      (sums && !aligned16(workspace)))
+    return LS_ERR_MISALIGNED;
+  uint32_t* status = nullptr;
+  st = static_cast<ls_status>(enter_call(stream, &status));
+  if (st != LS_OK) return st;
+  a.r.inverse = 1;
+  a.r.status = status;
+  a.xq = static_cast<const uint16_t*>(g->q_in);
+  a.xqs = g->q_in_stride;
+  a.xk = static_cast<const uint16_t*>(g->k_in);
+  a.xks = g->k_in_stride;
+  a.partial = sums ? static_cast<float*>(workspace) : nullptr;
+  cudaError_t e;
+  {
+    LaunchTimer t(LS_KERNEL_ROPE, static_cast<cudaStream_t>(stream));
+    e = injected_failure() ? cudaErrorLaunchFailure
+                           : launch_norm_rope_bwd(a, g->dq_weight, g->dk_weight, static_cast<cudaStream_t>(stream));
+  }
+  return e == cudaSuccess ? LS_OK : static_cast<ls_status>(launch_failed(e, "norm and rotary gradient launch"));
 }
 
 ls_status ls_rope_freqs(int32_t rot_dim, double theta, int32_t scaling, double factor,

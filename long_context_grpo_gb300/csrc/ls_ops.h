@@ -116,6 +116,25 @@ struct RopeArgs {
 };
 cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s);
 
+// ----- norms of heads with the rotation (k_norm_rope.cu)
+struct NormArgs {
+  RopeArgs r;                 // rot = 0: norms alone; gradient: q, k are dy, qo, ko are dx, inverse
+  const void* wq;             // [D], or nullptr: 1
+  const void* wk;
+  int w_fp32;                 // else bf16
+  float offset;               // added to the weights
+  float eps;
+  // gradient: the inputs of the forward pass
+  const uint16_t* xq;
+  int64_t xqs;
+  const uint16_t* xk;
+  int64_t xks;
+  float* partial;             // workspace [blocks][2][D], or nullptr: no weight gradients
+};
+cudaError_t launch_norm_rope(const NormArgs& n, cudaStream_t s);
+int norm_rope_bwd_blocks(int64_t T);
+cudaError_t launch_norm_rope_bwd(const NormArgs& n, float* dwq, float* dwk, cudaStream_t s);
+
 // ----- page management (k_pages.cu); ws as cache_pages_ws_bytes() lays it out
 size_t cache_pages_ws_bytes(int64_t num_pages);
 constexpr int kMaxList = 1024;

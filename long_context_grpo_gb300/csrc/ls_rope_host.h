@@ -3,9 +3,13 @@
 
 #include <cmath>
 
+#include "../../include/longstraw.h"
 #include "ls_ops.h"
 
 namespace ls {
+
+// Checks of the norm's part of a call and its arguments (an ls_status; in ls_ops.cu).
+int head_norm_args(const ls_head_norm* n, NormArgs* a);
 
 // Fills a->turns, a->rot and a->factor; false if the factor is not finite or a
 // frequency is not within +-2^20 a token.
