@@ -6,11 +6,13 @@
 //     dx = r (u - x r^2 mean(u x)),   dw = sum over tokens and heads of g x r
 //
 // All in fp32, rounded once to bf16; angles as in k_rope.cu.  Bound by HBM: 2 bytes read (4 for the gradient)
-// and 2 written a value.  D / 16 lanes share a head, a lane two 16-byte chunks (in the half layout the two
-// whose values turn together), so that a head's sums take three shuffles at D = 128; a block's lanes keep
-// their chunks and walk the heads of its tokens, the next head's chunks on their way while this one's
-// are at work.  Weight gradients: a lane's 16 columns in registers over all heads that it walks, a row of
-// partial sums a block, summed in a fixed order by a second kernel (no atomics).
+// and 2 written a value.  A warp takes a token, or a part of its heads where there are few tokens: D / 16
+// lanes share a head, a lane two 16-byte chunks (in the half layout the two whose values turn together), so
+// that a head's sums take three shuffles at D = 128, and the lane's angles and weights stay in its registers
+// over all the heads that it walks (read from shared memory for every head they cost 181 us instead of
+// FWD for 32,768 tokens of 48 heads).  The next head's chunks are on their way while this one's are at work.
+// Weight gradients: a lane's 16 columns in registers over all heads and tokens that it walks, a row of partial
+// sums a block, summed in a fixed order by a second kernel (no atomics).
 // Element path (a warp a head) for rows that are not 16-byte aligned, D not a multiple of 16 or rot_dim
 // not a multiple of 16 (8 interleaved).
 #include "ls_internal.h"
@@ -22,9 +24,8 @@ namespace ls {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kMaxTok = 4;       // tokens of a block at a time
-constexpr int kBlocks = 4;       // blocks of an SM
-constexpr int kBwdBlocks = 2;    // of the gradient (a lane's sums and two heads' chunks: up to 128 registers)
+constexpr int kBlocks = 3;       // blocks of an SM
+constexpr int kBwdBlocks = 2;    // of the gradient (up to 128 registers)
 
 // Weight d of queries (which = 0) or keys (1), with the offset.
 __device__ __forceinline__ float weight_of(const NormArgs& a, int which, int d) {
@@ -81,53 +82,58 @@ __device__ __forceinline__ Chunks chunks_of(const RopeArgs& a, int j) {
   return c;
 }
 
-// x0, x1 turned in place by the token's angles.
-__device__ __forceinline__ void turn(const Chunks& c, bool interleaved, const float2* cs, float (&x0)[8], float (&x1)[8]) {
+// A lane's angles: of its 8 pairs (half layout), or 4 and 4 of its two chunks (interleaved).
+struct Angles {
+  float2 e[8];
+};
+__device__ __forceinline__ Angles load_angles(const Chunks& c, bool interleaved, const float2* cs) {
+  Angles a;
+#pragma unroll
+  for (int u = 0; u < 8; u += 2) {
+    const int p = interleaved ? (u < 4 ? c.p0 + u : c.p1 + u - 4) : c.p0 + u;
+    const bool turns = (interleaved && u >= 4 ? c.p1 : c.p0) >= 0;
+    const float4 r = turns ? *reinterpret_cast<const float4*>(cs + p) : make_float4(1.0f, 0.0f, 1.0f, 0.0f);
+    a.e[u] = make_float2(r.x, r.y);
+    a.e[u + 1] = make_float2(r.z, r.w);
+  }
+  return a;
+}
+
+// x0, x1 turned in place.
+__device__ __forceinline__ void turn(const Chunks& c, bool interleaved, const Angles& a, float (&x0)[8], float (&x1)[8]) {
   if (interleaved) {
     if (c.p0 >= 0) {
-      const float4* t = reinterpret_cast<const float4*>(cs + c.p0);
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const float4 r = t[u];
-        const float a0 = x0[4 * u], b0 = x0[4 * u + 1], a1 = x0[4 * u + 2], b1 = x0[4 * u + 3];
-        x0[4 * u] = a0 * r.x - b0 * r.y;
-        x0[4 * u + 1] = b0 * r.x + a0 * r.y;
-        x0[4 * u + 2] = a1 * r.z - b1 * r.w;
-        x0[4 * u + 3] = b1 * r.z + a1 * r.w;
+      for (int u = 0; u < 4; ++u) {
+        const float x = x0[2 * u], y = x0[2 * u + 1];
+        x0[2 * u] = x * a.e[u].x - y * a.e[u].y;
+        x0[2 * u + 1] = y * a.e[u].x + x * a.e[u].y;
       }
     }
     if (c.p1 >= 0) {
-      const float4* t = reinterpret_cast<const float4*>(cs + c.p1);
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const float4 r = t[u];
-        const float a0 = x1[4 * u], b0 = x1[4 * u + 1], a1 = x1[4 * u + 2], b1 = x1[4 * u + 3];
-        x1[4 * u] = a0 * r.x - b0 * r.y;
-        x1[4 * u + 1] = b0 * r.x + a0 * r.y;
-        x1[4 * u + 2] = a1 * r.z - b1 * r.w;
-        x1[4 * u + 3] = b1 * r.z + a1 * r.w;
+      for (int u = 0; u < 4; ++u) {
+        const float x = x1[2 * u], y = x1[2 * u + 1];
+        x1[2 * u] = x * a.e[4 + u].x - y * a.e[4 + u].y;
+        x1[2 * u + 1] = y * a.e[4 + u].x + x * a.e[4 + u].y;
       }
     }
   } else if (c.p0 >= 0) {
-    const float4* t = reinterpret_cast<const float4*>(cs + c.p0);
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const float4 r = t[u];
-      const float a0 = x0[2 * u], b0 = x1[2 * u], a1 = x0[2 * u + 1], b1 = x1[2 * u + 1];
-      x0[2 * u] = a0 * r.x - b0 * r.y;
-      x1[2 * u] = b0 * r.x + a0 * r.y;
-      x0[2 * u + 1] = a1 * r.z - b1 * r.w;
-      x1[2 * u + 1] = b1 * r.z + a1 * r.w;
+    for (int u = 0; u < 8; ++u) {
+      const float x = x0[u], y = x1[u];
+      x0[u] = x * a.e[u].x - y * a.e[u].y;
+      x1[u] = y * a.e[u].x + x * a.e[u].y;
     }
   }
 }
 
-__device__ __forceinline__ void load_weights(const float* w, const Chunks& c, float (&w0)[8], float (&w1)[8]) {
+// A lane's weights of queries (0) or keys (1).
+__device__ __forceinline__ void load_weights(const NormArgs& n, int which, const Chunks& c, float (&w0)[8], float (&w1)[8]) {
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const float4 a = *reinterpret_cast<const float4*>(w + c.c0 + 4 * u), b = *reinterpret_cast<const float4*>(w + c.c1 + 4 * u);
-    w0[4 * u] = a.x; w0[4 * u + 1] = a.y; w0[4 * u + 2] = a.z; w0[4 * u + 3] = a.w;
-    w1[4 * u] = b.x; w1[4 * u + 1] = b.y; w1[4 * u + 2] = b.z; w1[4 * u + 3] = b.w;
+  for (int u = 0; u < 8; ++u) {
+    w0[u] = weight_of(n, which, c.c0 + u);
+    w1[u] = weight_of(n, which, c.c1 + u);
   }
 }
 
@@ -146,67 +152,75 @@ __device__ __forceinline__ uint16_t* target(const RopeArgs& a, int64_t t, int h,
   return a.c.v + page + (h - a.Hk) * a.c.head_stride;
 }
 
-// The positions (an append's places too) and the angles of a block's tokens.
-__device__ __forceinline__ void prepare_tokens(const RopeArgs& a, int64_t t0, int nt, Token* tok, float2* cs) {
+// A block's one token: its position (an append's place too) and the angles, for the element path.
+__device__ __forceinline__ void prepare_token(const RopeArgs& a, int64_t t, Token* tok, float2* cs) {
   const int tid = threadIdx.x, half = a.rot >> 1;
   if (a.append) {
-    for (int i = tid >> 5; i < nt; i += kWarps) {
-      const Token r = locate(a, t0 + i, tid & 31);
-      if ((tid & 31) == 0) tok[i] = r;
+    if (tid < 32) {
+      const Token r = locate(a, t, tid);
+      if (tid == 0) *tok = r;
     }
-  } else if (tid < nt) {
-    tok[tid].pos = a.positions != nullptr ? a.positions[t0 + tid] : a.pos0 + t0 + tid;
-    tok[tid].page = 0;
+  } else if (tid == 0) {
+    tok->pos = a.positions != nullptr ? a.positions[t] : a.pos0 + t;
+    tok->page = 0;
   }
   __syncthreads();
-  for (int i = tid; i < nt * half; i += kThreads) {
-    const int k = i / half, p = i - k * half;
-    cs[i] = angle_of(a, tok[k].pos, p);
+  for (int p = tid; p < half; p += kThreads) cs[p] = angle_of(a, tok->pos, p);
+}
+
+// A warp's token: its place, and its angles in the warp's part of shared memory.
+__device__ __forceinline__ int64_t warp_token(const RopeArgs& a, int64_t t, int lane, float2* cs) {
+  Token r;
+  if (a.append) {
+    r = locate(a, t, lane);
+    r.pos = __shfl_sync(0xffffffffu, r.pos, 0);
+    r.page = __shfl_sync(0xffffffffu, r.page, 0);
+  } else {
+    r.pos = a.positions != nullptr ? a.positions[t] : a.pos0 + t;
+    r.page = 0;
   }
+  __syncwarp();
+  for (int p = lane; p < a.rot >> 1; p += 32) cs[p] = angle_of(a, r.pos, p);
+  __syncwarp();
+  return r.page;
 }
 
 template <int kLanes>
-__global__ void __launch_bounds__(kThreads, kBlocks) norm_rope_kernel(const __grid_constant__ NormArgs n, int tb) {
-  extern __shared__ __align__(16) float2 cs[];       // [token][pair], then weights [2][D]
-  __shared__ Token tok[kMaxTok];
-  constexpr int kSlots = kThreads / kLanes;
+__global__ void __launch_bounds__(kThreads, kBlocks) norm_rope_kernel(const __grid_constant__ NormArgs n, int parts, int per) {
+  extern __shared__ __align__(16) float2 angles[];       // [warp][pair]
+  constexpr int kSlots = 32 / kLanes;
   const RopeArgs& a = n.r;
-  const int tid = threadIdx.x, half = a.rot >> 1;
-  float* weights = reinterpret_cast<float*>(cs + ((tb * half + 1) & ~1));
-  const int slot = tid / kLanes, j = tid % kLanes;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+  const int64_t t = unit / parts;
+  if (t >= a.T) return;
+  const int H = a.Hq + a.Hk + (a.append ? a.Hk : 0), first = static_cast<int>(unit - t * parts) * per;
+  const int end = first + per < H ? first + per : H;
+  const int j = lane % kLanes;
   const bool mine = 16 * j < a.D;
   const Chunks c = chunks_of(a, j);
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tb;
-  const int nt = static_cast<int>(a.T - t0 < tb ? a.T - t0 : tb);
-  const int H = a.Hq + a.Hk + (a.append ? a.Hk : 0), total = nt * H;
+  float2* cs = angles + warp * ((a.rot / 2 + 1) & ~1);
 
-  int k = 0, h = slot;             // this lane's token and head
-  while (h >= H) {
-    h -= H;
-    ++k;
-  }
+  int h = first + lane / kLanes;
   uint4 v0 = make_uint4(0u, 0u, 0u, 0u), v1 = v0;
-  if (slot < total && mine) {
-    const uint16_t* p = source(a, t0 + k, h);
+  if (h < end && mine) {
+    const uint16_t* p = source(a, t, h);
     v0 = *reinterpret_cast<const uint4*>(p + c.c0);
     v1 = *reinterpret_cast<const uint4*>(p + c.c1);
   }
-  for (int i = tid; i < 2 * a.D; i += kThreads) weights[i] = weight_of(n, i >= a.D, i >= a.D ? i - a.D : i);
-  prepare_tokens(a, t0, nt, tok, cs);
-  __syncthreads();
-
+  const int64_t page = warp_token(a, t, lane, cs);
+  if (page < 0) return;
+  const Angles e = load_angles(c, a.interleaved, cs);
+  float w0[8], w1[8];
+  int which = -1;                  // whose weights these are
   const float inv_d = 1.0f / static_cast<float>(a.D);
 #pragma unroll 1
-  for (int i = slot; i - slot < total; i += kSlots) {
+  for (int i = first; i < end; i += kSlots) {
     const uint4 x0v = v0, x1v = v1;
-    const int kk = k, hh = h;
+    const int hh = h;
     h += kSlots;
-    while (h >= H) {
-      h -= H;
-      ++k;
-    }
-    if (i + kSlots < total && mine) {
-      const uint16_t* p = source(a, t0 + k, h);
+    if (h < end && mine) {
+      const uint16_t* p = source(a, t, h);
       v0 = *reinterpret_cast<const uint4*>(p + c.c0);
       v1 = *reinterpret_cast<const uint4*>(p + c.c1);
     }
@@ -220,23 +234,23 @@ __global__ void __launch_bounds__(kThreads, kBlocks) norm_rope_kernel(const __gr
       st = fmaf(x1[u], x1[u], st);
     }
     const float r = rsqrtf(fmaf(lane_sum<kLanes>(ss + st), inv_d, n.eps));
-    if (i >= total || !mine) continue;
-    const int64_t page = tok[kk].page;
-    if (page < 0) continue;
-    uint16_t* out = target(a, t0 + kk, hh, page);
+    if (hh >= end || !mine) continue;
+    uint16_t* out = target(a, t, hh, page);
     if (hh >= a.Hq + a.Hk) {         // a value: as it is
       *reinterpret_cast<uint4*>(out + c.c0) = x0v;
       *reinterpret_cast<uint4*>(out + c.c1) = x1v;
       continue;
     }
-    float w0[8], w1[8];
-    load_weights(weights + (hh < a.Hq ? 0 : a.D), c, w0, w1);
+    if (which != (hh >= a.Hq ? 1 : 0)) {
+      which = hh >= a.Hq ? 1 : 0;
+      load_weights(n, which, c, w0, w1);
+    }
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       x0[u] *= r * w0[u];
       x1[u] *= r * w1[u];
     }
-    turn(c, a.interleaved, cs + kk * half, x0, x1);
+    turn(c, a.interleaved, e, x0, x1);
     *reinterpret_cast<uint4*>(out + c.c0) = pack8(x0);
     *reinterpret_cast<uint4*>(out + c.c1) = pack8(x1);
   }
@@ -250,7 +264,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_any_kernel(const __grid_co
   const RopeArgs& a = n.r;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = a.rot >> 1;
   const int64_t t = blockIdx.x;
-  prepare_tokens(a, t, 1, tok, cs);
+  prepare_token(a, t, tok, cs);
   __syncthreads();
   if (tok[0].page < 0) return;
   const int H = a.Hq + a.Hk + (a.append ? a.Hk : 0);
@@ -289,20 +303,19 @@ __global__ void __launch_bounds__(kThreads) norm_rope_any_kernel(const __grid_co
 // --------------------------------------------------------------------------------------
 // Gradient.  a.r holds dy (q, k) and dx (qo, ko) and turns back (inverse).
 template <int kLanes>
-__global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(const __grid_constant__ NormArgs n, int tb) {
-  extern __shared__ __align__(16) float2 cs[];       // [token][pair], weights [2][D], sums [warps][D]
-  __shared__ Token tok[kMaxTok];
-  constexpr int kSlots = kThreads / kLanes;
+__global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(const __grid_constant__ NormArgs n) {
+  extern __shared__ __align__(16) float2 angles[];       // [warp][pair], sums [warp][D]
+  constexpr int kSlots = 32 / kLanes;
   const RopeArgs& a = n.r;
-  const int tid = threadIdx.x, half = a.rot >> 1, lane = tid & 31, warp = tid >> 5;
-  float* weights = reinterpret_cast<float*>(cs + ((tb * half + 1) & ~1));
-  float* sums = weights + 2 * a.D;
-  const int slot = tid / kLanes, j = tid % kLanes;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int half = (a.rot / 2 + 1) & ~1;
+  float2* cs = angles + warp * half;
+  float* sums = reinterpret_cast<float*>(angles + kWarps * half);
+  const int j = lane % kLanes;
   const bool mine = 16 * j < a.D;
   const Chunks c = chunks_of(a, j);
-  for (int i = tid; i < 2 * a.D; i += kThreads) weights[i] = weight_of(n, i >= a.D, i >= a.D ? i - a.D : i);
   const float inv_d = 1.0f / static_cast<float>(a.D);
-  const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * kWarps;
 
   // queries, then keys: a lane's sums are of one weight
 #pragma unroll 1
@@ -315,60 +328,44 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(con
     const int64_t dys = which ? a.ks : a.qs;
     uint16_t* dx = which ? a.ko : a.qo;
     const int64_t dxs = which ? a.kos : a.qos;
-    float acc0[8], acc1[8];
+    // a warp's units: a token, or a part of its heads, so that every warp has a few of them
+    int parts = static_cast<int>((4 * warps + a.T - 1) / a.T);
+    parts = parts < (H + kSlots - 1) / kSlots ? parts : (H + kSlots - 1) / kSlots;
+    const int per = ((H + parts - 1) / parts + kSlots - 1) / kSlots * kSlots;
+    parts = (H + per - 1) / per;
+    float w0[8], w1[8], acc0[8], acc1[8];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) acc0[u] = acc1[u] = 0.0f;
+    for (int u = 0; u < 8; ++u) acc0[u] = acc1[u] = w0[u] = w1[u] = 0.0f;
+    if (mine) load_weights(n, which, c, w0, w1);
+    uint4 g0v = make_uint4(0u, 0u, 0u, 0u), g1v = g0v, x0v = g0v, x1v = g0v;
+    auto load = [&](int64_t t, int h) {
+      const uint16_t* p = dy + t * dys + h * a.D;
+      g0v = *reinterpret_cast<const uint4*>(p + c.c0);
+      g1v = *reinterpret_cast<const uint4*>(p + c.c1);
+      p = x + t * xs + h * a.D;
+      x0v = *reinterpret_cast<const uint4*>(p + c.c0);
+      x1v = *reinterpret_cast<const uint4*>(p + c.c1);
+    };
 #pragma unroll 1
-    for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * tb; t0 < a.T; t0 += static_cast<int64_t>(gridDim.x) * tb) {
-      const int nt = static_cast<int>(a.T - t0 < tb ? a.T - t0 : tb);
-      const int total = nt * H;
-      int k = 0, h = slot;
-      while (h >= H) {
-        h -= H;
-        ++k;
-      }
-      uint4 g0v = none, g1v = none, x0v = none, x1v = none;
-      if (slot < total && mine) {
-        const uint16_t* p = dy + (t0 + k) * dys + h * a.D;
-        g0v = *reinterpret_cast<const uint4*>(p + c.c0);
-        g1v = *reinterpret_cast<const uint4*>(p + c.c1);
-        p = x + (t0 + k) * xs + h * a.D;
-        x0v = *reinterpret_cast<const uint4*>(p + c.c0);
-        x1v = *reinterpret_cast<const uint4*>(p + c.c1);
-      }
-      __syncthreads();             // the last tokens' angles are no longer read
-      prepare_tokens(a, t0, nt, tok, cs);
-      __syncthreads();
+    for (int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + warp; unit < a.T * parts; unit += warps) {
+      const int64_t t = unit / parts;
+      const int first = static_cast<int>(unit - t * parts) * per;
+      const int end = first + per < H ? first + per : H;
+      int h = first + lane / kLanes;
+      if (h < end && mine) load(t, h);
+      warp_token(a, t, lane, cs);
+      const Angles e = load_angles(c, a.interleaved, cs);
 #pragma unroll 1
-      for (int i = slot; i - slot < total; i += kSlots) {
+      for (int i = first; i < end; i += kSlots) {
         float g0[8], g1[8], x0[8], x1[8];
         unpack8(g0v, g0);
         unpack8(g1v, g1);
         unpack8(x0v, x0);
         unpack8(x1v, x1);
-        const int kk = k, hh = h;
+        const int hh = h;
         h += kSlots;
-        while (h >= H) {
-          h -= H;
-          ++k;
-        }
-        if (i + kSlots < total && mine) {
-          const uint16_t* p = dy + (t0 + k) * dys + h * a.D;
-          g0v = *reinterpret_cast<const uint4*>(p + c.c0);
-          g1v = *reinterpret_cast<const uint4*>(p + c.c1);
-          p = x + (t0 + k) * xs + h * a.D;
-          x0v = *reinterpret_cast<const uint4*>(p + c.c0);
-          x1v = *reinterpret_cast<const uint4*>(p + c.c1);
-        }
-        const bool valid = i < total && mine;
-        if (valid) turn(c, a.interleaved, cs + kk * half, g0, g1);
-        float w0[8], w1[8];
-        if (mine) {
-          load_weights(weights + which * a.D, c, w0, w1);
-        } else {
-#pragma unroll
-          for (int u = 0; u < 8; ++u) w0[u] = w1[u] = 0.0f;
-        }
+        if (h < end && mine) load(t, h);
+        turn(c, a.interleaved, e, g0, g1);
         float ss = 0.0f, su = 0.0f;
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
@@ -379,20 +376,19 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(con
         }
         ss = lane_sum<kLanes>(ss);
         su = lane_sum<kLanes>(su);
-        if (!valid) continue;
+        if (hh >= end || !mine) continue;
         const float r = rsqrtf(fmaf(ss, inv_d, n.eps));
         const float m = r * r * su * inv_d;
-        float d0[8], d1[8];
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
           acc0[u] = fmaf(g0[u], x0[u] * r, acc0[u]);
           acc1[u] = fmaf(g1[u], x1[u] * r, acc1[u]);
-          d0[u] = r * (g0[u] * w0[u] - x0[u] * m);
-          d1[u] = r * (g1[u] * w1[u] - x1[u] * m);
+          g0[u] = r * (g0[u] * w0[u] - x0[u] * m);
+          g1[u] = r * (g1[u] * w1[u] - x1[u] * m);
         }
-        uint16_t* out = dx + (t0 + kk) * dxs + hh * a.D;
-        *reinterpret_cast<uint4*>(out + c.c0) = pack8(d0);
-        *reinterpret_cast<uint4*>(out + c.c1) = pack8(d1);
+        uint16_t* out = dx + t * dxs + hh * a.D;
+        *reinterpret_cast<uint4*>(out + c.c0) = pack8(g0);
+        *reinterpret_cast<uint4*>(out + c.c1) = pack8(g1);
       }
     }
     if (n.partial == nullptr) continue;
@@ -438,7 +434,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_any_kernel(const __gri
     for (int d = lane; d < a.D; d += 32) acc[warp][d] = 0.0f;
     for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
       __syncthreads();
-      prepare_tokens(a, t, 1, tok, cs);
+      prepare_token(a, t, tok, cs);
       __syncthreads();
       for (int h = warp; h < H; h += kWarps) {
         const uint16_t* dy = which ? a.k + t * a.ks + h * a.D : a.q + t * a.qs + h * a.D;
@@ -528,23 +524,7 @@ int lanes_of(const NormArgs& n) {
   return l;
 }
 
-// Tokens of a block at a time: the least with which its lanes are busiest in the last round of heads too, while
-// that leaves every SM two rounds of blocks.
-int tokens_of(int64_t T, int H, int lanes) {
-  const int slots = kThreads / lanes;
-  int best = 1;
-  double most = 0.0;
-  for (int tb = 1; tb <= kMaxTok && (tb == 1 || T / tb >= 2ll * kBlocks * num_sms()); tb *= 2) {
-    const double busy = static_cast<double>(tb * H) / ((tb * H + slots - 1) / slots * slots);
-    if (busy > most + 0.02) {
-      most = busy;
-      best = tb;
-    }
-  }
-  return best;
-}
-
-size_t angles_bytes(const RopeArgs& a, int tb) { return static_cast<size_t>((tb * (a.rot / 2) + 1) & ~1) * sizeof(float2); }
+size_t angles_bytes(const RopeArgs& a, int warps) { return static_cast<size_t>((a.rot / 2 + 1) & ~1) * warps * sizeof(float2); }
 
 }  // namespace
 
@@ -555,15 +535,23 @@ cudaError_t launch_norm_rope(const NormArgs& n, cudaStream_t s) {
     norm_rope_any_kernel<<<static_cast<unsigned>(a.T), kThreads, angles_bytes(a, 1), s>>>(n);
     return cudaGetLastError();
   }
-  const int tb = tokens_of(a.T, a.Hq + a.Hk + (a.append ? a.Hk : 0), lanes);
-  const unsigned grid = static_cast<unsigned>((a.T + tb - 1) / tb);
-  const size_t smem = angles_bytes(a, tb) + 2 * static_cast<size_t>(a.D) * sizeof(float);
+  // heads of a warp: all of a token's, or fewer while that leaves SMs without two rounds of warps
+  const int H = a.Hq + a.Hk + (a.append ? a.Hk : 0), slots = 32 / lanes;
+  const int64_t want = 2ll * kBlocks * kWarps * num_sms();
+  int64_t parts = (want + a.T - 1) / a.T;
+  const int most = (H + slots - 1) / slots;
+  if (parts > most) parts = most;
+  const int per = static_cast<int>((H + parts - 1) / parts + slots - 1) / slots * slots;
+  parts = (H + per - 1) / per;
+  const unsigned grid = static_cast<unsigned>((a.T * parts + kWarps - 1) / kWarps);
+  const size_t smem = angles_bytes(a, kWarps);
+  const int np = static_cast<int>(parts);
   switch (lanes) {
-    case 1: norm_rope_kernel<1><<<grid, kThreads, smem, s>>>(n, tb); break;
-    case 2: norm_rope_kernel<2><<<grid, kThreads, smem, s>>>(n, tb); break;
-    case 4: norm_rope_kernel<4><<<grid, kThreads, smem, s>>>(n, tb); break;
-    case 8: norm_rope_kernel<8><<<grid, kThreads, smem, s>>>(n, tb); break;
-    default: norm_rope_kernel<16><<<grid, kThreads, smem, s>>>(n, tb); break;
+    case 1: norm_rope_kernel<1><<<grid, kThreads, smem, s>>>(n, np, per); break;
+    case 2: norm_rope_kernel<2><<<grid, kThreads, smem, s>>>(n, np, per); break;
+    case 4: norm_rope_kernel<4><<<grid, kThreads, smem, s>>>(n, np, per); break;
+    case 8: norm_rope_kernel<8><<<grid, kThreads, smem, s>>>(n, np, per); break;
+    default: norm_rope_kernel<16><<<grid, kThreads, smem, s>>>(n, np, per); break;
   }
   return cudaGetLastError();
 }
@@ -580,14 +568,13 @@ cudaError_t launch_norm_rope_bwd(const NormArgs& n, float* dwq, float* dwk, cuda
   if (lanes == 0) {
     norm_rope_bwd_any_kernel<<<grid, kThreads, angles_bytes(a, 1), s>>>(n);
   } else {
-    const int tb = 1;
-    const size_t smem = angles_bytes(a, tb) + (2 + kWarps) * static_cast<size_t>(a.D) * sizeof(float);
+    const size_t smem = angles_bytes(a, kWarps) + kWarps * static_cast<size_t>(a.D) * sizeof(float);
     switch (lanes) {
-      case 1: norm_rope_bwd_kernel<1><<<grid, kThreads, smem, s>>>(n, tb); break;
-      case 2: norm_rope_bwd_kernel<2><<<grid, kThreads, smem, s>>>(n, tb); break;
-      case 4: norm_rope_bwd_kernel<4><<<grid, kThreads, smem, s>>>(n, tb); break;
-      case 8: norm_rope_bwd_kernel<8><<<grid, kThreads, smem, s>>>(n, tb); break;
-      default: norm_rope_bwd_kernel<16><<<grid, kThreads, smem, s>>>(n, tb); break;
+      case 1: norm_rope_bwd_kernel<1><<<grid, kThreads, smem, s>>>(n); break;
+      case 2: norm_rope_bwd_kernel<2><<<grid, kThreads, smem, s>>>(n); break;
+      case 4: norm_rope_bwd_kernel<4><<<grid, kThreads, smem, s>>>(n); break;
+      case 8: norm_rope_bwd_kernel<8><<<grid, kThreads, smem, s>>>(n); break;
+      default: norm_rope_bwd_kernel<16><<<grid, kThreads, smem, s>>>(n); break;
     }
   }
   cudaError_t e = cudaGetLastError();
