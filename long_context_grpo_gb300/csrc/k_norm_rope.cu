@@ -8,9 +8,8 @@
 // All in fp32, rounded once to bf16; angles as in k_rope.cu.  Bound by HBM: 2 bytes read (4 for the gradient)
 // and 2 written a value.  A warp takes a token, or a part of its heads where there are few tokens: D / 16
 // lanes share a head, a lane two 16-byte chunks (in the half layout the two whose values turn together), so
-// that a head's sums take three shuffles at D = 128, and the lane's angles and weights stay in its registers
-// over all the heads that it walks (read from shared memory for every head they cost 181 us instead of
-// FWD for 32,768 tokens of 48 heads).  The next head's chunks are on their way while this one's are at work.
+// that a head's sums take three shuffles at D = 128, and the lane's weights stay in its registers over all
+// the heads that it walks.  The next head's chunks are on their way while this one's are at work.
 // Weight gradients: a lane's 16 columns in registers over all heads and tokens that it walks, a row of partial
 // sums a block, summed in a fixed order by a second kernel (no atomics).
 // Element path (a warp a head) for rows that are not 16-byte aligned, D not a multiple of 16 or rot_dim
@@ -24,7 +23,7 @@ namespace ls {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kBlocks = 3;       // blocks of an SM
+constexpr int kBlocks = 4;       // blocks of an SM
 constexpr int kBwdBlocks = 2;    // of the gradient (up to 128 registers)
 
 // Weight d of queries (which = 0) or keys (1), with the offset.
@@ -82,50 +81,38 @@ __device__ __forceinline__ Chunks chunks_of(const RopeArgs& a, int j) {
   return c;
 }
 
-// A lane's angles: of its 8 pairs (half layout), or 4 and 4 of its two chunks (interleaved).
-struct Angles {
-  float2 e[8];
-};
-__device__ __forceinline__ Angles load_angles(const Chunks& c, bool interleaved, const float2* cs) {
-  Angles a;
+// x0, x1 turned in place.  Lane j's pairs are 8 j .. 8 j + 7 in both layouts; in the warp's part of shared
+// memory two of them lie behind one another for all lanes of a head, [4][kLanes], so that a head's lanes read
+// neighbouring 16 bytes.  (volatile: held in registers over the loop they push others out of them)
+template <int kLanes>
+__device__ __forceinline__ void turn(const Chunks& c, bool interleaved, const float2* cs, int j, float (&x0)[8], float (&x1)[8]) {
+  if (c.p0 < 0 && c.p1 < 0) return;
+  const uint32_t at = smem_u32(cs) + j * 16;
 #pragma unroll
-  for (int u = 0; u < 8; u += 2) {
-    const int p = interleaved ? (u < 4 ? c.p0 + u : c.p1 + u - 4) : c.p0 + u;
-    const bool turns = (interleaved && u >= 4 ? c.p1 : c.p0) >= 0;
-    const float4 r = turns ? *reinterpret_cast<const float4*>(cs + p) : make_float4(1.0f, 0.0f, 1.0f, 0.0f);
-    a.e[u] = make_float2(r.x, r.y);
-    a.e[u + 1] = make_float2(r.z, r.w);
+  for (int u = 0; u < 4; ++u) {
+    float4 r;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(r.x), "=f"(r.y), "=f"(r.z), "=f"(r.w) : "r"(at + u * kLanes * 16));
+    if (!interleaved) {
+      const float a0 = x0[2 * u], b0 = x1[2 * u], a1 = x0[2 * u + 1], b1 = x1[2 * u + 1];
+      x0[2 * u] = a0 * r.x - b0 * r.y;
+      x1[2 * u] = b0 * r.x + a0 * r.y;
+      x0[2 * u + 1] = a1 * r.z - b1 * r.w;
+      x1[2 * u + 1] = b1 * r.z + a1 * r.w;
+    } else if (u < 2 || c.p1 >= 0) {
+      float* x = u < 2 ? x0 + 4 * u : x1 + 4 * (u - 2);
+      const float a0 = x[0], b0 = x[1], a1 = x[2], b1 = x[3];
+      x[0] = a0 * r.x - b0 * r.y;
+      x[1] = b0 * r.x + a0 * r.y;
+      x[2] = a1 * r.z - b1 * r.w;
+      x[3] = b1 * r.z + a1 * r.w;
+    }
   }
-  return a;
 }
-
-// x0, x1 turned in place.
-__device__ __forceinline__ void turn(const Chunks& c, bool interleaved, const Angles& a, float (&x0)[8], float (&x1)[8]) {
-  if (interleaved) {
-    if (c.p0 >= 0) {
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const float x = x0[2 * u], y = x0[2 * u + 1];
-        x0[2 * u] = x * a.e[u].x - y * a.e[u].y;
-        x0[2 * u + 1] = y * a.e[u].x + x * a.e[u].y;
-      }
-    }
-    if (c.p1 >= 0) {
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const float x = x1[2 * u], y = x1[2 * u + 1];
-        x1[2 * u] = x * a.e[4 + u].x - y * a.e[4 + u].y;
-        x1[2 * u + 1] = y * a.e[4 + u].x + x * a.e[4 + u].y;
-      }
-    }
-  } else if (c.p0 >= 0) {
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const float x = x0[u], y = x1[u];
-      x0[u] = x * a.e[u].x - y * a.e[u].y;
-      x1[u] = y * a.e[u].x + x * a.e[u].y;
-    }
-  }
+// Where pair p of a warp's token lies.
+template <int kLanes>
+__device__ __forceinline__ int angle_place(int p) {
+  return (((p & 7) >> 1) * kLanes + (p >> 3)) * 2 + (p & 1);
 }
 
 // A lane's weights of queries (0) or keys (1).
@@ -168,8 +155,8 @@ __device__ __forceinline__ void prepare_token(const RopeArgs& a, int64_t t, Toke
   for (int p = tid; p < half; p += kThreads) cs[p] = angle_of(a, tok->pos, p);
 }
 
-// A warp's token: its place, and its angles in the warp's part of shared memory.
-__device__ __forceinline__ int64_t warp_token(const RopeArgs& a, int64_t t, int lane, float2* cs) {
+// The place of a warp's token (found by the whole warp).
+__device__ __forceinline__ Token warp_token(const RopeArgs& a, int64_t t, int lane) {
   Token r;
   if (a.append) {
     r = locate(a, t, lane);
@@ -179,51 +166,66 @@ __device__ __forceinline__ int64_t warp_token(const RopeArgs& a, int64_t t, int 
     r.pos = a.positions != nullptr ? a.positions[t] : a.pos0 + t;
     r.page = 0;
   }
+  return r;
+}
+// Its angles in the warp's part of shared memory.
+template <int kLanes>
+__device__ __forceinline__ void warp_angles(const RopeArgs& a, int64_t pos, int lane, float2* cs) {
   __syncwarp();
-  for (int p = lane; p < a.rot >> 1; p += 32) cs[p] = angle_of(a, r.pos, p);
+  for (int p = lane; p < a.rot >> 1; p += 32) cs[angle_place<kLanes>(p)] = angle_of(a, pos, p);
   __syncwarp();
-  return r.page;
+}
+
+// A warp's unit of work: some heads of one token.
+struct Split {
+  int parts, per;       // units of a token, heads of a unit
+};
+struct Unit {
+  int64_t t;
+  int first, end;
+};
+__device__ __forceinline__ Unit unit_of(int64_t u, const Split& s, int H) {
+  Unit w;
+  w.t = u / s.parts;
+  w.first = static_cast<int>(u - w.t * s.parts) * s.per;
+  w.end = w.first + s.per < H ? w.first + s.per : H;
+  return w;
 }
 
 template <int kLanes>
-__global__ void __launch_bounds__(kThreads, kBlocks) norm_rope_kernel(const __grid_constant__ NormArgs n, int parts, int per) {
-  extern __shared__ __align__(16) float2 angles[];       // [warp][pair]
+__global__ void __launch_bounds__(kThreads, kBlocks) norm_rope_kernel(const __grid_constant__ NormArgs n, const Split split) {
+  extern __shared__ __align__(16) float2 angles[];       // [warp][4][kLanes] pairs of pairs
   constexpr int kSlots = 32 / kLanes;
   const RopeArgs& a = n.r;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
-  const int64_t t = unit / parts;
-  if (t >= a.T) return;
-  const int H = a.Hq + a.Hk + (a.append ? a.Hk : 0), first = static_cast<int>(unit - t * parts) * per;
-  const int end = first + per < H ? first + per : H;
+  if (unit >= a.T * split.parts) return;
+  const Unit w = unit_of(unit, split, a.Hq + a.Hk + (a.append ? a.Hk : 0));
   const int j = lane % kLanes;
   const bool mine = 16 * j < a.D;
   const Chunks c = chunks_of(a, j);
-  float2* cs = angles + warp * ((a.rot / 2 + 1) & ~1);
+  float2* cs = angles + warp * 8 * kLanes;
 
-  int h = first + lane / kLanes;
+  int h = w.first + lane / kLanes;
   uint4 v0 = make_uint4(0u, 0u, 0u, 0u), v1 = v0;
-  if (h < end && mine) {
-    const uint16_t* p = source(a, t, h);
+  auto load = [&]() {
+    const uint16_t* p = source(a, w.t, h);
     v0 = *reinterpret_cast<const uint4*>(p + c.c0);
     v1 = *reinterpret_cast<const uint4*>(p + c.c1);
-  }
-  const int64_t page = warp_token(a, t, lane, cs);
-  if (page < 0) return;
-  const Angles e = load_angles(c, a.interleaved, cs);
+  };
+  if (h < w.end && mine) load();
+  const Token tok = warp_token(a, w.t, lane);
+  if (tok.page < 0) return;
+  warp_angles<kLanes>(a, tok.pos, lane, cs);
   float w0[8], w1[8];
   int which = -1;                  // whose weights these are
   const float inv_d = 1.0f / static_cast<float>(a.D);
 #pragma unroll 1
-  for (int i = first; i < end; i += kSlots) {
+  for (int i = w.first; i < w.end; i += kSlots) {
     const uint4 x0v = v0, x1v = v1;
     const int hh = h;
     h += kSlots;
-    if (h < end && mine) {
-      const uint16_t* p = source(a, t, h);
-      v0 = *reinterpret_cast<const uint4*>(p + c.c0);
-      v1 = *reinterpret_cast<const uint4*>(p + c.c1);
-    }
+    if (h < w.end && mine) load();
     float x0[8], x1[8];
     unpack8(x0v, x0);
     unpack8(x1v, x1);
@@ -234,8 +236,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks) norm_rope_kernel(const __gr
       st = fmaf(x1[u], x1[u], st);
     }
     const float r = rsqrtf(fmaf(lane_sum<kLanes>(ss + st), inv_d, n.eps));
-    if (hh >= end || !mine) continue;
-    uint16_t* out = target(a, t, hh, page);
+    if (hh >= w.end || !mine) continue;
+    uint16_t* out = target(a, w.t, hh, tok.page);
     if (hh >= a.Hq + a.Hk) {         // a value: as it is
       *reinterpret_cast<uint4*>(out + c.c0) = x0v;
       *reinterpret_cast<uint4*>(out + c.c1) = x1v;
@@ -250,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) norm_rope_kernel(const __gr
       x0[u] *= r * w0[u];
       x1[u] *= r * w1[u];
     }
-    turn(c, a.interleaved, e, x0, x1);
+    turn<kLanes>(c, a.interleaved, cs, j, x0, x1);
     *reinterpret_cast<uint4*>(out + c.c0) = pack8(x0);
     *reinterpret_cast<uint4*>(out + c.c1) = pack8(x1);
   }
@@ -303,19 +305,19 @@ __global__ void __launch_bounds__(kThreads) norm_rope_any_kernel(const __grid_co
 // --------------------------------------------------------------------------------------
 // Gradient.  a.r holds dy (q, k) and dx (qo, ko) and turns back (inverse).
 template <int kLanes>
-__global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(const __grid_constant__ NormArgs n) {
-  extern __shared__ __align__(16) float2 angles[];       // [warp][pair], sums [warp][D]
+__global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(const __grid_constant__ NormArgs n, const Split split_q, const Split split_k) {
+  extern __shared__ __align__(16) float2 angles[];       // [warp][4][kLanes] pairs of pairs, sums [warp][D]
   constexpr int kSlots = 32 / kLanes;
   const RopeArgs& a = n.r;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int half = (a.rot / 2 + 1) & ~1;
-  float2* cs = angles + warp * half;
-  float* sums = reinterpret_cast<float*>(angles + kWarps * half);
+  float2* cs = angles + warp * 8 * kLanes;
+  float* sums = reinterpret_cast<float*>(angles + kWarps * 8 * kLanes);
   const int j = lane % kLanes;
   const bool mine = 16 * j < a.D;
   const Chunks c = chunks_of(a, j);
   const float inv_d = 1.0f / static_cast<float>(a.D);
   const int64_t warps = static_cast<int64_t>(gridDim.x) * kWarps;
+  pdl_launch_dependents();
 
   // queries, then keys: a lane's sums are of one weight
 #pragma unroll 1
@@ -328,11 +330,8 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(con
     const int64_t dys = which ? a.ks : a.qs;
     uint16_t* dx = which ? a.ko : a.qo;
     const int64_t dxs = which ? a.kos : a.qos;
-    // a warp's units: a token, or a part of its heads, so that every warp has a few of them
-    int parts = static_cast<int>((4 * warps + a.T - 1) / a.T);
-    parts = parts < (H + kSlots - 1) / kSlots ? parts : (H + kSlots - 1) / kSlots;
-    const int per = ((H + parts - 1) / parts + kSlots - 1) / kSlots * kSlots;
-    parts = (H + per - 1) / per;
+    const Split split = which ? split_k : split_q;
+    const int64_t units = a.T * split.parts;
     float w0[8], w1[8], acc0[8], acc1[8];
 #pragma unroll
     for (int u = 0; u < 8; ++u) acc0[u] = acc1[u] = w0[u] = w1[u] = 0.0f;
@@ -346,26 +345,35 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(con
       x0v = *reinterpret_cast<const uint4*>(p + c.c0);
       x1v = *reinterpret_cast<const uint4*>(p + c.c1);
     };
+    int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+    Unit w = unit_of(unit < units ? unit : 0, split, H);
+    int h = w.first + lane / kLanes;
+    if (unit < units && h < w.end && mine) load(w.t, h);
+    int64_t pos = a.positions != nullptr ? a.positions[w.t] : a.pos0 + w.t;
 #pragma unroll 1
-    for (int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + warp; unit < a.T * parts; unit += warps) {
-      const int64_t t = unit / parts;
-      const int first = static_cast<int>(unit - t * parts) * per;
-      const int end = first + per < H ? first + per : H;
-      int h = first + lane / kLanes;
-      if (h < end && mine) load(t, h);
-      warp_token(a, t, lane, cs);
-      const Angles e = load_angles(c, a.interleaved, cs);
+    for (; unit < units; unit += warps) {
+      const bool more = unit + warps < units;
+      Unit next = w;
+      int64_t next_pos = 0;
+      if (more) {
+        next = unit_of(unit + warps, split, H);
+        next_pos = a.positions != nullptr ? a.positions[next.t] : a.pos0 + next.t;
+      }
+      warp_angles<kLanes>(a, pos, lane, cs);
+      pos = next_pos;
 #pragma unroll 1
-      for (int i = first; i < end; i += kSlots) {
+      for (int i = w.first; i < w.end; i += kSlots) {
         float g0[8], g1[8], x0[8], x1[8];
         unpack8(g0v, g0);
         unpack8(g1v, g1);
         unpack8(x0v, x0);
         unpack8(x1v, x1);
         const int hh = h;
-        h += kSlots;
-        if (h < end && mine) load(t, h);
-        turn(c, a.interleaved, e, g0, g1);
+        // the next head of this unit, or the first one of the next
+        const bool last = i + kSlots >= w.end;
+        h = last ? next.first + lane / kLanes : h + kSlots;
+        if (mine && (last ? more && h < next.end : h < w.end)) load(last ? next.t : w.t, h);
+        turn<kLanes>(c, a.interleaved, cs, j, g0, g1);
         float ss = 0.0f, su = 0.0f;
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
@@ -376,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(con
         }
         ss = lane_sum<kLanes>(ss);
         su = lane_sum<kLanes>(su);
-        if (hh >= end || !mine) continue;
+        if (hh >= w.end || !mine) continue;
         const float r = rsqrtf(fmaf(ss, inv_d, n.eps));
         const float m = r * r * su * inv_d;
 #pragma unroll
@@ -386,10 +394,11 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(con
           g0[u] = r * (g0[u] * w0[u] - x0[u] * m);
           g1[u] = r * (g1[u] * w1[u] - x1[u] * m);
         }
-        uint16_t* out = dx + t * dxs + hh * a.D;
+        uint16_t* out = dx + w.t * dxs + hh * a.D;
         *reinterpret_cast<uint4*>(out + c.c0) = pack8(g0);
         *reinterpret_cast<uint4*>(out + c.c1) = pack8(g1);
       }
+      w = next;
     }
     if (n.partial == nullptr) continue;
     // the lanes of one column: within the warp, then the warps in order
@@ -486,23 +495,22 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_any_kernel(const __gri
   }
 }
 
-// The blocks' partial rows summed in order: a block 32 columns, a warp every kWarps-th row.
+// The blocks' partial rows summed in order: a block 8 columns, a thread of each every 32nd row.
 __global__ void __launch_bounds__(kThreads) norm_rope_sum_kernel(const float* partial, int blocks, int D, float* dwq, float* dwk) {
-  __shared__ float s[kWarps][32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int col = static_cast<int>(blockIdx.x) * 32 + lane;        // of [2][D]
+  __shared__ float s[32][8];
+  const int at = threadIdx.x >> 3, col = static_cast<int>(blockIdx.x) * 8 + (threadIdx.x & 7);        // of [2][D]
+  const bool want = col < 2 * D && (col < D ? dwq : dwk) != nullptr;
   pdl_wait();
   float x = 0.0f;
-  const bool want = col < 2 * D && (col < D ? dwq : dwk) != nullptr;
   if (want) {
-#pragma unroll 8
-    for (int b = warp; b < blocks; b += kWarps) x += __ldcg(partial + static_cast<int64_t>(b) * 2 * D + col);
+#pragma unroll 10
+    for (int b = at; b < blocks; b += 32) x += __ldcg(partial + static_cast<int64_t>(b) * 2 * D + col);
   }
-  s[warp][lane] = x;
+  s[at][threadIdx.x & 7] = x;
   __syncthreads();
-  if (warp > 0 || !want) return;
+  if (at > 0 || !want) return;
 #pragma unroll
-  for (int w = 1; w < kWarps; ++w) x += s[w][lane];
+  for (int i = 1; i < 32; ++i) x += s[i][threadIdx.x & 7];
   if (col < D) dwq[col] = x; else dwk[col - D] = x;
 }
 
@@ -524,7 +532,24 @@ int lanes_of(const NormArgs& n) {
   return l;
 }
 
-size_t angles_bytes(const RopeArgs& a, int warps) { return static_cast<size_t>((a.rot / 2 + 1) & ~1) * warps * sizeof(float2); }
+size_t angles_bytes(int lanes) { return static_cast<size_t>(8) * lanes * kWarps * sizeof(float2); }
+
+// How a token's heads become units: the least rounds of heads on any of the warps, a unit's angles counted as one.
+Split split_of(int64_t T, int H, int lanes, int64_t warps) {
+  const int slots = 32 / lanes, most = (H + slots - 1) / slots;
+  Split best = {1, most * slots};
+  double least = 0.0;
+  for (int p = 1; p <= most; ++p) {
+    const int per = ((H + p - 1) / p + slots - 1) / slots * slots;
+    const int64_t parts = (H + per - 1) / per;
+    const double cost = static_cast<double>((T * parts + warps - 1) / warps) * (per / slots + 1.0);
+    if (p == 1 || cost < least) {
+      least = cost;
+      best = {static_cast<int>(parts), per};
+    }
+  }
+  return best;
+}
 
 }  // namespace
 
@@ -532,26 +557,18 @@ cudaError_t launch_norm_rope(const NormArgs& n, cudaStream_t s) {
   const RopeArgs& a = n.r;
   const int lanes = lanes_of(n);
   if (lanes == 0) {
-    norm_rope_any_kernel<<<static_cast<unsigned>(a.T), kThreads, angles_bytes(a, 1), s>>>(n);
+    norm_rope_any_kernel<<<static_cast<unsigned>(a.T), kThreads, (a.rot / 2) * sizeof(float2), s>>>(n);
     return cudaGetLastError();
   }
-  // heads of a warp: all of a token's, or fewer while that leaves SMs without two rounds of warps
-  const int H = a.Hq + a.Hk + (a.append ? a.Hk : 0), slots = 32 / lanes;
-  const int64_t want = 2ll * kBlocks * kWarps * num_sms();
-  int64_t parts = (want + a.T - 1) / a.T;
-  const int most = (H + slots - 1) / slots;
-  if (parts > most) parts = most;
-  const int per = static_cast<int>((H + parts - 1) / parts + slots - 1) / slots * slots;
-  parts = (H + per - 1) / per;
-  const unsigned grid = static_cast<unsigned>((a.T * parts + kWarps - 1) / kWarps);
-  const size_t smem = angles_bytes(a, kWarps);
-  const int np = static_cast<int>(parts);
+  const Split sp = split_of(a.T, a.Hq + a.Hk + (a.append ? a.Hk : 0), lanes, static_cast<int64_t>(num_sms()) * kBlocks * kWarps);
+  const unsigned grid = static_cast<unsigned>((a.T * sp.parts + kWarps - 1) / kWarps);
+  const size_t smem = angles_bytes(lanes);
   switch (lanes) {
-    case 1: norm_rope_kernel<1><<<grid, kThreads, smem, s>>>(n, np, per); break;
-    case 2: norm_rope_kernel<2><<<grid, kThreads, smem, s>>>(n, np, per); break;
-    case 4: norm_rope_kernel<4><<<grid, kThreads, smem, s>>>(n, np, per); break;
-    case 8: norm_rope_kernel<8><<<grid, kThreads, smem, s>>>(n, np, per); break;
-    default: norm_rope_kernel<16><<<grid, kThreads, smem, s>>>(n, np, per); break;
+    case 1: norm_rope_kernel<1><<<grid, kThreads, smem, s>>>(n, sp); break;
+    case 2: norm_rope_kernel<2><<<grid, kThreads, smem, s>>>(n, sp); break;
+    case 4: norm_rope_kernel<4><<<grid, kThreads, smem, s>>>(n, sp); break;
+    case 8: norm_rope_kernel<8><<<grid, kThreads, smem, s>>>(n, sp); break;
+    default: norm_rope_kernel<16><<<grid, kThreads, smem, s>>>(n, sp); break;
   }
   return cudaGetLastError();
 }
@@ -566,20 +583,22 @@ cudaError_t launch_norm_rope_bwd(const NormArgs& n, float* dwq, float* dwk, cuda
   const int lanes = lanes_of(n);
   const unsigned grid = static_cast<unsigned>(norm_rope_bwd_blocks(a.T));
   if (lanes == 0) {
-    norm_rope_bwd_any_kernel<<<grid, kThreads, angles_bytes(a, 1), s>>>(n);
+    norm_rope_bwd_any_kernel<<<grid, kThreads, (a.rot / 2) * sizeof(float2), s>>>(n);
   } else {
-    const size_t smem = angles_bytes(a, kWarps) + kWarps * static_cast<size_t>(a.D) * sizeof(float);
+    const size_t smem = angles_bytes(lanes) + kWarps * static_cast<size_t>(a.D) * sizeof(float);
+    const int64_t warps = static_cast<int64_t>(grid) * kWarps;
+    const Split q = split_of(a.T, a.Hq > 0 ? a.Hq : 1, lanes, warps), k = split_of(a.T, a.Hk > 0 ? a.Hk : 1, lanes, warps);
     switch (lanes) {
-      case 1: norm_rope_bwd_kernel<1><<<grid, kThreads, smem, s>>>(n); break;
-      case 2: norm_rope_bwd_kernel<2><<<grid, kThreads, smem, s>>>(n); break;
-      case 4: norm_rope_bwd_kernel<4><<<grid, kThreads, smem, s>>>(n); break;
-      case 8: norm_rope_bwd_kernel<8><<<grid, kThreads, smem, s>>>(n); break;
-      default: norm_rope_bwd_kernel<16><<<grid, kThreads, smem, s>>>(n); break;
+      case 1: norm_rope_bwd_kernel<1><<<grid, kThreads, smem, s>>>(n, q, k); break;
+      case 2: norm_rope_bwd_kernel<2><<<grid, kThreads, smem, s>>>(n, q, k); break;
+      case 4: norm_rope_bwd_kernel<4><<<grid, kThreads, smem, s>>>(n, q, k); break;
+      case 8: norm_rope_bwd_kernel<8><<<grid, kThreads, smem, s>>>(n, q, k); break;
+      default: norm_rope_bwd_kernel<16><<<grid, kThreads, smem, s>>>(n, q, k); break;
     }
   }
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || n.partial == nullptr) return e;
-  return launch_after(norm_rope_sum_kernel, dim3(static_cast<unsigned>((2 * a.D + 31) / 32)), kThreads, 0, s,
+  return launch_after(norm_rope_sum_kernel, dim3(static_cast<unsigned>((2 * a.D + 7) / 8)), kThreads, 0, s,
                       static_cast<const float*>(n.partial), static_cast<int>(grid), a.D, dwq, dwk);
 }
 
