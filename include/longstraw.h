@@ -112,7 +112,8 @@ ls_status ls_prefix_prepare(const ls_prefix_desc* desc, ls_prefix_t* out, void* 
  * Holds for ls_replay_fwd/bwd, the packed and the blockwise replay (there the position is prefix_len + t); the
  * softmax, its gradients and the accumulators are as without it, with the other keys left out: they
  * are neither read nor, in the accumulators, written.  A forward and its backward have to be made
- * under the same window.  The prompt-only calls return LS_ERR_UNSUPPORTED.  window >= 1 and sinks >= 0,
+ * under the same window; the backward's workspace is asked for after it is set (it needs 256 bytes
+ * more).  The prompt-only calls return LS_ERR_UNSUPPORTED.  window >= 1 and sinks >= 0,
  * either may pass the sequence; window = 0 with sinks = 0 takes the window away.
  */
 ls_status ls_prefix_set_window(ls_prefix_t h, int64_t window, int64_t sinks);

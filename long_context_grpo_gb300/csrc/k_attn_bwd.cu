@@ -132,6 +132,9 @@ __host__ __device__ inline int window_kv_tiles(const AttnShape& sh, const Varlen
   return pt.first + pt.n_pt - pt.second + vl.kt0[vl.G];
 }
 
+// Heads whose tiles follow one another through a window: their queries share L2.
+constexpr int kHeadGroup = 4;
+
 // Flat unit u -> (kv head, 128-key tile).  A prompt tile is seen by every Q tile of every
 // packed response; a suffix tile of response b by that response's tiles from the first
 // one holding a query at or after its first key.
@@ -140,14 +143,25 @@ __device__ __forceinline__ KvUnit make_kv_unit(int u, const AttnShape& sh, const
   const int n_pt = static_cast<int>((sh.P + 127) / 128);
   KvUnit w;
   if constexpr (kWindow) {
+    // The first tokens' tiles of all heads, which every query sees; then kHeadGroup heads after one another, their
+    // prompt tiles from the last one down and their suffix tiles: most queries first, as far as it goes.
     const PromptTiles pt = prompt_tiles(sh, 0);
-    const int n_p = pt.first + n_pt - pt.second, n_all = n_p + vl.kt0[vl.G];
-    w.kv = u / n_all;
-    const int j = u - w.kv * n_all;
-    w.prompt = j < n_p;
-    int64_t last;      // the tile's last key and its first one, counted from the prompt's end
+    const int n_long = sh.Hkv * pt.first, n_p = n_pt - pt.second, n_all = n_p + vl.kt0[vl.G];
+    const bool head = u < n_long;
+    int j;
+    if (head) {
+      w.kv = u / pt.first;
+      j = u - w.kv * pt.first;
+    } else {
+      const int k = u - n_long, group = k / (kHeadGroup * n_all), y = k - group * kHeadGroup * n_all;
+      const int heads = sh.Hkv - group * kHeadGroup < kHeadGroup ? sh.Hkv - group * kHeadGroup : kHeadGroup;
+      j = y / heads;
+      w.kv = group * kHeadGroup + y - j * heads;
+    }
+    w.prompt = head || j < n_p;
+    int64_t last;      // the tile's last key, counted from the prompt's end
     if (w.prompt) {
-      w.key0 = 128 * (j < pt.first ? j : j - pt.first + pt.second);
+      w.key0 = 128 * (head ? j : n_pt - 1 - j);
       w.base = 0;
       w.R = 0;
       w.b = 0;
@@ -223,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                          const float* __restrict__ rowstats, float* __restrict__ dk_acc,
                          float* __restrict__ dv_acc, uint16_t* __restrict__ dk_suf,
                          uint16_t* __restrict__ dv_suf, const int suffix_to_acc,
-                         const __grid_constant__ Varlen vl, uint32_t* status) {
+                         const __grid_constant__ Varlen vl, unsigned* __restrict__ queue, uint32_t* status) {
   using C = DkdvCfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -231,6 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kNumBars);
   __shared__ int abort_flag;
+  __shared__ int unit_of[2];      // of a window: the CTA's units, as they are taken
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n_qt = kPacked ? vl.qt0[vl.G] : static_cast<int>((sh.R + sh.qt - 1) / sh.qt);
@@ -301,11 +316,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_prefetch_desc(&tm_do);
       uint32_t qit = 0, uc = 0, q_sent = 0;
       bool ok = true, kv_pending = false;
-      for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x, ++uc) {
-        const KvUnit w = make_kv_unit<kPacked, kNoSuffix, kWindow>(u, sh, vl);
+      // Through a window the units differ: a CTA takes the next one when it has done its own, and the one behind
+      // the last tells the other warps that there are no more.
+      int u = blockIdx.x;
+      for (; (kWindow || u < n_units) && ok; ++uc) {
         kv_pending = false;
         if (uc > 0) ok = mbar_wait_hint<kHintDkdvProducer>(&bars[C::kBarKVEmpty], (uc - 1) & 1u, status, vabort);
         if (!ok) break;
+        int after = u + static_cast<int>(gridDim.x);
+        if constexpr (kWindow) {
+          *static_cast<volatile int*>(&unit_of[uc & 1u]) = u;
+          if (u >= n_units) {
+            mbar_arrive(&bars[C::kBarKVFull]);
+            break;
+          }
+          after = static_cast<int>(gridDim.x + atomicAdd(queue, 1u));
+        }
+        const KvUnit w = make_kv_unit<kPacked, kNoSuffix, kWindow>(u, sh, vl);
         mbar_arrive_expect_tx(&bars[C::kBarKVFull], 2 * C::kTile);
         for (int b = 0; b < C::kBoxes; ++b) {
           tma_load_3d(smem + C::kOffK + b * 16384, w.prompt ? &tm_kp : &tm_ks,
@@ -344,6 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_3d(smem + C::kOffO + so * C::kTile + b * 16384, &tm_do,
                         &bars[C::kBarOFull + so], 64 * b, w.kv * sh.g, qrow);
         }
+        u = after;
       }
       if (!ok) {
         *vabort = 1;
@@ -418,10 +446,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_commit_w(&bars[C::kBarOEmpty + it % C::kNO]);
         }
       };
-      for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x, ++uc) {
-        const KvUnit w = make_kv_unit<kPacked, kNoSuffix, kWindow>(u, sh, vl);
+      for (int u = blockIdx.x; (kWindow || u < n_units) && ok; u += gridDim.x, ++uc) {
         ok = mbar_wait_hint<kHintDkdvMma>(&bars[C::kBarKVFull], uc & 1u, status, vabort);
         if (!ok) break;
+        if constexpr (kWindow) {
+          u = *static_cast<volatile int*>(&unit_of[uc & 1u]);
+          if (u >= n_units) break;
+        }
+        const KvUnit w = make_kv_unit<kPacked, kNoSuffix, kWindow>(u, sh, vl);
         tc_fence_after();
         ok = issue_s(qit) && issue_dp(qit);
         for (int li = 0; li < w.n && ok; ++li) {
@@ -449,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         qit += w.n;
         mma_commit_w(&bars[C::kBarAccDone]);
-        if (u + static_cast<int>(gridDim.x) < n_units) mma_commit_w(&bars[C::kBarKVEmpty]);
+        if (kWindow || u + static_cast<int>(gridDim.x) < n_units) mma_commit_w(&bars[C::kBarKVEmpty]);
       }
       if (!ok) *vabort = 1;
       mma_commit_w(&bars[C::kBarDrain]);
@@ -464,7 +496,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float c2 = sh.scale * kLog2e;
     uint32_t qit = 0u, uc = 0u, n_tiles = 0u;
     bool ok = true;
-    for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x, ++uc) {
+    for (int u = blockIdx.x; (kWindow || u < n_units) && ok; u += gridDim.x, ++uc) {
+      if constexpr (kWindow) {
+        ok = mbar_wait_hint<kHintDkdvSoftmax>(&bars[C::kBarKVFull], uc & 1u, status, vabort);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        u = *static_cast<volatile int*>(&unit_of[uc & 1u]);
+        if (u >= n_units) break;
+      }
       const KvUnit w = make_kv_unit<kPacked, kNoSuffix, kWindow>(u, sh, vl);
       const int key = w.key0 + row;
       QWalk walk;
@@ -1186,7 +1225,7 @@ cudaError_t launch_dkdv_d(const BwdArgs& a, cudaStream_t s) {
   if (n_units < grid) grid = static_cast<int>(n_units);
   attn_bwd_dkdv_kernel<D, kPacked, kNoSuffix, kWindow><<<grid, kThreads, C::kSmem, s>>>(
       *a.tm_kp, *a.tm_vp, a.tm_ks, a.tm_vs, a.tm_q, a.tm_do, a.sh, a.rowstats, a.dk_acc,
-      a.dv_acc, a.dk_suf, a.dv_suf, a.suffix_to_acc, a.vl, a.status);
+      a.dv_acc, a.dk_suf, a.dv_suf, a.suffix_to_acc, a.vl, a.queue, a.status);
   return cudaGetLastError();
 }
 

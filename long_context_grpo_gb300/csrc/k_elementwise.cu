@@ -67,7 +67,8 @@ __global__ void __launch_bounds__(kThreads) scale_kernel(float4* acc, size_t n4,
 __global__ void __launch_bounds__(kThreads) bwd_prep_kernel(const uint4* o, const uint4* d_out,
                                                            const float* lse, float* rowstats,
                                                            AttnShape sh,
-                                                           const __grid_constant__ Varlen vl) {
+                                                           const __grid_constant__ Varlen vl, unsigned* queue) {
+  if (queue != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *queue = 0u;
   const int lane = threadIdx.x & 31;
   const int64_t warps_total = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
   const int per_row = sh.D / 8;   // 8 or 16 lanes, 8 bf16 each
@@ -272,11 +273,11 @@ cudaError_t launch_f32_to_bf16(const float* in, void* out, size_t count, cudaStr
 
 cudaError_t launch_bwd_prep(const uint16_t* o, const uint16_t* d_out, const float* lse,
                             float* rowstats, const AttnShape& sh, const Varlen& vl,
-                            cudaStream_t s) {
+                            unsigned* queue, cudaStream_t s) {
   const size_t slots = static_cast<size_t>(sh.Hkv) * vl.qt0[vl.G] * 128;
   bwd_prep_kernel<<<grid_for(slots * 32), kThreads, 0, s>>>(
       reinterpret_cast<const uint4*>(o), reinterpret_cast<const uint4*>(d_out), lse, rowstats, sh,
-      vl);
+      vl, queue);
   return cudaGetLastError();
 }
 

@@ -267,7 +267,9 @@ ls_status check_cu(int32_t G, const int64_t* cu) {
 size_t bwd_workspace_bytes(ls_prefix_t h, int32_t G, const int64_t* cu) {
   int64_t n_qt = 0;
   for (int b = 0; b < G; ++b) n_qt += (cu[b + 1] - cu[b] + h->shape.qt - 1) / h->shape.qt;
-  return align_up(static_cast<size_t>(h->shape.Hkv) * n_qt * 256 * sizeof(float), 256);
+  // (through a window the units' queue lies behind the row statistics)
+  return align_up(static_cast<size_t>(h->shape.Hkv) * n_qt * 256 * sizeof(float), 256) +
+         (h->shape.window > 0 ? 256 : 0);
 }
 
 // Replay forward of the packed responses cu (G of them, total rows cu[G]) against the first
@@ -361,6 +363,8 @@ ls_status replay_bwd_impl(ls_prefix_t h, int64_t P_eff, int32_t G, const int64_t
   if (st != LS_OK) return st;
   float* rowstats = static_cast<float*>(workspace);
   a.rowstats = rowstats;
+  if (sh.window > 0)
+    a.queue = reinterpret_cast<unsigned*>(static_cast<uint8_t*>(workspace) + bwd_workspace_bytes(h, G, cu) - 256);
   a.dq = static_cast<uint16_t*>(dq);
   a.dk_suf = static_cast<uint16_t*>(dk_suffix);
   a.dv_suf = static_cast<uint16_t*>(dv_suffix);
@@ -374,7 +378,7 @@ ls_status replay_bwd_impl(ls_prefix_t h, int64_t P_eff, int32_t G, const int64_t
   {
     LaunchTimer t(LS_KERNEL_BWD_PREP, s);
     e = injected_failure() ? cudaErrorLaunchFailure : launch_bwd_prep(static_cast<const uint16_t*>(o), static_cast<const uint16_t*>(d_out), lse,
-                        rowstats, sh, a.vl, s);
+                        rowstats, sh, a.vl, a.queue, s);
   }
   if (e != cudaSuccess) return cuda_fail(e, "replay backward prep launch");
   {

@@ -179,15 +179,16 @@ struct BwdArgs {
   float* dv_acc;
   int suffix_to_acc;          // suffix key gradients are added into rows P + key of dk/dv_acc
   int no_suffix;              // 1: prompt keys only (one shard of a context-parallel prompt)
+  unsigned* queue;            // workspace of a window: units taken by the dK/dV kernel (zero before it)
   uint32_t* status;
 };
 // Row statistics of every 128-row Q tile slot (kv, f, r) -- f the flat tile index over the
 // packed responses, tile i = f - qt0[b] of response b, r = (t - i qt) g + h - kv g: valid
 // rows get LSE log2 e and Delta = sum_d dO O; padding rows and rows past the response's
-// end get (+inf, 0) so their softmax probabilities are exactly 0.
+// end get (+inf, 0) so their softmax probabilities are exactly 0.  queue (or null) is set to zero.
 cudaError_t launch_bwd_prep(const uint16_t* o, const uint16_t* d_out, const float* lse,
                             float* rowstats, const AttnShape& sh, const Varlen& vl,
-                            cudaStream_t s);
+                            unsigned* queue, cudaStream_t s);
 cudaError_t launch_attn_bwd_dkdv(const BwdArgs& a, cudaStream_t s);
 cudaError_t launch_attn_bwd_dq(const BwdArgs& a, cudaStream_t s);
 
