@@ -7,14 +7,17 @@
 //   d x_v = (d_logp (1[v = y] - p_v) - d_entropy p_v (log p_v + entropy)) / t
 //
 // scores_kernel: a CTA a row, or a cluster of them where there are few rows, each with a slice; one read
-//   of the row.  A thread keeps a running maximum, how many logits equal it, the compensated sum of
-//   the others' exponentials and sum e z (fp32, joined across the CTA; the last logarithm in fp64): a
-//   token with nearly all of the probability keeps the digits of what is left.  For the alternatives the largest logit of every 32
-//   neighbours stays in shared memory: the k best logits of a row (ties to the lowest index) lie in the k
-//   groups with the largest maxima (ties to the lowest group), so that only these are looked at again.
-//   Proof: were one of them in another group, each of the k groups before that one would hold a
-//   logit before it.
-// scores_bwd_kernel: one pass, a block 4,096 logits of a row.
+//   of the row.  A thread keeps the sum of exponentials (compensated) and sum e z in fp32, relative to its warp's
+//   largest logit, and how many equal it; joined across the CTA, the last logarithm in
+//   fp64: a token with nearly all of the probability keeps the digits of what is left.  For the alternatives
+//   the largest logit of every 32 neighbours stays in shared memory: the k best logits of a row (ties to the
+//   lowest index) lie in the k groups with the largest maxima (ties to the lowest group), so that only these are
+//   looked at again.  Proof: were one of them in another group, each of the k groups before that one
+//   would hold a logit before it.
+//   Bound by HBM without alternatives (4,096 rows of 151,936: 190 us, 6.5 TB/s); with 20 of them (228 us) a row's
+//   end, a chain of eight barriers, keeps a ninth of the SM's CTAs from reading.  128 threads and nine CTAs an SM: with
+//   256 threads 281 us, one CTA an SM fed by bulk copies, with warps of its own for the alternatives, 291.
+// scores_bwd_kernel: one pass, a block 4,096 logits of a row (1,279 rows of 151,936: 110 us, 7.05 TB/s).
 #include <type_traits>
 
 #include "ls_internal.h"
@@ -164,21 +167,263 @@ __device__ __forceinline__ float chunk_entropy(const uint4 (&v)[kUnroll], float 
   return es;
 }
 
-// What a CTA knows of its slice: largest logit (as a whole number), sum, sum e z, its best logits.
+// A warp's sums of what it has read, relative to its own maximum m (one a warp).
+struct Sums {
+  float m, r, ones, hi, lo, e;
+  uint32_t top2;             // a lane's largest logits of even and odd places, a NaN if there is one
+  uint32_t group;            // the largest of the groups that it has stored, as select_best counts them
+};
+
+__device__ __forceinline__ Sums no_sums() { return {-INFINITY, -INFINITY, 0.0f, 0.0f, 0.0f, 0.0f, kNegInf2, 0u}; }
+
+// A step of kN threads: thread tid has logits base + 8 kN u + 8 tid .. + 7 of a slice of len in v[u].
+template <bool kTop, int kN>
+__device__ __forceinline__ void add_step(Sums& s, const uint4 (&v)[kUnroll], float scale2, int base, int tid, int len,
+                                         uint16_t* groups) {
+  uint32_t g[kUnroll / 2];      // the largest of each eight, two a register
+#pragma unroll
+  for (int u = 0; u < kUnroll; u += 2) {
+    const uint32_t p = max2(max2(v[u].x, v[u].y), max2(v[u].z, v[u].w));
+    const uint32_t q = max2(max2(v[u + 1].x, v[u + 1].y), max2(v[u + 1].z, v[u + 1].w));
+    g[u / 2] = max2(__byte_perm(p, q, 0x5410), __byte_perm(p, q, 0x7632));
+  }
+  if constexpr (kTop) {
+    // of 32 neighbours: four lanes together
+#pragma unroll
+    for (int i = 0; i < kUnroll / 2; ++i) {
+      g[i] = max2(g[i], __shfl_xor_sync(0xffffffffu, g[i], 1));
+      g[i] = max2(g[i], __shfl_xor_sync(0xffffffffu, g[i], 2));
+    }
+    const int u = tid & 3;
+    const uint32_t w = u & 2 ? g[1] : g[0];
+    const int at = (base + u * kN * 8 + tid * 8) >> 5;
+    if (at * 32 < len) {
+      const uint32_t o = order(u & 1 ? w >> 16 : w & 0xFFFFu);
+      groups[at] = static_cast<uint16_t>(o);
+      s.group = max(s.group, (o << 16) | (0xFFFFu - static_cast<uint32_t>(at)));
+    }
+  }
+  const uint32_t t2 = max2(g[0], g[1]);
+  s.top2 = max2(s.top2, t2);
+  // (one maximum a warp: a lane's own would grow in most steps of some lane)
+  const float cm = warp_max(fmaxf(lo_bf16(t2), hi_bf16(t2)));
+  if (cm > s.m) {
+    rebase(cm, scale2, s.m, s.r, s.ones, s.hi, s.lo, s.e);
+    s.m = cm;
+  }
+  // peak: the maximum is among these; its exponentials, 1 each, are counted and not added
+  const bool peak = cm == s.m;
+  float sum, es;
+  if (!(fabsf(s.r) < kFar)) {
+    add_chunk<true, true>(v, s.m, s.r, scale2, s.ones, sum, es);
+  } else if (peak) {
+    add_chunk<true, false>(v, s.m, s.r, scale2, s.ones, sum, es);
+  } else {
+    add_chunk<false, false>(v, s.m, s.r, scale2, s.ones, sum, es);
+  }
+  if (!(es == es)) es = chunk_entropy(v, s.m, s.r, scale2);     // 0 x -inf
+  two_sum_acc(s.hi, s.lo, sum);
+  s.e += es;
+}
+
+// Logits [begin, end) of a row by kThreads threads, tid of them; groups: the largest logit of every 32, as a whole number.
+template <bool kVec, bool kTop>
+__device__ __forceinline__ Sums stream(const ScoresArgs& a, const uint16_t* x, int64_t begin, int64_t end, int tid,
+                                       uint16_t* groups) {
+  const int len = end > begin ? static_cast<int>(end - begin) : 0;
+  Sums w = no_sums();
+  for (int base = 0; base < len; base += kStep) {
+    // the next step on its way to L2 (one step ahead: 231 us with 20 alternatives, two 233, none 251)
+    if (kVec && tid == 0 && base + 2 * kStep <= len) bulk_prefetch_l2(x + begin + base + kStep, kStep * 2);
+    uint4 v[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int at = base + u * kThreads * 8 + tid * 8;
+      v[u] = kVec && base + kStep <= len ? __ldg(reinterpret_cast<const uint4*>(x + begin + at)) : load8<kVec>(x, begin + at, end);
+    }
+    add_step<kTop, kThreads>(w, v, a.scale2, base, tid, len, groups);
+  }
+  return w;
+}
+
+// The warp's sums over its lanes, relative to `peak`.
+__device__ __forceinline__ void add_lanes(Sums& w, float peak, float scale2) {
+  if (w.m != peak) rebase(peak, scale2, w.m, w.r, w.ones, w.hi, w.lo, w.e);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    const float h = __shfl_xor_sync(0xffffffffu, w.hi, off);
+    w.lo += __shfl_xor_sync(0xffffffffu, w.lo, off);
+    two_sum_acc(w.hi, w.lo, h);
+    w.e += __shfl_xor_sync(0xffffffffu, w.e, off);
+    w.ones += __shfl_xor_sync(0xffffffffu, w.ones, off);
+  }
+}
+
+// Largest logit of a warp's part as a whole number.
+__device__ __forceinline__ uint32_t warp_top(const Sums& w) {
+  return __reduce_max_sync(0xffffffffu, max(order(w.top2 & 0xFFFFu), order(w.top2 >> 16)));
+}
+
+// What a part of a row has come to: its largest logit (as a whole number), sums relative to it.
 struct Slice {
   uint32_t top;
   float ones, hi, lo, e;
 };
+// A row from its parts, joined in order (one thread).
+struct Row {
+  uint32_t top;
+  bool none;       // a NaN or an infinite logit, or none that is larger than -inf: no distribution
+  double lns;      // log of the sum relative to the largest logit
+};
+__device__ __forceinline__ Row finish_row(const ScoresArgs& a, const Slice* parts, int n_parts, int64_t row, int y, float xy) {
+  uint32_t all = 0u;
+  for (int i = 0; i < n_parts; ++i) all = max(all, parts[i].top);
+  const float peak = value_of(all);
+  float n = 0.0f, h = 0.0f, l = 0.0f, w = 0.0f;
+  for (int i = 0; i < n_parts; ++i) {
+    Slice s = parts[i];
+    const float from = value_of(s.top);
+    float base = reference(from, a.scale2);
+    if (from != peak) rebase(peak, a.scale2, from, base, s.ones, s.hi, s.lo, s.e);
+    n += s.ones;
+    two_sum_acc(h, l, s.hi);
+    l += s.lo;
+    w += s.e;
+  }
+  Row out;
+  out.top = all;
+  out.none = all >= 0xFF80u || all <= 0x007Fu;
+  // the reference's rounding goes out again: z from the peak itself is z + off
+  const float base = reference(peak, a.scale2);
+  const double off = fabsf(base) < kFar ? static_cast<double>(base) - static_cast<double>(peak) * a.scale2 : 0.0;
+  const double back = fabs(off) < 0x1p-12 ? 1.0 + off * kLn2 : exp2(off);
+  const double rest = (static_cast<double>(h) + static_cast<double>(l)) * back, S = n + rest;
+  out.lns = out.none ? static_cast<double>(NAN) : log1p(n - 1.0 + rest);
+  a.logp[row] = y < 0 ? 0.0f : static_cast<float>((static_cast<double>(xy) - peak) * a.scale - out.lns);
+  if (a.lse != nullptr) a.lse[row] = static_cast<float>(peak * a.scale + out.lns);
+  if (a.entropy != nullptr) {
+    const double ent = out.lns - kLn2 * (w * back + off * rest) / S;
+    a.entropy[row] = ent < 0.0 ? 0.0f : static_cast<float>(ent);
+  }
+  return out;
+}
+
+// The row's given token (-1: out of range, reported) and its logit.
+__device__ __forceinline__ int given_token(const ScoresArgs& a, int64_t row, float* xy) {
+  const int y = a.ids[row];
+  *xy = 0.0f;
+  if (y < 0 || y >= a.V) {
+    set_device_status(a.status, DEV_BAD_INDEX);
+    return -1;
+  }
+  *xy = lo_bf16(a.logits[row * a.ldx + y]);
+  return y;
+}
+
+// The k largest logits of [begin, begin + len) of a row, largest first, equal ones the lowest index first, by kThreads
+// threads: keys (order, then the lowest index) to best, 0 where there are fewer.  groups: the largest of every 32.
+// mine: the largest group that the thread has stored while it read the row.  scratch: found [32 k], then list [list_size], then chosen [k].
+struct Select {
+  uint32_t key[kThreads];
+  uint32_t low, cut, n[2];
+};
+__host__ __device__ __forceinline__ int select_list(int64_t len, int k) { return k * static_cast<int>((len / 32 + kThreads) / kThreads); }
+__host__ __device__ __forceinline__ size_t select_scratch(int64_t len, int k) {
+  return 32 * static_cast<size_t>(k) * 8 + static_cast<size_t>(select_list(len, k)) * 4 + static_cast<size_t>(k) * 4;
+}
+template <class Sync>
+__device__ __forceinline__ void select_best(const uint16_t* x, int64_t begin, int len, const uint16_t* groups, int k,
+                                            unsigned long long* best, uint8_t* scratch, int list_size, Select& s, int tid,
+                                            uint32_t mine, Sync sync) {
+  const int n = (len + 31) >> 5, lane = tid & 31, warp = tid >> 5;
+  unsigned long long* found = reinterpret_cast<unsigned long long*>(scratch);
+  uint32_t* list = reinterpret_cast<uint32_t*>(found + 32 * k);
+  uint32_t* chosen = list + list_size;
+  // groups as whole numbers: maximum, then the lowest index; 0: none
+  auto key = [&](int g) { return (static_cast<uint32_t>(groups[g]) << 16) | (0xFFFFu - static_cast<uint32_t>(g)); };
+  if (tid == 0) {
+    s.low = s.cut = 0u;
+    s.n[0] = s.n[1] = 0u;
+  }
+  s.key[tid] = mine;
+  if (tid < k) best[tid] = 0ull;
+  sync();
+  // the k threads with the largest groups hold the k largest groups
+  int rank = 0;
+#pragma unroll 8
+  for (int i = 0; i < kThreads; i += 4) {
+    const uint4 o = *reinterpret_cast<const uint4*>(s.key + i);
+    rank += (o.x > mine) + (o.y > mine) + (o.z > mine) + (o.w > mine);
+  }
+  if (rank == k - 1) s.low = mine;
+  sync();
+  if (rank < k && mine > 0u) {
+    const uint32_t low = s.low;
+    // (the groups that this thread has stored)
+#pragma unroll 4
+    for (int g = (tid & 3) * (kThreads / 4) + (tid >> 2); g < n; g += kThreads) {
+      const uint32_t o = key(g);
+      if (o >= low) list[atomicAdd(&s.n[0], 1u)] = o;
+    }
+  }
+  sync();
+  const int listed = static_cast<int>(s.n[0]);
+  for (int i = tid; i < listed; i += kThreads) {
+    const uint32_t o = list[i];
+    int r = 0;
+#pragma unroll 4
+    for (int j = 0; j < listed; ++j) r += list[j] > o;
+    if (r < k) chosen[r] = 0xFFFFu - (o & 0xFFFFu);
+    if (r == k - 1) s.cut = o >> 16;       // nothing below the last group's maximum is among the best
+  }
+  sync();
+  const int groups_chosen = listed < k ? listed : k;
+  const uint32_t cut = s.cut;
+  for (int r0 = warp; r0 < groups_chosen; r0 += 8 * kWarps) {
+    uint32_t o[8];
+    int at[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {      // (eight loads at a time)
+      const int r = r0 + q * kWarps;
+      at[q] = r < groups_chosen ? static_cast<int>(chosen[r]) * 32 + lane : len;
+      o[q] = at[q] < len ? x[begin + at[q]] : 0u;
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const uint32_t key = order(o[q]);
+      if (at[q] < len && key >= cut)
+        found[atomicAdd(&s.n[1], 1u)] =
+            (static_cast<unsigned long long>(key) << 32) | (0xFFFFFFFFull - static_cast<unsigned long long>(begin + at[q]));
+    }
+  }
+  sync();
+  const int count = static_cast<int>(s.n[1]);
+  for (int i = tid; i < count; i += kThreads) {
+    const unsigned long long o = found[i];
+    int r = 0;
+#pragma unroll 4
+    for (int j = 0; j < count; ++j) r += found[j] > o;
+    if (r < k) best[r] = o;
+  }
+}
+
+// Alternative i of a row, given as a key.
+__device__ __forceinline__ void put_alternative(const ScoresArgs& a, int64_t row, int i, unsigned long long key, const Row& r) {
+  a.top_ids[row * a.top + i] = r.none ? -1 : static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(key));
+  a.top_logp[row * a.top + i] =
+      r.none ? NAN
+             : static_cast<float>((static_cast<double>(value_of(static_cast<uint32_t>(key >> 32))) - value_of(r.top)) * a.scale - r.lns);
+}
+
 constexpr int kMaxCluster = 8;
 
 template <bool kVec, bool kTop>
-__global__ void __launch_bounds__(kThreads) scores_kernel(const __grid_constant__ ScoresArgs a) {
-  extern __shared__ __align__(16) uint8_t dyn[];
+__global__ void __launch_bounds__(kThreads, 9) scores_kernel(const __grid_constant__ ScoresArgs a) {
+  extern __shared__ __align__(128) uint8_t dyn[];
   __shared__ uint32_t sh_max[kWarps];
   __shared__ float sh_sum[kWarps][4];
   __shared__ Slice sh_slice[kMaxCluster];
-  __shared__ uint32_t sh_key[kThreads];
-  __shared__ uint32_t sh_low, sh_cut, sh_n[2];
+  __shared__ Select sh_select;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int parts = a.parts;
   const int64_t row = blockIdx.x / parts;
@@ -193,155 +438,32 @@ __global__ void __launch_bounds__(kThreads) scores_kernel(const __grid_constant_
   // the given token's logit is on its way while the row is read
   int y = -1;
   float xy = 0.0f;
-  if (tid == 0 && part == 0) {
-    y = a.ids[row];
-    if (y < 0 || y >= a.V) {
-      set_device_status(a.status, DEV_BAD_INDEX);
-      y = -1;
-    } else {
-      xy = lo_bf16(x[y]);
-    }
-  }
+  if (tid == 0 && part == 0) y = given_token(a, row, &xy);
 
   uint16_t* groups = reinterpret_cast<uint16_t*>(dyn);
-  float m = -INFINITY, r = -INFINITY, ones = 0.0f, hi = 0.0f, lo = 0.0f, e = 0.0f;
-  uint32_t top2 = kNegInf2;
-  for (int base = 0; base < len; base += kStep) {
-    uint4 v[kUnroll];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) v[u] = load8<kVec>(x, begin + base + u * kThreads * 8 + tid * 8, end);
-    uint32_t g[kUnroll / 2];      // the largest of each eight, two a register
-#pragma unroll
-    for (int u = 0; u < kUnroll; u += 2) {
-      const uint32_t p = max2(max2(v[u].x, v[u].y), max2(v[u].z, v[u].w));
-      const uint32_t q = max2(max2(v[u + 1].x, v[u + 1].y), max2(v[u + 1].z, v[u + 1].w));
-      g[u / 2] = max2(__byte_perm(p, q, 0x5410), __byte_perm(p, q, 0x7632));
-    }
-    if constexpr (kTop) {
-      // of 32 neighbours: four lanes together
-#pragma unroll
-      for (int i = 0; i < kUnroll / 2; ++i) {
-        g[i] = max2(g[i], __shfl_xor_sync(0xffffffffu, g[i], 1));
-        g[i] = max2(g[i], __shfl_xor_sync(0xffffffffu, g[i], 2));
-      }
-      const int u = tid & 3;
-      const uint32_t w = u & 2 ? g[1] : g[0];
-      const int at = (base + u * kThreads * 8 + tid * 8) >> 5;
-      if (at * 32 < len) groups[at] = static_cast<uint16_t>(u & 1 ? w >> 16 : w & 0xFFFFu);
-    }
-    const uint32_t t2 = max2(g[0], g[1]);
-    top2 = max2(top2, t2);
-    // (one maximum a warp: a lane's own would grow in most steps of some lane)
-    const float cm = warp_max(fmaxf(lo_bf16(t2), hi_bf16(t2)));
-    if (cm > m) {
-      rebase(cm, a.scale2, m, r, ones, hi, lo, e);
-      m = cm;
-    }
-    // peak: the maximum is among these; its exponentials, 1 each, are counted and not added
-    float s, es;
-    if (!(fabsf(r) < kFar)) {
-      add_chunk<true, true>(v, m, r, a.scale2, ones, s, es);
-    } else if (cm == m) {
-      add_chunk<true, false>(v, m, r, a.scale2, ones, s, es);
-    } else {
-      add_chunk<false, false>(v, m, r, a.scale2, ones, s, es);
-    }
-    if (!(es == es)) es = chunk_entropy(v, m, r, a.scale2);     // 0 x -inf
-    two_sum_acc(hi, lo, s);
-    e += es;
-  }
+  Sums w = stream<kVec, kTop>(a, x, begin, end, tid, groups);
 
   // the slice's maximum, and the sums relative to it
-  uint32_t top = max(order(top2 & 0xFFFFu), order(top2 >> 16));
-  top = __reduce_max_sync(0xffffffffu, top);
+  uint32_t top = warp_top(w);
   if (lane == 0) sh_max[warp] = top;
-  if (tid == 0) {
-    sh_low = 0u;
-    sh_cut = 0u;
-    sh_n[0] = sh_n[1] = 0u;
-  }
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) top = max(top, sh_max[w]);
-  {
-    const float peak = value_of(top);
-    if (m != peak) rebase(peak, a.scale2, m, r, ones, hi, lo, e);
-  }
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) {
-    const float h = __shfl_xor_sync(0xffffffffu, hi, off);
-    lo += __shfl_xor_sync(0xffffffffu, lo, off);
-    two_sum_acc(hi, lo, h);
-    e += __shfl_xor_sync(0xffffffffu, e, off);
-    ones += __shfl_xor_sync(0xffffffffu, ones, off);
-  }
+  for (int i = 0; i < kWarps; ++i) top = max(top, sh_max[i]);
+  add_lanes(w, value_of(top), a.scale2);
   if (lane == 0) {
-    sh_sum[warp][0] = hi;
-    sh_sum[warp][1] = lo;
-    sh_sum[warp][2] = e;
-    sh_sum[warp][3] = ones;
+    sh_sum[warp][0] = w.hi;
+    sh_sum[warp][1] = w.lo;
+    sh_sum[warp][2] = w.e;
+    sh_sum[warp][3] = w.ones;
   }
 
   unsigned long long* best = nullptr;        // [parts][top]: the slices' best logits, in order
   if constexpr (kTop) {
-    const int k = a.top;
-    const int n = (len + 31) >> 5;
     uint8_t* at = dyn + ((static_cast<size_t>(a.slice) + 31) / 32 * 2 + 15) / 16 * 16;
     best = reinterpret_cast<unsigned long long*>(at);
-    at += static_cast<size_t>(parts) * k * 8;
-    unsigned long long* found = reinterpret_cast<unsigned long long*>(at);       // [32 k]
-    uint32_t* list = reinterpret_cast<uint32_t*>(found + 32 * k);                // [k groups of a thread]
-    uint32_t* chosen = list + static_cast<size_t>(k) * ((a.slice / 32 + kThreads) / kThreads);
-    // groups as whole numbers: maximum, then the lowest index; 0: none
-    auto key = [&](int g) { return (order(groups[g]) << 16) | (0xFFFFu - static_cast<uint32_t>(g)); };
-    uint32_t mine = 0u;
-    for (int g = tid; g < n; g += kThreads) mine = max(mine, key(g));
-    sh_key[tid] = mine;
-    if (tid < k) best[part * k + tid] = 0ull;
-    __syncthreads();
-    // the k threads with the largest groups hold the k largest groups
-    int rank = 0;
-    for (int i = 0; i < kThreads; i += 4) {
-      const uint4 o = *reinterpret_cast<const uint4*>(sh_key + i);
-      rank += (o.x > mine) + (o.y > mine) + (o.z > mine) + (o.w > mine);
-    }
-    if (rank == k - 1) sh_low = mine;
-    __syncthreads();
-    if (rank < k && mine > 0u) {
-      const uint32_t low = sh_low;
-      for (int g = tid; g < n; g += kThreads) {
-        const uint32_t o = key(g);
-        if (o >= low) list[atomicAdd(&sh_n[0], 1u)] = o;
-      }
-    }
-    __syncthreads();
-    const int listed = static_cast<int>(sh_n[0]);
-    for (int i = tid; i < listed; i += kThreads) {
-      const uint32_t o = list[i];
-      int r = 0;
-      for (int j = 0; j < listed; ++j) r += list[j] > o;
-      if (r < k) chosen[r] = 0xFFFFu - (o & 0xFFFFu);
-      if (r == k - 1) sh_cut = o >> 16;       // nothing below the last group's maximum is among the best
-    }
-    __syncthreads();
-    const int groups_chosen = listed < k ? listed : k;
-    const uint32_t cut = sh_cut;
-    for (int r = warp; r < groups_chosen; r += kWarps) {
-      const int i = static_cast<int>(chosen[r]) * 32 + lane;
-      if (i >= len) continue;
-      const uint32_t o = order(x[begin + i]);
-      if (o >= cut)
-        found[atomicAdd(&sh_n[1], 1u)] =
-            (static_cast<unsigned long long>(o) << 32) | (0xFFFFFFFFull - static_cast<unsigned long long>(begin + i));
-    }
-    __syncthreads();
-    const int count = static_cast<int>(sh_n[1]);
-    for (int i = tid; i < count; i += kThreads) {
-      const unsigned long long o = found[i];
-      int r = 0;
-      for (int j = 0; j < count; ++j) r += found[j] > o;
-      if (r < k) best[part * k + r] = o;
-    }
+    at += static_cast<size_t>(parts) * a.top * 8;
+    select_best(x, begin, len, groups, a.top, best + part * a.top, at, select_list(a.slice, a.top), sh_select, tid, w.group,
+                [] { __syncthreads(); });
   }
   if (parts > 1) cluster_wait();
   __syncthreads();
@@ -380,62 +502,24 @@ __global__ void __launch_bounds__(kThreads) scores_kernel(const __grid_constant_
   }
 
   // the row: the slices joined in order
-  __shared__ double sh_lns;
-  __shared__ uint32_t sh_top;
-  if (tid == 0) {
-    uint32_t all = 0u;
-    for (int i = 0; i < parts; ++i) all = max(all, sh_slice[i].top);
-    const float peak = value_of(all);
-    float n = 0.0f, h = 0.0f, l = 0.0f, w = 0.0f;
-    for (int i = 0; i < parts; ++i) {
-      Slice s = sh_slice[i];
-      const float from = value_of(s.top);
-      float base = reference(from, a.scale2);
-      if (from != peak) rebase(peak, a.scale2, from, base, s.ones, s.hi, s.lo, s.e);
-      n += s.ones;
-      two_sum_acc(h, l, s.hi);
-      l += s.lo;
-      w += s.e;
-    }
-    // a NaN or an infinite logit, or none that is larger than -inf: no distribution
-    const bool none = all >= 0xFF80u || all <= 0x007Fu;
-    // the reference's rounding goes out again: z from the peak itself is z + off
-    const float base = reference(peak, a.scale2);
-    const double off = fabsf(base) < kFar ? static_cast<double>(base) - static_cast<double>(peak) * a.scale2 : 0.0;
-    const double back = fabs(off) < 0x1p-12 ? 1.0 + off * kLn2 : exp2(off);
-    const double rest = (static_cast<double>(h) + static_cast<double>(l)) * back, S = n + rest;
-    const double lns = none ? static_cast<double>(NAN) : log1p(n - 1.0 + rest);
-    sh_lns = lns;
-    sh_top = all;
-    a.logp[row] = y < 0 ? 0.0f : static_cast<float>((static_cast<double>(xy) - peak) * a.scale - lns);
-    if (a.lse != nullptr) a.lse[row] = static_cast<float>(peak * a.scale + lns);
-    if (a.entropy != nullptr) {
-      const double ent = lns - kLn2 * (w * back + off * rest) / S;
-      a.entropy[row] = ent < 0.0 ? 0.0f : static_cast<float>(ent);
-    }
-  }
+  __shared__ Row sh_row;
+  if (tid == 0) sh_row = finish_row(a, sh_slice, parts, row, y, xy);
   if constexpr (kTop) {
     __syncthreads();
     const int k = a.top, all = parts * k;
-    const bool none = sh_top >= 0xFF80u || sh_top <= 0x007Fu;
-    if (none) {
-      if (tid < k) {
-        a.top_ids[row * k + tid] = -1;
-        a.top_logp[row * k + tid] = NAN;
-      }
+    const Row r = sh_row;
+    if (r.none) {
+      if (tid < k) put_alternative(a, row, tid, 0ull, r);
       return;
     }
     for (int i = tid; i < all; i += kThreads) {
       const unsigned long long o = best[i];
-      int r = i;
+      int at = i;
       if (parts > 1) {
-        r = 0;
-        for (int j = 0; j < all; ++j) r += best[j] > o;
+        at = 0;
+        for (int j = 0; j < all; ++j) at += best[j] > o;
       }
-      if (r >= k || o == 0ull) continue;
-      a.top_ids[row * k + r] = static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(o));
-      a.top_logp[row * k + r] =
-          static_cast<float>((static_cast<double>(value_of(static_cast<uint32_t>(o >> 32))) - value_of(sh_top)) * a.scale - sh_lns);
+      if (at < k && o != 0ull) put_alternative(a, row, at, o, r);
     }
   }
 }
@@ -541,10 +625,10 @@ cudaError_t launch_scores(const ScoresArgs& args, cudaStream_t s) {
   a.slice = (a.V + a.parts - 1) / a.parts;
   a.slice = (a.slice + 31) / 32 * 32;
   const bool vec = vec_ok(a.logits, a.ldx);
-  if (a.top == 0) return vec ? launch_scores_t<true, false>(a, 0, s) : launch_scores_t<false, false>(a, 0, s);
   const size_t k = static_cast<size_t>(a.top);
+  if (a.top == 0) return vec ? launch_scores_t<true, false>(a, 0, s) : launch_scores_t<false, false>(a, 0, s);
   size_t smem = ((static_cast<size_t>(a.slice) + 31) / 32 * 2 + 15) / 16 * 16;
-  smem += k * a.parts * 8 + 32 * k * 8 + k * ((a.slice / 32 + kThreads) / kThreads) * 4 + k * 4;
+  smem += k * a.parts * 8 + select_scratch(a.slice, a.top);
   if (smem > kScoresSmem) return cudaErrorInvalidValue;
   return vec ? launch_scores_t<true, true>(a, smem, s) : launch_scores_t<false, true>(a, smem, s);
 }
