@@ -280,8 +280,8 @@ def _norm(q_weight, k_weight, eps, weight_offset, D, dev):
                       kind is _f32, weight_offset, eps)
 
 
-def _rope_desc(q, k, inv_freq, positions, pos0, interleaved, attn_factor, q_out, k_out, dev):
-    """(packed descriptor, q_out, k_out, T, D, keep-alive) of a rotation, inv_freq None: of none."""
+def _rope_desc(q, k, inv_freq, positions, pos0, interleaved, attn_factor, q_out, k_out):
+    """(packed descriptor, q_out, k_out, T, D, device, keep-alive) of a rotation, inv_freq None: of none."""
     some = q if q is not None else k
     for t in (some, k):
         if t is not None and (not isinstance(t, _Tensor) or t.dim() != 3):
@@ -289,6 +289,7 @@ def _rope_desc(q, k, inv_freq, positions, pos0, interleaved, attn_factor, q_out,
     if some is None:
         raise TypeError("q or k must be a 3-D CUDA tensor")
     T, _, D = some.shape
+    dev = torch.cuda.current_device()
     f, n, keep = (0, 0, None) if inv_freq is None else _host_doubles(inv_freq, "inv_freq")
     Hq = Hk = qp = qs = qo = qos = kp = ks = ko = kos = 0
     if q is not None:
@@ -309,7 +310,7 @@ def _rope_desc(q, k, inv_freq, positions, pos0, interleaved, attn_factor, q_out,
             ko, kos = _heads(k_out, "k_out", T, Hk, D, dev)
     d = _ROPE.pack(T, Hq, Hk, D, 2 * n, bool(interleaved), False, f, attn_factor,
                    _opt(positions, "positions", _i64, (T,), dev), pos0, qp, qs, qo, qos, kp, ks, ko, kos)
-    return d, q_out, k_out, T, D, keep
+    return d, q_out, k_out, T, D, dev, keep
 
 
 def norm_rope(q, k, q_weight, k_weight, inv_freq=None, eps: float = 1e-6, positions=None, pos0: int = 0,
@@ -318,8 +319,7 @@ def norm_rope(q, k, q_weight, k_weight, inv_freq=None, eps: float = 1e-6, positi
     each: x / sqrt(mean x^2 + eps) * (weight + weight_offset), turned by their positions as rope() does it in the
     same pass (inv_freq None: norms alone).  Weights: bf16 or fp32 [D], None: 1.  q_out / k_out may be the
     inputs.  Returns (q_out, k_out)."""
-    dev = torch.cuda.current_device()
-    d, q_out, k_out, _, D, keep = _rope_desc(q, k, inv_freq, positions, pos0, interleaved, attn_factor, q_out, k_out, dev)
+    d, q_out, k_out, _, D, dev, keep = _rope_desc(q, k, inv_freq, positions, pos0, interleaved, attn_factor, q_out, k_out)
     b._check(b._lib().ls_norm_rope(d, _norm(q_weight, k_weight, eps, weight_offset, D, dev), _raw_stream(dev)),
              "ls_norm_rope")
     return q_out, k_out
@@ -341,11 +341,10 @@ def norm_rope_bwd(dq, dk, q, k, q_weight, k_weight, inv_freq=None, eps: float = 
                   dk_out=None, workspace=None) -> NormRopeGrads:
     """Gradients of norm_rope(): dq, dk are d loss / d its outputs, q, k its inputs.  dq_out / dk_out may be
     dq / dk.  Weight gradients are fp32 sums over tokens and heads (None for a weight that is None)."""
-    dev = torch.cuda.current_device()
     if (dq is None) != (q is None) or (dk is None) != (k is None):
         raise TypeError("dq comes with q, and dk with k")
-    d, dq_out, dk_out, T, D, keep = _rope_desc(dq, dk, inv_freq, positions, pos0, interleaved, attn_factor, dq_out, dk_out,
-                                               dev)
+    d, dq_out, dk_out, T, D, dev, keep = _rope_desc(dq, dk, inv_freq, positions, pos0, interleaved, attn_factor, dq_out,
+                                                    dk_out)
     qp = qs = kp = ks = 0
     dwq = dwk = None
     if q is not None:
