@@ -60,49 +60,61 @@ __global__ void __launch_bounds__(kThreads) scale_kernel(float4* acc, size_t n4,
   }
 }
 
-// One warp per 128-row Q tile slot (kv, i, r): row r of tile i packs query
-// t = i * qt + r / g and head h = kv * g + r % g.  Valid rows get LSE log2 e and
+// 128-row Q tiles (kv, i): row r of tile i packs query t = i * qt + r / g and head h = kv * g + r % g.  Valid rows get LSE log2 e and
 // Delta = sum_d dO O; padding rows and rows past R get (+inf, 0).  Layout per tile: the
 // 128 LSE values, then the 128 Delta values.
+template <int kLanes>
 __global__ void __launch_bounds__(kThreads) bwd_prep_kernel(const uint4* o, const uint4* d_out,
                                                            const float* lse, float* rowstats,
                                                            AttnShape sh,
                                                            const __grid_constant__ Varlen vl, unsigned* queue) {
+  // A block a tile, kLanes = D / 8 lanes a row, four rows of a lane group in flight: 8,192 tokens of 40 heads
+  // 33 us, 5.2 TB/s (a row a warp at a time, found by 64-bit divisions, 78 us).
+  constexpr int kRows = 32 / kLanes, kInFlight = 4;
   if (queue != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *queue = 0u;
-  const int lane = threadIdx.x & 31;
-  const int64_t warps_total = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
-  const int per_row = sh.D / 8;   // 8 or 16 lanes, 8 bf16 each
-  const int64_t n_qt = vl.qt0[vl.G];
-  const int64_t slots = static_cast<int64_t>(sh.Hkv) * n_qt * 128;
-  for (int64_t sidx = blockIdx.x * static_cast<int64_t>(kThreads / 32) + (threadIdx.x >> 5);
-       sidx < slots; sidx += warps_total) {
-    const int64_t tile = sidx >> 7;                // kv * n_qt + f
-    const int r = static_cast<int>(sidx & 127);
-    const int64_t kv = tile / n_qt;
-    const int f = static_cast<int>(tile - kv * n_qt);
-    const int b = varlen_find(vl.qt0, vl.G, f);
-    const int64_t t = static_cast<int64_t>(f - vl.qt0[b]) * sh.qt + r / sh.g;
-    const int64_t h = kv * sh.g + r % sh.g;
-    const bool valid = (r < sh.g * sh.qt) && (t < vl.row0[b + 1] - vl.row0[b]);
-    const int64_t row = (vl.row0[b] + t) * sh.Hq + h;
-    float acc = 0.f;
-    if (valid && lane < per_row) {
-      const uint4 a = __ldcs(o + row * per_row + lane);
-      const uint4 bb = __ldcs(d_out + row * per_row + lane);
-      const uint32_t aw[4] = {a.x, a.y, a.z, a.w};
-      const uint32_t bw[4] = {bb.x, bb.y, bb.z, bb.w};
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int n_qt = vl.qt0[vl.G];
+  const int tile = static_cast<int>(blockIdx.x);           // kv * n_qt + f
+  const int kv = tile / n_qt, f = tile - kv * n_qt;
+  const int b = varlen_find(vl.qt0, vl.G, f);
+  const int t0 = (f - vl.qt0[b]) * sh.qt, R = vl.row0[b + 1] - vl.row0[b];
+  float* dst = rowstats + static_cast<int64_t>(tile) * 256;
+  const int at = lane % kLanes, sub = lane / kLanes;
+  constexpr int kPerWarp = 128 / (kThreads / 32);
+#pragma unroll
+  for (int r0 = 0; r0 < kPerWarp; r0 += kRows * kInFlight) {
+    uint4 x[kInFlight], y[kInFlight];
+    float l[kInFlight];
+    bool valid[kInFlight];
+#pragma unroll
+    for (int i = 0; i < kInFlight; ++i) {
+      const int r = warp * kPerWarp + r0 + i * kRows + sub, tok = r / sh.g;
+      valid[i] = r < sh.g * sh.qt && t0 + tok < R;
+      const int64_t row = (static_cast<int64_t>(vl.row0[b]) + t0 + tok) * sh.Hq + kv * sh.g + (r - tok * sh.g);
+      x[i] = y[i] = make_uint4(0u, 0u, 0u, 0u);
+      l[i] = 0.0f;
+      if (valid[i]) {
+        x[i] = __ldcs(o + row * kLanes + at);
+        y[i] = __ldcs(d_out + row * kLanes + at);
+        if (at == 0) l[i] = lse[row];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kInFlight; ++i) {
+      const uint32_t aw[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, bw[4] = {y[i].x, y[i].y, y[i].z, y[i].w};
+      float acc = 0.f;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         acc = fmaf(__uint_as_float(aw[k] << 16), __uint_as_float(bw[k] << 16), acc);
         acc = fmaf(__uint_as_float(aw[k] & 0xFFFF0000u), __uint_as_float(bw[k] & 0xFFFF0000u), acc);
       }
-    }
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
-    if (lane == 0) {
-      float* dst = rowstats + tile * 256;
-      dst[r] = valid ? lse[row] * 1.4426950408889634f : INFINITY;
-      dst[128 + r] = valid ? acc : 0.f;
+      for (int off = kLanes / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
+      if (at == 0) {
+        const int r = warp * kPerWarp + r0 + i * kRows + sub;
+        dst[r] = valid[i] ? l[i] * 1.4426950408889634f : INFINITY;
+        dst[128 + r] = valid[i] ? acc : 0.f;
+      }
     }
   }
 }
@@ -274,10 +286,13 @@ cudaError_t launch_f32_to_bf16(const float* in, void* out, size_t count, cudaStr
 cudaError_t launch_bwd_prep(const uint16_t* o, const uint16_t* d_out, const float* lse,
                             float* rowstats, const AttnShape& sh, const Varlen& vl,
                             unsigned* queue, cudaStream_t s) {
-  const size_t slots = static_cast<size_t>(sh.Hkv) * vl.qt0[vl.G] * 128;
-  bwd_prep_kernel<<<grid_for(slots * 32), kThreads, 0, s>>>(
-      reinterpret_cast<const uint4*>(o), reinterpret_cast<const uint4*>(d_out), lse, rowstats, sh,
-      vl, queue);
+  const unsigned tiles = static_cast<unsigned>(sh.Hkv) * static_cast<unsigned>(vl.qt0[vl.G]);
+  const uint4* o4 = reinterpret_cast<const uint4*>(o);
+  const uint4* d4 = reinterpret_cast<const uint4*>(d_out);
+  if (sh.D == 128)
+    bwd_prep_kernel<16><<<tiles, kThreads, 0, s>>>(o4, d4, lse, rowstats, sh, vl, queue);
+  else
+    bwd_prep_kernel<8><<<tiles, kThreads, 0, s>>>(o4, d4, lse, rowstats, sh, vl, queue);
   return cudaGetLastError();
 }
 
