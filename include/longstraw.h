@@ -361,6 +361,7 @@ ls_status ls_policy_loss(const ls_policy_loss_desc* d, void* workspace, size_t w
  *   logits   device bf16, row t at logits + t logits_stride (elements, >= V)
  *   ids      device int32 [T] (an id outside [0, V) sets the device status; its logp is 0)
  *   logp     device fp32 [T]; lse, entropy device fp32 [T], may be NULL
+ *   temperature  2^-120 .. 2^120
  *   top      0 .. min(V, 64); with top > 0 top_ids device int32, top_logp device fp32 [T, top] and
  *            V <= 2^23 (else LS_ERR_UNSUPPORTED)
  * Logits of -inf (masked) have p = 0 and add nothing to the entropy; they are alternatives only where fewer

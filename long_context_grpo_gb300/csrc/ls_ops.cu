@@ -108,12 +108,14 @@ ls_status ls_policy_loss(const ls_policy_loss_desc* d, void* workspace, size_t w
   return e == cudaSuccess ? LS_OK : static_cast<ls_status>(launch_failed(e, "policy loss launch"));
 }
 
+// 1 / temperature and log2 e / temperature are fp32 factors: neither may pass its range, 0 x -inf would be NaN.
+static bool temperature_ok(double t) { return t >= 0x1p-120 && t <= 0x1p120; }
+
 ls_status ls_token_scores(const ls_token_scores_desc* d, void* stream) {
   NvtxRange nvtx_range("ls_token_scores");
   if (d == nullptr || d->logits == nullptr || d->ids == nullptr || d->logp == nullptr) return LS_ERR_INVALID_ARGUMENT;
   if (d->T < 1 || d->V < 1 || d->logits_stride < d->V || d->top < 0 || d->top > d->V) return LS_ERR_INVALID_ARGUMENT;
-  if (!(d->temperature > 0.0) || !std::isfinite(d->temperature) || !std::isfinite(1.0 / d->temperature))
-    return LS_ERR_INVALID_ARGUMENT;
+  if (!temperature_ok(d->temperature)) return LS_ERR_INVALID_ARGUMENT;
   if (d->top > 0 && (d->top_ids == nullptr || d->top_logp == nullptr)) return LS_ERR_INVALID_ARGUMENT;
   if (d->top > kMaxTop || (d->top > 0 && d->V > kMaxScoresVocab) || d->T >= (int64_t(1) << 28) ||
       d->V >= (int64_t(1) << 31) || d->logits_stride >= (int64_t(1) << 31))
@@ -155,8 +157,7 @@ ls_status ls_token_scores_bwd(const ls_token_scores_bwd_desc* d, void* stream) {
   if (d->d_logp == nullptr && d->d_entropy == nullptr) return LS_ERR_INVALID_ARGUMENT;
   if (d->d_entropy != nullptr && d->entropy == nullptr) return LS_ERR_INVALID_ARGUMENT;
   if (d->T < 1 || d->V < 1 || d->logits_stride < d->V || d->dlogits_stride < d->V) return LS_ERR_INVALID_ARGUMENT;
-  if (!(d->temperature > 0.0) || !std::isfinite(d->temperature) || !std::isfinite(1.0 / d->temperature))
-    return LS_ERR_INVALID_ARGUMENT;
+  if (!temperature_ok(d->temperature)) return LS_ERR_INVALID_ARGUMENT;
   if (d->logits == d->dlogits && d->logits_stride != d->dlogits_stride) return LS_ERR_INVALID_ARGUMENT;
   if (d->T >= (int64_t(1) << 28) || d->V >= (int64_t(1) << 31) || d->logits_stride >= (int64_t(1) << 31) ||
       d->dlogits_stride >= (int64_t(1) << 31))

@@ -301,6 +301,37 @@ def test_refusals():
     assert call(dlogits=0x8001) == 4 and call(d_logp=0x6002) == 4
 
 
+@pytest.mark.parametrize("temperature", [2.0 ** -121, 1e-40, 2.0 ** 121, 1e60])
+def test_a_temperature_past_fp32_is_refused(temperature):
+    from long_context_grpo_gb300 import build as lsbuild
+    lsbuild.build()
+    from long_context_grpo_gb300 import _lib as b
+    L = b._lib()
+    d = b.TokenScoresDesc(T=4, V=64, logits_stride=64, logits=0x1000, ids=0x2000, temperature=temperature, top=0, logp=0x3000)
+    assert L.ls_token_scores(ctypes.byref(d), None) == 1
+    d = b.TokenScoresBwdDesc(T=4, V=64, logits_stride=64, dlogits_stride=64, logits=0x1000, ids=0x2000,
+                             temperature=temperature, logp=0x3000, lse=0x4000, d_logp=0x6000, dlogits=0x8000)
+    assert L.ls_token_scores_bwd(ctypes.byref(d), None) == 1
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("temperature", [2.0 ** -120, 2.0 ** 120])
+def test_temperatures_at_the_ends(temperature):
+    """The coldest row is its largest logit alone; at the hottest all ids are alike, to fp32's rounding of log V."""
+    import long_context_grpo_gb300 as ls
+    x = torch.zeros(3, 500, dtype=torch.bfloat16, device="cuda")
+    x[:, 7] = 2.0
+    x[2, 9:] = float("-inf")
+    ids = torch.tensor([7, 7, 7], dtype=torch.int32, device="cuda")
+    r = ls.token_scores(x, ids, top=2, temperature=temperature)
+    n = torch.tensor([500.0, 500.0, 9.0], dtype=torch.float64)
+    want = torch.zeros(3, dtype=torch.float64) if temperature < 1 else -n.log()
+    assert torch.allclose(r.logp.double().cpu(), want, rtol=2.0 ** -23, atol=0)
+    assert torch.allclose(r.entropy.double().cpu(), -want, rtol=2.0 ** -20, atol=0)
+    assert r.top_ids.cpu().tolist() == [[7, 0]] * 3
+    assert not torch.isnan(r.top_logp).any()
+
+
 def test_packed_descriptors_have_the_structures_layout():
     from long_context_grpo_gb300 import _lib as b
     from long_context_grpo_gb300 import _ops
