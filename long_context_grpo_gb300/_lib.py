@@ -33,6 +33,11 @@ class LongStrawError(RuntimeError):
         super().__init__(msg)
 
 
+def _keys(n: int) -> int:
+    """A number of keys as the library takes it: one past 64 bits would reach it cut off."""
+    return min(max(n, -1), 1 << 62)
+
+
 class PrefixDesc(ctypes.Structure):
     _fields_ = [("P", ctypes.c_int64), ("Hq", ctypes.c_int32), ("Hkv", ctypes.c_int32),
                 ("D", ctypes.c_int32), ("softmax_scale", ctypes.c_float),
@@ -265,7 +270,7 @@ class Prefix:
     def set_window(self, window: int, sinks: int = 0):
         """A sliding window for the replays from now on (window = 0: none); a forward and its
         backward have to be made under the same one."""
-        _check(_lib().ls_prefix_set_window(self._h, window, sinks), "ls_prefix_set_window")
+        _check(_lib().ls_prefix_set_window(self._h, _keys(window), _keys(sinks)), "ls_prefix_set_window")
 
     def close(self):
         if getattr(self, "_h", None) is not None and self._h.value is not None:

@@ -506,7 +506,8 @@ class PagedCache:
     def attn_workspace_bytes(self, S: int, T: int, max_new: int, max_len: int, window: int = None,
                              sinks: int = 0) -> int:
         if window is not None:
-            return int(b._lib().ls_cache_attn_window_workspace_bytes(self._h, S, T, max_new, max_len, window, sinks))
+            return int(b._lib().ls_cache_attn_window_workspace_bytes(self._h, S, T, max_new, max_len, b._keys(window),
+                                                                     b._keys(sinks)))
         return int(b._lib().ls_cache_attn_workspace_bytes(self._h, S, T, max_new, max_len))
 
     def attn(self, q, cu_new, max_new: int, max_len: int, rows=None, group: int = 1,
@@ -544,6 +545,6 @@ class PagedCache:
         if window is None:
             b._check(b._lib().ls_cache_attn(self._h, d, wp, workspace.numel(), _raw_stream(dev)), "ls_cache_attn")
         else:
-            b._check(b._lib().ls_cache_attn_window(self._h, d, window, sinks, wp, workspace.numel(),
-                                                   _raw_stream(dev)), "ls_cache_attn_window")
+            b._check(b._lib().ls_cache_attn_window(self._h, d, b._keys(window), b._keys(sinks), wp,
+                                                   workspace.numel(), _raw_stream(dev)), "ls_cache_attn_window")
         return o, lse

@@ -92,7 +92,7 @@ __device__ __forceinline__ void turn(const Chunks& c, bool interleaved, const fl
   for (int u = 0; u < 4; ++u) {
     float4 r;
     asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(r.x), "=f"(r.y), "=f"(r.z), "=f"(r.w) : "r"(at + u * kLanes * 16));
+                 : "=f"(r.x), "=f"(r.y), "=f"(r.z), "=f"(r.w) : "r"(at + u * kLanes * 16) : "memory");
     if (!interleaved) {
       const float a0 = x0[2 * u], b0 = x1[2 * u], a1 = x0[2 * u + 1], b1 = x1[2 * u + 1];
       x0[2 * u] = a0 * r.x - b0 * r.y;

@@ -295,3 +295,19 @@ def test_binding_refuses_before_the_library():
         ls.token_scores(None, None)
     with pytest.raises(TypeError):
         ls.token_scores_bwd(x[0], None, None, None)
+
+
+@pytest.mark.gpu
+def test_a_window_past_64_bits_is_one_past_the_sequence():
+    import long_context_grpo_gb300 as ls
+    mk, _ = build([200], 16, 1, 64, seed=5, width=20)
+    c = mk(2)
+    q = torch.randn(3, 2, 64, device="cuda").to(torch.bfloat16)
+    offsets = torch.tensor([0, 3], dtype=torch.int32, device="cuda")
+    want = c.attn(q, offsets, 3, 200, window=200)
+    for window, sinks in ((1 << 64) + 1, 0), (5, (1 << 64) + 1), (1 << 200, 1 << 70):      # all keys are in sight
+        got = c.attn(q, offsets, 3, 200, window=window, sinks=sinks)
+        # lse is near log 200; sums of at most 200 terms in another order: 8 x 2^-24 of their value
+        assert torch.allclose(got[1], want[1], rtol=2.0 ** -20, atol=0)
+    with pytest.raises(ls.LongStrawError):
+        c.attn(q, offsets, 3, 200, window=-(1 << 70))
