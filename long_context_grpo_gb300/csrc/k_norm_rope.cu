@@ -10,10 +10,10 @@
 // lanes share a head, a lane two 16-byte chunks (in the half layout the two whose values turn together), so
 // that a head's sums take three shuffles at D = 128, and the lane's weights stay in its registers over all
 // the heads that it walks.  The next head's chunks are on their way while this one's are at work.
-// 48 heads of 128: 8,192 tokens 45 us (201 MB, 4.4 TB/s), 32,768 tokens 143 us (5.6 TB/s; the rotation alone, with
+// 48 heads of 128: 8,192 tokens 43 us (201 MB, 4.7 TB/s), 32,768 tokens 143 us (5.6 TB/s; the rotation alone, with
 // half the arithmetic, 123); appending 14,000 tokens of 80 heads 105 us (566 MB, 5.4 TB/s; without norms 93).  About
 // 290 instructions for four heads of a warp: the issue slots are half full.
-// Gradient: 3,001 tokens 37 us with its two launches (25 of them the first one's), 32,768 tokens 226 us (5.3 TB/s).
+// Gradient: 3,001 tokens 32 us with its two launches in a graph (25 of them the first one's), 32,768 tokens 224 us.
 // Weight gradients: a lane's 16 columns in registers over all heads and tokens that it walks, a row of partial
 // sums a block, summed in a fixed order by a second kernel (no atomics).
 // Element path (a warp a head) for rows that are not 16-byte aligned, D not a multiple of 16 or rot_dim
@@ -349,7 +349,10 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(con
       x0v = *reinterpret_cast<const uint4*>(p + c.c0);
       x1v = *reinterpret_cast<const uint4*>(p + c.c1);
     };
+    // keys from the last warp on: the warps that have a round of queries less than others begin
+    // (3,001 tokens of 48 heads 33.6 -> 31.6 us in a graph, one to 64 tokens 10 -> 9)
     int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+    if (which) unit = warps - 1 - unit;
     Unit w = unit_of(unit < units ? unit : 0, split, H);
     int h = w.first + lane / kLanes;
     if (unit < units && h < w.end && mine) load(w.t, h);
@@ -538,15 +541,18 @@ int lanes_of(const NormArgs& n) {
 
 size_t angles_bytes(int lanes) { return static_cast<size_t>(8) * lanes * kWarps * sizeof(float2); }
 
-// How a token's heads become units: the least rounds of heads on any of the warps, a unit's angles counted as one.
-Split split_of(int64_t T, int H, int lanes, int64_t warps) {
+// How a token's heads become units: the least rounds of heads on any of the warps, where a unit itself counts as
+// `own` of them.  A warp that ends with its unit: 5 (48 heads: 3,001 tokens 17.8 us in a graph, with 1 20.4; 20,000
+// 91 and 96); a warp that goes on to the next one, whose loads are on their way: 1 (gradient of 3,001 tokens 31.6 us,
+// with 5 34).
+Split split_of(int64_t T, int H, int lanes, int64_t warps, double own) {
   const int slots = 32 / lanes, most = (H + slots - 1) / slots;
   Split best = {1, most * slots};
   double least = 0.0;
   for (int p = 1; p <= most; ++p) {
     const int per = ((H + p - 1) / p + slots - 1) / slots * slots;
     const int64_t parts = (H + per - 1) / per;
-    const double cost = static_cast<double>((T * parts + warps - 1) / warps) * (per / slots + 1.0);
+    const double cost = static_cast<double>((T * parts + warps - 1) / warps) * (per / slots + own);
     if (p == 1 || cost < least) {
       least = cost;
       best = {static_cast<int>(parts), per};
@@ -564,7 +570,7 @@ cudaError_t launch_norm_rope(const NormArgs& n, cudaStream_t s) {
     norm_rope_any_kernel<<<static_cast<unsigned>(a.T), kThreads, (a.rot / 2) * sizeof(float2), s>>>(n);
     return cudaGetLastError();
   }
-  const Split sp = split_of(a.T, a.Hq + a.Hk + (a.append ? a.Hk : 0), lanes, static_cast<int64_t>(num_sms()) * kBlocks * kWarps);
+  const Split sp = split_of(a.T, a.Hq + a.Hk + (a.append ? a.Hk : 0), lanes, static_cast<int64_t>(num_sms()) * kBlocks * kWarps, 5.0);
   const unsigned grid = static_cast<unsigned>((a.T * sp.parts + kWarps - 1) / kWarps);
   const size_t smem = angles_bytes(lanes);
   switch (lanes) {
@@ -591,7 +597,7 @@ cudaError_t launch_norm_rope_bwd(const NormArgs& n, float* dwq, float* dwk, cuda
   } else {
     const size_t smem = angles_bytes(lanes) + kWarps * static_cast<size_t>(a.D) * sizeof(float);
     const int64_t warps = static_cast<int64_t>(grid) * kWarps;
-    const Split q = split_of(a.T, a.Hq > 0 ? a.Hq : 1, lanes, warps), k = split_of(a.T, a.Hk > 0 ? a.Hk : 1, lanes, warps);
+    const Split q = split_of(a.T, a.Hq > 0 ? a.Hq : 1, lanes, warps, 1.0), k = split_of(a.T, a.Hk > 0 ? a.Hk : 1, lanes, warps, 1.0);
     switch (lanes) {
       case 1: norm_rope_bwd_kernel<1><<<grid, kThreads, smem, s>>>(n, q, k); break;
       case 2: norm_rope_bwd_kernel<2><<<grid, kThreads, smem, s>>>(n, q, k); break;
