@@ -26,6 +26,12 @@
  * positions (and gradients back); ls_cache_* keep the group's keys and values in pages that
  * the responses share with their prompt, and attend new tokens over them (rollout, scoring).
  *
+ * For models whose heads are normed and whose layers are windowed: ls_norm_rope (and its gradient)
+ * norms queries and keys a head each on the way into ls_rope's rotation, ls_cache_append_norm into the
+ * pages; ls_cache_attn_window and ls_prefix_set_window let a token see the last keys up to its own
+ * and the first ones of its sequence, over the cache and in the replay with its gradients.
+ * ls_token_scores (and its gradient) gives log-probabilities, entropies and the likeliest alternatives.
+ *
  * Conventions shared by every entry point
  *  - Pointers named "device" must point to device memory of the current CUDA device,
  *    allocated and owned by the caller.  The library allocates no device memory and never
