@@ -49,16 +49,26 @@ __device__ __forceinline__ float lane_sum(float x) {
   return x;
 }
 
-__device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
+// Eight values as four pairs: the arithmetic goes two values an instruction.
+__device__ __forceinline__ void unpack8(const uint4& v, uint64_t (&x)[4]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = bf(w[i], 0);
-    x[2 * i + 1] = bf(w[i], 1);
-  }
+  for (int i = 0; i < 4; ++i) x[i] = f2_pack(bf(w[i], 0), bf(w[i], 1));
 }
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+__device__ __forceinline__ uint4 pack8(const uint64_t (&x)[4]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float lo, hi;
+    f2_unpack(x[i], lo, hi);
+    w[i] = pack_bf16x2(lo, hi);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ float f2_sum(uint64_t x) {
+  float lo, hi;
+  f2_unpack(x, lo, hi);
+  return lo + hi;
 }
 
 // The two chunks of lane j of a head, and the first pair of each one's angles (-1: not turned).  In the
@@ -86,45 +96,44 @@ __device__ __forceinline__ Chunks chunks_of(const RopeArgs& a, int j) {
 }
 
 // x0, x1 turned in place.  Lane j's pairs are 8 j .. 8 j + 7 in both layouts; in the warp's part of shared
-// memory two of them lie behind one another for all lanes of a head, [4][kLanes], so that a head's lanes read
-// neighbouring 16 bytes.  (volatile: held in registers over the loop they push others out of them)
+// memory two of them lie behind one another for all lanes of a head, [4][kLanes] of two cosines and two sines, so
+// that a head's lanes read neighbouring 16 bytes.  (volatile: held in registers over the loop they push others out)
 template <int kLanes>
-__device__ __forceinline__ void turn(const Chunks& c, bool interleaved, const float2* cs, int j, float (&x0)[8], float (&x1)[8]) {
+__device__ __forceinline__ void turn(const Chunks& c, bool interleaved, const float* cs, int j, uint64_t (&x0)[4], uint64_t (&x1)[4]) {
   if (c.p0 < 0 && c.p1 < 0) return;
   const uint32_t at = smem_u32(cs) + j * 16;
+  const uint64_t minus = f2_pack(-1.0f, -1.0f);
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     float4 r;
     asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
                  : "=f"(r.x), "=f"(r.y), "=f"(r.z), "=f"(r.w) : "r"(at + u * kLanes * 16) : "memory");
     if (!interleaved) {
-      const float a0 = x0[2 * u], b0 = x1[2 * u], a1 = x0[2 * u + 1], b1 = x1[2 * u + 1];
-      x0[2 * u] = a0 * r.x - b0 * r.y;
-      x1[2 * u] = b0 * r.x + a0 * r.y;
-      x0[2 * u + 1] = a1 * r.z - b1 * r.w;
-      x1[2 * u + 1] = b1 * r.z + a1 * r.w;
+      const uint64_t cc = f2_pack(r.x, r.y), ss = f2_pack(r.z, r.w), a = x0[u], b = x1[u];
+      x0[u] = f2_fma(b, f2_mul(ss, minus), f2_mul(a, cc));
+      x1[u] = f2_fma(a, ss, f2_mul(b, cc));
     } else if (u < 2 || c.p1 >= 0) {
-      float* x = u < 2 ? x0 + 4 * u : x1 + 4 * (u - 2);
-      const float a0 = x[0], b0 = x[1], a1 = x[2], b1 = x[3];
-      x[0] = a0 * r.x - b0 * r.y;
-      x[1] = b0 * r.x + a0 * r.y;
-      x[2] = a1 * r.z - b1 * r.w;
-      x[3] = b1 * r.z + a1 * r.w;
+      uint64_t* x = u < 2 ? x0 + 2 * u : x1 + 2 * (u - 2);
+      float a, b;
+      f2_unpack(x[0], a, b);
+      x[0] = f2_pack(a * r.x - b * r.z, b * r.x + a * r.z);
+      f2_unpack(x[1], a, b);
+      x[1] = f2_pack(a * r.y - b * r.w, b * r.y + a * r.w);
     }
   }
 }
-// Where pair p of a warp's token lies.
+// Where the cosine of pair p of a warp's token lies; the sine lies two behind.
 template <int kLanes>
 __device__ __forceinline__ int angle_place(int p) {
-  return (((p & 7) >> 1) * kLanes + (p >> 3)) * 2 + (p & 1);
+  return (((p & 7) >> 1) * kLanes + (p >> 3)) * 4 + (p & 1);
 }
 
 // A lane's weights of queries (0) or keys (1).
-__device__ __forceinline__ void load_weights(const NormArgs& n, int which, const Chunks& c, float (&w0)[8], float (&w1)[8]) {
+__device__ __forceinline__ void load_weights(const NormArgs& n, int which, const Chunks& c, uint64_t (&w0)[4], uint64_t (&w1)[4]) {
 #pragma unroll
-  for (int u = 0; u < 8; ++u) {
-    w0[u] = weight_of(n, which, c.c0 + u);
-    w1[u] = weight_of(n, which, c.c1 + u);
+  for (int u = 0; u < 4; ++u) {
+    w0[u] = f2_pack(weight_of(n, which, c.c0 + 2 * u), weight_of(n, which, c.c0 + 2 * u + 1));
+    w1[u] = f2_pack(weight_of(n, which, c.c1 + 2 * u), weight_of(n, which, c.c1 + 2 * u + 1));
   }
 }
 
@@ -174,9 +183,13 @@ __device__ __forceinline__ Token warp_token(const RopeArgs& a, int64_t t, int la
 }
 // Its angles in the warp's part of shared memory.
 template <int kLanes>
-__device__ __forceinline__ void warp_angles(const RopeArgs& a, int64_t pos, int lane, float2* cs) {
+__device__ __forceinline__ void warp_angles(const RopeArgs& a, int64_t pos, int lane, float* cs) {
   __syncwarp();
-  for (int p = lane; p < a.rot >> 1; p += 32) cs[angle_place<kLanes>(p)] = angle_of(a, pos, p);
+  for (int p = lane; p < a.rot >> 1; p += 32) {
+    const float2 e = angle_of(a, pos, p);
+    cs[angle_place<kLanes>(p)] = e.x;
+    cs[angle_place<kLanes>(p) + 2] = e.y;
+  }
   __syncwarp();
 }
 
@@ -198,7 +211,7 @@ __device__ __forceinline__ Unit unit_of(int64_t u, const Split& s, int H) {
 
 template <int kLanes>
 __global__ void __launch_bounds__(kThreads, kBlocks) norm_rope_kernel(const __grid_constant__ NormArgs n, const Split split) {
-  extern __shared__ __align__(16) float2 angles[];       // [warp][4][kLanes] pairs of pairs
+  extern __shared__ __align__(16) float angles[];        // [warp][4][kLanes][4]
   constexpr int kSlots = 32 / kLanes;
   const RopeArgs& a = n.r;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -208,21 +221,32 @@ __global__ void __launch_bounds__(kThreads, kBlocks) norm_rope_kernel(const __gr
   const int j = lane % kLanes;
   const bool mine = 16 * j < a.D;
   const Chunks c = chunks_of(a, j);
-  float2* cs = angles + warp * 8 * kLanes;
+  float* cs = angles + warp * 16 * kLanes;
 
+  // 0 queries, 1 keys, 2 values: within a kind heads lie at one distance from one another
+  auto kind_of = [&](int h) { return h < a.Hq ? 0 : (h < a.Hq + a.Hk ? 1 : 2); };
   int h = w.first + lane / kLanes;
+  int from = -1;                   // kind that `in` is of
+  const uint16_t* in = nullptr;
   uint4 v0 = make_uint4(0u, 0u, 0u, 0u), v1 = v0;
   auto load = [&]() {
-    const uint16_t* p = source(a, w.t, h);
-    v0 = *reinterpret_cast<const uint4*>(p + c.c0);
-    v1 = *reinterpret_cast<const uint4*>(p + c.c1);
+    const int kind = kind_of(h);
+    if (kind != from) {
+      from = kind;
+      in = source(a, w.t, h);
+    } else {
+      in += kSlots * a.D;
+    }
+    v0 = *reinterpret_cast<const uint4*>(in + c.c0);
+    v1 = *reinterpret_cast<const uint4*>(in + c.c1);
   };
   if (h < w.end && mine) load();
   const Token tok = warp_token(a, w.t, lane);
   if (tok.page < 0) return;
   warp_angles<kLanes>(a, tok.pos, lane, cs);
-  float w0[8], w1[8];
-  int which = -1;                  // whose weights these are
+  uint64_t w0[4], w1[4];
+  int to = -1;                     // kind that `out` and the weights are of
+  uint16_t* out = nullptr;
   const float inv_d = 1.0f / static_cast<float>(a.D);
 #pragma unroll 1
   for (int i = w.first; i < w.end; i += kSlots) {
@@ -230,31 +254,34 @@ __global__ void __launch_bounds__(kThreads, kBlocks) norm_rope_kernel(const __gr
     const int hh = h;
     h += kSlots;
     if (h < w.end && mine) load();
-    float x0[8], x1[8];
+    uint64_t x0[4], x1[4], sq[2] = {0ull, 0ull};
     unpack8(x0v, x0);
     unpack8(x1v, x1);
-    float ss = 0.0f, st = 0.0f;
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      ss = fmaf(x0[u], x0[u], ss);
-      st = fmaf(x1[u], x1[u], st);
+    for (int u = 0; u < 4; ++u) {
+      sq[0] = f2_fma(x0[u], x0[u], sq[0]);
+      sq[1] = f2_fma(x1[u], x1[u], sq[1]);
     }
-    const float r = rsqrtf(fmaf(lane_sum<kLanes>(ss + st), inv_d, n.eps));
+    const float r = rsqrtf(fmaf(lane_sum<kLanes>(f2_sum(f2_add(sq[0], sq[1]))), inv_d, n.eps));
     if (hh >= w.end || !mine) continue;
-    uint16_t* out = target(a, w.t, hh, tok.page);
-    if (hh >= a.Hq + a.Hk) {         // a value: as it is
+    const int kind = kind_of(hh);
+    if (kind != to) {
+      to = kind;
+      out = target(a, w.t, hh, tok.page);
+      if (kind < 2) load_weights(n, kind, c, w0, w1);
+    } else {
+      out += kSlots * (a.append && kind > 0 ? a.c.head_stride : static_cast<int64_t>(a.D));
+    }
+    if (kind == 2) {                 // a value: as it is
       *reinterpret_cast<uint4*>(out + c.c0) = x0v;
       *reinterpret_cast<uint4*>(out + c.c1) = x1v;
       continue;
     }
-    if (which != (hh >= a.Hq ? 1 : 0)) {
-      which = hh >= a.Hq ? 1 : 0;
-      load_weights(n, which, c, w0, w1);
-    }
+    const uint64_t r2 = f2_pack(r, r);
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      x0[u] *= r * w0[u];
-      x1[u] *= r * w1[u];
+    for (int u = 0; u < 4; ++u) {
+      x0[u] = f2_mul(x0[u], f2_mul(w0[u], r2));
+      x1[u] = f2_mul(x1[u], f2_mul(w1[u], r2));
     }
     turn<kLanes>(c, a.interleaved, cs, j, x0, x1);
     *reinterpret_cast<uint4*>(out + c.c0) = pack8(x0);
@@ -310,12 +337,12 @@ __global__ void __launch_bounds__(kThreads) norm_rope_any_kernel(const __grid_co
 // Gradient.  a.r holds dy (q, k) and dx (qo, ko) and turns back (inverse).
 template <int kLanes>
 __global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(const __grid_constant__ NormArgs n, const Split split_q, const Split split_k) {
-  extern __shared__ __align__(16) float2 angles[];       // [warp][4][kLanes] pairs of pairs, sums [warp][D]
+  extern __shared__ __align__(16) float angles[];        // [warp][4][kLanes][4], sums [warp][D]
   constexpr int kSlots = 32 / kLanes;
   const RopeArgs& a = n.r;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  float2* cs = angles + warp * 8 * kLanes;
-  float* sums = reinterpret_cast<float*>(angles + kWarps * 8 * kLanes);
+  float* cs = angles + warp * 16 * kLanes;
+  float* sums = angles + kWarps * 16 * kLanes;
   const int j = lane % kLanes;
   const bool mine = 16 * j < a.D;
   const Chunks c = chunks_of(a, j);
@@ -336,9 +363,9 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(con
     const int64_t dxs = which ? a.kos : a.qos;
     const Split split = which ? split_k : split_q;
     const int64_t units = a.T * split.parts;
-    float w0[8], w1[8], acc0[8], acc1[8];
+    uint64_t w0[4], w1[4], acc0[4], acc1[4];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) acc0[u] = acc1[u] = w0[u] = w1[u] = 0.0f;
+    for (int u = 0; u < 4; ++u) acc0[u] = acc1[u] = w0[u] = w1[u] = 0ull;
     if (mine) load_weights(n, which, c, w0, w1);
     uint4 g0v = make_uint4(0u, 0u, 0u, 0u), g1v = g0v, x0v = g0v, x1v = g0v;
     auto load = [&](int64_t t, int h) {
@@ -370,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(con
       pos = next_pos;
 #pragma unroll 1
       for (int i = w.first; i < w.end; i += kSlots) {
-        float g0[8], g1[8], x0[8], x1[8];
+        uint64_t g0[4], g1[4], x0[4], x1[4];
         unpack8(g0v, g0);
         unpack8(g1v, g1);
         unpack8(x0v, x0);
@@ -381,25 +408,28 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(con
         h = last ? next.first + lane / kLanes : h + kSlots;
         if (mine && (last ? more && h < next.end : h < w.end)) load(last ? next.t : w.t, h);
         turn<kLanes>(c, a.interleaved, cs, j, g0, g1);
-        float ss = 0.0f, su = 0.0f;
+        uint64_t sq[2] = {0ull, 0ull}, sx[2] = {0ull, 0ull}, u0[4], u1[4];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          ss = fmaf(x0[u], x0[u], ss);
-          ss = fmaf(x1[u], x1[u], ss);
-          su = fmaf(g0[u] * w0[u], x0[u], su);
-          su = fmaf(g1[u] * w1[u], x1[u], su);
+        for (int u = 0; u < 4; ++u) {
+          u0[u] = f2_mul(g0[u], w0[u]);
+          u1[u] = f2_mul(g1[u], w1[u]);
+          sq[0] = f2_fma(x0[u], x0[u], sq[0]);
+          sq[1] = f2_fma(x1[u], x1[u], sq[1]);
+          sx[0] = f2_fma(u0[u], x0[u], sx[0]);
+          sx[1] = f2_fma(u1[u], x1[u], sx[1]);
         }
-        ss = lane_sum<kLanes>(ss);
-        su = lane_sum<kLanes>(su);
+        const float ss = lane_sum<kLanes>(f2_sum(f2_add(sq[0], sq[1])));
+        const float su = lane_sum<kLanes>(f2_sum(f2_add(sx[0], sx[1])));
         if (hh >= w.end || !mine) continue;
         const float r = rsqrtf(fmaf(ss, inv_d, n.eps));
-        const float m = r * r * su * inv_d;
+        const float m = -(r * r * su * inv_d);
+        const uint64_t r2 = f2_pack(r, r), m2 = f2_pack(m, m);
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          acc0[u] = fmaf(g0[u], x0[u] * r, acc0[u]);
-          acc1[u] = fmaf(g1[u], x1[u] * r, acc1[u]);
-          g0[u] = r * (g0[u] * w0[u] - x0[u] * m);
-          g1[u] = r * (g1[u] * w1[u] - x1[u] * m);
+        for (int u = 0; u < 4; ++u) {
+          acc0[u] = f2_fma(g0[u], f2_mul(x0[u], r2), acc0[u]);
+          acc1[u] = f2_fma(g1[u], f2_mul(x1[u], r2), acc1[u]);
+          g0[u] = f2_mul(f2_fma(x0[u], m2, u0[u]), r2);
+          g1[u] = f2_mul(f2_fma(x1[u], m2, u1[u]), r2);
         }
         uint16_t* out = dx + w.t * dxs + hh * a.D;
         *reinterpret_cast<uint4*>(out + c.c0) = pack8(g0);
@@ -409,20 +439,26 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(con
     }
     if (n.partial == nullptr) continue;
     // the lanes of one column: within the warp, then the warps in order
+    float col[2][8];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      f2_unpack(acc0[u], col[0][2 * u], col[0][2 * u + 1]);
+      f2_unpack(acc1[u], col[1][2 * u], col[1][2 * u + 1]);
+    }
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
 #pragma unroll
       for (int off = 16; off >= kLanes; off >>= 1) {
-        acc0[u] += __shfl_xor_sync(0xffffffffu, acc0[u], off);
-        acc1[u] += __shfl_xor_sync(0xffffffffu, acc1[u], off);
+        col[0][u] += __shfl_xor_sync(0xffffffffu, col[0][u], off);
+        col[1][u] += __shfl_xor_sync(0xffffffffu, col[1][u], off);
       }
     }
     __syncthreads();               // (the sums of the queries are read)
     if (lane < kLanes && mine) {
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
-        sums[warp * a.D + c.c0 + u] = acc0[u];
-        sums[warp * a.D + c.c1 + u] = acc1[u];
+        sums[warp * a.D + c.c0 + u] = col[0][u];
+        sums[warp * a.D + c.c1 + u] = col[1][u];
       }
     }
     __syncthreads();
