@@ -39,7 +39,7 @@
 // launches, every CTA works out its own jobs (one token over 1,000 keys 10.9 us in a graph).  The tiles in sight are
 // the row's first ones and the window's, with one leap between; only they are loaded, only those that a bound cuts
 // are masked, and warps 2 and 3 clear the V rows that no token of the job sees.  128 sequences of one to
-// four tokens, 4,096 keys and 8 key heads: 328 us for 2.03 GB, 6.2 TB/s, 84 % of a kernel that only reads; 4 chunks of
+// four tokens, 4,096 keys and 8 key heads: 327 us for 2.03 GB, 6.2 TB/s, 84 % of a kernel that only reads; 4 chunks of
 // 1,775 tokens of 40 heads through 4,096 keys and 64 first ones: 584 us, 1,070 TFLOP/s, 55 % of the measured rate:
 // jobs have 35 tiles, and the softmax's start and end of a job are not hidden.
 //

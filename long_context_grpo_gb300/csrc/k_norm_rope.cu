@@ -10,10 +10,10 @@
 // lanes share a head, a lane two 16-byte chunks (in the half layout the two whose values turn together), so
 // that a head's sums take three shuffles at D = 128, and the lane's weights stay in its registers over all
 // the heads that it walks.  The next head's chunks are on their way while this one's are at work.
-// 48 heads of 128: 8,192 tokens 43 us (201 MB, 4.7 TB/s), 32,768 tokens 143 us (5.6 TB/s; the rotation alone, with
-// half the arithmetic, 123); appending 14,000 tokens of 80 heads 105 us (566 MB, 5.4 TB/s; without norms 93).  About
-// 290 instructions for four heads of a warp: the issue slots are half full.
-// Gradient: 3,001 tokens 32 us with its two launches in a graph (25 of them the first one's), 32,768 tokens 224 us.
+// 48 heads of 128: 8,192 tokens 41 us in a graph (201 MB, 4.9 TB/s), 32,768 tokens 139 us (5.8 TB/s; the rotation
+// alone 36 and 123); appending 14,000 tokens of 80 heads 101 us (566 MB, 5.6 TB/s; without norms 93).
+// Gradient: 3,001 tokens 31 us with its two launches in a graph (25 of them the first one's), 32,768 tokens 222 us
+// (5.4 TB/s): 16 warps an SM at 128 registers hold 32 KB in flight.
 // Weight gradients: a lane's 16 columns in registers over all heads and tokens that it walks, a row of partial
 // sums a block, summed in a fixed order by a second kernel (no atomics).
 // Element path (a warp a head) for rows that are not 16-byte aligned, D not a multiple of 16 or rot_dim
