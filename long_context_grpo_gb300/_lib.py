@@ -35,7 +35,7 @@ class LongStrawError(RuntimeError):
 
 def _keys(n: int) -> int:
     """A number of keys as the library takes it: one past 64 bits would reach it cut off."""
-    return min(max(n, -1), 1 << 62)
+    return n if 0 <= n <= 1 << 62 else (-1 if n < 0 else 1 << 62)
 
 
 class PrefixDesc(ctypes.Structure):

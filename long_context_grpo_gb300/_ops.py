@@ -49,6 +49,14 @@ def _opt(t, name, dtype, shape, dev):
     return 0 if t is None else _ptr(t, name, dtype, shape, dev)
 
 
+def _out(t, name, dtype, shape, dev, at):
+    """(tensor, address) of an output: the one given, or a new one."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=at)
+        return t, t.data_ptr()
+    return t, _ptr(t, name, dtype, shape, dev)
+
+
 def _strided(t, name, shape, strides, width, dev):
     """(pointer, elements between rows) of a bf16 tensor of this shape whose dimensions behind
     the first have these strides; the rows hold `width` values each."""
@@ -177,19 +185,13 @@ def token_scores(logits, ids, top: int = 0, temperature: float = 1.0, logp=None,
     at = logits.device
     x, ldx = _strided(logits, "logits", (T, V), (1,), V, dev)
     n, nt = (T,), (T, max(top, 0))
-    if logp is None:
-        logp = torch.empty(n, dtype=_f32, device=at)
-    if lse is None:
-        lse = torch.empty(n, dtype=_f32, device=at)
-    if entropy is None:
-        entropy = torch.empty(n, dtype=_f32, device=at)
-    if top_ids is None:
-        top_ids = torch.empty(nt, dtype=_i32, device=at)
-    if top_logp is None:
-        top_logp = torch.empty(nt, dtype=_f32, device=at)
-    d = _SCORES.pack(T, V, ldx, x, _ptr(ids, "ids", _i32, n, dev), temperature, top, _ptr(logp, "logp", _f32, n, dev),
-                     _ptr(lse, "lse", _f32, n, dev), _ptr(entropy, "entropy", _f32, n, dev),
-                     _ptr(top_ids, "top_ids", _i32, nt, dev), _ptr(top_logp, "top_logp", _f32, nt, dev))
+    y = _ptr(ids, "ids", _i32, n, dev)
+    logp, lp = _out(logp, "logp", _f32, n, dev, at)
+    lse, ls = _out(lse, "lse", _f32, n, dev, at)
+    entropy, ep = _out(entropy, "entropy", _f32, n, dev, at)
+    top_ids, ti = _out(top_ids, "top_ids", _i32, nt, dev, at)
+    top_logp, tl = _out(top_logp, "top_logp", _f32, nt, dev, at)
+    d = _SCORES.pack(T, V, ldx, x, y, temperature, top, lp, ls, ep, ti, tl)
     b._check(b._lib().ls_token_scores(d, _raw_stream(dev)), "ls_token_scores")
     return TokenScores(logp, lse, entropy, top_ids, top_logp)
 
