@@ -230,6 +230,10 @@ def _stream(stream=None) -> int:
 def _ptr(t, name, dtype, shape=None):
     if t is None:
         return None
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.is_contiguous()
+            and (shape is None or t.shape == shape)):
+        return t.data_ptr()
+    # (what follows says what is wrong with it)
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError("%s must be a CUDA tensor" % name)
     if t.dtype != dtype:
@@ -307,9 +311,8 @@ class Prefix:
         dq = torch.empty_like(q) if dq is None else dq
         dk_suffix = torch.empty_like(k_suffix) if dk_suffix is None else dk_suffix
         dv_suffix = torch.empty_like(v_suffix) if dv_suffix is None else dv_suffix
-        need = self.bwd_workspace_bytes(R)
         if workspace is None:
-            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+            workspace = torch.empty(max(self.bwd_workspace_bytes(R), 16), dtype=torch.uint8, device=q.device)
         _check(_lib().ls_replay_bwd(
             self._h, R,
             _ptr(q, "q", torch.bfloat16, (R, self.Hq, self.D)),
@@ -425,9 +428,8 @@ class Prefix:
         0 .. prefix_len+R-1 added into the accumulators."""
         R = q.shape[0]
         dq = torch.empty_like(q) if dq is None else dq
-        need = self.bwd_workspace_bytes(R)
         if workspace is None:
-            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+            workspace = torch.empty(max(self.bwd_workspace_bytes(R), 16), dtype=torch.uint8, device=q.device)
         _check(_lib().ls_block_replay_bwd(
             self._h, prefix_len, R,
             _ptr(q, "q", torch.bfloat16, (R, self.Hq, self.D)),
