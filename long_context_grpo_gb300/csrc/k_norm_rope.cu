@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_any_kernel(const __grid_co
 // Gradient.  a.r holds dy (q, k) and dx (qo, ko) and turns back (inverse).
 template <int kLanes>
 __global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(const __grid_constant__ NormArgs n, const Split split_q, const Split split_k) {
-  extern __shared__ __align__(16) float angles[];        // [warp][4][kLanes][4], sums [warp][D]
+  extern __shared__ __align__(16) float angles[];        // [warp][4][kLanes][4], sums [2][warp][D]
   constexpr int kSlots = 32 / kLanes;
   const RopeArgs& a = n.r;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -453,21 +453,26 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(con
         col[1][u] += __shfl_xor_sync(0xffffffffu, col[1][u], off);
       }
     }
-    __syncthreads();               // (the sums of the queries are read)
     if (lane < kLanes && mine) {
+      float* to = sums + (which * kWarps + warp) * a.D;
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        sums[warp * a.D + c.c0 + u] = col[0][u];
-        sums[warp * a.D + c.c1 + u] = col[1][u];
+      for (int u = 0; u < 8; u += 4) {
+        *reinterpret_cast<float4*>(to + c.c0 + u) = make_float4(col[0][u], col[0][u + 1], col[0][u + 2], col[0][u + 3]);
+        *reinterpret_cast<float4*>(to + c.c1 + u) = make_float4(col[1][u], col[1][u + 1], col[1][u + 2], col[1][u + 3]);
       }
     }
-    __syncthreads();
-    for (int d = tid; d < a.D; d += kThreads) {
-      float s = 0.0f;
+  }
+  if (n.partial == nullptr) return;
+  // (one wait for both kinds: a warp goes from its queries to its keys without the others)
+  __syncthreads();
+  for (int d = tid; d < 2 * a.D; d += kThreads) {
+    const int which = d < a.D ? 0 : 1;
+    if ((which ? a.Hk : a.Hq) == 0) continue;
+    const float* of = sums + which * (kWarps - 1) * a.D + d;       // (d counts the first kind's columns too)
+    float s = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) s += sums[w * a.D + d];
-      n.partial[(static_cast<int64_t>(blockIdx.x) * 2 + which) * a.D + d] = s;
-    }
+    for (int w = 0; w < kWarps; ++w) s += of[w * a.D];
+    n.partial[static_cast<int64_t>(blockIdx.x) * 2 * a.D + d] = s;
   }
 }
 
@@ -631,7 +636,7 @@ cudaError_t launch_norm_rope_bwd(const NormArgs& n, float* dwq, float* dwk, cuda
   if (lanes == 0) {
     norm_rope_bwd_any_kernel<<<grid, kThreads, (a.rot / 2) * sizeof(float2), s>>>(n);
   } else {
-    const size_t smem = angles_bytes(lanes) + kWarps * static_cast<size_t>(a.D) * sizeof(float);
+    const size_t smem = angles_bytes(lanes) + 2 * kWarps * static_cast<size_t>(a.D) * sizeof(float);
     const int64_t warps = static_cast<int64_t>(grid) * kWarps;
     const Split q = split_of(a.T, a.Hq > 0 ? a.Hq : 1, lanes, warps, 1.0), k = split_of(a.T, a.Hk > 0 ? a.Hk : 1, lanes, warps, 1.0);
     switch (lanes) {
