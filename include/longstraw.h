@@ -116,8 +116,9 @@ ls_status ls_prefix_prepare(const ls_prefix_desc* desc, ls_prefix_t* out, void* 
  * `window` keys up to their own and the sequence's first `sinks` (the sequence: prompt and response; query
  * t of a response has position P + t and sees the keys j <= P + t with j > P + t - window or j < sinks).
  * Holds for ls_replay_fwd/bwd, the packed and the blockwise replay (there the position is prefix_len + t); the
- * softmax, its gradients and the accumulators are as without it, with the other keys left out: they
- * are neither read nor, in the accumulators, written.  A forward and its backward have to be made
+ * softmax, its gradients and the accumulators are as without it, with the other keys left out: their
+ * rows of the accumulators are left as they are.  (Keys are visited in tiles of 128: those of a tile
+ * with keys in sight have to be finite, as without a window.)  A forward and its backward have to be made
  * under the same window; the backward's workspace is asked for after it is set (it needs 256 bytes
  * more).  The prompt-only calls return LS_ERR_UNSUPPORTED.  window >= 1 and sinks >= 0,
  * either may pass the sequence; window = 0 with sinks = 0 takes the window away.
