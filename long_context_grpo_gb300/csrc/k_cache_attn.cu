@@ -35,13 +35,14 @@
 //   writes zeros for tokens that see no key.
 //
 // Through a window (cache_attn_kernel<D, wide, true> and window_join_kernel) a token sees the last keys up to its own
-// and the first ones of its sequence.  A Q tile sees a bounded number of tiles, so no plan is needed: two or three
-// launches, every CTA works out its own jobs (one token over 1,000 keys 10.9 us in a graph).  The tiles in sight are
-// the row's first ones and the window's, with one leap between; only they are loaded, only those that a bound cuts
-// are masked, and warps 2 and 3 clear the V rows that no token of the job sees.  128 sequences of one to
-// four tokens, 4,096 keys and 8 key heads: 327 us for 2.03 GB, 6.2 TB/s, 84 % of a kernel that only reads; 4 chunks of
-// 1,775 tokens of 40 heads through 4,096 keys and 64 first ones: 584 us, 1,070 TFLOP/s, 55 % of the measured rate:
-// jobs have 35 tiles, and the softmax's start and end of a job are not hidden.
+// and the first ones of its sequence.  A Q tile sees a bounded number of tiles, so no plan is needed: every CTA works
+// out its own jobs, in one to three launches (narrow; wide for long runs of tokens; a join where units are cut; one
+// token over 1,000 keys 10.8 us in a graph).  The tiles in sight are the row's first ones and the window's, with one
+// leap between; only they are loaded, only those that a bound cuts are masked, and warps 2 and 3 clear the V rows that
+// no token of the job sees.  128 sequences of one to four tokens, 4,096 keys and 8 key heads: 325 us for 2.03 GB,
+// 6.2 TB/s, 85 % of a kernel that only reads; 4 chunks of 1,775 tokens of 40 heads through 4,096 keys and 64 first
+// ones: 584 us, 1,070 TFLOP/s, 55 % of the measured rate: jobs have 35 tiles, and the softmax's start and end of a job
+// are not hidden.
 //
 // V rows behind a sequence's end are cleared in shared memory before the MMA (0 x NaN); pages
 // outside the pool read as zeros (the TMA's fill).  P is rounded to bf16, the type of V, for the
@@ -613,6 +614,36 @@ __device__ __forceinline__ int window_start(const CacheView& c, const Window& w,
   }
   __syncthreads();
   return w.n_jobs;
+}
+
+// Zeros for the tokens that see no key and that no job is made for, 32 tokens a warp of each CTA (all of
+// them where the offsets are refused; none behind the last sequence).
+__device__ __forceinline__ void window_empty(const CacheView& c, const Window& w, bool bad, uint16_t* o, float* lse, int lane) {
+  const int g = c.Hq / c.Hkv;
+  for (int64_t first = static_cast<int64_t>(blockIdx.x) * 32; first < w.T; first += static_cast<int64_t>(gridDim.x) * 32) {
+    const int64_t t = first + lane;
+    int lo = 0, hi = t < w.T ? w.S : 0; // entries [0, lo) end at or before t, [hi, S) do not
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (w.cu[mid + 1] <= t) lo = mid + 1; else hi = mid;
+    }
+    bool empty = t < w.T && lo < w.S && t >= w.cu[lo];
+    if (empty && !bad) {
+      const int c0 = w.cu[lo], n = w.cu[lo + 1] - c0;
+      const bool wide = n > kNarrowRows / g;
+      const int per = wide ? 2 * (128 / g) : kNarrowRows / g;
+      const int t0 = c0 + (static_cast<int>(t) - c0) / per * per;
+      empty = window_sight(c, w, lo, t0, per, wide, nullptr).tiles == 0;
+    }
+    uint32_t todo = __ballot_sync(0xffffffffu, empty);
+    while (todo != 0) {
+      const int64_t at = first + __ffs(todo) - 1;
+      todo &= todo - 1;
+      for (int i = lane; i < c.Hq * c.D / 8; i += 32)
+        reinterpret_cast<uint4*>(o + at * c.Hq * c.D)[i] = make_uint4(0u, 0u, 0u, 0u);
+      for (int h = lane; h < c.Hq; h += 32) lse[at * c.Hq + h] = -INFINITY;
+    }
+  }
 }
 
 // The row's tile that tile v in sight is.
@@ -1384,6 +1415,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++uq;
       }
       if (!ok) *vabort = 1;
+    } else if constexpr (kWin && !kWide) {
+      // (a warp without rows of the narrow kernel, which runs in every call: at the end of another warp's jobs
+      // its chains of loads took 2 us of 172)
+      if (warp == 4 + kNarrowRows / 32) window_empty(a.c, a.w, n_jobs == 0, a.o, a.lse, lane);
     }
   }
 
@@ -1514,13 +1549,11 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
   if (lane == 0) a.lse[out] = l == 0.0f ? -INFINITY : (m + __log2f(l)) * kLn2;
 }
 
-// The end of a call through a window.  The first blocks write the tokens that see no key, a thread a
-// token; the others join the partial results of the units that were cut, kPer warps a row, in chunk
-// order.  Nothing is done for rows that the attention kernels have written.
+// The end of a call through a window that has cut units: their partial results are joined, kPer warps a row, in
+// chunk order.  Nothing is done for rows that the attention kernels have written.
 struct WindowJoinArgs {
   CacheView c;
   Window w[2];                    // narrow, wide
-  int token_blocks;
   int64_t rows[2];                // partial rows of a chunk of all units that are cut
   const float* part_o;
   const float* part_lse;
@@ -1534,36 +1567,7 @@ __global__ void __launch_bounds__(kJoinThreads) window_join_kernel(const __grid_
   __shared__ float so[kPer > 1 ? kJoinWarps : 1][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = a.c.Hq / a.c.Hkv;
-  if (static_cast<int>(blockIdx.x) < a.token_blocks) {
-    const Window& w = a.w[0];
-    const int64_t t = static_cast<int64_t>(blockIdx.x) * kJoinThreads + threadIdx.x;
-    int lo = 0, hi = t < w.T ? w.S : 0; // entries [0, lo) end at or before t, [hi, S) do not
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (w.cu[mid + 1] <= t) lo = mid + 1; else hi = mid;
-    }
-    bool empty = false;
-    if (t < w.T && lo < w.S && t >= w.cu[lo]) {
-      const int c0 = w.cu[lo], n = w.cu[lo + 1] - c0;
-      const bool wide = n > kNarrowRows / g;
-      const int per = wide ? 2 * (128 / g) : kNarrowRows / g;
-      const int t0 = c0 + (static_cast<int>(t) - c0) / per * per;
-      empty = window_sight(a.c, w, lo, t0, per, wide, nullptr).tiles == 0;
-    }
-    pdl_wait();
-    if (*w.bad != 0) empty = t < w.T && lo < w.S && t >= w.cu[lo];
-    uint32_t todo = __ballot_sync(0xffffffffu, empty);
-    const int64_t first = t - lane;
-    while (todo != 0) {
-      const int64_t at = first + __ffs(todo) - 1;
-      todo &= todo - 1;
-      for (int i = lane; i < a.c.Hq * D / 8; i += 32)
-        reinterpret_cast<uint4*>(a.o + at * a.c.Hq * D)[i] = make_uint4(0u, 0u, 0u, 0u);
-      for (int h = lane; h < a.c.Hq; h += 32) a.lse[at * a.c.Hq + h] = -INFINITY;
-    }
-    return;
-  }
-  int64_t x = ((static_cast<int64_t>(blockIdx.x) - a.token_blocks) * kJoinWarps + warp) / kPer;
+  int64_t x = (static_cast<int64_t>(blockIdx.x) * kJoinWarps + warp) / kPer;
   const int cls = x < a.rows[0] ? 0 : 1;
   if (cls == 1) x -= a.rows[0];
   Sight s;
@@ -1607,7 +1611,8 @@ __global__ void __launch_bounds__(kJoinThreads) window_join_kernel(const __grid_
 #pragma unroll
     for (int i = 0; i < kV; ++i) acc[i] *= f;
     const int cnt = total - p0 < 32 ? total - p0 : 32;
-#pragma unroll 4
+    // (four at a time take the registers of a block an SM: 64 sequences through 4,096 keys 174.2 us, so 171.5)
+#pragma unroll 2
     for (int k = warp % kPer; k < cnt; k += kPer) {
       const float wk = __shfl_sync(0xffffffffu, e, k);
       const float* src = a.part_o + (first + (p0 + k) * step) * D + lane * kV;
@@ -1903,7 +1908,6 @@ cudaError_t launch_cache_window(const CacheAttnArgs& a, const CacheWindowLayout&
   }
   WindowJoinArgs j{};
   j.c = a.c;
-  j.token_blocks = static_cast<int>((a.T + kJoinThreads - 1) / kJoinThreads);
   for (int cls = 0; cls < 2; ++cls) {
     j.w[cls] = both[cls];
     j.rows[cls] = l.chunks[cls] > 1 ? (l.units[cls] - l.whole[cls]) * l.unit_rows[cls] : 0;
@@ -1913,12 +1917,13 @@ cudaError_t launch_cache_window(const CacheAttnArgs& a, const CacheWindowLayout&
   j.o = a.o;
   j.lse = a.lse;
   const int64_t rows = j.rows[0] + j.rows[1];
+  if (rows == 0) return cudaSuccess;
   if (rows <= 16 * num_sms()) {       // few rows have many parts each: a block a row
-    const dim3 grid(static_cast<unsigned>(j.token_blocks + rows));
+    const dim3 grid(static_cast<unsigned>(rows));
     return a.c.D == 128 ? launch_after(window_join_kernel<128, kJoinWarps>, grid, kJoinThreads, 0, s, j)
                         : launch_after(window_join_kernel<64, kJoinWarps>, grid, kJoinThreads, 0, s, j);
   }
-  const dim3 grid(static_cast<unsigned>(j.token_blocks + (rows + kJoinWarps - 1) / kJoinWarps));
+  const dim3 grid(static_cast<unsigned>((rows + kJoinWarps - 1) / kJoinWarps));
   return a.c.D == 128 ? launch_after(window_join_kernel<128, 1>, grid, kJoinThreads, 0, s, j)
                       : launch_after(window_join_kernel<64, 1>, grid, kJoinThreads, 0, s, j);
 }
