@@ -83,8 +83,9 @@ __device__ __forceinline__ uint4 load8(const uint16_t* x, int64_t i, int64_t end
 // Sums are kept of 2^z, z = x scale2 - r, r = m scale2 rounded, m the largest logit of theirs: one fused
 // product and difference an exponent, right to 2^-24 of it.  The logits that equal m are counted instead, 1 each
 // (m's own z is only the rounding of r).  Where r is past kFar, or m is -inf, z is (x - m) scale2: any two
-// logits there differ by more than fp32's exponents hold.
-constexpr float kFar = 1e30f;
+// logits there differ by 2^-9 of the larger or more, so z is below -2^13 for all but the counted ones, and the rounding
+// of r, half an ulp of it, stays below 1 (past 2^34 it would pass fp32's exponents, whose 2^z is then no correction).
+constexpr float kFar = 8388608.0f;       // 2^23
 __device__ __forceinline__ float reference(float m, float scale2) { return m * scale2; }
 
 // Sums with the largest logit m and reference r, for a larger one.
