@@ -540,18 +540,20 @@ __global__ void __launch_bounds__(kThreads) scores_bwd_kernel(const __grid_const
   if (wild && begin == 0 && tid == 0) set_device_status(a.status, DEV_BAD_INDEX);
   // a row that nothing is asked of is not looked at
   const bool zero = wild || (dl == 0.0f && de == 0.0f);
-  const float lse2 = zero ? 0.0f : a.lse[row] * kLog2e;
+  const float base = zero ? 0.0f : fmaf(a.lse[row], kLog2e, -a.lift);
   const float ent = zero || a.d_entropy == nullptr ? 0.0f : a.entropy[row];
   dl *= a.scale;
   de *= a.scale;
-  // d = -p (dl + de (log p + entropy)) = -p (k0 + k1 z), z = log2 p (a row without a distribution stays NaN)
-  const float k0 = fmaf(de, ent, dl) + (lse2 - lse2), k1 = de * static_cast<float>(kLn2);
+  // d = -p (dl + de (log p + entropy)) / t = -2^z (k0 + k1 z), z = log2 p + lift (a row without a distribution stays
+  // NaN).  1 / t is scale 2^lift, and its second part is the exponentials': dl / t may pass fp32 where p is 0.
+  const float k1 = de * static_cast<float>(kLn2), k0 = fmaf(-k1, a.lift, fmaf(de, ent, dl)) + (base - base);
   float own = 0.0f;
   if (!zero && y >= begin && y < begin + kStep) {
     // 1 - p from the log-probability itself: exact where p is close to 1
     const float lp = a.logp[row];
     own = -expm1f(lp) * dl;
     if (de != 0.0f) own -= de * expf(lp) * (fmaxf(lp, -1000.0f) + ent);
+    own *= a.lifted;
   }
   uint4 v[kUnroll];
 #pragma unroll
@@ -567,15 +569,20 @@ __global__ void __launch_bounds__(kThreads) scores_bwd_kernel(const __grid_const
     const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
     uint32_t o[4] = {0u, 0u, 0u, 0u};
     if (!zero) {
-      const int at = y >= i && y < i + 8 ? static_cast<int>(y - i) : -1;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const float z0 = fmaxf(fmaf(lo_bf16(w[k]), a.scale2, -lse2), -1000.0f);
-        const float z1 = fmaxf(fmaf(hi_bf16(w[k]), a.scale2, -lse2), -1000.0f);
-        float d0 = -ex2_approx(z0) * fmaf(k1, z0, k0), d1 = -ex2_approx(z1) * fmaf(k1, z1, k0);
-        if (at == 2 * k) d0 = own;
-        if (at == 2 * k + 1) d1 = own;
-        o[k] = pack_bf16x2(d0, d1);
+        const float z0 = fmaxf(fmaf(lo_bf16(w[k]), a.scale2, -base), -1000.0f);
+        const float z1 = fmaxf(fmaf(hi_bf16(w[k]), a.scale2, -base), -1000.0f);
+        o[k] = pack_bf16x2(-ex2_approx(z0) * fmaf(k1, z0, k0), -ex2_approx(z1) * fmaf(k1, z1, k0));
+      }
+      if (y >= i && y < i + 8) {       // (one chunk of a row has the given token: no select in the others)
+        const int at = static_cast<int>(y - i);
+        const uint32_t b = pack_bf16x2(own, own);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (at == 2 * k) o[k] = __byte_perm(o[k], b, 0x3254);
+          if (at == 2 * k + 1) o[k] = __byte_perm(o[k], b, 0x5410);
+        }
       }
     }
     if (kVec) {

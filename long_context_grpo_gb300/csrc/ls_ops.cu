@@ -2,6 +2,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "../../include/longstraw.h"
@@ -180,7 +181,10 @@ ls_status ls_token_scores_bwd(const ls_token_scores_bwd_desc* d, void* stream) {
   a.entropy = d->entropy;
   a.d_logp = d->d_logp;
   a.d_entropy = d->d_entropy;
-  a.scale = static_cast<float>(1.0 / d->temperature);
+  const int lift = std::max(std::ilogb(1.0 / d->temperature), 0);
+  a.scale = static_cast<float>(std::ldexp(1.0 / d->temperature, -lift));
+  a.lift = static_cast<float>(lift);
+  a.lifted = std::ldexp(1.0f, lift);
   a.scale2 = static_cast<float>(1.4426950408889634074 / d->temperature);
   a.dlogits = static_cast<uint16_t*>(d->dlogits);
   a.status = status;

@@ -66,7 +66,8 @@ struct ScoresBwdArgs {
   const float* entropy;       // or nullptr without d_entropy
   const float* d_logp;        // or nullptr
   const float* d_entropy;     // or nullptr
-  float scale, scale2;
+  float scale, lift, lifted;  // 1 / temperature = scale lifted, lifted = 2^lift, lift a whole number >= 0, scale < 2
+  float scale2;
   uint16_t* dlogits;          // row t at dlogits + t * ldd; may be the logits
   uint32_t* status;
   int rows_y;                 // rows of the grid's second dimension (set by the launch)

@@ -4,6 +4,7 @@ import numpy as np
 import pytest
 import torch
 
+from oracle.scores import scores_grad
 from test_token_scores import check
 
 COLD = [10.0 ** -k for k in range(1, 37)]
@@ -42,3 +43,48 @@ def test_scores_of_large_logits(scale):
         x, ids = rows(V, 1.0, around, V, scale)
         check(ls.token_scores(x, ids, top=4), x, ids, 4, 1.0)
     assert ls.device_status() == (0, 0)
+
+
+def grad_check(got, x, ids, dl, de, t, lse):
+    """Every value of the gradient.  log p is right to 4 x 2^-24 |lse| (lse as it is given, its product with
+    log2 e, the temperature's factor, the fused difference) or, past 1,024, to what its parts relative to the row's
+    maximum are, and to 2^-23 of itself; an exponential to 2^-22, products to 2^-22; both hold 1 / t's exponent (2^-23 of it); probabilities below 2^-126 may be 0."""
+    x, dl, de, lse = (a.double().cpu().numpy() for a in (x, dl, de, lse))
+    i = ids.cpu().numpy()
+    want = scores_grad(x, i, dl, de, t)
+    z = x / t
+    m = z.max(1, keepdims=True)
+    logp = np.maximum(z - m - np.log(np.exp(z - m).sum(1, keepdims=True)), -1000.0)
+    p = np.exp(logp)
+    ent = -(p * logp).sum(1)
+    dl, de, ent = np.abs(dl)[:, None], np.abs(de)[:, None], ent[:, None]
+    off = 4 * 2.0 ** -24 * np.minimum(np.abs(lse), 1024.0)[:, None] + 2.0 ** -23 * np.abs(logp) + 2.0 ** -21
+    off += 2.0 ** -23 * max(0.0, -np.log2(t))
+    size = (dl + de * (np.abs(logp) + ent + 1.0)) / t
+    room = 2.0 ** -8 * np.abs(want) + (p * off + 2.0 ** -126) * size + 2.0 ** -133
+    at = (np.arange(len(x)), i)
+    # the given token's 1 - p: expm1 of a log-probability rounded to fp32 (at most 2^-24 x p |log p|, below 2^-25)
+    room[at] += 2.0 ** -22 * dl[:, 0] / t
+    g = got.double().cpu().numpy()
+    assert np.isfinite(g).all()
+    err = np.abs(g - want)
+    assert (err <= room).all(), (err / room).max()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("temperature", [2.0 ** -120, 1e-36, 2.0 ** 120])
+def test_gradient_at_the_ends(temperature):
+    """Gradients of ordinary size whose quotient by the temperature is past fp32 only where a probability is not 0."""
+    import long_context_grpo_gb300 as ls
+    x = torch.zeros(4, 3000, dtype=torch.bfloat16)
+    x[:, 7] = 2.0
+    x[1, 9:] = float("-inf")
+    x = x.cuda()
+    ids = torch.tensor([7, 7, 7, 7], dtype=torch.int32, device="cuda")
+    dl, de = torch.tensor([1000.0, -3.0, 0.0, 1.0], device="cuda"), torch.tensor([0.0, 1.0, -50.0, 1.0], device="cuda")
+    r = ls.token_scores(x, ids, temperature=temperature)
+    got = ls.token_scores_bwd(x, ids, r.logp, r.lse, r.entropy, dl, de, temperature=temperature).double().cpu()
+    if temperature < 1:             # the largest logit has all of the probability: nothing moves it
+        assert not got.any()
+    else:
+        assert torch.isfinite(got).all()
