@@ -17,7 +17,7 @@
 //   Bound by HBM without alternatives (4,096 rows of 151,936: 190 us, 6.5 TB/s); with 20 of them (228 us) a row's
 //   end, a chain of eight barriers, keeps a ninth of the SM's CTAs from reading.  128 threads and nine CTAs an SM: with
 //   256 threads 281 us, one CTA an SM fed by bulk copies, with warps of its own for the alternatives, 291.
-// scores_bwd_kernel: one pass, a block 4,096 logits of a row (1,279 rows of 151,936: 110 us, 7.05 TB/s).
+// scores_bwd_kernel: one pass, a block 4,096 logits of a row, but for rows whose lse is far from zero (1,279 rows of 151,936: 110 us, 7.05 TB/s).
 #include <type_traits>
 
 #include "ls_internal.h"
@@ -526,6 +526,97 @@ __global__ void __launch_bounds__(kThreads, 9) scores_kernel(const __grid_consta
 }
 
 // --------------------------------------------------------------------------------------
+// Past this |lse|, p = 2^(x log2 e / t - lse log2 e) from an lse rounded to fp32 would be off by more than 2^-10 (4 x 2^-24
+// |lse|: lse, log2 e, 1 / t and their products), half of what the gradient's own rounding is.
+constexpr float kFarLse = 4096.0f;
+
+// Eight values of a row's gradient from index i on.
+template <bool kVec>
+__device__ __forceinline__ void put8(uint16_t* out, int64_t i, int64_t end, const uint32_t (&o)[4]) {
+  if (kVec) {
+    __stcs(reinterpret_cast<uint4*>(out + i), make_uint4(o[0], o[1], o[2], o[3]));
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (i + k < end) out[i + k] = static_cast<uint16_t>(k & 1 ? o[k / 2] >> 16 : o[k / 2] & 0xFFFFu);
+  }
+}
+// The given token's value in the chunk that has it.
+__device__ __forceinline__ void put_own(uint32_t (&o)[4], int64_t i, int y, float own) {
+  if (y < i || y >= i + 8) return;
+  const int at = static_cast<int>(y - i);
+  const uint32_t b = pack_bf16x2(own, own);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (at == 2 * k) o[k] = __byte_perm(o[k], b, 0x3254);
+    if (at == 2 * k + 1) o[k] = __byte_perm(o[k], b, 0x5410);
+  }
+}
+
+// The gradient of a row with such an lse, by one block (in place no other one may have written any of it): exponents
+// relative to the row's maximum and its sum, both found again.  Three reads of the row, two of them from L2.
+template <bool kVec>
+__device__ __noinline__ void far_row(const ScoresBwdArgs& a, const uint16_t* x, uint16_t* out, int y, float own, float k0,
+                                     float k1) {
+  __shared__ uint32_t sh_top[kWarps];
+  __shared__ double sh_sum[kWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // f(first index, four pairs) for all of the thread's chunks, four loads at a time (-inf behind the row)
+  auto all = [&](auto f) {
+    for (int64_t first = tid * 8; first < a.V; first += kStep) {
+      uint4 v[kUnroll];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int64_t i = first + u * kThreads * 8;
+        v[u] = make_uint4(kNegInf2, kNegInf2, kNegInf2, kNegInf2);
+        if (i < a.V) v[u] = kVec ? __ldcg(reinterpret_cast<const uint4*>(x + i)) : load8<false>(x, i, a.V);
+      }
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+        f(first + u * kThreads * 8, w);
+      }
+    }
+  };
+  uint32_t top2 = kNegInf2;
+  all([&](int64_t, const uint32_t (&w)[4]) { top2 = max2(top2, max2(max2(w[0], w[1]), max2(w[2], w[3]))); });
+  uint32_t top = __reduce_max_sync(0xffffffffu, max(order(top2 & 0xFFFFu), order(top2 >> 16)));
+  if (lane == 0) sh_top[warp] = top;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) top = max(top, sh_top[i]);
+  const float m = value_of(top);
+  float hi = 0.0f, lo = 0.0f;
+  all([&](int64_t, const uint32_t (&w)[4]) {
+    float s = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      s += ex2_approx((lo_bf16(w[k]) - m) * a.scale2) + ex2_approx((hi_bf16(w[k]) - m) * a.scale2);
+    two_sum_acc(hi, lo, s);
+  });
+  double sum = static_cast<double>(hi) + lo;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+  if (lane == 0) sh_sum[warp] = sum;
+  __syncthreads();
+  sum = 0.0;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) sum += sh_sum[i];
+  const float base = static_cast<float>(log2(sum)) - a.lift;
+  all([&](int64_t i, const uint32_t (&w)[4]) {
+    if (i >= a.V) return;
+    uint32_t o[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float z0 = fmaxf(fmaf(lo_bf16(w[k]) - m, a.scale2, -base), -1000.0f);
+      const float z1 = fmaxf(fmaf(hi_bf16(w[k]) - m, a.scale2, -base), -1000.0f);
+      o[k] = pack_bf16x2(-ex2_approx(z0) * fmaf(k1, z0, k0), -ex2_approx(z1) * fmaf(k1, z1, k0));
+    }
+    put_own(o, i, y, own);
+    put8<kVec>(out, i, a.V, o);
+  });
+}
+
 template <bool kVec>
 __global__ void __launch_bounds__(kThreads) scores_bwd_kernel(const __grid_constant__ ScoresBwdArgs a) {
   const int tid = threadIdx.x;
@@ -536,25 +627,32 @@ __global__ void __launch_bounds__(kThreads) scores_bwd_kernel(const __grid_const
   uint16_t* out = a.dlogits + row * a.ldd;
   float dl = a.d_logp != nullptr ? a.d_logp[row] : 0.0f, de = a.d_entropy != nullptr ? a.d_entropy[row] : 0.0f;
   const int y = a.ids[row];
+  const float lse = a.lse[row];
   const bool wild = y < 0 || y >= a.V;
   if (wild && begin == 0 && tid == 0) set_device_status(a.status, DEV_BAD_INDEX);
   // a row that nothing is asked of is not looked at
   const bool zero = wild || (dl == 0.0f && de == 0.0f);
-  const float base = zero ? 0.0f : fmaf(a.lse[row], kLog2e, -a.lift);
+  const float base = zero ? 0.0f : fmaf(lse, kLog2e, -a.lift);
   const float ent = zero || a.d_entropy == nullptr ? 0.0f : a.entropy[row];
   dl *= a.scale;
   de *= a.scale;
   // d = -p (dl + de (log p + entropy)) / t = -2^z (k0 + k1 z), z = log2 p + lift (a row without a distribution stays
   // NaN).  1 / t is scale 2^lift, and its second part is the exponentials': dl / t may pass fp32 where p is 0.
-  const float k1 = de * static_cast<float>(kLn2), k0 = fmaf(-k1, a.lift, fmaf(de, ent, dl)) + (base - base);
-  float own = 0.0f;
-  if (!zero && y >= begin && y < begin + kStep) {
+  const float k1 = de * static_cast<float>(kLn2);
+  float k0 = fmaf(-k1, a.lift, fmaf(de, ent, dl)), own = 0.0f;
+  const bool far = !zero && fabsf(lse) > kFarLse;
+  if (!zero && (far || (y >= begin && y < begin + kStep))) {
     // 1 - p from the log-probability itself: exact where p is close to 1
     const float lp = a.logp[row];
     own = -expm1f(lp) * dl;
     if (de != 0.0f) own -= de * expf(lp) * (fmaxf(lp, -1000.0f) + ent);
     own *= a.lifted;
   }
+  if (far) {
+    if (begin == 0) far_row<kVec>(a, x, out, y, own, k0, k1);
+    return;
+  }
+  k0 += base - base;
   uint4 v[kUnroll];
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
@@ -575,23 +673,9 @@ __global__ void __launch_bounds__(kThreads) scores_bwd_kernel(const __grid_const
         const float z1 = fmaxf(fmaf(hi_bf16(w[k]), a.scale2, -base), -1000.0f);
         o[k] = pack_bf16x2(-ex2_approx(z0) * fmaf(k1, z0, k0), -ex2_approx(z1) * fmaf(k1, z1, k0));
       }
-      if (y >= i && y < i + 8) {       // (one chunk of a row has the given token: no select in the others)
-        const int at = static_cast<int>(y - i);
-        const uint32_t b = pack_bf16x2(own, own);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (at == 2 * k) o[k] = __byte_perm(o[k], b, 0x3254);
-          if (at == 2 * k + 1) o[k] = __byte_perm(o[k], b, 0x5410);
-        }
-      }
+      put_own(o, i, y, own);           // (one chunk of a row has it: no select in the others)
     }
-    if (kVec) {
-      __stcs(reinterpret_cast<uint4*>(out + i), make_uint4(o[0], o[1], o[2], o[3]));
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (i + k < a.V) out[i + k] = static_cast<uint16_t>(k & 1 ? o[k / 2] >> 16 : o[k / 2] & 0xFFFFu);
-    }
+    put8<kVec>(out, i, a.V, o);
   }
 }
 

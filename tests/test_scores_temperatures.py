@@ -47,7 +47,7 @@ def test_scores_of_large_logits(scale):
 
 def grad_check(got, x, ids, dl, de, t, lse):
     """Every value of the gradient.  log p is right to 4 x 2^-24 |lse| (lse as it is given, its product with
-    log2 e, the temperature's factor, the fused difference) or, past 1,024, to what its parts relative to the row's
+    log2 e, the temperature's factor, the fused difference) or, past 4,096, to what its parts relative to the row's
     maximum are, and to 2^-23 of itself; an exponential to 2^-22, products to 2^-22; both hold 1 / t's exponent (2^-23 of it); probabilities below 2^-126 may be 0."""
     x, dl, de, lse = (a.double().cpu().numpy() for a in (x, dl, de, lse))
     i = ids.cpu().numpy()
@@ -58,7 +58,7 @@ def grad_check(got, x, ids, dl, de, t, lse):
     p = np.exp(logp)
     ent = -(p * logp).sum(1)
     dl, de, ent = np.abs(dl)[:, None], np.abs(de)[:, None], ent[:, None]
-    off = 4 * 2.0 ** -24 * np.minimum(np.abs(lse), 1024.0)[:, None] + 2.0 ** -23 * np.abs(logp) + 2.0 ** -21
+    off = 4 * 2.0 ** -24 * np.minimum(np.abs(lse), 4096.0)[:, None] + 2.0 ** -23 * np.abs(logp) + 2.0 ** -21
     off += 2.0 ** -23 * max(0.0, -np.log2(t))
     size = (dl + de * (np.abs(logp) + ent + 1.0)) / t
     room = 2.0 ** -8 * np.abs(want) + (p * off + 2.0 ** -126) * size + 2.0 ** -133
@@ -88,3 +88,47 @@ def test_gradient_at_the_ends(temperature):
         assert not got.any()
     else:
         assert torch.isfinite(got).all()
+
+
+def both(x, ids, temperature, seed):
+    """The gradient of scores and entropies, into a tensor of its own and in place."""
+    import long_context_grpo_gb300 as ls
+    g = torch.Generator().manual_seed(seed)
+    dl, de = (torch.randn(len(ids), generator=g).cuda() for _ in range(2))
+    r = ls.token_scores(x, ids, temperature=temperature)
+    got = ls.token_scores_bwd(x, ids, r.logp, r.lse, r.entropy, dl, de, temperature=temperature)
+    grad_check(got, x, ids, dl, de, temperature, r.lse)
+    y = torch.empty(len(ids), x.shape[1] + 8, dtype=x.dtype, device="cuda").fill_(7.0)
+    y[:, :x.shape[1]] = x
+    z = y[:, :x.shape[1]]
+    assert torch.equal(ls.token_scores_bwd(z, ids, r.logp, r.lse, r.entropy, dl, de, temperature=temperature, dlogits=z), got)
+    assert (y[:, x.shape[1]:] == 7.0).all() and ls.device_status() == (0, 0)
+    only = ls.token_scores_bwd(x, ids, r.logp, r.lse, d_logp=dl, temperature=temperature)
+    grad_check(only, x, ids, dl, 0 * de, temperature, r.lse)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("temperature", [0.03, 0.005] + COLD + [1e3, 1e20])
+@pytest.mark.parametrize("V", [9, 700, 20000])
+def test_gradient_at_every_temperature(V, temperature):
+    for std, around in ((2.0, 10.0), (3.0, -24.0), (40.0, -3000.0)):
+        both(*rows(V, std, around, V), temperature, V)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scale", [10.0 ** k for k in range(1, 37, 5)])
+def test_gradient_of_large_logits(scale):
+    for V, around in ((700, 10.0), (20000, -9.0)):
+        both(*rows(V, 1.0, around, V, scale), 1.0, V)
+
+
+@pytest.mark.gpu
+def test_masked_tokens_of_cold_rows():
+    """Masked logits, the given token among them, where lse is past what exponents from it could hold."""
+    import long_context_grpo_gb300 as ls
+    x, ids = rows(3000, 2.0, 30.0, 1)
+    x[:, 100::3] = float("-inf")
+    ids[::4] = 103
+    r = ls.token_scores(x, ids, temperature=1e-3)
+    dl = torch.ones(len(ids), device="cuda")
+    grad_check(ls.token_scores_bwd(x, ids, r.logp, r.lse, d_logp=dl, temperature=1e-3), x, ids, dl, 0 * dl, 1e-3, r.lse)
