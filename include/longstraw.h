@@ -472,7 +472,8 @@ ls_status ls_rope_freqs(int32_t rot_dim, double theta, int32_t scaling, double f
  * ls_rope (d->inverse has to be 0).  inv_freq NULL with rot_dim 0: norms alone.  All of it in fp32,
  * rounded once.  Tensors, strides, positions and limits as in ls_rope; the outputs may be the inputs.
  *   q_weight, k_weight  device [D], bf16 or fp32 (weight_fp32 for both); NULL: 1, without the offset
- *   eps > 0.  A head with an infinity or NaN gives NaN or what the formula gives; a head of zeros gives 0.
+ *   eps > 0.  A head with an infinity or NaN gives NaN, and so does one whose squares add up past fp32 (a value past
+ *   1.8e19): outputs, gradient and, with it, the weights' gradients; a head of zeros gives 0.
  * Rows that are 16-byte aligned with D and rot_dim multiples of 16 are fast.
  *
  * ls_norm_rope_bwd -- the gradient: d->q, d->k are d loss / d output, d->q_out, d->k_out receive d loss / d
