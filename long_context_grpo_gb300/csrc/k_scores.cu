@@ -466,6 +466,7 @@ __global__ void __launch_bounds__(kThreads, 9) scores_kernel(const __grid_consta
     select_best(x, begin, len, groups, a.top, best + part * a.top, at, select_list(a.slice, a.top), sh_select, tid, w.group,
                 [] { __syncthreads(); });
   }
+  __syncwarp();                          // (the cluster's barriers take whole warps; the loops above end lane by lane)
   if (parts > 1) cluster_wait();
   __syncthreads();
   if (tid == 0) {
@@ -496,6 +497,7 @@ __global__ void __launch_bounds__(kThreads, 9) scores_kernel(const __grid_consta
       st_cluster_u32(to, static_cast<uint32_t>(o));
       st_cluster_u32(to + 4, static_cast<uint32_t>(o >> 32));
     }
+    __syncwarp();
     cluster_sync_all();
     if (part > 0) return;
   } else {
