@@ -255,7 +255,8 @@ size_t ls_cache_attn_window_workspace_bytes(ls_cache_t h, int32_t S, int64_t T, 
   if (check_cache(h) != LS_OK || S < 1 || T < 1 || max_new < 1 || max_len < 1 || window < 1 || sinks < 0 ||
       S > kMaxSeqs || T >= (int64_t(1) << 31) || max_len >= (int64_t(1) << 31))
     return 0;
-  return cache_window_layout(h->view, S, T, max_new, max_len, window, sinks).total;
+  const CacheWindowLayout l = cache_window_layout(h->view, S, T, max_new, max_len, window, sinks);
+  return l.ok ? l.total : 0;
 }
 
 ls_status ls_cache_attn(ls_cache_t h, const ls_cache_attn_desc* d, void* workspace,
