@@ -1833,7 +1833,7 @@ CacheWindowLayout cache_window_layout(const CacheView& c, int S, int64_t T, int 
   const int64_t all = (max_len + 127) / 128;
   // tiles in sight of n tokens at most
   auto in_sight = [&](int64_t n) {
-    const int64_t t = (l.keys + n - 2) / 128 + 2 + (l.sinks + 127) / 128;
+    const int64_t t = (l.keys + n - 2) / 128 + 2 + (static_cast<int64_t>(l.sinks) + 127) / 128;
     return t < all ? t : all;
   };
   const int64_t per[2] = {kNarrowRows / g, 2 * (128 / g)};

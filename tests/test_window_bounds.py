@@ -22,3 +22,20 @@ def test_no_workspace_for_bounds_that_are_refused():
     d = b.CacheAttnDesc(S=1, T=T, cu_new=p, q=p, q_stride=256 * 64, o=p, lse=p, group=1, **bounds)
     assert b._lib().ls_cache_attn_window(c._h, ctypes.byref(d), 9, 0, p, 256, None) == 2
     assert ls.device_status() == (0, 0)
+
+
+@pytest.mark.gpu
+def test_first_tokens_up_to_the_longest_sequence_there_is():
+    """All keys in sight, by first tokens that fill 31 bits or nearly so: the same split of the work."""
+    import long_context_grpo_gb300 as ls
+    make, _ = build([500], 16, 1, 64, seed=2, width=40)
+    c = make(2)
+    most = (1 << 31) - 1
+    want = c.attn_workspace_bytes(1, 1, 1, most, window=1, sinks=most - 128)
+    assert want > 1 << 10
+    for sinks in (most - 126, most - 1, most, 1 << 50):
+        assert c.attn_workspace_bytes(1, 1, 1, most, window=1, sinks=sinks) == want
+    q = torch.randn(1, 2, 64, device="cuda").to(torch.bfloat16)
+    o = [c.attn(q, cu([1]), max_new=1, max_len=most, window=1, sinks=s) for s in (most - 128, most, 1 << 50)]
+    assert all(torch.equal(x, y) for a in o[1:] for x, y in zip(a, o[0]))
+    assert ls.device_status() == (0, 0)
