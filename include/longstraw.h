@@ -615,7 +615,8 @@ ls_status ls_cache_compact(ls_cache_t src, ls_cache_t dst, int32_t* n_live, void
  *   Probabilities are rounded to bf16, the values' type, before they meet the values, as in
  *   ls_replay_fwd; the sum that divides them is taken before that.
  *   A NaN in a query or in a key that it sees gives NaN for o and lse; NaN or infinite values v_j
- *   also reach the call's tokens before j that attend the same 128 keys (0 x NaN).
+ *   also reach o of tokens before j that share its products (0 x NaN): those of the same entry (with group > 1 of the
+ *   same group) that come at most 126 + 2 floor(128 Hkv / Hq) before a token that sees j.
  *   max_new, max_len: host bounds on the new tokens and the length of any entry; an entry
  *   above them sets the device status and gets o = 0, lse = -inf.
  *   group, shared_len: with group > 1 (S a multiple of it) the entries come in groups that
@@ -674,8 +675,9 @@ ls_status ls_cache_attn(ls_cache_t h, const ls_cache_attn_desc* d, void* workspa
  *   longest sequence.  Only pages with keys in sight are looked at: table entries of others, pages
  *   that lie before the window and hold none of the first tokens, may be anything (-1 once a caller
  *   has given the page away).  All else as ls_cache_attn, but for two things: NaN or
- *   infinite values v_j also reach tokens of the call that no longer see them, if an earlier token of
- *   the same entry, at most 128 before, does (0 x NaN); and with group > 1 every entry reads the
+ *   infinite values v_j also reach tokens that no longer see them, if an earlier token of the same
+ *   entry, at most 2 floor(128 Hkv / Hq) - 1 before, does (0 x NaN), and of those before j no more than as many
+ *   before a token that sees j; and with group > 1 every entry reads the
  *   keys that it sees for itself (the windows of a group's entries are a few thousand keys, which
  *   stay in L2).
  *   workspace device, 16-byte aligned, >= ls_cache_attn_window_workspace_bytes of the same bounds
