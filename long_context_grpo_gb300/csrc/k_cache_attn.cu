@@ -616,8 +616,8 @@ __device__ __forceinline__ int window_start(const CacheView& c, const Window& w,
   return w.n_jobs;
 }
 
-// Zeros for the tokens that see no key and that no job is made for, 32 tokens a warp of each CTA (all of
-// them where the offsets are refused; none behind the last sequence).
+// Zeros for the tokens that see no key and that no job is made for, 32 tokens a warp of each CTA (every entry's
+// where the offsets are refused; none of those before the first entry or behind the last).
 __device__ __forceinline__ void window_empty(const CacheView& c, const Window& w, bool bad, uint16_t* o, float* lse, int lane) {
   const int g = c.Hq / c.Hkv;
   for (int64_t first = static_cast<int64_t>(blockIdx.x) * 32; first < w.T; first += static_cast<int64_t>(gridDim.x) * 32) {
