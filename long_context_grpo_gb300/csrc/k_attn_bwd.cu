@@ -323,6 +323,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the last tells the other warps that there are no more.
       int u = blockIdx.x;
       for (; (kWindow || u < n_units) && ok; ++uc) {
+        KvUnit w;
+        if constexpr (!kWindow) w = make_kv_unit<kPacked, kNoSuffix, kWindow>(u, sh, vl);     // (beside the unit before)
         kv_pending = false;
         if (uc > 0) ok = mbar_wait_hint<kHintDkdvProducer>(&bars[C::kBarKVEmpty], (uc - 1) & 1u, status, vabort);
         if (!ok) break;
@@ -334,8 +336,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           after = static_cast<int>(gridDim.x + atomicAdd(queue, 1u));
+          w = make_kv_unit<kPacked, kNoSuffix, kWindow>(u, sh, vl);
         }
-        const KvUnit w = make_kv_unit<kPacked, kNoSuffix, kWindow>(u, sh, vl);
         mbar_arrive_expect_tx(&bars[C::kBarKVFull], 2 * C::kTile);
         for (int b = 0; b < C::kBoxes; ++b) {
           tma_load_3d(smem + C::kOffK + b * 16384, w.prompt ? &tm_kp : &tm_ks,
@@ -450,13 +452,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       };
       for (int u = blockIdx.x; (kWindow || u < n_units) && ok; u += gridDim.x, ++uc) {
+        KvUnit w;
+        if constexpr (!kWindow) w = make_kv_unit<kPacked, kNoSuffix, kWindow>(u, sh, vl);
         ok = mbar_wait_hint<kHintDkdvMma>(&bars[C::kBarKVFull], uc & 1u, status, vabort);
         if (!ok) break;
         if constexpr (kWindow) {
           u = *static_cast<volatile int*>(&unit_of[uc & 1u]);
           if (u >= n_units) break;
+          w = make_kv_unit<kPacked, kNoSuffix, kWindow>(u, sh, vl);
         }
-        const KvUnit w = make_kv_unit<kPacked, kNoSuffix, kWindow>(u, sh, vl);
         tc_fence_after();
         ok = issue_s(qit) && issue_dp(qit);
         for (int li = 0; li < w.n && ok; ++li) {
