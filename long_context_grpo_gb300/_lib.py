@@ -250,7 +250,8 @@ class Prefix:
 
     The tensors are borrowed: they must outlive the handle, and k/v are never written.
     Creating the handle zeroes dk_acc / dv_acc on the current stream.  window: the layer is
-    windowed, a query sees the last `window` keys up to its own and the sequence's first `sinks`.
+    windowed, a query sees the last `window` keys up to its own and the sequence's first `sinks`;
+    None, as in PagedCache.attn, or 0 is no window.
     """
 
     def __init__(self, k_prefix, v_prefix, dk_acc, dv_acc, Hq: int, softmax_scale: float = 0.0,
@@ -268,13 +269,13 @@ class Prefix:
         _check(L.ls_prefix_prepare(ctypes.byref(d), ctypes.byref(h), _stream()), "ls_prefix_prepare")
         self._h = h
         self.dk_acc, self.dv_acc = dk_acc, dv_acc
-        if window != 0 or sinks != 0:
+        if window or sinks:
             self.set_window(window, sinks)
 
     def set_window(self, window: int, sinks: int = 0):
-        """A sliding window for the replays from now on (window = 0: none); a forward and its
+        """A sliding window for the replays from now on (None or 0: none); a forward and its
         backward have to be made under the same one."""
-        _check(_lib().ls_prefix_set_window(self._h, _keys(window), _keys(sinks)), "ls_prefix_set_window")
+        _check(_lib().ls_prefix_set_window(self._h, _keys(window or 0), _keys(sinks)), "ls_prefix_set_window")
 
     def close(self):
         if getattr(self, "_h", None) is not None and self._h.value is not None:

@@ -517,7 +517,8 @@ class PagedCache:
         """Attention of the new tokens q [T, Hq, D] over their sequences' pages, causal within
         the sequence (append first).  group > 1: runs of `group` entries share their first
         shared_len[i] tokens' pages, which are read once.  window: a token sees the last `window`
-        keys up to its own and the first `sinks` of its sequence.  Returns (o, lse)."""
+        keys up to its own and the first `sinks` of its sequence (None: all of them; 0 is refused, a
+        token sees its own key).  Returns (o, lse)."""
         if window is None and sinks != 0:
             raise ValueError("sinks are of a window")
         if not isinstance(q, torch.Tensor) or q.dim() != 3:
