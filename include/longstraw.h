@@ -383,6 +383,7 @@ ls_status ls_policy_loss(const ls_policy_loss_desc* d, void* workspace, size_t w
  *     dlogits[t,v] = (d_logp (1[v = y] - p_v) - d_entropy p_v (log p_v + entropy)) / temperature
  *   dlogits  device bf16, row t at dlogits + t dlogits_stride; columns past V are left as they were.  May
  *            be the logits themselves (same pointer and stride).
+ * 16-byte aligned rows of both with V a multiple of 8 are fast.
  * p_v is formed from lse while |lse| <= 4,096 (it is then right to 2^-10); past that, with logits or 1 / temperature that
  * large, relative to the row's maximum: one block then reads the row three times.
  * A row whose two gradients are 0 is left out: its inputs are not looked at, its gradient is 0.  So is the
