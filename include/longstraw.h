@@ -674,7 +674,8 @@ ls_status ls_cache_attn(ls_cache_t h, const ls_cache_attn_desc* d, void* workspa
  *   position p sees the keys j <= p with j > p - window or j < sinks, that is the last `window` keys
  *   up to its own and the sequence's first `sinks`.  window >= 1, sinks >= 0; either may pass the
  *   longest sequence (a layer without a window is ls_cache_attn's: window = 0 is refused here, while
- *   ls_prefix_set_window, which changes a handle, takes its window away with it).  Only pages with keys in sight are looked at: table entries of others, pages
+ *   ls_prefix_set_window, which changes a handle, takes its window away with it).
+ *   Only pages with keys in sight are looked at: table entries of others, pages
  *   that lie before the window and hold none of the first tokens, may be anything (-1 once a caller
  *   has given the page away).  All else as ls_cache_attn, but for two things: NaN or
  *   infinite values v_j also reach tokens that no longer see them, if an earlier token of the same

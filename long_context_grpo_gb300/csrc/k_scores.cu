@@ -17,7 +17,8 @@
 //   Bound by HBM without alternatives (4,096 rows of 151,936: 190 us, 6.5 TB/s); with 20 of them (228 us) a row's
 //   end, a chain of eight barriers, keeps a ninth of the SM's CTAs from reading.  128 threads and nine CTAs an SM: with
 //   256 threads 281 us, one CTA an SM fed by bulk copies, with warps of its own for the alternatives, 291.
-// scores_bwd_kernel: one pass, a block 4,096 logits of a row, but for rows whose lse is far from zero (1,279 rows of 151,936: 108 us, 7.2 TB/s).
+// scores_bwd_kernel: one pass, a block 4,096 logits of a row (1,279 rows of 151,936: 108 us, 7.2 TB/s); rows whose lse is
+//   far from zero by one block each.
 #include <type_traits>
 
 #include "ls_internal.h"
