@@ -87,7 +87,9 @@ __device__ __forceinline__ uint4 load8(const uint16_t* x, int64_t i, int64_t end
 // logits there differ by 2^-9 of the larger or more, so z is below -2^13 for all but the counted ones, and the rounding
 // of r, half an ulp of it, stays below 1 (past 2^34 it would pass fp32's exponents, whose 2^z is then no correction).
 constexpr float kFar = 8388608.0f;       // 2^23
-__device__ __forceinline__ float reference(float m, float scale2) { return m * scale2; }
+// (a product by itself: fused into the difference of two references it would not be the rounded one that the sums are
+// relative to)
+__device__ __forceinline__ float reference(float m, float scale2) { return __fmul_rn(m, scale2); }
 
 // Sums with the largest logit m and reference r, for a larger one.
 __device__ __forceinline__ void rebase(float to, float scale2, float m, float& r, float& ones, float& hi, float& lo, float& e) {

@@ -132,3 +132,21 @@ def test_masked_tokens_of_cold_rows():
     r = ls.token_scores(x, ids, temperature=1e-3)
     dl = torch.ones(len(ids), device="cuda")
     grad_check(ls.token_scores_bwd(x, ids, r.logp, r.lse, d_logp=dl, temperature=1e-3), x, ids, dl, 0 * dl, 1e-3, r.lse)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,V", [(3, 13000), (400, 13000), (400, 13001), (300, 13387)])
+@pytest.mark.parametrize("temperature", [0.01, 0.03, 0.2])
+def test_maxima_that_grow_within_a_warp(T, V, temperature):
+    """Two likely tokens of which the larger one comes a step behind the other, in the same warp: the sums change
+    their reference by a whole number of its roundings."""
+    import long_context_grpo_gb300 as ls
+    g = torch.Generator().manual_seed(T)
+    x = torch.randn(T, V, generator=g)
+    at = torch.randint(0, 4096, (T,), generator=g)
+    row = torch.arange(T)
+    small = (4.0 + 11.9 * torch.rand(T, generator=g)).to(torch.bfloat16)
+    x[row, at] = small.float()
+    x[row, at + 4096] = (small.float() * (1.0 + 2.0 ** -7)).to(torch.bfloat16).float()      # the next value or the one after it
+    x, ids = x.to(torch.bfloat16).cuda(), at.to(torch.int32).cuda()
+    check(ls.token_scores(x, ids, top=3, temperature=temperature), x, ids, 3, temperature)
